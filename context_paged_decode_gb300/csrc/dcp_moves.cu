@@ -1,0 +1,256 @@
+// Moves of cached bytes: whole pages, and single tokens inside a request.
+//
+// dcp_pages_copy carries out the copies that a fork or a cut asks for (the
+// open page of each, per rank), dcp_cache_compact moves the accepted drafted
+// tokens together behind the context:
+//     row(ctx + path[i]) -> row(ctx + i),  path strictly increasing.
+// Both take every pool of a model (keys and values of all layers) in one
+// launch, through a device array of pool pointers.  Both are bound by bytes
+// read and written once, and by latency when there are few.
+#include "dcp_common.cuh"
+#include "dcp_ptx.cuh"
+
+namespace dcp {
+
+struct PoolSet {
+  const uint64_t* ptr;   // [num_pools][dcp]
+  int num_pools, H, n16; // heads, 16-byte chunks of a row
+  int64_t nb;
+};
+
+// A usable pool pointer, or NULL.
+__device__ __forceinline__ uint4* pool_at(const PoolSet& P, int pool, int dcp, int r) {
+  const uint64_t p = __ldcg(P.ptr + (int64_t)pool * dcp + r);
+  return (p & 15) ? nullptr : reinterpret_cast<uint4*>(p);
+}
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyDepth = 8;     // 16-byte loads in flight per thread
+
+// One CTA per (copy, rank, pool): a page is H * bs rows in one piece.
+__global__ void __launch_bounds__(kCopyThreads)
+pages_copy_kernel(PoolSet P, int dcp, int tables, const int32_t* src,
+                  const int32_t* dst, int n, int64_t page16, int32_t* err) {
+  griddep_launch_dependents();   // the next call's first kernel may start its launch
+  griddep_wait();                // launched chained: the preceding kernel completed
+  const int64_t units = (int64_t)n * dcp * P.num_pools;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int pool = (int)(u % P.num_pools);
+    const int r = (int)(u / P.num_pools % dcp);
+    const int i = (int)(u / P.num_pools / dcp);
+    const int64_t e = (int64_t)(tables == 1 ? 0 : r) * n + i;
+    const int a = __ldcg(src + e), b = __ldcg(dst + e);
+    if (a == -1 && b == -1) continue;
+    uint4* base = pool_at(P, pool, dcp, r);
+    if (a < 0 || a >= P.nb || b < 0 || b >= P.nb || !base) {
+      if (threadIdx.x == 0) count_error(err);
+      continue;
+    }
+    if (a == b) continue;
+    const uint4* from = base + a * page16;
+    uint4* to = base + b * page16;
+    for (int64_t c = threadIdx.x; c < page16; c += kCopyThreads * kCopyDepth) {
+      uint4 x[kCopyDepth];
+#pragma unroll
+      for (int j = 0; j < kCopyDepth; ++j)
+        if (c + j * kCopyThreads < page16) x[j] = __ldcg(from + c + j * kCopyThreads);
+#pragma unroll
+      for (int j = 0; j < kCopyDepth; ++j)
+        if (c + j * kCopyThreads < page16) to[c + j * kCopyThreads] = x[j];
+    }
+  }
+}
+
+struct CompactTokArgs {
+  Layout L;
+  PoolSet P;
+  const int32_t* bt;
+  int max_vb;
+  int64_t stride;
+  const int32_t* ctx;
+  const int32_t* path;   // [B][max_path]
+  const int32_t* n;      // [B]
+  int max_path;
+  int32_t* new_lens;     // [B] or NULL
+  int32_t* err;
+};
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveChunk = 128;   // moves resolved at a time
+constexpr int kMoveDepth = 8;
+
+// blockIdx.x = request, blockIdx.y = share of its columns.  A thread owns a
+// 16-byte column of a (pool, head) and moves its rows in order.  Row i goes to
+// place i and comes from path[i] >= i, and every later row comes from behind
+// place i, so a row is read before anything is written over it, by the thread
+// that writes it.
+__global__ void __launch_bounds__(kMoveThreads) cache_compact_kernel(const __grid_constant__ CompactTokArgs A) {
+  __shared__ int s_sr[kMoveChunk], s_dr[kMoveChunk];          // ranks
+  __shared__ int64_t s_src[kMoveChunk], s_dst[kMoveChunk];    // row of head 0 in the rank's pool
+  __shared__ int s_good;
+  griddep_launch_dependents();   // the next call's first kernel may start its launch
+  griddep_wait();                // launched chained: the preceding kernel completed
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int64_t ctx = __ldcg(A.ctx + b);
+  const int n = __ldcg(A.n + b);
+  const int32_t* path = A.path + (int64_t)b * A.max_path;
+  const int dcp = A.L.dcp;
+  if (ctx < 0 || n < 0 || n > A.max_path) {
+    if (blockIdx.y == 0 && tid == 0) {
+      count_error(A.err);
+      if (A.new_lens) A.new_lens[b] = (int32_t)max(ctx, (int64_t)0);
+    }
+    return;
+  }
+  const int64_t cols = (int64_t)A.P.num_pools * A.P.H * A.P.n16;
+  int kept = 0;
+  for (int i0 = 0; i0 < n; i0 += kMoveChunk) {
+    const int m = min(kMoveChunk, n - i0);
+    __syncthreads();   // the last chunk's moves are done with the arrays
+    if (tid == 0) s_good = m;
+    __syncthreads();
+    if (tid < m) {
+      const int i = i0 + tid;
+      const int64_t p = __ldcg(path + i);
+      bool ok = p >= i && (i == 0 || p > __ldcg(path + i - 1));
+      auto place = [&](int64_t x, int& r, int64_t& row) {
+        int64_t vb;
+        int loc;
+        place_token(x, A.L, r, vb, loc);
+        const int64_t phys =
+            vb < A.max_vb ? (int64_t)__ldcg(A.bt + r * A.stride + (int64_t)b * A.max_vb + vb) : -1;
+        if (phys < 0 || phys >= A.P.nb) return false;
+        row = phys * A.P.H * A.L.bs + loc;
+        return true;
+      };
+      int sr = 0, dr = 0;
+      int64_t src = 0, dst = 0;
+      if (ok) ok = place(ctx + p, sr, src) && place(ctx + i, dr, dst);
+      s_sr[tid] = sr;
+      s_dr[tid] = dr;
+      s_src[tid] = src;
+      s_dst[tid] = dst;
+      if (!ok) atomicMin(&s_good, tid);
+    }
+    __syncthreads();
+    const int good = s_good;
+    kept += good;
+    // a prefix that stays where it is needs no move
+    int first = 0;
+    while (first < good && s_src[first] == s_dst[first] && s_sr[first] == s_dr[first]) ++first;
+    if (first < good)
+      for (int64_t c = blockIdx.y * (int64_t)kMoveThreads + tid; c < cols;
+           c += (int64_t)gridDim.y * kMoveThreads) {
+        const int chunk = (int)(c % A.P.n16);
+        const int h = (int)(c / A.P.n16 % A.P.H);
+        const int pool = (int)(c / A.P.n16 / A.P.H);
+        const int64_t head = (int64_t)h * A.L.bs;
+        for (int j0 = first; j0 < good; j0 += kMoveDepth) {
+          uint4 x[kMoveDepth];
+#pragma unroll
+          for (int j = 0; j < kMoveDepth; ++j)
+            if (j0 + j < good) {
+              const uint4* p = pool_at(A.P, pool, dcp, s_sr[j0 + j]);
+              if (p) x[j] = __ldcg(p + (s_src[j0 + j] + head) * A.P.n16 + chunk);
+            }
+#pragma unroll
+          for (int j = 0; j < kMoveDepth; ++j)
+            if (j0 + j < good) {
+              uint4* p = pool_at(A.P, pool, dcp, s_dr[j0 + j]);
+              const bool from = pool_at(A.P, pool, dcp, s_sr[j0 + j]) != nullptr;
+              if (p && from)
+                p[(s_dst[j0 + j] + head) * A.P.n16 + chunk] = x[j];
+              else if (h == 0 && chunk == 0)
+                count_error(A.err);
+            }
+        }
+      }
+    if (good < m) {   // nothing behind a bad entry is moved
+      if (blockIdx.y == 0 && tid == 0) count_error(A.err);
+      break;
+    }
+  }
+  if (A.new_lens && blockIdx.y == 0 && tid == 0) A.new_lens[b] = (int32_t)(ctx + kept);
+}
+
+static bool pool_set_ok(const dcp_pool_set_t& p) {
+  return p.num_pools >= 0 && p.num_heads >= 1 && p.row_bytes >= 1 && p.num_blocks >= 0;
+}
+
+}  // namespace dcp
+
+using namespace dcp;
+
+extern "C" {
+
+int dcp_pages_copy(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* copy_src,
+                   const int32_t* copy_dst, int32_t num_tables, int32_t num, int32_t* err_count,
+                   dcp_stream_t stream) {
+  dcp::NvtxRange nvtx_range("dcp_pages_copy");
+  if (!layout_ok(layout) || !pool_set_ok(pools) || num < 0 ||
+      (num_tables != 1 && num_tables != layout.dcp_size))
+    return DCP_EINVAL;
+  if (pools.row_bytes % 16 != 0) return DCP_EUNSUPPORTED;
+  if (num == 0 || pools.num_pools == 0) return DCP_OK;
+  if (!pools.ptr || !copy_src || !copy_dst) return DCP_EINVAL;
+  const PoolSet P{pools.ptr, pools.num_pools, pools.num_heads, pools.row_bytes / 16,
+                  pools.num_blocks};
+  const int64_t page16 = (int64_t)pools.num_heads * layout.block_size * (pools.row_bytes / 16);
+  const int64_t units = (int64_t)num * layout.dcp_size * pools.num_pools;
+  const int64_t most = (int64_t)32 * num_sms();
+  const cudaError_t e = launch_chained(
+      pages_copy_kernel, (unsigned)(units < most ? units : most), kCopyThreads, 0,
+      (cudaStream_t)stream, P, (int)layout.dcp_size, (int)num_tables, copy_src, copy_dst, (int)num,
+      page16, err_count);
+  if (e != cudaSuccess) return launch_status_report(e);
+  return launch_status();
+}
+
+int dcp_cache_compact(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* block_table,
+                      int32_t num_reqs, int32_t max_vblocks, int64_t bt_rank_stride,
+                      const int32_t* ctx_lens, const int32_t* path, const int32_t* path_len,
+                      int32_t max_path, int32_t* new_lens, int32_t* err_count,
+                      dcp_stream_t stream) {
+  dcp::NvtxRange nvtx_range("dcp_cache_compact");
+  if (!layout_ok(layout) || !pool_set_ok(pools) || num_reqs < 0 || max_vblocks < 0 ||
+      bt_rank_stride < 0 || max_path < 0)
+    return DCP_EINVAL;
+  if (pools.row_bytes % 16 != 0) return DCP_EUNSUPPORTED;
+  if (num_reqs == 0) return DCP_OK;
+  if ((pools.num_pools > 0 && !pools.ptr) || !block_table || !ctx_lens || !path_len ||
+      (max_path > 0 && !path))
+    return DCP_EINVAL;
+  CompactTokArgs A;
+  A.L = Layout{layout.dcp_size, layout.block_size, layout.interleave};
+  A.P = PoolSet{pools.ptr, pools.num_pools, pools.num_heads, pools.row_bytes / 16,
+                pools.num_blocks};
+  A.bt = block_table;
+  A.max_vb = max_vblocks;
+  A.stride = bt_rank_stride;
+  A.ctx = ctx_lens;
+  A.path = path;
+  A.n = path_len;
+  A.max_path = max_path;
+  A.new_lens = new_lens;
+  A.err = err_count;
+  // one column per thread where the card can hold them all (eight CTAs an SM)
+  const int64_t cols = (int64_t)pools.num_pools * pools.num_heads * A.P.n16;
+  int64_t y = (cols + kMoveThreads - 1) / kMoveThreads;
+  const int64_t most = ((int64_t)8 * num_sms() + num_reqs - 1) / num_reqs;
+  if (y > most) y = most;
+  if (y < 1) y = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)num_reqs, (unsigned)y);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, cache_compact_kernel, A);
+  if (e != cudaSuccess) return launch_status_report(e);
+  return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,403 @@
+// Rotary positions with one or several axes, fused with the owner-masked
+// write of keys and values into the per-rank paged pools.
+//
+// Pair i of a token's rotated entries turns by
+//     angle = positions[axis[i]][t] * inv_freq[i],
+//     (a, b) -> (a cos - b sin, b cos + a sin),   cos, sin times `scaling`.
+// Images and video give each token a time, a height and a width, and `axis`
+// says which of them a pair follows; text has one axis.
+//
+// The angle is needed only modulo one turn.  inv_freq / 2pi is held as a
+// 64-bit fraction of a turn (from two doubles, so that all 64 bits count), and
+// position * fraction in wrapping 64-bit integers is the angle's fraction; its
+// error is the position times 2^-65 of a turn.  A 32-bit float product loses
+// it (a position of 10^6 at frequency 1 is off by 0.03 rad).  The top 32 bits
+// of the fraction go to sincospif.
+//
+// What bounds it: reading q, k, v and writing them once.  One CTA per token:
+// a thread first issues the loads of its first units (a unit is two 16-byte
+// chunks, for rotated entries the two that hold both members of its pairs),
+// then the CTA computes the token's rot/2 cosines and sines once for all heads,
+// so the trigonometry hides behind the loads.
+#include "dcp_common.cuh"
+#include "dcp_ptx.cuh"
+
+namespace dcp {
+
+struct RopeArgs {
+  const uint4* q;
+  const uint4* k;
+  const uint4* v;
+  uint4* q_out;
+  uint4* k_out;
+  int64_t q_stride, k_stride, v_stride;  // 16-byte chunks between tokens
+  const int64_t* pos;                    // [axes][T]
+  const float* inv_freq;                 // [half]
+  const int32_t* axis;                   // [half] or NULL
+  const int64_t* slot;                   // [dcp][T]
+  int64_t T, num_slots;
+  int Hq, Hk, Hv;                        // heads of q, of k, of v (0: no v)
+  int n16;                               // chunks of a head row
+  int ru, off16;                         // rotated units of a row; first rotated chunk
+  int uq, uk, uv;                        // units of a q, k and v row (a q row in place: only the
+                                         // rotated ones)
+  uint32_t mq, mk, mv;                   // ceil(2^32 / units), for the division
+  int half, axes, bs, dcp;
+  float scaling;
+  dcp_rank_ptrs_t kp, vp;
+  int32_t* err;
+};
+
+// n / d for n * d < 2^32 with m = ceil(2^32 / d)
+__device__ __forceinline__ int fast_div(uint32_t n, uint32_t m, int d) {
+  return d == 1 ? (int)n : (int)__umulhi(n, m);
+}
+
+// The rotation of one unit: its kN pairs are u * kN + i.  The table holds pair
+// p's (cos, sin) at (p % kN) * ru + p / kN, so that a warp's units, which
+// follow one another, read neighbouring entries.
+template <bool kF32, bool kHalves>
+__device__ __forceinline__ void rotate_unit(uint4& x, uint4& y, int u, int ru, const float2* cs) {
+  constexpr int kN = kF32 ? 4 : 8;     // elements of a chunk
+  float a[kN], b[kN];
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kF32) {
+      a[i] = __uint_as_float(xs[i]);
+      b[i] = __uint_as_float(ys[i]);
+    } else {
+      a[2 * i] = bf16_lo(xs[i]);
+      a[2 * i + 1] = bf16_hi(xs[i]);
+      b[2 * i] = bf16_lo(ys[i]);
+      b[2 * i + 1] = bf16_hi(ys[i]);
+    }
+  }
+  if (kHalves) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const float2 t = cs[i * ru + u];
+      const float p = a[i], q = b[i];
+      a[i] = p * t.x - q * t.y;
+      b[i] = q * t.x + p * t.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) {
+      const float2 t = cs[i * ru + u], s = cs[(i + kN / 2) * ru + u];
+      const float p = a[2 * i], q = a[2 * i + 1], r = b[2 * i], w = b[2 * i + 1];
+      a[2 * i] = p * t.x - q * t.y;
+      a[2 * i + 1] = q * t.x + p * t.y;
+      b[2 * i] = r * s.x - w * s.y;
+      b[2 * i + 1] = w * s.x + r * s.y;
+    }
+  }
+  if (kF32) {
+    x = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
+                   __float_as_uint(a[3]));
+    y = make_uint4(__float_as_uint(b[0]), __float_as_uint(b[1]), __float_as_uint(b[2]),
+                   __float_as_uint(b[3]));
+  } else {
+    x = make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2 % kN], a[3 % kN]),
+                   pack_bf16(a[4 % kN], a[5 % kN]), pack_bf16(a[6 % kN], a[7 % kN]));
+    y = make_uint4(pack_bf16(b[0], b[1]), pack_bf16(b[2 % kN], b[3 % kN]),
+                   pack_bf16(b[4 % kN], b[5 % kN]), pack_bf16(b[6 % kN], b[7 % kN]));
+  }
+}
+
+constexpr double kInv2Pi = 0.15915494309189535;          // 1 / (2 pi), rounded
+constexpr double kInv2PiLow = -9.839338337591243e-18;     // what the rounding left
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeBatch = 4;        // units in flight per thread
+constexpr int kMaxHalf = 512;
+
+struct RopeUnit {
+  int kind;                // 0 q, 1 k, 2 v
+  int h, u;                // head, unit of the row; u < ru: rotated
+  int c0, c1;              // chunks of the row (c1 < 0: one chunk)
+};
+
+template <bool kHalves>
+__device__ __forceinline__ RopeUnit rope_unit(const RopeArgs& A, int i) {
+  RopeUnit U;
+  int nq = A.Hq * A.uq, nk = A.Hk * A.uk;
+  int rel;
+  if (i < nq) {
+    U.kind = 0;
+    U.h = fast_div(i, A.mq, A.uq);
+    U.u = i - U.h * A.uq;
+  } else if (i < nq + nk) {
+    U.kind = 1;
+    U.h = fast_div(i - nq, A.mk, A.uk);
+    U.u = i - nq - U.h * A.uk;
+  } else {
+    U.kind = 2;
+    U.h = fast_div(i - nq - nk, A.mv, A.uv);
+    U.u = i - nq - nk - U.h * A.uv;
+  }
+  const int ru = U.kind == 2 ? 0 : A.ru;
+  if (U.u < ru) {
+    U.c0 = A.off16 + (kHalves ? U.u : 2 * U.u);
+    U.c1 = U.c0 + (kHalves ? A.ru : 1);
+  } else {
+    rel = 2 * (U.u - ru);
+    const int rest = A.n16 - 2 * ru;
+    U.c0 = ru > 0 && rel >= A.off16 ? rel + 2 * ru : rel;
+    ++rel;
+    U.c1 = rel >= rest ? -1 : (ru > 0 && rel >= A.off16 ? rel + 2 * ru : rel);
+    U.u = -1;
+  }
+  return U;
+}
+
+template <bool kF32, bool kHalves>
+__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_constant__ RopeArgs A) {
+  __shared__ float2 cs[kMaxHalf];
+  __shared__ int s_dst[DCP_MAX_RANKS];
+  __shared__ int64_t s_row[DCP_MAX_RANKS];
+  __shared__ int s_n;
+  griddep_launch_dependents();   // the next call's first kernel may start its launch
+  griddep_wait();                // launched chained: the preceding kernel completed
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int total = A.Hq * A.uq + A.Hk * A.uk + A.Hv * A.uv;
+  const uint4* src[3] = {A.q + t * A.q_stride, A.k + t * A.k_stride, A.v + t * A.v_stride};
+
+  auto load = [&](int i, RopeUnit& U, uint4& x, uint4& y) {
+    U = rope_unit<kHalves>(A, i);
+    const uint4* p = (U.kind == 0 ? src[0] : U.kind == 1 ? src[1] : src[2]) + (int64_t)U.h * A.n16;
+    x = __ldcg(p + U.c0);
+    y = U.c1 >= 0 ? __ldcg(p + U.c1) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto finish = [&](const RopeUnit& U, uint4 x, uint4 y) {
+    if (U.u >= 0) rotate_unit<kF32, kHalves>(x, y, U.u, A.ru, cs);
+    if (U.kind == 0) {
+      uint4* p = A.q_out + (t * A.Hq + U.h) * A.n16;
+      p[U.c0] = x;
+      if (U.c1 >= 0) p[U.c1] = y;
+      return;
+    }
+    if (U.kind == 1 && A.k_out) {
+      uint4* p = A.k_out + (t * A.Hk + U.h) * A.n16;
+      p[U.c0] = x;
+      if (U.c1 >= 0) p[U.c1] = y;
+    }
+    for (int j = 0; j < s_n; ++j) {
+      const int r = s_dst[j];
+      uint4* p = (uint4*)(U.kind == 1 ? A.kp.ptr[r] : A.vp.ptr[r]) +
+                 (s_row[j] + (int64_t)U.h * A.bs) * A.n16;
+      p[U.c0] = x;
+      if (U.c1 >= 0) p[U.c1] = y;
+    }
+  };
+
+  RopeUnit U[kRopeBatch];
+  uint4 x[kRopeBatch], y[kRopeBatch];
+#pragma unroll
+  for (int j = 0; j < kRopeBatch; ++j)
+    if (tid + j * kRopeThreads < total) load(tid + j * kRopeThreads, U[j], x[j], y[j]);
+
+  // the ranks that store this token (warp 7, the last to have trigonometry)
+  if (tid >= kRopeThreads - 32) {
+    const int r = tid - (kRopeThreads - 32);
+    const int64_t s = r < A.dcp ? __ldcg(A.slot + (int64_t)r * A.T + t) : -1;
+    const bool ok = s >= 0 && s < A.num_slots;
+    if (!ok && s != -1) count_error(A.err);
+    const uint32_t m = __ballot_sync(0xffffffffu, ok);
+    if (ok) {
+      const int at = __popc(m & ((1u << r) - 1u));
+      const int64_t blk = s / A.bs;
+      s_dst[at] = r;
+      s_row[at] = blk * A.Hk * A.bs + (s - blk * A.bs);
+    }
+    if (r == 0) s_n = __popc(m);
+  }
+  for (int i = tid; i < A.half; i += kRopeThreads) {
+    int ax = A.axis ? __ldcg(A.axis + i) : 0;
+    if (ax < 0 || ax >= A.axes) {
+      if (t == 0) count_error(A.err);
+      ax = 0;
+    }
+    const uint64_t p = (uint64_t)__ldcg(A.pos + (int64_t)ax * A.T + t);
+    // turns per position as a 64-bit fraction: inv_freq / (2 pi) in two doubles
+    const double f = (double)__ldcg(A.inv_freq + i);
+    const double hi = f * kInv2Pi;
+    const double lo = fma(f, kInv2Pi, -hi) + f * kInv2PiLow;
+    const uint64_t per = (uint64_t)((hi - floor(hi)) * 18446744073709551616.0) +
+                         (uint64_t)(int64_t)rint(lo * 18446744073709551616.0);
+    const uint64_t frac = p * per;
+    float s, c;
+    sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
+    constexpr int kN = kF32 ? 4 : 8;
+    cs[(i % kN) * A.ru + i / kN] = make_float2(c * A.scaling, s * A.scaling);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kRopeBatch; ++j)
+    if (tid + j * kRopeThreads < total) finish(U[j], x[j], y[j]);
+  for (int i0 = tid + kRopeBatch * kRopeThreads; i0 < total; i0 += kRopeBatch * kRopeThreads) {
+#pragma unroll
+    for (int j = 0; j < kRopeBatch; ++j)
+      if (i0 + j * kRopeThreads < total) load(i0 + j * kRopeThreads, U[j], x[j], y[j]);
+#pragma unroll
+    for (int j = 0; j < kRopeBatch; ++j)
+      if (i0 + j * kRopeThreads < total) finish(U[j], x[j], y[j]);
+  }
+}
+
+static uint32_t div_magic(int d) {
+  return d <= 1 ? 0u : (uint32_t)(((uint64_t(1) << 32) + (uint64_t)d - 1) / (uint64_t)d);
+}
+
+static int launch_rope(RopeArgs& A, int rot, int rot_at, int d, int es, bool interleaved,
+                       cudaStream_t s) {
+  A.n16 = d * es / 16;
+  A.ru = rot * es / 32;
+  A.off16 = rot_at * es / 16;
+  A.half = rot / 2;
+  const int rest = A.n16 - 2 * A.ru;
+  A.uk = A.ru + (rest + 1) / 2;
+  A.uv = (A.n16 + 1) / 2;
+  // in place, the unrotated chunks of q stay where they are
+  A.uq = A.q_out == A.q && A.q_stride == (int64_t)A.Hq * A.n16 ? A.ru : A.uk;
+  A.mq = div_magic(A.uq);
+  A.mk = div_magic(A.uk);
+  A.mv = div_magic(A.uv);
+  const unsigned grid = (unsigned)A.T;
+  cudaError_t e;
+  if (es == 4)
+    e = interleaved ? launch_chained(rope_write_kernel<true, false>, grid, kRopeThreads, 0, s, A)
+                    : launch_chained(rope_write_kernel<true, true>, grid, kRopeThreads, 0, s, A);
+  else
+    e = interleaved ? launch_chained(rope_write_kernel<false, false>, grid, kRopeThreads, 0, s, A)
+                    : launch_chained(rope_write_kernel<false, true>, grid, kRopeThreads, 0, s, A);
+  if (e != cudaSuccess) return launch_status_report(e);
+  return launch_status();
+}
+
+static inline int elem_bytes(dcp_dtype_t d) { return d == DCP_F32 ? 4 : (d == DCP_BF16 ? 2 : 0); }
+static inline bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// Checks shared by both entry points; DCP_OK when the shape can run.
+static int rope_shape(const dcp_layout_t& L, int64_t T, int Hq, int Hk, int d, int es, int rot,
+                      int axes, int64_t num_blocks) {
+  if (!layout_ok(L) || es == 0 || T < 0 || Hq < 0 || Hk < 1 || d < 1 || rot < 2 || rot > d ||
+      axes < 1 || num_blocks < 0)
+    return DCP_EINVAL;
+  // the division by units a row takes under 2^20 units a token and 4096 a row
+  if (T >= (int64_t(1) << 31) || d > 8192 || (d * es) % 16 != 0 || rot % 16 != 0 ||
+      rot / 2 > kMaxHalf ||
+      ((int64_t)Hq + 2 * (int64_t)Hk) * (d * es / 16) >= (int64_t(1) << 20))
+    return DCP_EUNSUPPORTED;
+  return DCP_OK;
+}
+
+}  // namespace dcp
+
+using namespace dcp;
+
+extern "C" {
+
+int dcp_rope_write_gqa(dcp_layout_t layout, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, int64_t num_tokens,
+                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                       dcp_dtype_t dtype, const int64_t* positions, int32_t num_axes,
+                       const float* inv_freq, const int32_t* axis, int32_t rot_dim,
+                       int32_t interleaved, float scaling, const int64_t* slot,
+                       int64_t num_blocks, dcp_rank_ptrs_t k_cache, dcp_rank_ptrs_t v_cache,
+                       void* q_out, void* k_out, int32_t* err_count, dcp_stream_t stream) {
+  dcp::NvtxRange nvtx_range("dcp_rope_write_gqa");
+  const int es = elem_bytes(dtype);
+  const int rc = rope_shape(layout, num_tokens, num_q_heads, num_kv_heads, head_dim, es, rot_dim,
+                            num_axes, num_blocks);
+  if (rc != DCP_OK) return rc;
+  if (num_tokens == 0) return DCP_OK;
+  if ((num_q_heads > 0 && (!q || !q_out)) || !k || !v || !positions || !inv_freq || !slot ||
+      !ranks_ok(k_cache, layout.dcp_size) || !ranks_ok(v_cache, layout.dcp_size))
+    return DCP_EINVAL;
+  if (q_stride < (int64_t)num_q_heads * head_dim || k_stride < (int64_t)num_kv_heads * head_dim ||
+      v_stride < (int64_t)num_kv_heads * head_dim)
+    return DCP_EINVAL;
+  if (!al16(q) || !al16(k) || !al16(v) || !al16(q_out) || !al16(k_out) || (q_stride * es) % 16 ||
+      (k_stride * es) % 16 || (v_stride * es) % 16)
+    return DCP_EUNSUPPORTED;
+  for (int r = 0; r < layout.dcp_size; ++r)
+    if (!al16(k_cache.ptr[r]) || !al16(v_cache.ptr[r])) return DCP_EUNSUPPORTED;
+  RopeArgs A;
+  A.q = (const uint4*)q;
+  A.k = (const uint4*)k;
+  A.v = (const uint4*)v;
+  A.q_out = (uint4*)q_out;
+  A.k_out = (uint4*)k_out;
+  A.q_stride = q_stride * es / 16;
+  A.k_stride = k_stride * es / 16;
+  A.v_stride = v_stride * es / 16;
+  A.pos = positions;
+  A.inv_freq = inv_freq;
+  A.axis = axis;
+  A.slot = slot;
+  A.T = num_tokens;
+  A.num_slots = num_blocks * layout.block_size;
+  A.Hq = num_q_heads;
+  A.Hk = A.Hv = num_kv_heads;
+  A.axes = num_axes;
+  A.bs = layout.block_size;
+  A.dcp = layout.dcp_size;
+  A.scaling = scaling;
+  A.kp = k_cache;
+  A.vp = v_cache;
+  A.err = err_count;
+  return launch_rope(A, rot_dim, 0, head_dim, es, interleaved != 0, (cudaStream_t)stream);
+}
+
+int dcp_rope_write_mla(dcp_layout_t layout, const void* q, int64_t q_stride, const void* kv,
+                       int64_t kv_stride, int64_t num_tokens, int32_t num_q_heads, int32_t kv_dim,
+                       dcp_dtype_t dtype, const int64_t* positions, int32_t num_axes,
+                       const float* inv_freq, const int32_t* axis, int32_t rot_dim,
+                       int32_t interleaved, float scaling, const int64_t* slot,
+                       int64_t num_blocks, dcp_rank_ptrs_t cache, void* q_out,
+                       int32_t* err_count, dcp_stream_t stream) {
+  dcp::NvtxRange nvtx_range("dcp_rope_write_mla");
+  const int es = elem_bytes(dtype);
+  const int rc = rope_shape(layout, num_tokens, num_q_heads, 1, kv_dim, es, rot_dim, num_axes,
+                            num_blocks);
+  if (rc != DCP_OK) return rc;
+  if (num_tokens == 0) return DCP_OK;
+  if ((num_q_heads > 0 && (!q || !q_out)) || !kv || !positions || !inv_freq || !slot ||
+      !ranks_ok(cache, layout.dcp_size))
+    return DCP_EINVAL;
+  if (q_stride < (int64_t)num_q_heads * kv_dim || kv_stride < kv_dim) return DCP_EINVAL;
+  if (!al16(q) || !al16(kv) || !al16(q_out) || (q_stride * es) % 16 || (kv_stride * es) % 16)
+    return DCP_EUNSUPPORTED;
+  for (int r = 0; r < layout.dcp_size; ++r)
+    if (!al16(cache.ptr[r])) return DCP_EUNSUPPORTED;
+  RopeArgs A;
+  A.q = (const uint4*)q;
+  A.k = (const uint4*)kv;
+  A.v = nullptr;
+  A.q_out = (uint4*)q_out;
+  A.k_out = nullptr;
+  A.q_stride = q_stride * es / 16;
+  A.k_stride = kv_stride * es / 16;
+  A.v_stride = 0;
+  A.pos = positions;
+  A.inv_freq = inv_freq;
+  A.axis = axis;
+  A.slot = slot;
+  A.T = num_tokens;
+  A.num_slots = num_blocks * layout.block_size;
+  A.Hq = num_q_heads;
+  A.Hk = 1;
+  A.Hv = 0;
+  A.axes = num_axes;
+  A.bs = layout.block_size;
+  A.dcp = layout.dcp_size;
+  A.scaling = scaling;
+  A.kp = A.vp = cache;
+  A.err = err_count;
+  return launch_rope(A, rot_dim, kv_dim - rot_dim, kv_dim, es, interleaved != 0,
+                     (cudaStream_t)stream);
+}
+
+}  // extern "C"

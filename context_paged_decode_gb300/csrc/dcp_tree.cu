@@ -1,0 +1,608 @@
+// Attention of drafted token trees over the sharded paged cache: plan, the
+// CUDA-core kernel for any supported shape, merge, and the entry points.
+//
+// Request b has ctx_b cached tokens and T_b drafted nodes stored behind them,
+// node j at position ctx_b + j.  Every node sees the whole context and those
+// nodes whose bits its mask has (its ancestors and itself).  Ranks attend
+// their own shards and the parts are joined by log-sum-exp, page "Decode
+// Context Parallel (DCP)", section "Decode"; with one node and its own bit
+// set this is the ordinary decode step.
+#include "dcp_ptx.cuh"
+#include "dcp_tree.cuh"
+
+namespace dcp {
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+
+// Every kernel here may be launched, as a programmatic dependent, while the
+// kernels before it still run, so what those write (and the plan, which the
+// next call writes to the same workspace) is read past the SM's L1 (__ldcg):
+// a read-only load may find a line that an earlier grid left there.
+constexpr int kTreePlanThreads = 256;
+
+// One CTA: checks the requests, counts each entry's tiles and units, and
+// prefix-sums them.
+__global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __grid_constant__ TreeArgs A) {
+  __shared__ int64_t sh_t[kTreePlanThreads / 32];
+  __shared__ int sh_u[kTreePlanThreads / 32];
+  griddep_launch_dependents();   // the next call's first kernel may start its launch
+  griddep_wait();                // launched chained: the preceding kernel completed
+  const int E = A.per_rank ? A.B * A.L.dcp : A.B;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  int64_t run_t = 0;
+  int run_u = 0;
+  for (int e0 = 0; e0 < E; e0 += kTreePlanThreads) {
+    const int e = e0 + tid;
+    int64_t tiles = 0;
+    int units = 0;
+    if (e < E) {
+      const int b = A.per_rank ? e / A.L.dcp : e;
+      const int q0 = __ldcg(A.q_start + b), q1 = __ldcg(A.q_start + b + 1);
+      const int64_t ctx = __ldcg(A.ctx + b);
+      int T = q1 - q0;
+      if (q0 < 0 || q1 < q0 || q1 > A.N || T > A.max_tree || ctx < 0 ||
+          ctx + T > (int64_t)A.max_vb * A.L.bs * A.L.dcp) {
+        if (!A.per_rank || e % A.L.dcp == 0) count_error(A.err);
+        T = 0;
+      }
+      if (!A.per_rank || e % A.L.dcp == 0) A.nodes[b] = T;
+      if (T > 0) {
+        const int r0 = A.per_rank ? e % A.L.dcp : 0, r1 = A.per_rank ? r0 + 1 : A.L.dcp;
+        for (int r = r0; r < r1; ++r)
+          tiles += (tree_local(ctx + T, r, A.L) + A.tile - 1) / A.tile;
+        if (tiles > 0) units = A.Hkv * ((T * A.G + A.rows - 1) / A.rows);
+        tiles *= units;
+      }
+    }
+    // scan both over the CTA
+    int64_t t = tiles;
+    int u = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t pt = __shfl_up_sync(0xffffffffu, t, o);
+      const int pu = __shfl_up_sync(0xffffffffu, u, o);
+      if (lane >= o) {
+        t += pt;
+        u += pu;
+      }
+    }
+    __syncthreads();
+    if (lane == 31) {
+      sh_t[w] = t;
+      sh_u[w] = u;
+    }
+    __syncthreads();
+    int64_t bt = run_t;
+    int bu = run_u;
+    for (int i = 0; i < kTreePlanThreads / 32; ++i) {
+      if (i < w) {
+        bt += sh_t[i];
+        bu += sh_u[i];
+      }
+      run_t += sh_t[i];
+      run_u += sh_u[i];
+    }
+    if (e < E) {
+      A.first_tile[e] = bt + t - tiles;
+      A.first_unit[e] = bu + u - units;
+    }
+  }
+  if (tid == 0) {
+    A.first_tile[E] = run_t;
+    A.first_unit[E] = run_u;
+    A.hdr[0] = run_t < A.parts ? (int)run_t : A.parts;
+    A.hdr[1] = 0;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// writing a row
+// ---------------------------------------------------------------------------
+
+// Factor for an unnormalised row (maximum m in log2 units, sum l) with an
+// optional sink, and its LSE in log2 units (-inf: nothing was seen).
+__device__ __forceinline__ float tree_close(float m, float l, bool has_sink, float sink,
+                                            float& lse2) {
+  if (has_sink) {
+    const float s2 = sink * kLog2e, M = fmaxf(m, s2);
+    if (M > -INFINITY) {
+      const float a = m == -INFINITY ? 0.f : exp2f(m - M);
+      const float L = l * a + exp2f(s2 - M);
+      lse2 = M + log2f(L);
+      return a / L;
+    }
+  }
+  if (l == 0.f) {
+    lse2 = -INFINITY;
+    return 0.f;
+  }
+  lse2 = m + log2f(l);
+  return 1.f / l;
+}
+
+// ---------------------------------------------------------------------------
+// CUDA-core kernel
+// ---------------------------------------------------------------------------
+
+constexpr int kTgRows = 32;     // query rows of a CTA, four per warp
+constexpr int kTgTile = 32;     // tokens of a tile, one per lane
+constexpr int kTgWarps = 8;
+constexpr int kTgPad = 4;       // floats: a lane's 16-byte reads of its own K row hit 32 banks
+
+template <typename T>
+struct Chunk;                   // 16 bytes of T as floats
+template <>
+struct Chunk<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ void to(const uint4& x, float* f) {
+    f[0] = __uint_as_float(x.x);
+    f[1] = __uint_as_float(x.y);
+    f[2] = __uint_as_float(x.z);
+    f[3] = __uint_as_float(x.w);
+  }
+};
+template <>
+struct Chunk<__nv_bfloat16> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ void to(const uint4& x, float* f) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+};
+
+// Scores on the lanes (lane = token of the tile, K row from shared memory),
+// output on the lanes as well (lane owns entries lane + 32 i); a warp carries
+// four query rows so that each K and V value read serves four products.
+// Masked tokens are skipped, not multiplied by zero: their values may be
+// anything.
+template <typename T, int DPL>
+__global__ void __launch_bounds__(kTgWarps * 32)
+tree_generic_kernel(const __grid_constant__ TreeArgs A) {
+  extern __shared__ float sm[];
+  __shared__ int64_t s_row[kTgTile];   // K/V row of a token, -1: not there
+  __shared__ int s_code[kTgTile];      // node, 64: seen by all, 255: by none
+  const int d = A.d, ks = d + kTgPad;
+  float* sq = sm;                      // [rows][d]
+  float* sk = sq + kTgRows * d;        // [tile][d + pad]
+  float* sv = sk + kTgTile * ks;       // [tile][d]
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int E = A.per_rank ? A.B * A.L.dcp : A.B;
+  const int64_t total = __ldcg(A.first_tile + E);
+  const int parts = __ldcg(A.hdr);
+  for (int run = blockIdx.x; run < parts; run += gridDim.x) {
+    const int64_t begin = tree_run(total, parts, run), end = tree_run(total, parts, run + 1);
+    int e = tree_entry(A, E, begin);
+    for (int64_t t = begin; t < end;) {
+      const TreePiece p = tree_piece(A, e, t, begin, end, run);
+      t += p.n;
+      const int T_b = __ldcg(A.nodes + p.b);
+      const int64_t ctx = __ldcg(A.ctx + p.b), len = ctx + T_b;
+      const int row0 = p.rb * kTgRows, nrows = min(kTgRows, T_b * A.G - row0);
+      __syncthreads();                 // the last piece is done with sq
+      for (int i = tid; i < kTgRows * d; i += kTgWarps * 32) {
+        const int row = i / d, c = i - row * d;
+        float x = 0.f;
+        if (row < nrows) {
+          const int rr = row0 + row;
+          const int64_t tok = __ldcg(A.q_start + p.b) + rr / A.G;
+          x = (float)__ldcg((const T*)A.q + (tok * A.Hq + p.g * A.G + rr % A.G) * d + c);
+        }
+        sq[i] = x;
+      }
+      uint64_t mask[4];
+      float m[4], l[4], o[4][DPL];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = warp * 4 + x;
+        mask[x] = row < nrows
+                      ? __ldcg((const unsigned long long*)A.mask + __ldcg(A.q_start + p.b) + (row0 + row) / A.G)
+                      : 0ull;
+        m[x] = -INFINITY;
+        l[x] = 0.f;
+#pragma unroll
+        for (int i = 0; i < DPL; ++i) o[x][i] = 0.f;
+      }
+      // rank and tile within the rank of the piece's first tile
+      int r = p.r0, tr = p.t0;
+      int n_r = tree_local(len, r, A.L);
+      for (int step = 0; step < p.n; ++step) {
+        while (tr >= (n_r + kTgTile - 1) / kTgTile) {
+          tr -= (n_r + kTgTile - 1) / kTgTile;
+          n_r = tree_local(len, ++r, A.L);
+        }
+        const int p0 = tr * kTgTile;
+        ++tr;
+        __syncthreads();               // the last tile is done with sk, sv
+        if (tid < kTgTile) {
+          const int pos = p0 + tid;
+          int code = 255;
+          int64_t row = -1;
+          if (pos < n_r) {
+            const int j = pos / A.L.bs;
+            const int64_t phys =
+                j < A.max_vb ? (int64_t)__ldcg(A.bt + r * A.stride + (int64_t)p.b * A.max_vb + j) : -1;
+            if (phys >= 0 && phys < A.nb) {
+              row = (phys * A.Hkv + p.g) * A.L.bs + (pos - j * A.L.bs);
+              const int64_t x = tree_global(pos, r, A.L) - ctx;
+              code = x < 0 ? 64 : (int)x;
+            } else {
+              count_error(A.err);
+            }
+          }
+          s_row[tid] = row;
+          s_code[tid] = code;
+        }
+        __syncthreads();
+        constexpr int CN = Chunk<T>::n;
+        const int cpr = d / CN;
+        const T* kp = (const T*)A.k.ptr[r];
+        const T* vp = (const T*)A.v.ptr[r];
+        for (int i = tid; i < kTgTile * cpr; i += kTgWarps * 32) {
+          const int j = i / cpr, c = (i - j * cpr) * CN;
+          const int64_t row = s_row[j];
+          float f[CN], g[CN];
+          if (row >= 0) {
+            Chunk<T>::to(__ldcg((const uint4*)(kp + row * d + c)), f);
+            Chunk<T>::to(__ldcg((const uint4*)(vp + row * d + c)), g);
+          } else {
+#pragma unroll
+            for (int x = 0; x < CN; ++x) f[x] = g[x] = 0.f;
+          }
+#pragma unroll
+          for (int x = 0; x < CN; x += 4) {
+            *(float4*)(sk + j * ks + c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
+            *(float4*)(sv + j * d + c + x) = make_float4(g[x], g[x + 1], g[x + 2], g[x + 3]);
+          }
+        }
+        __syncthreads();
+        if (warp * 4 >= nrows) continue;   // no rows here (uniform in the warp)
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        const float4* kr = (const float4*)(sk + lane * ks);
+        const float4* qr = (const float4*)(sq + warp * 4 * d);
+        const int d4 = d >> 2;
+#pragma unroll 4
+        for (int c = 0; c < d4; ++c) {
+          const float4 a = kr[c];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float4 b = qr[x * d4 + c];
+            s[x] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s[x]))));
+          }
+        }
+        const int code = s_code[lane];
+        float pr[4];
+        uint32_t vis[4];
+        bool all = true;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const bool on = code == 64 || (code < 64 && ((mask[x] >> code) & 1));
+          vis[x] = __ballot_sync(0xffffffffu, on);
+          all = all && vis[x] == 0xffffffffu;
+          const float sc = on ? s[x] * A.sl2 : -INFINITY;
+          const float mn = fmaxf(m[x], warp_max(sc));
+          const float mb = mn == -INFINITY ? 0.f : mn;
+          const float al = exp2f(m[x] - mb);
+          pr[x] = on ? exp2f(sc - mb) : 0.f;
+          l[x] = l[x] * al + pr[x];      // this lane's tokens
+          m[x] = mn;
+#pragma unroll
+          for (int i = 0; i < DPL; ++i) o[x][i] *= al;
+        }
+        if (all) {
+#pragma unroll 4
+          for (int j = 0; j < kTgTile; ++j) {
+            float pj[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) pj[x] = __shfl_sync(0xffffffffu, pr[x], j);
+#pragma unroll
+            for (int i = 0; i < DPL; ++i)
+              if (i * 32 < d) {
+                const float v = sv[j * d + i * 32 + lane];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[x][i] = fmaf(pj[x], v, o[x][i]);
+              }
+          }
+        } else {
+          for (int j = 0; j < kTgTile; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              if (!((vis[x] >> j) & 1)) continue;
+              const float pj = __shfl_sync(0xffffffffu, pr[x], j);
+#pragma unroll
+              for (int i = 0; i < DPL; ++i)
+                if (i * 32 < d) o[x][i] = fmaf(pj, sv[j * d + i * 32 + lane], o[x][i]);
+            }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = warp * 4 + x;
+        if (row >= nrows) continue;
+        const float lt = warp_sum(l[x]);
+        float lse2;
+        if (p.slot >= 0) {
+          const float f = tree_close(m[x], lt, false, 0.f, lse2);
+          float* dst = A.part_o + ((int64_t)p.slot * kTgRows + row) * d;
+#pragma unroll
+          for (int i = 0; i < DPL; ++i)
+            if (i * 32 < d) dst[i * 32 + lane] = lt == 0.f ? 0.f : o[x][i] * f;
+          if (lane == 0) A.part_lse[(int64_t)p.slot * kTgRows + row] = lse2;
+          continue;
+        }
+        const int h = p.g * A.G + (row0 + row) % A.G;
+        const bool sunk = A.sink != nullptr;
+        const float f = tree_close(m[x], lt, sunk, sunk ? __ldcg(A.sink + h) : 0.f, lse2);
+        const int64_t orow = tree_out_row(A, p, row0 + row);
+#pragma unroll
+        for (int i = 0; i < DPL; ++i)
+          if (i * 32 < d) {
+            const float y = lt == 0.f ? 0.f : o[x][i] * f;
+            if (A.out_dtype == DCP_F32)
+              ((float*)A.out)[orow * d + i * 32 + lane] = y;
+            else
+              ((__nv_bfloat16*)A.out)[orow * d + i * 32 + lane] = __float2bfloat16_rn(y);
+          }
+        if (lane == 0 && A.lse) A.lse[orow] = lse2 * kLn2;
+      }
+    }
+  }
+}
+
+template <typename T>
+static int launch_tree_generic(const TreeArgs& A, cudaStream_t s) {
+  const int smem = (int)sizeof(float) * (kTgRows * A.d + kTgTile * (A.d + kTgPad) + kTgTile * A.d);
+  auto go = [&](auto kernel) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return (int)DCP_ECUDA;
+    }
+    const cudaError_t e = launch_chained(kernel, (unsigned)A.parts, kTgWarps * 32, smem, s, A);
+    return e == cudaSuccess ? launch_status() : launch_status_report(e);
+  };
+  if (A.d <= 64) return go(tree_generic_kernel<T, 2>);
+  if (A.d <= 128) return go(tree_generic_kernel<T, 4>);
+  return go(tree_generic_kernel<T, 8>);
+}
+
+// ---------------------------------------------------------------------------
+// merge of cut units, and of ranks that hold nothing
+// ---------------------------------------------------------------------------
+
+// One warp per output row.  Rows whose unit lay in one run were written by its
+// CTA; rows of refused requests and behind the last request stay as they were.
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs A) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int E = A.per_rank ? A.B * A.L.dcp : A.B;
+  const int64_t total = __ldcg(A.first_tile + E);
+  const int parts = __ldcg(A.hdr);
+  const int64_t rows = (int64_t)A.N * A.Hq * (A.per_rank ? A.L.dcp : 1);
+  for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8ll) {
+    const int h = (int)(row % A.Hq);
+    const int tok = (int)(row / A.Hq % A.N);
+    const int r = (int)(row / A.Hq / A.N);
+    // the last request that starts at or before the token and has it
+    int lo = 0, hi = A.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldcg(A.q_start + mid) <= tok) lo = mid; else hi = mid;
+    }
+    const int j = tok - __ldcg(A.q_start + lo);
+    if (j < 0 || j >= __ldcg(A.nodes + lo)) continue;
+    const int e = A.per_rank ? lo * A.L.dcp + r : lo;
+    const int64_t base = __ldcg(A.first_tile + e);
+    const int units = __ldcg(A.first_unit + e + 1) - __ldcg(A.first_unit + e);
+    float* of = (float*)A.out + row * A.d;
+    __nv_bfloat16* ob = (__nv_bfloat16*)A.out + row * A.d;
+    if (units == 0) {   // a rank without tokens of this request
+      for (int c = lane; c < A.d; c += 32) of[c] = 0.f;
+      if (lane == 0) A.lse[row] = -INFINITY;
+      continue;
+    }
+    const int per = (int)((__ldcg(A.first_tile + e + 1) - base) / units);
+    const int g = h / A.G, ur = j * A.G + h % A.G;   // row of the unit's request
+    const int rb = ur / A.rows, rr = ur - rb * A.rows;
+    const int64_t t0 = base + (int64_t)(g * (units / A.Hkv) + rb) * per;
+    const int k0 = tree_run_of(total, parts, t0), k1 = tree_run_of(total, parts, t0 + per - 1);
+    if (k0 == k1) continue;
+    const bool late = tree_run(total, parts, k0) != t0;   // run k0 began before this unit
+    float M = -INFINITY;
+    for (int k = k0; k <= k1; ++k)
+      M = fmaxf(M, __ldcg(A.part_lse + (int64_t)(2 * k + (k == k0 && late)) * A.rows + rr));
+    const bool sunk = A.sink != nullptr;
+    const float s2 = sunk ? __ldcg(A.sink + h) * kLog2e : -INFINITY;
+    M = fmaxf(M, s2);
+    const float mb = M == -INFINITY ? 0.f : M;
+    float L = sunk ? exp2f(s2 - mb) : 0.f;
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    for (int k = k0; k <= k1; ++k) {
+      const int64_t slot = (int64_t)(2 * k + (k == k0 && late)) * A.rows + rr;
+      const float lse = __ldcg(A.part_lse + slot);
+      if (lse == -INFINITY) continue;    // saw nothing: its values do not count
+      const float wgt = exp2f(lse - mb);
+      L += wgt;
+      const float* src = A.part_o + slot * A.d;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i * 32 < A.d) acc[i] = fmaf(wgt, __ldcg(src + i * 32 + lane), acc[i]);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i * 32 < A.d) {
+        if (A.out_dtype == DCP_F32)
+          of[i * 32 + lane] = acc[i] * inv;
+        else
+          ob[i * 32 + lane] = __float2bfloat16_rn(acc[i] * inv);
+      }
+    if (lane == 0 && A.lse) A.lse[row] = L == 0.f ? -INFINITY : (mb + log2f(L)) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+// Query rows of a CTA, tokens of a tile and runs of the kernel for a call.
+struct TreeShape {
+  int rows, tile, parts;
+};
+
+static TreeShape tree_shape(bool tc, int G, int max_tree) {
+  (void)tc;
+  (void)G;
+  (void)max_tree;
+  return TreeShape{kTgRows, kTgTile, 4 * num_sms()};
+}
+
+static size_t tree_carve(TreeArgs* A, void* ws, int B, int dcp, int parts, int rows, int d) {
+  const size_t E = (size_t)B * dcp;   // enough for both kinds of entries
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = (char*)ws + at;
+    at += align_up(bytes, 256);
+    return p;
+  };
+  char* hdr = take(16);
+  char* ft = take(sizeof(int64_t) * (E + 1));
+  char* fu = take(sizeof(int32_t) * (E + 1));
+  char* nd = take(sizeof(int32_t) * (size_t)B);
+  char* pl = take(sizeof(float) * 2 * (size_t)parts * rows);
+  char* po = take(sizeof(float) * 2 * (size_t)parts * rows * d);
+  if (A) {
+    A->hdr = (int32_t*)hdr;
+    A->first_tile = (int64_t*)ft;
+    A->first_unit = (int32_t*)fu;
+    A->nodes = (int32_t*)nd;
+    A->part_lse = (float*)pl;
+    A->part_o = (float*)po;
+  }
+  return at;
+}
+
+static bool tree_shape_ok(const dcp_layout_t& L, int B, int max_tree, int Hq, int Hkv, int d,
+                          dcp_dtype_t dtype) {
+  return layout_ok(L) && B >= 0 && max_tree >= 1 && max_tree <= kTreeMaxNodes && Hq >= 1 &&
+         Hkv >= 1 && Hq % Hkv == 0 && Hq / Hkv <= 16 && d >= 32 && d % 32 == 0 && d <= 256 &&
+         (dtype == DCP_F32 || dtype == DCP_BF16);
+}
+
+static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q_start, int N,
+                     int B, int max_tree, int Hq, int Hkv, int d, float scale, dcp_dtype_t dtype,
+                     const dcp_paged_kv_t& kv, const int32_t* ctx, const uint64_t* mask,
+                     const float* sink, void* out, dcp_dtype_t out_dtype, float* lse,
+                     bool per_rank, void* ws, size_t ws_bytes, int32_t* err, cudaStream_t s) {
+  if (!tree_shape_ok(layout, B, max_tree, Hq, Hkv, d, dtype) || N < 0 || kv.num_blocks < 0 ||
+      kv.max_vblocks < 0 || kv.bt_rank_stride < 0 || !(scale > 0.f) ||
+      (out_dtype != DCP_F32 && out_dtype != DCP_BF16))
+    return DCP_EINVAL;
+  if (N == 0 || B == 0) return DCP_OK;
+  if (!q || !q_start || !ctx || !mask || !out || (per_rank && !lse) || !kv.block_table ||
+      !ranks_ok(kv.k, layout.dcp_size) || !ranks_ok(kv.v, layout.dcp_size))
+    return DCP_EINVAL;
+  if ((int64_t)B * layout.dcp_size * Hkv * 64 >= (int64_t(1) << 30) ||
+      (int64_t)kv.max_vblocks * layout.block_size * layout.dcp_size >= (int64_t(1) << 31) ||
+      ((uintptr_t)q & 15))
+    return DCP_EUNSUPPORTED;
+  for (int r = 0; r < layout.dcp_size; ++r)
+    if (((uintptr_t)kv.k.ptr[r] & 15) || ((uintptr_t)kv.v.ptr[r] & 15)) return DCP_EUNSUPPORTED;
+  const TreeShape S = tree_shape(false, Hq / Hkv, max_tree);
+  TreeArgs A;
+  A.q = q;
+  A.q_start = q_start;
+  A.ctx = ctx;
+  A.mask = mask;
+  A.N = N;
+  A.B = B;
+  A.Hq = Hq;
+  A.Hkv = Hkv;
+  A.G = Hq / Hkv;
+  A.d = d;
+  A.max_tree = max_tree;
+  A.L = Layout{layout.dcp_size, layout.block_size, layout.interleave};
+  A.per_rank = per_rank ? 1 : 0;
+  A.rows = S.rows;
+  A.tile = S.tile;
+  A.parts = S.parts;
+  A.sl2 = scale * kLog2e;
+  A.k = kv.k;
+  A.v = kv.v;
+  A.bt = kv.block_table;
+  A.max_vb = kv.max_vblocks;
+  A.stride = kv.bt_rank_stride;
+  A.nb = kv.num_blocks;
+  A.sink = sink;
+  A.out = out;
+  A.out_dtype = out_dtype;
+  A.lse = lse;
+  A.err = err;
+  const size_t need = tree_carve(&A, ws, B, layout.dcp_size, S.parts, S.rows, d);
+  if (!ws || ws_bytes < need) return DCP_EWORKSPACE;
+  cudaError_t e = launch_chained(tree_plan_kernel, 1, kTreePlanThreads, 0, s, A);
+  if (e != cudaSuccess) return launch_status_report(e);
+  const int rc = dtype == DCP_F32 ? launch_tree_generic<float>(A, s)
+                                  : launch_tree_generic<__nv_bfloat16>(A, s);
+  if (rc != DCP_OK) return rc;
+  const int64_t rows = (int64_t)N * Hq * (per_rank ? layout.dcp_size : 1);
+  const int64_t blocks = (rows + 7) / 8, most = (int64_t)8 * num_sms();
+  e = launch_chained(tree_merge_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, s, A);
+  if (e != cudaSuccess) return launch_status_report(e);
+  return launch_status();
+}
+
+}  // namespace dcp
+
+using namespace dcp;
+
+extern "C" {
+
+int dcp_tree_workspace_size(dcp_layout_t layout, int32_t num_reqs, int32_t max_tree,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                            dcp_dtype_t dtype, size_t* bytes) {
+  if (!bytes || !tree_shape_ok(layout, num_reqs, max_tree, num_q_heads, num_kv_heads, head_dim,
+                               dtype))
+    return DCP_EINVAL;
+  const TreeShape S = tree_shape(false, num_q_heads / num_kv_heads, max_tree);
+  *bytes = tree_carve(nullptr, nullptr, num_reqs, layout.dcp_size, S.parts, S.rows, head_dim);
+  return DCP_OK;
+}
+
+int dcp_tree_partial_gqa(dcp_layout_t layout, const void* q, const int32_t* q_start,
+                         int32_t num_tokens, int32_t num_reqs, int32_t max_tree,
+                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                         dcp_dtype_t dtype, dcp_paged_kv_t kv, const int32_t* ctx_lens,
+                         const uint64_t* tree_mask, float* part_o, float* part_lse,
+                         void* workspace, size_t workspace_bytes, int32_t* err_count,
+                         dcp_stream_t stream) {
+  dcp::NvtxRange nvtx_range("dcp_tree_partial_gqa");
+  return tree_call(layout, q, q_start, num_tokens, num_reqs, max_tree, num_q_heads, num_kv_heads,
+                   head_dim, scale, dtype, kv, ctx_lens, tree_mask, nullptr, part_o, DCP_F32,
+                   part_lse, true, workspace, workspace_bytes, err_count, (cudaStream_t)stream);
+}
+
+int dcp_tree_decode_gqa(dcp_layout_t layout, const void* q, const int32_t* q_start,
+                        int32_t num_tokens, int32_t num_reqs, int32_t max_tree,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                        dcp_dtype_t dtype, dcp_paged_kv_t kv, const int32_t* ctx_lens,
+                        const uint64_t* tree_mask, const float* sink, void* out,
+                        dcp_dtype_t out_dtype, float* out_lse, void* workspace,
+                        size_t workspace_bytes, int32_t* err_count, dcp_stream_t stream) {
+  dcp::NvtxRange nvtx_range("dcp_tree_decode_gqa");
+  return tree_call(layout, q, q_start, num_tokens, num_reqs, max_tree, num_q_heads, num_kv_heads,
+                   head_dim, scale, dtype, kv, ctx_lens, tree_mask, sink, out, out_dtype, out_lse,
+                   false, workspace, workspace_bytes, err_count, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -470,6 +470,221 @@ int dcp_sfa_decode(dcp_layout_t layout, const void* q, int32_t num_reqs, int32_t
                    dcp_dtype_t out_dtype, float* out_lse, void* workspace,
                    size_t workspace_bytes, int32_t* err_count, dcp_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Around the decode step: drafted token trees, rotary positions, pages.
+ * ---------------------------------------------------------------------------
+ * The pages name none of these; they are what a serving loop runs next to the
+ * calls above, over the same sharded paged cache.  Each takes the cache as the
+ * other calls leave it and leaves it as they read it.
+ */
+
+/* Most drafted nodes of a request: one bit each of a node's mask. */
+#define DCP_MAX_TREE 64
+
+/*
+ * dcp_tree_decode_gqa -- attention of drafted token trees over the sharded
+ * paged cache: dcp_decode_gqa for several queries per request.  Request b has
+ * ctx_lens[b] cached tokens and T_b = q_start[b+1] - q_start[b] drafted nodes,
+ * whose keys and values are stored behind them (node j at position
+ * ctx_lens[b] + j; its rotary position may be another).  A node sees every
+ * cached token and the nodes whose bits its mask has:
+ *     lse = ln( sum_visible exp(s) + exp(sink[h]) ),  s = scale * q.k,
+ *     o   = sum_visible exp(s - lse) * v.
+ * A node that sees nothing gives o = 0 and lse = -inf (with a sink, o = 0 and
+ * the sink's logit).  Keys and values of unseen nodes do not count, whatever
+ * they hold (infinities and NaN too).
+ *  q          [num_tokens][num_q_heads][head_dim], the requests' nodes packed.
+ *  q_start    [num_reqs + 1] int32, not decreasing, within [0, num_tokens].
+ *             Rows outside every request are left as they were.
+ *  max_tree   most nodes of a request, 1 .. DCP_MAX_TREE (a host bound).
+ *  ctx_lens   [num_reqs] int32, each >= 0.
+ *  tree_mask  [num_tokens] uint64: bit j = sees node j of its request.  Bits of
+ *             nodes that the request does not have are ignored.
+ *  out        [num_tokens][num_q_heads][head_dim] of out_dtype;
+ *  out_lse    [num_tokens][num_q_heads] float32 or NULL.
+ * A request with a negative length, more than max_tree nodes, rows outside
+ * [0, num_tokens] or tokens beyond max_vblocks bumps err_count and its rows
+ * are left as they were.  Unusable block-table entries are skipped and counted
+ * as in dcp_decode_gqa.
+ * Supported: dtype F32 or BF16, head_dim a multiple of 32 up to 256,
+ * num_q_heads / num_kv_heads <= 16, scale > 0, q and the pools 16-byte aligned.
+ */
+int dcp_tree_decode_gqa(dcp_layout_t layout, const void* q, const int32_t* q_start,
+                        int32_t num_tokens, int32_t num_reqs, int32_t max_tree,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                        dcp_dtype_t dtype, dcp_paged_kv_t kv, const int32_t* ctx_lens,
+                        const uint64_t* tree_mask, const float* sink, void* out,
+                        dcp_dtype_t out_dtype, float* out_lse, void* workspace,
+                        size_t workspace_bytes, int32_t* err_count, dcp_stream_t stream);
+
+/*
+ * dcp_tree_partial_gqa -- the same per rank, without the sink: what each rank
+ * hands to dcp_lse_merge (page "Decode Context Parallel (DCP)", section
+ * "Decode").
+ *  part_o   [dcp_size][num_tokens][num_q_heads][head_dim] float32, part_lse
+ *           [dcp_size][num_tokens][num_q_heads] float32 (a rank on which a
+ *           node sees nothing: 0 and -inf).
+ */
+int dcp_tree_partial_gqa(dcp_layout_t layout, const void* q, const int32_t* q_start,
+                         int32_t num_tokens, int32_t num_reqs, int32_t max_tree,
+                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                         dcp_dtype_t dtype, dcp_paged_kv_t kv, const int32_t* ctx_lens,
+                         const uint64_t* tree_mask, float* part_o, float* part_lse,
+                         void* workspace, size_t workspace_bytes, int32_t* err_count,
+                         dcp_stream_t stream);
+
+/* Bytes of workspace of both calls (for any lengths and trees up to max_tree). */
+int dcp_tree_workspace_size(dcp_layout_t layout, int32_t num_reqs, int32_t max_tree,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                            dcp_dtype_t dtype, size_t* bytes);
+
+/*
+ * dcp_rope_write_gqa -- rotary positions on the way into the cache: q and k of
+ * new tokens are rotated, q goes to q_out, and k and v to the slots that
+ * dcp_slot_mapping gave (dcp_cache_write_gqa's rules for slots).  Entries
+ * [0, rot_dim) of a head are rotated, the others copied.  Pair i is entries
+ * (i, i + rot_dim/2), or (2i, 2i + 1) with interleaved != 0, and turns by
+ *     angle = positions[axis[i]][t] * inv_freq[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ * cos and sin times `scaling`, in float32, rounded once.  The angle is exact
+ * to about 2^-31 of a turn for positions up to 2^32.
+ *  q, k, v    [num_tokens][heads][head_dim] of dtype; *_stride elements between
+ *             tokens (slices of one fused projection), heads in one piece.
+ *             num_q_heads may be 0 (q, q_out unused).  q_out may be q.
+ *  positions  [num_axes][num_tokens] int64 (time, height, width, ...).
+ *  inv_freq   [rot_dim/2] float32; axis [rot_dim/2] int32, or NULL (axis 0).
+ *             An axis outside [0, num_axes) counts as 0 and bumps err_count.
+ *  k_out      [num_tokens][num_kv_heads][head_dim]: the rotated keys once more
+ *             (for prefill attention), or NULL.
+ * Two tokens with one slot: either may stay.  rot_dim is a multiple of 16 up
+ * to 1024; rows and strides are multiples of 16 bytes and pointers 16-byte
+ * aligned.
+ */
+int dcp_rope_write_gqa(dcp_layout_t layout, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, int64_t num_tokens,
+                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                       dcp_dtype_t dtype, const int64_t* positions, int32_t num_axes,
+                       const float* inv_freq, const int32_t* axis, int32_t rot_dim,
+                       int32_t interleaved, float scaling, const int64_t* slot,
+                       int64_t num_blocks, dcp_rank_ptrs_t k_cache, dcp_rank_ptrs_t v_cache,
+                       void* q_out, void* k_out, int32_t* err_count, dcp_stream_t stream);
+
+/*
+ * dcp_rope_write_mla -- the same for a latent cache: the last rot_dim entries
+ * of each query head and of the latent row are rotated.
+ *  q [num_tokens][num_q_heads][kv_dim], kv [num_tokens][kv_dim].
+ */
+int dcp_rope_write_mla(dcp_layout_t layout, const void* q, int64_t q_stride, const void* kv,
+                       int64_t kv_stride, int64_t num_tokens, int32_t num_q_heads, int32_t kv_dim,
+                       dcp_dtype_t dtype, const int64_t* positions, int32_t num_axes,
+                       const float* inv_freq, const int32_t* axis, int32_t rot_dim,
+                       int32_t interleaved, float scaling, const int64_t* slot,
+                       int64_t num_blocks, dcp_rank_ptrs_t cache, void* q_out,
+                       int32_t* err_count, dcp_stream_t stream);
+
+/*
+ * The pages of a cache: who holds which.  One table per rank, or one for all
+ * ranks (bt_rank_stride == 0); T = tables.
+ *  block_table [T][num_reqs][max_vblocks] int32, -1 where a request has no page.
+ *  seq_lens    [num_reqs] int32 tokens of each request (0: an unused row).
+ *  ref_count   [T][num_blocks] int32 requests that hold a page.
+ *  free_bits   [T][(num_blocks + 31) / 32] uint32: bit set = free (count 0).
+ * A request of length n holds ceil(n / (block_size*dcp_size)) pages of each
+ * table.  The page that the next token is written to (the open page, unless it
+ * is full) is always the request's own.  max_vblocks*block_size*dcp_size < 2^31.
+ */
+typedef struct {
+  int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* ref_count;
+  uint32_t* free_bits;
+  int32_t num_reqs;
+  int32_t max_vblocks;
+  int64_t bt_rank_stride;
+  int64_t num_blocks;
+} dcp_pages_t;
+
+/* Every request unused, every page free. */
+int dcp_pages_init(dcp_layout_t layout, dcp_pages_t pages, dcp_stream_t stream);
+
+/* Bytes of workspace of dcp_pages_resize / dcp_pages_fork with `num` entries. */
+int dcp_pages_workspace_size(dcp_layout_t layout, dcp_pages_t pages, int32_t num, size_t* bytes);
+
+/*
+ * dcp_pages_resize -- admit, grow, trim and free requests: request req[n] gets
+ * length new_lens[n].  First every page behind the new lengths is released,
+ * then missing pages are allocated: the lowest free page goes to the first
+ * need, in the order of the list and of each request's blocks.  If a cut
+ * leaves an open page that others hold too, the request gets a page of its own
+ * instead, and the copy is asked for:
+ *  copy_src, copy_dst [T][num] int32: copy page src to dst (dcp_pages_copy) for
+ *           every layer before anything is written; -1: nothing to copy.
+ * An entry whose request is outside [0, num_reqs) or was named by an earlier
+ * entry, or whose length is negative or beyond max_vblocks, is skipped and
+ * bumps err_count.  When the pages run out, each page that is missing bumps
+ * err_count and its table entry is -1 (the tokens there are lost).
+ */
+int dcp_pages_resize(dcp_layout_t layout, dcp_pages_t pages, const int32_t* req,
+                     const int32_t* new_lens, int32_t num, int32_t* copy_src, int32_t* copy_dst,
+                     void* workspace, size_t workspace_bytes, int32_t* err_count,
+                     dcp_stream_t stream);
+
+/*
+ * dcp_pages_fork -- child[n] becomes a copy of parent[n] (samples, beams): what
+ * the child held is released, full pages are shared, and the open page gets a
+ * page of the child's own, to be copied as above.  Allocation as above.  A
+ * request that is both a parent and a child of the same call, a child named
+ * twice, and rows outside [0, num_reqs) bump err_count; the entry (for a child
+ * named twice the later one) is skipped.
+ */
+int dcp_pages_fork(dcp_layout_t layout, dcp_pages_t pages, const int32_t* parent,
+                   const int32_t* child, int32_t num, int32_t* copy_src, int32_t* copy_dst,
+                   void* workspace, size_t workspace_bytes, int32_t* err_count,
+                   dcp_stream_t stream);
+
+/*
+ * Every pool of a model with pages of the same shape: ptr [num_pools][dcp_size]
+ * DEVICE array of device addresses (keys and values of all layers; 16-byte
+ * aligned), each [num_blocks][num_heads][block_size][row_bytes].  A latent pool
+ * has num_heads 1.  row_bytes is a multiple of 16.
+ */
+typedef struct {
+  const uint64_t* ptr;
+  int32_t num_pools;
+  int32_t num_heads;
+  int32_t row_bytes;
+  int64_t num_blocks;
+} dcp_pool_set_t;
+
+/*
+ * dcp_pages_copy -- copy pages inside every pool of every rank, in one launch.
+ *  copy_src, copy_dst [num_tables][num] (num_tables 1: the same pages on every
+ *           rank; else dcp_size).  Both -1: nothing.  A page outside
+ *           [0, num_blocks) or an unaligned pool is skipped and counted.  No
+ *           page may be written twice or both read and written in one call.
+ */
+int dcp_pages_copy(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* copy_src,
+                   const int32_t* copy_dst, int32_t num_tables, int32_t num, int32_t* err_count,
+                   dcp_stream_t stream);
+
+/*
+ * dcp_cache_compact -- keep the accepted nodes of each request's drafted tree:
+ * in every pool, the token at position ctx_lens[b] + path[b][i] moves to
+ * position ctx_lens[b] + i, for i < path_len[b].
+ *  path     [num_reqs][max_path] int32, strictly increasing from >= 0.
+ *  path_len [num_reqs] int32, 0 .. max_path.
+ *  new_lens [num_reqs] int32 or NULL: ctx_lens[b] + nodes kept.
+ * The moves of a request stop at the first entry that breaks the order or does
+ * not resolve to a stored token, which bumps err_count once.  A bad length
+ * keeps nothing and counts once.
+ */
+int dcp_cache_compact(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* block_table,
+                      int32_t num_reqs, int32_t max_vblocks, int64_t bt_rank_stride,
+                      const int32_t* ctx_lens, const int32_t* path, const int32_t* path_len,
+                      int32_t max_path, int32_t* new_lens, int32_t* err_count,
+                      dcp_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,175 @@
+"""Host-side refusals of the calls around the decode step (CPU only: each
+returns before anything is launched; the pointers are never followed), and the
+page model that the GPU tests compare with."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from tests import serving_ref as R
+
+EINVAL, EWORKSPACE, EUNSUPPORTED = -1, -2, -4
+P = C.c_void_p(1 << 20)          # an aligned address that nothing reads
+
+
+@pytest.fixture(scope="module")
+def dcp():
+    from context_paged_decode_gb300 import build
+    build.build_all()
+    import context_paged_decode_gb300 as d
+    d.load()
+    return d
+
+
+def ranks(dcp, n, base=1 << 20):
+    rp = dcp.RankPtrs()
+    for i in range(n):
+        rp.ptr[i] = base
+    return rp
+
+
+def kv(dcp, n=2, base=1 << 20, max_vb=4, nb=8):
+    s = dcp.PagedKVStruct()
+    s.k = s.v = ranks(dcp, n, base)
+    s.num_blocks, s.block_table, s.max_vblocks, s.bt_rank_stride = nb, 1 << 20, max_vb, 16
+    return s
+
+
+def test_tree(dcp):
+    lib, L = dcp.load(), dcp.Layout(2, 16, 1)
+
+    def call(layout=L, q=P, start=P, N=5, B=2, most=4, Hq=8, Hkv=2, d=128, scale=1.0, dt=1,
+             cache=None, ctx=P, mask=P, out=P, odt=1, ws=P, n=1 << 40):
+        return lib.dcp_tree_decode_gqa(layout, q, start, N, B, most, Hq, Hkv, d, scale, dt,
+                                       cache or kv(dcp), ctx, mask, None, out, odt, None, ws, n,
+                                       None, None)
+
+    assert call(N=0) == 0 and call(B=0) == 0
+    for bad in (dict(layout=dcp.Layout(0, 16, 1)), dict(layout=dcp.Layout(2, 16, 3)), dict(N=-1),
+                dict(B=-1), dict(most=0), dict(most=65), dict(Hq=6, Hkv=4), dict(Hq=34, Hkv=2),
+                dict(Hkv=0), dict(d=0), dict(d=48), dict(d=288), dict(dt=2), dict(odt=2),
+                dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(q=None),
+                dict(start=None), dict(ctx=None), dict(mask=None), dict(out=None),
+                dict(cache=kv(dcp, 1)), dict(cache=kv(dcp, nb=-1)), dict(cache=kv(dcp, max_vb=-1))):
+        assert call(**bad) == EINVAL, bad
+    assert call(ws=None) == EWORKSPACE and call(n=100) == EWORKSPACE
+    assert call(q=C.c_void_p((1 << 20) + 2)) == EUNSUPPORTED
+    assert call(cache=kv(dcp, base=(1 << 20) + 8)) == EUNSUPPORTED
+    assert call(cache=kv(dcp, max_vb=1 << 27)) == EUNSUPPORTED
+    assert call(B=1 << 27) == EUNSUPPORTED
+    n = C.c_size_t(0)
+    assert lib.dcp_tree_workspace_size(L, 2, 4, 8, 2, 128, 1, C.byref(n)) == 0 and n.value > 0
+    assert lib.dcp_tree_workspace_size(L, 2, 65, 8, 2, 128, 1, C.byref(n)) == EINVAL
+    assert lib.dcp_tree_partial_gqa(L, P, P, 5, 2, 4, 8, 2, 128, 1.0, 1, kv(dcp), P, P, P, None, P,
+                                    1 << 40, None, None) == EINVAL
+
+
+def test_rope(dcp):
+    lib, L = dcp.load(), dcp.Layout(2, 16, 1)
+
+    def call(layout=L, q=P, qs=1024, k=P, ks=256, v=P, vs=256, T=3, Hq=8, Hkv=2, d=128, dt=1, pos=P,
+             axes=1, inv=P, rot=128, slot=P, nb=8, kc=None, vc=None, q_out=P, k_out=None):
+        return lib.dcp_rope_write_gqa(layout, q, qs, k, ks, v, vs, T, Hq, Hkv, d, dt, pos, axes,
+                                      inv, None, rot, 0, 1.0, slot, nb, kc or ranks(dcp, 2),
+                                      vc or ranks(dcp, 2), q_out, k_out, None, None)
+
+    assert call(T=0) == 0
+    for bad in (dict(layout=dcp.Layout(2, 16, 5)), dict(T=-1), dict(Hq=-1), dict(Hkv=0), dict(d=0),
+                dict(dt=7), dict(rot=0), dict(rot=144), dict(axes=0), dict(nb=-1), dict(q=None),
+                dict(q_out=None), dict(k=None), dict(v=None), dict(pos=None), dict(inv=None),
+                dict(slot=None), dict(kc=ranks(dcp, 1)), dict(vc=ranks(dcp, 1)), dict(qs=1000),
+                dict(ks=255), dict(vs=0)):
+        assert call(**bad) == EINVAL, bad
+    odd = C.c_void_p((1 << 20) + 8)
+    for bad in (dict(rot=24), dict(d=132, qs=1 << 20, ks=1 << 20, vs=1 << 20), dict(T=1 << 31),
+                dict(d=16384, qs=1 << 20, ks=1 << 20, vs=1 << 20), dict(q=odd), dict(k=odd),
+                dict(v=odd), dict(q_out=odd), dict(k_out=odd), dict(qs=1028), dict(ks=257),
+                dict(kc=ranks(dcp, 2, (1 << 20) + 4)), dict(Hq=1 << 30, qs=1 << 40)):
+        assert call(**bad) == EUNSUPPORTED, bad
+    mla = lambda **k: lib.dcp_rope_write_mla(  # noqa: E731
+        L, P, k.get("qs", 4608), P, k.get("ks", 576), 3, 8, 576, 1, P, 1, P, None, k.get("rot", 64),
+        1, 1.0, P, 8, ranks(dcp, k.get("n", 2)), P, None, None)
+    assert mla(rot=592) == EINVAL and mla(qs=4000) == EINVAL and mla(n=1) == EINVAL
+    assert mla(rot=56) == EUNSUPPORTED and mla(ks=577) == EUNSUPPORTED
+
+
+def test_pages(dcp):
+    lib, L = dcp.load(), dcp.Layout(2, 16, 1)
+
+    def pages(**k):
+        s = dict(block_table=1 << 20, seq_lens=1 << 20, ref_count=1 << 20, free_bits=1 << 20,
+                 num_reqs=4, max_vblocks=8, bt_rank_stride=32, num_blocks=100)
+        s.update(k)
+        return dcp.PagesStruct(*s.values())
+
+    def call(p=None, layout=L, a=P, b=P, n=3, src=P, dst=P, ws=P, nb=1 << 40, name="resize"):
+        return getattr(lib, "dcp_pages_" + name)(layout, p or pages(), a, b, n, src, dst, ws, nb,
+                                                 None, None)
+
+    for name in ("resize", "fork"):
+        assert call(n=0, name=name) == 0
+        for bad in (dict(layout=dcp.Layout(2, 0, 1)), dict(n=-1), dict(a=None), dict(b=None),
+                    dict(src=None), dict(dst=None), dict(p=pages(num_reqs=-1)),
+                    dict(p=pages(max_vblocks=-1)), dict(p=pages(num_blocks=-1)),
+                    dict(p=pages(bt_rank_stride=-1)), dict(p=pages(bt_rank_stride=31)),
+                    dict(p=pages(block_table=None)), dict(p=pages(seq_lens=None)),
+                    dict(p=pages(ref_count=None)), dict(p=pages(free_bits=None))):
+            assert call(name=name, **bad) == EINVAL, bad
+        assert call(ws=None, name=name) == EWORKSPACE and call(nb=64, name=name) == EWORKSPACE
+        assert call(p=pages(num_blocks=1 << 31), name=name) == EUNSUPPORTED
+        assert call(p=pages(max_vblocks=1 << 26, bt_rank_stride=1 << 40), name=name) == EUNSUPPORTED
+    n = C.c_size_t(0)
+    assert lib.dcp_pages_workspace_size(L, pages(), 3, C.byref(n)) == 0 and n.value > 0
+    assert lib.dcp_pages_workspace_size(L, pages(), -1, C.byref(n)) == EINVAL
+    assert lib.dcp_pages_init(L, pages(seq_lens=None), None) == EINVAL
+
+
+def test_moves(dcp):
+    lib, L = dcp.load(), dcp.Layout(2, 16, 1)
+
+    def pools(**k):
+        s = dict(ptr=1 << 20, num_pools=2, num_heads=2, row_bytes=256, num_blocks=8)
+        s.update(k)
+        return dcp.PoolSetStruct(*s.values())
+
+    copy = lambda p=None, L=L, src=P, dst=P, t=2, n=3: lib.dcp_pages_copy(  # noqa: E731
+        L, p or pools(), src, dst, t, n, None, None)
+    assert copy(n=0) == 0 and copy(p=pools(num_pools=0)) == 0
+    for bad in (dict(L=dcp.Layout(2, 16, 7)), dict(p=pools(num_pools=-1)), dict(p=pools(num_heads=0)),
+                dict(p=pools(row_bytes=0)), dict(p=pools(num_blocks=-1)), dict(p=pools(ptr=None)),
+                dict(src=None), dict(dst=None), dict(t=3), dict(n=-1)):
+        assert copy(**bad) == EINVAL, bad
+    assert copy(p=pools(row_bytes=24)) == EUNSUPPORTED
+
+    def move(p=None, L=L, bt=P, B=2, vb=4, stride=8, ctx=P, path=P, n=P, most=4):
+        return lib.dcp_cache_compact(L, p or pools(), bt, B, vb, stride, ctx, path, n, most, None,
+                                     None, None)
+
+    assert move(B=0) == 0
+    for bad in (dict(L=dcp.Layout(17, 16, 1)), dict(p=pools(ptr=None)), dict(bt=None), dict(B=-1),
+                dict(vb=-1), dict(stride=-1), dict(ctx=None), dict(path=None), dict(n=None),
+                dict(most=-1)):
+        assert move(**bad) == EINVAL, bad
+    assert move(p=pools(row_bytes=8)) == EUNSUPPORTED
+
+
+def test_page_model_keeps_its_invariants():
+    """Counts are the holders, every page is held or free, open pages have one holder."""
+    rng = np.random.default_rng(0)
+    for dcp, bs, I, shared in ((2, 4, 2, False), (3, 4, 4, False), (2, 4, 1, True)):
+        m = R.PageModel(dcp, bs, I, 6, 5, 80, shared)
+        for step in range(60):
+            if step % 3 < 2:
+                k = rng.permutation(6)[:3]
+                m.resize(k, rng.integers(0, 5 * bs * dcp + 1, 3))
+            else:
+                p = rng.permutation(6)
+                m.fork(p[3:], p[:3])
+            for t in range(m.tables):
+                held = np.bincount(m.bt[t][m.bt[t] >= 0], minlength=80)
+                assert np.array_equal(held, m.ref[t])
+                for b in range(6):
+                    assert ((m.bt[t, b] >= 0).sum()) == m.blocks(m.seq[b])
+                    at = m.open(int(m.seq[b]), t)
+                    assert at is None or m.ref[t, m.bt[t, b, at[0]]] == 1
+        assert m.err == 0
