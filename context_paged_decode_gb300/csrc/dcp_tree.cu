@@ -461,9 +461,7 @@ struct TreeShape {
 };
 
 static TreeShape tree_shape(bool tc, int G, int max_tree) {
-  (void)tc;
-  (void)G;
-  (void)max_tree;
+  if (tc) return TreeShape{max_tree * G <= 128 ? 128 : 256, 128, num_sms()};
   return TreeShape{kTgRows, kTgTile, 4 * num_sms()};
 }
 
@@ -518,7 +516,8 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
     return DCP_EUNSUPPORTED;
   for (int r = 0; r < layout.dcp_size; ++r)
     if (((uintptr_t)kv.k.ptr[r] & 15) || ((uintptr_t)kv.v.ptr[r] & 15)) return DCP_EUNSUPPORTED;
-  const TreeShape S = tree_shape(false, Hq / Hkv, max_tree);
+  const bool tc = tree_tc_supported(layout, d, dtype, kv, Hkv);
+  const TreeShape S = tree_shape(tc, Hq / Hkv, max_tree);
   TreeArgs A;
   A.q = q;
   A.q_start = q_start;
@@ -552,8 +551,9 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
   if (!ws || ws_bytes < need) return DCP_EWORKSPACE;
   cudaError_t e = launch_chained(tree_plan_kernel, 1, kTreePlanThreads, 0, s, A);
   if (e != cudaSuccess) return launch_status_report(e);
-  const int rc = dtype == DCP_F32 ? launch_tree_generic<float>(A, s)
-                                  : launch_tree_generic<__nv_bfloat16>(A, s);
+  const int rc = tc                 ? launch_tree_tc(A, s)
+                 : dtype == DCP_F32 ? launch_tree_generic<float>(A, s)
+                                    : launch_tree_generic<__nv_bfloat16>(A, s);
   if (rc != DCP_OK) return rc;
   const int64_t rows = (int64_t)N * Hq * (per_rank ? layout.dcp_size : 1);
   const int64_t blocks = (rows + 7) / 8, most = (int64_t)8 * num_sms();
@@ -574,8 +574,14 @@ int dcp_tree_workspace_size(dcp_layout_t layout, int32_t num_reqs, int32_t max_t
   if (!bytes || !tree_shape_ok(layout, num_reqs, max_tree, num_q_heads, num_kv_heads, head_dim,
                                dtype))
     return DCP_EINVAL;
-  const TreeShape S = tree_shape(false, num_q_heads / num_kv_heads, max_tree);
-  *bytes = tree_carve(nullptr, nullptr, num_reqs, layout.dcp_size, S.parts, S.rows, head_dim);
+  // a call on a cache too large for 32-bit rows takes the other kernel
+  *bytes = 0;
+  for (int tc = 0; tc <= (tree_tc_shape(head_dim, dtype, layout.block_size) ? 1 : 0); ++tc) {
+    const TreeShape S = tree_shape(tc != 0, num_q_heads / num_kv_heads, max_tree);
+    const size_t n =
+        tree_carve(nullptr, nullptr, num_reqs, layout.dcp_size, S.parts, S.rows, head_dim);
+    if (n > *bytes) *bytes = n;
+  }
   return DCP_OK;
 }
 

@@ -120,9 +120,11 @@ __device__ __forceinline__ int64_t tree_out_row(const TreeArgs& A, const TreePie
   return ((int64_t)(A.per_rank ? p.r0 : 0) * A.N + tok) * A.Hq + p.g * A.G + row % A.G;
 }
 
-// Rows of a block and tokens of a tile of the kernel that a call takes.
-bool tree_tc_supported(const dcp_layout_t& layout, int d, dcp_dtype_t dtype, const void* q,
-                       const dcp_paged_kv_t& kv);
+// The tensor-core kernel (dcp_tree_tc.cu): bf16, head_dim 64 or 128, pages of a
+// multiple of 16 tokens.  Blocks of 128 or 256 rows, tiles of 128 tokens.
+bool tree_tc_shape(int d, dcp_dtype_t dtype, int block_size);
+bool tree_tc_supported(const dcp_layout_t& layout, int d, dcp_dtype_t dtype,
+                       const dcp_paged_kv_t& kv, int Hkv);
 int launch_tree_tc(const TreeArgs& A, cudaStream_t s);
 
 }  // namespace dcp
