@@ -22,78 +22,86 @@ namespace dcp {
 // a read-only load may find a line that an earlier grid left there.
 constexpr int kTreePlanThreads = 256;
 
-// One CTA: checks the requests, counts each entry's tiles and units, and
-// prefix-sums them.
+// One CTA: checks the requests, counts each entry's tiles and units, sums them
+// up, and finds each run's first entry.
 __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __grid_constant__ TreeArgs A) {
   __shared__ int64_t sh_t[kTreePlanThreads / 32];
-  __shared__ int sh_u[kTreePlanThreads / 32];
+  __shared__ int64_t s_end[kTreePlanThreads];   // tiles up to each entry of the block
   griddep_launch_dependents();   // the next call's first kernel may start its launch
   griddep_wait();                // launched chained: the preceding kernel completed
   const int E = A.per_rank ? A.B * A.L.dcp : A.B;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   int64_t run_t = 0;
-  int run_u = 0;
-  for (int e0 = 0; e0 < E; e0 += kTreePlanThreads) {
-    const int e = e0 + tid;
-    int64_t tiles = 0;
-    int units = 0;
-    if (e < E) {
-      const int b = A.per_rank ? e / A.L.dcp : e;
-      const int q0 = __ldcg(A.q_start + b), q1 = __ldcg(A.q_start + b + 1);
-      const int64_t ctx = __ldcg(A.ctx + b);
-      int T = q1 - q0;
-      if (q0 < 0 || q1 < q0 || q1 > A.N || T > A.max_tree || ctx < 0 ||
-          ctx + T > (int64_t)A.max_vb * A.L.bs * A.L.dcp) {
-        if (!A.per_rank || e % A.L.dcp == 0) count_error(A.err);
-        T = 0;
+  // two rounds over the entries: the number of tiles decides where runs begin
+  for (int round = 0; round < (E > kTreePlanThreads ? 2 : 1); ++round) {
+    const int64_t total = run_t;
+    run_t = 0;
+    for (int e0 = 0; e0 < E; e0 += kTreePlanThreads) {
+      const int e = e0 + tid;
+      TreeEntry n;
+      n.units = n.per = n.nodes = n.ctx = n.q0 = n.pad = 0;
+      if (e < E) {
+        const int b = A.per_rank ? e / A.L.dcp : e, r = A.per_rank ? e % A.L.dcp : 0;
+        const int q0 = __ldcg(A.q_start + b), q1 = __ldcg(A.q_start + b + 1);
+        const int64_t ctx = __ldcg(A.ctx + b);
+        int T = q1 - q0;
+        if (q0 < 0 || q1 < q0 || q1 > A.N || T > A.max_tree || ctx < 0 ||
+            ctx + T > (int64_t)A.max_vb * A.L.bs * A.L.dcp) {
+          if (r == 0 && round == 0) count_error(A.err);
+          T = 0;
+        }
+        if (T > 0) {
+          const int r1 = A.per_rank ? r + 1 : A.L.dcp;
+          for (int x = r; x < r1; ++x)
+            n.per += (tree_local(ctx + T, x, A.L) + A.tile - 1) / A.tile;
+          if (n.per > 0) n.units = A.Hkv * ((T * A.G + A.rows - 1) / A.rows);
+          n.nodes = T;
+          n.ctx = (int)ctx;
+          n.q0 = q0;
+        }
       }
-      if (!A.per_rank || e % A.L.dcp == 0) A.nodes[b] = T;
-      if (T > 0) {
-        const int r0 = A.per_rank ? e % A.L.dcp : 0, r1 = A.per_rank ? r0 + 1 : A.L.dcp;
-        for (int r = r0; r < r1; ++r)
-          tiles += (tree_local(ctx + T, r, A.L) + A.tile - 1) / A.tile;
-        if (tiles > 0) units = A.Hkv * ((T * A.G + A.rows - 1) / A.rows);
-        tiles *= units;
-      }
-    }
-    // scan both over the CTA
-    int64_t t = tiles;
-    int u = units;
+      const int64_t tiles = (int64_t)n.units * n.per;
+      int64_t t = tiles;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t pt = __shfl_up_sync(0xffffffffu, t, o);
-      const int pu = __shfl_up_sync(0xffffffffu, u, o);
-      if (lane >= o) {
-        t += pt;
-        u += pu;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t pt = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o) t += pt;
       }
-    }
-    __syncthreads();
-    if (lane == 31) {
-      sh_t[w] = t;
-      sh_u[w] = u;
-    }
-    __syncthreads();
-    int64_t bt = run_t;
-    int bu = run_u;
-    for (int i = 0; i < kTreePlanThreads / 32; ++i) {
-      if (i < w) {
-        bt += sh_t[i];
-        bu += sh_u[i];
+      __syncthreads();
+      if (lane == 31) sh_t[w] = t;
+      __syncthreads();
+      const int64_t block0 = run_t;
+      int64_t before = run_t;
+      for (int i = 0; i < kTreePlanThreads / 32; ++i) {
+        if (i < w) before += sh_t[i];
+        run_t += sh_t[i];
       }
-      run_t += sh_t[i];
-      run_u += sh_u[i];
-    }
-    if (e < E) {
-      A.first_tile[e] = bt + t - tiles;
-      A.first_unit[e] = bu + u - units;
+      n.tile0 = before + t - tiles;
+      if (e < E && round == 0) A.entry[e] = n;
+      if (E <= kTreePlanThreads || round == 1) {
+        // runs that begin in this block's entries
+        s_end[tid] = n.tile0 + tiles;
+        __syncthreads();
+        const int64_t all = E <= kTreePlanThreads ? run_t : total;
+        const int parts = (int)(all < A.parts ? all : A.parts);
+        for (int k = tid; k < parts; k += kTreePlanThreads) {
+          const int64_t at = tree_run(all, parts, k);
+          if (at < block0 || at >= run_t) continue;
+          int lo = 0, hi = kTreePlanThreads - 1;   // first entry that ends behind `at`
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_end[mid] > at) hi = mid; else lo = mid + 1;
+          }
+          A.run_entry[k] = e0 + lo;
+        }
+        __syncthreads();
+      }
     }
   }
   if (tid == 0) {
-    A.first_tile[E] = run_t;
-    A.first_unit[E] = run_u;
     A.hdr[0] = run_t < A.parts ? (int)run_t : A.parts;
     A.hdr[1] = 0;
+    *reinterpret_cast<int64_t*>(A.hdr + 2) = run_t;
   }
 }
 
@@ -174,25 +182,20 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int E = A.per_rank ? A.B * A.L.dcp : A.B;
-  const int64_t total = __ldcg(A.first_tile + E);
-  const int parts = __ldcg(A.hdr);
-  for (int run = blockIdx.x; run < parts; run += gridDim.x) {
-    const int64_t begin = tree_run(total, parts, run), end = tree_run(total, parts, run + 1);
-    int e = tree_entry(A, E, begin);
-    for (int64_t t = begin; t < end;) {
-      const TreePiece p = tree_piece(A, e, t, begin, end, run);
-      t += p.n;
-      const int T_b = __ldcg(A.nodes + p.b);
-      const int64_t ctx = __ldcg(A.ctx + p.b), len = ctx + T_b;
-      const int row0 = p.rb * kTgRows, nrows = min(kTgRows, T_b * A.G - row0);
+  for (int run = blockIdx.x; run < A.parts; run += gridDim.x) {
+    TreeWalk walk = tree_walk(A, run);
+    while (walk.t < walk.end) {
+      const TreePiece p = tree_next(A, walk);
+      const int T_b = p.T;
+      const int64_t ctx = p.ctx, len = ctx + T_b;
+      const int row0 = p.rb * A.rows, nrows = min(A.rows, T_b * A.G - row0);
       __syncthreads();                 // the last piece is done with sq
       for (int i = tid; i < kTgRows * d; i += kTgWarps * 32) {
         const int row = i / d, c = i - row * d;
         float x = 0.f;
         if (row < nrows) {
           const int rr = row0 + row;
-          const int64_t tok = __ldcg(A.q_start + p.b) + rr / A.G;
+          const int64_t tok = p.q0 + rr / A.G;
           x = (float)__ldcg((const T*)A.q + (tok * A.Hq + p.g * A.G + rr % A.G) * d + c);
         }
         sq[i] = x;
@@ -203,7 +206,7 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
       for (int x = 0; x < 4; ++x) {
         const int row = warp * 4 + x;
         mask[x] = row < nrows
-                      ? __ldcg((const unsigned long long*)A.mask + __ldcg(A.q_start + p.b) + (row0 + row) / A.G)
+                      ? __ldcg((const unsigned long long*)A.mask + p.q0 + (row0 + row) / A.G)
                       : 0ull;
         m[x] = -INFINITY;
         l[x] = 0.f;
@@ -330,11 +333,11 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
         float lse2;
         if (p.slot >= 0) {
           const float f = tree_close(m[x], lt, false, 0.f, lse2);
-          float* dst = A.part_o + ((int64_t)p.slot * kTgRows + row) * d;
+          float* dst = A.part_o + ((int64_t)p.slot * A.rows + row) * d;
 #pragma unroll
           for (int i = 0; i < DPL; ++i)
             if (i * 32 < d) dst[i * 32 + lane] = lt == 0.f ? 0.f : o[x][i] * f;
-          if (lane == 0) A.part_lse[(int64_t)p.slot * kTgRows + row] = lse2;
+          if (lane == 0) A.part_lse[(int64_t)p.slot * A.rows + row] = lse2;
           continue;
         }
         const int h = p.g * A.G + (row0 + row) % A.G;
@@ -378,41 +381,34 @@ static int launch_tree_generic(const TreeArgs& A, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 
 // One warp per output row.  Rows whose unit lay in one run were written by its
-// CTA; rows of refused requests and behind the last request stay as they were.
+// CTA; rows of refused requests and outside every request stay as they were.
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs A) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int E = A.per_rank ? A.B * A.L.dcp : A.B;
-  const int64_t total = __ldcg(A.first_tile + E);
   const int parts = __ldcg(A.hdr);
-  const int64_t rows = (int64_t)A.N * A.Hq * (A.per_rank ? A.L.dcp : 1);
-  for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8ll) {
-    const int h = (int)(row % A.Hq);
-    const int tok = (int)(row / A.Hq % A.N);
-    const int r = (int)(row / A.Hq / A.N);
-    // the last request that starts at or before the token and has it
-    int lo = 0, hi = A.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldcg(A.q_start + mid) <= tok) lo = mid; else hi = mid;
-    }
-    const int j = tok - __ldcg(A.q_start + lo);
-    if (j < 0 || j >= __ldcg(A.nodes + lo)) continue;
-    const int e = A.per_rank ? lo * A.L.dcp + r : lo;
-    const int64_t base = __ldcg(A.first_tile + e);
-    const int units = __ldcg(A.first_unit + e + 1) - __ldcg(A.first_unit + e);
+  const int64_t total = __ldcg(reinterpret_cast<const int64_t*>(A.hdr + 2));
+  // rows in the order (rank,) request, node, head
+  const int64_t rows = (int64_t)A.B * A.max_tree * A.Hq * (A.per_rank ? A.L.dcp : 1);
+  for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < rows; i += gridDim.x * 8ll) {
+    const int h = (int)(i % A.Hq);
+    const int64_t br = i / A.Hq / A.max_tree;
+    const int j = (int)(i / A.Hq - br * A.max_tree);
+    const int r = (int)(br / A.B), b = (int)(br - (int64_t)r * A.B);
+    const TreeEntry n = tree_load(A, A.per_rank ? b * A.L.dcp + r : b);
+    if (j >= n.nodes) continue;
+    const int64_t row = ((int64_t)r * A.N + n.q0 + j) * A.Hq + h;
     float* of = (float*)A.out + row * A.d;
     __nv_bfloat16* ob = (__nv_bfloat16*)A.out + row * A.d;
-    if (units == 0) {   // a rank without tokens of this request
+    if (n.units == 0) {   // a rank without tokens of this request
       for (int c = lane; c < A.d; c += 32) of[c] = 0.f;
       if (lane == 0) A.lse[row] = -INFINITY;
       continue;
     }
-    const int per = (int)((__ldcg(A.first_tile + e + 1) - base) / units);
+    const int per = n.per;
     const int g = h / A.G, ur = j * A.G + h % A.G;   // row of the unit's request
     const int rb = ur / A.rows, rr = ur - rb * A.rows;
-    const int64_t t0 = base + (int64_t)(g * (units / A.Hkv) + rb) * per;
+    const int64_t t0 = n.tile0 + (int64_t)(g * (n.units / A.Hkv) + rb) * per;
     const int k0 = tree_run_of(total, parts, t0), k1 = tree_run_of(total, parts, t0 + per - 1);
     if (k0 == k1) continue;
     const bool late = tree_run(total, parts, k0) != t0;   // run k0 began before this unit
@@ -455,14 +451,17 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
 // host
 // ---------------------------------------------------------------------------
 
-// Query rows of a CTA, tokens of a tile and runs of the kernel for a call.
+// Query rows of a block (whole nodes), tokens of a tile and runs of the kernel
+// for a call.  The tensor-core kernel takes one 128-row tile of queries where
+// all nodes of a request fit it, else two.
 struct TreeShape {
   int rows, tile, parts;
 };
 
 static TreeShape tree_shape(bool tc, int G, int max_tree) {
-  if (tc) return TreeShape{max_tree * G <= 128 ? 128 : 256, 128, num_sms()};
-  return TreeShape{kTgRows, kTgTile, 4 * num_sms()};
+  if (!tc) return TreeShape{kTgRows / G * G, kTgTile, 4 * num_sms()};
+  const int nodes = 128 / G;
+  return TreeShape{(max_tree <= nodes ? 1 : 2) * nodes * G, 128, num_sms()};
 }
 
 static size_t tree_carve(TreeArgs* A, void* ws, int B, int dcp, int parts, int rows, int d) {
@@ -473,17 +472,15 @@ static size_t tree_carve(TreeArgs* A, void* ws, int B, int dcp, int parts, int r
     at += align_up(bytes, 256);
     return p;
   };
-  char* hdr = take(16);
-  char* ft = take(sizeof(int64_t) * (E + 1));
-  char* fu = take(sizeof(int32_t) * (E + 1));
-  char* nd = take(sizeof(int32_t) * (size_t)B);
+  char* hdr = take(32);
+  char* en = take(sizeof(TreeEntry) * E);
+  char* re = take(sizeof(int32_t) * (size_t)parts);
   char* pl = take(sizeof(float) * 2 * (size_t)parts * rows);
   char* po = take(sizeof(float) * 2 * (size_t)parts * rows * d);
   if (A) {
     A->hdr = (int32_t*)hdr;
-    A->first_tile = (int64_t*)ft;
-    A->first_unit = (int32_t*)fu;
-    A->nodes = (int32_t*)nd;
+    A->entry = (TreeEntry*)en;
+    A->run_entry = (int32_t*)re;
     A->part_lse = (float*)pl;
     A->part_o = (float*)po;
   }
@@ -555,7 +552,7 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
                  : dtype == DCP_F32 ? launch_tree_generic<float>(A, s)
                                     : launch_tree_generic<__nv_bfloat16>(A, s);
   if (rc != DCP_OK) return rc;
-  const int64_t rows = (int64_t)N * Hq * (per_rank ? layout.dcp_size : 1);
+  const int64_t rows = (int64_t)B * max_tree * Hq * (per_rank ? layout.dcp_size : 1);
   const int64_t blocks = (rows + 7) / 8, most = (int64_t)8 * num_sms();
   e = launch_chained(tree_merge_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, s, A);
   if (e != cudaSuccess) return launch_status_report(e);

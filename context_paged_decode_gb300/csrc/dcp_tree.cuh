@@ -25,7 +25,7 @@ struct TreeArgs {
   int N, B, Hq, Hkv, G, d, max_tree;
   Layout L;
   int per_rank;           // 0: a unit spans the ranks; 1: units per rank
-  int rows;               // query rows of a block
+  int rows;               // query rows of a block: whole nodes
   int tile;               // tokens of a tile
   int parts;              // most runs
   float sl2;              // scale * log2(e)
@@ -40,13 +40,37 @@ struct TreeArgs {
   float* lse;             // fused: [N][Hq] or NULL; partials: [dcp][N][Hq]
   int32_t* err;
   // workspace
-  int64_t* first_tile;    // [E + 1] first tile of entry e's units, E = B or B * dcp
-  int32_t* first_unit;    // [E + 1]
-  int32_t* nodes;         // [B] nodes of a request (0: none, or refused)
-  int32_t* hdr;           // runs in use, error word
-  float* part_o;          // [2 parts][rows][d], normalised
-  float* part_lse;        // [2 parts][rows], in log2 units
+  struct TreeEntry* entry;   // [E], E = B or B * dcp
+  int32_t* run_entry;        // [parts] entry of each run's first tile
+  int32_t* hdr;              // runs in use, error word, tiles (64 bits)
+  float* part_o;             // [2 parts][rows][d], normalised
+  float* part_lse;           // [2 parts][rows], in log2 units
 };
+
+// One request's units (on one rank, for partials), in one 32-byte read.
+struct __align__(32) TreeEntry {
+  int64_t tile0;   // first tile of its units
+  int32_t units;   // 0: none (refused, no nodes, or nothing on the rank)
+  int32_t per;     // tiles of a unit
+  int32_t nodes;
+  int32_t ctx;
+  int32_t q0;      // first token
+  int32_t pad;
+};
+
+__device__ __forceinline__ TreeEntry tree_load(const TreeArgs& A, int e) {
+  const int4* p = reinterpret_cast<const int4*>(A.entry + e);
+  const int4 x = __ldcg(p), y = __ldcg(p + 1);
+  TreeEntry n;
+  n.tile0 = (int64_t)(uint32_t)x.x | (int64_t)x.y << 32;
+  n.units = x.z;
+  n.per = x.w;
+  n.nodes = y.x;
+  n.ctx = y.y;
+  n.q0 = y.z;
+  n.pad = 0;
+  return n;
+}
 
 // Tokens of [0, len) on rank r.
 __host__ __device__ __forceinline__ int tree_local(int64_t len, int r, const Layout& L) {
@@ -74,49 +98,61 @@ __device__ __forceinline__ int tree_run_of(int64_t total, int parts, int64_t til
 
 // A piece: tiles [t0, t0 + n) of one unit.
 struct TreePiece {
-  int e, b, r0, r1;     // entry, request, ranks
+  int b, r0, r1;        // request, ranks
+  int T, ctx, q0;       // its nodes, cached tokens and first token
   int g, rb;            // key/value head, row block
   int t0, n;            // first tile (within the unit) and count
   int slot;             // partial slot, -1: the whole unit
 };
 
-// The piece at tile `t` of run `run`, [begin, end); e: an entry at or before it.
-__device__ __forceinline__ TreePiece tree_piece(const TreeArgs& A, int& e, int64_t t,
-                                                int64_t begin, int64_t end, int run) {
-  while (__ldcg(A.first_tile + e + 1) <= t) ++e;
-  const int64_t base = __ldcg(A.first_tile + e);
-  const int u0 = __ldcg(A.first_unit + e);
-  const int units = __ldcg(A.first_unit + e + 1) - u0;
-  const int per = (int)((__ldcg(A.first_tile + e + 1) - base) / units);
-  const int ui = (int)((t - base) / per);
-  TreePiece p;
-  p.e = e;
-  p.b = A.per_rank ? e / A.L.dcp : e;
-  p.r0 = A.per_rank ? e % A.L.dcp : 0;
-  p.r1 = A.per_rank ? p.r0 + 1 : A.L.dcp;
-  const int blocks = units / A.Hkv;
-  p.g = ui / blocks;
-  p.rb = ui - p.g * blocks;
-  p.t0 = (int)((t - base) - (int64_t)ui * per);
-  const int64_t left = end - t;
-  p.n = per - p.t0 < left ? per - p.t0 : (int)left;
-  p.slot = p.t0 == 0 && p.n == per ? -1 : 2 * run + (t == begin ? 0 : 1);
-  return p;
+// A run's pieces in order.
+struct TreeWalk {
+  int64_t t, begin, end;
+  int run, e;
+  TreeEntry n;
+};
+
+__device__ __forceinline__ TreeWalk tree_walk(const TreeArgs& A, int run) {
+  TreeWalk w;
+  const int parts = __ldcg(A.hdr);
+  const int64_t total = __ldcg(reinterpret_cast<const int64_t*>(A.hdr + 2));
+  w.run = run;
+  w.e = 0;
+  w.t = w.begin = w.end = 0;
+  if (run < parts) {
+    w.e = __ldcg(A.run_entry + run);
+    w.t = w.begin = tree_run(total, parts, run);
+    w.end = tree_run(total, parts, run + 1);
+    w.n = tree_load(A, w.e);
+  }
+  return w;
 }
 
-// Entry that holds tile t (first_tile[e] <= t < first_tile[e + 1]).
-__device__ __forceinline__ int tree_entry(const TreeArgs& A, int E, int64_t t) {
-  int lo = 0, hi = E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldcg(A.first_tile + mid) <= t) lo = mid; else hi = mid;
-  }
-  return lo;
+// The piece at the walk's tile, which then stands behind it.
+__device__ __forceinline__ TreePiece tree_next(const TreeArgs& A, TreeWalk& w) {
+  while (w.t >= w.n.tile0 + (int64_t)w.n.units * w.n.per) w.n = tree_load(A, ++w.e);
+  TreePiece p;
+  p.b = A.per_rank ? w.e / A.L.dcp : w.e;
+  p.r0 = A.per_rank ? w.e % A.L.dcp : 0;
+  p.r1 = A.per_rank ? p.r0 + 1 : A.L.dcp;
+  p.T = w.n.nodes;
+  p.ctx = w.n.ctx;
+  p.q0 = w.n.q0;
+  const int in = (int)(w.t - w.n.tile0);
+  const int ui = in / w.n.per, blocks = w.n.units / A.Hkv;
+  p.g = ui / blocks;
+  p.rb = ui - p.g * blocks;
+  p.t0 = in - ui * w.n.per;
+  const int64_t left = w.end - w.t;
+  p.n = w.n.per - p.t0 < left ? w.n.per - p.t0 : (int)left;
+  p.slot = p.t0 == 0 && p.n == w.n.per ? -1 : 2 * w.run + (w.t == w.begin ? 0 : 1);
+  w.t += p.n;
+  return p;
 }
 
 // Token row of an output row: request row `row` (node * G + head of the group).
 __device__ __forceinline__ int64_t tree_out_row(const TreeArgs& A, const TreePiece& p, int row) {
-  const int64_t tok = __ldcg(A.q_start + p.b) + row / A.G;
+  const int64_t tok = p.q0 + row / A.G;
   return ((int64_t)(A.per_rank ? p.r0 : 0) * A.N + tok) * A.Hq + p.g * A.G + row % A.G;
 }
 

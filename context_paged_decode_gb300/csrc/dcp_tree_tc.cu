@@ -14,16 +14,18 @@
 //  * up to 128 rows (kTwo false) they take the tiles in turn, with the same
 //    queries, and join their sums at the end of a unit: one computes its
 //    softmax while the tensor core works for the other;
-//  * up to 256 rows (kTwo true) each has 128 of the rows and both go through
+//  * up to 256 rows (kTwo true) each has half of the rows and both go through
 //    every tile, which is read once.
-// Warps: 0 loads keys and values by TMA (boxes of 16 to 128 rows, a page or part
-// of one, a lane each) into a ring of slots that alternate K and V; 1 issues the products; 2 and 3 load queries; 4-7 and 8-11
-// are the softmax, one row per thread.  P goes back to tensor memory over the
-// scores it came from (bf16, half the columns) and is the A operand of P V.
-// The score product of a stream's next tile is issued after P V of its last,
-// so a score barrier also says that the accumulator is at rest, and the rare
-// rescale (only when the maximum grows by more than 2^8) needs no wait of its
-// own.
+// Warps: 0 and 2 load keys and values by TMA (boxes of 16 to 128 rows, a page
+// or part of one, a lane each), into a ring of their own; 3 loads the queries,
+// whose rows (node, head of the group) are one box of the query tensor; 1
+// issues the products; 4-7 and 8-11 are the softmax, one row per thread, its
+// 128 scores in registers (which the other warps give up for it).  P goes back
+// to tensor memory over the scores it came from (bf16, half the columns) and
+// is the A operand of P V.  The score product of a stream's next tile is issued
+// after P V of its last, so a score barrier also says that the accumulator is
+// at rest, and the rare rescale (only when the maximum grows by more than 2^8)
+// needs no wait of its own.
 //
 // Masked tokens have P = 0, but 0 * x is not 0 for infinities and NaN.  Rows of
 // V past the end or of unusable pages are zeroed in shared memory, and so are
@@ -43,7 +45,9 @@ namespace dcp {
 struct TreeTcArgs {
   CUtensorMap kmap[DCP_MAX_RANKS];   // [num_blocks * Hkv * bs rows][d], box 64 x `box`
   CUtensorMap vmap[DCP_MAX_RANKS];
+  CUtensorMap qmap;                  // [N][Hq][d], box 64 x G x `nodes`
   TreeArgs t;
+  int nodes;                         // of a query tile: 128 / G
   int box;                           // rows of a box: a power of two that divides bs, 16 .. 128
 };
 
@@ -57,13 +61,15 @@ template <int D, bool kTwo>
 struct TreeTc {
   static constexpr int kSlot = kTtTile * D * 2;
   static constexpr int kQ = (kTwo ? 2 : 1) * kSlot;
-  static constexpr int kSlots = (224 * 1024 - kQ) / kSlot;  // 3 KB stay for the rest
-  static constexpr int kQOff = kSlots * kSlot;
+  // 224 KB of tiles; 3 KB stay for the rest
+  static constexpr int kKSlots = (224 * 1024 - kQ) / kSlot / 2;
+  static constexpr int kVSlots = (224 * 1024 - kQ) / kSlot - kKSlots;
+  static constexpr int kVOff = kKSlots * kSlot;
+  static constexpr int kQOff = kVOff + kVSlots * kSlot;
   static constexpr int kMlOff = kQOff + kQ;                 // float2 [2 stream][128]
-  static constexpr int kCodeOff = kMlOff + 2 * 128 * 8;     // uint8 [2 stream][128]
-  static constexpr int kFlagOff = kCodeOff + 2 * 128;       // int [2 parity]
+  static constexpr int kFlagOff = kMlOff + 2 * 128 * 8;     // int [2 parity]
   static constexpr int kBarOff = kFlagOff + 16;
-  static constexpr int kBars = 2 * kSlots + 8;
+  static constexpr int kBars = 2 * (kKSlots + kVSlots) + 8;
   static constexpr int kSmem = kBarOff + 8 * kBars + 16;
   static constexpr uint32_t kColS = 0, kColO = 256;         // two of each, 128 and D apart
 };
@@ -106,10 +112,10 @@ __device__ __forceinline__ bool bf16_odd(uint32_t h) { return (h & 0x7F80u) == 0
 // Adds to output row `row` (columns [c0, c1)) what it sees of non-finite values
 // of drafted nodes, which the product took as zero.  Rare and slow.
 template <int D>
-__device__ __noinline__ void tree_fix(const TreeArgs& A, const TreePiece& p, int T, int64_t ctx,
-                                      int row, int c0, int c1, float M, float f, void* dst,
-                                      bool f32) {
-  const int64_t tok = __ldcg(A.q_start + p.b) + row / A.G;
+__device__ __noinline__ void tree_fix(const TreeArgs& A, const TreePiece& p, int row, int c0,
+                                      int c1, float M, float f, void* dst, bool f32) {
+  const int T = p.T;
+  const int64_t ctx = p.ctx, tok = p.q0 + row / A.G;
   const uint64_t mask = __ldcg((const unsigned long long*)A.mask + tok);
   const __nv_bfloat16* q =
       (const __nv_bfloat16*)A.q + (tok * A.Hq + p.g * A.G + row % A.G) * (int64_t)D;
@@ -156,8 +162,9 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
   extern __shared__ __align__(1024) uint8_t smem[];   // no room is left to round up in
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + C::kBarOff;
-  const uint32_t b_full = bars, b_empty = bars + 8 * C::kSlots;
-  const uint32_t b_s = b_empty + 8 * C::kSlots;   // +stream: scores are there
+  const uint32_t b_k = bars, b_kfree = b_k + 8 * C::kKSlots;        // keys: there, read
+  const uint32_t b_v = b_kfree + 8 * C::kKSlots, b_vfree = b_v + 8 * C::kVSlots;
+  const uint32_t b_s = b_vfree + 8 * C::kVSlots;  // +stream: scores are there
   const uint32_t b_p = b_s + 16;                  // +stream: P is there
   const uint32_t b_o = b_p + 16, b_ofree = b_o + 8, b_q = b_o + 16, b_qfree = b_o + 24;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * C::kBars);
@@ -170,9 +177,13 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(b_full + 8 * i, 1);
-      mbar_init(b_empty + 8 * i, 1);
+    for (int i = 0; i < C::kKSlots; ++i) {
+      mbar_init(b_k + 8 * i, 1);
+      mbar_init(b_kfree + 8 * i, 1);
+    }
+    for (int i = 0; i < C::kVSlots; ++i) {
+      mbar_init(b_v + 8 * i, 1);
+      mbar_init(b_vfree + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_s + 8 * i, 1);
@@ -180,10 +191,15 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
     }
     mbar_init(b_o, 1);
     mbar_init(b_ofree, 8);
-    mbar_init(b_q, 2);
+    mbar_init(b_q, 1);
     mbar_init(b_qfree, 1);
     fence_mbar_init();
     flag[0] = flag[1] = 0;
+    prefetch_tmap(&X.qmap);
+    for (int r = 0; r < A.L.dcp; ++r) {
+      prefetch_tmap(&X.kmap[r]);
+      prefetch_tmap(&X.vmap[r]);
+    }
   }
   if (warp == 1) {
     tc_alloc(smem_u32(tmem_slot), 512);
@@ -195,59 +211,69 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
   const uint32_t tmem = *tmem_slot;
   griddep_wait();   // the plan, and what the calls before wrote
 
-  const int E = A.per_rank ? A.B * A.L.dcp : A.B;
-  const int64_t total = __ldcg(A.first_tile + E);
-  const int parts = __ldcg(A.hdr);
-  const int run = blockIdx.x;
   int32_t* errp = A.err ? A.err : A.hdr + 1;
-  const int64_t begin = run < parts ? tree_run(total, parts, run) : 0;
-  const int64_t end = run < parts ? tree_run(total, parts, run + 1) : 0;
-  int e = begin < end ? tree_entry(A, E, begin) : 0;
+  TreeWalk walk = tree_walk(A, blockIdx.x);
+  const int srows = X.nodes * A.G;   // rows of a stream's query tile
+  auto block_rows = [&](const TreePiece& p) { return min(A.rows, p.T * A.G - p.rb * A.rows); };
 
-  auto block_rows = [&](const TreePiece& p, int T) {
-    return min(A.rows, T * A.G - p.rb * A.rows);
-  };
-
-  if (warp == 0) {
-    // ---------------- keys and values ----------------
-    const uint64_t pol = policy_evict_first();
-    const int box = X.box, nu = kTtTile / box;
-    uint32_t seq = 0;
-    bool dead = false;
-    for (int64_t t = begin; t < end && !dead;) {
-      const TreePiece p = tree_piece(A, e, t, begin, end, run);
-      t += p.n;
-      const int64_t ctx = __ldcg(A.ctx + p.b), len = ctx + __ldcg(A.nodes + p.b);
-      const int32_t* bt = A.bt + (int64_t)p.b * A.max_vb;
-      TileIt it;
-      it.seek(A, p, len, ctx);
-      // row of this lane's part of the tile, -1: nothing there, -2: unusable page
-      auto part = [&](const TileIt& i) -> int64_t {
-        const int pos = i.tr * kTtTile + lane * box;
-        if (lane >= nu || pos >= i.n) return -1;
-        const int j = pos / A.L.bs;
-        const int64_t phys = j < A.max_vb ? (int64_t)__ldcg(bt + i.r * A.stride + j) : -1;
-        if (phys < 0 || phys >= A.nb) return -2;
-        return (phys * A.Hkv + p.g) * A.L.bs + (pos - j * A.L.bs);
-      };
-      int64_t row = part(it);
-      for (int k = 0; k < p.n && !dead; ++k) {
-        const int64_t mine = row;
-        const int r = it.r;
-        if (k + 1 < p.n) {
-          it.step(A, p, len, ctx, 1);
-          row = part(it);
-        }
-        const uint32_t m = __ballot_sync(0xffffffffu, mine >= 0);
-        if (mine == -2) count_error(A.err);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++seq) {
-          const uint32_t slot = seq % C::kSlots, u = seq / C::kSlots;
-          if (!__all_sync(0xffffffffu, mbar_wait(b_empty + 8 * slot, (u & 1) ^ 1))) {
+  if (warp < 4) {
+    // 128 x 88 + 256 x 208 registers are the 384 x 168 of the launch
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0 || warp == 2) {
+      // ---------------- keys (0) and values (2) ----------------
+      const bool val = warp == 2;
+      const uint64_t pol = policy_evict_first();
+      const int box = X.box, nu = kTtTile / box;
+      const int slots = val ? C::kVSlots : C::kKSlots;
+      const uint32_t full = val ? b_v : b_k, free = val ? b_vfree : b_kfree;
+      const uint32_t ring = sbase + (val ? C::kVOff : 0) + lane * box * 128;
+      const CUtensorMap* maps = val ? X.vmap : X.kmap;
+      uint32_t slot = 0, par = 1;
+      bool dead = false;
+      while (walk.t < walk.end && !dead) {
+        const TreePiece p = tree_next(A, walk);
+        const int64_t ctx = p.ctx, len = ctx + p.T;
+        const int32_t* bt = A.bt + (int64_t)p.b * A.max_vb;
+        // This lane's part of a tile: table entry (-1: beyond the table), its
+        // row in the page, and whether it has tokens.  The entry is loaded
+        // two tiles ahead and first looked at when its turn comes.
+        struct Part {
+          int raw, off, r;
+          bool has;
+        };
+        TileIt it;
+        it.seek(A, p, len, ctx);
+        int fetched = 0;
+        auto fetch = [&]() {
+          Part x;
+          x.raw = -1;
+          x.off = 0;
+          x.r = it.r;
+          x.has = false;
+          if (fetched < p.n) {
+            const int pos = it.tr * kTtTile + lane * box;
+            x.has = lane < nu && pos < it.n;
+            const int j = pos / A.L.bs;
+            x.off = pos - j * A.L.bs;
+            if (x.has && j < A.max_vb) x.raw = __ldcg(bt + it.r * A.stride + j);
+            ++fetched;
+            if (fetched < p.n) it.step(A, p, len, ctx, 1);
+          }
+          return x;
+        };
+        Part a = fetch(), b = fetch();
+        for (int k = 0; k < p.n; ++k) {
+          const Part c = a;
+          a = b;
+          b = fetch();
+          const bool ok = c.has && c.raw >= 0 && (int64_t)c.raw < A.nb;
+          const uint32_t m = __ballot_sync(0xffffffffu, ok);
+          if (c.has && !ok && !val) count_error(A.err);
+          if (!__all_sync(0xffffffffu, mbar_wait(free + 8 * slot, par))) {
             dead = true;
             break;
           }
-          const uint32_t bar = b_full + 8 * slot;
+          const uint32_t bar = full + 8 * slot;
           if (lane == 0) {
             if (m)
               mbar_arrive_expect_tx(bar, __popc(m) * box * D * 2);
@@ -255,36 +281,61 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
               mbar_arrive(bar);
           }
           __syncwarp();
-          if (mine >= 0) {
-            const void* map = kv ? &X.vmap[r] : &X.kmap[r];
-            const uint32_t dst = sbase + slot * C::kSlot + lane * box * 128;
+          if (ok) {
+            const int row = (int)(((int64_t)c.raw * A.Hkv + p.g) * A.L.bs + c.off);
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_2d_hint(dst + c * kHalfBytes, map, 64 * c, (int)mine, bar, pol);
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_2d_hint(ring + slot * C::kSlot + h * kHalfBytes, &maps[c.r], 64 * h, row,
+                               bar, pol);
           }
           __syncwarp();
+          if (++slot == (uint32_t)slots) {
+            slot = 0;
+            par ^= 1;
+          }
         }
       }
-    }
-    if (dead && lane == 0) atomicAdd(errp, kTtStuck);
-  } else if (warp == 1) {
-    // ---------------- products ----------------
-    if (lane == 0) {
+      if (dead && lane == 0) atomicAdd(errp, kTtStuck);
+    } else if (warp == 3) {
+      // ---------------- queries ----------------
+      if (lane == 0) {
+        uint32_t item = 0;
+        bool dead = false;
+        while (walk.t < walk.end) {
+          const TreePiece p = tree_next(A, walk);
+          if (item > 0 && !mbar_wait(b_qfree, (item - 1) & 1)) {
+            dead = true;
+            break;
+          }
+          const bool two = kTwo && block_rows(p) > srows;
+          mbar_arrive_expect_tx(b_q, (two ? 2 : 1) * srows * D * 2);
+          const int node = p.q0 + p.rb * (A.rows / A.G);
+          for (int s = 0; s < (two ? 2 : 1); ++s)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(sbase + C::kQOff + s * C::kSlot + h * kHalfBytes, &X.qmap, 64 * h,
+                          p.g * A.G, node + s * X.nodes, b_q);
+          ++item;
+        }
+        if (dead) atomicAdd(errp, kTtStuck);
+      }
+    } else if (lane == 0) {
+      // ---------------- products ----------------
       constexpr uint32_t kIdQK = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t kIdPV = idesc_bf16_f32(128, D, false, true);
-      uint32_t seq = 0, item = 0, np[2] = {0, 0};
+      uint32_t ks = 0, kp = 0, vs = 0, vp = 0;   // ring places and parities
+      uint32_t item = 0, np0 = 0, np1 = 0;
       bool dead = false;
       auto wait = [&](uint32_t bar, uint32_t par) {
         if (!dead && !mbar_wait(bar, par)) dead = true;
         return !dead;
       };
-      // scores of tile `tile` (counted over the run) into stream s
-      auto qk = [&](int s, uint32_t tile, bool last) {
-        const uint32_t i = 2 * tile, slot = i % C::kSlots;
-        if (!wait(b_full + 8 * slot, (i / C::kSlots) & 1)) return;
+      // scores of the ring's next tile into stream s; `last`: its last reader
+      auto qk = [&](int s, bool last) {
+        if (!wait(b_k + 8 * ks, kp)) return;
         tc_fence_after();
         const uint64_t a = sdesc_sw128(sbase + C::kQOff + (kTwo ? s * C::kSlot : 0), 0, 1024);
-        const uint64_t b = sdesc_sw128(sbase + slot * C::kSlot, 0, 1024);
+        const uint64_t b = sdesc_sw128(sbase + ks * C::kSlot, 0, 1024);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
 #pragma unroll
@@ -293,110 +344,72 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
             tc_mma_ss(tmem + C::kColS + s * 128, a + off, b + off, kIdQK, (c | kk) != 0);
           }
         tc_commit(b_s + 8 * s);
-        if (last) tc_commit(b_empty + 8 * slot);
+        if (last) {
+          tc_commit(b_kfree + 8 * ks);
+          if (++ks == C::kKSlots) {
+            ks = 0;
+            kp ^= 1;
+          }
+        }
       };
-      auto pv = [&](int s, uint32_t tile, bool first, bool last) {
-        const uint32_t i = 2 * tile + 1, slot = i % C::kSlots;
-        if (!wait(b_p + 8 * s, np[s] & 1) || !wait(b_full + 8 * slot, (i / C::kSlots) & 1)) return;
-        ++np[s];
+      auto pv = [&](int s, bool first, bool last) {
+        if (!wait(b_p + 8 * s, (s ? np1 : np0) & 1) || !wait(b_v + 8 * vs, vp)) return;
+        if (s) ++np1; else ++np0;
         tc_fence_after();
-        const uint32_t v = sbase + slot * C::kSlot;
+        const uint64_t v = sdesc_sw128(sbase + C::kVOff + vs * C::kSlot, kHalfBytes, 1024);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           tc_mma_ts(tmem + C::kColO + s * D, tmem + C::kColS + s * 128 + kk * 8,
-                    sdesc_sw128(v + kk * 16 * 128, kHalfBytes, 1024), kIdPV,
-                    (!first || kk > 0) ? 1u : 0u);
-        if (last) tc_commit(b_empty + 8 * slot);
+                    v + (uint64_t)((kk * 16 * 128) >> 4), kIdPV, (!first || kk > 0) ? 1u : 0u);
+        if (last) {
+          tc_commit(b_vfree + 8 * vs);
+          if (++vs == C::kVSlots) {
+            vs = 0;
+            vp ^= 1;
+          }
+        }
       };
-      for (int64_t t = begin; t < end && !dead; ++item) {
-        const TreePiece p = tree_piece(A, e, t, begin, end, run);
-        t += p.n;
-        const bool two = kTwo && block_rows(p, __ldcg(A.nodes + p.b)) > 128;
+      for (; walk.t < walk.end && !dead; ++item) {
+        const TreePiece p = tree_next(A, walk);
         wait(b_q, item & 1);
         if (!kTwo) {
           for (int k = 0; k <= p.n && !dead; ++k) {
             if (k < p.n) {
-              qk(k & 1, seq + k, true);
+              qk(k & 1, true);
               if (k == p.n - 1) tc_commit(b_qfree);
             }
             if (k == 1) wait(b_ofree, (item & 1) ^ 1);
-            if (k > 0) pv((k - 1) & 1, seq + k - 1, k <= 2, true);
+            if (k > 0) pv((k - 1) & 1, k <= 2, true);
           }
         } else {
-          qk(0, seq, !two);
-          if (two) qk(1, seq, true);
+          const bool two = block_rows(p) > srows;
+          qk(0, !two);
+          if (two) qk(1, true);
           if (p.n == 1) tc_commit(b_qfree);
           wait(b_ofree, (item & 1) ^ 1);
           for (int k = 0; k < p.n && !dead; ++k) {
-            pv(0, seq + k, k == 0, !two);
-            if (k + 1 < p.n) qk(0, seq + k + 1, !two);
+            pv(0, k == 0, !two);
+            if (k + 1 < p.n) qk(0, !two);
             if (two) {
-              pv(1, seq + k, k == 0, true);
-              if (k + 1 < p.n) qk(1, seq + k + 1, true);
+              pv(1, k == 0, true);
+              if (k + 1 < p.n) qk(1, true);
             }
             if (k + 2 == p.n) tc_commit(b_qfree);
           }
         }
-        seq += p.n;
         if (!dead) tc_commit(b_o);
       }
       if (dead) atomicAdd(errp, kTtStuck);
     }
-  } else if (warp < 4) {
-    // ---------------- queries ----------------
-    const int tid = threadIdx.x - 64;
-    uint32_t item = 0;
-    bool dead = false;
-    for (int64_t t = begin; t < end && !dead; ++item) {
-      const TreePiece p = tree_piece(A, e, t, begin, end, run);
-      t += p.n;
-      const int T = __ldcg(A.nodes + p.b), nrows = block_rows(p, T);
-      const int64_t tok0 = __ldcg(A.q_start + p.b);
-      constexpr int cpr = D / 8;
-      if (item > 0 && !__all_sync(0xffffffffu, mbar_wait(b_qfree, (item - 1) & 1))) {
-        dead = true;
-        break;
-      }
-      for (int i0 = tid; i0 < nrows * cpr; i0 += 64 * 8) {
-        uint4 x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = i0 + 64 * j;
-          if (i < nrows * cpr) {
-            const int rr = p.rb * A.rows + i / cpr;
-            const int node = rr / A.G;
-            x[j] = __ldcg((const uint4*)A.q +
-                          ((tok0 + node) * A.Hq + p.g * A.G + (rr - node * A.G)) * cpr + i % cpr);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = i0 + 64 * j;
-          if (i < nrows * cpr) {
-            const int row = i / cpr, c = i % cpr;
-            const uint32_t dst = sbase + C::kQOff + (row >> 7) * C::kSlot + (c >> 3) * kHalfBytes +
-                                 (row & 127) * 128 + (((c & 7) ^ (row & 7)) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x[j].x),
-                         "r"(x[j].y), "r"(x[j].z), "r"(x[j].w)
-                         : "memory");
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_q);
-    }
-    if (dead && lane == 0) atomicAdd(errp, kTtStuck);
   } else {
     // ---------------- softmax: a row per thread ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int s = (warp - 4) >> 2;                 // stream
     const int quarter = warp & 3;                  // tensor-memory lanes 32 quarter ..
-    const int row = quarter * 32 + lane;           // row of the stream's 128
-    const int wtid = threadIdx.x - 128 - s * 128;  // thread of the warpgroup
+    const int row = quarter * 32 + lane;           // row of the stream's query tile
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t ts = tmem + lane_off + C::kColS + s * 128;
     const uint32_t to = tmem + lane_off + C::kColO + s * D;
-    uint8_t* code = smem + C::kCodeOff + s * 128;
     float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff);
     const int step = kTwo ? 1 : 2;
     uint32_t seq = 0, item = 0, ns = 0;
@@ -404,119 +417,129 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
     auto wait = [&](uint32_t bar, uint32_t par) {
       if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar, par))) dead = true;
     };
-    for (int64_t t = begin; t < end; ++item) {
-      const TreePiece p = tree_piece(A, e, t, begin, end, run);
-      t += p.n;
-      const int T = __ldcg(A.nodes + p.b);
-      const int64_t ctx = __ldcg(A.ctx + p.b), len = ctx + T;
-      const int nrows = block_rows(p, T);
-      const int brow = kTwo ? s * 128 + row : row;       // row of the block
-      const bool mine = (kTwo ? s * 128 : 0) + quarter * 32 < nrows;   // warp has rows
-      const bool takes = !kTwo || s == 0 || nrows > 128;               // stream has work
+    for (; walk.t < walk.end; ++item) {
+      const TreePiece p = tree_next(A, walk);
+      const int64_t ctx = p.ctx, len = ctx + p.T;
+      const int nrows = block_rows(p);
+      const int srow0 = kTwo ? s * srows : 0;            // the stream's first row of the block
+      const int brow = srow0 + row;                      // row of the block
+      const int have = min(srows, nrows - srow0);        // rows of the stream
+      const bool real = row < have;
+      const bool mine = quarter * 32 < have;             // warp has rows
+      const bool takes = have > 0;                       // stream has work
       const int urow = p.rb * A.rows + brow;             // row of the request
       const uint64_t mask =
-          brow < nrows
-              ? __ldcg((const unsigned long long*)A.mask + __ldcg(A.q_start + p.b) + urow / A.G)
-              : 0ull;
+          real ? __ldcg((const unsigned long long*)A.mask + p.q0 + urow / A.G) : 0ull;
       float m = -INFINITY, l = 0.f;
       bool filled = false;                               // the accumulator holds earlier tiles
       if (takes) {
         TileIt it;
         it.seek(A, p, len, ctx);
-        if (!kTwo && s == 1) it.step(A, p, len, ctx, 1);
+        if (!kTwo && s == 1 && p.n > 1) it.step(A, p, len, ctx, 1);
         for (int k = kTwo ? 0 : s; k < p.n; k += step) {
           const int p0 = it.tr * kTtTile, nv = min(kTtTile, it.n - p0);
           // usable pages of the tile, 16 tokens a bit
           bool good = true;
           if (lane < 8 && lane * 16 < nv) {
             const int j = (p0 + lane * 16) / A.L.bs;
-            const int64_t phys =
-                j < A.max_vb
-                    ? (int64_t)__ldcg(A.bt + it.r * A.stride + (int64_t)p.b * A.max_vb + j)
-                    : -1;
-            good = phys >= 0 && phys < A.nb;
+            const int raw =
+                j < A.max_vb ? __ldcg(A.bt + it.r * A.stride + (int64_t)p.b * A.max_vb + j) : -1;
+            good = raw >= 0 && (int64_t)raw < A.nb;
           }
           const uint32_t pages = __ballot_sync(0xffffffffu, good);
           const bool special = nv < kTtTile || p0 + nv > it.lc || (pages & 0xFFu) != 0xFFu;
-          const uint32_t vi = 2 * (seq + k) + 1;          // the tile's V slot
           uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
           if (special) {
-            // who sees token wtid: 64 everyone, 255 nobody, else node's bit
-            const int pos = p0 + wtid;
-            int c = 255;
-            if (wtid < nv && ((pages >> (wtid >> 4)) & 1))
-              c = pos < it.lc ? 64 : (int)(tree_global(pos, it.r, A.L) - ctx);
-            code[wtid] = (uint8_t)c;
-            bar_sync(1 + s, 128);
-            wait(b_full + 8 * (vi % C::kSlots), (vi / C::kSlots) & 1);
-            const uint32_t v = sbase + (vi % C::kSlots) * C::kSlot;
-            if (!dead) {
-              // V rows nobody sees become zero, as do odd values of nodes
-              for (int i = wtid; i < kTtTile * (D / 8); i += 128) {
-                const int tok = i / (D / 8), ch = i % (D / 8), cd = code[tok];
-                if (cd == 64) continue;
-                const uint32_t at = v + (ch >> 3) * kHalfBytes + tok * 128 +
-                                    (((ch & 7) ^ (tok & 7)) << 4);
-                uint32_t w[4] = {0u, 0u, 0u, 0u};
-                bool odd = cd == 255;
-                if (!odd) {
-                  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                               : "r"(at));
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    if (bf16_odd(w[x])) {
-                      w[x] &= 0xFFFF0000u;
-                      odd = true;
-                    }
-                    if (bf16_odd(w[x] >> 16)) {
-                      w[x] &= 0xFFFFu;
-                      odd = true;
-                    }
-                  }
-                  if (odd) flag[item & 1] = (int)item + 1;
-                }
-                if (odd)
-                  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]),
-                               "r"(w[1]), "r"(w[2]), "r"(w[3])
-                               : "memory");
-              }
-              fence_proxy_async_smem();
-            }
+            // V rows of this warp's 32 tokens: those nobody sees become zero,
+            // and so do odd values of nodes
+            const uint32_t vi = seq + k, vslot = vi % C::kVSlots;
+            wait(b_v + 8 * vslot, (vi / C::kVSlots) & 1);
+            const uint32_t v = sbase + C::kVOff + vslot * C::kSlot;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              uint32_t bits = 0;
-              for (int i = 0; i < 32; ++i) {
-                const int cd = code[g * 32 + i];
-                const uint32_t on = cd == 64 ? 1u : cd < 64 ? (uint32_t)(mask >> cd) & 1u : 0u;
-                bits |= on << i;
+              // token g * 32 + lane: seen by everyone, a node, or not there
+              const int tk = g * 32 + lane, pos = p0 + tk;
+              const bool there = tk < nv && ((pages >> (tk >> 4)) & 1);
+              const bool old = there && pos < it.lc;
+              const uint32_t olds = __ballot_sync(0xffffffffu, old);
+              uint32_t nodes = __ballot_sync(0xffffffffu, there && !old);
+              const int node =
+                  there && !old ? (int)(tree_global(pos, it.r, A.L) - ctx) & 63 : 0;
+              vis[g] = olds;
+              if (g == quarter && !dead) {
+                constexpr int kRow = D / 8;                // 16-byte pieces of a row
+                for (int i = lane; i < 32 * kRow; i += 32) {
+                  const int o = i / kRow, ch = i % kRow;
+                  if ((olds >> o) & 1) continue;
+                  const int tok = g * 32 + o;
+                  const uint32_t at = v + (ch >> 3) * kHalfBytes + tok * 128 +
+                                      (((ch & 7) ^ (tok & 7)) << 4);
+                  uint32_t w[4] = {0u, 0u, 0u, 0u};
+                  bool odd = !((nodes >> o) & 1);
+                  if (!odd) {
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(at));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                      if (bf16_odd(w[x])) {
+                        w[x] &= 0xFFFF0000u;
+                        odd = true;
+                      }
+                      if (bf16_odd(w[x] >> 16)) {
+                        w[x] &= 0xFFFFu;
+                        odd = true;
+                      }
+                    }
+                    if (odd) flag[item & 1] = (int)item + 1;
+                  }
+                  if (odd)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]),
+                                 "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
               }
-              vis[g] = bits;
+              // the nodes among them, by this row's mask
+              while (nodes) {
+                const int o = __ffs(nodes) - 1;
+                nodes &= nodes - 1;
+                const int j = __shfl_sync(0xffffffffu, node, o);
+                vis[g] |= ((uint32_t)(mask >> j) & 1u) << o;
+              }
             }
-            bar_sync(1 + s, 128);   // the codes may be written again
           }
           wait(b_s + 8 * s, ns & 1);
           ++ns;
           if (!dead && mine) {
             tc_fence_after();
-            float mx = -INFINITY;
-            uint32_t x[32];
+            uint32_t x[4][32];
+            auto load = [&]() {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              tc_ld32(ts + g * 32, x);
-              tc_wait_ld(x);
+              for (int g = 0; g < 4; ++g) tc_ld32(ts + g * 32, x[g]);
+#pragma unroll
+              for (int g = 0; g < 4; ++g) tc_wait_ld(x[g]);
               if (special) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  mx = fmaxf(mx, (vis[g] >> i) & 1 ? __uint_as_float(x[i]) : -INFINITY);
-              } else {
-                float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                for (int g = 0; g < 4; ++g)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) y[i & 3] = fmaxf(y[i & 3], __uint_as_float(x[i]));
-                mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+                  for (int i = 0; i < 32; ++i)
+                    if (!((vis[g] >> i) & 1)) x[g][i] = 0xff800000u;   // -inf
               }
-            }
-            mx *= A.sl2;
+            };
+            load();
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i & 7] = fmaxf(y[i & 7], __uint_as_float(x[g][i]));
+#pragma unroll
+            for (int w = 4; w > 0; w >>= 1)
+#pragma unroll
+              for (int i = 0; i < w; ++i) y[i] = fmaxf(y[i], y[i + w]);
+            const float mx = y[0] * A.sl2;
             float f = 1.f;                  // for what the accumulator holds
             if (mx > m + kTtGrow || m == -INFINITY) {
               if (m != -INFINITY) {
@@ -528,28 +551,24 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
             if (filled && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
               for (int g = 0; g < D / 32; ++g) {
-                tc_ld32(to + g * 32, x);
-                tc_wait_ld(x);
+                tc_ld32(to + g * 32, x[0]);
+                tc_wait_ld(x[0]);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                tc_st32(to + g * 32, x);
+                for (int i = 0; i < 32; ++i) x[0][i] = __float_as_uint(__uint_as_float(x[0][i]) * f);
+                tc_st32(to + g * 32, x[0]);
               }
+              tc_wait_st();
+              load();   // the registers held the accumulator meanwhile
             }
             const float mb = m == -INFINITY ? 0.f : m;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              tc_ld32(ts + g * 32, x);
-              tc_wait_ld(x);
               uint32_t pk[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                float a = ex2_ftz(fmaf(__uint_as_float(x[2 * i]), A.sl2, -mb));
-                float b = ex2_ftz(fmaf(__uint_as_float(x[2 * i + 1]), A.sl2, -mb));
-                if (special) {
-                  a = (vis[g] >> (2 * i)) & 1 ? a : 0.f;
-                  b = (vis[g] >> (2 * i + 1)) & 1 ? b : 0.f;
-                }
+                const float a = ex2_ftz(fmaf(__uint_as_float(x[g][2 * i]), A.sl2, -mb));
+                const float b = ex2_ftz(fmaf(__uint_as_float(x[g][2 * i + 1]), A.sl2, -mb));
                 sum[i & 3] += a + b;
                 pk[i] = pack_bf16(a, b);
               }
@@ -591,7 +610,6 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
         const bool sunk = direct && A.sink != nullptr;
         float lse2 = -INFINITY, f = 0.f;
         const int h = p.g * A.G + urow % A.G;
-        float M2 = M;
         if (sunk) {
           const float s2 = __ldcg(A.sink + h) * kLog2e;
           const float top = L == 0.f ? s2 : fmaxf(M, s2);
@@ -608,7 +626,6 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
           lse2 = M + log2f(L);
           f = 1.f / L;
         }
-        const bool real = brow < nrows;
         const int64_t orow = direct && real ? tree_out_row(A, p, urow) : 0;
         const bool f32 = !direct || A.out_dtype == DCP_F32;
         void* dst = direct ? (f32 ? (void*)((float*)A.out + orow * D)
@@ -653,7 +670,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
           }
         }
         if (real) {
-          if (odd) tree_fix<D>(A, p, T, ctx, urow, c0, c1, M2, f, dst, f32);
+          if (odd) tree_fix<D>(A, p, urow, c0, c1, M, f, dst, f32);
           if (kTwo || s == 0) {
             if (!direct)
               A.part_lse[(int64_t)p.slot * A.rows + brow] = lse2;
@@ -676,6 +693,19 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
     tc_fence_after();
     tc_dealloc(tmem, 512);
   }
+}
+
+// [N][Hq][d] as boxes of 64 columns, G heads and `nodes` tokens.
+static bool encode_q(CUtensorMap* map, const TreeArgs& A, int nodes) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)A.d, (cuuint64_t)A.Hq, (cuuint64_t)A.N};
+  cuuint64_t strides[2] = {(cuuint64_t)A.d * 2, (cuuint64_t)A.Hq * A.d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)A.G, (cuuint32_t)nodes};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(A.q), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 static int tree_box(int bs) {
@@ -714,14 +744,17 @@ int launch_tree_tc(const TreeArgs& A, cudaStream_t s) {
   memset(&X, 0, sizeof(X));
   X.t = A;
   X.box = tree_box(A.L.bs);
+  X.nodes = 128 / A.G;
+  if (!encode_q(&X.qmap, A, X.nodes)) return DCP_ECUDA;
   const uint64_t rows = (uint64_t)A.nb * A.Hkv * A.L.bs;
   for (int r = 0; r < A.L.dcp; ++r)
     if (!encode_2d_bf16_sw128(&X.kmap[r], A.k.ptr[r], A.d, rows > 0 ? rows : 1, A.d * 2, 64,
                               X.box) ||
         !encode_2d_bf16_sw128(&X.vmap[r], A.v.ptr[r], A.d, rows > 0 ? rows : 1, A.d * 2, 64, X.box))
       return DCP_ECUDA;
-  if (A.d == 64) return A.rows > 128 ? go<64, true>(X, s) : go<64, false>(X, s);
-  return A.rows > 128 ? go<128, true>(X, s) : go<128, false>(X, s);
+  const bool two = A.rows > X.nodes * A.G;
+  if (A.d == 64) return two ? go<64, true>(X, s) : go<64, false>(X, s);
+  return two ? go<128, true>(X, s) : go<128, false>(X, s);
 }
 
 }  // namespace dcp
