@@ -52,15 +52,15 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __gri
         }
         if (T > 0) {
           const int r1 = A.per_rank ? r + 1 : A.L.dcp;
-          for (int x = r; x < r1; ++x)
-            n.per += (tree_local(ctx + T, x, A.L) + A.tile - 1) / A.tile;
+          const TreeLen len((int)ctx + T, A.L);
+          for (int x = r; x < r1; ++x) n.per += (len.on(x, A.L) + A.tile - 1) / A.tile;
           if (n.per > 0) n.units = A.Hkv * ((T * A.G + A.rows - 1) / A.rows);
           n.nodes = T;
           n.ctx = (int)ctx;
           n.q0 = q0;
         }
       }
-      const int64_t tiles = (int64_t)n.units * n.per;
+      const int64_t tiles = n.units ? (int64_t)n.units * (n.per + A.extra) : 0;
       int64_t t = tiles;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -184,10 +184,11 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int run = blockIdx.x; run < A.parts; run += gridDim.x) {
     TreeWalk walk = tree_walk(A, run);
-    while (walk.t < walk.end) {
-      const TreePiece p = tree_next(A, walk);
+    TreePiece p;
+    while (tree_next(A, walk, p)) {
       const int T_b = p.T;
-      const int64_t ctx = p.ctx, len = ctx + T_b;
+      const int ctx = p.ctx;
+      const TreeLen len(ctx + T_b, A.L);
       const int row0 = p.rb * A.rows, nrows = min(A.rows, T_b * A.G - row0);
       __syncthreads();                 // the last piece is done with sq
       for (int i = tid; i < kTgRows * d; i += kTgWarps * 32) {
@@ -215,11 +216,11 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
       }
       // rank and tile within the rank of the piece's first tile
       int r = p.r0, tr = p.t0;
-      int n_r = tree_local(len, r, A.L);
+      int n_r = len.on(r, A.L);
       for (int step = 0; step < p.n; ++step) {
         while (tr >= (n_r + kTgTile - 1) / kTgTile) {
           tr -= (n_r + kTgTile - 1) / kTgTile;
-          n_r = tree_local(len, ++r, A.L);
+          n_r = len.on(++r, A.L);
         }
         const int p0 = tr * kTgTile;
         ++tr;
@@ -234,8 +235,8 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
                 j < A.max_vb ? (int64_t)__ldcg(A.bt + r * A.stride + (int64_t)p.b * A.max_vb + j) : -1;
             if (phys >= 0 && phys < A.nb) {
               row = (phys * A.Hkv + p.g) * A.L.bs + (pos - j * A.L.bs);
-              const int64_t x = tree_global(pos, r, A.L) - ctx;
-              code = x < 0 ? 64 : (int)x;
+              const int x = tree_global(pos, r, A.L) - ctx;
+              code = x < 0 ? 64 : x;
             } else {
               count_error(A.err);
             }
@@ -408,31 +409,46 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     const int per = n.per;
     const int g = h / A.G, ur = j * A.G + h % A.G;   // row of the unit's request
     const int rb = ur / A.rows, rr = ur - rb * A.rows;
-    const int64_t t0 = n.tile0 + (int64_t)(g * (n.units / A.Hkv) + rb) * per;
+    const int64_t t0 = n.tile0 + (int64_t)(g * (n.units / A.Hkv) + rb) * (per + A.extra);
     const int k0 = tree_run_of(total, parts, t0), k1 = tree_run_of(total, parts, t0 + per - 1);
     if (k0 == k1) continue;
     const bool late = tree_run(total, parts, k0) != t0;   // run k0 began before this unit
-    float M = -INFINITY;
-    for (int k = k0; k <= k1; ++k)
-      M = fmaxf(M, __ldcg(A.part_lse + (int64_t)(2 * k + (k == k0 && late)) * A.rows + rr));
+    auto slot = [&](int k) { return (int64_t)(2 * k + (k == k0 && late)) * A.rows + rr; };
+    // a lane per part: one wait for up to 32 parts' LSEs
     const bool sunk = A.sink != nullptr;
     const float s2 = sunk ? __ldcg(A.sink + h) * kLog2e : -INFINITY;
-    M = fmaxf(M, s2);
+    float M = s2;
+    for (int k = k0; k <= k1; k += 32)
+      M = fmaxf(M, warp_max(k + lane <= k1 ? __ldcg(A.part_lse + slot(k + lane)) : -INFINITY));
     const float mb = M == -INFINITY ? 0.f : M;
     float L = sunk ? exp2f(s2 - mb) : 0.f;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    for (int k = k0; k <= k1; ++k) {
-      const int64_t slot = (int64_t)(2 * k + (k == k0 && late)) * A.rows + rr;
-      const float lse = __ldcg(A.part_lse + slot);
-      if (lse == -INFINITY) continue;    // saw nothing: its values do not count
-      const float wgt = exp2f(lse - mb);
-      L += wgt;
-      const float* src = A.part_o + slot * A.d;
+    for (int k = k0; k <= k1; k += 32) {
+      const float lse = k + lane <= k1 ? __ldcg(A.part_lse + slot(k + lane)) : -INFINITY;
+      // a part that saw nothing does not count, whatever its values are
+      const float mine = lse == -INFINITY ? 0.f : exp2f(lse - mb);
+      L += warp_sum(mine);
+      const int n = min(32, k1 - k + 1);
+      for (int j0 = 0; j0 < n; j0 += 8) {
+        float v[8][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i * 32 < A.d) acc[i] = fmaf(wgt, __ldcg(src + i * 32 + lane), acc[i]);
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[j][i] = j0 + j < n && i * 32 < A.d
+                          ? __ldcg(A.part_o + slot(k + j0 + j) * A.d + i * 32 + lane)
+                          : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float wgt = __shfl_sync(0xffffffffu, mine, (j0 + j) & 31);
+          if (j0 + j < n && wgt != 0.f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(wgt, v[j][i], acc[i]);
+          }
+        }
+      }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
@@ -455,13 +471,13 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
 // for a call.  The tensor-core kernel takes one 128-row tile of queries where
 // all nodes of a request fit it, else two.
 struct TreeShape {
-  int rows, tile, parts;
+  int rows, tile, parts, extra;
 };
 
 static TreeShape tree_shape(bool tc, int G, int max_tree) {
-  if (!tc) return TreeShape{kTgRows / G * G, kTgTile, 4 * num_sms()};
+  if (!tc) return TreeShape{kTgRows / G * G, kTgTile, 4 * num_sms(), 0};
   const int nodes = 128 / G;
-  return TreeShape{(max_tree <= nodes ? 1 : 2) * nodes * G, 128, num_sms()};
+  return TreeShape{(max_tree <= nodes ? 1 : 2) * nodes * G, 128, num_sms(), 2};
 }
 
 static size_t tree_carve(TreeArgs* A, void* ws, int B, int dcp, int parts, int rows, int d) {
@@ -532,6 +548,7 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
   A.rows = S.rows;
   A.tile = S.tile;
   A.parts = S.parts;
+  A.extra = S.extra;
   A.sl2 = scale * kLog2e;
   A.k = kv.k;
   A.v = kv.v;

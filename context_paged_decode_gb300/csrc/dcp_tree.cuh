@@ -3,8 +3,9 @@
 // A unit is the work of one key/value head on one block of query rows of one
 // request (row = node * G + head of the group), over the request's tokens on
 // all ranks (fused call) or on one rank (partials).  Its tokens are counted in
-// tiles; a tile never crosses a rank.  All units' tiles in a row are cut into
-// equal runs, one per CTA, so a CTA holds the end of one unit, some whole
+// tiles; a tile never crosses a rank.  What a unit costs beside them (loading
+// queries, writing rows) counts as `extra` empty tiles behind its own.  All
+// units' tiles in a row are cut into equal runs, one per CTA, so a CTA holds the end of one unit, some whole
 // units and the start of another.  A unit inside one run is finished by its
 // CTA; one that is cut leaves a partial per run, which the merge joins.
 // Partial slots: a run has at most two cut pieces, its first (slot 2 run) and
@@ -28,6 +29,7 @@ struct TreeArgs {
   int rows;               // query rows of a block: whole nodes
   int tile;               // tokens of a tile
   int parts;              // most runs
+  int extra;              // tiles that a unit's start and end cost beside its own
   float sl2;              // scale * log2(e)
   dcp_rank_ptrs_t k, v;
   const int32_t* bt;
@@ -72,20 +74,28 @@ __device__ __forceinline__ TreeEntry tree_load(const TreeArgs& A, int e) {
   return n;
 }
 
-// Tokens of [0, len) on rank r.
-__host__ __device__ __forceinline__ int tree_local(int64_t len, int r, const Layout& L) {
-  const int64_t vbs = (int64_t)L.bs * L.dcp;
-  const int rem = (int)(len % vbs), turn = L.I * L.dcp;
-  int p = rem % turn - r * L.I;
-  p = p < 0 ? 0 : (p > L.I ? L.I : p);
-  return (int)(len / vbs * L.bs) + rem / turn * L.I + p;
-}
+// Tokens of [0, len) on rank r are base + clamp(rest - r * I, 0, I): whole
+// turns round the ranks, and what the last one leaves.
+struct TreeLen {
+  int base, rest;
+  __host__ __device__ __forceinline__ TreeLen(int len, const Layout& L) {
+    const uint32_t vbs = (uint32_t)(L.bs * L.dcp), turn = (uint32_t)(L.I * L.dcp);
+    const uint32_t full = (uint32_t)len / vbs, rem = (uint32_t)len - full * vbs;
+    const uint32_t q = rem / turn;
+    base = (int)(full * L.bs + q * L.I);
+    rest = (int)(rem - q * turn);
+  }
+  __host__ __device__ __forceinline__ int on(int r, const Layout& L) const {
+    const int p = rest - r * L.I;
+    return base + (p < 0 ? 0 : (p > L.I ? L.I : p));
+  }
+};
 
 // Global position of rank r's local position p.
-__device__ __forceinline__ int64_t tree_global(int p, int r, const Layout& L) {
+__device__ __forceinline__ int tree_global(int p, int r, const Layout& L) {
   const int vb = p / L.bs, loc = p - vb * L.bs;
   const int run = loc / L.I;
-  return (int64_t)vb * L.bs * L.dcp + ((int64_t)run * L.dcp + r) * L.I + (loc - run * L.I);
+  return vb * L.bs * L.dcp + (run * L.dcp + r) * L.I + (loc - run * L.I);
 }
 
 // Run k of the tiles [0, total) over `parts`.
@@ -128,26 +138,34 @@ __device__ __forceinline__ TreeWalk tree_walk(const TreeArgs& A, int run) {
   return w;
 }
 
-// The piece at the walk's tile, which then stands behind it.
-__device__ __forceinline__ TreePiece tree_next(const TreeArgs& A, TreeWalk& w) {
-  while (w.t >= w.n.tile0 + (int64_t)w.n.units * w.n.per) w.n = tree_load(A, ++w.e);
-  TreePiece p;
-  p.b = A.per_rank ? w.e / A.L.dcp : w.e;
-  p.r0 = A.per_rank ? w.e % A.L.dcp : 0;
-  p.r1 = A.per_rank ? p.r0 + 1 : A.L.dcp;
-  p.T = w.n.nodes;
-  p.ctx = w.n.ctx;
-  p.q0 = w.n.q0;
-  const int in = (int)(w.t - w.n.tile0);
-  const int ui = in / w.n.per, blocks = w.n.units / A.Hkv;
-  p.g = ui / blocks;
-  p.rb = ui - p.g * blocks;
-  p.t0 = in - ui * w.n.per;
-  const int64_t left = w.end - w.t;
-  p.n = w.n.per - p.t0 < left ? w.n.per - p.t0 : (int)left;
-  p.slot = p.t0 == 0 && p.n == w.n.per ? -1 : 2 * w.run + (w.t == w.begin ? 0 : 1);
-  w.t += p.n;
-  return p;
+// The next piece of the walk, if one is left.
+__device__ __forceinline__ bool tree_next(const TreeArgs& A, TreeWalk& w, TreePiece& p) {
+  while (w.t < w.end) {
+    const int unit = w.n.per + A.extra;
+    if (w.t >= w.n.tile0 + (int64_t)w.n.units * unit) {
+      w.n = tree_load(A, ++w.e);
+      continue;
+    }
+    const int64_t in = w.t - w.n.tile0;
+    const int ui = (int)(in / unit), blocks = w.n.units / A.Hkv;
+    p.t0 = (int)(in - (int64_t)ui * unit);
+    const int64_t left = w.end - w.t;
+    const int take = unit - p.t0 < left ? unit - p.t0 : (int)left;   // with empty ones
+    p.n = min(p.t0 + take, w.n.per) - p.t0;
+    p.slot = p.t0 == 0 && p.n == w.n.per ? -1 : 2 * w.run + (w.t == w.begin ? 0 : 1);
+    w.t += take;
+    if (p.n <= 0) continue;
+    p.b = A.per_rank ? w.e / A.L.dcp : w.e;
+    p.r0 = A.per_rank ? w.e % A.L.dcp : 0;
+    p.r1 = A.per_rank ? p.r0 + 1 : A.L.dcp;
+    p.T = w.n.nodes;
+    p.ctx = w.n.ctx;
+    p.q0 = w.n.q0;
+    p.g = ui / blocks;
+    p.rb = ui - p.g * blocks;
+    return true;
+  }
+  return false;
 }
 
 // Token row of an output row: request row `row` (node * G + head of the group).

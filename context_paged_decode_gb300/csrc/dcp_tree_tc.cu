@@ -74,32 +74,31 @@ struct TreeTc {
   static constexpr uint32_t kColS = 0, kColO = 256;         // two of each, 128 and D apart
 };
 
-// Tiles of a unit in order: rank by rank.
+// Tiles of a piece in order: rank by rank.
 struct TileIt {
+  TreeLen len, old;       // with and without the nodes
   int r, tr, n, nt, lc;   // rank, tile on it, its tokens, tiles and context tokens
-  __device__ __forceinline__ void at(const TreeArgs& A, int rank, int64_t len, int64_t ctx) {
+  __device__ __forceinline__ void at(const TreeArgs& A, int rank) {
     r = rank;
-    n = tree_local(len, r, A.L);
+    n = len.on(r, A.L);
     nt = (n + kTtTile - 1) / kTtTile;
-    lc = tree_local(ctx, r, A.L);
+    lc = old.on(r, A.L);
   }
-  __device__ __forceinline__ void seek(const TreeArgs& A, const TreePiece& p, int64_t len,
-                                       int64_t ctx) {
-    at(A, p.r0, len, ctx);
+  __device__ __forceinline__ TileIt(const TreeArgs& A, const TreePiece& p)
+      : len(p.ctx + p.T, A.L), old(p.ctx, A.L) {
+    at(A, p.r0);
     tr = p.t0;
-    settle(A, p, len, ctx);
+    settle(A, p);
   }
-  __device__ __forceinline__ void settle(const TreeArgs& A, const TreePiece& p, int64_t len,
-                                         int64_t ctx) {
+  __device__ __forceinline__ void settle(const TreeArgs& A, const TreePiece& p) {
     while (tr >= nt && r + 1 < p.r1) {
       tr -= nt;
-      at(A, r + 1, len, ctx);
+      at(A, r + 1);
     }
   }
-  __device__ __forceinline__ void step(const TreeArgs& A, const TreePiece& p, int64_t len,
-                                       int64_t ctx, int k) {
+  __device__ __forceinline__ void step(const TreeArgs& A, const TreePiece& p, int k) {
     tr += k;
-    settle(A, p, len, ctx);
+    settle(A, p);
   }
 };
 
@@ -126,8 +125,8 @@ __device__ __noinline__ void tree_fix(const TreeArgs& A, const TreePiece& p, int
     place_token(ctx + j, A.L, r, vb, loc);
     if (r < p.r0 || r >= p.r1) continue;
     int t = (int)((vb * A.L.bs + loc) / kTtTile);        // tile of the unit
-    for (int x = p.r0; x < r; ++x)
-      t += (tree_local(ctx + T, x, A.L) + kTtTile - 1) / kTtTile;
+    const TreeLen len(p.ctx + T, A.L);
+    for (int x = p.r0; x < r; ++x) t += (len.on(x, A.L) + kTtTile - 1) / kTtTile;
     if (t < p.t0 || t >= p.t0 + p.n) continue;
     const int64_t phys =
         vb < A.max_vb ? (int64_t)__ldcg(A.bt + r * A.stride + (int64_t)p.b * A.max_vb + vb) : -1;
@@ -230,9 +229,8 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       const CUtensorMap* maps = val ? X.vmap : X.kmap;
       uint32_t slot = 0, par = 1;
       bool dead = false;
-      while (walk.t < walk.end && !dead) {
-        const TreePiece p = tree_next(A, walk);
-        const int64_t ctx = p.ctx, len = ctx + p.T;
+      TreePiece p;
+      while (!dead && tree_next(A, walk, p)) {
         const int32_t* bt = A.bt + (int64_t)p.b * A.max_vb;
         // This lane's part of a tile: table entry (-1: beyond the table), its
         // row in the page, and whether it has tokens.  The entry is loaded
@@ -241,8 +239,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
           int raw, off, r;
           bool has;
         };
-        TileIt it;
-        it.seek(A, p, len, ctx);
+        TileIt it(A, p);
         int fetched = 0;
         auto fetch = [&]() {
           Part x;
@@ -257,7 +254,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
             x.off = pos - j * A.L.bs;
             if (x.has && j < A.max_vb) x.raw = __ldcg(bt + it.r * A.stride + j);
             ++fetched;
-            if (fetched < p.n) it.step(A, p, len, ctx, 1);
+            if (fetched < p.n) it.step(A, p, 1);
           }
           return x;
         };
@@ -301,8 +298,8 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       if (lane == 0) {
         uint32_t item = 0;
         bool dead = false;
-        while (walk.t < walk.end) {
-          const TreePiece p = tree_next(A, walk);
+        TreePiece p;
+        while (tree_next(A, walk, p)) {
           if (item > 0 && !mbar_wait(b_qfree, (item - 1) & 1)) {
             dead = true;
             break;
@@ -319,15 +316,20 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
         }
         if (dead) atomicAdd(errp, kTtStuck);
       }
-    } else if (lane == 0) {
+    } else {
       // ---------------- products ----------------
+      // The whole warp runs this, with values that all lanes share (what is
+      // read from memory is broadcast so that the compiler knows it), and one
+      // lane is elected per instruction.  From a single-lane branch, beside
+      // two softmax warps, a product took twice its 64 cycles to issue.
       constexpr uint32_t kIdQK = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t kIdPV = idesc_bf16_f32(128, D, false, true);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       uint32_t ks = 0, kp = 0, vs = 0, vp = 0;   // ring places and parities
       uint32_t item = 0, np0 = 0, np1 = 0;
       bool dead = false;
       auto wait = [&](uint32_t bar, uint32_t par) {
-        if (!dead && !mbar_wait(bar, par)) dead = true;
+        if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar, par))) dead = true;
         return !dead;
       };
       // scores of the ring's next tile into stream s; `last`: its last reader
@@ -337,15 +339,13 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
         const uint64_t a = sdesc_sw128(sbase + C::kQOff + (kTwo ? s * C::kSlot : 0), 0, 1024);
         const uint64_t b = sdesc_sw128(sbase + ks * C::kSlot, 0, 1024);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t off = (uint64_t)((c * kHalfBytes + kk * 32) >> 4);
-            tc_mma_ss(tmem + C::kColS + s * 128, a + off, b + off, kIdQK, (c | kk) != 0);
-          }
-        tc_commit(b_s + 8 * s);
+        for (int i = 0; i < D / 16; ++i) {
+          const uint64_t off = (uint64_t)(((i >> 2) * kHalfBytes + (i & 3) * 32) >> 4);
+          tc_mma_ss_elect(tm + C::kColS + s * 128, a + off, b + off, kIdQK, i);
+        }
+        tc_commit_elect(b_s + 8 * s);
         if (last) {
-          tc_commit(b_kfree + 8 * ks);
+          tc_commit_elect(b_kfree + 8 * ks);
           if (++ks == C::kKSlots) {
             ks = 0;
             kp ^= 1;
@@ -358,48 +358,47 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
         tc_fence_after();
         const uint64_t v = sdesc_sw128(sbase + C::kVOff + vs * C::kSlot, kHalfBytes, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc_mma_ts(tmem + C::kColO + s * D, tmem + C::kColS + s * 128 + kk * 8,
-                    v + (uint64_t)((kk * 16 * 128) >> 4), kIdPV, (!first || kk > 0) ? 1u : 0u);
+        for (int i = 0; i < kTtTile / 16; ++i)
+          tc_mma_ts_elect(tm + C::kColO + s * D, tm + C::kColS + s * 128 + i * 8,
+                          v + (uint64_t)((i * 16 * 128) >> 4), kIdPV, (!first || i > 0) ? 1u : 0u);
         if (last) {
-          tc_commit(b_vfree + 8 * vs);
+          tc_commit_elect(b_vfree + 8 * vs);
           if (++vs == C::kVSlots) {
             vs = 0;
             vp ^= 1;
           }
         }
       };
-      for (; walk.t < walk.end && !dead; ++item) {
-        const TreePiece p = tree_next(A, walk);
+      TreePiece p;
+      for (; !dead && tree_next(A, walk, p); ++item) {
+        const int n = __shfl_sync(0xffffffffu, p.n, 0);
         wait(b_q, item & 1);
         if (!kTwo) {
-          for (int k = 0; k <= p.n && !dead; ++k) {
-            if (k < p.n) {
+#pragma unroll 1
+          for (int k = 0; k <= n && !dead; ++k) {
+            if (k < n) {
               qk(k & 1, true);
-              if (k == p.n - 1) tc_commit(b_qfree);
+              if (k == n - 1) tc_commit_elect(b_qfree);
             }
             if (k == 1) wait(b_ofree, (item & 1) ^ 1);
             if (k > 0) pv((k - 1) & 1, k <= 2, true);
           }
         } else {
-          const bool two = block_rows(p) > srows;
-          qk(0, !two);
-          if (two) qk(1, true);
-          if (p.n == 1) tc_commit(b_qfree);
-          wait(b_ofree, (item & 1) ^ 1);
-          for (int k = 0; k < p.n && !dead; ++k) {
-            pv(0, k == 0, !two);
-            if (k + 1 < p.n) qk(0, !two);
-            if (two) {
-              pv(1, k == 0, true);
-              if (k + 1 < p.n) qk(1, true);
+          const int streams = __shfl_sync(0xffffffffu, block_rows(p) > srows ? 2 : 1, 0);
+#pragma unroll 1
+          for (int k = 0; k <= n && !dead; ++k) {
+            if (k == 1) wait(b_ofree, (item & 1) ^ 1);
+#pragma unroll 1
+            for (int s = 0; s < streams; ++s) {
+              if (k > 0) pv(s, k == 1, s + 1 == streams);
+              if (k < n) qk(s, s + 1 == streams);
             }
-            if (k + 2 == p.n) tc_commit(b_qfree);
+            if (k == n - 1) tc_commit_elect(b_qfree);
           }
         }
-        if (!dead) tc_commit(b_o);
+        if (!dead) tc_commit_elect(b_o);
       }
-      if (dead) atomicAdd(errp, kTtStuck);
+      if (dead && lane == 0) atomicAdd(errp, kTtStuck);
     }
   } else {
     // ---------------- softmax: a row per thread ----------------
@@ -417,9 +416,8 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
     auto wait = [&](uint32_t bar, uint32_t par) {
       if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar, par))) dead = true;
     };
-    for (; walk.t < walk.end; ++item) {
-      const TreePiece p = tree_next(A, walk);
-      const int64_t ctx = p.ctx, len = ctx + p.T;
+    TreePiece p;
+    for (; tree_next(A, walk, p); ++item) {
       const int nrows = block_rows(p);
       const int srow0 = kTwo ? s * srows : 0;            // the stream's first row of the block
       const int brow = srow0 + row;                      // row of the block
@@ -433,79 +431,57 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       float m = -INFINITY, l = 0.f;
       bool filled = false;                               // the accumulator holds earlier tiles
       if (takes) {
-        TileIt it;
-        it.seek(A, p, len, ctx);
-        if (!kTwo && s == 1 && p.n > 1) it.step(A, p, len, ctx, 1);
-        for (int k = kTwo ? 0 : s; k < p.n; k += step) {
-          const int p0 = it.tr * kTtTile, nv = min(kTtTile, it.n - p0);
-          // usable pages of the tile, 16 tokens a bit
-          bool good = true;
-          if (lane < 8 && lane * 16 < nv) {
-            const int j = (p0 + lane * 16) / A.L.bs;
-            const int raw =
-                j < A.max_vb ? __ldcg(A.bt + it.r * A.stride + (int64_t)p.b * A.max_vb + j) : -1;
-            good = raw >= 0 && (int64_t)raw < A.nb;
+        // The table entries of a tile's pages (16 tokens a lane) are loaded
+        // a tile ahead.
+        TileIt it(A, p);
+        if (!kTwo && s == 1 && p.n > 1) it.step(A, p, 1);
+        int raw;
+        auto fetch = [&]() {
+          raw = -2;   // no tokens
+          const int p0 = it.tr * kTtTile + lane * 16;
+          if (lane < 8 && p0 < it.n) {
+            const int j = p0 / A.L.bs;
+            raw = j < A.max_vb ? __ldcg(A.bt + it.r * A.stride + (int64_t)p.b * A.max_vb + j) : -1;
           }
-          const uint32_t pages = __ballot_sync(0xffffffffu, good);
-          const bool special = nv < kTtTile || p0 + nv > it.lc || (pages & 0xFFu) != 0xFFu;
+        };
+        fetch();
+        for (int k = kTwo ? 0 : s; k < p.n; k += step) {
+          const int p0 = it.tr * kTtTile, nv = min(kTtTile, it.n - p0), old_n = it.lc - p0;
+          const int rank = it.r;
+          const uint32_t pages =
+              __ballot_sync(0xffffffffu, raw == -2 || (raw >= 0 && (int64_t)raw < A.nb));
+          if (k + step < p.n) {
+            it.step(A, p, step);
+            fetch();
+          }
+          // a tile whose tokens all rows see takes no masks
+          const bool special = nv < kTtTile || nv > old_n || (pages & 0xFFu) != 0xFFu;
           uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+          uint32_t v_old = ~0u, v_node = 0;   // of this warp's 32 tokens of V
+          uint32_t masked = 0;                // groups that some row sees in part
           if (special) {
-            // V rows of this warp's 32 tokens: those nobody sees become zero,
-            // and so do odd values of nodes
-            const uint32_t vi = seq + k, vslot = vi % C::kVSlots;
-            wait(b_v + 8 * vslot, (vi / C::kVSlots) & 1);
-            const uint32_t v = sbase + C::kVOff + vslot * C::kSlot;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               // token g * 32 + lane: seen by everyone, a node, or not there
-              const int tk = g * 32 + lane, pos = p0 + tk;
+              const int tk = g * 32 + lane;
               const bool there = tk < nv && ((pages >> (tk >> 4)) & 1);
-              const bool old = there && pos < it.lc;
-              const uint32_t olds = __ballot_sync(0xffffffffu, old);
+              const bool old = there && tk < old_n;
+              vis[g] = __ballot_sync(0xffffffffu, old);
               uint32_t nodes = __ballot_sync(0xffffffffu, there && !old);
-              const int node =
-                  there && !old ? (int)(tree_global(pos, it.r, A.L) - ctx) & 63 : 0;
-              vis[g] = olds;
-              if (g == quarter && !dead) {
-                constexpr int kRow = D / 8;                // 16-byte pieces of a row
-                for (int i = lane; i < 32 * kRow; i += 32) {
-                  const int o = i / kRow, ch = i % kRow;
-                  if ((olds >> o) & 1) continue;
-                  const int tok = g * 32 + o;
-                  const uint32_t at = v + (ch >> 3) * kHalfBytes + tok * 128 +
-                                      (((ch & 7) ^ (tok & 7)) << 4);
-                  uint32_t w[4] = {0u, 0u, 0u, 0u};
-                  bool odd = !((nodes >> o) & 1);
-                  if (!odd) {
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                 : "r"(at));
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                      if (bf16_odd(w[x])) {
-                        w[x] &= 0xFFFF0000u;
-                        odd = true;
-                      }
-                      if (bf16_odd(w[x] >> 16)) {
-                        w[x] &= 0xFFFFu;
-                        odd = true;
-                      }
-                    }
-                    if (odd) flag[item & 1] = (int)item + 1;
-                  }
-                  if (odd)
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]),
-                                 "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                 : "memory");
-                }
-                fence_proxy_async_smem();
+              if (vis[g] != ~0u) masked |= 1u << g;
+              if (g == quarter) {
+                v_old = vis[g];
+                v_node = nodes;
               }
-              // the nodes among them, by this row's mask
-              while (nodes) {
-                const int o = __ffs(nodes) - 1;
-                nodes &= nodes - 1;
-                const int j = __shfl_sync(0xffffffffu, node, o);
-                vis[g] |= ((uint32_t)(mask >> j) & 1u) << o;
+              if (nodes) {   // by this row's mask
+                const int node =
+                    there && !old ? (tree_global(p0 + tk, rank, A.L) - p.ctx) & 63 : 0;
+                do {
+                  const int o = __ffs(nodes) - 1;
+                  nodes &= nodes - 1;
+                  const int j = __shfl_sync(0xffffffffu, node, o);
+                  vis[g] |= ((uint32_t)(mask >> j) & 1u) << o;
+                } while (nodes);
               }
             }
           }
@@ -522,9 +498,11 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
               if (special) {
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
+                  if ((masked >> g) & 1) {
 #pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    if (!((vis[g] >> i) & 1)) x[g][i] = 0xff800000u;   // -inf
+                    for (int i = 0; i < 32; ++i)
+                      if (!((vis[g] >> i) & 1)) x[g][i] = 0xff800000u;   // -inf
+                  }
               }
             };
             load();
@@ -577,11 +555,50 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             filled = true;
             tc_wait_st();
-            tc_fence_before();
           }
+          if (v_old != ~0u) {
+            // V rows of this warp's tokens: those nobody sees become zero, and
+            // so do odd values of nodes
+            const uint32_t vi = seq + k, vslot = vi % C::kVSlots;
+            wait(b_v + 8 * vslot, (vi / C::kVSlots) & 1);
+            const uint32_t v = sbase + C::kVOff + vslot * C::kSlot;
+            constexpr int kRow = D / 8;                // 16-byte pieces of a row
+            if (!dead)
+              for (int i = lane; i < 32 * kRow; i += 32) {
+                const int o = i / kRow, ch = i % kRow;
+                if ((v_old >> o) & 1) continue;
+                const int tok = quarter * 32 + o;
+                const uint32_t at =
+                    v + (ch >> 3) * kHalfBytes + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4);
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+                bool odd = !((v_node >> o) & 1);
+                if (!odd) {
+                  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                               : "r"(at));
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    if (bf16_odd(w[x])) {
+                      w[x] &= 0xFFFF0000u;
+                      odd = true;
+                    }
+                    if (bf16_odd(w[x] >> 16)) {
+                      w[x] &= 0xFFFFu;
+                      odd = true;
+                    }
+                  }
+                  if (odd) flag[item & 1] = (int)item + 1;
+                }
+                if (odd)
+                  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]),
+                               "r"(w[1]), "r"(w[2]), "r"(w[3])
+                               : "memory");
+              }
+            fence_proxy_async_smem();
+          }
+          tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(b_p + 8 * s);
-          if (k + step < p.n) it.step(A, p, len, ctx, step);
         }
       }
       // ---------------- the unit's (or piece's) rows ----------------
