@@ -15,11 +15,15 @@
 // order does not matter; two that a request's release and another's share one
 // page are both counted before any page is taken.
 //
-// One cluster of eight CTAs runs each table from end to end; its phases are
-// separated by cluster barriers, so a call is one launch (and a small one that
-// stores the lengths, which every table reads).  What bounds it: latency, a
-// dozen dependent loads and barriers; the entries themselves move at 4096
-// threads a table.
+// One cluster of eight CTAs runs each table from end to end, separated by two
+// or three cluster barriers; a small second launch stores the lengths, which
+// every table reads.  What bounds it: latency.  So each CTA checks the whole
+// list for itself in shared memory (a hash of the requests finds names that
+// come twice, and children that are parents) rather than ask the others, and
+// pages are handed out 32 at a time, a lane per bit of the bitmap.  (With the
+// claims and prefix sums in global memory and a thread per bitmap word, 128
+// forks of 250 pages on 8 ranks took 41 us, and 128 requests of a few new
+// pages 28.)
 #include "dcp_common.cuh"
 #include "dcp_ptx.cuh"
 
@@ -28,6 +32,9 @@ namespace dcp {
 constexpr int kPgCluster = 8;
 constexpr int kPgThreads = 512;
 constexpr int kPgAll = kPgCluster * kPgThreads;   // threads of a table
+
+constexpr int kPgWarps = kPgAll / 32;
+constexpr int kPgMaxList = 2048;
 
 struct PagesArgs {
   Layout L;
@@ -43,79 +50,45 @@ struct PagesArgs {
   const int32_t* up;   // fork: parent rows
   const int32_t* row;  // requests that change
   const int32_t* len;  // resize: their new lengths
-  int N;
+  int N, hash;         // list entries, slots of the hash (a power of two)
   int32_t* src;        // [tables][N]
   int32_t* dst;
-  char* ws;
-  size_t ws_table;     // workspace bytes of a table
+  int32_t* sums;       // workspace: free pages of each CTA's words [tables][kPgCluster]
+  int32_t* new_len;    // workspace: [N] what the lengths become (-1: entry skipped)
   int32_t* err;
 };
 
-// Workspace of one table: claim[B] (which list entry owns a request),
-// need[N] (pages << 1 | replaces the open page), first[N + 1] (needs before
-// n), old[N] (page to release after the allocation), sums[kPgCluster].
-struct PagesWs {
-  int32_t *claim, *need, *first, *old, *sums;
+// Shared memory of a CTA, in ints: the list and what was found about it.  The
+// hash is done with when needs are counted, and lies over the arrays for that.
+struct PagesList {
+  int *c, *p, *old, *len;          // request (-1: skipped), parent, old and new length
+  int *first, *need, *page;        // needs before n [N + 1], needs << 1 | open page again, page
+  int *key, *val;
+  __device__ __forceinline__ PagesList(int* sm, int N, int hash) {
+    c = sm;
+    p = c + N;
+    old = p + N;
+    len = old + N;
+    first = len + N;
+    need = first + N + 1;
+    page = need + N;
+    key = first;
+    val = key + hash;
+  }
 };
 
-__host__ __device__ inline size_t pages_ws_table(int64_t B, int64_t N) {
-  return ((size_t)(B + 3 * N + 1 + kPgCluster) * sizeof(int32_t) + 255) / 256 * 256;
-}
-
-__device__ __forceinline__ PagesWs pages_ws(const PagesArgs& A, int table) {
-  PagesWs w;
-  w.claim = (int32_t*)(A.ws + A.ws_table * table);
-  w.need = w.claim + A.B;
-  w.first = w.need + A.N;
-  w.old = w.first + A.N + 1;
-  w.sums = w.old + A.N;
-  return w;
+static size_t pages_smem(int N, int hash) {
+  const size_t over = (size_t)2 * hash > (size_t)3 * N + 1 ? (size_t)2 * hash : (size_t)3 * N + 1;
+  return ((size_t)4 * N + over) * sizeof(int32_t);
 }
 
 // Tokens of the open page of a length on rank r (0 .. bs; a shared table's
 // page stands for the whole virtual block).
-__device__ __forceinline__ int open_tokens(const PagesArgs& A, int64_t len, int r) {
+__device__ __forceinline__ int open_tokens(const PagesArgs& A, int len, int r) {
   const int vbs = A.L.bs * A.L.dcp, turn = A.L.I * A.L.dcp;
-  const int rem = (int)(len % vbs);
+  const int rem = len % vbs;
   if (A.shared) return rem;
   return rem / turn * A.L.I + min(max(rem % turn - r * A.L.I, 0), A.L.I);
-}
-
-// State is read past the SM's L1 (__ldcg) throughout: other CTAs write it in
-// this call, and the kernels of the call before may still run when this one is
-// launched.
-struct PagesReq {
-  bool ok;
-  int c;          // row that changes
-  int p;          // fork: parent
-  int64_t old, len;
-  int ov, nv;     // virtual blocks held before and after
-};
-
-// One entry of the list, checked.  Reads claim, so only after its barrier.
-template <bool kFork>
-__device__ __forceinline__ PagesReq pages_req(const PagesArgs& A, const PagesWs& w, int n) {
-  PagesReq q;
-  const int64_t vbs = (int64_t)A.L.bs * A.L.dcp;
-  q.ok = false;
-  q.c = __ldcg(A.row + n);
-  q.p = kFork ? __ldcg(A.up + n) : -1;
-  q.old = q.len = 0;
-  q.ov = q.nv = 0;
-  if (q.c < 0 || q.c >= A.B || __ldcg(w.claim + q.c) != n) return q;
-  if (kFork) {
-    // a parent that the same call overwrites has no defined pages
-    if (q.p < 0 || q.p >= A.B || __ldcg(w.claim + q.p) != 0x7fffffff) return q;
-    q.len = __ldcg(A.seq + q.p);
-  } else {
-    q.len = __ldcg(A.len + n);
-  }
-  q.old = max(__ldcg(A.seq + q.c), 0);
-  if (q.len < 0 || (q.len + vbs - 1) / vbs > A.max_vb) return q;
-  q.nv = (int)((q.len + vbs - 1) / vbs);
-  q.ov = (int)min((q.old + vbs - 1) / vbs, (int64_t)A.max_vb);
-  q.ok = true;
-  return q;
 }
 
 __device__ __forceinline__ void release_page(const PagesArgs& A, int32_t* ref, uint32_t* bits,
@@ -153,125 +126,178 @@ __device__ __forceinline__ int pg_scan(int v, int* sh, int* total) {
   return before + x - v;
 }
 
+// State is read past the SM's L1 (__ldcg) throughout: other CTAs write it in
+// this call, and the kernels of the call before may still run when this one is
+// launched.
 template <bool kFork>
 __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
 pages_kernel(const __grid_constant__ PagesArgs A) {
+  extern __shared__ int sm[];
   __shared__ int sh[kPgThreads / 32];
+  __shared__ int s_any;
   griddep_launch_dependents();   // the next call's first kernel may start its launch
   griddep_wait();                // launched chained: the preceding kernel completed
   const int table = blockIdx.x / kPgCluster;
   const int cta = (int)cluster_ctarank();
   const int tid = threadIdx.x, lane = tid & 31;
-  const int gid = cta * kPgThreads + tid;
-  const PagesWs w = pages_ws(A, table);
+  const int gw = cta * (kPgThreads / 32) + (tid >> 5);   // warp of the table
+  const int N = A.N, vbs = A.L.bs * A.L.dcp;
   int32_t* bt = A.bt + table * A.stride;
   int32_t* ref = A.ref + (int64_t)table * A.nb;
   uint32_t* bits = A.bits + (int64_t)table * A.words;
-  int32_t* src = A.src + (int64_t)table * A.N;
-  int32_t* dst = A.dst + (int64_t)table * A.N;
-  const int full = A.shared ? A.L.bs * A.L.dcp : A.L.bs;   // tokens that fill an open page
+  int32_t* src = A.src + (int64_t)table * N;
+  int32_t* dst = A.dst + (int64_t)table * N;
+  const int full = A.shared ? vbs : A.L.bs;   // tokens that fill an open page
+  auto blocks = [&](int len) { return (int)(((int64_t)len + vbs - 1) / vbs); };
 
-  // who changes which request: the first entry that names it
-  for (int i = gid; i < A.B; i += kPgAll) w.claim[i] = 0x7fffffff;
-  cluster_sync();
-  for (int n = gid; n < A.N; n += kPgAll) {
-    const int c = __ldcg(A.row + n);
-    if (c >= 0 && c < A.B) atomicMin(w.claim + c, n);
+  // the list, and the first entry that names each request
+  PagesList S(sm, N, A.hash);
+  if (tid == 0) s_any = 0;
+  for (int n = tid; n < N; n += kPgThreads) {
+    S.c[n] = __ldcg(A.row + n);
+    S.p[n] = kFork ? __ldcg(A.up + n) : __ldcg(A.len + n);
   }
-  cluster_sync();
-
-  // releases.  `share` warps take turns on one entry where there are few.
-  const int nwarps = kPgAll / 32, gw = gid >> 5;
-  const int share = A.N < nwarps ? nwarps / max(A.N, 1) : 1;
-  for (int n = gw / share; n < A.N; n += nwarps / share) {
-    const PagesReq q = pages_req<kFork>(A, w, n);
-    if (!q.ok) continue;
-    int32_t* row = bt + (int64_t)q.c * A.max_vb;
-    const int v0 = kFork ? 0 : q.nv;
-    const int step = 32 * share;
-    for (int v = v0 + (gw % share) * 32 + lane; v < q.ov; v += 4 * step) {
-      int id[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) id[j] = v + j * step < q.ov ? __ldcg(row + v + j * step) : 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (v + j * step < q.ov) {
-          release_page(A, ref, bits, id[j]);
-          row[v + j * step] = -1;
-        }
+  for (int i = tid; i < A.hash; i += kPgThreads) {
+    S.key[i] = -1;
+    S.val[i] = 0x7fffffff;
+  }
+  __syncthreads();
+  auto slot = [&](int c) { return (int)((uint32_t)c * 2654435761u >> 7) & (A.hash - 1); };
+  for (int n = tid; n < N; n += kPgThreads) {
+    const int c = S.c[n];
+    if (c < 0 || c >= A.B) continue;
+    int h = slot(c);
+    for (;;) {   // ends: the hash has at least twice as many slots as entries
+      const int k = atomicCAS(S.key + h, -1, c);
+      if (k == -1 || k == c) break;
+      h = (h + 1) & (A.hash - 1);
+    }
+    atomicMin(S.val + h, n);
+  }
+  __syncthreads();
+  auto named = [&](int c) {   // first entry that names c, or none
+    int h = slot(c);
+    while (S.key[h] != c && S.key[h] != -1) h = (h + 1) & (A.hash - 1);
+    return S.key[h] == c ? S.val[h] : 0x7fffffff;
+  };
+  for (int n = tid; n < N; n += kPgThreads) {
+    const int c = S.c[n], x = S.p[n];
+    bool ok = c >= 0 && c < A.B && named(c) == n;
+    int old = 0, len = x;
+    // a parent that the same call overwrites has no defined pages
+    if (ok && kFork) ok = x >= 0 && x < A.B && named(x) == 0x7fffffff;
+    if (ok) {
+      old = max(__ldcg(A.seq + c), 0);
+      if (kFork) len = __ldcg(A.seq + x);
+      ok = len >= 0 && blocks(len) <= A.max_vb;
+    }
+    S.old[n] = min(blocks(old), A.max_vb) == blocks(old) ? old : A.max_vb * vbs;
+    S.len[n] = ok ? len : -1;
+    if (table == 0 && cta == 0) {
+      if (!ok) count_error(A.err);
+      A.new_len[n] = ok ? len : -1;
     }
   }
-  cluster_sync();
+  __syncthreads();   // (the hash is read for the last time above)
 
-  // needs of each entry, and the free pages of each CTA's part of the bitmap
-  for (int n = gid; n < A.N; n += kPgAll) {
-    const PagesReq q = pages_req<kFork>(A, w, n);
-    int need = 0, again = 0;
-    src[n] = dst[n] = -1;
-    w.old[n] = -1;
-    if (!q.ok) {
-      if (table == 0) count_error(A.err);
-    } else {
-      const int64_t cut = kFork ? q.len : min(q.old, q.len);
-      const int64_t vbs = (int64_t)A.L.bs * A.L.dcp;
-      const int cv = (int)(cut / vbs);
-      if (cut % vbs != 0 && open_tokens(A, cut, table) < full) {
-        if (kFork) {
-          again = 1;
-        } else {
-          const int id = __ldcg(bt + (int64_t)q.c * A.max_vb + cv);
-          again = id >= 0 && id < A.nb && __ldcg(ref + id) > 1;
-        }
+  // Releases, and for a fork the pages that the child shares with its parent.
+  // The parent holds those throughout, so no release can free one.  `share`
+  // warps take turns on an entry where there are few.
+  const int share = N < kPgWarps ? kPgWarps / N : 1;
+  for (int n = gw / share; n < N; n += kPgWarps / share) {
+    const int len = S.len[n];
+    if (len < 0) continue;
+    int32_t* row = bt + (int64_t)S.c[n] * A.max_vb;
+    const int32_t* from = bt + (int64_t)(kFork ? S.p[n] : 0) * A.max_vb;
+    const int ov = blocks(S.old[n]), nv = blocks(len);
+    // a fork's last page is not shared if it is open
+    const int kept = kFork ? nv - (len % vbs != 0 && open_tokens(A, len, table) < full) : 0;
+    const int v0 = kFork ? 0 : nv, v1 = max(ov, kept), step = 32 * share;
+    for (int v = v0 + (gw % share) * 32 + lane; v < v1; v += 4 * step) {
+      int gone[4], take[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int u = v + j * step;
+        gone[j] = u < ov ? __ldcg(row + u) : -1;
+        take[j] = u < kept ? __ldcg(from + u) : -1;
       }
-      need = again + (kFork ? 0 : max(q.nv - q.ov, 0));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int u = v + j * step;
+        if (u >= v1) continue;
+        if (u < ov) release_page(A, ref, bits, gone[j]);
+        int id = -1;
+        if (u < kept) {
+          if (take[j] >= 0 && take[j] < A.nb) {
+            id = take[j];
+            atomicAdd(ref + id, 1);
+          } else {
+            count_error(A.err);
+          }
+        }
+        row[u] = id;
+      }
     }
-    w.need[n] = need << 1 | again;
   }
-  const int per = (A.words + kPgAll - 1) / kPgAll;
-  const int w0 = min(gid * per, A.words), w1 = min(w0 + per, A.words);
+  cluster_sync();
+
+  // what each entry needs, summed up by every CTA for itself
+  int W = 0;
+  for (int n0 = 0; n0 < N; n0 += kPgThreads) {
+    const int n = n0 + tid;
+    int need = 0, again = 0, page = -1;
+    if (n < N && S.len[n] >= 0) {
+      const int old = S.old[n], len = S.len[n], cut = kFork ? len : min(old, len);
+      const int cv = cut / vbs;
+      if (cut % vbs != 0 && open_tokens(A, cut, table) < full) {
+        page = __ldcg(bt + (int64_t)(kFork ? S.p[n] : S.c[n]) * A.max_vb + cv);
+        again = kFork || (page >= 0 && page < A.nb && __ldcg(ref + page) > 1);
+      }
+      need = again + (kFork ? 0 : max(blocks(len) - blocks(old), 0));
+    }
+    int sum;
+    const int at = pg_scan(need, sh, &sum);
+    if (n < N) {
+      S.first[n] = W + at;
+      S.need[n] = need << 1 | again;
+      S.page[n] = page;
+      if (again) s_any = 1;
+      if (n / kPgThreads % kPgCluster == cta) src[n] = dst[n] = -1;
+    }
+    W += sum;
+  }
+  if (tid == 0) S.first[N] = W;
+  // free pages of this warp's words
+  const int per = (A.words + kPgWarps - 1) / kPgWarps;
+  const int w0 = min(gw * per, A.words), w1 = min(w0 + per, A.words);
   int mine = 0, sum;
-  for (int i = w0; i < w1; ++i) mine += __popc(__ldcg(bits + i));
-  int base = pg_scan(mine, sh, &sum);
-  if (tid == 0) w.sums[cta] = sum;
+  for (int i = w0 + lane; i < w1; i += 32) mine += __popc(__ldcg(bits + i));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  int base = pg_scan(lane == 0 ? mine : 0, sh, &sum);
+  base = __shfl_sync(0xffffffffu, base, 0);
+  if (tid == 0) A.sums[table * kPgCluster + cta] = sum;
   cluster_sync();
 
-  // CTA 0 counts the needs before each entry
-  if (cta == 0) {
-    int run = 0;
-    for (int n0 = 0; n0 < A.N; n0 += kPgThreads) {
-      const int n = n0 + tid;
-      const int v = n < A.N ? __ldcg(w.need + n) >> 1 : 0;
-      const int at = pg_scan(v, sh, &sum);
-      if (n < A.N) w.first[n] = run + at;
-      run += sum;
-    }
-    if (tid == 0) w.first[A.N] = run;
-  }
-  cluster_sync();
-
-  // page k of the free ones, in increasing order, goes to need k
-  const int W = __ldcg(w.first + A.N);
   int have = 0;
   for (int i = 0; i < kPgCluster; ++i) {
-    const int s = __ldcg(w.sums + i);
+    const int s = __ldcg(A.sums + table * kPgCluster + i);
     if (i < cta) base += s;
     have += s;
   }
+  // page k of the free ones, in increasing order, goes to need k
   auto give = [&](int k, int id) {
-    int lo = 0, hi = A.N;   // first[lo] <= k < first[hi]
+    int lo = 0, hi = N;   // first[lo] <= k < first[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldcg(w.first + mid) <= k) lo = mid; else hi = mid;
+      if (S.first[mid] <= k) lo = mid; else hi = mid;
     }
-    const PagesReq q = pages_req<kFork>(A, w, lo);
-    int j = k - __ldcg(w.first + lo);
-    int32_t* row = bt + (int64_t)q.c * A.max_vb;
-    if (__ldcg(w.need + lo) & 1) {
+    int j = k - S.first[lo];
+    int32_t* row = bt + (int64_t)S.c[lo] * A.max_vb;
+    if (S.need[lo] & 1) {
       if (j == 0) {   // the open page
-        const int64_t cut = kFork ? q.len : min(q.old, q.len);
-        const int cv = (int)(cut / ((int64_t)A.L.bs * A.L.dcp));
-        const int from = __ldcg(kFork ? bt + (int64_t)q.p * A.max_vb + cv : row + cv);
-        if (!kFork) w.old[lo] = from;
+        const int cut = kFork ? S.len[lo] : min(S.old[lo], S.len[lo]);
+        const int from = S.page[lo];
         if (open_tokens(A, cut, table) > 0) {
           if (from < 0 || from >= A.nb) {
             count_error(A.err);
@@ -280,78 +306,48 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
             dst[lo] = id;
           }
         }
-        row[cv] = id;
+        row[cut / vbs] = id;
         return;
       }
       --j;
     }
-    row[q.ov + j] = id;
+    row[blocks(S.old[lo]) + j] = id;
   };
-  if (mine > 0 && base < W) {
-    int k = base;
-    for (int i = w0; i < w1 && k < W; ++i) {
-      uint32_t word = __ldcg(bits + i), taken = 0;
-      while (word && k < W) {
-        const int bit = __ffs(word) - 1;
-        word &= word - 1;
-        taken |= 1u << bit;
-        const int id = i * 32 + bit;
+  for (int i0 = w0; i0 < w1 && base < W; i0 += 32) {
+    const uint32_t mine_w = i0 + lane < w1 ? __ldcg(bits + i0 + lane) : 0u;
+    for (int i = i0; i < min(i0 + 32, w1) && base < W; ++i) {
+      const uint32_t word = __shfl_sync(0xffffffffu, mine_w, i - i0);
+      const int k = base + __popc(word & ((1u << lane) - 1u));
+      const bool take = ((word >> lane) & 1) && k < W;
+      if (take) {
+        const int id = i * 32 + lane;
         ref[id] = 1;
-        give(k++, id);
+        give(k, id);
       }
-      if (taken) atomicAnd(bits + i, ~taken);
+      const uint32_t taken = __ballot_sync(0xffffffffu, take);
+      if (lane == 0 && taken) bits[i] = word & ~taken;
+      base += __popc(word);
     }
   }
-  for (int k = have + gid; k < W; k += kPgAll) {   // no page left
+  for (int k = have + cta * kPgThreads + tid; k < W; k += kPgAll) {   // no page left
     count_error(A.err);
     give(k, -1);
   }
-  cluster_sync();
-
-  if (kFork) {
-    // the parents' other pages, one holder more
-    for (int n = gw / share; n < A.N; n += nwarps / share) {
-      const PagesReq q = pages_req<true>(A, w, n);
-      if (!q.ok) continue;
-      const int32_t* from = bt + (int64_t)q.p * A.max_vb;
-      int32_t* row = bt + (int64_t)q.c * A.max_vb;
-      const int nv = q.nv - (__ldcg(w.need + n) & 1);   // the open page has been given
-      const int step = 32 * share;
-      for (int v = (gw % share) * 32 + lane; v < nv; v += 4 * step) {
-        int id[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) id[j] = v + j * step < nv ? __ldcg(from + v + j * step) : 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (v + j * step >= nv) continue;
-          if (id[j] < 0 || id[j] >= A.nb) {
-            count_error(A.err);
-            id[j] = -1;
-          } else {
-            atomicAdd(ref + id[j], 1);
-          }
-          row[v + j * step] = id[j];
-        }
-      }
-    }
-  } else {
+  if (!kFork && s_any) {   // (the same in every CTA)
     // the shared open pages that were replaced, one holder less
-    for (int n = gid; n < A.N; n += kPgAll) {
-      const int id = __ldcg(w.old + n);
-      if (id >= 0) release_page(A, ref, bits, id);
-    }
+    cluster_sync();
+    for (int n = cta * kPgThreads + tid; n < N; n += kPgAll)
+      if (S.need[n] & 1) release_page(A, ref, bits, S.page[n]);
   }
 }
 
-// The lengths, once every table has read the old ones (table 0's claims).
-template <bool kFork>
+// The lengths, once every table has read the old ones.
 __global__ void pages_lens_kernel(const __grid_constant__ PagesArgs A) {
   griddep_launch_dependents();
   griddep_wait();
-  const PagesWs w = pages_ws(A, 0);
   for (int n = blockIdx.x * blockDim.x + threadIdx.x; n < A.N; n += gridDim.x * blockDim.x) {
-    const PagesReq q = pages_req<kFork>(A, w, n);
-    if (q.ok) A.seq[q.c] = (int32_t)q.len;
+    const int len = __ldcg(A.new_len + n);
+    if (len >= 0) A.seq[__ldcg(A.row + n)] = len;
   }
 }
 
@@ -369,6 +365,10 @@ __global__ void pages_init_kernel(int32_t* bt, int64_t entries, int32_t* seq, in
     const int64_t left = nb - (i % wpt) * 32;
     bits[i] = left >= 32 ? 0xffffffffu : (left > 0 ? (1u << left) - 1u : 0u);
   }
+}
+
+static size_t pages_ws_bytes(int N) {
+  return (size_t)(DCP_MAX_RANKS * kPgCluster + N) * sizeof(int32_t);
 }
 
 static int pages_tables(const dcp_layout_t& L, const dcp_pages_t& p) {
@@ -398,7 +398,7 @@ static int launch_pages(const dcp_layout_t& L, const dcp_pages_t& p, const int32
   if (N < 0) return DCP_EINVAL;
   if (N == 0) return DCP_OK;
   if (!row || (kFork ? !up : !len) || !src || !dst) return DCP_EINVAL;
-  if ((int64_t)N * p.max_vblocks >= (int64_t(1) << 30)) return DCP_EUNSUPPORTED;
+  if (N > kPgMaxList || (int64_t)N * p.max_vblocks >= (int64_t(1) << 30)) return DCP_EUNSUPPORTED;
   const int tables = pages_tables(L, p);
   PagesArgs A;
   A.L = Layout{L.dcp_size, L.block_size, L.interleave};
@@ -416,17 +416,26 @@ static int launch_pages(const dcp_layout_t& L, const dcp_pages_t& p, const int32
   A.row = row;
   A.len = len;
   A.N = N;
+  A.hash = 64;
+  while (A.hash < 2 * N) A.hash *= 2;
   A.src = src;
   A.dst = dst;
-  A.ws = (char*)ws;
-  A.ws_table = pages_ws_table(p.num_reqs, N);
+  A.sums = (int32_t*)ws;
+  A.new_len = A.sums + DCP_MAX_RANKS * kPgCluster;
   A.err = err;
-  if (!ws || ws_bytes < A.ws_table * tables) return DCP_EWORKSPACE;
+  if (!ws || ws_bytes < pages_ws_bytes(N)) return DCP_EWORKSPACE;
+  const size_t smem = pages_smem(N, A.hash);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(pages_kernel<kFork>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return DCP_ECUDA;
+  }
   cudaError_t e = launch_chained(pages_kernel<kFork>, (unsigned)(tables * kPgCluster), kPgThreads,
-                                 0, s, A);
+                                 smem, s, A);
   if (e != cudaSuccess) return launch_status_report(e);
   const unsigned grid = (unsigned)((N + 255) / 256 < 64 ? (N + 255) / 256 : 64);
-  e = launch_chained(pages_lens_kernel<kFork>, grid, 256, 0, s, A);
+  e = launch_chained(pages_lens_kernel, grid, 256, 0, s, A);
   if (e != cudaSuccess) return launch_status_report(e);
   return launch_status();
 }
@@ -460,7 +469,8 @@ int dcp_pages_workspace_size(dcp_layout_t layout, dcp_pages_t pages, int32_t num
   const int rc = pages_ok(layout, pages);
   if (rc != DCP_OK) return rc;
   if (!bytes || num < 0) return DCP_EINVAL;
-  *bytes = pages_ws_table(pages.num_reqs, num) * pages_tables(layout, pages);
+  if (num > kPgMaxList) return DCP_EUNSUPPORTED;
+  *bytes = pages_ws_bytes(num);
   return DCP_OK;
 }
 

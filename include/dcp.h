@@ -608,7 +608,10 @@ typedef struct {
 /* Every request unused, every page free. */
 int dcp_pages_init(dcp_layout_t layout, dcp_pages_t pages, dcp_stream_t stream);
 
-/* Bytes of workspace of dcp_pages_resize / dcp_pages_fork with `num` entries. */
+/*
+ * Bytes of workspace of dcp_pages_resize / dcp_pages_fork with `num` entries
+ * (at most 2048 a call).
+ */
 int dcp_pages_workspace_size(dcp_layout_t layout, dcp_pages_t pages, int32_t num, size_t* bytes);
 
 /*

@@ -117,6 +117,7 @@ def test_pages(dcp):
             assert call(name=name, **bad) == EINVAL, bad
         assert call(ws=None, name=name) == EWORKSPACE and call(nb=64, name=name) == EWORKSPACE
         assert call(p=pages(num_blocks=1 << 31), name=name) == EUNSUPPORTED
+        assert call(n=2049, name=name) == EUNSUPPORTED
         assert call(p=pages(max_vblocks=1 << 26, bt_rank_stride=1 << 40), name=name) == EUNSUPPORTED
     n = C.c_size_t(0)
     assert lib.dcp_pages_workspace_size(L, pages(), 3, C.byref(n)) == 0 and n.value > 0
