@@ -14,11 +14,14 @@
 // it (a position of 10^6 at frequency 1 is off by 0.03 rad).  The top 32 bits
 // of the fraction go to sincospif.
 //
-// What bounds it: reading q, k, v and writing them once.  One CTA per token:
-// a thread first issues the loads of its first units (a unit is two 16-byte
-// chunks, for rotated entries the two that hold both members of its pairs),
-// then the CTA computes the token's rot/2 cosines and sines once for all heads,
-// so the trigonometry hides behind the loads.
+// What bounds it: reading q, k, v and writing them once.  The heads of a token
+// are rows of one size; up to 16 KB of them (all of a token's, or a part) are
+// brought into a ring of shared memory by bulk copies, rotated in place, and
+// sent by bulk copies to q_out, k_out and each rank's pool, so no thread waits
+// for global memory and values and unrotated rows pass through no register.
+// The token's cosines and sines are computed meanwhile, once for its heads.
+// In place (q_out is q) only the rotated entries of q move: that is a kernel
+// with a CTA per token and plain loads.
 #include "dcp_common.cuh"
 #include "dcp_ptx.cuh"
 
@@ -107,6 +110,15 @@ __device__ __forceinline__ void rotate_unit(uint4& x, uint4& y, int u, int ru, c
 
 constexpr double kInv2Pi = 0.15915494309189535;          // 1 / (2 pi), rounded
 constexpr double kInv2PiLow = -9.839338337591243e-18;     // what the rounding left
+
+// Turns per position as a 64-bit fraction: inv_freq / (2 pi) in two doubles.
+__device__ __forceinline__ uint64_t turns_of(float inv_freq) {
+  const double f = (double)inv_freq;
+  const double hi = f * kInv2Pi;
+  const double lo = fma(f, kInv2Pi, -hi) + f * kInv2PiLow;
+  return (uint64_t)((hi - floor(hi)) * 18446744073709551616.0) +
+         (uint64_t)(int64_t)rint(lo * 18446744073709551616.0);
+}
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeBatch = 4;        // units in flight per thread
@@ -220,13 +232,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_c
       ax = 0;
     }
     const uint64_t p = (uint64_t)__ldcg(A.pos + (int64_t)ax * A.T + t);
-    // turns per position as a 64-bit fraction: inv_freq / (2 pi) in two doubles
-    const double f = (double)__ldcg(A.inv_freq + i);
-    const double hi = f * kInv2Pi;
-    const double lo = fma(f, kInv2Pi, -hi) + f * kInv2PiLow;
-    const uint64_t per = (uint64_t)((hi - floor(hi)) * 18446744073709551616.0) +
-                         (uint64_t)(int64_t)rint(lo * 18446744073709551616.0);
-    const uint64_t frac = p * per;
+    const uint64_t frac = p * turns_of(__ldcg(A.inv_freq + i));
     float s, c;
     sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
     constexpr int kN = kF32 ? 4 : 8;
@@ -244,6 +250,161 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_c
     for (int j = 0; j < kRopeBatch; ++j)
       if (i0 + j * kRopeThreads < total) finish(U[j], x[j], y[j]);
   }
+}
+
+constexpr int kRbThreads = 128;
+constexpr int kRbStages = 3;
+constexpr int kRbItem = 16 * 1024;    // most bytes of an item, unless a row is longer
+constexpr int kRbPairs = kMaxHalf / kRbThreads;
+
+struct RopeBulk {
+  int rows, parts;       // rows of an item, items of a token
+  uint32_t mr;           // for i / ru
+  int items;
+  int stage;             // bytes of a stage
+};
+
+template <bool kF32, bool kHalves>
+__global__ void __launch_bounds__(kRbThreads)
+rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 cs[2][kMaxHalf];
+  __shared__ uint64_t full[kRbStages];
+  constexpr int kN = kF32 ? 4 : 8;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const uint32_t base = smem_u32(smem);
+  const int row_bytes = A.n16 * 16, R = A.Hq + A.Hk + A.Hv;
+  griddep_launch_dependents();   // the next call's first kernel may start its launch
+  if (tid == 0) {
+    for (int i = 0; i < kRbStages; ++i) mbar_init(smem_u32(full + i), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  griddep_wait();                // launched chained: the preceding kernel completed
+
+  // rows [r0, r1) of an item's token, by whose they are
+  auto load = [&](int item, int stage) {   // thread 0
+    const int64_t t = item / B.parts;
+    const int r0 = (item - (int)t * B.parts) * B.rows, r1 = min(r0 + B.rows, R);
+    const uint32_t bar = smem_u32(full + stage), dst = base + stage * B.stage;
+    mbar_arrive_expect_tx(bar, (r1 - r0) * row_bytes);
+    auto part = [&](const uint4* src, int64_t stride, int lo, int hi) {
+      const int a = max(r0, lo), b = min(r1, hi);
+      if (a < b)
+        bulk_load(dst + (a - r0) * row_bytes, src + t * stride + (int64_t)(a - lo) * A.n16,
+                  (b - a) * row_bytes, bar);
+    };
+    part(A.q, A.q_stride, 0, A.Hq);
+    part(A.k, A.k_stride, A.Hq, A.Hq + A.Hk);
+    part(A.v, A.v_stride, A.Hq + A.Hk, R);
+  };
+  if (tid == 0)
+    for (int k = 0; k < kRbStages - 1; ++k) {
+      const int64_t item = blockIdx.x + (int64_t)k * gridDim.x;
+      if (item < B.items) load((int)item, k);
+    }
+  // this thread's pairs: turns per position as a 64-bit fraction
+  uint64_t per[kRbPairs];
+  int ax[kRbPairs];
+#pragma unroll
+  for (int j = 0; j < kRbPairs; ++j) {
+    const int i = tid + j * kRbThreads;
+    per[j] = 0;
+    ax[j] = 0;
+    if (i >= A.half) continue;
+    per[j] = turns_of(__ldcg(A.inv_freq + i));
+    ax[j] = A.axis ? __ldcg(A.axis + i) : 0;
+    if (ax[j] < 0 || ax[j] >= A.axes) {
+      if (blockIdx.x == 0) count_error(A.err);
+      ax[j] = 0;
+    }
+  }
+  auto position = [&](int item, int j) -> uint64_t {
+    return tid + j * kRbThreads < A.half && item < B.items
+               ? (uint64_t)__ldcg(A.pos + (int64_t)ax[j] * A.T + item / B.parts)
+               : 0ull;
+  };
+  uint64_t pos[kRbPairs];
+#pragma unroll
+  for (int j = 0; j < kRbPairs; ++j) pos[j] = position(blockIdx.x, j);
+
+  int64_t dead = 0;
+  uint32_t k = 0;
+  for (int64_t it = blockIdx.x; it < B.items; it += gridDim.x, ++k) {
+    const int item = (int)it, stage = k % kRbStages;
+    const int64_t t = item / B.parts;
+    const int r0 = (item - (int)t * B.parts) * B.rows, r1 = min(r0 + B.rows, R);
+    const int64_t nxt = it + gridDim.x;
+    const bool writes = r1 > A.Hq;            // keys or values among the rows
+    // the token's slot on rank `lane` (warp 0, which issues the stores)
+    int64_t slot = -1;
+    if (tid < 32 && writes && lane < A.dcp) slot = __ldcg(A.slot + (int64_t)lane * A.T + t);
+    float2* tab = cs[k & 1];
+#pragma unroll
+    for (int j = 0; j < kRbPairs; ++j) {
+      const int i = tid + j * kRbThreads;
+      if (j * kRbThreads < A.half && i < A.half) {
+        const uint64_t frac = pos[j] * per[j];
+        float s, c;
+        sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
+        tab[(i % kN) * A.ru + i / kN] = make_float2(c * A.scaling, s * A.scaling);
+      }
+      pos[j] = position(nxt < B.items ? (int)nxt : B.items, j);
+    }
+    if (!dead && !mbar_wait(smem_u32(full + stage), (k / kRbStages) & 1)) dead = 1;
+    __syncthreads();
+    uint4* rows = reinterpret_cast<uint4*>(smem + stage * B.stage);
+    const int turn = max(min(r1, A.Hq + A.Hk) - r0, 0) * A.ru;
+    for (int i = tid; i < turn; i += kRbThreads) {
+      const int row = fast_div(i, B.mr, A.ru), u = i - row * A.ru;
+      uint4* p = rows + row * A.n16 + A.off16 + (kHalves ? u : 2 * u);
+      uint4* q = p + (kHalves ? A.ru : 1);
+      uint4 x = *p, y = *q;
+      rotate_unit<kF32, kHalves>(x, y, u, A.ru, tab);
+      *p = x;
+      *q = y;
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid < 32) {
+      const uint32_t src = base + stage * B.stage;
+      if (!__any_sync(0xffffffffu, dead != 0)) {
+        if (lane == 0) {
+          const int b = min(r1, A.Hq);
+          if (r0 < b)
+            bulk_store(A.q_out + (t * A.Hq + r0) * A.n16, src, (b - r0) * row_bytes);
+          const int c0 = max(r0, A.Hq), c1 = min(r1, A.Hq + A.Hk);
+          if (A.k_out && c0 < c1)
+            bulk_store(A.k_out + (t * A.Hk + c0 - A.Hq) * A.n16, src + (c0 - r0) * row_bytes,
+                       (c1 - c0) * row_bytes);
+        }
+        if (writes) {
+          const bool ok = slot >= 0 && slot < A.num_slots;
+          if (!ok && slot != -1 && r0 <= A.Hq) count_error(A.err);
+          uint32_t m = __ballot_sync(0xffffffffu, ok);
+          while (m) {
+            const int r = __ffs(m) - 1;
+            m &= m - 1;
+            const int64_t s = __shfl_sync(0xffffffffu, slot, r), blk = s / A.bs;
+            for (int row = max(r0, A.Hq) + lane; row < r1; row += 32) {
+              const bool val = row >= A.Hq + A.Hk;
+              const int h = row - A.Hq - (val ? A.Hk : 0);
+              bulk_store((uint4*)(val ? A.vp.ptr[r] : A.kp.ptr[r]) +
+                             ((blk * A.Hk + h) * A.bs + (s - blk * A.bs)) * A.n16,
+                         src + (row - r0) * row_bytes, row_bytes);
+            }
+          }
+        }
+      }
+      bulk_commit();
+      bulk_wait_read<1>();     // the stage before this one has been read
+      __syncwarp();
+      const int64_t ahead = it + (int64_t)(kRbStages - 1) * gridDim.x;
+      if (lane == 0 && ahead < B.items) load((int)ahead, (k + kRbStages - 1) % kRbStages);
+    }
+  }
+  if (tid < 32) bulk_wait_read<0>();   // shared memory is left only when it has been read
+  if (dead && tid == 0 && A.err) atomicAdd(A.err, 1 << 20);
 }
 
 static uint32_t div_magic(int d) {
@@ -264,8 +425,41 @@ static int launch_rope(RopeArgs& A, int rot, int rot_at, int d, int es, bool int
   A.mq = div_magic(A.uq);
   A.mk = div_magic(A.uk);
   A.mv = div_magic(A.uv);
-  const unsigned grid = (unsigned)A.T;
   cudaError_t e;
+  const int R = A.Hq + A.Hk + A.Hv, row_bytes = A.n16 * 16;
+  RopeBulk B;
+  B.parts = 1;
+  if (row_bytes * R > kRbItem) {
+    B.rows = kRbItem / row_bytes > 0 ? kRbItem / row_bytes : 1;
+    B.parts = (R + B.rows - 1) / B.rows;
+  }
+  B.rows = (R + B.parts - 1) / B.parts;
+  B.parts = (R + B.rows - 1) / B.rows;
+  B.mr = div_magic(A.ru);
+  B.stage = (B.rows * row_bytes + 127) / 128 * 128;
+  const bool in_place = A.Hq > 0 && A.uq != A.uk;
+  if (!in_place && A.T * B.parts < (int64_t(1) << 31)) {
+    B.items = (int)(A.T * B.parts);
+    const int smem = kRbStages * B.stage;
+    const int per_sm = 200 * 1024 / (smem + 9 * 1024) > 1 ? 200 * 1024 / (smem + 9 * 1024) : 1;
+    const int64_t most = (int64_t)per_sm * num_sms();
+    const unsigned grid = (unsigned)(B.items < most ? B.items : most);
+    auto go = [&](auto kernel) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+          cudaSuccess) {
+        cudaGetLastError();
+        return cudaErrorInvalidValue;
+      }
+      return launch_chained(kernel, grid, kRbThreads, smem, s, A, B);
+    };
+    if (es == 4)
+      e = interleaved ? go(rope_bulk_kernel<true, false>) : go(rope_bulk_kernel<true, true>);
+    else
+      e = interleaved ? go(rope_bulk_kernel<false, false>) : go(rope_bulk_kernel<false, true>);
+    if (e != cudaSuccess) return launch_status_report(e);
+    return launch_status();
+  }
+  const unsigned grid = (unsigned)A.T;
   if (es == 4)
     e = interleaved ? launch_chained(rope_write_kernel<true, false>, grid, kRopeThreads, 0, s, A)
                     : launch_chained(rope_write_kernel<true, true>, grid, kRopeThreads, 0, s, A);
