@@ -425,12 +425,7 @@ static int launch_pages(const dcp_layout_t& L, const dcp_pages_t& p, const int32
   A.err = err;
   if (!ws || ws_bytes < pages_ws_bytes(N)) return DCP_EWORKSPACE;
   const size_t smem = pages_smem(N, A.hash);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(pages_kernel<kFork>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return DCP_ECUDA;
-  }
+  if (!allow_smem<pages_kernel<kFork>>()) return DCP_ECUDA;
   cudaError_t e = launch_chained(pages_kernel<kFork>, (unsigned)(tables * kPgCluster), kPgThreads,
                                  smem, s, A);
   if (e != cudaSuccess) return launch_status_report(e);

@@ -88,6 +88,25 @@ cudaError_t launch_chained(void (*kernel)(Exp...), unsigned grid, unsigned block
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Act&&>(args)...);
 }
 
+// Allow a kernel all the shared memory it can have, once per device; false if
+// that fails.
+template <auto Kernel>
+inline bool allow_smem() {
+  static bool done[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64 && done[dev]) return true;
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, Kernel) != cudaSuccess ||
+      cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           227 * 1024 - (int)a.sharedSizeBytes) != cudaSuccess) {
+    cudaGetLastError();   // not sticky: leave no error for the next call to misread
+    return false;
+  }
+  if (dev >= 0 && dev < 64) done[dev] = true;
+  return true;
+}
+
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }

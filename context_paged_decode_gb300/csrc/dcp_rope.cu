@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_c
 }
 
 constexpr int kRbThreads = 128;
-constexpr int kRbStages = 3;
+constexpr int kRbStages = 2;
+constexpr int kRbPerSm = 8;           // CTAs of an SM, as far as shared memory goes
 constexpr int kRbItem = 16 * 1024;    // most bytes of an item, unless a row is longer
 constexpr int kRbPairs = kMaxHalf / kRbThreads;
 
@@ -268,12 +269,12 @@ template <bool kF32, bool kHalves>
 __global__ void __launch_bounds__(kRbThreads)
 rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 cs[2][kMaxHalf];
   __shared__ uint64_t full[kRbStages];
   constexpr int kN = kF32 ? 4 : 8;
   const int tid = threadIdx.x, lane = tid & 31;
   const uint32_t base = smem_u32(smem);
   const int row_bytes = A.n16 * 16, R = A.Hq + A.Hk + A.Hv;
+  float2* const cs = reinterpret_cast<float2*>(smem + kRbStages * B.stage);   // [2][half]
   griddep_launch_dependents();   // the next call's first kernel may start its launch
   if (tid == 0) {
     for (int i = 0; i < kRbStages; ++i) mbar_init(smem_u32(full + i), 1);
@@ -339,7 +340,7 @@ rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
     // the token's slot on rank `lane` (warp 0, which issues the stores)
     int64_t slot = -1;
     if (tid < 32 && writes && lane < A.dcp) slot = __ldcg(A.slot + (int64_t)lane * A.T + t);
-    float2* tab = cs[k & 1];
+    float2* tab = cs + (k & 1) * A.half;
 #pragma unroll
     for (int j = 0; j < kRbPairs; ++j) {
       const int i = tid + j * kRbThreads;
@@ -411,6 +412,13 @@ static uint32_t div_magic(int d) {
   return d <= 1 ? 0u : (uint32_t)(((uint64_t(1) << 32) + (uint64_t)d - 1) / (uint64_t)d);
 }
 
+template <bool kF32, bool kHalves>
+static cudaError_t launch_bulk(const RopeArgs& A, const RopeBulk& B, unsigned grid, int smem,
+                               cudaStream_t s) {
+  if (!allow_smem<rope_bulk_kernel<kF32, kHalves>>()) return cudaErrorInvalidValue;
+  return launch_chained(rope_bulk_kernel<kF32, kHalves>, grid, kRbThreads, smem, s, A, B);
+}
+
 static int launch_rope(RopeArgs& A, int rot, int rot_at, int d, int es, bool interleaved,
                        cudaStream_t s) {
   A.n16 = d * es / 16;
@@ -440,22 +448,17 @@ static int launch_rope(RopeArgs& A, int rot, int rot_at, int d, int es, bool int
   const bool in_place = A.Hq > 0 && A.uq != A.uk;
   if (!in_place && A.T * B.parts < (int64_t(1) << 31)) {
     B.items = (int)(A.T * B.parts);
-    const int smem = kRbStages * B.stage;
-    const int per_sm = 200 * 1024 / (smem + 9 * 1024) > 1 ? 200 * 1024 / (smem + 9 * 1024) : 1;
+    const int smem = kRbStages * B.stage + 2 * A.half * (int)sizeof(float2);
+    const int fit = 224 * 1024 / (smem + 1024 + 64);
+    const int per_sm = fit < 1 ? 1 : (fit < kRbPerSm ? fit : kRbPerSm);
     const int64_t most = (int64_t)per_sm * num_sms();
     const unsigned grid = (unsigned)(B.items < most ? B.items : most);
-    auto go = [&](auto kernel) {
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-          cudaSuccess) {
-        cudaGetLastError();
-        return cudaErrorInvalidValue;
-      }
-      return launch_chained(kernel, grid, kRbThreads, smem, s, A, B);
-    };
     if (es == 4)
-      e = interleaved ? go(rope_bulk_kernel<true, false>) : go(rope_bulk_kernel<true, true>);
+      e = interleaved ? launch_bulk<true, false>(A, B, grid, smem, s)
+                      : launch_bulk<true, true>(A, B, grid, smem, s);
     else
-      e = interleaved ? go(rope_bulk_kernel<false, false>) : go(rope_bulk_kernel<false, true>);
+      e = interleaved ? launch_bulk<false, false>(A, B, grid, smem, s)
+                      : launch_bulk<false, true>(A, B, grid, smem, s);
     if (e != cudaSuccess) return launch_status_report(e);
     return launch_status();
   }

@@ -360,21 +360,20 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
   }
 }
 
+template <typename T, int DPL>
+static int launch_tree_cores(const TreeArgs& A, int smem, cudaStream_t s) {
+  if (!allow_smem<tree_generic_kernel<T, DPL>>()) return DCP_ECUDA;
+  const cudaError_t e = launch_chained(tree_generic_kernel<T, DPL>, (unsigned)A.parts,
+                                       kTgWarps * 32, smem, s, A);
+  return e == cudaSuccess ? launch_status() : launch_status_report(e);
+}
+
 template <typename T>
 static int launch_tree_generic(const TreeArgs& A, cudaStream_t s) {
   const int smem = (int)sizeof(float) * (kTgRows * A.d + kTgTile * (A.d + kTgPad) + kTgTile * A.d);
-  auto go = [&](auto kernel) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-        cudaSuccess) {
-      cudaGetLastError();
-      return (int)DCP_ECUDA;
-    }
-    const cudaError_t e = launch_chained(kernel, (unsigned)A.parts, kTgWarps * 32, smem, s, A);
-    return e == cudaSuccess ? launch_status() : launch_status_report(e);
-  };
-  if (A.d <= 64) return go(tree_generic_kernel<T, 2>);
-  if (A.d <= 128) return go(tree_generic_kernel<T, 4>);
-  return go(tree_generic_kernel<T, 8>);
+  if (A.d <= 64) return launch_tree_cores<T, 2>(A, smem, s);
+  if (A.d <= 128) return launch_tree_cores<T, 4>(A, smem, s);
+  return launch_tree_cores<T, 8>(A, smem, s);
 }
 
 // ---------------------------------------------------------------------------

@@ -746,11 +746,7 @@ template <int D, bool kTwo>
 static int go(const TreeTcArgs& X, cudaStream_t s) {
   const int smem = TreeTc<D, kTwo>::kSmem;
   static_assert(TreeTc<D, kTwo>::kSmem <= 227 * 1024, "shared memory");
-  if (cudaFuncSetAttribute(tree_tc_kernel<D, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           smem) != cudaSuccess) {
-    cudaGetLastError();
-    return DCP_ECUDA;
-  }
+  if (!allow_smem<tree_tc_kernel<D, kTwo>>()) return DCP_ECUDA;
   const cudaError_t e = launch_chained(tree_tc_kernel<D, kTwo>, (unsigned)X.t.parts, kTtThreads,
                                        smem, s, X);
   return e == cudaSuccess ? launch_status() : launch_status_report(e);
