@@ -23,19 +23,22 @@ namespace dcp {
 constexpr int kTreePlanThreads = 256;
 
 // One CTA: checks the requests, counts each entry's tiles and units, sums them
-// up, and finds each run's first entry.
+// up, and finds each run's first entry.  A unit counts as up to A.extra tiles
+// more than it has, but no more than a run would have: small calls spread their
+// tiles over all CTAs.
 __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __grid_constant__ TreeArgs A) {
-  __shared__ int64_t sh_t[kTreePlanThreads / 32];
+  __shared__ int64_t sh_t[kTreePlanThreads / 32], sh_u[kTreePlanThreads / 32];
   __shared__ int64_t s_end[kTreePlanThreads];   // tiles up to each entry of the block
   griddep_launch_dependents();   // the next call's first kernel may start its launch
   griddep_wait();                // launched chained: the preceding kernel completed
   const int E = A.per_rank ? A.B * A.L.dcp : A.B;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  int64_t run_t = 0;
-  // two rounds over the entries: the number of tiles decides where runs begin
-  for (int round = 0; round < (E > kTreePlanThreads ? 2 : 1); ++round) {
-    const int64_t total = run_t;
-    run_t = 0;
+  const bool single = E <= kTreePlanThreads;
+  int64_t tiles = 0, units = 0, extra = 0, total = 0;
+  // more entries than threads: a first round only for the sums
+  for (int round = single ? 1 : 0; round < 2; ++round) {
+    const int64_t all_t = tiles, all_u = units;
+    tiles = units = 0;
     for (int e0 = 0; e0 < E; e0 += kTreePlanThreads) {
       const int e = e0 + tid;
       TreeEntry n;
@@ -47,7 +50,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __gri
         int T = q1 - q0;
         if (q0 < 0 || q1 < q0 || q1 > A.N || T > A.max_tree || ctx < 0 ||
             ctx + T > (int64_t)A.max_vb * A.L.bs * A.L.dcp) {
-          if (r == 0 && round == 0) count_error(A.err);
+          if (r == 0 && round == 1) count_error(A.err);
           T = 0;
         }
         if (T > 0) {
@@ -60,48 +63,63 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __gri
           n.q0 = q0;
         }
       }
-      const int64_t tiles = n.units ? (int64_t)n.units * (n.per + A.extra) : 0;
-      int64_t t = tiles;
+      int64_t t = (int64_t)n.units * n.per, u = n.units;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t pt = __shfl_up_sync(0xffffffffu, t, o);
-        if (lane >= o) t += pt;
-      }
-      __syncthreads();
-      if (lane == 31) sh_t[w] = t;
-      __syncthreads();
-      const int64_t block0 = run_t;
-      int64_t before = run_t;
-      for (int i = 0; i < kTreePlanThreads / 32; ++i) {
-        if (i < w) before += sh_t[i];
-        run_t += sh_t[i];
-      }
-      n.tile0 = before + t - tiles;
-      if (e < E && round == 0) A.entry[e] = n;
-      if (E <= kTreePlanThreads || round == 1) {
-        // runs that begin in this block's entries
-        s_end[tid] = n.tile0 + tiles;
-        __syncthreads();
-        const int64_t all = E <= kTreePlanThreads ? run_t : total;
-        const int parts = (int)(all < A.parts ? all : A.parts);
-        for (int k = tid; k < parts; k += kTreePlanThreads) {
-          const int64_t at = tree_run(all, parts, k);
-          if (at < block0 || at >= run_t) continue;
-          int lo = 0, hi = kTreePlanThreads - 1;   // first entry that ends behind `at`
-          while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (s_end[mid] > at) hi = mid; else lo = mid + 1;
-          }
-          A.run_entry[k] = e0 + lo;
+        const int64_t pu = __shfl_up_sync(0xffffffffu, u, o);
+        if (lane >= o) {
+          t += pt;
+          u += pu;
         }
-        __syncthreads();
+      }
+      __syncthreads();
+      if (lane == 31) {
+        sh_t[w] = t;
+        sh_u[w] = u;
+      }
+      __syncthreads();
+      const int64_t block_t = tiles, block_u = units;
+      t += tiles;
+      u += units;   // with this entry's own
+      for (int i = 0; i < kTreePlanThreads / 32; ++i) {
+        if (i < w) {
+          t += sh_t[i];
+          u += sh_u[i];
+        }
+        tiles += sh_t[i];
+        units += sh_u[i];
+      }
+      if (round == 0) continue;
+      const int64_t sum_t = single ? tiles : all_t, sum_u = single ? units : all_u;
+      extra = sum_t / A.parts;
+      if (extra > A.extra) extra = A.extra;
+      total = sum_t + extra * sum_u;
+      const int64_t end = t + extra * u;
+      n.tile0 = end - n.units * (n.per + extra);
+      if (e < E) A.entry[e] = n;
+      // the runs that begin in this block's entries
+      s_end[tid] = end;
+      __syncthreads();
+      const int64_t first = block_t + extra * block_u, last = tiles + extra * units;
+      const int parts = (int)(total < A.parts ? total : A.parts);
+      for (int k = tid; k < parts; k += kTreePlanThreads) {
+        const int64_t at = tree_run(total, parts, k);
+        if (at < first || at >= last) continue;
+        int lo = 0, hi = kTreePlanThreads - 1;   // first entry that ends behind `at`
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (s_end[mid] > at) hi = mid; else lo = mid + 1;
+        }
+        A.run_entry[k] = e0 + lo;
       }
     }
   }
   if (tid == 0) {
-    A.hdr[0] = run_t < A.parts ? (int)run_t : A.parts;
+    A.hdr[0] = total < A.parts ? (int)total : A.parts;
     A.hdr[1] = 0;
-    *reinterpret_cast<int64_t*>(A.hdr + 2) = run_t;
+    *reinterpret_cast<int64_t*>(A.hdr + 2) = total;
+    A.hdr[4] = (int)extra;
   }
 }
 
@@ -134,8 +152,7 @@ __device__ __forceinline__ float tree_close(float m, float l, bool has_sink, flo
 // CUDA-core kernel
 // ---------------------------------------------------------------------------
 
-constexpr int kTgRows = 32;     // query rows of a CTA, four per warp
-constexpr int kTgTile = 32;     // tokens of a tile, one per lane
+constexpr int kTgTile = 64;     // tokens of a tile, two per lane
 constexpr int kTgWarps = 8;
 constexpr int kTgPad = 4;       // floats: a lane's 16-byte reads of its own K row hit 32 banks
 
@@ -164,51 +181,60 @@ struct Chunk<__nv_bfloat16> {
   }
 };
 
-// Scores on the lanes (lane = token of the tile, K row from shared memory),
-// output on the lanes as well (lane owns entries lane + 32 i); a warp carries
-// four query rows so that each K and V value read serves four products.
-// Masked tokens are skipped, not multiplied by zero: their values may be
-// anything.
-template <typename T, int DPL>
+// Scores on the lanes (a lane has tokens lane and lane + 32 of the tile, whose
+// K rows it reads from shared memory), output on the lanes as well (entries
+// lane + 32 i), the probabilities between them through shared memory.  A warp
+// carries RW query rows, so each K and V value read serves RW products.  Eight
+// rows would halve the shared-memory reads, but leave registers for one CTA an
+// SM, whose eight warps cannot hide each other's latency (4 requests x 16
+// nodes, d 128, 8192 tokens: 140 us against 69).  Masked tokens have probability zero, and values that nobody sees are
+// zeros in shared memory; if a drafted node's value is not finite, the tile's
+// products skip unseen nodes one by one.
+template <typename T, int DPL, int RW>
 __global__ void __launch_bounds__(kTgWarps * 32)
 tree_generic_kernel(const __grid_constant__ TreeArgs A) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float smf[];
   __shared__ int64_t s_row[kTgTile];   // K/V row of a token, -1: not there
   __shared__ int s_code[kTgTile];      // node, 64: seen by all, 255: by none
-  const int d = A.d, ks = d + kTgPad;
-  float* sq = sm;                      // [rows][d]
-  float* sk = sq + kTgRows * d;        // [tile][d + pad]
-  float* sv = sk + kTgTile * ks;       // [tile][d]
+  __shared__ int s_odd;                // a node's value is not finite
+  constexpr int kRows = kTgWarps * RW;
+  const int d = A.d, ks = d + kTgPad, d4 = d >> 2;
+  float* sq = smf;                     // [rows][d]
+  float* sv = sq + kRows * d;          // [tile][d]
+  float* sk = sv + kTgTile * d;        // [tile][d + pad], then the probabilities
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float* pw = sk + warp * kTgTile * RW;   // [warp][tile][RW]
   for (int run = blockIdx.x; run < A.parts; run += gridDim.x) {
     TreeWalk walk = tree_walk(A, run);
     TreePiece p;
     while (tree_next(A, walk, p)) {
-      const int T_b = p.T;
       const int ctx = p.ctx;
-      const TreeLen len(ctx + T_b, A.L);
-      const int row0 = p.rb * A.rows, nrows = min(A.rows, T_b * A.G - row0);
+      const TreeLen len(ctx + p.T, A.L);
+      const int row0 = p.rb * A.rows, nrows = min(A.rows, p.T * A.G - row0);
       __syncthreads();                 // the last piece is done with sq
-      for (int i = tid; i < kTgRows * d; i += kTgWarps * 32) {
-        const int row = i / d, c = i - row * d;
-        float x = 0.f;
-        if (row < nrows) {
-          const int rr = row0 + row;
-          const int64_t tok = p.q0 + rr / A.G;
-          x = (float)__ldcg((const T*)A.q + (tok * A.Hq + p.g * A.G + rr % A.G) * d + c);
-        }
-        sq[i] = x;
-      }
-      uint64_t mask[4];
-      float m[4], l[4], o[4][DPL];
+      constexpr int CN = Chunk<T>::n;
+      const int cpr = d / CN;          // 16-byte pieces of a row
+      for (int i = tid; i < nrows * cpr; i += kTgWarps * 32) {
+        const int row = i / cpr, c = (i - row * cpr) * CN, rr = row0 + row;
+        const int64_t tok = p.q0 + rr / A.G;
+        float f[CN];
+        Chunk<T>::to(__ldcg((const uint4*)((const T*)A.q +
+                                           (tok * A.Hq + p.g * A.G + rr % A.G) * d + c)),
+                     f);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = warp * 4 + x;
-        mask[x] = row < nrows
-                      ? __ldcg((const unsigned long long*)A.mask + p.q0 + (row0 + row) / A.G)
-                      : 0ull;
+        for (int x = 0; x < CN; x += 4)
+          *(float4*)(sq + row * d + c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
+      }
+      uint64_t mask[RW];
+      float m[RW], l[RW], o[RW][DPL];
+#pragma unroll
+      for (int x = 0; x < RW; ++x) {
+        const int row = warp * RW + x;
+        mask[x] = row < nrows ? __ldcg((const unsigned long long*)A.mask + p.q0 +
+                                       (row0 + row) / A.G)
+                              : 0ull;
         m[x] = -INFINITY;
         l[x] = 0.f;
 #pragma unroll
@@ -232,7 +258,8 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
           if (pos < n_r) {
             const int j = pos / A.L.bs;
             const int64_t phys =
-                j < A.max_vb ? (int64_t)__ldcg(A.bt + r * A.stride + (int64_t)p.b * A.max_vb + j) : -1;
+                j < A.max_vb ? (int64_t)__ldcg(A.bt + r * A.stride + (int64_t)p.b * A.max_vb + j)
+                             : -1;
             if (phys >= 0 && phys < A.nb) {
               row = (phys * A.Hkv + p.g) * A.L.bs + (pos - j * A.L.bs);
               const int x = tree_global(pos, r, A.L) - ctx;
@@ -243,83 +270,114 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
           }
           s_row[tid] = row;
           s_code[tid] = code;
+          if (tid == 0) s_odd = 0;
         }
         __syncthreads();
-        constexpr int CN = Chunk<T>::n;
-        const int cpr = d / CN;
         const T* kp = (const T*)A.k.ptr[r];
         const T* vp = (const T*)A.v.ptr[r];
-        for (int i = tid; i < kTgTile * cpr; i += kTgWarps * 32) {
-          const int j = i / cpr, c = (i - j * cpr) * CN;
-          const int64_t row = s_row[j];
-          float f[CN], g[CN];
-          if (row >= 0) {
-            Chunk<T>::to(__ldcg((const uint4*)(kp + row * d + c)), f);
-            Chunk<T>::to(__ldcg((const uint4*)(vp + row * d + c)), g);
-          } else {
+        for (int i0 = tid; i0 < kTgTile * cpr; i0 += 4 * kTgWarps * 32) {
+          uint4 a[4], b[4];
 #pragma unroll
-            for (int x = 0; x < CN; ++x) f[x] = g[x] = 0.f;
+          for (int y = 0; y < 4; ++y) {
+            const int i = i0 + y * kTgWarps * 32;
+            a[y] = b[y] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < kTgTile * cpr) {
+              const int j = i / cpr, c = (i - j * cpr) * CN;
+              const int64_t row = s_row[j];
+              if (row >= 0) {
+                a[y] = __ldcg((const uint4*)(kp + row * d + c));
+                b[y] = __ldcg((const uint4*)(vp + row * d + c));
+              }
+            }
           }
 #pragma unroll
-          for (int x = 0; x < CN; x += 4) {
-            *(float4*)(sk + j * ks + c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
-            *(float4*)(sv + j * d + c + x) = make_float4(g[x], g[x + 1], g[x + 2], g[x + 3]);
+          for (int y = 0; y < 4; ++y) {
+            const int i = i0 + y * kTgWarps * 32;
+            if (i >= kTgTile * cpr) continue;
+            const int j = i / cpr, c = (i - j * cpr) * CN;
+            float f[CN], g[CN];
+            Chunk<T>::to(a[y], f);
+            Chunk<T>::to(b[y], g);
+            if (s_code[j] < 64) {
+#pragma unroll
+              for (int x = 0; x < CN; ++x)
+                if (!isfinite(g[x])) s_odd = 1;
+            }
+#pragma unroll
+            for (int x = 0; x < CN; x += 4) {
+              *(float4*)(sk + j * ks + c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
+              *(float4*)(sv + j * d + c + x) = make_float4(g[x], g[x + 1], g[x + 2], g[x + 3]);
+            }
           }
         }
         __syncthreads();
-        if (warp * 4 >= nrows) continue;   // no rows here (uniform in the warp)
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        const float4* kr = (const float4*)(sk + lane * ks);
-        const float4* qr = (const float4*)(sq + warp * 4 * d);
-        const int d4 = d >> 2;
-#pragma unroll 4
-        for (int c = 0; c < d4; ++c) {
-          const float4 a = kr[c];
+        const bool idle = warp * RW >= nrows;   // no rows here (uniform in the warp)
+        float s[2][RW];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < RW; ++x) s[0][x] = s[1][x] = 0.f;
+        const float4* k0 = (const float4*)(sk + lane * ks);
+        const float4* k1 = (const float4*)(sk + (lane + 32) * ks);
+        const float4* qr = (const float4*)(sq + warp * RW * d);
+#pragma unroll 2
+        for (int c = 0; c < (idle ? 0 : d4); ++c) {
+          const float4 a = k0[c], e = k1[c];
+#pragma unroll
+          for (int x = 0; x < RW; ++x) {
             const float4 b = qr[x * d4 + c];
-            s[x] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s[x]))));
+            s[0][x] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s[0][x]))));
+            s[1][x] = fmaf(e.x, b.x, fmaf(e.y, b.y, fmaf(e.z, b.z, fmaf(e.w, b.w, s[1][x]))));
           }
         }
-        const int code = s_code[lane];
-        float pr[4];
-        uint32_t vis[4];
-        bool all = true;
+        __syncthreads();               // the keys are done with
+        if (idle) continue;
+        const int code0 = s_code[lane], code1 = s_code[lane + 32];
+        uint32_t vis[2][RW];
+        float pr[2][RW];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const bool on = code == 64 || (code < 64 && ((mask[x] >> code) & 1));
-          vis[x] = __ballot_sync(0xffffffffu, on);
-          all = all && vis[x] == 0xffffffffu;
-          const float sc = on ? s[x] * A.sl2 : -INFINITY;
-          const float mn = fmaxf(m[x], warp_max(sc));
+        for (int x = 0; x < RW; ++x) {
+          const bool on0 = code0 == 64 || (code0 < 64 && ((mask[x] >> code0) & 1));
+          const bool on1 = code1 == 64 || (code1 < 64 && ((mask[x] >> code1) & 1));
+          vis[0][x] = __ballot_sync(0xffffffffu, on0);
+          vis[1][x] = __ballot_sync(0xffffffffu, on1);
+          const float s0 = on0 ? s[0][x] * A.sl2 : -INFINITY;
+          const float s1 = on1 ? s[1][x] * A.sl2 : -INFINITY;
+          const float mn = fmaxf(m[x], warp_max(fmaxf(s0, s1)));
           const float mb = mn == -INFINITY ? 0.f : mn;
           const float al = exp2f(m[x] - mb);
-          pr[x] = on ? exp2f(sc - mb) : 0.f;
-          l[x] = l[x] * al + pr[x];      // this lane's tokens
+          pr[0][x] = on0 ? exp2f(s0 - mb) : 0.f;
+          pr[1][x] = on1 ? exp2f(s1 - mb) : 0.f;
+          l[x] = l[x] * al + (pr[0][x] + pr[1][x]);      // this lane's tokens
           m[x] = mn;
 #pragma unroll
           for (int i = 0; i < DPL; ++i) o[x][i] *= al;
         }
-        if (all) {
+#pragma unroll
+        for (int x = 0; x < RW; ++x) {
+          pw[lane * RW + x] = pr[0][x];
+          pw[(lane + 32) * RW + x] = pr[1][x];
+        }
+        __syncwarp();
+        if (!s_odd) {
 #pragma unroll 4
           for (int j = 0; j < kTgTile; ++j) {
-            float pj[4];
+            float pj[RW];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) pj[x] = __shfl_sync(0xffffffffu, pr[x], j);
+            for (int x = 0; x < RW; ++x) pj[x] = pw[j * RW + x];
 #pragma unroll
             for (int i = 0; i < DPL; ++i)
               if (i * 32 < d) {
                 const float v = sv[j * d + i * 32 + lane];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) o[x][i] = fmaf(pj[x], v, o[x][i]);
+                for (int x = 0; x < RW; ++x) o[x][i] = fmaf(pj[x], v, o[x][i]);
               }
           }
         } else {
+#pragma unroll 1
           for (int j = 0; j < kTgTile; ++j)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              if (!((vis[x] >> j) & 1)) continue;
-              const float pj = __shfl_sync(0xffffffffu, pr[x], j);
+            for (int x = 0; x < RW; ++x) {
+              if (!(((j < 32 ? vis[0][x] : vis[1][x]) >> (j & 31)) & 1)) continue;
+              const float pj = pw[j * RW + x];
 #pragma unroll
               for (int i = 0; i < DPL; ++i)
                 if (i * 32 < d) o[x][i] = fmaf(pj, sv[j * d + i * 32 + lane], o[x][i]);
@@ -327,8 +385,8 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
         }
       }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = warp * 4 + x;
+      for (int x = 0; x < RW; ++x) {
+        const int row = warp * RW + x;
         if (row >= nrows) continue;
         const float lt = warp_sum(l[x]);
         float lse2;
@@ -360,20 +418,28 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
   }
 }
 
-template <typename T, int DPL>
-static int launch_tree_cores(const TreeArgs& A, int smem, cudaStream_t s) {
-  if (!allow_smem<tree_generic_kernel<T, DPL>>()) return DCP_ECUDA;
-  const cudaError_t e = launch_chained(tree_generic_kernel<T, DPL>, (unsigned)A.parts,
+template <typename T, int DPL, int RW>
+static int launch_tree_cores(const TreeArgs& A, cudaStream_t s) {
+  constexpr int kRows = kTgWarps * RW;
+  const size_t keys = (size_t)kTgTile * (A.d + kTgPad), probs = (size_t)kTgTile * kRows;
+  const size_t smem = sizeof(float) * ((size_t)kRows * A.d + (size_t)kTgTile * A.d +
+                                       (keys > probs ? keys : probs));
+  if (!allow_smem<tree_generic_kernel<T, DPL, RW>>()) return DCP_ECUDA;
+  const cudaError_t e = launch_chained(tree_generic_kernel<T, DPL, RW>, (unsigned)A.parts,
                                        kTgWarps * 32, smem, s, A);
   return e == cudaSuccess ? launch_status() : launch_status_report(e);
 }
 
+template <typename T, int DPL>
+static int launch_tree_rows(const TreeArgs& A, cudaStream_t s) {
+  return A.rows <= 16 ? launch_tree_cores<T, DPL, 2>(A, s) : launch_tree_cores<T, DPL, 4>(A, s);
+}
+
 template <typename T>
 static int launch_tree_generic(const TreeArgs& A, cudaStream_t s) {
-  const int smem = (int)sizeof(float) * (kTgRows * A.d + kTgTile * (A.d + kTgPad) + kTgTile * A.d);
-  if (A.d <= 64) return launch_tree_cores<T, 2>(A, smem, s);
-  if (A.d <= 128) return launch_tree_cores<T, 4>(A, smem, s);
-  return launch_tree_cores<T, 8>(A, smem, s);
+  if (A.d <= 64) return launch_tree_rows<T, 2>(A, s);
+  if (A.d <= 128) return launch_tree_rows<T, 4>(A, s);
+  return launch_tree_rows<T, 8>(A, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -382,11 +448,13 @@ static int launch_tree_generic(const TreeArgs& A, cudaStream_t s) {
 
 // One warp per output row.  Rows whose unit lay in one run were written by its
 // CTA; rows of refused requests and outside every request stay as they were.
+template <int DPL>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs A) {
+  constexpr int kFly = 64 / DPL;         // parts whose values are in flight at once
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int parts = __ldcg(A.hdr);
+  const int parts = __ldcg(A.hdr), extra = __ldcg(A.hdr + 4);
   const int64_t total = __ldcg(reinterpret_cast<const int64_t*>(A.hdr + 2));
   // rows in the order (rank,) request, node, head
   const int64_t rows = (int64_t)A.B * A.max_tree * A.Hq * (A.per_rank ? A.L.dcp : 1);
@@ -408,7 +476,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     const int per = n.per;
     const int g = h / A.G, ur = j * A.G + h % A.G;   // row of the unit's request
     const int rb = ur / A.rows, rr = ur - rb * A.rows;
-    const int64_t t0 = n.tile0 + (int64_t)(g * (n.units / A.Hkv) + rb) * (per + A.extra);
+    const int64_t t0 = n.tile0 + (int64_t)(g * (n.units / A.Hkv) + rb) * (per + extra);
     const int k0 = tree_run_of(total, parts, t0), k1 = tree_run_of(total, parts, t0 + per - 1);
     if (k0 == k1) continue;
     const bool late = tree_run(total, parts, k0) != t0;   // run k0 began before this unit
@@ -421,37 +489,37 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
       M = fmaxf(M, warp_max(k + lane <= k1 ? __ldcg(A.part_lse + slot(k + lane)) : -INFINITY));
     const float mb = M == -INFINITY ? 0.f : M;
     float L = sunk ? exp2f(s2 - mb) : 0.f;
-    float acc[8];
+    float acc[DPL];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
     for (int k = k0; k <= k1; k += 32) {
       const float lse = k + lane <= k1 ? __ldcg(A.part_lse + slot(k + lane)) : -INFINITY;
       // a part that saw nothing does not count, whatever its values are
       const float mine = lse == -INFINITY ? 0.f : exp2f(lse - mb);
       L += warp_sum(mine);
       const int n = min(32, k1 - k + 1);
-      for (int j0 = 0; j0 < n; j0 += 8) {
-        float v[8][8];
+      for (int j0 = 0; j0 < n; j0 += kFly) {
+        float v[kFly][DPL];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < kFly; ++j)
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < DPL; ++i)
             v[j][i] = j0 + j < n && i * 32 < A.d
                           ? __ldcg(A.part_o + slot(k + j0 + j) * A.d + i * 32 + lane)
                           : 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kFly; ++j) {
           const float wgt = __shfl_sync(0xffffffffu, mine, (j0 + j) & 31);
           if (j0 + j < n && wgt != 0.f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = fmaf(wgt, v[j][i], acc[i]);
+            for (int i = 0; i < DPL; ++i) acc[i] = fmaf(wgt, v[j][i], acc[i]);
           }
         }
       }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < DPL; ++i)
       if (i * 32 < A.d) {
         if (A.out_dtype == DCP_F32)
           of[i * 32 + lane] = acc[i] * inv;
@@ -473,10 +541,17 @@ struct TreeShape {
   int rows, tile, parts, extra;
 };
 
-static TreeShape tree_shape(bool tc, int G, int max_tree) {
-  if (!tc) return TreeShape{kTgRows / G * G, kTgTile, 4 * num_sms(), 0};
+static TreeShape tree_shape(bool tc, int G, int max_tree, int ranks) {
+  if (!tc) {
+    // blocks of 16 rows where they hold a request's, else of 32
+    const int rows = max_tree * G <= 16 ? 16 : 32;
+    return TreeShape{rows / G * G, kTgTile, 2 * num_sms(), 0};
+  }
   const int nodes = 128 / G;
-  return TreeShape{(max_tree <= nodes ? 1 : 2) * nodes * G, 128, num_sms(), 2};
+  // what a unit costs beside its tiles: a start and an end, and at each rank's
+  // end a tile that is masked (32 requests x 16 nodes, 8 ranks: 488 us with 2 more, 467
+  // with 10)
+  return TreeShape{(max_tree <= nodes ? 1 : 2) * nodes * G, 128, num_sms(), 2 + ranks};
 }
 
 static size_t tree_carve(TreeArgs* A, void* ws, int B, int dcp, int parts, int rows, int d) {
@@ -529,7 +604,7 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
   for (int r = 0; r < layout.dcp_size; ++r)
     if (((uintptr_t)kv.k.ptr[r] & 15) || ((uintptr_t)kv.v.ptr[r] & 15)) return DCP_EUNSUPPORTED;
   const bool tc = tree_tc_supported(layout, d, dtype, kv, Hkv);
-  const TreeShape S = tree_shape(tc, Hq / Hkv, max_tree);
+  const TreeShape S = tree_shape(tc, Hq / Hkv, max_tree, per_rank ? 1 : layout.dcp_size);
   TreeArgs A;
   A.q = q;
   A.q_start = q_start;
@@ -570,7 +645,10 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
   if (rc != DCP_OK) return rc;
   const int64_t rows = (int64_t)B * max_tree * Hq * (per_rank ? layout.dcp_size : 1);
   const int64_t blocks = (rows + 7) / 8, most = (int64_t)8 * num_sms();
-  e = launch_chained(tree_merge_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, s, A);
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+  e = d <= 64    ? launch_chained(tree_merge_kernel<2>, grid, 256, 0, s, A)
+      : d <= 128 ? launch_chained(tree_merge_kernel<4>, grid, 256, 0, s, A)
+                 : launch_chained(tree_merge_kernel<8>, grid, 256, 0, s, A);
   if (e != cudaSuccess) return launch_status_report(e);
   return launch_status();
 }
@@ -590,7 +668,7 @@ int dcp_tree_workspace_size(dcp_layout_t layout, int32_t num_reqs, int32_t max_t
   // a call on a cache too large for 32-bit rows takes the other kernel
   *bytes = 0;
   for (int tc = 0; tc <= (tree_tc_shape(head_dim, dtype, layout.block_size) ? 1 : 0); ++tc) {
-    const TreeShape S = tree_shape(tc != 0, num_q_heads / num_kv_heads, max_tree);
+    const TreeShape S = tree_shape(tc != 0, num_q_heads / num_kv_heads, max_tree, 1);
     const size_t n =
         tree_carve(nullptr, nullptr, num_reqs, layout.dcp_size, S.parts, S.rows, head_dim);
     if (n > *bytes) *bytes = n;

@@ -29,7 +29,7 @@ struct TreeArgs {
   int rows;               // query rows of a block: whole nodes
   int tile;               // tokens of a tile
   int parts;              // most runs
-  int extra;              // tiles that a unit's start and end cost beside its own
+  int extra;              // most tiles that a unit counts for beside its own
   float sl2;              // scale * log2(e)
   dcp_rank_ptrs_t k, v;
   const int32_t* bt;
@@ -44,7 +44,7 @@ struct TreeArgs {
   // workspace
   struct TreeEntry* entry;   // [E], E = B or B * dcp
   int32_t* run_entry;        // [parts] entry of each run's first tile
-  int32_t* hdr;              // runs in use, error word, tiles (64 bits)
+  int32_t* hdr;              // runs in use, error word, tiles (64 bits), extra in use
   float* part_o;             // [2 parts][rows][d], normalised
   float* part_lse;           // [2 parts][rows], in log2 units
 };
@@ -118,7 +118,7 @@ struct TreePiece {
 // A run's pieces in order.
 struct TreeWalk {
   int64_t t, begin, end;
-  int run, e;
+  int run, e, extra;
   TreeEntry n;
 };
 
@@ -128,6 +128,7 @@ __device__ __forceinline__ TreeWalk tree_walk(const TreeArgs& A, int run) {
   const int64_t total = __ldcg(reinterpret_cast<const int64_t*>(A.hdr + 2));
   w.run = run;
   w.e = 0;
+  w.extra = __ldcg(A.hdr + 4);
   w.t = w.begin = w.end = 0;
   if (run < parts) {
     w.e = __ldcg(A.run_entry + run);
@@ -141,7 +142,7 @@ __device__ __forceinline__ TreeWalk tree_walk(const TreeArgs& A, int run) {
 // The next piece of the walk, if one is left.
 __device__ __forceinline__ bool tree_next(const TreeArgs& A, TreeWalk& w, TreePiece& p) {
   while (w.t < w.end) {
-    const int unit = w.n.per + A.extra;
+    const int unit = w.n.per + w.extra;
     if (w.t >= w.n.tile0 + (int64_t)w.n.units * unit) {
       w.n = tree_load(A, ++w.e);
       continue;
