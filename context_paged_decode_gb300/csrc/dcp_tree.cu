@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __gri
         if (T > 0) {
           const int r1 = A.per_rank ? r + 1 : A.L.dcp;
           const TreeLen len((int)ctx + T, A.L);
-          for (int x = r; x < r1; ++x) n.per += (len.on(x, A.L) + A.tile - 1) / A.tile;
+          for (int x = r; x < r1; ++x) n.per += (len.on(x, A.L) + A.chunk - 1) / A.chunk;
+          n.per = (n.per + A.tile / A.chunk - 1) / (A.tile / A.chunk);
           if (n.per > 0) n.units = A.Hkv * ((T * A.G + A.rows - 1) / A.rows);
           n.nodes = T;
           n.ctx = (int)ctx;
@@ -538,20 +539,20 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
 // for a call.  The tensor-core kernel takes one 128-row tile of queries where
 // all nodes of a request fit it, else two.
 struct TreeShape {
-  int rows, tile, parts, extra;
+  int rows, chunk, tile, parts, extra;
 };
 
 static TreeShape tree_shape(bool tc, int G, int max_tree, int ranks) {
   if (!tc) {
     // blocks of 16 rows where they hold a request's, else of 32
     const int rows = max_tree * G <= 16 ? 16 : 32;
-    return TreeShape{rows / G * G, kTgTile, 2 * num_sms(), 0};
+    return TreeShape{rows / G * G, kTgTile, kTgTile, 2 * num_sms(), 0};
   }
   const int nodes = 128 / G;
   // what a unit costs beside its tiles: a start and an end, and at each rank's
   // end a tile that is masked (32 requests x 16 nodes, 8 ranks: 488 us with 2 more, 467
   // with 10)
-  return TreeShape{(max_tree <= nodes ? 1 : 2) * nodes * G, 128, num_sms(), 2 + ranks};
+  return TreeShape{(max_tree <= nodes ? 1 : 2) * nodes * G, 16, 128, num_sms(), 2 + ranks};
 }
 
 static size_t tree_carve(TreeArgs* A, void* ws, int B, int dcp, int parts, int rows, int d) {
@@ -620,6 +621,7 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
   A.L = Layout{layout.dcp_size, layout.block_size, layout.interleave};
   A.per_rank = per_rank ? 1 : 0;
   A.rows = S.rows;
+  A.chunk = S.chunk;
   A.tile = S.tile;
   A.parts = S.parts;
   A.extra = S.extra;

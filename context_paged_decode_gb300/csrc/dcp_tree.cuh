@@ -2,8 +2,8 @@
 //
 // A unit is the work of one key/value head on one block of query rows of one
 // request (row = node * G + head of the group), over the request's tokens on
-// all ranks (fused call) or on one rank (partials).  Its tokens are counted in
-// tiles; a tile never crosses a rank.  What a unit costs beside them (loading
+// all ranks (fused call) or on one rank (partials).  Each rank's tokens are cut
+// into chunks, and the chunks of a unit, rank after rank, into tiles.  What a unit costs beside them (loading
 // queries, writing rows) counts as `extra` empty tiles behind its own.  All
 // units' tiles in a row are cut into equal runs, one per CTA, so a CTA holds the end of one unit, some whole
 // units and the start of another.  A unit inside one run is finished by its
@@ -27,7 +27,7 @@ struct TreeArgs {
   Layout L;
   int per_rank;           // 0: a unit spans the ranks; 1: units per rank
   int rows;               // query rows of a block: whole nodes
-  int tile;               // tokens of a tile
+  int chunk, tile;        // tokens of a chunk and of a tile
   int parts;              // most runs
   int extra;              // most tiles that a unit counts for beside its own
   float sl2;              // scale * log2(e)

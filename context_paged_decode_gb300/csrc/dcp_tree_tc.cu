@@ -16,8 +16,8 @@
 //    softmax while the tensor core works for the other;
 //  * up to 256 rows (kTwo true) each has half of the rows and both go through
 //    every tile, which is read once.
-// Warps: 0 and 2 load keys and values by TMA (boxes of 16 to 128 rows, a page
-// or part of one, a lane each), into a ring of their own; 3 loads the queries,
+// Warps: 0 and 2 load keys and values by TMA (chunks of 16 rows, a page or part
+// of one, a lane each), into a ring of their own; 3 loads the queries,
 // whose rows (node, head of the group) are one box of the query tensor; 1
 // issues the products; 4-7 and 8-11 are the softmax, one row per thread, its
 // 128 scores in registers (which the other warps give up for it).  P goes back
@@ -43,15 +43,16 @@
 namespace dcp {
 
 struct TreeTcArgs {
-  CUtensorMap kmap[DCP_MAX_RANKS];   // [num_blocks * Hkv * bs rows][d], box 64 x `box`
+  CUtensorMap kmap[DCP_MAX_RANKS];   // [num_blocks * Hkv * bs rows][d], box 64 x 16
   CUtensorMap vmap[DCP_MAX_RANKS];
   CUtensorMap qmap;                  // [N][Hq][d], box 64 x G x `nodes`
   TreeArgs t;
   int nodes;                         // of a query tile: 128 / G
-  int box;                           // rows of a box: a power of two that divides bs, 16 .. 128
 };
 
 constexpr int kTtTile = 128;
+constexpr int kTtChunk = 16;                 // tokens of one box: a page or part of one
+constexpr int kTtChunks = kTtTile / kTtChunk;
 constexpr int kTtThreads = 384;
 constexpr int kHalfBytes = kTtTile * 128;    // 64 columns of a tile or of a query block
 constexpr float kTtGrow = 8.f;               // log2 units
@@ -74,32 +75,36 @@ struct TreeTc {
   static constexpr uint32_t kColS = 0, kColO = 256;         // two of each, 128 and D apart
 };
 
-// Tiles of a piece in order: rank by rank.
-struct TileIt {
+// A lane's chunk of a tile (lanes 0 .. 7 have one), tile after tile.  Chunks of
+// several ranks share a tile: with a tile per rank's end, short contexts over
+// many ranks spent most of their tiles on a few tokens each.
+struct ChunkIt {
   TreeLen len, old;       // with and without the nodes
-  int r, tr, n, nt, lc;   // rank, tile on it, its tokens, tiles and context tokens
+  int r, x;               // rank, chunk on it
+  int n, c, lc;           // the rank's tokens, chunks and context tokens
   __device__ __forceinline__ void at(const TreeArgs& A, int rank) {
     r = rank;
     n = len.on(r, A.L);
-    nt = (n + kTtTile - 1) / kTtTile;
+    c = (n + kTtChunk - 1) / kTtChunk;
     lc = old.on(r, A.L);
   }
-  __device__ __forceinline__ TileIt(const TreeArgs& A, const TreePiece& p)
+  __device__ __forceinline__ ChunkIt(const TreeArgs& A, const TreePiece& p, int tile, int lane)
       : len(p.ctx + p.T, A.L), old(p.ctx, A.L) {
     at(A, p.r0);
-    tr = p.t0;
+    x = (p.t0 + tile) * kTtChunks + lane;
     settle(A, p);
   }
   __device__ __forceinline__ void settle(const TreeArgs& A, const TreePiece& p) {
-    while (tr >= nt && r + 1 < p.r1) {
-      tr -= nt;
+    while (x >= c && r + 1 < p.r1) {
+      x -= c;
       at(A, r + 1);
     }
   }
-  __device__ __forceinline__ void step(const TreeArgs& A, const TreePiece& p, int k) {
-    tr += k;
+  __device__ __forceinline__ void step(const TreeArgs& A, const TreePiece& p, int tiles) {
+    x += tiles * kTtChunks;
     settle(A, p);
   }
+  __device__ __forceinline__ bool has(int lane) const { return lane < kTtChunks && x < c; }
 };
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
@@ -124,10 +129,10 @@ __device__ __noinline__ void tree_fix(const TreeArgs& A, const TreePiece& p, int
     int64_t vb;
     place_token(ctx + j, A.L, r, vb, loc);
     if (r < p.r0 || r >= p.r1) continue;
-    int t = (int)((vb * A.L.bs + loc) / kTtTile);        // tile of the unit
+    int x = (int)((vb * A.L.bs + loc) / kTtChunk);       // chunk of the unit
     const TreeLen len(p.ctx + T, A.L);
-    for (int x = p.r0; x < r; ++x) t += (len.on(x, A.L) + kTtTile - 1) / kTtTile;
-    if (t < p.t0 || t >= p.t0 + p.n) continue;
+    for (int y = p.r0; y < r; ++y) x += (len.on(y, A.L) + kTtChunk - 1) / kTtChunk;
+    if (x / kTtChunks < p.t0 || x / kTtChunks >= p.t0 + p.n) continue;
     const int64_t phys =
         vb < A.max_vb ? (int64_t)__ldcg(A.bt + r * A.stride + (int64_t)p.b * A.max_vb + vb) : -1;
     if (phys < 0 || phys >= A.nb) continue;
@@ -222,10 +227,9 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       // ---------------- keys (0) and values (2) ----------------
       const bool val = warp == 2;
       const uint64_t pol = policy_evict_first();
-      const int box = X.box, nu = kTtTile / box;
       const int slots = val ? C::kVSlots : C::kKSlots;
       const uint32_t full = val ? b_v : b_k, free = val ? b_vfree : b_kfree;
-      const uint32_t ring = sbase + (val ? C::kVOff : 0) + lane * box * 128;
+      const uint32_t ring = sbase + (val ? C::kVOff : 0) + lane * kTtChunk * 128;
       const CUtensorMap* maps = val ? X.vmap : X.kmap;
       uint32_t slot = 0, par = 1;
       bool dead = false;
@@ -239,7 +243,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
           int raw, off, r;
           bool has;
         };
-        TileIt it(A, p);
+        ChunkIt it(A, p, 0, lane);
         int fetched = 0;
         auto fetch = [&]() {
           Part x;
@@ -248,9 +252,8 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
           x.r = it.r;
           x.has = false;
           if (fetched < p.n) {
-            const int pos = it.tr * kTtTile + lane * box;
-            x.has = lane < nu && pos < it.n;
-            const int j = pos / A.L.bs;
+            x.has = it.has(lane);
+            const int pos = it.x * kTtChunk, j = pos / A.L.bs;
             x.off = pos - j * A.L.bs;
             if (x.has && j < A.max_vb) x.raw = __ldcg(bt + it.r * A.stride + j);
             ++fetched;
@@ -273,7 +276,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
           const uint32_t bar = full + 8 * slot;
           if (lane == 0) {
             if (m)
-              mbar_arrive_expect_tx(bar, __popc(m) * box * D * 2);
+              mbar_arrive_expect_tx(bar, __popc(m) * kTtChunk * D * 2);
             else
               mbar_arrive(bar);
           }
@@ -431,31 +434,29 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       float m = -INFINITY, l = 0.f;
       bool filled = false;                               // the accumulator holds earlier tiles
       if (takes) {
-        // The table entries of a tile's pages (16 tokens a lane) are loaded
-        // a tile ahead.
-        TileIt it(A, p);
-        if (!kTwo && s == 1 && p.n > 1) it.step(A, p, 1);
+        // The table entry of a lane's chunk is loaded a tile ahead.
+        ChunkIt it(A, p, !kTwo && p.n > s ? s : 0, lane);
         int raw;
         auto fetch = [&]() {
-          raw = -2;   // no tokens
-          const int p0 = it.tr * kTtTile + lane * 16;
-          if (lane < 8 && p0 < it.n) {
-            const int j = p0 / A.L.bs;
-            raw = j < A.max_vb ? __ldcg(A.bt + it.r * A.stride + (int64_t)p.b * A.max_vb + j) : -1;
-          }
+          raw = -1;
+          const int j = it.x * kTtChunk / A.L.bs;
+          if (it.has(lane) && j < A.max_vb)
+            raw = __ldcg(A.bt + it.r * A.stride + (int64_t)p.b * A.max_vb + j);
         };
         fetch();
         for (int k = kTwo ? 0 : s; k < p.n; k += step) {
-          const int p0 = it.tr * kTtTile, nv = min(kTtTile, it.n - p0), old_n = it.lc - p0;
-          const int rank = it.r;
-          const uint32_t pages =
-              __ballot_sync(0xffffffffu, raw == -2 || (raw >= 0 && (int64_t)raw < A.nb));
+          // this lane's chunk: first position, rank, and the ends of what is
+          // there and of what all rows see
+          const int c_pos = it.x * kTtChunk, c_rank = it.r;
+          const bool usable = it.has(lane) && raw >= 0 && (int64_t)raw < A.nb;
+          const int c_end = usable ? it.n : 0, c_old = usable ? it.lc : 0;
+          const uint32_t plain = __ballot_sync(0xffffffffu, c_pos + kTtChunk <= c_old);
           if (k + step < p.n) {
             it.step(A, p, step);
             fetch();
           }
           // a tile whose tokens all rows see takes no masks
-          const bool special = nv < kTtTile || nv > old_n || (pages & 0xFFu) != 0xFFu;
+          const bool special = (plain & 0xFFu) != 0xFFu;
           uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
           uint32_t v_old = ~0u, v_node = 0;   // of this warp's 32 tokens of V
           uint32_t masked = 0;                // groups that some row sees in part
@@ -463,9 +464,11 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               // token g * 32 + lane: seen by everyone, a node, or not there
-              const int tk = g * 32 + lane;
-              const bool there = tk < nv && ((pages >> (tk >> 4)) & 1);
-              const bool old = there && tk < old_n;
+              const int from = 2 * g + (lane >> 4);
+              const int pos = __shfl_sync(0xffffffffu, c_pos, from) + (lane & 15);
+              const bool there = pos < __shfl_sync(0xffffffffu, c_end, from);
+              const bool old = pos < __shfl_sync(0xffffffffu, c_old, from);
+              const int rank = __shfl_sync(0xffffffffu, c_rank, from);
               vis[g] = __ballot_sync(0xffffffffu, old);
               uint32_t nodes = __ballot_sync(0xffffffffu, there && !old);
               if (vis[g] != ~0u) masked |= 1u << g;
@@ -474,8 +477,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
                 v_node = nodes;
               }
               if (nodes) {   // by this row's mask
-                const int node =
-                    there && !old ? (tree_global(p0 + tk, rank, A.L) - p.ctx) & 63 : 0;
+                const int node = there && !old ? (tree_global(pos, rank, A.L) - p.ctx) & 63 : 0;
                 do {
                   const int o = __ffs(nodes) - 1;
                   nodes &= nodes - 1;
@@ -725,12 +727,6 @@ static bool encode_q(CUtensorMap* map, const TreeArgs& A, int nodes) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static int tree_box(int bs) {
-  int b = 16;
-  while (b < 128 && bs % (2 * b) == 0) b *= 2;
-  return b;
-}
-
 bool tree_tc_shape(int d, dcp_dtype_t dtype, int block_size) {
   return dtype == DCP_BF16 && (d == 64 || d == 128) && block_size % 16 == 0;
 }
@@ -756,14 +752,13 @@ int launch_tree_tc(const TreeArgs& A, cudaStream_t s) {
   TreeTcArgs X;
   memset(&X, 0, sizeof(X));
   X.t = A;
-  X.box = tree_box(A.L.bs);
   X.nodes = 128 / A.G;
   if (!encode_q(&X.qmap, A, X.nodes)) return DCP_ECUDA;
   const uint64_t rows = (uint64_t)A.nb * A.Hkv * A.L.bs;
   for (int r = 0; r < A.L.dcp; ++r)
     if (!encode_2d_bf16_sw128(&X.kmap[r], A.k.ptr[r], A.d, rows > 0 ? rows : 1, A.d * 2, 64,
-                              X.box) ||
-        !encode_2d_bf16_sw128(&X.vmap[r], A.v.ptr[r], A.d, rows > 0 ? rows : 1, A.d * 2, 64, X.box))
+                              kTtChunk) ||
+        !encode_2d_bf16_sw128(&X.vmap[r], A.v.ptr[r], A.d, rows > 0 ? rows : 1, A.d * 2, 64, kTtChunk))
       return DCP_ECUDA;
   const bool two = A.rows > X.nodes * A.G;
   if (A.d == 64) return two ? go<64, true>(X, s) : go<64, false>(X, s);
