@@ -448,9 +448,13 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
           // this lane's chunk: first position, rank, and the ends of what is
           // there and of what all rows see
           const int c_pos = it.x * kTtChunk, c_rank = it.r;
-          const bool usable = it.has(lane) && raw >= 0 && (int64_t)raw < A.nb;
-          const int c_end = usable ? it.n : 0, c_old = usable ? it.lc : 0;
-          const uint32_t plain = __ballot_sync(0xffffffffu, c_pos + kTtChunk <= c_old);
+          // its tokens as bits: low half seen by all rows, high half there
+          uint32_t bits = 0;
+          if (it.has(lane) && raw >= 0 && (int64_t)raw < A.nb) {
+            const int there = min(it.n - c_pos, kTtChunk), old = min(max(it.lc - c_pos, 0), there);
+            bits = ((1u << old) - 1u) | ((1u << there) - 1u) << 16;
+          }
+          const uint32_t plain = __ballot_sync(0xffffffffu, bits == ~0u);
           if (k + step < p.n) {
             it.step(A, p, step);
             fetch();
@@ -463,21 +467,20 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
           if (special) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              // token g * 32 + lane: seen by everyone, a node, or not there
-              const int from = 2 * g + (lane >> 4);
-              const int pos = __shfl_sync(0xffffffffu, c_pos, from) + (lane & 15);
-              const bool there = pos < __shfl_sync(0xffffffffu, c_end, from);
-              const bool old = pos < __shfl_sync(0xffffffffu, c_old, from);
-              const int rank = __shfl_sync(0xffffffffu, c_rank, from);
-              vis[g] = __ballot_sync(0xffffffffu, old);
-              uint32_t nodes = __ballot_sync(0xffffffffu, there && !old);
+              const uint32_t lo = __shfl_sync(0xffffffffu, bits, 2 * g);
+              const uint32_t hi = __shfl_sync(0xffffffffu, bits, 2 * g + 1);
+              vis[g] = __byte_perm(lo, hi, 0x5410);
+              uint32_t nodes = __byte_perm(lo, hi, 0x7632) & ~vis[g];
               if (vis[g] != ~0u) masked |= 1u << g;
               if (g == quarter) {
                 v_old = vis[g];
                 v_node = nodes;
               }
               if (nodes) {   // by this row's mask
-                const int node = there && !old ? (tree_global(pos, rank, A.L) - p.ctx) & 63 : 0;
+                const int from = 2 * g + (lane >> 4);
+                const int pos = __shfl_sync(0xffffffffu, c_pos, from) + (lane & 15);
+                const int rank = __shfl_sync(0xffffffffu, c_rank, from);
+                const int node = (tree_global(pos, rank, A.L) - p.ctx) & 63;
                 do {
                   const int o = __ffs(nodes) - 1;
                   nodes &= nodes - 1;
@@ -565,10 +568,12 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
             wait(b_v + 8 * vslot, (vi / C::kVSlots) & 1);
             const uint32_t v = sbase + C::kVOff + vslot * C::kSlot;
             constexpr int kRow = D / 8;                // 16-byte pieces of a row
-            if (!dead)
-              for (int i = lane; i < 32 * kRow; i += 32) {
-                const int o = i / kRow, ch = i % kRow;
-                if ((v_old >> o) & 1) continue;
+            constexpr int kAtOnce = 32 / kRow;         // rows of the warp at once
+            const int ch = lane % kRow;
+            for (int o0 = 0; o0 < 32 && !dead; o0 += kAtOnce) {
+              if (((v_old >> o0) & ((1u << kAtOnce) - 1u)) == (1u << kAtOnce) - 1u) continue;
+              const int o = o0 + lane / kRow;
+              if (!((v_old >> o) & 1)) {
                 const int tok = quarter * 32 + o;
                 const uint32_t at =
                     v + (ch >> 3) * kHalfBytes + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4);
@@ -596,6 +601,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
                                "r"(w[1]), "r"(w[2]), "r"(w[3])
                                : "memory");
               }
+            }
             fence_proxy_async_smem();
           }
           tc_fence_before();
