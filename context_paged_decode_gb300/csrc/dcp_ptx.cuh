@@ -73,10 +73,10 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 // set-up overlap the preceding kernel's tail, never its reads or writes (and
 // when the preceding work is not a kernel the launch is an ordinary one).
 template <typename... Exp, typename... Act>
-cudaError_t launch_chained(void (*kernel)(Exp...), unsigned grid, unsigned block, size_t smem,
+cudaError_t launch_chained(void (*kernel)(Exp...), dim3 grid, unsigned block, size_t smem,
                            cudaStream_t st, Act&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -35,6 +35,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __gri
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const bool single = E <= kTreePlanThreads;
   int64_t tiles = 0, units = 0, extra = 0, total = 0;
+  for (int k = tid; k < A.parts; k += kTreePlanThreads) A.arrived[k] = 0;
   // more entries than threads: a first round only for the sums
   for (int round = single ? 1 : 0; round < 2; ++round) {
     const int64_t all_t = tiles, all_u = units;
@@ -449,40 +450,50 @@ static int launch_tree_generic(const TreeArgs& A, cudaStream_t s) {
 
 // One warp per output row.  Rows whose unit lay in one run were written by its
 // CTA; rows of refused requests and outside every request stay as they were.
+// Latency bounds it: a row waits for its entry, then for its parts' LSEs (a
+// lane each) and the first parts' values together.  `joined`: the parts are
+// joined already, only ranks that hold nothing are left.
 template <int DPL>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs A) {
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs A, bool joined) {
   constexpr int kFly = 64 / DPL;         // parts whose values are in flight at once
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int parts = __ldcg(A.hdr), extra = __ldcg(A.hdr + 4);
   const int64_t total = __ldcg(reinterpret_cast<const int64_t*>(A.hdr + 2));
-  // rows in the order (rank,) request, node, head
-  const int64_t rows = (int64_t)A.B * A.max_tree * A.Hq * (A.per_rank ? A.L.dcp : 1);
-  for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < rows; i += gridDim.x * 8ll) {
-    const int h = (int)(i % A.Hq);
-    const int64_t br = i / A.Hq / A.max_tree;
-    const int j = (int)(i / A.Hq - br * A.max_tree);
-    const int r = (int)(br / A.B), b = (int)(br - (int64_t)r * A.B);
-    const TreeEntry n = tree_load(A, A.per_rank ? b * A.L.dcp + r : b);
-    if (j >= n.nodes) continue;
+  // blockIdx.x: (rank,) request; rows of it (node, head) by warp
+  const int r = A.per_rank ? blockIdx.x / A.B : 0, b = blockIdx.x - r * A.B;
+  const TreeEntry n = tree_load(A, A.per_rank ? b * A.L.dcp + r : b);
+  const int mine = n.nodes * A.Hq;
+  for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < mine; i += gridDim.y * 8) {
+    const int j = i / A.Hq, h = i - j * A.Hq;
     const int64_t row = ((int64_t)r * A.N + n.q0 + j) * A.Hq + h;
     float* of = (float*)A.out + row * A.d;
     __nv_bfloat16* ob = (__nv_bfloat16*)A.out + row * A.d;
+    if (n.units > 0 && joined) return;
     if (n.units == 0) {   // a rank without tokens of this request
       for (int c = lane; c < A.d; c += 32) of[c] = 0.f;
       if (lane == 0) A.lse[row] = -INFINITY;
       continue;
     }
-    const int per = n.per;
     const int g = h / A.G, ur = j * A.G + h % A.G;   // row of the unit's request
     const int rb = ur / A.rows, rr = ur - rb * A.rows;
-    const int64_t t0 = n.tile0 + (int64_t)(g * (n.units / A.Hkv) + rb) * (per + extra);
-    const int k0 = tree_run_of(total, parts, t0), k1 = tree_run_of(total, parts, t0 + per - 1);
+    const int64_t t0 = n.tile0 + (int64_t)(g * (n.units / A.Hkv) + rb) * (n.per + extra);
+    const int k0 = tree_run_of(total, parts, t0), k1 = tree_run_of(total, parts, t0 + n.per - 1);
     if (k0 == k1) continue;
     const bool late = tree_run(total, parts, k0) != t0;   // run k0 began before this unit
     auto slot = [&](int k) { return (int64_t)(2 * k + (k == k0 && late)) * A.rows + rr; };
-    // a lane per part: one wait for up to 32 parts' LSEs
+    float v[kFly][DPL];
+    auto fetch = [&](int k) {
+#pragma unroll
+      for (int x = 0; x < kFly; ++x)
+#pragma unroll
+        for (int y = 0; y < DPL; ++y)
+          v[x][y] = k + x <= k1 && y * 32 < A.d
+                        ? __ldcg(A.part_o + slot(k + x) * A.d + y * 32 + lane)
+                        : 0.f;
+    };
+    fetch(k0);
     const bool sunk = A.sink != nullptr;
     const float s2 = sunk ? __ldcg(A.sink + h) * kLog2e : -INFINITY;
     float M = s2;
@@ -492,40 +503,32 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     float L = sunk ? exp2f(s2 - mb) : 0.f;
     float acc[DPL];
 #pragma unroll
-    for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
+    for (int y = 0; y < DPL; ++y) acc[y] = 0.f;
     for (int k = k0; k <= k1; k += 32) {
       const float lse = k + lane <= k1 ? __ldcg(A.part_lse + slot(k + lane)) : -INFINITY;
       // a part that saw nothing does not count, whatever its values are
-      const float mine = lse == -INFINITY ? 0.f : exp2f(lse - mb);
-      L += warp_sum(mine);
-      const int n = min(32, k1 - k + 1);
-      for (int j0 = 0; j0 < n; j0 += kFly) {
-        float v[kFly][DPL];
+      const float part = lse == -INFINITY ? 0.f : exp2f(lse - mb);
+      L += warp_sum(part);
+      for (int x0 = 0; x0 < 32 && k + x0 <= k1; x0 += kFly) {
+        if (k + x0 > k0) fetch(k + x0);
 #pragma unroll
-        for (int j = 0; j < kFly; ++j)
+        for (int x = 0; x < kFly; ++x) {
+          const float wgt = __shfl_sync(0xffffffffu, part, (x0 + x) & 31);
+          if (wgt != 0.f) {   // (zero for parts that are not there)
 #pragma unroll
-          for (int i = 0; i < DPL; ++i)
-            v[j][i] = j0 + j < n && i * 32 < A.d
-                          ? __ldcg(A.part_o + slot(k + j0 + j) * A.d + i * 32 + lane)
-                          : 0.f;
-#pragma unroll
-        for (int j = 0; j < kFly; ++j) {
-          const float wgt = __shfl_sync(0xffffffffu, mine, (j0 + j) & 31);
-          if (j0 + j < n && wgt != 0.f) {
-#pragma unroll
-            for (int i = 0; i < DPL; ++i) acc[i] = fmaf(wgt, v[j][i], acc[i]);
+            for (int y = 0; y < DPL; ++y) acc[y] = fmaf(wgt, v[x][y], acc[y]);
           }
         }
       }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-    for (int i = 0; i < DPL; ++i)
-      if (i * 32 < A.d) {
+    for (int y = 0; y < DPL; ++y)
+      if (y * 32 < A.d) {
         if (A.out_dtype == DCP_F32)
-          of[i * 32 + lane] = acc[i] * inv;
+          of[y * 32 + lane] = acc[y] * inv;
         else
-          ob[i * 32 + lane] = __float2bfloat16_rn(acc[i] * inv);
+          ob[y * 32 + lane] = __float2bfloat16_rn(acc[y] * inv);
       }
     if (lane == 0 && A.lse) A.lse[row] = L == 0.f ? -INFINITY : (mb + log2f(L)) * kLn2;
   }
@@ -566,12 +569,14 @@ static size_t tree_carve(TreeArgs* A, void* ws, int B, int dcp, int parts, int r
   char* hdr = take(32);
   char* en = take(sizeof(TreeEntry) * E);
   char* re = take(sizeof(int32_t) * (size_t)parts);
+  char* ar = take(sizeof(int32_t) * (size_t)parts);
   char* pl = take(sizeof(float) * 2 * (size_t)parts * rows);
   char* po = take(sizeof(float) * 2 * (size_t)parts * rows * d);
   if (A) {
     A->hdr = (int32_t*)hdr;
     A->entry = (TreeEntry*)en;
     A->run_entry = (int32_t*)re;
+    A->arrived = (int32_t*)ar;
     A->part_lse = (float*)pl;
     A->part_o = (float*)po;
   }
@@ -625,6 +630,12 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
   A.tile = S.tile;
   A.parts = S.parts;
   A.extra = S.extra;
+  // With at least as many units as runs a unit is cut into two or three parts,
+  // which the last CTA to come joins in passing; with fewer it is cut into many,
+  // and the merge's warps join them faster than one CTA would (GPU time, 32 x 16
+  // nodes over up to 4096 tokens: 77 us against 79 and a launch less; 16 x 5
+  // nodes on one key head: 45 us against 20).
+  A.join = tc && (int64_t)B * Hkv * (per_rank ? layout.dcp_size : 1) >= S.parts ? 1 : 0;
   A.sl2 = scale * kLog2e;
   A.k = kv.k;
   A.v = kv.v;
@@ -645,12 +656,12 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
                  : dtype == DCP_F32 ? launch_tree_generic<float>(A, s)
                                     : launch_tree_generic<__nv_bfloat16>(A, s);
   if (rc != DCP_OK) return rc;
-  const int64_t rows = (int64_t)B * max_tree * Hq * (per_rank ? layout.dcp_size : 1);
-  const int64_t blocks = (rows + 7) / 8, most = (int64_t)8 * num_sms();
-  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-  e = d <= 64    ? launch_chained(tree_merge_kernel<2>, grid, 256, 0, s, A)
-      : d <= 128 ? launch_chained(tree_merge_kernel<4>, grid, 256, 0, s, A)
-                 : launch_chained(tree_merge_kernel<8>, grid, 256, 0, s, A);
+  if (A.join && !per_rank) return launch_status();   // nothing is left to merge
+  const int64_t by = ((int64_t)max_tree * Hq + 7) / 8;
+  const dim3 grid((unsigned)B * (per_rank ? layout.dcp_size : 1), (unsigned)(by < 8192 ? by : 8192));
+  e = d <= 64    ? launch_chained(tree_merge_kernel<2>, grid, 256, 0, s, A, A.join != 0)
+      : d <= 128 ? launch_chained(tree_merge_kernel<4>, grid, 256, 0, s, A, A.join != 0)
+                 : launch_chained(tree_merge_kernel<8>, grid, 256, 0, s, A, A.join != 0);
   if (e != cudaSuccess) return launch_status_report(e);
   return launch_status();
 }

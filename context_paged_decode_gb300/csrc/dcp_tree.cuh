@@ -7,7 +7,8 @@
 // queries, writing rows) counts as `extra` empty tiles behind its own.  All
 // units' tiles in a row are cut into equal runs, one per CTA, so a CTA holds the end of one unit, some whole
 // units and the start of another.  A unit inside one run is finished by its
-// CTA; one that is cut leaves a partial per run, which the merge joins.
+// CTA; one that is cut leaves a partial per run, and the partials are joined in
+// the order of the runs (by the last CTA that comes to them, or by a merge).
 // Partial slots: a run has at most two cut pieces, its first (slot 2 run) and
 // its last (2 run + 1).
 #pragma once
@@ -30,6 +31,7 @@ struct TreeArgs {
   int chunk, tile;        // tokens of a chunk and of a tile
   int parts;              // most runs
   int extra;              // most tiles that a unit counts for beside its own
+  int join;               // the last CTA to come joins a cut unit, not the merge
   float sl2;              // scale * log2(e)
   dcp_rank_ptrs_t k, v;
   const int32_t* bt;
@@ -47,6 +49,7 @@ struct TreeArgs {
   int32_t* hdr;              // runs in use, error word, tiles (64 bits), extra in use
   float* part_o;             // [2 parts][rows][d], normalised
   float* part_lse;           // [2 parts][rows], in log2 units
+  int32_t* arrived;          // [parts] partials there of the unit whose first run it is
 };
 
 // One request's units (on one rank, for partials), in one 32-byte read.
@@ -98,12 +101,16 @@ __device__ __forceinline__ int tree_global(int p, int r, const Layout& L) {
   return vb * L.bs * L.dcp + (run * L.dcp + r) * L.I + (loc - run * L.I);
 }
 
-// Run k of the tiles [0, total) over `parts`.
+// Run k of the tiles [0, total) over `parts` begins at total * k / parts, and
+// tile t is in run ((t + 1) * parts - 1) / total; in 32 bits where they hold it
+// (a 64-bit division is some 150 instructions, and the merge takes three a row).
 __device__ __forceinline__ int64_t tree_run(int64_t total, int parts, int k) {
-  return total * k / parts;
+  const int64_t x = total * k;
+  return (uint64_t)x >> 32 ? x / parts : (int64_t)((uint32_t)x / (uint32_t)parts);
 }
 __device__ __forceinline__ int tree_run_of(int64_t total, int parts, int64_t tile) {
-  return (int)(((tile + 1) * parts - 1) / total);
+  const int64_t x = (tile + 1) * parts - 1;
+  return (uint64_t)x >> 32 ? (int)(x / total) : (int)((uint32_t)x / (uint32_t)total);
 }
 
 // A piece: tiles [t0, t0 + n) of one unit.
@@ -113,19 +120,21 @@ struct TreePiece {
   int g, rb;            // key/value head, row block
   int t0, n;            // first tile (within the unit) and count
   int slot;             // partial slot, -1: the whole unit
+  int64_t u0;           // the unit's first tile, among all
+  int per;              // its tiles
 };
 
 // A run's pieces in order.
 struct TreeWalk {
-  int64_t t, begin, end;
-  int run, e, extra;
+  int64_t t, begin, end, total;
+  int run, e, extra, parts;
   TreeEntry n;
 };
 
 __device__ __forceinline__ TreeWalk tree_walk(const TreeArgs& A, int run) {
   TreeWalk w;
-  const int parts = __ldcg(A.hdr);
-  const int64_t total = __ldcg(reinterpret_cast<const int64_t*>(A.hdr + 2));
+  const int parts = w.parts = __ldcg(A.hdr);
+  const int64_t total = w.total = __ldcg(reinterpret_cast<const int64_t*>(A.hdr + 2));
   w.run = run;
   w.e = 0;
   w.extra = __ldcg(A.hdr + 4);
@@ -156,6 +165,8 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& A, TreeWalk& w, TreePi
     p.slot = p.t0 == 0 && p.n == w.n.per ? -1 : 2 * w.run + (w.t == w.begin ? 0 : 1);
     w.t += take;
     if (p.n <= 0) continue;
+    p.u0 = w.n.tile0 + (int64_t)ui * unit;
+    p.per = w.n.per;
     p.b = A.per_rank ? w.e / A.L.dcp : w.e;
     p.r0 = A.per_rank ? w.e % A.L.dcp : 0;
     p.r1 = A.per_rank ? p.r0 + 1 : A.L.dcp;

@@ -68,7 +68,7 @@ struct TreeTc {
   static constexpr int kVOff = kKSlots * kSlot;
   static constexpr int kQOff = kVOff + kVSlots * kSlot;
   static constexpr int kMlOff = kQOff + kQ;                 // float2 [2 stream][128]
-  static constexpr int kFlagOff = kMlOff + 2 * 128 * 8;     // int [2 parity]
+  static constexpr int kFlagOff = kMlOff + 2 * 128 * 8;     // int [2 parity], joins
   static constexpr int kBarOff = kFlagOff + 16;
   static constexpr int kBars = 2 * (kKSlots + kVSlots) + 8;
   static constexpr int kSmem = kBarOff + 8 * kBars + 16;
@@ -154,6 +154,113 @@ __device__ __noinline__ void tree_fix(const TreeArgs& A, const TreePiece& p, int
       else
         ((__nv_bfloat16*)dst)[c] =
             __float2bfloat16_rn(__bfloat162float(((__nv_bfloat16*)dst)[c]) + w * x);
+    }
+  }
+}
+
+// Joins the partials of a unit that was cut (runs k0 .. k1), in the order of the
+// runs, whoever does it: a warp takes four rows at a time, a lane a part's LSE
+// of each and D / 32 columns, four parts' values in flight.
+template <int D>
+__device__ __forceinline__ void tree_join(const TreeArgs& A, const TreePiece& p, int k0, int k1,
+                                          bool late, int nrows, int warp) {
+  constexpr int kV = D / 32, kR = 4, kP = 4;
+  const int lane = threadIdx.x & 31;
+  auto slot = [&](int k) { return (int64_t)(2 * k + (k == k0 && late)) * A.rows; };
+  const bool sunk = A.sink != nullptr;
+#pragma unroll 1
+  for (int r0 = warp * kR; r0 < nrows; r0 += 8 * kR) {
+    float v[kR][kP][kV];
+    auto fetch = [&](int k) {
+#pragma unroll
+      for (int x = 0; x < kR; ++x)
+#pragma unroll
+        for (int y = 0; y < kP; ++y)
+#pragma unroll
+          for (int z = 0; z < kV; ++z) v[x][y][z] = 0.f;
+#pragma unroll
+      for (int x = 0; x < kR; ++x)
+#pragma unroll
+        for (int y = 0; y < kP; ++y)
+          if (r0 + x < nrows && k + y <= k1) {
+            const float* src = A.part_o + (slot(k + y) + r0 + x) * D + lane * kV;
+            if (kV == 4) {
+              const float4 q = __ldcg((const float4*)src);
+              v[x][y][0] = q.x;
+              v[x][y][1] = q.y;
+              v[x][y][2 % kV] = q.z;
+              v[x][y][3 % kV] = q.w;
+            } else {
+              const float2 q = __ldcg((const float2*)src);
+              v[x][y][0] = q.x;
+              v[x][y][1] = q.y;
+            }
+          }
+    };
+    fetch(k0);
+    float M[kR], L[kR], s2[kR], acc[kR][kV];
+#pragma unroll
+    for (int x = 0; x < kR; ++x) {
+      const int h = p.g * A.G + (p.rb * A.rows + r0 + x) % A.G;
+      M[x] = s2[x] = sunk ? __ldcg(A.sink + h) * kLog2e : -INFINITY;
+#pragma unroll
+      for (int z = 0; z < kV; ++z) acc[x][z] = 0.f;
+    }
+#pragma unroll 1
+    for (int k = k0; k <= k1; k += 32)
+#pragma unroll
+      for (int x = 0; x < kR; ++x)
+        M[x] = fmaxf(M[x], warp_max(r0 + x < nrows && k + lane <= k1
+                                        ? __ldcg(A.part_lse + slot(k + lane) + r0 + x)
+                                        : -INFINITY));
+#pragma unroll
+    for (int x = 0; x < kR; ++x) {
+      if (M[x] == -INFINITY) M[x] = 0.f;
+      L[x] = sunk ? exp2f(s2[x] - M[x]) : 0.f;
+    }
+#pragma unroll 1
+    for (int k = k0; k <= k1; k += 32) {
+      float part[kR];
+#pragma unroll
+      for (int x = 0; x < kR; ++x) {
+        const float lse = r0 + x < nrows && k + lane <= k1
+                              ? __ldcg(A.part_lse + slot(k + lane) + r0 + x)
+                              : -INFINITY;
+        // a part that saw nothing does not count, whatever its values are
+        part[x] = lse == -INFINITY ? 0.f : exp2f(lse - M[x]);
+        L[x] += warp_sum(part[x]);
+      }
+#pragma unroll 1
+      for (int y0 = 0; y0 < 32 && k + y0 <= k1; y0 += kP) {
+        if (k + y0 > k0) fetch(k + y0);
+#pragma unroll
+        for (int x = 0; x < kR; ++x)
+#pragma unroll
+          for (int y = 0; y < kP; ++y) {
+            const float w = __shfl_sync(0xffffffffu, part[x], (y0 + y) & 31);
+            if (w != 0.f) {
+#pragma unroll
+              for (int z = 0; z < kV; ++z) acc[x][z] = fmaf(w, v[x][y][z], acc[x][z]);
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kR; ++x) {
+      if (r0 + x >= nrows) continue;
+      const float inv = L[x] == 0.f ? 0.f : 1.f / L[x];
+      const int64_t orow = tree_out_row(A, p, p.rb * A.rows + r0 + x);
+      if (A.out_dtype == DCP_F32) {
+        float* dst = (float*)A.out + orow * D + lane * kV;
+#pragma unroll
+        for (int z = 0; z < kV; z += 2)
+          *(float2*)(dst + z) = make_float2(acc[x][z] * inv, acc[x][z + 1] * inv);
+      } else {
+        uint32_t* dst = (uint32_t*)((__nv_bfloat16*)A.out + orow * D + lane * kV);
+#pragma unroll
+        for (int z = 0; z < kV; z += 2) dst[z / 2] = pack_bf16(acc[x][z] * inv, acc[x][z + 1] * inv);
+      }
+      if (lane == 0 && A.lse) A.lse[orow] = L[x] == 0.f ? -INFINITY : (M[x] + log2f(L[x])) * kLn2;
     }
   }
 }
@@ -708,6 +815,21 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       __syncwarp();
       if (lane == 0) mbar_arrive(b_ofree);
       seq += p.n;
+      if (p.slot >= 0 && A.join) {
+        // the last run to bring its part joins them all
+        const int k0 = tree_run_of(walk.total, walk.parts, p.u0);
+        const int k1 = tree_run_of(walk.total, walk.parts, p.u0 + p.per - 1);
+        __threadfence();
+        bar_sync(3, 256);
+        if (threadIdx.x == 128) {
+          const int before = atomicAdd(A.arrived + k0, 1);
+          flag[2] = before == k1 - k0;
+          __threadfence();
+        }
+        bar_sync(3, 256);
+        if (flag[2])
+          tree_join<D>(A, p, k0, k1, tree_run(walk.total, walk.parts, k0) != p.u0, nrows, warp - 4);
+      }
     }
     if (dead && lane == 0) atomicAdd(errp, kTtStuck);
   }
