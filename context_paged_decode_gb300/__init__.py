@@ -11,8 +11,6 @@ is no fallback implementation.
 from __future__ import annotations
 
 import ctypes as C
-import functools
-import operator
 import os
 
 import torch
@@ -62,11 +60,27 @@ class PoolSetStruct(C.Structure):
 
 
 _lib = None
+_bind = None     # the native extension, once it knows the library
+_loaded_from = LIB_PATH
+
+
+def _load_binding():
+    """Load the library and the extension that hands tensors to it (once)."""
+    global _bind
+    load()
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise DcpError(f"the native binding is not built ({e}): build it with "
+                       "__graft_entry__.build()") from None
+    _binding.init(_loaded_from, DcpError)
+    _bind = _binding
+    return _bind
 
 
 def load(path: str = LIB_PATH):
     """Load libdcp.so (once).  Raises if it is missing: there is no fallback."""
-    global _lib
+    global _lib, _bind, _loaded_from
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -133,7 +147,7 @@ def load(path: str = LIB_PATH):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    _lib = lib
+    _lib, _bind, _loaded_from = lib, None, os.path.abspath(path)
     return lib
 
 
@@ -553,159 +567,18 @@ def sfa_decode(layout, q, kv: PagedKV, topk, seq_lens, scale, v_dim=512, sink=No
 # ---------------------------------------------------------------------------
 # around the decode step: drafted token trees, rotary positions, pages
 # ---------------------------------------------------------------------------
-# These calls are short (a few microseconds on the GPU), so what a call costs
-# on the host counts: each tensor is checked once, in one place, handles keep
-# their C structs, and pointers go to C as plain integers.
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_new_empty = torch.empty
-
-
-def _cur_stream(stream, dev):
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(dev)
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
-def _device_of(t, what):
-    """Index of a tensor's device, which has to be the current one (the kernels launch there)."""
-    dev = t.get_device()
-    if dev < 0:
-        raise DcpError(f"{what} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise DcpError(f"{what} is on cuda:{dev}, but the current device is "
-                       f"cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _ptr(t, what, dtype, shape, dev):
-    """Address of a contiguous tensor of this type and shape on this device."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or \
-            not t.is_contiguous():
-        raise DcpError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                       f"cuda:{dev}, got {t.dtype}, {tuple(t.shape)}, {t.device}"
-                       f"{'' if t.is_contiguous() else ', not contiguous'}")
-    return t.data_ptr()
-
-
-def _opt(t, what, dtype, shape, dev):
-    return None if t is None else _ptr(t, what, dtype, shape, dev)
-
-
-def _err_ptr(err, dev):
-    if err is None:
-        return None
-    if err.dtype is not torch.int32 or err.get_device() != dev or err.numel() < 1:
-        raise DcpError("err must be an int32 tensor on the call's device")
-    return err.data_ptr()
-
-
-def _ws_ptr(ws, need, dev):
-    """Address and bytes of a workspace (allocated if there is none), and what keeps it."""
-    if ws is None:
-        ws = _new_empty(max(need, 1), dtype=torch.uint8, device=dev)
-    elif ws.get_device() != dev or not ws.is_contiguous():
-        raise DcpError("the workspace must be a contiguous tensor on the call's device")
-    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
-
-
-def _dims(t, n, what):
-    if t.dim() != n:
-        raise DcpError(f"{what} must have {n} dimensions, got {tuple(t.shape)}")
-    return t.shape
-
-
-def _rank_list(layout, pools, what, dtype, shape, dev):
-    """RankPtrs of a list of one pool per rank, each checked."""
-    n = layout.dcp_size
-    if not 1 <= n <= MAX_RANKS or len(pools) < n:
-        raise DcpError(f"{what}: {len(pools)} pools for {n} ranks")
-    ptrs = []
-    for p in pools[:n]:
-        if p.dtype is not dtype or p.shape != shape or p.get_device() != dev or \
-                not p.is_contiguous():
-            _ptr(p, what, dtype, shape, dev)
-        ptrs.append(p.data_ptr())
-    return RankPtrs(_RankArray(*ptrs))
-
-
-_RankArray = C.c_void_p * MAX_RANKS
-
-
-class _Seal:
-    """What the tree calls need of a PagedKV, checked once: the handle's C
-    struct and the shape, type and device of its pools."""
-
-    def __init__(self, kv, layout):
-        self.refs = (kv.block_table, *kv.k_pools, *(kv.v_pools or ()))
-        self.key = (layout.dcp_size, layout.block_size, kv.num_blocks, kv.bt_rank_stride, kv.max_vb)
-        if kv.v_pools is None or kv.k_pools[0].dim() != 4:
-            raise DcpError("the cache needs key and value pools [blocks, heads, block_size, d]")
-        n = layout.dcp_size
-        first = kv.k_pools[0]
-        self.dtype, self.dev = first.dtype, first.get_device()
-        self.dt = _dtype(first)
-        self.Hkv, self.d = first.shape[1], first.shape[3]
-        shape = (kv.num_blocks, self.Hkv, layout.block_size, self.d)
-        _rank_list(layout, kv.k_pools, "k_pools", self.dtype, shape, self.dev)
-        _rank_list(layout, kv.v_pools, "v_pools", self.dtype, shape, self.dev)
-        bt = kv.block_table
-        if bt.get_device() != self.dev:
-            raise DcpError("the block table is on another device than the pools")
-        if kv.bt_rank_stride and bt.shape[0] < n:
-            raise DcpError(f"{bt.shape[0]} block tables for {n} ranks")
-        self.reqs = bt.shape[-2]
-        self.struct = kv.struct()
-
-
-def _seal(kv, layout):
-    s = getattr(kv, "_sealed", None)
-    if s is not None and s.key == (layout.dcp_size, layout.block_size, kv.num_blocks,
-                                   kv.bt_rank_stride, kv.max_vb):
-        now = (kv.block_table, *kv.k_pools, *(kv.v_pools or ()))
-        if len(now) == len(s.refs) and all(map(operator.is_, now, s.refs)):
-            return s
-    s = kv._sealed = _Seal(kv, layout)
-    return s
-
-
-@functools.lru_cache(maxsize=256)
-def _tree_ws(dcp, bs, I, B, max_tree, Hq, Hkv, d, dt, dev):
-    n = C.c_size_t(0)
-    _check(load().dcp_tree_workspace_size(Layout(dcp, bs, I), B, max_tree, Hq, Hkv, d, dt,
-                                          C.byref(n)))
-    return n.value
-
+# These calls are short (a few microseconds on the GPU), so their arguments are
+# checked and handed to the C ABI by a native extension (binding/dcp_binding.cpp).
+# Whatever it refuses, and every error of the library, is a DcpError.
 
 def tree_workspace_size(layout, num_reqs, max_tree, num_q_heads, num_kv_heads, head_dim, dtype):
     """Bytes of workspace of tree_decode_gqa and tree_partial_gqa for this shape."""
     if dtype not in _DT:
         raise DcpError(f"unsupported dtype {dtype}")
-    return _tree_ws(layout.dcp_size, layout.block_size, layout.interleave, int(num_reqs),
-                    int(max_tree), int(num_q_heads), int(num_kv_heads), int(head_dim), _DT[dtype],
-                    torch.cuda.current_device() if torch.cuda.is_available() else -1)
-
-
-def _tree_args(layout, q, kv, q_start, ctx_lens, tree_mask, max_tree, workspace, err):
-    dev = _device_of(q, "q")
-    N, Hq, d = _dims(q, 3, "q")
-    s = _seal(kv, layout)
-    if s.dev != dev:
-        raise DcpError(f"the cache is on cuda:{s.dev}, q on cuda:{dev}")
-    if d != s.d or Hq % s.Hkv:
-        raise DcpError(f"q [{N}, {Hq}, {d}] does not fit pools of {s.Hkv} heads of {s.d}")
-    B, = _dims(ctx_lens, 1, "ctx_lens")
-    if s.reqs < B:
-        raise DcpError(f"a block table of {s.reqs} requests, {B} are needed")
-    need = _tree_ws(layout.dcp_size, layout.block_size, layout.interleave, B, int(max_tree), Hq,
-                    s.Hkv, d, s.dt, dev)
-    return (s, dev, N, Hq, d, B, _ptr(q, "q", s.dtype, (N, Hq, d), dev),
-            _ptr(q_start, "q_start", torch.int32, (B + 1,), dev),
-            _ptr(ctx_lens, "ctx_lens", torch.int32, (B,), dev),
-            _ptr(tree_mask, "tree_mask", torch.int64, (N,), dev),
-            *_ws_ptr(workspace, need, dev), _err_ptr(err, dev))
+    n = C.c_size_t(0)
+    _check(load().dcp_tree_workspace_size(layout, num_reqs, max_tree, num_q_heads, num_kv_heads,
+                                          head_dim, _DT[dtype], C.byref(n)))
+    return n.value
 
 
 def tree_decode_gqa(layout, q, kv: PagedKV, q_start, ctx_lens, tree_mask, scale, max_tree,
@@ -714,67 +587,17 @@ def tree_decode_gqa(layout, q, kv: PagedKV, q_start, ctx_lens, tree_mask, scale,
     """Attention of drafted token trees: q [N, Hq, d] holds the nodes of all
     requests, packed; node j of request b is stored at position ctx_lens[b] + j.
     tree_mask [N] int64: bit j = sees node j of its request."""
-    s, dev, N, Hq, d, B, pq, pstart, pctx, pmask, pws, nws, keep, perr = _tree_args(
-        layout, q, kv, q_start, ctx_lens, tree_mask, max_tree, workspace, err)
-    psink = _opt(sink, "sink", torch.float32, (Hq,), dev)
-    if out is None:
-        out = _new_empty((N, Hq, d), dtype=out_dtype or q.dtype, device=q.device)
-    odt = _dtype(out)
-    if out_lse is None:
-        out_lse = _new_empty((N, Hq), dtype=torch.float32, device=q.device)
-    _check(load().dcp_tree_decode_gqa(
-        layout, pq, pstart, N, B, int(max_tree), Hq, s.Hkv, d, float(scale), s.dt, s.struct, pctx,
-        pmask, psink, _ptr(out, "out", out.dtype, (N, Hq, d), dev), odt,
-        _ptr(out_lse, "out_lse", torch.float32, (N, Hq), dev), pws, nws, perr,
-        _cur_stream(stream, dev)))
-    return out, out_lse
+    return (_bind or _load_binding()).tree(
+        False, layout, q, kv, q_start, ctx_lens, tree_mask, scale, max_tree, sink, out_dtype, out,
+        out_lse, workspace, err, stream)
 
 
 def tree_partial_gqa(layout, q, kv: PagedKV, q_start, ctx_lens, tree_mask, scale, max_tree,
                      part_o=None, part_lse=None, workspace=None, err=None, stream=None):
     """tree_decode_gqa's per-rank partials, for lse_merge."""
-    s, dev, N, Hq, d, B, pq, pstart, pctx, pmask, pws, nws, keep, perr = _tree_args(
-        layout, q, kv, q_start, ctx_lens, tree_mask, max_tree, workspace, err)
-    n = layout.dcp_size
-    if part_o is None:
-        part_o = _new_empty((n, N, Hq, d), dtype=torch.float32, device=q.device)
-    if part_lse is None:
-        part_lse = _new_empty((n, N, Hq), dtype=torch.float32, device=q.device)
-    _check(load().dcp_tree_partial_gqa(
-        layout, pq, pstart, N, B, int(max_tree), Hq, s.Hkv, d, float(scale), s.dt, s.struct, pctx,
-        pmask, _ptr(part_o, "part_o", torch.float32, (n, N, Hq, d), dev),
-        _ptr(part_lse, "part_lse", torch.float32, (n, N, Hq), dev), pws, nws, perr,
-        _cur_stream(stream, dev)))
-    return part_o, part_lse
-
-
-def _tokens(t, what, dtype, shape, dev):
-    """Address and elements between tokens of a tensor [tokens, ...] whose
-    tokens are each in one piece (a slice of a wider projection)."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        raise DcpError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, "
-                       f"got {t.dtype}, {tuple(t.shape)}, {t.device}")
-    st = t.stride()
-    d = shape[-1]
-    if (d > 1 and st[-1] != 1) or (len(shape) == 3 and shape[1] > 1 and st[1] != d):
-        raise DcpError(f"{what}: the heads of a token must be in one piece")
-    inner = d if len(shape) == 2 else shape[1] * d
-    return t.data_ptr(), st[0] if shape[0] > 1 else inner
-
-
-def _rope_tables(layout, T, positions, inv_freq, slot, axis, dev):
-    if positions.dim() == 1:
-        axes, shape = 1, (T,)
-    else:
-        axes = _dims(positions, 2, "positions")[0]
-        shape = (axes, T)
-    half, = _dims(inv_freq, 1, "inv_freq")
-    if axis is None and axes > 1:
-        raise DcpError("several axes of positions need `axis`, the axis of each pair")
-    return (_ptr(positions, "positions", torch.int64, shape, dev), axes,
-            _ptr(inv_freq, "inv_freq", torch.float32, (half,), dev),
-            _opt(axis, "axis", torch.int32, (half,), dev), 2 * half,
-            _ptr(slot, "slot", torch.int64, (layout.dcp_size, T), dev))
+    return (_bind or _load_binding()).tree(
+        True, layout, q, kv, q_start, ctx_lens, tree_mask, scale, max_tree, None, None, part_o,
+        part_lse, workspace, err, stream)
 
 
 def rope_write_gqa(layout, q, k, v, positions, inv_freq, slot, k_pools, v_pools, num_blocks,
@@ -782,57 +605,18 @@ def rope_write_gqa(layout, q, k, v, positions, inv_freq, slot, k_pools, v_pools,
                    stream=None):
     """Rotate q and k by their positions and write k, v into the cache at
     `slot`; returns the rotated q.  q, k, v may be slices of one projection."""
-    dev = _device_of(k, "k")
-    dt = k.dtype
-    cdt = _dtype(k)
-    T, Hkv, d = _dims(k, 3, "k")
-    num_blocks = int(num_blocks)
-    pk, sk = _tokens(k, "k", dt, (T, Hkv, d), dev)
-    pv, sv = _tokens(v, "v", dt, (T, Hkv, d), dev)
-    Hq, pq, sq, pqo = 0, None, 0, None
-    if q is not None:
-        Hq = _dims(q, 3, "q")[1]
-        pq, sq = _tokens(q, "q", dt, (T, Hq, d), dev)
-        if q_out is None:
-            q_out = _new_empty((T, Hq, d), dtype=dt, device=k.device)
-        pqo = _ptr(q_out, "q_out", dt, (T, Hq, d), dev)
-    ppos, axes, pinv, pax, rot, pslot = _rope_tables(layout, T, positions, inv_freq, slot, axis,
-                                                     dev)
-    shape = (num_blocks, Hkv, layout.block_size, d)
-    _check(load().dcp_rope_write_gqa(
-        layout, pq, sq, pk, sk, pv, sv, T, Hq, Hkv, d, cdt, ppos, axes, pinv, pax, rot,
-        1 if interleaved else 0, float(scaling), pslot, num_blocks,
-        _rank_list(layout, k_pools, "k_pools", dt, shape, dev),
-        _rank_list(layout, v_pools, "v_pools", dt, shape, dev), pqo,
-        _opt(k_out, "k_out", dt, (T, Hkv, d), dev), _err_ptr(err, dev), _cur_stream(stream, dev)))
-    return q_out
+    return (_bind or _load_binding()).rope(
+        False, layout, q, k, v, positions, inv_freq, slot, k_pools, v_pools, num_blocks, axis,
+        interleaved, scaling, q_out, k_out, err, stream)
 
 
 def rope_write_mla(layout, q, kv, positions, inv_freq, slot, pools, num_blocks, axis=None,
                    interleaved=True, scaling=1.0, q_out=None, err=None, stream=None):
     """Rotate the last entries of q's heads and of the latent rows, and write
     the rows into the cache at `slot`; returns the rotated q."""
-    dev = _device_of(kv, "kv")
-    dt = kv.dtype
-    cdt = _dtype(kv)
-    T, d = _dims(kv, 2, "kv")
-    num_blocks = int(num_blocks)
-    pk, sk = _tokens(kv, "kv", dt, (T, d), dev)
-    Hq, pq, sq, pqo = 0, None, 0, None
-    if q is not None:
-        Hq = _dims(q, 3, "q")[1]
-        pq, sq = _tokens(q, "q", dt, (T, Hq, d), dev)
-        if q_out is None:
-            q_out = _new_empty((T, Hq, d), dtype=dt, device=kv.device)
-        pqo = _ptr(q_out, "q_out", dt, (T, Hq, d), dev)
-    ppos, axes, pinv, pax, rot, pslot = _rope_tables(layout, T, positions, inv_freq, slot, axis,
-                                                     dev)
-    _check(load().dcp_rope_write_mla(
-        layout, pq, sq, pk, sk, T, Hq, d, cdt, ppos, axes, pinv, pax, rot,
-        1 if interleaved else 0, float(scaling), pslot, num_blocks,
-        _rank_list(layout, pools, "pools", dt, (num_blocks, layout.block_size, d), dev), pqo,
-        _err_ptr(err, dev), _cur_stream(stream, dev)))
-    return q_out
+    return (_bind or _load_binding()).rope(
+        True, layout, q, kv, None, positions, inv_freq, slot, pools, None, num_blocks, axis,
+        interleaved, scaling, q_out, None, err, stream)
 
 
 class Pages:
@@ -842,23 +626,21 @@ class Pages:
     table that all ranks share), seq_lens [B] int32, ref_count [T, num_blocks]
     int32, free_bits [T, ceil(num_blocks / 32)] int32.  ``Pages.new`` makes them.
     The decode calls take the table as it is, a shared one as block_table[0].
-    The tensors stay the same ones while the handle is used.
     """
 
     def __init__(self, block_table, seq_lens, ref_count, free_bits, num_blocks):
-        dev = _device_of(block_table, "block_table")
-        self.num_blocks = int(num_blocks)
-        self.tables, self.num_reqs, self.max_vb = _dims(block_table, 3, "block_table")
         self.block_table, self.seq_lens = block_table, seq_lens
         self.ref_count, self.free_bits = ref_count, free_bits
-        self.dev = dev
-        i32 = torch.int32
-        self._struct = PagesStruct(
-            _ptr(block_table, "block_table", i32, block_table.shape, dev),
-            _ptr(seq_lens, "seq_lens", i32, (self.num_reqs,), dev),
-            _ptr(ref_count, "ref_count", i32, (self.tables, self.num_blocks), dev),
-            _ptr(free_bits, "free_bits", i32, (self.tables, (self.num_blocks + 31) // 32), dev),
-            self.num_reqs, self.max_vb, 0, self.num_blocks)
+        self.num_blocks = int(num_blocks)
+        T, B, _ = block_table.shape
+        for t, shape in ((block_table, block_table.shape), (seq_lens, (B,)),
+                         (ref_count, (T, self.num_blocks)),
+                         (free_bits, (T, (self.num_blocks + 31) // 32))):
+            if t.dtype != torch.int32 or t.shape != shape or not t.is_cuda or \
+                    not t.is_contiguous():
+                raise DcpError(f"the pages' state: a contiguous int32 CUDA tensor of shape "
+                               f"{tuple(shape)} is needed, got {t.dtype} {tuple(t.shape)} on "
+                               f"{t.device}")
 
     @classmethod
     def new(cls, layout, num_reqs, max_vblocks, num_blocks, shared=False, device="cuda",
@@ -870,71 +652,26 @@ class Pages:
         pages_init(layout, p, stream=stream)
         return p
 
-    def struct(self, layout) -> PagesStruct:
-        if self.tables == layout.dcp_size:
-            self._struct.bt_rank_stride = self.num_reqs * self.max_vb
-        elif self.tables == 1:
-            self._struct.bt_rank_stride = 0
-        else:
-            raise DcpError(f"{self.tables} block tables for {layout.dcp_size} ranks")
-        return self._struct
-
-
-def _on_current(dev, what):
-    if dev != torch.cuda.current_device():
-        raise DcpError(f"{what} is on cuda:{dev}, but the current device is "
-                       f"cuda:{torch.cuda.current_device()}")
-
 
 def pages_init(layout, pages: Pages, stream=None):
     """Every request unused, every page free."""
-    _on_current(pages.dev, "the pages' state")
-    _check(load().dcp_pages_init(layout, pages.struct(layout), _cur_stream(stream, pages.dev)))
-
-
-@functools.lru_cache(maxsize=256)
-def _pages_ws(dcp, B, max_vb, stride, nb, n):
-    st = PagesStruct(256, 256, 256, 256, B, max_vb, stride, nb)   # only the sizes count
-    need = C.c_size_t(0)
-    _check(load().dcp_pages_workspace_size(Layout(dcp, 1, 1), st, n, C.byref(need)))
-    return need.value
-
-
-def _pages_call(fn, layout, pages, a, b, copy_src, copy_dst, workspace, err, stream):
-    dev, tables, i32 = pages.dev, pages.tables, torch.int32
-    _on_current(dev, "the pages' state")
-    n, = _dims(a, 1, "the list")
-    st = pages.struct(layout)
-    pa, pb = _ptr(a, "the list", i32, (n,), dev), _ptr(b, "the list", i32, (n,), dev)
-    if copy_src is None and copy_dst is None:
-        both = _new_empty((2, tables, n), dtype=i32, device=a.device)
-        copy_src, copy_dst = both[0], both[1]
-    elif copy_src is None:
-        copy_src = torch.empty_like(copy_dst)
-    elif copy_dst is None:
-        copy_dst = torch.empty_like(copy_src)
-    pws, nws, keep = _ws_ptr(workspace, _pages_ws(layout.dcp_size, pages.num_reqs, pages.max_vb,
-                                                  st.bt_rank_stride, pages.num_blocks, n), dev)
-    _check(fn(layout, st, pa, pb, n, _ptr(copy_src, "copy_src", i32, (tables, n), dev),
-              _ptr(copy_dst, "copy_dst", i32, (tables, n), dev), pws, nws, _err_ptr(err, dev),
-              _cur_stream(stream, dev)))
-    return copy_src, copy_dst
+    (_bind or _load_binding()).pages_init(layout, pages, stream)
 
 
 def pages_resize(layout, pages: Pages, req, new_lens, copy_src=None, copy_dst=None, workspace=None,
                  err=None, stream=None):
     """Requests req [n] to lengths new_lens [n]: admit, grow, trim or free.
     Returns (copy_src, copy_dst) [tables, n] for pages_copy."""
-    return _pages_call(load().dcp_pages_resize, layout, pages, req, new_lens, copy_src, copy_dst,
-                       workspace, err, stream)
+    return (_bind or _load_binding()).pages(False, layout, pages, req, new_lens, copy_src, copy_dst,
+                                            workspace, err, stream)
 
 
 def pages_fork(layout, pages: Pages, parent, child, copy_src=None, copy_dst=None, workspace=None,
                err=None, stream=None):
     """child [n] become copies of parent [n]: full pages shared, open ones to
     be copied.  Returns (copy_src, copy_dst) [tables, n] for pages_copy."""
-    return _pages_call(load().dcp_pages_fork, layout, pages, parent, child, copy_src, copy_dst,
-                       workspace, err, stream)
+    return (_bind or _load_binding()).pages(True, layout, pages, parent, child, copy_src, copy_dst,
+                                            workspace, err, stream)
 
 
 class PoolSet:
@@ -948,38 +685,24 @@ class PoolSet:
         if not flat or len({len(p) for p in self.pools}) != 1:
             raise DcpError("a pool set needs pools with one tensor per rank each")
         first = flat[0]
-        self.dev = first.get_device()
-        if self.dev < 0 or first.dim() not in (3, 4):
-            raise DcpError("pools must be CUDA tensors [blocks, heads, block_size, d] or [blocks, "
-                           "block_size, d]")
-        ptrs = [[_ptr(t, "every pool", first.dtype, first.shape, self.dev) for t in p]
-                for p in self.pools]
-        if any(x % 16 for p in ptrs for x in p):
-            raise DcpError("pools must be 16-byte aligned")
+        if first.dim() not in (3, 4):
+            raise DcpError("pools must be [blocks, heads, block_size, d] or [blocks, block_size, d]")
+        for t in flat:
+            if t.dtype != first.dtype or t.shape != first.shape or t.device != first.device or \
+                    not t.is_cuda or not t.is_contiguous() or t.data_ptr() % 16:
+                raise DcpError("the pools of a set must be contiguous, 16-byte aligned CUDA "
+                               "tensors of one type, shape and device")
         self.ranks = len(self.pools[0])
         self.num_blocks, self.block_size = first.shape[0], first.shape[-2]
         self.num_heads = first.shape[1] if first.dim() == 4 else 1
         self.row_bytes = first.shape[-1] * first.element_size()
-        self.ptr = torch.tensor(ptrs, dtype=torch.int64).to(first.device)
-        self._struct = PoolSetStruct(self.ptr.data_ptr(), len(self.pools), self.num_heads,
-                                     self.row_bytes, self.num_blocks)
-
-    def struct(self, layout) -> PoolSetStruct:
-        if self.ranks != layout.dcp_size or self.block_size != layout.block_size:
-            raise DcpError(f"pools of {self.ranks} ranks and {self.block_size}-token pages for "
-                           f"{layout}")
-        return self._struct
+        self.ptr = torch.tensor([[t.data_ptr() for t in p] for p in self.pools],
+                                dtype=torch.int64).to(first.device)
 
 
 def pages_copy(layout, pools: PoolSet, copy_src, copy_dst, err=None, stream=None):
     """Copy pages copy_src -> copy_dst [tables, n] inside every pool (-1: nothing)."""
-    dev = pools.dev
-    _on_current(dev, "the pool set")
-    tables, n = _dims(copy_src, 2, "copy_src")
-    _check(load().dcp_pages_copy(
-        layout, pools.struct(layout), _ptr(copy_src, "copy_src", torch.int32, (tables, n), dev),
-        _ptr(copy_dst, "copy_dst", torch.int32, (tables, n), dev), tables, n, _err_ptr(err, dev),
-        _cur_stream(stream, dev)))
+    (_bind or _load_binding()).pages_copy(layout, pools, copy_src, copy_dst, err, stream)
 
 
 def cache_compact(layout, pools: PoolSet, block_table, num_blocks, ctx_lens, path, path_len,
@@ -988,23 +711,5 @@ def cache_compact(layout, pools: PoolSet, block_table, num_blocks, ctx_lens, pat
     ctx_lens [B], path_len [B] of them) together behind the context, in every
     pool; returns the new lengths [B].  block_table [dcp, B, max_vb], or one
     that all ranks share: [B, max_vb] or [1, B, max_vb]."""
-    dev, i32 = pools.dev, torch.int32
-    _on_current(dev, "the pool set")
-    if int(num_blocks) != pools.num_blocks:
-        raise DcpError(f"num_blocks {num_blocks}, but the pools have {pools.num_blocks}")
-    B, = _dims(ctx_lens, 1, "ctx_lens")
-    most = _dims(path, 2, "path")[1]
-    if new_lens is None:
-        new_lens = torch.empty_like(ctx_lens)
-    shape = block_table.shape
-    if len(shape) not in (2, 3) or shape[-2] < B or \
-            (len(shape) == 3 and shape[0] not in (1, layout.dcp_size)):
-        raise DcpError(f"block_table {tuple(shape)} for {B} requests and {layout}")
-    stride = shape[1] * shape[2] if len(shape) == 3 and shape[0] == layout.dcp_size else 0
-    _check(load().dcp_cache_compact(
-        layout, pools.struct(layout), _ptr(block_table, "block_table", i32, shape, dev), B,
-        shape[-1], stride, _ptr(ctx_lens, "ctx_lens", i32, (B,), dev),
-        _ptr(path, "path", i32, (B, most), dev), _ptr(path_len, "path_len", i32, (B,), dev), most,
-        _ptr(new_lens, "new_lens", i32, (B,), dev), _err_ptr(err, dev),
-        _cur_stream(stream, dev)))
-    return new_lens
+    return (_bind or _load_binding()).cache_compact(layout, pools, block_table, num_blocks,
+                                                    ctx_lens, path, path_len, new_lens, err, stream)

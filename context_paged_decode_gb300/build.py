@@ -1,5 +1,6 @@
 """Build libdcp.so (sm_103a) in-tree with nvcc: one object per .cu, compiled
-in parallel, then linked into a shared library next to this file."""
+in parallel, then linked into a shared library next to this file; and with the
+host compiler the extension that hands tensors to it (_binding.so)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -72,12 +73,42 @@ def build_library(lib=LIB, srcdir=CSRC, name="dcp", verbose=False, extra=()) -> 
     return lib
 
 
-def build_all(verbose=False):
-    out = [build_library(verbose=verbose)]
-    synth_dir = os.path.join(ROOT, "workloads")
-    out.append(build_library(os.path.join(synth_dir, "libdcp_synth.so"), synth_dir, "synth",
-                             verbose=verbose))
+def build_binding() -> str:
+    """Compile the Python extension (against this machine's torch and Python)."""
+    src = os.path.join(HERE, "binding", "dcp_binding.cpp")
+    out = os.path.join(HERE, "_binding.so")
+    if not _stale(out, [src, __file__, *_headers(os.path.join(ROOT, "include"))]):
+        return out
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    if not cxx:
+        raise RuntimeError("g++ not found")
+    inc = [os.path.join(home, "include"), os.path.join(ROOT, "include"),
+           sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
+    libs = os.path.join(home, "lib")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{i}" for i in inc), src, "-o", out + ".tmp", f"-L{libs}", f"-Wl,-rpath,{libs}",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed for the binding:\n{r.stderr}")
+    os.replace(out + ".tmp", out)
     return out
+
+
+def build_all(verbose=False):
+    synth_dir = os.path.join(ROOT, "workloads")
+    with cf.ThreadPoolExecutor(max_workers=3) as ex:
+        jobs = [ex.submit(build_library, verbose=verbose),
+                ex.submit(build_library, os.path.join(synth_dir, "libdcp_synth.so"), synth_dir,
+                          "synth", verbose=verbose),
+                ex.submit(build_binding)]
+        return [j.result() for j in jobs]
 
 
 if __name__ == "__main__":
