@@ -1,0 +1,227 @@
+"""A run of the calls around the decode step together, as a serving loop makes
+them: admit, write prompts, draft, attend, accept, trim, fork, decode on, free.
+What each request has stored is kept on the host, and every attention result is
+compared with plain 64-bit attention over it."""
+import numpy as np
+import pytest
+import torch
+
+from tests import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def dev(x, dtype=np.int32):
+    return torch.from_numpy(np.asarray(x, dtype=dtype)).cuda()
+
+
+class Loop:
+    """Two layers of keys and values, their pages, and the tokens of each request."""
+
+    def __init__(self, lib, dtype, Hq, Hkv, d, dcp, bs, I, reqs, VB, nb, shared, seed):
+        self.lib, self.dtype, self.Hq, self.Hkv, self.d = lib, dtype, Hq, Hkv, d
+        self.geo = dcp, bs, I
+        self.L = lib.Layout(dcp, bs, I)
+        self.nb = nb
+        self.pages = lib.Pages.new(self.L, reqs, VB, nb, shared=shared)
+        shape = (nb, Hkv, bs, d)
+        mk = lambda: [torch.full(shape, float("nan"), dtype=dtype, device="cuda")  # noqa: E731
+                      for _ in range(dcp)]
+        self.k, self.v = [mk() for _ in range(2)], [mk() for _ in range(2)]
+        self.set = lib.PoolSet([*self.k, *self.v])
+        self.table = self.pages.block_table[0] if shared else self.pages.block_table
+        self.kv = [lib.PagedKV(k, v, self.table, nb) for k, v in zip(self.k, self.v)]
+        self.inv = dev(10000.0 ** (-np.arange(d // 2) / (d // 2)), np.float32)
+        self.stored = {}                   # request -> [layer][k or v] list of rows [Hkv, d]
+        self.gen = torch.Generator().manual_seed(seed)
+        self.rng = np.random.default_rng(seed)
+        self.err = torch.zeros(1, dtype=I32, device="cuda")
+
+    def resize(self, reqs, lens):
+        src, dst = self.lib.pages_resize(self.L, self.pages, dev(reqs), dev(lens), err=self.err)
+        self.lib.pages_copy(self.L, self.set, src, dst, err=self.err)
+
+    def write(self, req, at, positions):
+        """Tokens at cache places `at` with rotary `positions`; returns the rotated queries."""
+        T = len(req)
+        _, slot = self.lib.slot_mapping(self.L, dev(req), dev(at, np.int64), self.table, self.nb,
+                                        err=self.err)
+        out = []
+        for layer in range(2):
+            x = torch.randn((T, self.Hq + 2 * self.Hkv, self.d), generator=self.gen)
+            q, k, v = x.to(self.dtype).cuda().split([self.Hq, self.Hkv, self.Hkv], 1)
+            k_out = torch.empty((T, self.Hkv, self.d), dtype=self.dtype, device="cuda")
+            out.append(self.lib.rope_write_gqa(self.L, q, k, v, dev(positions, np.int64), self.inv,
+                                               slot, self.k[layer], self.v[layer], self.nb,
+                                               k_out=k_out, err=self.err))
+            kr, vr = k_out.float().cpu().numpy(), v.float().cpu().numpy()
+            for t, (b, a) in enumerate(zip(req, at)):
+                rows = self.stored.setdefault(b, [[{}, {}], [{}, {}]])[layer]
+                rows[0][a], rows[1][a] = kr[t], vr[t]
+        return out
+
+    def expect(self, layer, req, q, seen, out, lse):
+        """out [T, Hq, d] of queries q [T, Hq, d] that see `seen` [T, tokens] of a request."""
+        rows = self.stored[req][layer]
+        n = seen.shape[1]
+        k, v = (np.stack([rows[i][x] for x in range(n)], 1).astype(np.float64) for i in (0, 1))
+        q = q.double().cpu().numpy()
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for h in range(self.Hq):
+            g = h // (self.Hq // self.Hkv)
+            o, el, wabs, size = R.attend(q[:, h], k[g], v[g], seen, self.d ** -0.5)
+            tol = R.attend_tol(self.dtype, self.dtype, o, wabs, size, self.d, n)
+            assert (np.abs(out[:, h] - o) <= tol).all(), (layer, req, h)
+            assert (np.abs(lse[:, h] - el) <= R.lse_tol(el, size, self.d, n)).all()
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,d,dcp,bs,I,shared", [
+    (BF16, 8, 2, 128, 2, 16, 1, False),
+    (BF16, 8, 2, 64, 3, 32, 8, True),
+    (F32, 4, 2, 64, 4, 16, 16, False),
+])
+def test_a_serving_loop(lib, dtype, Hq, Hkv, d, dcp, bs, I, shared):
+    s = Loop(lib, dtype, Hq, Hkv, d, dcp, bs, I, 8, 12, 200, shared, seed=d + dcp)
+    lens = {0: 37, 1: 1, 2: bs * dcp * 2 + 3}
+    s.resize(list(lens), list(lens.values()))
+    req = [b for b, n in lens.items() for _ in range(n)]
+    at = [x for n in lens.values() for x in range(n)]
+    s.write(req, at, at)
+
+    for step in range(3):
+        # draft: a random tree for each request, stored behind its tokens
+        T = {b: int(s.rng.integers(1, 9)) for b in lens}
+        parent = {b: [-1] + [int(s.rng.integers(max(0, j - 3), j)) for j in range(1, T[b])]
+                  for b in lens}
+        s.resize(list(lens), [lens[b] + T[b] for b in lens])
+        req, at, pos, mask = [], [], [], []
+        for b in lens:
+            bits, depth = [], []
+            for j, p in enumerate(parent[b]):
+                bits.append((bits[p] if p >= 0 else 0) | 1 << j)
+                depth.append(depth[p] + 1 if p >= 0 else 0)
+            req += [b] * T[b]
+            at += [lens[b] + j for j in range(T[b])]
+            pos += [lens[b] + x for x in depth]
+            mask += bits
+        qs = s.write(req, at, pos)
+        # the calls take rows of the block table in order: all requests, some without nodes
+        count = [T.get(b, 0) for b in range(8)]
+        start = np.concatenate([[0], np.cumsum(count)])
+        ctx = [lens.get(b, 0) for b in range(8)]
+        for layer in range(2):
+            out, lse = lib.tree_decode_gqa(s.L, qs[layer], s.kv[layer], dev(start), dev(ctx),
+                                           dev(mask, np.int64), d ** -0.5, 8, err=s.err)
+            for b in lens:
+                rows = slice(int(start[b]), int(start[b + 1]))
+                seen = np.array([[x < lens[b] or (m >> (x - lens[b])) & 1 == 1
+                                  for x in range(lens[b] + T[b])] for m in mask[rows]], dtype=bool)
+                s.expect(layer, b, qs[layer][rows], seen, out[rows], lse[rows])
+        # accept a path from the root, and drop the rest
+        path = np.full((8, 8), -1, dtype=np.int32)
+        kept = [0] * 8
+        for b in lens:
+            node, got = 0, [0]
+            while True:
+                nxt = [j for j in range(T[b]) if parent[b][j] == node]
+                if not nxt or s.rng.random() < 0.2:
+                    break
+                node = nxt[int(s.rng.integers(len(nxt)))]
+                got.append(node)
+            path[b, :len(got)], kept[b] = got, len(got)
+            for layer in s.stored[b]:
+                for rows in layer:
+                    new = {i: rows[lens[b] + j] for i, j in enumerate(got)}
+                    for i, r in new.items():
+                        rows[lens[b] + i] = r
+        new = lib.cache_compact(s.L, s.set, s.table, s.nb, dev(ctx), dev(path), dev(kept),
+                                err=s.err)
+        for b in lens:
+            lens[b] += kept[b]
+        assert new.tolist() == [lens.get(b, 0) for b in range(8)]
+        s.resize(list(lens), list(lens.values()))
+
+    # two samples of request 2 and one of request 0, then every request goes on by itself
+    src, dst = lib.pages_fork(s.L, s.pages, dev([2, 2, 0]), dev([5, 6, 7]), err=s.err)
+    lib.pages_copy(s.L, s.set, src, dst, err=s.err)
+    import copy
+    for child, p in ((5, 2), (6, 2), (7, 0)):
+        lens[child] = lens[p]
+        s.stored[child] = copy.deepcopy(s.stored[p])
+    for _ in range(2):
+        order = sorted(lens)
+        s.resize(order, [lens[b] + 1 for b in order])
+        qs = s.write(order, [lens[b] for b in order], [lens[b] for b in order])
+        for b in order:
+            lens[b] += 1
+        full = torch.zeros((8, Hq, d), dtype=dtype, device="cuda")
+        seq = dev([lens.get(b, 0) for b in range(8)])
+        for layer in range(2):
+            full[order] = qs[layer]
+            out, lse = lib.decode_gqa(s.L, full, s.kv[layer], lib.local_seq_lens(s.L, seq),
+                                      d ** -0.5, err=s.err)
+            one, l1 = lib.tree_decode_gqa(
+                s.L, full, s.kv[layer], dev(np.arange(9)), seq - 1 * (seq > 0).int(),
+                torch.ones(8, dtype=torch.int64, device="cuda"), d ** -0.5, 1, err=s.err)
+            for i, b in enumerate(order):
+                seen = np.ones((1, lens[b]), dtype=bool)
+                s.expect(layer, b, qs[layer][i:i + 1], seen, out[b:b + 1], lse[b:b + 1])
+                s.expect(layer, b, qs[layer][i:i + 1], seen, one[b:b + 1], l1[b:b + 1])
+    # a request that has no pages (rows 3 and 4) looked for its own node's page above
+    missing = s.err.item()
+    s.resize(list(range(8)), [0] * 8)
+    assert s.err.item() == missing
+    assert (s.pages.ref_count == 0).all() and (s.pages.seq_lens == 0).all()
+    assert (s.pages.block_table == -1).all()
+
+
+def test_a_step_in_a_graph(lib):
+    """Rotary write, attention and compaction of a step, captured and replayed on new inputs."""
+    Hq, Hkv, d, dcp, bs, B, T, ctx0 = 8, 2, 128, 2, 16, 3, 4, 40
+    L = lib.Layout(dcp, bs, 1)
+    rng = np.random.default_rng(3)
+    bt, nb = R.random_tables(rng, [200] * B, dcp, bs)
+    base = torch.randn((2, dcp, nb, Hkv, bs, d), generator=torch.Generator().manual_seed(1)).to(BF16)
+    pools = base.cuda()
+    table = dev(bt)
+    kv = lib.PagedKV(list(pools[0]), list(pools[1]), table, nb)
+    pset = lib.PoolSet([list(pools[0]), list(pools[1])])
+    x = torch.empty((B * T, Hq + 2 * Hkv, d), dtype=BF16, device="cuda")
+    q, k, v = x.split([Hq, Hkv, Hkv], 1)
+    inv = dev(10000.0 ** (-np.arange(64) / 64), np.float32)
+    ctx = torch.empty(B, dtype=I32, device="cuda")
+    req = dev(np.repeat(np.arange(B), T))
+    node = dev(np.tile(np.arange(T), B), np.int64)
+    start, path, n = dev(np.arange(B + 1) * T), dev([[0, 2], [1, 3], [3, 0]]), dev([2, 2, 1])
+    mask = dev(np.tile([1, 3, 5, 13], B), np.int64)
+
+    def step():
+        at = ctx.long().repeat_interleave(T) + node
+        _, slot = lib.slot_mapping(L, req, at, table, nb)
+        qr = lib.rope_write_gqa(L, q, k, v, at, inv, slot, list(pools[0]), list(pools[1]), nb)
+        out, lse = lib.tree_decode_gqa(L, qr, kv, start, ctx, mask, d ** -0.5, T)
+        return out, lse, lib.cache_compact(L, pset, table, nb, ctx, path, n)
+
+    ctx.fill_(ctx0)
+    x.copy_(torch.randn(x.shape))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for lens in ([40, 0, 7], [150, 33, 64], [1, 2, 3]):
+        ctx.copy_(torch.tensor(lens, dtype=I32))
+        x.copy_(torch.randn(x.shape))
+        pools.copy_(base)
+        g.replay()
+        after = pools.clone(), [t.clone() for t in got]
+        pools.copy_(base)
+        want = step()
+        for a, b in zip(after[1], want):
+            assert torch.equal(a, b)
+        assert torch.equal(after[0], pools)
