@@ -23,9 +23,7 @@ namespace dcp {
 constexpr int kTreePlanThreads = 256;
 
 // One CTA: checks the requests, counts each entry's tiles and units, sums them
-// up, and finds each run's first entry.  A unit counts as up to A.extra tiles
-// more than it has, but no more than a run would have: small calls spread their
-// tiles over all CTAs.
+// up, and finds each run's first entry.
 __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __grid_constant__ TreeArgs A) {
   __shared__ int64_t sh_t[kTreePlanThreads / 32], sh_u[kTreePlanThreads / 32];
   __shared__ int64_t s_end[kTreePlanThreads];   // tiles up to each entry of the block
@@ -44,27 +42,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __gri
       const int e = e0 + tid;
       TreeEntry n;
       n.units = n.per = n.nodes = n.ctx = n.q0 = n.pad = 0;
-      if (e < E) {
-        const int b = A.per_rank ? e / A.L.dcp : e, r = A.per_rank ? e % A.L.dcp : 0;
-        const int q0 = __ldcg(A.q_start + b), q1 = __ldcg(A.q_start + b + 1);
-        const int64_t ctx = __ldcg(A.ctx + b);
-        int T = q1 - q0;
-        if (q0 < 0 || q1 < q0 || q1 > A.N || T > A.max_tree || ctx < 0 ||
-            ctx + T > (int64_t)A.max_vb * A.L.bs * A.L.dcp) {
-          if (r == 0 && round == 1) count_error(A.err);
-          T = 0;
-        }
-        if (T > 0) {
-          const int r1 = A.per_rank ? r + 1 : A.L.dcp;
-          const TreeLen len((int)ctx + T, A.L);
-          for (int x = r; x < r1; ++x) n.per += (len.on(x, A.L) + A.chunk - 1) / A.chunk;
-          n.per = (n.per + A.tile / A.chunk - 1) / (A.tile / A.chunk);
-          if (n.per > 0) n.units = A.Hkv * ((T * A.G + A.rows - 1) / A.rows);
-          n.nodes = T;
-          n.ctx = (int)ctx;
-          n.q0 = q0;
-        }
-      }
+      if (e < E) n = tree_request(A, e, round == 1);
       int64_t t = (int64_t)n.units * n.per, u = n.units;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -94,8 +72,7 @@ __global__ void __launch_bounds__(kTreePlanThreads) tree_plan_kernel(const __gri
       }
       if (round == 0) continue;
       const int64_t sum_t = single ? tiles : all_t, sum_u = single ? units : all_u;
-      extra = sum_t / A.parts;
-      if (extra > A.extra) extra = A.extra;
+      extra = tree_extra(A, sum_t);
       total = sum_t + extra * sum_u;
       const int64_t end = t + extra * u;
       n.tile0 = end - n.units * (n.per + extra);
@@ -199,6 +176,7 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
   __shared__ int64_t s_row[kTgTile];   // K/V row of a token, -1: not there
   __shared__ int s_code[kTgTile];      // node, 64: seen by all, 255: by none
   __shared__ int s_odd;                // a node's value is not finite
+  __shared__ TreeSelf s_plan;
   constexpr int kRows = kTgWarps * RW;
   const int d = A.d, ks = d + kTgPad, d4 = d >> 2;
   float* sq = smf;                     // [rows][d]
@@ -208,8 +186,12 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float* pw = sk + warp * kTgTile * RW;   // [warp][tile][RW]
+  if (A.self) {
+    if (warp == 0) tree_self_plan(A, &s_plan);
+    __syncthreads();
+  }
   for (int run = blockIdx.x; run < A.parts; run += gridDim.x) {
-    TreeWalk walk = tree_walk(A, run);
+    TreeWalk walk = tree_walk(A, run, A.self ? &s_plan : nullptr);
     TreePiece p;
     while (tree_next(A, walk, p)) {
       const int ctx = p.ctx;
@@ -635,7 +617,8 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
   // and the merge's warps join them faster than one CTA would (GPU time, 32 x 16
   // nodes over up to 4096 tokens: 77 us against 79 and a launch less; 16 x 5
   // nodes on one key head: 45 us against 20).
-  A.join = tc && (int64_t)B * Hkv * (per_rank ? layout.dcp_size : 1) >= S.parts ? 1 : 0;
+  A.self = (per_rank ? (int64_t)B * layout.dcp_size : (int64_t)B) <= kTreeSelf ? 1 : 0;
+  A.join = tc && !A.self && (int64_t)B * Hkv * (per_rank ? layout.dcp_size : 1) >= S.parts ? 1 : 0;
   A.sl2 = scale * kLog2e;
   A.k = kv.k;
   A.v = kv.v;
@@ -650,7 +633,8 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
   A.err = err;
   const size_t need = tree_carve(&A, ws, B, layout.dcp_size, S.parts, S.rows, d);
   if (!ws || ws_bytes < need) return DCP_EWORKSPACE;
-  cudaError_t e = launch_chained(tree_plan_kernel, 1, kTreePlanThreads, 0, s, A);
+  cudaError_t e = cudaSuccess;
+  if (!A.self) e = launch_chained(tree_plan_kernel, 1, kTreePlanThreads, 0, s, A);
   if (e != cudaSuccess) return launch_status_report(e);
   const int rc = tc                 ? launch_tree_tc(A, s)
                  : dtype == DCP_F32 ? launch_tree_generic<float>(A, s)

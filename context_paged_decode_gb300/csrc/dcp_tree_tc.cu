@@ -69,7 +69,8 @@ struct TreeTc {
   static constexpr int kQOff = kVOff + kVSlots * kSlot;
   static constexpr int kMlOff = kQOff + kQ;                 // float2 [2 stream][128]
   static constexpr int kFlagOff = kMlOff + 2 * 128 * 8;     // int [2 parity], joins
-  static constexpr int kBarOff = kFlagOff + 16;
+  static constexpr int kPlanOff = kFlagOff + 32;            // TreeSelf
+  static constexpr int kBarOff = kPlanOff + (int)sizeof(TreeSelf);
   static constexpr int kBars = 2 * (kKSlots + kVSlots) + 8;
   static constexpr int kSmem = kBarOff + 8 * kBars + 16;
   static constexpr uint32_t kColS = 0, kColO = 256;         // two of each, 128 and D apart
@@ -322,8 +323,13 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
   const uint32_t tmem = *tmem_slot;
   griddep_wait();   // the plan, and what the calls before wrote
 
+  TreeSelf* own_plan = reinterpret_cast<TreeSelf*>(smem + C::kPlanOff);
+  if (A.self) {
+    if (warp == 0) tree_self_plan(A, own_plan);
+    __syncthreads();
+  }
   int32_t* errp = A.err ? A.err : A.hdr + 1;
-  TreeWalk walk = tree_walk(A, blockIdx.x);
+  TreeWalk walk = tree_walk(A, blockIdx.x, A.self ? own_plan : nullptr);
   const int srows = X.nodes * A.G;   // rows of a stream's query tile
   auto block_rows = [&](const TreePiece& p) { return min(A.rows, p.T * A.G - p.rb * A.rows); };
 
