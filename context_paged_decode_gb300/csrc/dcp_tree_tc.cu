@@ -112,6 +112,24 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// Of each eight lanes, lane i's piece j (four registers) goes to lane j's piece i.
+__device__ __forceinline__ void transpose8(uint32_t (&x)[32], int lane) {
+#pragma unroll
+  for (int b = 1; b < 8; b <<= 1) {
+    const bool up = lane & b;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!(j & b)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t &lo = x[4 * j + i], &hi = x[4 * (j | b) + i];
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, b);
+          if (up) lo = got; else hi = got;
+        }
+      }
+  }
+}
+
 __device__ __forceinline__ bool bf16_odd(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
 // Adds to output row `row` (columns [c0, c1)) what it sees of non-finite values
@@ -344,7 +362,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       const uint32_t full = val ? b_v : b_k, free = val ? b_vfree : b_kfree;
       const uint32_t ring = sbase + (val ? C::kVOff : 0) + lane * kTtChunk * 128;
       const CUtensorMap* maps = val ? X.vmap : X.kmap;
-      uint32_t slot = 0, par = 1;
+      uint32_t slot = 0, par = 1, loaded = 0;
       bool dead = false;
       TreePiece p;
       while (!dead && tree_next(A, walk, p)) {
@@ -406,8 +424,12 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
             slot = 0;
             par ^= 1;
           }
+          ++loaded;
         }
       }
+      // nothing may still be on its way when the CTA ends, whoever gave up
+      for (uint32_t t = loaded < (uint32_t)slots ? 0 : loaded - slots; t < loaded; ++t)
+        mbar_wait(full + 8 * (t % slots), (t / slots) & 1);
       if (dead && lane == 0) atomicAdd(errp, kTtStuck);
     } else if (warp == 3) {
       // ---------------- queries ----------------
@@ -430,6 +452,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
                           p.g * A.G, node + s * X.nodes, b_q);
           ++item;
         }
+        if (item > 0) mbar_wait(b_q, (item - 1) & 1);
         if (dead) atomicAdd(errp, kTtStuck);
       }
     } else {
@@ -445,12 +468,21 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       uint32_t item = 0, np0 = 0, np1 = 0;
       bool dead = false;
       auto wait = [&](uint32_t bar, uint32_t par) {
-        if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar, par))) dead = true;
+        if (dead) return false;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, par))) return true;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar, par))) dead = true;
         return !dead;
       };
+      // A wait for what is there already still takes this warp 150 to 250
+      // cycles beside the softmax, so a tile's keys and values are waited for
+      // before P is, on which the softmax of the next tile hangs (64 nodes over
+      // 65536 tokens: 75.5 us, 77.0 the other way round), and a wait tries once
+      // before it loops (73.4).
+      auto have_k = [&]() { wait(b_k + 8 * ks, kp); };
+      auto have_v = [&]() { wait(b_v + 8 * vs, vp); };
       // scores of the ring's next tile into stream s; `last`: its last reader
       auto qk = [&](int s, bool last) {
-        if (!wait(b_k + 8 * ks, kp)) return;
+        if (dead) return;
         tc_fence_after();
         const uint64_t a = sdesc_sw128(sbase + C::kQOff + (kTwo ? s * C::kSlot : 0), 0, 1024);
         const uint64_t b = sdesc_sw128(sbase + ks * C::kSlot, 0, 1024);
@@ -469,7 +501,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
         }
       };
       auto pv = [&](int s, bool first, bool last) {
-        if (!wait(b_p + 8 * s, (s ? np1 : np0) & 1) || !wait(b_v + 8 * vs, vp)) return;
+        if (!wait(b_p + 8 * s, (s ? np1 : np0) & 1)) return;
         if (s) ++np1; else ++np0;
         tc_fence_after();
         const uint64_t v = sdesc_sw128(sbase + C::kVOff + vs * C::kSlot, kHalfBytes, 1024);
@@ -493,17 +525,23 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
 #pragma unroll 1
           for (int k = 0; k <= n && !dead; ++k) {
             if (k < n) {
+              have_k();
               qk(k & 1, true);
               if (k == n - 1) tc_commit_elect(b_qfree);
             }
             if (k == 1) wait(b_ofree, (item & 1) ^ 1);
-            if (k > 0) pv((k - 1) & 1, k <= 2, true);
+            if (k > 0) {
+              have_v();
+              pv((k - 1) & 1, k <= 2, true);
+            }
           }
         } else {
           const int streams = __shfl_sync(0xffffffffu, block_rows(p) > srows ? 2 : 1, 0);
 #pragma unroll 1
           for (int k = 0; k <= n && !dead; ++k) {
             if (k == 1) wait(b_ofree, (item & 1) ^ 1);
+            if (k > 0) have_v();
+            if (k < n) have_k();
 #pragma unroll 1
             for (int s = 0; s < streams; ++s) {
               if (k > 0) pv(s, k == 1, s + 1 == streams);
@@ -513,6 +551,11 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
           }
         }
         if (!dead) tc_commit_elect(b_o);
+      }
+      if (dead) {   // the products issued so far come to an end first
+        tc_commit_elect(b_o);
+        mbar_wait(b_o, (item - 1) & 1);
+        __syncwarp();
       }
       if (dead && lane == 0) atomicAdd(errp, kTtStuck);
     }
@@ -788,7 +831,21 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
             if (other && fb != 0.f) v = fmaf(__uint_as_float(y[i]), fb, v);
             x[i] = __float_as_uint(v);
           }
-          if (real) {
+          if (kTwo && !direct) {
+            // eight lanes exchange pieces so that they write 128 bytes of a row
+            // at a time: 64 nodes over 65536 tokens 71.2 us, 73.4 when each lane
+            // writes its own row.  With half of the rows the exchange's cold
+            // instructions cost as much (8 nodes over 1500 tokens 16.0 and 15.3).
+            transpose8(x, lane);
+            float* part = A.part_o + ((int64_t)p.slot * A.rows + srow0) * D + c + 4 * (lane & 7);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int to_row = quarter * 32 + (lane & 24) + i;
+              if (to_row < have)
+                *reinterpret_cast<uint4*>(part + to_row * D) =
+                    make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+          } else if (real) {
             if (f32) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
@@ -807,6 +864,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
             }
           }
         }
+        if (kTwo && odd) __syncwarp();
         if (real) {
           if (odd) tree_fix<D>(A, p, urow, c0, c1, M, f, dst, f32);
           if (kTwo || s == 0) {
