@@ -15,9 +15,11 @@
 // order does not matter; two that a request's release and another's share one
 // page are both counted before any page is taken.
 //
-// One cluster of eight CTAs runs each table from end to end, separated by two
-// or three cluster barriers; a small second launch stores the lengths, which
-// every table reads.  What bounds it: latency.  So each CTA checks the whole
+// Clusters of eight CTAs run the tables from end to end, with two or three
+// cluster barriers: one for all tables if the work is small, whose CTAs are
+// divided among them, else one for each.  One cluster stores the lengths,
+// which every table reads, itself, after its first barrier; several leave that
+// to a small second launch.  What bounds it: latency.  So each CTA checks the whole
 // list for itself in shared memory (a hash of the requests finds names that
 // come twice, and children that are parents) rather than ask the others, and
 // pages are handed out 32 at a time, a lane per bit of the bitmap.  (With the
@@ -31,10 +33,13 @@ namespace dcp {
 
 constexpr int kPgCluster = 8;
 constexpr int kPgThreads = 512;
-constexpr int kPgAll = kPgCluster * kPgThreads;   // threads of a table
-
-constexpr int kPgWarps = kPgAll / 32;
 constexpr int kPgMaxList = 2048;
+// Most table columns (and 32 for each list entry) of a CTA for one cluster to do
+// all tables.  Free, fork, copy and grow of 4 requests of 33 columns on 2 ranks
+// take 25.3 us so and 28.9 us with a cluster for each, 16 requests of 252
+// columns on 8 ranks (4544 to a CTA) 33.1 and 36.0; but 32 such requests (9088)
+// 48.6 and 41.8, 128 of 33 columns (8320) 63.0 and 46.2.
+constexpr int64_t kPgSmall = 5120;
 
 struct PagesArgs {
   Layout L;
@@ -44,6 +49,8 @@ struct PagesArgs {
   int64_t nb;
   int words;           // of the bitmap
   int shared;          // one table for every rank
+  int tables, per;     // CTAs of each: kPgCluster, or a power of two below
+  int alone;           // one cluster does everything
   int32_t* seq;
   int32_t* ref;
   uint32_t* bits;
@@ -137,11 +144,12 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
   __shared__ int s_any;
   griddep_launch_dependents();   // the next call's first kernel may start its launch
   griddep_wait();                // launched chained: the preceding kernel completed
-  const int table = blockIdx.x / kPgCluster;
-  const int cta = (int)cluster_ctarank();
+  const int table = blockIdx.x / A.per, cta = blockIdx.x % A.per;
   const int tid = threadIdx.x, lane = tid & 31;
   const int gw = cta * (kPgThreads / 32) + (tid >> 5);   // warp of the table
-  const int N = A.N, vbs = A.L.bs * A.L.dcp;
+  const int warps = A.per * (kPgThreads / 32);           // and how many it has
+  const bool spare = table >= A.tables;                  // a CTA too many keeps step
+  const int N = spare ? 0 : A.N, words = spare ? 0 : A.words, vbs = A.L.bs * A.L.dcp;
   int32_t* bt = A.bt + table * A.stride;
   int32_t* ref = A.ref + (int64_t)table * A.nb;
   uint32_t* bits = A.bits + (int64_t)table * A.words;
@@ -195,7 +203,7 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
     S.len[n] = ok ? len : -1;
     if (table == 0 && cta == 0) {
       if (!ok) count_error(A.err);
-      A.new_len[n] = ok ? len : -1;
+      if (!A.alone) A.new_len[n] = ok ? len : -1;
     }
   }
   __syncthreads();   // (the hash is read for the last time above)
@@ -203,8 +211,8 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
   // Releases, and for a fork the pages that the child shares with its parent.
   // The parent holds those throughout, so no release can free one.  `share`
   // warps take turns on an entry where there are few.
-  const int share = N < kPgWarps ? kPgWarps / N : 1;
-  for (int n = gw / share; n < N; n += kPgWarps / share) {
+  const int share = N > 0 && N < warps ? warps / N : 1;
+  for (int n = gw / share; n < N; n += warps / share) {
     const int len = S.len[n];
     if (len < 0) continue;
     int32_t* row = bt + (int64_t)S.c[n] * A.max_vb;
@@ -240,6 +248,9 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
     }
   }
   cluster_sync();
+  if (A.alone && blockIdx.x == 0)   // every table has read the old lengths
+    for (int n = tid; n < N; n += kPgThreads)
+      if (S.len[n] >= 0) A.seq[S.c[n]] = S.len[n];
 
   // what each entry needs, summed up by every CTA for itself
   int W = 0;
@@ -262,26 +273,26 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
       S.need[n] = need << 1 | again;
       S.page[n] = page;
       if (again) s_any = 1;
-      if (n / kPgThreads % kPgCluster == cta) src[n] = dst[n] = -1;
+      if (n / kPgThreads % A.per == cta) src[n] = dst[n] = -1;
     }
     W += sum;
   }
   if (tid == 0) S.first[N] = W;
   // free pages of this warp's words
-  const int per = (A.words + kPgWarps - 1) / kPgWarps;
-  const int w0 = min(gw * per, A.words), w1 = min(w0 + per, A.words);
+  const int each = (words + warps - 1) / warps;
+  const int w0 = min(gw * each, words), w1 = min(w0 + each, words);
   int mine = 0, sum;
   for (int i = w0 + lane; i < w1; i += 32) mine += __popc(__ldcg(bits + i));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   int base = pg_scan(lane == 0 ? mine : 0, sh, &sum);
   base = __shfl_sync(0xffffffffu, base, 0);
-  if (tid == 0) A.sums[table * kPgCluster + cta] = sum;
+  if (tid == 0) A.sums[blockIdx.x] = sum;
   cluster_sync();
 
   int have = 0;
-  for (int i = 0; i < kPgCluster; ++i) {
-    const int s = __ldcg(A.sums + table * kPgCluster + i);
+  for (int i = 0; i < A.per; ++i) {
+    const int s = __ldcg(A.sums + table * A.per + i);
     if (i < cta) base += s;
     have += s;
   }
@@ -329,14 +340,14 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
       base += __popc(word);
     }
   }
-  for (int k = have + cta * kPgThreads + tid; k < W; k += kPgAll) {   // no page left
+  for (int k = have + cta * kPgThreads + tid; k < W; k += warps * 32) {   // no page left
     count_error(A.err);
     give(k, -1);
   }
-  if (!kFork && s_any) {   // (the same in every CTA)
+  if (!kFork && (s_any || A.per < kPgCluster)) {   // (the same in a table's CTAs)
     // the shared open pages that were replaced, one holder less
     cluster_sync();
-    for (int n = cta * kPgThreads + tid; n < N; n += kPgAll)
+    for (int n = cta * kPgThreads + tid; n < N; n += warps * 32)
       if (S.need[n] & 1) release_page(A, ref, bits, S.page[n]);
   }
 }
@@ -415,6 +426,11 @@ static int launch_pages(const dcp_layout_t& L, const dcp_pages_t& p, const int32
   A.up = up;
   A.row = row;
   A.len = len;
+  A.tables = tables;
+  A.per = kPgCluster;
+  while (A.per > 0 && A.per * tables > kPgCluster) A.per /= 2;
+  A.alone = tables == 1 || (int64_t)N * (p.max_vblocks + 32) <= kPgSmall * A.per;
+  if (!A.alone) A.per = kPgCluster;
   A.N = N;
   A.hash = 64;
   while (A.hash < 2 * N) A.hash *= 2;
@@ -426,9 +442,10 @@ static int launch_pages(const dcp_layout_t& L, const dcp_pages_t& p, const int32
   if (!ws || ws_bytes < pages_ws_bytes(N)) return DCP_EWORKSPACE;
   const size_t smem = pages_smem(N, A.hash);
   if (!allow_smem<pages_kernel<kFork>>()) return DCP_ECUDA;
-  cudaError_t e = launch_chained(pages_kernel<kFork>, (unsigned)(tables * kPgCluster), kPgThreads,
-                                 smem, s, A);
+  const unsigned ctas = A.alone ? kPgCluster : (unsigned)(tables * kPgCluster);
+  cudaError_t e = launch_chained(pages_kernel<kFork>, ctas, kPgThreads, smem, s, A);
   if (e != cudaSuccess) return launch_status_report(e);
+  if (A.alone) return launch_status();
   const unsigned grid = (unsigned)((N + 255) / 256 < 64 ? (N + 255) / 256 : 64);
   e = launch_chained(pages_lens_kernel, grid, 256, 0, s, A);
   if (e != cudaSuccess) return launch_status_report(e);
