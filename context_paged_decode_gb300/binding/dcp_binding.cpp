@@ -9,12 +9,14 @@
 #include <Python.h>
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <string>
 
 #include "dcp.h"
@@ -143,10 +145,22 @@ int device_of(const at::Tensor& t, const char* what) {
   return dev;
 }
 
-dcp_stream_t stream_of(PyObject* o, int dev) {
-  if (o == Py_None) return (dcp_stream_t)c10::cuda::getCurrentCUDAStream(dev).stream();
-  return (dcp_stream_t)(uintptr_t)integer_attr(o, "cuda_stream");
-}
+// The stream that a call runs on.  What the call allocates is allocated for that
+// stream too: memory of another one may still be in use by work queued there.
+struct OnStream {
+  std::optional<c10::cuda::CUDAStreamGuard> guard;
+  dcp_stream_t st;
+  OnStream(PyObject* o, int dev) {
+    if (o == Py_None) {
+      st = (dcp_stream_t)c10::cuda::getCurrentCUDAStream(dev).stream();
+      return;
+    }
+    if (PyObject_HasAttrString(o, "device_index") && integer_attr(o, "device_index") != dev)
+      refuse("the stream is on another device than the tensors");
+    st = (dcp_stream_t)(uintptr_t)integer_attr(o, "cuda_stream");
+    guard.emplace(c10::cuda::getStreamFromExternal((cudaStream_t)st, dev));
+  }
+};
 
 dcp_dtype_t dtype_of(at::ScalarType t) {
   if (t == at::kFloat) return DCP_F32;
@@ -233,6 +247,7 @@ PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const dcp_layout_t L = layout_of(a[1]);
     const at::Tensor& q = tensor(a[2], "q");
     const int dev = device_of(q, "q");
+    const OnStream on(a[15], dev);
     if (q.dim() != 3) refuse("q must be [tokens, heads, head_dim]");
     const int64_t N = q.size(0), Hq = q.size(1), d = q.size(2);
     const at::ScalarType type = q.scalar_type();
@@ -304,15 +319,16 @@ PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor out, lse;
     if (a[11] == Py_None) out = fresh(os, odt, dev);
     if (a[12] == Py_None) lse = fresh(ls, at::kFloat, dev);
-    const char* on = partial ? "part_o" : "out";
-    const char* ln = partial ? "part_lse" : "out_lse";
-    void* po = a[11] == Py_None ? out.data_ptr() : ptr(a[11], on, odt, os, dev);
-    float* pl = (float*)(a[12] == Py_None ? lse.data_ptr() : ptr(a[12], ln, at::kFloat, ls, dev));
-    dcp_stream_t st = stream_of(a[15], dev);
+    const char* oname = partial ? "part_o" : "out";
+    const char* lname = partial ? "part_lse" : "out_lse";
+    void* po = a[11] == Py_None ? out.data_ptr() : ptr(a[11], oname, odt, os, dev);
+    float* pl =
+        (float*)(a[12] == Py_None ? lse.data_ptr() : ptr(a[12], lname, at::kFloat, ls, dev));
     check(partial ? g_lib.tree_partial_gqa(L, pq, start, n32, b32, most, hq, hkv, d32, scale, dt, c,
-                                           pctx, mask, (float*)po, pl, ws.p, ws.bytes, err, st)
+                                           pctx, mask, (float*)po, pl, ws.p, ws.bytes, err, on.st)
                   : g_lib.tree_decode_gqa(L, pq, start, n32, b32, most, hq, hkv, d32, scale, dt, c,
-                                          pctx, mask, sink, po, codt, pl, ws.p, ws.bytes, err, st));
+                                          pctx, mask, sink, po, codt, pl, ws.p, ws.bytes, err,
+                                          on.st));
     PyObject* both = PyTuple_New(2);
     if (!both) return nullptr;
     PyTuple_SET_ITEM(both, 0, a[11] == Py_None ? THPVariable_Wrap(out) : given(a[11]));
@@ -346,6 +362,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const char* kn = latent ? "kv" : "k";
     const at::Tensor& k = tensor(a[3], kn);
     const int dev = device_of(k, kn);
+    const OnStream on(a[17], dev);
     const at::ScalarType type = k.scalar_type();
     const dcp_dtype_t dt = dtype_of(type);
     if (k.dim() != (latent ? 2 : 3))
@@ -391,19 +408,18 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t inter = truth(a[12]) ? 1 : 0;
     const float scaling = (float)number(a[13]);
     int32_t* err = err_ptr(a[16], dev);
-    dcp_stream_t st = stream_of(a[17], dev);
     if (latent) {
       const int64_t shape[3] = {nb, L.block_size, d};
       check(g_lib.rope_write_mla(L, pq, sq, pk, sk, T, hq, d32, dt, ppos, ax32, pinv, pax, rot,
                                  inter, scaling, slot, nb,
-                                 rank_list(L, a[8], "pools", type, shape, dev), pqo, err, st));
+                                 rank_list(L, a[8], "pools", type, shape, dev), pqo, err, on.st));
     } else {
       const int64_t shape[4] = {nb, Hkv, L.block_size, d};
       check(g_lib.rope_write_gqa(
           L, pq, sq, pk, sk, pv, sv, T, hq, small(Hkv, "heads"), d32, dt, ppos, ax32, pinv, pax,
           rot, inter, scaling, slot, nb, rank_list(L, a[8], "k_pools", type, shape, dev),
           rank_list(L, a[9], "v_pools", type, shape, dev), pqo,
-          opt(a[15], "k_out", type, k.sizes(), dev), err, st));
+          opt(a[15], "k_out", type, k.sizes(), dev), err, on.st));
     }
     if (a[2] == Py_None) return given(Py_None);
     return q_out == Py_None ? THPVariable_Wrap(own) : given(q_out);
@@ -419,6 +435,7 @@ dcp_pages_t pages_of(PyObject* o, const dcp_layout_t& L, int& dev, int64_t& tabl
   if (bt.dim() != 3) refuse("block_table must be [tables, requests, max_vblocks]");
   tables = bt.size(0);
   const int64_t B = bt.size(1), VB = bt.size(2), nb = integer_attr(o, "num_blocks");
+  if (B * VB == 0) refuse("block_table has no entries");
   if (tables != 1 && tables != L.dcp_size)
     refuse(std::to_string(tables) + " block tables for " + std::to_string(L.dcp_size) + " ranks");
   dcp_pages_t p = {};
@@ -441,7 +458,7 @@ PyObject* pages_init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int dev;
     int64_t tables;
     const dcp_pages_t p = pages_of(a[1], L, dev, tables);
-    check(g_lib.pages_init(L, p, stream_of(a[2], dev)));
+    check(g_lib.pages_init(L, p, OnStream(a[2], dev).st));
     return given(Py_None);
   });
 }
@@ -455,6 +472,7 @@ PyObject* pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int dev;
     int64_t tables;
     const dcp_pages_t p = pages_of(a[2], L, dev, tables);
+    const OnStream on(a[9], dev);
     const at::Tensor& x = tensor(a[3], "the list");
     if (x.dim() != 1) refuse("the list must have one dimension");
     const int64_t N = x.size(0);
@@ -473,7 +491,7 @@ PyObject* pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* pd = (int32_t*)(a[6] == Py_None ? dst.data_ptr()
                                              : ptr(a[6], "copy_dst", at::kInt, {tables, N}, dev));
     check((fork ? g_lib.pages_fork : g_lib.pages_resize)(L, p, px, py, n32, ps, pd, ws.p, ws.bytes,
-                                                         err, stream_of(a[9], dev)));
+                                                         err, on.st));
     PyObject* both = PyTuple_New(2);
     if (!both) return nullptr;
     PyTuple_SET_ITEM(both, 0, a[5] == Py_None ? THPVariable_Wrap(src) : given(a[5]));
@@ -512,7 +530,7 @@ PyObject* pages_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* ps = (const int32_t*)ptr(s, "copy_src", at::kInt, s.sizes(), dev);
     const int32_t* pd = (const int32_t*)ptr(a[3], "copy_dst", at::kInt, s.sizes(), dev);
     check(g_lib.pages_copy(L, p, ps, pd, small(s.size(0), "tables"), small(s.size(1), "copies"),
-                           err_ptr(a[4], dev), stream_of(a[5], dev)));
+                           err_ptr(a[4], dev), OnStream(a[5], dev).st));
     return given(Py_None);
   });
 }
@@ -525,6 +543,7 @@ PyObject* cache_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const dcp_layout_t L = layout_of(a[0]);
     int dev;
     const dcp_pool_set_t p = pools_of(a[1], L, dev);
+    const OnStream on(a[9], dev);
     if (integer(a[3]) != p.num_blocks)
       refuse("num_blocks is not that of the pools, " + std::to_string(p.num_blocks));
     const at::Tensor& ctx = tensor(a[4], "ctx_lens");
@@ -550,8 +569,7 @@ PyObject* cache_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* out = (int32_t*)(a[7] == Py_None ? own.data_ptr()
                                               : ptr(a[7], "new_lens", at::kInt, {B}, dev));
     check(g_lib.cache_compact(L, p, pb, small(B, "requests"), small(bt.size(dim - 1), "max_vblocks"),
-                              stride, pc, pp, pn, small(most, "max_path"), out, err,
-                              stream_of(a[9], dev)));
+                              stride, pc, pp, pn, small(most, "max_path"), out, err, on.st));
     return a[7] == Py_None ? THPVariable_Wrap(own) : given(a[7]);
   });
 }

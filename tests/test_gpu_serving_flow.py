@@ -225,3 +225,29 @@ def test_a_step_in_a_graph(lib):
         for a, b in zip(after[1], want):
             assert torch.equal(a, b)
         assert torch.equal(after[0], pools)
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(lib):
+    """Memory that another stream's queued work still writes is not handed out."""
+    L = lib.Layout(2, 16, 1)
+    gen = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(s, generator=gen).to(BF16).cuda()
+               for s in ((64, 8, 128), (2, 6, 2, 16, 128), (2, 6, 2, 16, 128)))
+    bt = dev([[[0, 1, 2]], [[3, 4, 5]]])
+    kv = lib.PagedKV(list(k), list(v), bt, 6)
+    mask = torch.full((64,), -1, dtype=torch.int64, device="cuda")
+    args = L, q, kv, dev([0, 64]), dev([20]), mask, 0.1, 64
+    want, lse = lib.tree_decode_gqa(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = [torch.empty_like(want) for _ in range(4)] + \
+        [torch.empty(n, dtype=torch.uint8, device="cuda")
+         for n in (lib.tree_workspace_size(L, 1, 64, 8, 2, 128, BF16), lse.nbytes)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)         # some 50 ms, then the memory is written
+    for x in freed:
+        x.zero_()
+    del freed, x
+    got, got_lse = lib.tree_decode_gqa(*args, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(got_lse, lse)
