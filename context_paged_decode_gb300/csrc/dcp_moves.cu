@@ -192,7 +192,7 @@ int dcp_pages_copy(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* cop
     return DCP_EINVAL;
   if (pools.row_bytes % 16 != 0) return DCP_EUNSUPPORTED;
   if (num == 0 || pools.num_pools == 0) return DCP_OK;
-  if (!pools.ptr || !copy_src || !copy_dst) return DCP_EINVAL;
+  if (!pools.ptr || !copy_src || !copy_dst || copy_src == copy_dst) return DCP_EINVAL;
   const PoolSet P{pools.ptr, pools.num_pools, pools.num_heads, pools.row_bytes / 16,
                   pools.num_blocks};
   const int64_t page16 = (int64_t)pools.num_heads * layout.block_size * (pools.row_bytes / 16);
@@ -215,10 +215,15 @@ int dcp_cache_compact(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* 
   if (!layout_ok(layout) || !pool_set_ok(pools) || num_reqs < 0 || max_vblocks < 0 ||
       bt_rank_stride < 0 || max_path < 0)
     return DCP_EINVAL;
-  if (pools.row_bytes % 16 != 0) return DCP_EUNSUPPORTED;
+  if (pools.row_bytes % 16 != 0 ||
+      (int64_t)layout.block_size * layout.dcp_size >= (int64_t(1) << 31))
+    return DCP_EUNSUPPORTED;
   if (num_reqs == 0) return DCP_OK;
   if ((pools.num_pools > 0 && !pools.ptr) || !block_table || !ctx_lens || !path_len ||
       (max_path > 0 && !path))
+    return DCP_EINVAL;
+  // every CTA of a request reads its length, and one stores the new one
+  if (new_lens && new_lens < ctx_lens + num_reqs && ctx_lens < new_lens + num_reqs)
     return DCP_EINVAL;
   CompactTokArgs A;
   A.L = Layout{layout.dcp_size, layout.block_size, layout.interleave};

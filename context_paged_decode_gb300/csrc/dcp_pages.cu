@@ -392,6 +392,7 @@ static int pages_ok(const dcp_layout_t& L, const dcp_pages_t& p) {
       (p.bt_rank_stride != 0 && p.bt_rank_stride < (int64_t)p.num_reqs * p.max_vblocks))
     return DCP_EINVAL;
   if (p.num_blocks >= (int64_t(1) << 31) - 32 ||
+      (int64_t)L.block_size * L.dcp_size >= (int64_t(1) << 31) ||
       (int64_t)p.max_vblocks * L.block_size * L.dcp_size >= (int64_t(1) << 31))
     return DCP_EUNSUPPORTED;
   if ((p.num_reqs > 0 && (!p.seq_lens || (p.max_vblocks > 0 && !p.block_table))) ||
@@ -439,7 +440,8 @@ static int launch_pages(const dcp_layout_t& L, const dcp_pages_t& p, const int32
   A.sums = (int32_t*)ws;
   A.new_len = A.sums + DCP_MAX_RANKS * kPgCluster;
   A.err = err;
-  if (!ws || ws_bytes < pages_ws_bytes(N)) return DCP_EWORKSPACE;
+  if (!ws || ws_bytes < pages_ws_bytes(N) || ((uintptr_t)ws & 3)) return DCP_EWORKSPACE;
+  if (src == dst) return DCP_EINVAL;
   const size_t smem = pages_smem(N, A.hash);
   if (!allow_smem<pages_kernel<kFork>>()) return DCP_ECUDA;
   const unsigned ctas = A.alone ? kPgCluster : (unsigned)(tables * kPgCluster);

@@ -673,8 +673,9 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
       !ranks_ok(kv.k, layout.dcp_size) || !ranks_ok(kv.v, layout.dcp_size))
     return DCP_EINVAL;
   if ((int64_t)B * layout.dcp_size * Hkv * 64 >= (int64_t(1) << 30) ||
+      (int64_t)layout.block_size * layout.dcp_size >= (int64_t(1) << 31) ||
       (int64_t)kv.max_vblocks * layout.block_size * layout.dcp_size >= (int64_t(1) << 31) ||
-      ((uintptr_t)q & 15))
+      ((uintptr_t)q & 15) || ((uintptr_t)out & 15))
     return DCP_EUNSUPPORTED;
   for (int r = 0; r < layout.dcp_size; ++r)
     if (((uintptr_t)kv.k.ptr[r] & 15) || ((uintptr_t)kv.v.ptr[r] & 15)) return DCP_EUNSUPPORTED;
@@ -719,7 +720,8 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
   A.lse = lse;
   A.err = err;
   const size_t need = tree_carve(&A, ws, B, layout.dcp_size, S.parts, S.rows, d);
-  if (!ws || ws_bytes < need) return DCP_EWORKSPACE;
+  if (!ws || ws_bytes < need || ((uintptr_t)ws & 15)) return DCP_EWORKSPACE;
+  if (out == q) return DCP_EINVAL;   // other CTAs read the queries until the end
   cudaError_t e = cudaSuccess;
   if (!A.self) e = launch_chained(tree_plan_kernel, 1, kTreePlanThreads, 0, s, A);
   if (e != cudaSuccess) return launch_status_report(e);

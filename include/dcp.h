@@ -508,7 +508,10 @@ int dcp_sfa_decode(dcp_layout_t layout, const void* q, int32_t num_reqs, int32_t
  * are left as they were.  Unusable block-table entries are skipped and counted
  * as in dcp_decode_gqa.
  * Supported: dtype F32 or BF16, head_dim a multiple of 32 up to 256,
- * num_q_heads / num_kv_heads <= 16, scale > 0, q and the pools 16-byte aligned.
+ * num_q_heads / num_kv_heads <= 16, scale > 0; q, out, the workspace and the
+ * pools 16-byte aligned.  out may not be q, and no other call may use the
+ * workspace at the same time (two captured graphs that share one may not
+ * overlap).
  */
 int dcp_tree_decode_gqa(dcp_layout_t layout, const void* q, const int32_t* q_start,
                         int32_t num_tokens, int32_t num_reqs, int32_t max_tree,
@@ -557,7 +560,7 @@ int dcp_tree_workspace_size(dcp_layout_t layout, int32_t num_reqs, int32_t max_t
  *             An axis outside [0, num_axes) counts as 0 and bumps err_count.
  *  k_out      [num_tokens][num_kv_heads][head_dim]: the rotated keys once more
  *             (for prefill attention), or NULL.
- * Two tokens with one slot: either may stay.  rot_dim is a multiple of 16 up
+ * Two tokens with one slot: either may stay, row by row.  rot_dim is a multiple of 16 up
  * to 1024; rows and strides are multiples of 16 bytes and pointers 16-byte
  * aligned.
  */
@@ -593,6 +596,7 @@ int dcp_rope_write_mla(dcp_layout_t layout, const void* q, int64_t q_stride, con
  * A request of length n holds ceil(n / (block_size*dcp_size)) pages of each
  * table.  The page that the next token is written to (the open page, unless it
  * is full) is always the request's own.  max_vblocks*block_size*dcp_size < 2^31.
+ * A call changes the state, so calls on one state run one after the other.
  */
 typedef struct {
   int32_t* block_table;
@@ -677,7 +681,7 @@ int dcp_pages_copy(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* cop
  * position ctx_lens[b] + i, for i < path_len[b].
  *  path     [num_reqs][max_path] int32, strictly increasing from >= 0.
  *  path_len [num_reqs] int32, 0 .. max_path.
- *  new_lens [num_reqs] int32 or NULL: ctx_lens[b] + nodes kept.
+ *  new_lens [num_reqs] int32 or NULL: ctx_lens[b] + nodes kept; not ctx_lens.
  * The moves of a request stop at the first entry that breaks the order or does
  * not resolve to a stored token, which bumps err_count once.  A bad length
  * keeps nothing and counts once.

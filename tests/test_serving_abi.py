@@ -174,3 +174,30 @@ def test_page_model_keeps_its_invariants():
                     at = m.open(int(m.seq[b]), t)
                     assert at is None or m.ref[t, m.bt[t, b, at[0]]] == 1
         assert m.err == 0
+
+
+def test_outputs_over_inputs_and_odd_workspaces(dcp):
+    """What the kernels could not keep apart is refused before anything is launched."""
+    lib, L = dcp.load(), dcp.Layout(2, 16, 1)
+    Q, odd = C.c_void_p(1 << 21), lambda n: C.c_void_p((1 << 20) + n)  # noqa: E731
+
+    def tree(out=Q, ws=P, layout=L, cache=None):
+        return lib.dcp_tree_decode_gqa(layout, P, P, 5, 2, 4, 8, 2, 128, 1.0, 1, cache or kv(dcp), P,
+                                       P, None, out, 1, None, ws, 1 << 40, None, None)
+
+    assert tree(out=P) == EINVAL and tree(out=odd(8)) == EUNSUPPORTED
+    assert tree(ws=odd(8)) == EWORKSPACE
+    assert tree(layout=dcp.Layout(4, 1 << 29, 1), cache=kv(dcp, 4, max_vb=0)) == EUNSUPPORTED
+    pages = lambda vb=8: dcp.PagesStruct(1 << 20, 1 << 20, 1 << 20, 1 << 20, 4, vb, 32, 100)  # noqa: E731
+    for name in ("resize", "fork"):
+        f = getattr(lib, "dcp_pages_" + name)
+        assert f(L, pages(), P, P, 3, P, P, P, 1 << 40, None, None) == EINVAL
+        assert f(L, pages(), P, P, 3, P, Q, odd(2), 1 << 40, None, None) == EWORKSPACE
+        assert f(dcp.Layout(4, 1 << 29, 1), pages(0), P, P, 3, P, Q, P, 1 << 40, None,
+                 None) == EUNSUPPORTED
+    pools = dcp.PoolSetStruct(1 << 20, 2, 2, 256, 8)
+    assert lib.dcp_pages_copy(L, pools, P, P, 2, 3, None, None) == EINVAL
+    move = lambda new, L=L: lib.dcp_cache_compact(  # noqa: E731
+        L, pools, P, 2, 4, 8, P, Q, P, 4, new, None, None)
+    assert move(P) == EINVAL and move(odd(4)) == EINVAL and move(odd(-4)) == EINVAL
+    assert move(None, dcp.Layout(4, 1 << 29, 1)) == EUNSUPPORTED
