@@ -330,7 +330,7 @@ rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
   for (int j = 0; j < kRbPairs; ++j) pos[j] = position(blockIdx.x, j);
 
   int64_t dead = 0;
-  uint32_t k = 0;
+  uint32_t k = 0, last = 0;
   for (int64_t it = blockIdx.x; it < B.items; it += gridDim.x, ++k) {
     const int item = (int)it, stage = k % kRbStages;
     const int64_t t = item / B.parts;
@@ -352,7 +352,10 @@ rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
       }
       pos[j] = position(nxt < B.items ? (int)nxt : B.items, j);
     }
-    if (!dead && !mbar_wait(smem_u32(full + stage), (k / kRbStages) & 1)) dead = 1;
+    if (!dead && !mbar_wait(smem_u32(full + stage), (k / kRbStages) & 1)) {
+      dead = 1;
+      last = k;
+    }
     __syncthreads();
     uint4* rows = reinterpret_cast<uint4*>(smem + stage * B.stage);
     const int turn = max(min(r1, A.Hq + A.Hk) - r0, 0) * A.ru;
@@ -401,11 +404,14 @@ rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
       bulk_wait_read<1>();     // the stage before this one has been read
       __syncwarp();
       const int64_t ahead = it + (int64_t)(kRbStages - 1) * gridDim.x;
-      if (lane == 0 && ahead < B.items) load((int)ahead, (k + kRbStages - 1) % kRbStages);
+      if (lane == 0 && !dead && ahead < B.items) load((int)ahead, (k + kRbStages - 1) % kRbStages);
     }
   }
   if (tid < 32) bulk_wait_read<0>();   // shared memory is left only when it has been read
-  if (dead && tid == 0 && A.err) atomicAdd(A.err, 1 << 20);
+  if (dead && tid == 0) {   // the load that did not come, for a last time
+    mbar_wait(smem_u32(full + last % kRbStages), (last / kRbStages) & 1);
+    if (A.err) atomicAdd(A.err, 1 << 20);
+  }
 }
 
 static uint32_t div_magic(int d) {

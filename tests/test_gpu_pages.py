@@ -257,3 +257,40 @@ def test_refusals(lib):
             bad()
     with pytest.raises(lib.DcpError):                    # pages of 2^31 tokens a request
         lib.Pages.new(lib.Layout(16, 1 << 20, 1), 1, 1 << 8, 4)
+
+
+@pytest.mark.parametrize("shape", [(5, 16, 1, 30, 6, 120, False), (2, 16, 2, 2048, 2, 3000, False),
+                                   (8, 16, 16, 170, 30, 1500, False)], ids=str)
+def test_whole_lists(lib, shape):
+    """Every request in one call: the longest list, more CTAs than tables need, a cluster each."""
+    dcp, bs, I, B, VB, nb, shared = shape
+    L = lib.Layout(dcp, bs, I)
+    pages, m = lib.Pages.new(L, B, VB, nb, shared=shared), R.PageModel(dcp, bs, I, B, VB, nb, shared)
+    rng = np.random.default_rng(B)
+    err = torch.zeros(1, dtype=I32, device="cuda")
+    half = B // 2
+    for lens in (rng.integers(0, bs * dcp + 1, B), rng.integers(0, 9, B)):
+        new = np.where(np.arange(B) < half, lens, 0)
+        order = rng.permutation(B)
+        src, dst = lib.pages_resize(L, pages, dev(order), dev(new[order]), err=err)
+        es, ed = m.resize(order, new[order])
+        same(pages, m)
+        assert np.array_equal(src.cpu().numpy(), es) and np.array_equal(dst.cpu().numpy(), ed)
+        parent, child = rng.permutation(half), half + rng.permutation(half)
+        src, dst = lib.pages_fork(L, pages, dev(parent), dev(child), err=err)
+        es, ed = m.fork(parent, child)
+        same(pages, m)
+        assert np.array_equal(src.cpu().numpy(), es) and np.array_equal(dst.cpu().numpy(), ed)
+    assert err.item() == 0 and m.err == 0
+
+
+def test_lengths_from_the_state_itself(lib):
+    """The list of lengths may be the state's own: nothing changes."""
+    L = lib.Layout(2, 16, 1)
+    pages = lib.Pages.new(L, 4, 4, 20)
+    lib.pages_resize(L, pages, dev([0, 2]), dev([40, 7]))
+    before = [x.clone() for x in (pages.block_table, pages.ref_count, pages.seq_lens)]
+    src, dst = lib.pages_resize(L, pages, dev([0, 1, 2, 3]), pages.seq_lens)
+    assert (src == -1).all() and (dst == -1).all()
+    for a, b in zip(before, (pages.block_table, pages.ref_count, pages.seq_lens)):
+        assert torch.equal(a, b)
