@@ -141,15 +141,17 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
 pages_kernel(const __grid_constant__ PagesArgs A) {
   extern __shared__ int sm[];
   __shared__ int sh[kPgThreads / 32];
-  __shared__ int s_any;
+  __shared__ int s_any, s_needs;
   griddep_launch_dependents();   // the next call's first kernel may start its launch
   griddep_wait();                // launched chained: the preceding kernel completed
   const int table = blockIdx.x / A.per, cta = blockIdx.x % A.per;
   const int tid = threadIdx.x, lane = tid & 31;
   const int gw = cta * (kPgThreads / 32) + (tid >> 5);   // warp of the table
   const int warps = A.per * (kPgThreads / 32);           // and how many it has
-  const bool spare = table >= A.tables;                  // a CTA too many keeps step
-  const int N = spare ? 0 : A.N, words = spare ? 0 : A.words, vbs = A.L.bs * A.L.dcp;
+  const int N = A.N, vbs = A.L.bs * A.L.dcp;
+  // a CTA too many checks the list and keeps step, and has no work
+  const bool spare = table >= A.tables;
+  const int mine_n = spare ? 0 : N, words = spare ? 0 : A.words;
   int32_t* bt = A.bt + table * A.stride;
   int32_t* ref = A.ref + (int64_t)table * A.nb;
   uint32_t* bits = A.bits + (int64_t)table * A.words;
@@ -160,7 +162,7 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
 
   // the list, and the first entry that names each request
   PagesList S(sm, N, A.hash);
-  if (tid == 0) s_any = 0;
+  if (tid == 0) s_any = s_needs = 0;
   for (int n = tid; n < N; n += kPgThreads) {
     S.c[n] = __ldcg(A.row + n);
     S.p[n] = kFork ? __ldcg(A.up + n) : __ldcg(A.len + n);
@@ -201,6 +203,8 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
     }
     S.old[n] = min(blocks(old), A.max_vb) == blocks(old) ? old : A.max_vb * vbs;
     S.len[n] = ok ? len : -1;
+    if (!kFork && ok && (blocks(len) > blocks(S.old[n]) || min(S.old[n], len) % vbs != 0))
+      s_needs = 1;
     if (table == 0 && cta == 0) {
       if (!ok) count_error(A.err);
       if (!A.alone) A.new_len[n] = ok ? len : -1;
@@ -211,8 +215,8 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
   // Releases, and for a fork the pages that the child shares with its parent.
   // The parent holds those throughout, so no release can free one.  `share`
   // warps take turns on an entry where there are few.
-  const int share = N > 0 && N < warps ? warps / N : 1;
-  for (int n = gw / share; n < N; n += warps / share) {
+  const int share = N < warps ? warps / N : 1;
+  for (int n = gw / share; n < mine_n; n += warps / share) {
     const int len = S.len[n];
     if (len < 0) continue;
     int32_t* row = bt + (int64_t)S.c[n] * A.max_vb;
@@ -252,9 +256,16 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
     for (int n = tid; n < N; n += kPgThreads)
       if (S.len[n] >= 0) A.seq[S.c[n]] = S.len[n];
 
+  // Nothing to take when the lengths alone say so, as in every table: requests
+  // that are freed, or cut at the end of a page.
+  if (!kFork && !s_needs) {
+    for (int n = cta * kPgThreads + tid; n < mine_n; n += warps * 32) src[n] = dst[n] = -1;
+    return;
+  }
+
   // what each entry needs, summed up by every CTA for itself
   int W = 0;
-  for (int n0 = 0; n0 < N; n0 += kPgThreads) {
+  for (int n0 = 0; n0 < mine_n; n0 += kPgThreads) {
     const int n = n0 + tid;
     int need = 0, again = 0, page = -1;
     if (n < N && S.len[n] >= 0) {
@@ -347,7 +358,7 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
   if (!kFork && (s_any || A.per < kPgCluster)) {   // (the same in a table's CTAs)
     // the shared open pages that were replaced, one holder less
     cluster_sync();
-    for (int n = cta * kPgThreads + tid; n < N; n += warps * 32)
+    for (int n = cta * kPgThreads + tid; n < mine_n; n += warps * 32)
       if (S.need[n] & 1) release_page(A, ref, bits, S.page[n]);
   }
 }
