@@ -69,10 +69,11 @@ struct TreeTc {
   static constexpr int kQOff = kVOff + kVSlots * kSlot;
   static constexpr int kMlOff = kQOff + kQ;                 // float2 [2 stream][128]
   static constexpr int kFlagOff = kMlOff + 2 * 128 * 8;     // int [2 parity], joins
-  static constexpr int kPlanOff = kFlagOff + 32;            // TreeSelf
+  static constexpr int kPlanOff = kFlagOff + 16;            // TreeSelf
   static constexpr int kBarOff = kPlanOff + (int)sizeof(TreeSelf);
-  static constexpr int kBars = 2 * (kKSlots + kVSlots) + 8;
-  static constexpr int kSmem = kBarOff + 8 * kBars + 16;
+  static constexpr int kBars = 2 * kKSlots + 3 * kVSlots + 8;
+  static constexpr int kSmem = kBarOff + 8 * kBars + 8;
+  static_assert(kSmem <= 227 * 1024 && kBarOff % 8 == 0, "shared memory");
   static constexpr uint32_t kColS = 0, kColO = 256;         // two of each, 128 and D apart
 };
 
@@ -106,6 +107,33 @@ struct ChunkIt {
     settle(A, p);
   }
   __device__ __forceinline__ bool has(int lane) const { return lane < kTtChunks && x < c; }
+};
+
+// The chunks of a tile as bits of tokens: the low half those that all rows see,
+// the high half those that are there.  The table entry is loaded a tile ahead.
+struct ChunkBits {
+  ChunkIt it;
+  int raw;
+  __device__ __forceinline__ ChunkBits(const TreeArgs& A, const TreePiece& p, int tile, int lane)
+      : it(A, p, tile, lane) {
+    fetch(A, p, lane);
+  }
+  __device__ __forceinline__ void fetch(const TreeArgs& A, const TreePiece& p, int lane) {
+    raw = -1;
+    const int j = it.x * kTtChunk / A.L.bs;
+    if (it.has(lane) && j < A.max_vb)
+      raw = __ldcg(A.bt + it.r * A.stride + (int64_t)p.b * A.max_vb + j);
+  }
+  __device__ __forceinline__ void next(const TreeArgs& A, const TreePiece& p, int tiles, int lane) {
+    it.step(A, p, tiles);
+    fetch(A, p, lane);
+  }
+  __device__ __forceinline__ uint32_t bits(const TreeArgs& A, int lane) const {
+    if (!it.has(lane) || raw < 0 || (int64_t)raw >= A.nb) return 0u;
+    const int at = it.x * kTtChunk, there = min(it.n - at, kTtChunk);
+    const int old = min(max(it.lc - at, 0), there);
+    return ((1u << old) - 1u) | ((1u << there) - 1u) << 16;
+  }
 };
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
@@ -294,7 +322,8 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
   const uint32_t bars = sbase + C::kBarOff;
   const uint32_t b_k = bars, b_kfree = b_k + 8 * C::kKSlots;        // keys: there, read
   const uint32_t b_v = b_kfree + 8 * C::kKSlots, b_vfree = b_v + 8 * C::kVSlots;
-  const uint32_t b_s = b_vfree + 8 * C::kVSlots;  // +stream: scores are there
+  const uint32_t b_vok = b_vfree + 8 * C::kVSlots;   // values may be read by the product
+  const uint32_t b_s = b_vok + 8 * C::kVSlots;    // +stream: scores are there
   const uint32_t b_p = b_s + 16;                  // +stream: P is there
   const uint32_t b_o = b_p + 16, b_ofree = b_o + 8, b_q = b_o + 16, b_qfree = b_o + 24;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * C::kBars);
@@ -314,6 +343,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
     for (int i = 0; i < C::kVSlots; ++i) {
       mbar_init(b_v + 8 * i, 1);
       mbar_init(b_vfree + 8 * i, 1);
+      mbar_init(b_vok + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_s + 8 * i, 1);
@@ -432,16 +462,17 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
         mbar_wait(full + 8 * (t % slots), (t / slots) & 1);
       if (dead && lane == 0) atomicAdd(errp, kTtStuck);
     } else if (warp == 3) {
-      // ---------------- queries ----------------
-      if (lane == 0) {
-        uint32_t item = 0;
-        bool dead = false;
-        TreePiece p;
-        while (tree_next(A, walk, p)) {
-          if (item > 0 && !mbar_wait(b_qfree, (item - 1) & 1)) {
-            dead = true;
-            break;
-          }
+      // ---------------- queries, and values that must not count ----------------
+      uint32_t item = 0, vs = 0, vp = 0;
+      bool dead = false;
+      auto wait = [&](uint32_t bar, uint32_t par) {
+        if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar, par))) dead = true;
+      };
+      TreePiece p;
+      while (!dead && tree_next(A, walk, p)) {
+        if (item > 0) wait(b_qfree, (item - 1) & 1);
+        if (dead) break;
+        if (lane == 0) {
           const bool two = kTwo && block_rows(p) > srows;
           mbar_arrive_expect_tx(b_q, (two ? 2 : 1) * srows * D * 2);
           const int node = p.q0 + p.rb * (A.rows / A.G);
@@ -450,11 +481,77 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
             for (int h = 0; h < D / 64; ++h)
               tma_load_3d(sbase + C::kQOff + s * C::kSlot + h * kHalfBytes, &X.qmap, 64 * h,
                           p.g * A.G, node + s * X.nodes, b_q);
-          ++item;
         }
-        if (item > 0) mbar_wait(b_q, (item - 1) & 1);
-        if (dead) atomicAdd(errp, kTtStuck);
+        __syncwarp();
+        ChunkBits it(A, p, 0, lane);
+        for (int k = 0; k < p.n && !dead; ++k) {
+          const uint32_t bits = it.bits(A, lane);
+          if (k + 1 < p.n) it.next(A, p, 1, lane);
+          wait(b_v + 8 * vs, vp);
+          if (dead) break;
+          uint32_t odd_chunks = __ballot_sync(0xffffffffu, bits != ~0u) & 0xFFu;
+          if (odd_chunks) {
+            // rows of V that nobody sees become zero, and so do odd values of
+            // nodes; a row is kRow lanes of 16 bytes
+            const uint32_t v = sbase + C::kVOff + vs * C::kSlot;
+            constexpr int kRow = D / 8, kAtOnce = 32 / kRow;
+            const int ch = lane % kRow;
+            do {
+              const int c = __ffs(odd_chunks) - 1;
+              odd_chunks &= odd_chunks - 1;
+              const uint32_t mine = __shfl_sync(0xffffffffu, bits, c);
+              uint32_t rows = ~mine & 0xFFFFu;            // not seen by all
+              for (; rows; rows &= rows - 1) {
+                // the next kAtOnce such rows, one for each kRow lanes
+                uint32_t rest = rows;
+#pragma unroll
+                for (int i = 1; i < kAtOnce; ++i)
+                  if (lane / kRow >= i) rest &= rest - 1;
+                if (rest) {
+                  const int o = __ffs(rest) - 1, tok = c * kTtChunk + o;
+                  const uint32_t at =
+                      v + (ch >> 3) * kHalfBytes + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4);
+                  uint32_t w[4] = {0u, 0u, 0u, 0u};
+                  bool odd = !((mine >> (16 + o)) & 1);
+                  if (!odd) {
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(at));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                      if (bf16_odd(w[x])) {
+                        w[x] &= 0xFFFF0000u;
+                        odd = true;
+                      }
+                      if (bf16_odd(w[x] >> 16)) {
+                        w[x] &= 0xFFFFu;
+                        odd = true;
+                      }
+                    }
+                    if (odd) flag[item & 1] = (int)item + 1;
+                  }
+                  if (odd)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]),
+                                 "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                }
+#pragma unroll
+                for (int i = 1; i < kAtOnce; ++i) rows &= rows - 1;
+              }
+            } while (odd_chunks);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(b_vok + 8 * vs);
+          if (++vs == C::kVSlots) {
+            vs = 0;
+            vp ^= 1;
+          }
+        }
+        ++item;
       }
+      if (item > 0) mbar_wait(b_q, (item - 1) & 1);
+      if (dead && lane == 0) atomicAdd(errp, kTtStuck);
     } else {
       // ---------------- products ----------------
       // The whole warp runs this, with values that all lanes share (what is
@@ -479,7 +576,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       // 65536 tokens: 75.5 us, 77.0 the other way round), and a wait tries once
       // before it loops (73.4).
       auto have_k = [&]() { wait(b_k + 8 * ks, kp); };
-      auto have_v = [&]() { wait(b_v + 8 * vs, vp); };
+      auto have_v = [&]() { wait(b_vok + 8 * vs, vp); };
       // scores of the ring's next tile into stream s; `last`: its last reader
       auto qk = [&](int s, bool last) {
         if (dead) return;
@@ -570,7 +667,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
     const uint32_t to = tmem + lane_off + C::kColO + s * D;
     float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff);
     const int step = kTwo ? 1 : 2;
-    uint32_t seq = 0, item = 0, ns = 0;
+    uint32_t item = 0, ns = 0;
     bool dead = false;
     auto wait = [&](uint32_t bar, uint32_t par) {
       if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar, par))) dead = true;
@@ -590,35 +687,16 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       float m = -INFINITY, l = 0.f;
       bool filled = false;                               // the accumulator holds earlier tiles
       if (takes) {
-        // The table entry of a lane's chunk is loaded a tile ahead.
-        ChunkIt it(A, p, !kTwo && p.n > s ? s : 0, lane);
-        int raw;
-        auto fetch = [&]() {
-          raw = -1;
-          const int j = it.x * kTtChunk / A.L.bs;
-          if (it.has(lane) && j < A.max_vb)
-            raw = __ldcg(A.bt + it.r * A.stride + (int64_t)p.b * A.max_vb + j);
-        };
-        fetch();
+        ChunkBits it(A, p, !kTwo && p.n > s ? s : 0, lane);
         for (int k = kTwo ? 0 : s; k < p.n; k += step) {
-          // this lane's chunk: first position, rank, and the ends of what is
-          // there and of what all rows see
-          const int c_pos = it.x * kTtChunk, c_rank = it.r;
-          // its tokens as bits: low half seen by all rows, high half there
-          uint32_t bits = 0;
-          if (it.has(lane) && raw >= 0 && (int64_t)raw < A.nb) {
-            const int there = min(it.n - c_pos, kTtChunk), old = min(max(it.lc - c_pos, 0), there);
-            bits = ((1u << old) - 1u) | ((1u << there) - 1u) << 16;
-          }
+          // this lane's chunk: first position and rank, and its tokens
+          const int c_pos = it.it.x * kTtChunk, c_rank = it.it.r;
+          const uint32_t bits = it.bits(A, lane);
           const uint32_t plain = __ballot_sync(0xffffffffu, bits == ~0u);
-          if (k + step < p.n) {
-            it.step(A, p, step);
-            fetch();
-          }
+          if (k + step < p.n) it.next(A, p, step, lane);
           // a tile whose tokens all rows see takes no masks
           const bool special = (plain & 0xFFu) != 0xFFu;
           uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-          uint32_t v_old = ~0u, v_node = 0;   // of this warp's 32 tokens of V
           uint32_t masked = 0;                // groups that some row sees in part
           if (special) {
 #pragma unroll
@@ -628,10 +706,6 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
               vis[g] = __byte_perm(lo, hi, 0x5410);
               uint32_t nodes = __byte_perm(lo, hi, 0x7632) & ~vis[g];
               if (vis[g] != ~0u) masked |= 1u << g;
-              if (g == quarter) {
-                v_old = vis[g];
-                v_node = nodes;
-              }
               if (nodes) {   // by this row's mask
                 const int from = 2 * g + (lane >> 4);
                 const int pos = __shfl_sync(0xffffffffu, c_pos, from) + (lane & 15);
@@ -716,49 +790,6 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             filled = true;
             tc_wait_st();
-          }
-          if (v_old != ~0u) {
-            // V rows of this warp's tokens: those nobody sees become zero, and
-            // so do odd values of nodes
-            const uint32_t vi = seq + k, vslot = vi % C::kVSlots;
-            wait(b_v + 8 * vslot, (vi / C::kVSlots) & 1);
-            const uint32_t v = sbase + C::kVOff + vslot * C::kSlot;
-            constexpr int kRow = D / 8;                // 16-byte pieces of a row
-            constexpr int kAtOnce = 32 / kRow;         // rows of the warp at once
-            const int ch = lane % kRow;
-            for (int o0 = 0; o0 < 32 && !dead; o0 += kAtOnce) {
-              if (((v_old >> o0) & ((1u << kAtOnce) - 1u)) == (1u << kAtOnce) - 1u) continue;
-              const int o = o0 + lane / kRow;
-              if (!((v_old >> o) & 1)) {
-                const int tok = quarter * 32 + o;
-                const uint32_t at =
-                    v + (ch >> 3) * kHalfBytes + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4);
-                uint32_t w[4] = {0u, 0u, 0u, 0u};
-                bool odd = !((v_node >> o) & 1);
-                if (!odd) {
-                  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                               : "r"(at));
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    if (bf16_odd(w[x])) {
-                      w[x] &= 0xFFFF0000u;
-                      odd = true;
-                    }
-                    if (bf16_odd(w[x] >> 16)) {
-                      w[x] &= 0xFFFFu;
-                      odd = true;
-                    }
-                  }
-                  if (odd) flag[item & 1] = (int)item + 1;
-                }
-                if (odd)
-                  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]),
-                               "r"(w[1]), "r"(w[2]), "r"(w[3])
-                               : "memory");
-              }
-            }
-            fence_proxy_async_smem();
           }
           tc_fence_before();
           __syncwarp();
@@ -878,7 +909,6 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_ofree);
-      seq += p.n;
       if (p.slot >= 0 && A.join) {
         // the last run to bring its part joins them all
         const int k0 = tree_run_of(walk.total, walk.parts, p.u0);
