@@ -266,7 +266,7 @@ struct RopeBulk {
 };
 
 template <bool kF32, bool kHalves>
-__global__ void __launch_bounds__(kRbThreads)
+__global__ void __launch_bounds__(kRbThreads, kRbPerSm)
 rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kRbStages];
@@ -329,8 +329,8 @@ rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
 #pragma unroll
   for (int j = 0; j < kRbPairs; ++j) pos[j] = position(blockIdx.x, j);
 
-  int64_t dead = 0;
-  uint32_t k = 0, last = 0;
+  uint32_t dead = 0;             // 1 + the round whose load did not come
+  uint32_t k = 0;
   for (int64_t it = blockIdx.x; it < B.items; it += gridDim.x, ++k) {
     const int item = (int)it, stage = k % kRbStages;
     const int64_t t = item / B.parts;
@@ -352,10 +352,7 @@ rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
       }
       pos[j] = position(nxt < B.items ? (int)nxt : B.items, j);
     }
-    if (!dead && !mbar_wait(smem_u32(full + stage), (k / kRbStages) & 1)) {
-      dead = 1;
-      last = k;
-    }
+    if (!dead && !mbar_wait(smem_u32(full + stage), (k / kRbStages) & 1)) dead = k + 1;
     __syncthreads();
     uint4* rows = reinterpret_cast<uint4*>(smem + stage * B.stage);
     const int turn = max(min(r1, A.Hq + A.Hk) - r0, 0) * A.ru;
@@ -409,7 +406,7 @@ rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
   }
   if (tid < 32) bulk_wait_read<0>();   // shared memory is left only when it has been read
   if (dead && tid == 0) {   // the load that did not come, for a last time
-    mbar_wait(smem_u32(full + last % kRbStages), (last / kRbStages) & 1);
+    mbar_wait(smem_u32(full + (dead - 1) % kRbStages), ((dead - 1) / kRbStages) & 1);
     if (A.err) atomicAdd(A.err, 1 << 20);
   }
 }
