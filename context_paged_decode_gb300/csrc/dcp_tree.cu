@@ -170,7 +170,7 @@ struct Chunk<__nv_bfloat16> {
 // probability zero, and values that nobody sees are zeros in shared memory; if
 // a drafted node's value is not finite, the tile's products skip unseen nodes
 // one by one.  What bounds it: the products on the CUDA cores and the
-// shared-memory reads that feed them (those 69 us are 0.9 GB/ms of KV and 16
+// shared-memory reads that feed them (those 69 us are 0.6 TB/s and 17
 // TFLOP/s), and on short contexts latency: 2 x 11 nodes over up to 3001
 // tokens of 2 heads of 64 in fp32 (4.3 MB) take 20 us, the merge 5 of them.
 template <typename T, int DPL, int RW>
