@@ -133,7 +133,7 @@ __device__ __forceinline__ float tree_close(float m, float l, bool has_sink, flo
 
 constexpr int kTgTile = 64;     // tokens of a tile, two per lane
 constexpr int kTgWarps = 8;
-constexpr int kTgPad = 4;       // floats: a lane's 16-byte reads of its own K row hit 32 banks
+constexpr int kTgPad = 16;      // bytes: a lane's 16-byte reads of its own K row hit 32 banks
 
 template <typename T>
 struct Chunk;                   // 16 bytes of T as floats
@@ -160,36 +160,102 @@ struct Chunk<__nv_bfloat16> {
   }
 };
 
+// Columns of a lane: consecutive ones, so that a row of V is read in one piece
+// per lane (two columns of up to 64, four of each 128).
+template <int DPL>
+__device__ __forceinline__ int tg_col(int lane, int i) {
+  return DPL == 2 ? lane * 2 + i : (i >> 2) * 128 + lane * 4 + (i & 3);
+}
+
+// A lane's columns of a row, zeros beyond its end.
+template <int DPL>
+__device__ __forceinline__ void tg_row(const float* row, int d, int lane, float* v) {
+#pragma unroll
+  for (int i = 0; i < DPL; i += 4) {
+    const int c = tg_col<DPL>(lane, i);
+    if (DPL == 2) {
+      const float2 x = c < d ? *(const float2*)(row + c) : make_float2(0.f, 0.f);
+      v[0] = x.x;
+      v[1] = x.y;
+    } else {
+      const float4 x = c < d ? *(const float4*)(row + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[i] = x.x;
+      v[i + 1] = x.y;
+      v[(i + 2) % DPL] = x.z;
+      v[(i + 3) % DPL] = x.w;
+    }
+  }
+}
+template <int DPL>
+__device__ __forceinline__ void tg_row(const __nv_bfloat16* row, int d, int lane, float* v) {
+#pragma unroll
+  for (int i = 0; i < DPL; i += 4) {
+    const int c = tg_col<DPL>(lane, i);
+    uint2 x = make_uint2(0u, 0u);
+    if (DPL == 2) {
+      if (c < d) x.x = *(const uint32_t*)(row + c);
+    } else if (c < d) {
+      x = *(const uint2*)(row + c);
+    }
+    v[i] = bf16_lo(x.x);
+    v[i + 1] = bf16_hi(x.x);
+    if (DPL > 2) {
+      v[(i + 2) % DPL] = bf16_lo(x.y);
+      v[(i + 3) % DPL] = bf16_hi(x.y);
+    }
+  }
+}
+
+// 16 bytes to shared memory, past the L1; zeros if `there` is false.
+__device__ __forceinline__ void tg_copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void tg_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All groups but the newest one have landed.
+__device__ __forceinline__ void tg_wait() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
 // Scores on the lanes (a lane has tokens lane and lane + 32 of the tile, whose
-// K rows it reads from shared memory), output on the lanes as well (entries
-// lane + 32 i), the probabilities between them through shared memory.  A warp
-// carries RW query rows, so each K and V value read serves RW products.  Eight
-// rows would halve the shared-memory reads, but leave registers for one CTA an
-// SM, whose eight warps cannot hide each other's latency (4 requests x 16
-// nodes, d 128, 8192 tokens: 140 us against 69).  Masked tokens have
-// probability zero, and values that nobody sees are zeros in shared memory; if
-// a drafted node's value is not finite, the tile's products skip unseen nodes
-// one by one.  What bounds it: the products on the CUDA cores and the
-// shared-memory reads that feed them (those 69 us are 0.6 TB/s and 17
-// TFLOP/s), and on short contexts latency: 2 x 11 nodes over up to 3001
-// tokens of 2 heads of 64 in fp32 (4.3 MB) take 20 us, the merge 5 of them.
+// K rows it reads from shared memory), output on the lanes as well, the
+// probabilities between them through shared memory.  A warp carries RW query
+// rows, so each K and V value read serves RW products.  Eight rows would halve
+// the shared-memory reads, but leave registers for one CTA an SM, whose eight
+// warps cannot hide each other's latency (4 requests x 16 nodes, d 128, 8192
+// tokens: 140 us against 69).  Keys of the next tile are on their way while the
+// values of this one are used, and its values while the next scores are made,
+// so one buffer of each does.  With d 256, where an SM holds one CTA, that took
+// 4 requests x 4 nodes over up to 8192 tokens (8 heads, bf16) from 219 us to
+// 135; with two CTAs it changes nothing (d 128 as above: 66 and 67).  Masked
+// tokens have probability zero, and values that nobody sees are zeros in shared
+// memory; if a drafted node's value is not finite, the tile's products skip
+// unseen nodes one by one.  What bounds it: the products on the CUDA cores and
+// the shared-memory reads that feed them (those 66 us are 17 TFLOP/s; a tile's
+// products would take 43% of its cycles, its reads 60%), and on short contexts
+// latency: 2 x 11 nodes over up to 3001 tokens of 2 heads of 64 in fp32 (4.3
+// MB) take 20 to 22 us, the merge 5 of them.
 template <typename T, int DPL, int RW>
 __global__ void __launch_bounds__(kTgWarps * 32)
 tree_generic_kernel(const __grid_constant__ TreeArgs A) {
-  extern __shared__ __align__(16) float smf[];
-  __shared__ int64_t s_row[kTgTile];   // K/V row of a token, -1: not there
-  __shared__ int s_code[kTgTile];      // node, 64: seen by all, 255: by none
-  __shared__ int s_odd;                // a node's value is not finite
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int64_t s_row[2][kTgTile];   // K/V row of a token, -1: not there
+  __shared__ int s_code[2][kTgTile];      // node, 64: seen by all, 255: by none
   __shared__ TreeSelf s_plan;
-  constexpr int kRows = kTgWarps * RW;
-  const int d = A.d, ks = d + kTgPad, d4 = d >> 2;
-  float* sq = smf;                     // [rows][d]
-  float* sv = sq + kRows * d;          // [tile][d]
-  float* sk = sv + kTgTile * d;        // [tile][d + pad], then the probabilities
+  constexpr int kRows = kTgWarps * RW, CN = Chunk<T>::n;
+  const int d = A.d, d4 = d >> 2;
+  const int row_bytes = d * (int)sizeof(T), pitch = row_bytes + kTgPad;
+  float* sq = reinterpret_cast<float*>(smem);                  // [rows][d]
+  float* sp = sq + kRows * d;                                  // [warps][tile][RW]
+  uint8_t* sv = reinterpret_cast<uint8_t*>(sp + kTgTile * kRows);   // [tile][d]
+  uint8_t* sk = sv + kTgTile * row_bytes;                      // [tile][d + pad]
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float* pw = sk + warp * kTgTile * RW;   // [warp][tile][RW]
+  float* pw = sp + warp * kTgTile * RW;
+  const int cpr = d / CN;          // 16-byte pieces of a row
+  const int lpr = cpr <= 8 ? 8 : (cpr <= 16 ? 16 : 32);   // lanes that copy one
   if (A.self) {
     if (warp == 0) tree_self_plan(A, &s_plan);
     __syncthreads();
@@ -201,9 +267,52 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
       const int ctx = p.ctx;
       const TreeLen len(ctx + p.T, A.L);
       const int row0 = p.rb * A.rows, nrows = min(A.rows, p.T * A.G - row0);
-      __syncthreads();                 // the last piece is done with sq
-      constexpr int CN = Chunk<T>::n;
-      const int cpr = d / CN;          // 16-byte pieces of a row
+      // rank and tile within the rank of the next tile to be loaded
+      int r = p.r0, tr = p.t0, n_r = len.on(r, A.L);
+      auto settle = [&]() {
+        while (tr >= (n_r + kTgTile - 1) / kTgTile) {
+          tr -= (n_r + kTgTile - 1) / kTgTile;
+          n_r = len.on(++r, A.L);
+        }
+      };
+      // its token `tid`: the row, and who sees it
+      int64_t t_row = -1;
+      int t_code = 255;
+      auto look = [&]() {
+        t_row = -1;
+        t_code = 255;
+        const int pos = tr * kTgTile + tid;
+        if (tid >= kTgTile || pos >= n_r) return;
+        const int j = pos / A.L.bs;
+        const int64_t phys =
+            j < A.max_vb ? (int64_t)__ldcg(A.bt + r * A.stride + (int64_t)p.b * A.max_vb + j) : -1;
+        if (phys >= 0 && phys < A.nb) {
+          t_row = (phys * A.Hkv + p.g) * A.L.bs + (pos - j * A.L.bs);
+          const int x = tree_global(pos, r, A.L) - ctx;
+          t_code = x < 0 ? 64 : x;
+        } else {
+          count_error(A.err);
+        }
+      };
+      auto keep = [&](int buf) {
+        if (tid < kTgTile) {
+          s_row[buf][tid] = t_row;
+          s_code[buf][tid] = t_code;
+        }
+      };
+      auto bring = [&](uint8_t* to, int to_pitch, const void* pool, int buf) {
+        for (int j = (warp * 32 + lane) / lpr; j < kTgTile; j += kTgWarps * 32 / lpr) {
+          const int64_t row = s_row[buf][j];
+          const uint8_t* from = (const uint8_t*)pool + (row < 0 ? 0 : row) * row_bytes;
+          for (int c = lane % lpr; c < cpr; c += lpr)
+            tg_copy16(smem_u32(to + j * to_pitch + c * 16), from + c * 16, row >= 0);
+        }
+        tg_commit();
+      };
+      settle();
+      look();
+      __syncthreads();                 // the last piece is done with all of it
+      keep(0);
       for (int i = tid; i < nrows * cpr; i += kTgWarps * 32) {
         const int row = i / cpr, c = (i - row * cpr) * CN, rr = row0 + row;
         const int64_t tok = p.q0 + rr / A.G;
@@ -228,148 +337,127 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
 #pragma unroll
         for (int i = 0; i < DPL; ++i) o[x][i] = 0.f;
       }
-      // rank and tile within the rank of the piece's first tile
-      int r = p.r0, tr = p.t0;
-      int n_r = len.on(r, A.L);
+      const bool idle = warp * RW >= nrows;   // no rows here (uniform in the warp)
+      __syncthreads();
+      bring(sk, pitch, A.k.ptr[r], 0);
+      bring(sv, row_bytes, A.v.ptr[r], 0);
       for (int step = 0; step < p.n; ++step) {
-        while (tr >= (n_r + kTgTile - 1) / kTgTile) {
-          tr -= (n_r + kTgTile - 1) / kTgTile;
-          n_r = len.on(++r, A.L);
+        const int buf = step & 1;
+        const bool more = step + 1 < p.n;
+        if (more) {   // the next tile's table entries come during the scores
+          ++tr;
+          settle();
+          look();
         }
-        const int p0 = tr * kTgTile;
-        ++tr;
-        __syncthreads();               // the last tile is done with sk, sv
-        if (tid < kTgTile) {
-          const int pos = p0 + tid;
-          int code = 255;
-          int64_t row = -1;
-          if (pos < n_r) {
-            const int j = pos / A.L.bs;
-            const int64_t phys =
-                j < A.max_vb ? (int64_t)__ldcg(A.bt + r * A.stride + (int64_t)p.b * A.max_vb + j)
-                             : -1;
-            if (phys >= 0 && phys < A.nb) {
-              row = (phys * A.Hkv + p.g) * A.L.bs + (pos - j * A.L.bs);
-              const int x = tree_global(pos, r, A.L) - ctx;
-              code = x < 0 ? 64 : x;
-            } else {
-              count_error(A.err);
-            }
-          }
-          s_row[tid] = row;
-          s_code[tid] = code;
-          if (tid == 0) s_odd = 0;
-        }
-        __syncthreads();
-        const T* kp = (const T*)A.k.ptr[r];
-        const T* vp = (const T*)A.v.ptr[r];
-        for (int i0 = tid; i0 < kTgTile * cpr; i0 += 4 * kTgWarps * 32) {
-          uint4 a[4], b[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int i = i0 + y * kTgWarps * 32;
-            a[y] = b[y] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < kTgTile * cpr) {
-              const int j = i / cpr, c = (i - j * cpr) * CN;
-              const int64_t row = s_row[j];
-              if (row >= 0) {
-                a[y] = __ldcg((const uint4*)(kp + row * d + c));
-                b[y] = __ldcg((const uint4*)(vp + row * d + c));
-              }
-            }
-          }
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int i = i0 + y * kTgWarps * 32;
-            if (i >= kTgTile * cpr) continue;
-            const int j = i / cpr, c = (i - j * cpr) * CN;
-            float f[CN], g[CN];
-            Chunk<T>::to(a[y], f);
-            Chunk<T>::to(b[y], g);
-            if (s_code[j] < 64) {
-#pragma unroll
-              for (int x = 0; x < CN; ++x)
-                if (!isfinite(g[x])) s_odd = 1;
-            }
-#pragma unroll
-            for (int x = 0; x < CN; x += 4) {
-              *(float4*)(sk + j * ks + c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
-              *(float4*)(sv + j * d + c + x) = make_float4(g[x], g[x + 1], g[x + 2], g[x + 3]);
-            }
-          }
-        }
-        __syncthreads();
-        const bool idle = warp * RW >= nrows;   // no rows here (uniform in the warp)
+        tg_wait();
+        __syncthreads();               // the keys are there
         float s[2][RW];
 #pragma unroll
         for (int x = 0; x < RW; ++x) s[0][x] = s[1][x] = 0.f;
-        const float4* k0 = (const float4*)(sk + lane * ks);
-        const float4* k1 = (const float4*)(sk + (lane + 32) * ks);
+        const uint4* k0 = (const uint4*)(sk + lane * pitch);
+        const uint4* k1 = (const uint4*)(sk + (lane + 32) * pitch);
         const float4* qr = (const float4*)(sq + warp * RW * d);
 #pragma unroll 2
-        for (int c = 0; c < (idle ? 0 : d4); ++c) {
-          const float4 a = k0[c], e = k1[c];
+        for (int c = 0; c < (idle ? 0 : cpr); ++c) {
+          float a[CN], e[CN];
+          Chunk<T>::to(k0[c], a);
+          Chunk<T>::to(k1[c], e);
 #pragma unroll
-          for (int x = 0; x < RW; ++x) {
-            const float4 b = qr[x * d4 + c];
-            s[0][x] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s[0][x]))));
-            s[1][x] = fmaf(e.x, b.x, fmaf(e.y, b.y, fmaf(e.z, b.z, fmaf(e.w, b.w, s[1][x]))));
-          }
-        }
-        __syncthreads();               // the keys are done with
-        if (idle) continue;
-        const int code0 = s_code[lane], code1 = s_code[lane + 32];
-        uint32_t vis[2][RW];
-        float pr[2][RW];
-#pragma unroll
-        for (int x = 0; x < RW; ++x) {
-          const bool on0 = code0 == 64 || (code0 < 64 && ((mask[x] >> code0) & 1));
-          const bool on1 = code1 == 64 || (code1 < 64 && ((mask[x] >> code1) & 1));
-          vis[0][x] = __ballot_sync(0xffffffffu, on0);
-          vis[1][x] = __ballot_sync(0xffffffffu, on1);
-          const float s0 = on0 ? s[0][x] * A.sl2 : -INFINITY;
-          const float s1 = on1 ? s[1][x] * A.sl2 : -INFINITY;
-          const float mn = fmaxf(m[x], warp_max(fmaxf(s0, s1)));
-          const float mb = mn == -INFINITY ? 0.f : mn;
-          const float al = exp2f(m[x] - mb);
-          pr[0][x] = on0 ? exp2f(s0 - mb) : 0.f;
-          pr[1][x] = on1 ? exp2f(s1 - mb) : 0.f;
-          l[x] = l[x] * al + (pr[0][x] + pr[1][x]);      // this lane's tokens
-          m[x] = mn;
-#pragma unroll
-          for (int i = 0; i < DPL; ++i) o[x][i] *= al;
-        }
-#pragma unroll
-        for (int x = 0; x < RW; ++x) {
-          pw[lane * RW + x] = pr[0][x];
-          pw[(lane + 32) * RW + x] = pr[1][x];
-        }
-        __syncwarp();
-        if (!s_odd) {
-#pragma unroll 4
-          for (int j = 0; j < kTgTile; ++j) {
-            float pj[RW];
-#pragma unroll
-            for (int x = 0; x < RW; ++x) pj[x] = pw[j * RW + x];
-#pragma unroll
-            for (int i = 0; i < DPL; ++i)
-              if (i * 32 < d) {
-                const float v = sv[j * d + i * 32 + lane];
-#pragma unroll
-                for (int x = 0; x < RW; ++x) o[x][i] = fmaf(pj[x], v, o[x][i]);
-              }
-          }
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < kTgTile; ++j)
+          for (int y = 0; y < CN; y += 4)
 #pragma unroll
             for (int x = 0; x < RW; ++x) {
-              if (!(((j < 32 ? vis[0][x] : vis[1][x]) >> (j & 31)) & 1)) continue;
-              const float pj = pw[j * RW + x];
+              const float4 b = qr[x * d4 + c * (CN / 4) + y / 4];
+              s[0][x] = fmaf(a[y], b.x,
+                             fmaf(a[y + 1], b.y, fmaf(a[y + 2], b.z, fmaf(a[y + 3], b.w, s[0][x]))));
+              s[1][x] = fmaf(e[y], b.x,
+                             fmaf(e[y + 1], b.y, fmaf(e[y + 2], b.z, fmaf(e[y + 3], b.w, s[1][x]))));
+            }
+        }
+        if (more) keep(buf ^ 1);
+        __syncthreads();               // the keys are done with
+        if (more)
+          bring(sk, pitch, A.k.ptr[r], buf ^ 1);
+        else
+          tg_commit();
+        uint32_t vis[2][RW];
+        if (!idle) {
+          const int code0 = s_code[buf][lane], code1 = s_code[buf][lane + 32];
+#pragma unroll
+          for (int x = 0; x < RW; ++x) {
+            const bool on0 = code0 == 64 || (code0 < 64 && ((mask[x] >> code0) & 1));
+            const bool on1 = code1 == 64 || (code1 < 64 && ((mask[x] >> code1) & 1));
+            vis[0][x] = __ballot_sync(0xffffffffu, on0);
+            vis[1][x] = __ballot_sync(0xffffffffu, on1);
+            const float s0 = on0 ? s[0][x] * A.sl2 : -INFINITY;
+            const float s1 = on1 ? s[1][x] * A.sl2 : -INFINITY;
+            const float mn = fmaxf(m[x], warp_max(fmaxf(s0, s1)));
+            const float mb = mn == -INFINITY ? 0.f : mn;
+            const float al = exp2f(m[x] - mb);
+            const float p0 = on0 ? exp2f(s0 - mb) : 0.f, p1 = on1 ? exp2f(s1 - mb) : 0.f;
+            l[x] = l[x] * al + (p0 + p1);      // this lane's tokens
+            m[x] = mn;
+#pragma unroll
+            for (int i = 0; i < DPL; ++i) o[x][i] *= al;
+            pw[lane * RW + x] = p0;
+            pw[(lane + 32) * RW + x] = p1;
+          }
+        }
+        tg_wait();
+        // the values are there, and if nodes are among them some may not be finite
+        bool odd = __syncthreads_or(tid < kTgTile && s_code[buf][tid] < 64);
+        if (odd) {
+          bool bad = false;
+          for (int j = (warp * 32 + lane) / lpr; j < kTgTile; j += kTgWarps * 32 / lpr)
+            if (s_code[buf][j] < 64)
+              for (int c = lane % lpr; c < cpr; c += lpr) {
+                float f[CN];
+                Chunk<T>::to(*(const uint4*)(sv + j * row_bytes + c * 16), f);
+#pragma unroll
+                for (int x = 0; x < CN; ++x) bad |= !isfinite(f[x]);
+              }
+          odd = __syncthreads_or(bad);
+        }
+        if (!idle) {
+          const T* vt = reinterpret_cast<const T*>(sv);
+          if (!odd) {
+#pragma unroll 4
+            for (int j = 0; j < kTgTile; ++j) {
+              float pj[RW], v[DPL];
+              if (RW == 4) {
+                const float4 q = *(const float4*)(pw + j * RW);
+                pj[0] = q.x;
+                pj[1] = q.y;
+                pj[2 % RW] = q.z;
+                pj[3 % RW] = q.w;
+              } else {
+                const float2 q = *(const float2*)(pw + j * RW);
+                pj[0] = q.x;
+                pj[1] = q.y;
+              }
+              tg_row<DPL>(vt + j * d, d, lane, v);
 #pragma unroll
               for (int i = 0; i < DPL; ++i)
-                if (i * 32 < d) o[x][i] = fmaf(pj, sv[j * d + i * 32 + lane], o[x][i]);
+#pragma unroll
+                for (int x = 0; x < RW; ++x) o[x][i] = fmaf(pj[x], v[i], o[x][i]);
             }
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < kTgTile; ++j) {
+              float v[DPL];
+              tg_row<DPL>(vt + j * d, d, lane, v);
+#pragma unroll
+              for (int x = 0; x < RW; ++x) {
+                if (!(((j < 32 ? vis[0][x] : vis[1][x]) >> (j & 31)) & 1)) continue;
+                const float pj = pw[j * RW + x];
+#pragma unroll
+                for (int i = 0; i < DPL; ++i) o[x][i] = fmaf(pj, v[i], o[x][i]);
+              }
+            }
+          }
+        }
+        if (more) {
+          __syncthreads();             // the values are done with
+          bring(sv, row_bytes, A.v.ptr[r], buf ^ 1);
         }
       }
 #pragma unroll
@@ -377,30 +465,30 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
         const int row = warp * RW + x;
         if (row >= nrows) continue;
         const float lt = warp_sum(l[x]);
-        float lse2;
-        if (p.slot >= 0) {
-          const float f = tree_close(m[x], lt, false, 0.f, lse2);
-          float* dst = A.part_o + ((int64_t)p.slot * A.rows + row) * d;
-#pragma unroll
-          for (int i = 0; i < DPL; ++i)
-            if (i * 32 < d) dst[i * 32 + lane] = lt == 0.f ? 0.f : o[x][i] * f;
-          if (lane == 0) A.part_lse[(int64_t)p.slot * A.rows + row] = lse2;
-          continue;
-        }
+        const bool whole = p.slot < 0, sunk = whole && A.sink != nullptr;
         const int h = p.g * A.G + (row0 + row) % A.G;
-        const bool sunk = A.sink != nullptr;
+        float lse2;
         const float f = tree_close(m[x], lt, sunk, sunk ? __ldcg(A.sink + h) : 0.f, lse2);
-        const int64_t orow = tree_out_row(A, p, row0 + row);
+        const int64_t at = whole ? tree_out_row(A, p, row0 + row) : (int64_t)p.slot * A.rows + row;
+        float* of = (whole ? (float*)A.out : A.part_o) + at * d;
+        __nv_bfloat16* ob = (__nv_bfloat16*)A.out + at * d;
+        const bool wide = !whole || A.out_dtype == DCP_F32;
 #pragma unroll
-        for (int i = 0; i < DPL; ++i)
-          if (i * 32 < d) {
-            const float y = lt == 0.f ? 0.f : o[x][i] * f;
-            if (A.out_dtype == DCP_F32)
-              ((float*)A.out)[orow * d + i * 32 + lane] = y;
-            else
-              ((__nv_bfloat16*)A.out)[orow * d + i * 32 + lane] = __float2bfloat16_rn(y);
-          }
-        if (lane == 0 && A.lse) A.lse[orow] = lse2 * kLn2;
+        for (int i = 0; i < DPL; i += 2) {
+          const int c = tg_col<DPL>(lane, i);
+          if (c >= d) continue;
+          const float a = lt == 0.f ? 0.f : o[x][i] * f, b = lt == 0.f ? 0.f : o[x][i + 1] * f;
+          if (wide)
+            *(float2*)(of + c) = make_float2(a, b);
+          else
+            *(uint32_t*)(ob + c) = pack_bf16(a, b);
+        }
+        if (lane == 0) {
+          if (!whole)
+            A.part_lse[at] = lse2;
+          else if (A.lse)
+            A.lse[at] = lse2 * kLn2;
+        }
       }
     }
   }
@@ -409,9 +497,9 @@ tree_generic_kernel(const __grid_constant__ TreeArgs A) {
 template <typename T, int DPL, int RW>
 static int launch_tree_cores(const TreeArgs& A, cudaStream_t s) {
   constexpr int kRows = kTgWarps * RW;
-  const size_t keys = (size_t)kTgTile * (A.d + kTgPad), probs = (size_t)kTgTile * kRows;
-  const size_t smem = sizeof(float) * ((size_t)kRows * A.d + (size_t)kTgTile * A.d +
-                                       (keys > probs ? keys : probs));
+  const size_t row = (size_t)A.d * sizeof(T);
+  const size_t smem = sizeof(float) * kRows * ((size_t)A.d + kTgTile) +
+                      kTgTile * (2 * row + kTgPad);
   if (!allow_smem<tree_generic_kernel<T, DPL, RW>>()) return DCP_ECUDA;
   const cudaError_t e = launch_chained(tree_generic_kernel<T, DPL, RW>, (unsigned)A.parts,
                                        kTgWarps * 32, smem, s, A);
