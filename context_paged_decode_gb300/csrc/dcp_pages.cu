@@ -25,8 +25,7 @@
 // pages are handed out 32 at a time, a lane per bit of the bitmap.  (With the
 // claims and prefix sums in global memory and a thread per bitmap word, 128
 // forks of 250 pages on 8 ranks took 41 us, and 128 requests of a few new
-// pages 28; they take 16 and 14 now, and 4 requests on 2 ranks 11 and 11, with
-// 2 us of launch in each.)
+// pages 28; they take 16 and 14 now, 2 us of launch in each.)
 #include "dcp_common.cuh"
 #include "dcp_ptx.cuh"
 
@@ -41,6 +40,10 @@ constexpr int kPgMaxList = 2048;
 // columns on 8 ranks (4544 to a CTA) 33.1 and 36.0; but 32 such requests (9088)
 // 48.6 and 41.8, 128 of 33 columns (8320) 63.0 and 46.2.
 constexpr int64_t kPgSmall = 5120;
+// And most of them for a CTA alone to do a table, whose threads then meet in
+// the CTA: those 4 requests 20.9 us, 23.0 with four CTAs a table; 12 of them
+// (780) 21.5 and 23.8, but 32 (2080) 27.1 and 26.6.
+constexpr int64_t kPgOne = 1024;
 
 struct PagesArgs {
   Layout L;
@@ -159,6 +162,9 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
   int32_t* src = A.src + (int64_t)table * N;
   int32_t* dst = A.dst + (int64_t)table * N;
   const int full = A.shared ? vbs : A.L.bs;   // tokens that fill an open page
+  auto table_sync = [&]() {                   // of a table's CTAs, and whoever shares their cluster
+    if (A.per == 1) __syncthreads(); else cluster_sync();
+  };
   auto blocks = [&](int len) { return (int)(((int64_t)len + vbs - 1) / vbs); };
 
   // the list, and the first entry that names each request
@@ -252,7 +258,7 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
       }
     }
   }
-  cluster_sync();
+  if (A.tables == 1) table_sync(); else cluster_sync();
   if (A.alone && blockIdx.x == 0)   // every table has read the old lengths
     for (int n = tid; n < N; n += kPgThreads)
       if (S.len[n] >= 0) A.seq[S.c[n]] = S.len[n];
@@ -299,11 +305,11 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   int base = pg_scan(lane == 0 ? mine : 0, sh, &sum);
   base = __shfl_sync(0xffffffffu, base, 0);
-  if (tid == 0) A.sums[blockIdx.x] = sum;
-  cluster_sync();
+  if (tid == 0 && A.per > 1) A.sums[blockIdx.x] = sum;
+  table_sync();
 
-  int have = 0;
-  for (int i = 0; i < A.per; ++i) {
+  int have = A.per == 1 ? sum : 0;
+  for (int i = 0; i < A.per && A.per > 1; ++i) {
     const int s = __ldcg(A.sums + table * A.per + i);
     if (i < cta) base += s;
     have += s;
@@ -358,7 +364,7 @@ pages_kernel(const __grid_constant__ PagesArgs A) {
   }
   if (!kFork && (s_any || A.per < kPgCluster)) {   // (the same in a table's CTAs)
     // the shared open pages that were replaced, one holder less
-    cluster_sync();
+    table_sync();
     for (int n = cta * kPgThreads + tid; n < mine_n; n += warps * 32)
       if (S.need[n] & 1) release_page(A, ref, bits, S.page[n]);
   }
@@ -444,6 +450,7 @@ static int launch_pages(const dcp_layout_t& L, const dcp_pages_t& p, const int32
   while (A.per > 0 && A.per * tables > kPgCluster) A.per /= 2;
   A.alone = tables == 1 || (int64_t)N * (p.max_vblocks + 32) <= kPgSmall * A.per;
   if (!A.alone) A.per = kPgCluster;
+  if (A.alone && (int64_t)N * (p.max_vblocks + 32) <= kPgOne) A.per = 1;
   A.N = N;
   A.hash = 64;
   while (A.hash < 2 * N) A.hash *= 2;
