@@ -66,14 +66,16 @@ struct Ref {
   ~Ref() { Py_DECREF(o); }
 };
 
-Ref attr(PyObject* o, const char* name) { return Ref(PyObject_GetAttrString(o, name)); }
+Ref attr(PyObject* o, PyObject* name) { return Ref(PyObject_GetAttr(o, name)); }
+// An attribute's name, made once.
+#define NAME(s) ([]() -> PyObject* { static PyObject* const n = PyUnicode_InternFromString(s); return n; }())
 
 int64_t integer(PyObject* o) {
   const int64_t v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) python_error();
   return v;
 }
-int64_t integer_attr(PyObject* o, const char* name) { return integer(attr(o, name).o); }
+int64_t integer_attr(PyObject* o, PyObject* name) { return integer(attr(o, name).o); }
 
 // Into an int32 argument; what does not fit is refused here.
 int32_t small(int64_t v, const char* what) {
@@ -155,9 +157,9 @@ struct OnStream {
       st = (dcp_stream_t)c10::cuda::getCurrentCUDAStream(dev).stream();
       return;
     }
-    if (PyObject_HasAttrString(o, "device_index") && integer_attr(o, "device_index") != dev)
+    if (PyObject_HasAttr(o, NAME("device_index")) && integer_attr(o, NAME("device_index")) != dev)
       refuse("the stream is on another device than the tensors");
-    st = (dcp_stream_t)(uintptr_t)integer_attr(o, "cuda_stream");
+    st = (dcp_stream_t)(uintptr_t)integer_attr(o, NAME("cuda_stream"));
     guard.emplace(c10::cuda::getStreamFromExternal((cudaStream_t)st, dev));
   }
 };
@@ -169,13 +171,24 @@ dcp_dtype_t dtype_of(at::ScalarType t) {
 }
 
 dcp_layout_t layout_of(PyObject* o) {
-  return dcp_layout_t{small(integer_attr(o, "dcp_size"), "dcp_size"),
-                      small(integer_attr(o, "block_size"), "block_size"),
-                      small(integer_attr(o, "interleave"), "interleave")};
+  return dcp_layout_t{small(integer_attr(o, NAME("dcp_size")), "dcp_size"),
+                      small(integer_attr(o, NAME("block_size")), "block_size"),
+                      small(integer_attr(o, NAME("interleave")), "interleave")};
 }
 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, dev));
+}
+
+// Elements [at, ...) of a buffer as a tensor of its own (a fresh one, no view of
+// anything a caller has).
+at::Tensor part(const at::Tensor& all, int64_t from, at::IntArrayRef shape, int dev) {
+  if (!all.defined()) return fresh(shape, at::kInt, dev);   // nothing in it
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()),
+                                                          all.key_set(), all.dtype());
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  t.unsafeGetTensorImpl()->set_storage_offset(from);
+  return t;
 }
 
 // The call's workspace: the caller's, or one for this call alone (the caching
@@ -257,9 +270,9 @@ PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t B = ctx.size(0);
     // the cache
     PyObject* kv = a[3];
-    Ref kp(attr(kv, "k_pools")), vp(attr(kv, "v_pools")), bto(attr(kv, "block_table"));
+    Ref kp(attr(kv, NAME("k_pools"))), vp(attr(kv, NAME("v_pools"))), bto(attr(kv, NAME("block_table")));
     if (vp.o == Py_None) refuse("the cache has no value pools");
-    const int64_t nb = integer_attr(kv, "num_blocks");
+    const int64_t nb = integer_attr(kv, NAME("num_blocks"));
     Ref kseq(PySequence_Fast(kp.o, "k_pools must be a sequence of tensors"));
     if (PySequence_Fast_GET_SIZE(kseq.o) < 1) refuse("the cache has no pools");
     const at::Tensor& first = tensor(PySequence_Fast_GET_ITEM(kseq.o, 0), "k_pools");
@@ -428,13 +441,13 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // The pages' state, from the tensors of a Pages object.
 dcp_pages_t pages_of(PyObject* o, const dcp_layout_t& L, int& dev, int64_t& tables) {
-  Ref bto(attr(o, "block_table")), sqo(attr(o, "seq_lens")), rfo(attr(o, "ref_count")),
-      fbo(attr(o, "free_bits"));
+  Ref bto(attr(o, NAME("block_table"))), sqo(attr(o, NAME("seq_lens"))), rfo(attr(o, NAME("ref_count"))),
+      fbo(attr(o, NAME("free_bits")));
   const at::Tensor& bt = tensor(bto.o, "block_table");
   dev = device_of(bt, "block_table");
   if (bt.dim() != 3) refuse("block_table must be [tables, requests, max_vblocks]");
   tables = bt.size(0);
-  const int64_t B = bt.size(1), VB = bt.size(2), nb = integer_attr(o, "num_blocks");
+  const int64_t B = bt.size(1), VB = bt.size(2), nb = integer_attr(o, NAME("num_blocks"));
   if (B * VB == 0) refuse("block_table has no entries");
   if (tables != 1 && tables != L.dcp_size)
     refuse(std::to_string(tables) + " block tables for " + std::to_string(L.dcp_size) + " ranks");
@@ -481,17 +494,25 @@ PyObject* pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t n32 = small(N, "entries");
     size_t need = 0;
     check(g_lib.pages_workspace_size(L, p, n32, &need));
-    Workspace ws(a[7], need, dev);
     int32_t* err = err_ptr(a[8], dev);
-    at::Tensor src, dst;
-    if (a[5] == Py_None) src = fresh({tables, N}, at::kInt, dev);
-    if (a[6] == Py_None) dst = fresh({tables, N}, at::kInt, dev);
-    int32_t* ps = (int32_t*)(a[5] == Py_None ? src.data_ptr()
-                                             : ptr(a[5], "copy_src", at::kInt, {tables, N}, dev));
-    int32_t* pd = (int32_t*)(a[6] == Py_None ? dst.data_ptr()
-                                             : ptr(a[6], "copy_dst", at::kInt, {tables, N}, dev));
-    check((fork ? g_lib.pages_fork : g_lib.pages_resize)(L, p, px, py, n32, ps, pd, ws.p, ws.bytes,
-                                                         err, on.st));
+    // what the caller did not bring comes in one allocation
+    const int64_t shape[2] = {tables, N}, each = tables * N;
+    const bool own_s = a[5] == Py_None, own_d = a[6] == Py_None, own_w = a[7] == Py_None;
+    const int64_t ints = (own_w ? (int64_t)need / 4 : 0) + (own_s ? each : 0) + (own_d ? each : 0);
+    at::Tensor all, src, dst;
+    if (ints > 0) all = fresh({ints}, at::kInt, dev);
+    int64_t from = own_w ? (int64_t)need / 4 : 0;
+    if (own_s) src = part(all, from, shape, dev);
+    if (own_s) from += each;
+    if (own_d) dst = part(all, from, shape, dev);
+    std::optional<Workspace> given_ws;
+    if (!own_w) given_ws.emplace(a[7], need, dev);
+    void* const pw = own_w ? all.data_ptr() : given_ws->p;
+    const size_t bytes = own_w ? need : given_ws->bytes;
+    int32_t* ps = (int32_t*)(own_s ? src.data_ptr() : ptr(a[5], "copy_src", at::kInt, shape, dev));
+    int32_t* pd = (int32_t*)(own_d ? dst.data_ptr() : ptr(a[6], "copy_dst", at::kInt, shape, dev));
+    check((fork ? g_lib.pages_fork : g_lib.pages_resize)(L, p, px, py, n32, ps, pd, pw, bytes, err,
+                                                         on.st));
     PyObject* both = PyTuple_New(2);
     if (!both) return nullptr;
     PyTuple_SET_ITEM(both, 0, a[5] == Py_None ? THPVariable_Wrap(src) : given(a[5]));
@@ -502,19 +523,19 @@ PyObject* pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // What a PoolSet holds: the device array of addresses and the pools' shape.
 dcp_pool_set_t pools_of(PyObject* o, const dcp_layout_t& L, int& dev) {
-  Ref po(attr(o, "ptr"));
+  Ref po(attr(o, NAME("ptr")));
   const at::Tensor& t = tensor(po.o, "the pool set");
   dev = device_of(t, "the pool set");
-  const int64_t ranks = integer_attr(o, "ranks"), bs = integer_attr(o, "block_size");
+  const int64_t ranks = integer_attr(o, NAME("ranks")), bs = integer_attr(o, NAME("block_size"));
   if (ranks != L.dcp_size || bs != L.block_size)
     refuse("pools of " + std::to_string(ranks) + " ranks and " + std::to_string(bs) +
            "-token pages for another layout");
   dcp_pool_set_t p = {};
   p.num_pools = small(t.size(0), "pools");
   p.ptr = (const uint64_t*)ptr(t, "the pool set", at::kLong, {t.size(0), ranks}, dev);
-  p.num_heads = small(integer_attr(o, "num_heads"), "heads");
-  p.row_bytes = small(integer_attr(o, "row_bytes"), "row_bytes");
-  p.num_blocks = integer_attr(o, "num_blocks");
+  p.num_heads = small(integer_attr(o, NAME("num_heads")), "heads");
+  p.row_bytes = small(integer_attr(o, NAME("row_bytes")), "row_bytes");
+  p.num_blocks = integer_attr(o, NAME("num_blocks"));
   return p;
 }
 
