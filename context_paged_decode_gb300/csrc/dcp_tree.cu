@@ -235,7 +235,7 @@ __device__ __forceinline__ void tg_wait() { asm volatile("cp.async.wait_group 1;
 // the shared-memory reads that feed them (those 66 us are 17 TFLOP/s; a tile's
 // products would take 43% of its cycles, its reads 60%), and on short contexts
 // latency: 2 x 11 nodes over up to 3001 tokens of 2 heads of 64 in fp32 (4.3
-// MB) take 20 to 22 us, the merge 5 of them.
+// MB) take 21 to 23 us, the merge 5 of them.
 template <typename T, int DPL, int RW>
 __global__ void __launch_bounds__(kTgWarps * 32)
 tree_generic_kernel(const __grid_constant__ TreeArgs A) {
