@@ -251,3 +251,15 @@ def test_what_a_call_allocates_belongs_to_its_stream(lib):
     got, got_lse = lib.tree_decode_gqa(*args, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(got_lse, lse)
+
+
+def test_streams_named_one_by_one(lib):
+    """The default and the current stream given by name are the call without one."""
+    L = lib.Layout(2, 16, 1)
+    pages = [lib.Pages.new(L, 4, 4, 20, stream=s) for s in (None, torch.cuda.default_stream())]
+    for p, s in zip(pages, (torch.cuda.current_stream(), None)):
+        lib.pages_resize(L, p, dev([0, 3]), dev([70, 9]), stream=s)
+        src, dst = lib.pages_fork(L, p, dev([0]), dev([2]), stream=torch.cuda.default_stream())
+        assert (src >= 0).all() and (dst >= 0).all()
+    for a in ("block_table", "seq_lens", "ref_count", "free_bits"):
+        assert torch.equal(getattr(pages[0], a), getattr(pages[1], a))
