@@ -177,7 +177,6 @@ def test_unseen_nodes_may_hold_anything(lib, dtype, G, dcp, T):
     c.round()
     out, lse = lib.tree_decode_gqa(*c.args(lib), out_dtype=F32)
     rows = [j for j in range(T) if j != bad]
-    saved = c.start.copy(), c.T, c.mask, c.q
     # rows of request 0 but the bad one
     d0 = c.expected(0)
     (o, el, wabs, size), L = d0
@@ -187,7 +186,6 @@ def test_unseen_nodes_may_hold_anything(lib, dtype, G, dcp, T):
     assert (np.abs(got - o) <= tol)[rows].all()
     assert np.isfinite(lse[:T].cpu().numpy()[rows]).all()
     assert torch.isnan(lse[bad]).all() and torch.isnan(out[bad]).all()
-    del saved
     c.check(out, lse, F32, requests=[1])
     # a finite key and infinite values: the node that sees it gets them in those columns alone
     c = Case(lib, dtype, Hkv * G, Hkv, d, dcp, 16, 1, [50, 129], [T, 5], seed=4)
