@@ -617,9 +617,10 @@ tree_merge_kernel(const __grid_constant__ TreeArgs A, bool joined) {
       float top = M;
 #pragma unroll
       for (int x = 0; x < kFly; ++x) top = fmaxf(top, e[x]);
+      // the maximum stays -inf while no part saw anything: 0 would bury parts far below it
       const float base = top == -INFINITY ? 0.f : top;
       const float f = L == 0.f ? 0.f : exp2f(M - base);
-      M = base;
+      M = top;
       L *= f;
 #pragma unroll
       for (int y = 0; y < DPL; ++y) acc[y] *= f;

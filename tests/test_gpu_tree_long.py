@@ -1,0 +1,182 @@
+"""Drafted-tree attention where work runs on: rings that go round, accumulators that are
+rescaled, units cut and joined in every way, many requests, and rows whose first parts see
+nothing.  The plan of each call is worked out on the host, so that a case is known to take
+the path that it is for."""
+import numpy as np
+import pytest
+import torch
+
+from tests import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def dev(x, dtype=np.int32):
+    return torch.from_numpy(np.asarray(x, dtype=dtype)).cuda()
+
+
+def places(n, dcp, bs, I):
+    """R.place of the tokens 0 .. n - 1 as arrays."""
+    x = np.arange(n)
+    vb, off = np.divmod(x, bs * dcp)
+    run = off // I
+    return run % dcp, vb, run // dcp * I + off % I
+
+
+class Case:
+    """Requests of ctx cached tokens and T nodes; every row of the pools holds a number."""
+
+    def __init__(self, lib, dtype, Hq, Hkv, d, dcp, bs, I, ctx, T, seed=0, scale=None):
+        rng = self.rng = np.random.default_rng(seed)
+        self.dtype, self.dims = dtype, (Hq, Hkv, d, dcp, bs, I)
+        self.ctx, self.T = [int(n) for n in ctx], [int(t) for t in T]
+        self.layout = lib.Layout(dcp, bs, I)
+        self.bt, self.nb = R.random_tables(rng, [c + t for c, t in zip(ctx, T)], dcp, bs)
+        gen = torch.Generator().manual_seed(seed)
+        mk = lambda *s: torch.randn(s, generator=gen).to(dtype)  # noqa: E731
+        self.k, self.v = (mk(dcp, self.nb, Hkv, bs, d) for _ in range(2))
+        self.start = np.concatenate([[0], np.cumsum(T)]).astype(np.int32)
+        self.N = int(self.start[-1])
+        self.q = mk(self.N, Hq, d)
+        self.mask = []
+        for t in T:   # each node sees itself and what one of the four before it sees
+            own = []
+            for j in range(t):
+                own.append((own[rng.integers(max(0, j - 4), j)] if j else 0) | 1 << j)
+            self.mask += own
+        self.scale = scale or d ** -0.5
+
+    def at(self, b, n=None):
+        """(rank, page, place) of request b's tokens."""
+        r, vb, loc = places(self.ctx[b] + self.T[b] if n is None else n, *self.dims[3:])
+        return r, self.bt[r, b, vb], loc
+
+    def args(self, lib, bt=None, most=None):
+        kv = lib.PagedKV(list(self.k.cuda()), list(self.v.cuda()),
+                         dev(self.bt if bt is None else bt), self.nb)
+        m = np.array(self.mask, dtype=np.uint64).view(np.int64)
+        return (self.layout, self.q.cuda(), kv, dev(self.start), dev(self.ctx),
+                torch.from_numpy(m).cuda(), self.scale, most or max(max(self.T), 1))
+
+    def seen(self, b):
+        n, T, s0 = self.ctx[b], self.T[b], self.start[b]
+        out = np.ones((T, n + T), dtype=bool)
+        for t in range(T):
+            for j in range(T):
+                out[t, n + j] = (self.mask[s0 + t] >> j) & 1
+        return out
+
+    def check(self, out, lse, out_dtype, rank=None, sink=None, there=None, requests=None,
+              columns=None):
+        """Every row against 64 bits; `there`(b): which of b's tokens can be read."""
+        Hq, Hkv, d, dcp, bs, I = self.dims
+        G = Hq // Hkv
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        k, v, q = (x.float().numpy() for x in (self.k, self.v, self.q))
+        for b in requests if requests is not None else range(len(self.T)):
+            if self.T[b] == 0:
+                continue
+            r, page, loc = self.at(b)
+            keep = np.ones(len(r), dtype=bool) if rank is None else r == rank
+            if there is not None:
+                keep &= there(b)
+            kb = k[r[keep], page[keep], :, loc[keep]].astype(np.float64)   # [tokens, Hkv, d]
+            vb = v[r[keep], page[keep], :, loc[keep]].astype(np.float64)
+            seen, L = self.seen(b)[:, keep], int(keep.sum())
+            rows = slice(self.start[b], self.start[b + 1])
+            for g in range(Hkv):
+                qs = q[rows, g * G:(g + 1) * G].astype(np.float64)
+                for x in range(G):
+                    h = g * G + x
+                    o, el, wabs, size = R.attend(qs[:, x], kb[:, g], vb[:, g], seen, self.scale,
+                                                 None if sink is None else float(sink[h]))
+                    tol = R.attend_tol(self.dtype, out_dtype, o, wabs, size, d, L)
+                    ok = np.abs(out[rows, h] - o) <= tol
+                    if columns is not None:
+                        ok = ok[:, columns]
+                    assert ok.all(), (b, h, rank, np.argwhere(~ok)[:3])
+                    empty = np.isneginf(el)
+                    assert np.array_equal(np.isneginf(lse[rows, h]), empty), (b, h, rank)
+                    off = np.abs(lse[rows, h][~empty] - el[~empty])
+                    assert (off <= R.lse_tol(el, size, d, L)[~empty]).all(), (b, h, rank, off.max())
+
+
+def plan(c, tc, per_rank=False, most=None):
+    """The work of a call, as the kernels lay it out: (run, unit, first tile, tiles, whole)
+    of every piece, and the number of runs."""
+    Hq, Hkv, d, dcp, bs, I = c.dims
+    G, most = Hq // Hkv, most or max(c.T)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    if tc:
+        nodes = 128 // G
+        rows, chunk, tile, parts = (1 if most <= nodes else 2) * nodes * G, 16, 128, sms
+        extra = 2 + (1 if per_rank else dcp)
+    else:
+        rows, chunk, tile, parts, extra = (16 if most * G <= 16 else 32) // G * G, 64, 64, 2 * sms, 0
+    entries = []
+    for b, (n, T) in enumerate(zip(c.ctx, c.T)):
+        held = np.bincount(places(n + T, dcp, bs, I)[0], minlength=dcp) if T else np.zeros(dcp, int)
+        for group in ([[r] for r in range(dcp)] if per_rank else [range(dcp)]):
+            chunks = sum(-(-int(held[r]) // chunk) for r in group)
+            per = -(-chunks // (tile // chunk))
+            entries.append((Hkv * -(-T * G // rows) if per else 0, per))
+    tiles = sum(u * p for u, p in entries)
+    extra = min(extra, tiles // parts)
+    total = tiles + extra * sum(u for u, _ in entries)
+    parts = min(parts, total)
+    pieces, at, unit = [], 0, 0
+    for u, per in entries:
+        for _ in range(u):
+            t = at
+            while t < at + per:
+                run = ((t + 1) * parts - 1) // total
+                end = min(total * (run + 1) // parts, at + per)
+                pieces.append((run, unit, t - at, end - t, t == at and end == at + per))
+                t = end
+            at += per + extra
+            unit += 1
+    return pieces, parts
+
+
+@pytest.mark.parametrize("most", [4, 64])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_first_parts_that_saw_nothing(lib, dtype, most):
+    """A unit in many parts, of which the first have only pages that cannot be used, and scores
+    near -120: a part that saw nothing sets no maximum for those behind it.  (Up to 2048 rows
+    of max_tree nodes two warps join a row's parts, beyond that one.)"""
+    Hq, Hkv, d, bs, n = 48, 3, 64, 16, 6000
+    c = Case(lib, dtype, Hq, Hkv, d, 1, bs, 1, [n], [2], seed=most, scale=0.125)
+    assert (most * Hq > 2048) == (most == 64)
+    c.q = torch.ones_like(c.q)
+    c.k = (-15.0 + 0.25 * c.k.float()).to(dtype)
+    pieces, _ = plan(c, dtype == BF16, most=most)
+    tile = 128 if dtype == BF16 else 64
+    # everything before the last ten parts is gone
+    gone = (max(t for _, u, t, _, _ in pieces if u == 0) - 9) * tile // bs
+    assert len([p for p in pieces if p[1] == 0 and p[2] * tile < gone * bs]) > 20
+    bt = c.bt.copy()
+    bt[0, 0, :gone] = -1
+    there = lambda b: np.arange(n + 2) >= gone * bs  # noqa: E731
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for sink in (None, torch.full((Hq,), -125.0, device="cuda")):
+        out, lse = lib.tree_decode_gqa(*c.args(lib, bt, most), sink=sink, out_dtype=F32, err=err)
+        c.check(out, lse, F32, there=there, sink=None if sink is None else sink.cpu().numpy())
+    assert err.item() > 0
+    po, pl = lib.tree_partial_gqa(*c.args(lib, bt, most))
+    c.check(po[0], pl[0], F32, there=there)
+
+
+@pytest.mark.parametrize("offset", [0.0, -15.0])
+def test_nodes_of_many_ranks_that_see_themselves_alone(lib, offset):
+    """No context, 64 nodes on 16 ranks that see only themselves, and units of six parts: most
+    parts of a row saw nothing, the first ones among them."""
+    c = Case(lib, F32, 33, 33, 64, 16, 16, 1, [0], [64], scale=0.125)
+    c.mask = [1 << j for j in range(64)]
+    c.q = torch.ones_like(c.q)
+    c.k = offset + 0.25 * c.k
+    pieces, _ = plan(c, False)
+    assert 64 * 33 > 2048 and max(np.bincount([u for _, u, *_ in pieces])) > 4
+    out, lse = lib.tree_decode_gqa(*c.args(lib))
+    c.check(out, lse, F32)
