@@ -72,6 +72,12 @@ constexpr int kTtThreads = 384;
 constexpr int kHalfBytes = kTtTile * 128;    // 64 columns of a tile or of a query block
 constexpr float kTtGrow = 8.f;               // log2 units
 constexpr int kTtStuck = 1 << 20;
+// Places of the flag that says that a unit's values were cleaned, one unit after
+// another.  The value warp comes to unit i + 2 when the scores of unit i + 1 are
+// done, which the row writes of unit i may not be (with a tile or two a unit no
+// wait for them lies between), so two places are too few.  It comes to unit
+// i + 3 after the scores of i + 2, which are issued behind the wait for unit i.
+constexpr int kTtFlags = 3;
 
 template <int D, bool kTwo>
 struct TreeTc {
@@ -83,8 +89,8 @@ struct TreeTc {
   static constexpr int kVOff = kKSlots * kSlot;
   static constexpr int kQOff = kVOff + kVSlots * kSlot;
   static constexpr int kMlOff = kQOff + kQ;                 // float2 [2 stream][128]
-  static constexpr int kFlagOff = kMlOff + 2 * 128 * 8;     // int [2 parity], joins
-  static constexpr int kPlanOff = kFlagOff + 16;            // TreeSelf
+  static constexpr int kFlagOff = kMlOff + 2 * 128 * 8;     // int [kTtFlags], joins
+  static constexpr int kPlanOff = kFlagOff + 4 * (kTtFlags + 1);   // TreeSelf
   static constexpr int kBarOff = kPlanOff + (int)sizeof(TreeSelf);
   static constexpr int kBars = 2 * kKSlots + 3 * kVSlots + 8;
   static constexpr int kSmem = kBarOff + 8 * kBars + 8;
@@ -369,7 +375,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
     mbar_init(b_q, 1);
     mbar_init(b_qfree, 1);
     fence_mbar_init();
-    flag[0] = flag[1] = 0;
+    for (int i = 0; i < kTtFlags; ++i) flag[i] = 0;
     prefetch_tmap(&X.qmap);
     for (int r = 0; r < A.L.dcp; ++r) {
       prefetch_tmap(&X.kmap[r]);
@@ -543,7 +549,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
                         odd = true;
                       }
                     }
-                    if (odd) flag[item & 1] = (int)item + 1;
+                    if (odd) flag[item % kTtFlags] = (int)item + 1;
                   }
                   if (odd)
                     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]),
@@ -818,7 +824,7 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
       // for every warp to have left this one)
       ml[s * 128 + row] = make_float2(m, l);
       bar_sync(3, 256);
-      const bool odd = flag[item & 1] == (int)item + 1;
+      const bool odd = flag[item % kTtFlags] == (int)item + 1;
       if (!dead && mine && takes) {
         const float mb = m == -INFINITY ? 0.f : m;
         float M = mb, L = l, a0 = 1.f, a1 = 0.f;
@@ -932,11 +938,11 @@ tree_tc_kernel(const __grid_constant__ TreeTcArgs X) {
         bar_sync(3, 256);
         if (threadIdx.x == 128) {
           const int before = atomicAdd(A.arrived + k0, 1);
-          flag[2] = before == k1 - k0;
+          flag[kTtFlags] = before == k1 - k0;
           __threadfence();
         }
         bar_sync(3, 256);
-        if (flag[2])
+        if (flag[kTtFlags])
           tree_join<D>(A, p, k0, k1, tree_run(walk.total, walk.parts, k0) != p.u0, nrows, warp - 4);
       }
     }

@@ -140,6 +140,39 @@ def plan(c, tc, per_rank=False, most=None):
     return pieces, parts
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [3, 40])
+def test_values_that_are_not_finite_in_many_short_units(lib, d, T):
+    """Units of one tile, several to a run, each with an infinite and a NaN value in a node that
+    one other node sees: those two rows get them, in those columns, and no others do."""
+    B = 400
+    rng = np.random.default_rng(d + T)
+    c = Case(lib, BF16, 8, 2, d, 2, 16, 1, rng.integers(0, 40, B), [T] * B, seed=T)
+    pieces, parts = plan(c, True)
+    assert max(n for _, _, _, n, _ in pieces) == 1 and len(pieces) >= 4 * parts
+    bad, other = T // 2, T - 1
+    for b in range(B):
+        s0 = c.start[b]
+        for j in range(T):
+            c.mask[s0 + j] &= ~(1 << bad)
+        c.mask[s0 + bad] |= 1 << bad
+        c.mask[s0 + other] |= 1 << bad
+        r, page, loc = c.at(b)
+        x = c.ctx[b] + bad
+        c.v[r[x], page[x], :, loc[x], 5] = float("inf")
+        c.v[r[x], page[x], :, loc[x], d - 3] = float("nan")
+    finite = [i for i in range(d) if i not in (5, d - 3)]
+    for _ in range(5):
+        out, lse = lib.tree_decode_gqa(*c.args(lib), out_dtype=F32)
+        got = out.view(B, T, 8, d)
+        sees = torch.zeros(T, dtype=torch.bool, device="cuda")
+        sees[[bad, other]] = True
+        assert (got[:, sees][..., 5] == float("inf")).all()
+        assert torch.isnan(got[:, sees][..., d - 3]).all()
+        assert torch.isfinite(got[:, ~sees]).all() and torch.isfinite(got[..., finite]).all()
+    c.check(out, lse, F32, columns=finite, requests=range(0, B, 7))
+
+
 @pytest.mark.parametrize("most", [4, 64])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_first_parts_that_saw_nothing(lib, dtype, most):
