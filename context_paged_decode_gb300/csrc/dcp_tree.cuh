@@ -53,8 +53,9 @@ struct TreeArgs {
   int32_t* arrived;          // [parts] partials there of the unit whose first run it is
 };
 
-// One request's units (on one rank, for partials), in one 32-byte read.
-struct __align__(32) TreeEntry {
+// One request's units (on one rank, for partials), in two 16-byte reads: a
+// workspace is aligned to 16 bytes and no more, and so is a plan in shared memory.
+struct __align__(16) TreeEntry {
   int64_t tile0;   // first tile of its units
   int32_t units;   // 0: none (refused, no nodes, or nothing on the rank)
   int32_t per;     // tiles of a unit
@@ -63,6 +64,7 @@ struct __align__(32) TreeEntry {
   int32_t q0;      // first token
   int32_t pad;
 };
+static_assert(sizeof(TreeEntry) == 32 && alignof(TreeEntry) == 16, "two 16-byte pieces");
 
 __device__ __forceinline__ TreeEntry tree_load(const TreeArgs& A, int e) {
   const int4* p = reinterpret_cast<const int4*>(A.entry + e);

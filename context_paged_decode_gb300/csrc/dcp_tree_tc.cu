@@ -94,7 +94,8 @@ struct TreeTc {
   static constexpr int kBarOff = kPlanOff + (int)sizeof(TreeSelf);
   static constexpr int kBars = 2 * kKSlots + 3 * kVSlots + 8;
   static constexpr int kSmem = kBarOff + 8 * kBars + 8;
-  static_assert(kSmem <= 227 * 1024 && kBarOff % 8 == 0, "shared memory");
+  static_assert(kSmem <= 227 * 1024 && kBarOff % 8 == 0 && kPlanOff % alignof(TreeSelf) == 0,
+                "shared memory");
   static constexpr uint32_t kColS = 0, kColO = 256;         // two of each, 128 and D apart
 };
 

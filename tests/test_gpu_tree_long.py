@@ -213,3 +213,20 @@ def test_nodes_of_many_ranks_that_see_themselves_alone(lib, offset):
     assert 64 * 33 > 2048 and max(np.bincount([u for _, u, *_ in pieces])) > 4
     out, lse = lib.tree_decode_gqa(*c.args(lib))
     c.check(out, lse, F32)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B", [3, 40])
+def test_a_workspace_aligned_to_sixteen_bytes(lib, dtype, B):
+    """And to no more, with a plan made by the kernel's CTAs (3 requests) and one by itself."""
+    c = Case(lib, dtype, 8, 2, 64, 2, 16, 1, [90 + b for b in range(B)], [1 + b % 9 for b in range(B)])
+    need = lib.tree_workspace_size(c.layout, B, 9, 8, 2, 64, dtype)
+    room = torch.empty(need + 64, dtype=torch.uint8, device="cuda")
+    args = c.args(lib)
+    want = lib.tree_decode_gqa(*args)
+    c.check(*want, dtype)
+    for off in (0, 16, 32, 48):
+        ws = room[off:off + need]
+        assert ws.data_ptr() % 64 == off
+        got = lib.tree_decode_gqa(*args, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
