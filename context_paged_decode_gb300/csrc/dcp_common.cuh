@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "dcp.h"
 
 #ifndef DCP_NO_NVTX
@@ -25,6 +27,28 @@ inline bool layout_ok(const dcp_layout_t& L) {
 inline bool ranks_ok(const dcp_rank_ptrs_t& p, int dcp) {
   for (int r = 0; r < dcp; ++r)
     if (p.ptr[r] == nullptr) return false;
+  return true;
+}
+
+// Bytes at an address (NULL: none).
+struct Bytes {
+  const void* p;
+  int64_t n;
+};
+
+inline bool overlap(const Bytes& a, const Bytes& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return a.p && b.p && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+}
+
+// What a call writes lies apart from what it reads and from what else it writes.
+inline bool apart(std::initializer_list<Bytes> written, std::initializer_list<Bytes> read) {
+  for (auto a = written.begin(); a != written.end(); ++a) {
+    for (auto b = a + 1; b != written.end(); ++b)
+      if (overlap(*a, *b)) return false;
+    for (const Bytes& b : read)
+      if (overlap(*a, b)) return false;
+  }
   return true;
 }
 

@@ -487,6 +487,24 @@ static int launch_rope(RopeArgs& A, int rot, int rot_at, int d, int es, bool int
 static inline int elem_bytes(dcp_dtype_t d) { return d == DCP_F32 ? 4 : (d == DCP_BF16 ? 2 : 0); }
 static inline bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
+// Rows of `row` bytes, one for each token, `stride` bytes apart.
+struct TokenRows {
+  const void* p;
+  int64_t stride, row;
+};
+
+// Whether the packed rows of an output lie over rows of an input: CTAs read and
+// write different tokens at the same time, so that is refused, but for an output
+// that is the input itself, token by token (`same`: where the rows hold the same heads).
+static bool rows_clash(const void* out, int64_t row, const TokenRows& in, int64_t T, bool same) {
+  if (!out || !in.p || row <= 0 || in.row <= 0) return false;
+  const int64_t off = (int64_t)((uintptr_t)out - (uintptr_t)in.p);
+  if (same && off == 0 && (T == 1 || in.stride == row)) return false;
+  // the first token whose row ends behind the output's start
+  const int64_t i = off < in.row ? 0 : (off - in.row) / in.stride + 1;
+  return i < T && i * in.stride < off + T * row;
+}
+
 // Checks shared by both entry points; DCP_OK when the shape can run.
 static int rope_shape(const dcp_layout_t& L, int64_t T, int Hq, int Hk, int d, int es, int rot,
                       int axes, int64_t num_blocks) {
@@ -532,6 +550,18 @@ int dcp_rope_write_gqa(dcp_layout_t layout, const void* q, int64_t q_stride, con
     return DCP_EUNSUPPORTED;
   for (int r = 0; r < layout.dcp_size; ++r)
     if (!al16(k_cache.ptr[r]) || !al16(v_cache.ptr[r])) return DCP_EUNSUPPORTED;
+  const int64_t T = num_tokens, half = rot_dim / 2, qr = (int64_t)num_q_heads * head_dim * es,
+                kr = (int64_t)num_kv_heads * head_dim * es;
+  const TokenRows tq{num_q_heads > 0 ? q : nullptr, q_stride * es, qr}, tk{k, k_stride * es, kr},
+      tv{v, v_stride * es, kr};
+  if (num_q_heads == 0) q_out = nullptr;
+  if (rows_clash(q_out, qr, tq, T, true) || rows_clash(q_out, qr, tk, T, false) ||
+      rows_clash(q_out, qr, tv, T, false) || rows_clash(k_out, kr, tk, T, true) ||
+      rows_clash(k_out, kr, tq, T, false) || rows_clash(k_out, kr, tv, T, false) ||
+      !apart({{q_out, T * qr}, {k_out, T * kr}},
+             {{positions, num_axes * T * 8}, {inv_freq, half * 4}, {axis, half * 4},
+              {slot, layout.dcp_size * T * 8}}))
+    return DCP_EINVAL;
   RopeArgs A;
   A.q = (const uint4*)q;
   A.k = (const uint4*)k;
@@ -580,6 +610,13 @@ int dcp_rope_write_mla(dcp_layout_t layout, const void* q, int64_t q_stride, con
     return DCP_EUNSUPPORTED;
   for (int r = 0; r < layout.dcp_size; ++r)
     if (!al16(cache.ptr[r])) return DCP_EUNSUPPORTED;
+  const int64_t T = num_tokens, half = rot_dim / 2, qr = (int64_t)num_q_heads * kv_dim * es;
+  if (num_q_heads == 0) q_out = nullptr;
+  if (rows_clash(q_out, qr, {q, q_stride * es, qr}, T, true) ||
+      rows_clash(q_out, qr, {kv, kv_stride * es, (int64_t)kv_dim * es}, T, false) ||
+      !apart({{q_out, T * qr}}, {{positions, num_axes * T * 8}, {inv_freq, half * 4},
+                                 {axis, half * 4}, {slot, layout.dcp_size * T * 8}}))
+    return DCP_EINVAL;
   RopeArgs A;
   A.q = (const uint4*)q;
   A.k = (const uint4*)kv;

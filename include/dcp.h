@@ -554,7 +554,9 @@ int dcp_tree_workspace_size(dcp_layout_t layout, int32_t num_reqs, int32_t max_t
  * to about 2^-31 of a turn for positions up to 2^32.
  *  q, k, v    [num_tokens][heads][head_dim] of dtype; *_stride elements between
  *             tokens (slices of one fused projection), heads in one piece.
- *             num_q_heads may be 0 (q, q_out unused).  q_out may be q.
+ *             num_q_heads may be 0 (q, q_out unused).  q_out may be a packed q
+ *             (q_stride = num_q_heads * head_dim) itself, and k_out a packed k;
+ *             otherwise what is written may not lie over what is read.
  *  positions  [num_axes][num_tokens] int64 (time, height, width, ...).
  *  inv_freq   [rot_dim/2] float32; axis [rot_dim/2] int32, or NULL (axis 0).
  *             An axis outside [0, num_axes) counts as 0 and bumps err_count.

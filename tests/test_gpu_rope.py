@@ -208,3 +208,42 @@ def test_refusals(lib):
     call(q=torch.randn((T, 4, d + 4), device="cuda").to(BF16)[..., 4:])   # heads apart
     odd = torch.randn((T * 4 * d + 1), device="cuda").to(BF16)[1:].view(T, 4, d)
     call(q=odd)                                                 # not 16-byte aligned
+
+
+@pytest.mark.parametrize("T,rot", [(1, 64), (1, 128), (40, 64), (40, 128), (3000, 128)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_packed_inputs_rotated_in_place(lib, dtype, T, rot):
+    """q_out and k_out that are q and k themselves, rotated in whole or in part; of a single
+    token also when they are slices of one projection."""
+    Hq, Hkv, d, dcp, bs = 4, 2, 128, 2, 16
+    L, nb = lib.Layout(dcp, bs, 1), T // bs + 2
+    rng = np.random.default_rng(T)
+    slot = torch.from_numpy(slots(rng, T, dcp, nb, bs)).cuda()
+    inv = torch.from_numpy(inv_freqs(rot // 2)).cuda()
+    pos = torch.from_numpy(rng.integers(0, 1 << 20, T)).cuda()
+    x = torch.randn((T, Hq + 2 * Hkv, d), generator=torch.Generator().manual_seed(T)).to(dtype).cuda()
+    q, k, v = x.split([Hq, Hkv, Hkv], 1)
+    if T > 1:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    want_k, p, p2 = torch.empty_like(k), *[pools(dcp, (nb, Hkv, bs, d), dtype) for _ in range(2)]
+    vp, vp2 = (pools(dcp, (nb, Hkv, bs, d), dtype) for _ in range(2))
+    want = lib.rope_write_gqa(L, q, k, v, pos, inv, slot, p, vp, nb, k_out=want_k)
+    lib.rope_write_gqa(L, q, k, v, pos, inv, slot, p2, vp2, nb, q_out=q, k_out=k)
+    assert torch.equal(q, want) and torch.equal(k, want_k)
+    for a, b in zip(p + vp, p2 + vp2):
+        assert torch.equal(a, b)
+
+
+def test_outputs_over_inputs_are_refused(lib):
+    T, d, nb = 4, 64, 2
+    L = lib.Layout(1, 16, 1)
+    slot = torch.full((1, T), -1, dtype=torch.int64).cuda()
+    inv, pos = torch.from_numpy(inv_freqs(32)).cuda(), torch.zeros(T, dtype=torch.int64).cuda()
+    x = torch.randn((T, 6, d), device="cuda")
+    q, k, v = x.split([2, 2, 2], 1)
+    p = pools(1, (nb, 2, 16, d), F32)
+    over = x.view(-1)[:T * 2 * d].view(T, 2, d)           # packed, over the projection
+    other = torch.empty((T, 2, d), device="cuda")
+    for q_out, k_out in ((over, None), (None, over), (other, other)):
+        with pytest.raises(lib.DcpError):
+            lib.rope_write_gqa(L, q, k, v, pos, inv, slot, p, p, nb, q_out=q_out, k_out=k_out)

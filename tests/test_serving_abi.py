@@ -201,3 +201,34 @@ def test_outputs_over_inputs_and_odd_workspaces(dcp):
         L, pools, P, 2, 4, 8, P, Q, P, 4, new, None, None)
     assert move(P) == EINVAL and move(odd(4)) == EINVAL and move(odd(-4)) == EINVAL
     assert move(None, dcp.Layout(4, 1 << 29, 1)) == EUNSUPPORTED
+
+
+def test_rotated_rows_over_their_inputs(dcp):
+    """CTAs read some tokens while others are written: an output may be its own input, packed,
+    and nothing else."""
+    lib, L = dcp.load(), dcp.Layout(2, 16, 1)
+    at = lambda n: C.c_void_p((1 << 24) + n)  # noqa: E731
+    far = [C.c_void_p(x << 20) for x in (1, 2, 3, 4)]
+    row, kr = 8 * 128 * 2, 2 * 128 * 2          # bytes of a token's queries and keys
+
+    def gqa(q_out, k_out=None, q=at(0), qs=1024, k=far[0], ks=256, v=far[1], vs=256, T=3, inv=far[2]):
+        return lib.dcp_rope_write_gqa(L, q, qs, k, ks, v, vs, T, 8, 2, 128, 1, far[2], 1, inv, None,
+                                      128, 0, 1.0, far[3], 8, ranks(dcp, 2), ranks(dcp, 2), q_out,
+                                      k_out, None, None)
+
+    wide = 8 * 128 + 4 * 128                    # elements of a token in a fused projection
+    assert gqa(at(0), qs=wide) == EINVAL                            # the slice itself
+    assert gqa(at(16)) == EINVAL and gqa(at(-16)) == EINVAL         # a packed q, off by a little
+    assert gqa(at(3 * row - 16)) == EINVAL and gqa(at(16 - 3 * row)) == EINVAL
+    for kw in (dict(k=at(row), v=at(row + kr)), dict(k=at(row), v=far[1]), dict(k=far[0], v=at(row))):
+        assert gqa(at(0), q=far[1], ks=wide, vs=wide, **kw) == EINVAL   # over keys or values
+    assert gqa(far[1], at(0), qs=wide) == EINVAL and gqa(at(1 << 23), far[1]) == EINVAL
+    assert gqa(at(1 << 23), far[0], ks=512) == EINVAL               # keys that are not packed
+    assert gqa(at(1 << 23), at((1 << 23) + 16)) == EINVAL           # outputs over one another
+    for x in (far[2], far[3], C.c_void_p((2 << 20) + 16)):
+        assert gqa(x) == EINVAL
+    mla = lambda q_out, qs=8 * 576, ks=576, kv=far[0], T=3: lib.dcp_rope_write_mla(  # noqa: E731
+        L, at(0), qs, kv, ks, T, 8, 576, 1, far[2], 1, far[2], None, 64, 1, 1.0, far[3], 8,
+        ranks(dcp, 2), q_out, None, None)
+    assert mla(at(0), qs=9 * 576) == EINVAL and mla(at(0), kv=at(8 * 576 * 2), ks=9 * 576) == EINVAL
+    assert mla(at(32)) == EINVAL and mla(far[0]) == EINVAL and mla(far[3]) == EINVAL
