@@ -460,7 +460,22 @@ static int launch_pages(const dcp_layout_t& L, const dcp_pages_t& p, const int32
   A.new_len = A.sums + DCP_MAX_RANKS * kPgCluster;
   A.err = err;
   if (!ws || ws_bytes < pages_ws_bytes(N) || ((uintptr_t)ws & 3)) return DCP_EWORKSPACE;
-  if (src == dst) return DCP_EINVAL;
+  // Other CTAs still read the list while these are written, and the lengths are
+  // stored by its requests at the end: a list that changes meanwhile would name
+  // requests that were never checked.  (New lengths are read before any are
+  // stored, so the state's own may be the list.)
+  const int64_t list = (int64_t)N * 4, T = tables;
+  const Bytes state[4] = {
+      {p.block_table, ((T - 1) * p.bt_rank_stride + (int64_t)p.num_reqs * p.max_vblocks) * 4},
+      {p.ref_count, T * p.num_blocks * 4},
+      {p.free_bits, T * A.words * 4},
+      {p.seq_lens, (int64_t)p.num_reqs * 4}};
+  const Bytes which{row, list}, other{kFork ? up : len, list};
+  if (!apart({{src, T * list}, {dst, T * list}, {ws, (int64_t)pages_ws_bytes(N)}},
+             {which, other, state[0], state[1], state[2], state[3]}) ||
+      !apart({state[0], state[1], state[2], state[3]}, {which}) ||
+      !apart({state[0], state[1], state[2]}, {other}))
+    return DCP_EINVAL;
   const size_t smem = pages_smem(N, A.hash);
   if (!allow_smem<pages_kernel<kFork>>()) return DCP_ECUDA;
   const unsigned ctas = A.alone ? kPgCluster : (unsigned)(tables * kPgCluster);

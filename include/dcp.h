@@ -599,6 +599,8 @@ int dcp_rope_write_mla(dcp_layout_t layout, const void* q, int64_t q_stride, con
  * table.  The page that the next token is written to (the open page, unless it
  * is full) is always the request's own.  max_vblocks*block_size*dcp_size < 2^31.
  * A call changes the state, so calls on one state run one after the other.
+ * The lists, the copies asked for, the workspace and the state lie apart from
+ * one another, but for new_lens, which may be seq_lens.
  */
 typedef struct {
   int32_t* block_table;

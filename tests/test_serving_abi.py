@@ -232,3 +232,28 @@ def test_rotated_rows_over_their_inputs(dcp):
         ranks(dcp, 2), q_out, None, None)
     assert mla(at(0), qs=9 * 576) == EINVAL and mla(at(0), kv=at(8 * 576 * 2), ks=9 * 576) == EINVAL
     assert mla(at(32)) == EINVAL and mla(far[0]) == EINVAL and mla(far[3]) == EINVAL
+
+
+def test_lists_of_pages_lie_apart(dcp):
+    """A list that the call itself writes over would name requests that were never checked."""
+    lib, L = dcp.load(), dcp.Layout(2, 16, 1)
+    at = lambda mib, off=0: C.c_void_p((mib << 20) + off)  # noqa: E731
+    # 4 requests of 8 pages, 2 tables of 100 pages
+    state = dict(block_table=1, seq_lens=2, ref_count=3, free_bits=4)
+    pages = dcp.PagesStruct(*(x << 20 for x in state.values()), 4, 8, 32, 100)
+    size = dict(block_table=256, seq_lens=16, ref_count=800, free_bits=32)
+
+    def call(name, a=at(5), b=at(6), src=at(7), dst=at(8), ws=at(9)):
+        return getattr(lib, "dcp_pages_" + name)(L, pages, a, b, 3, src, dst, ws, 1 << 20, None, None)
+
+    for name in ("resize", "fork"):
+        row = "a" if name == "resize" else "b"       # the requests that change
+        for a, b in (("src", "dst"), ("src", "a"), ("src", "b"), ("dst", "a"), ("dst", "b"),
+                     ("ws", "a"), ("ws", "b"), ("src", "ws"), ("dst", "ws")):
+            assert call(name, **{a: at(20), b: at(20, 8)}) == EINVAL, (a, b)
+            assert call(name, **{b: at(20), a: at(20, 8)}) == EINVAL, (a, b)
+        for what, mib in state.items():
+            end = at(mib, size[what] - 4)
+            for arg in ("src", "dst", "ws", row) + (() if what == "seq_lens" else ("a", "b")):
+                assert call(name, **{arg: at(mib)}) == EINVAL, (what, arg)
+                assert call(name, **{arg: end}) == EINVAL, (what, arg)
