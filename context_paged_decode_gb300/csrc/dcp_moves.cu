@@ -244,8 +244,12 @@ int dcp_cache_compact(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* 
   if ((pools.num_pools > 0 && !pools.ptr) || !block_table || !ctx_lens || !path_len ||
       (max_path > 0 && !path))
     return DCP_EINVAL;
-  // every CTA of a request reads its length, and one stores the new one
-  if (new_lens && new_lens < ctx_lens + num_reqs && ctx_lens < new_lens + num_reqs)
+  // every CTA of a request reads its length, its path and its table, and one stores the new length
+  const int64_t each = (int64_t)num_reqs * 4;
+  if (!apart({{new_lens, each}},
+             {{ctx_lens, each}, {path_len, each}, {path, each * max_path},
+              {block_table, (layout.dcp_size - 1) * bt_rank_stride * 4 + each * max_vblocks},
+              {pools.ptr, (int64_t)pools.num_pools * layout.dcp_size * 8}}))
     return DCP_EINVAL;
   CompactTokArgs A;
   A.L = Layout{layout.dcp_size, layout.block_size, layout.interleave};

@@ -685,7 +685,8 @@ int dcp_pages_copy(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* cop
  * position ctx_lens[b] + i, for i < path_len[b].
  *  path     [num_reqs][max_path] int32, strictly increasing from >= 0.
  *  path_len [num_reqs] int32, 0 .. max_path.
- *  new_lens [num_reqs] int32 or NULL: ctx_lens[b] + nodes kept; not ctx_lens.
+ *  new_lens [num_reqs] int32 or NULL: ctx_lens[b] + nodes kept; apart from all
+ *           that the call reads.
  * The moves of a request stop at the first entry that breaks the order or does
  * not resolve to a stored token, which bumps err_count once.  A bad length
  * keeps nothing and counts once.

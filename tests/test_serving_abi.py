@@ -257,3 +257,15 @@ def test_lists_of_pages_lie_apart(dcp):
             for arg in ("src", "dst", "ws", row) + (() if what == "seq_lens" else ("a", "b")):
                 assert call(name, **{arg: at(mib)}) == EINVAL, (what, arg)
                 assert call(name, **{arg: end}) == EINVAL, (what, arg)
+
+
+def test_new_lengths_lie_apart_from_what_a_compaction_reads(dcp):
+    lib, L = dcp.load(), dcp.Layout(2, 16, 1)
+    at = lambda mib, off=0: C.c_void_p((mib << 20) + off)  # noqa: E731
+    pools = dcp.PoolSetStruct(1 << 20, 2, 2, 256, 8)
+    # 3 requests, paths of 5 entries, tables of 3 x 4 pages 16 apart, 4 pool addresses
+    move = lambda new: lib.dcp_cache_compact(  # noqa: E731
+        L, pools, at(2), 3, 4, 16, at(3), at(4), at(5), 5, new, None, None)
+    for mib, size in ((1, 4 * 8), (2, (16 + 12) * 4), (3, 12), (4, 60), (5, 12)):
+        for off in (0, size - 4, -8):
+            assert move(at(mib, off)) == EINVAL, (mib, off)
