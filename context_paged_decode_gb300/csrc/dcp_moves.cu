@@ -30,35 +30,78 @@ constexpr int kCopyDepth = 8;     // 16-byte loads in flight per thread
 // One CTA per (copy, rank, pool): a page is H * bs rows in one piece.  128 open
 // pages of 32 KB on 8 ranks in 2 pools (134 MB) take 14 us beside the launch;
 // a few pages are bound by two dependent loads, 5 us with the launch.
+//
+// Copies that touch the same page (one writes what another reads or writes) have
+// to keep the order of the list.  CTAs cannot wait for one another, so the first
+// of them does all such copies of its rank and pool, where each thread moves the
+// same 16 bytes of every page and needs no barrier.  Whether there are any is
+// found from the whole list while the first rows of the page are on their way.
 __global__ void __launch_bounds__(kCopyThreads)
 pages_copy_kernel(PoolSet P, int dcp, int tables, const int32_t* src,
                   const int32_t* dst, int n, int64_t page16, int32_t* err) {
   griddep_launch_dependents();   // the next call's first kernel may start its launch
   griddep_wait();                // launched chained: the preceding kernel completed
   const int64_t units = (int64_t)n * dcp * P.num_pools;
+  const int tid = threadIdx.x;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int pool = (int)(u % P.num_pools);
     const int r = (int)(u / P.num_pools % dcp);
     const int i = (int)(u / P.num_pools / dcp);
-    const int64_t e = (int64_t)(tables == 1 ? 0 : r) * n + i;
-    const int a = __ldcg(src + e), b = __ldcg(dst + e);
+    const int32_t* from = src + (int64_t)(tables == 1 ? 0 : r) * n;
+    const int32_t* to = dst + (int64_t)(tables == 1 ? 0 : r) * n;
+    const int a = __ldcg(from + i), b = __ldcg(to + i);
     if (a == -1 && b == -1) continue;
     uint4* base = pool_at(P, pool, dcp, r);
+    auto moves = [&](int x, int y) {   // is a copy that can be made, and has work
+      return x >= 0 && x < P.nb && y >= 0 && y < P.nb && x != y;
+    };
     if (a < 0 || a >= P.nb || b < 0 || b >= P.nb || !base) {
-      if (threadIdx.x == 0) count_error(err);
+      if (tid == 0) count_error(err);
       continue;
     }
     if (a == b) continue;
-    const uint4* from = base + a * page16;
-    uint4* to = base + b * page16;
-    for (int64_t c = threadIdx.x; c < page16; c += kCopyThreads * kCopyDepth) {
-      uint4 x[kCopyDepth];
+    // does another copy touch a page of the copy x -> y, number k? (all threads ask)
+    auto shared = [&](int x, int y, int k) {
+      bool hit = false;
+      for (int j = tid; j < n; j += kCopyThreads) {
+        const int p = __ldcg(from + j), q = __ldcg(to + j);
+        hit |= j != k && moves(p, q) && (q == x || p == y || q == y);
+      }
+      return __syncthreads_or(hit) != 0;
+    };
+    uint4 x[kCopyDepth];
+    auto load = [&](int p, int64_t c) {
 #pragma unroll
       for (int j = 0; j < kCopyDepth; ++j)
-        if (c + j * kCopyThreads < page16) x[j] = __ldcg(from + c + j * kCopyThreads);
+        if (c + j * kCopyThreads < page16) x[j] = __ldcg(base + p * page16 + c + j * kCopyThreads);
+    };
+    auto store = [&](int p, int64_t c) {
 #pragma unroll
       for (int j = 0; j < kCopyDepth; ++j)
-        if (c + j * kCopyThreads < page16) to[c + j * kCopyThreads] = x[j];
+        if (c + j * kCopyThreads < page16) base[p * page16 + c + j * kCopyThreads] = x[j];
+    };
+    load(a, tid);
+    if (n > 1 && shared(a, b, i)) {
+      int k = 0;
+      for (; k < i; ++k) {           // an earlier one does them all
+        const int p = __ldcg(from + k), q = __ldcg(to + k);
+        if (moves(p, q) && shared(p, q, k)) break;
+      }
+      if (k < i) continue;
+      for (; k < n; ++k) {
+        const int p = __ldcg(from + k), q = __ldcg(to + k);
+        if (!moves(p, q) || !shared(p, q, k)) continue;
+        for (int64_t c = tid; c < page16; c += kCopyThreads * kCopyDepth) {
+          load(p, c);
+          store(q, c);
+        }
+      }
+      continue;
+    }
+    store(b, tid);
+    for (int64_t c = tid + kCopyThreads * kCopyDepth; c < page16; c += kCopyThreads * kCopyDepth) {
+      load(a, c);
+      store(b, c);
     }
   }
 }

@@ -672,8 +672,9 @@ typedef struct {
  * dcp_pages_copy -- copy pages inside every pool of every rank, in one launch.
  *  copy_src, copy_dst [num_tables][num] (num_tables 1: the same pages on every
  *           rank; else dcp_size).  Both -1: nothing.  A page outside
- *           [0, num_blocks) or an unaligned pool is skipped and counted.  No
- *           page may be written twice or both read and written in one call.
+ *           [0, num_blocks) or an unaligned pool is skipped and counted.  Copies
+ *           of which one writes a page that another reads or writes are made in
+ *           the order of the list (and by one CTA for each rank and pool).
  */
 int dcp_pages_copy(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* copy_src,
                    const int32_t* copy_dst, int32_t num_tables, int32_t num, int32_t* err_count,

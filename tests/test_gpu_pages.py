@@ -294,3 +294,41 @@ def test_lengths_from_the_state_itself(lib):
     assert (src == -1).all() and (dst == -1).all()
     for a, b in zip(before, (pages.block_table, pages.ref_count, pages.seq_lens)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("order", ["chain", "shift", "exchange", "twice", "mixed", "long"])
+@pytest.mark.parametrize("d", [64, 576])
+def test_copies_of_the_same_pages_keep_the_order_of_the_list(lib, order, d):
+    dcp, nb, bs, pools = 2, 700, 16, 3
+    rng = np.random.default_rng(d)
+    n = np.arange(40)
+    pairs = {
+        "chain": list(zip(n, n + 1)),                       # page 0 goes everywhere
+        "shift": list(zip(n[::-1], n[::-1] + 1)),           # every page moves one up
+        "exchange": [(1, 2), (2, 1), (3, 4), (4, 5), (5, 3)],
+        "twice": [(1, 9), (2, 9), (3, 9), (9, 10), (4, 9)],
+        "mixed": [(100, 200), (5, 6), (101, 201), (-1, -1), (6, 7), (102, 202), (7, 7), (8, 6),
+                  (103, 200)] + [(300 + i, 400 + i) for i in range(50)],
+        "long": list(zip(rng.integers(0, nb, 600), rng.integers(0, nb, 600))),
+    }[order]
+    src, dst = (np.array([[p[i] for p in pairs], [p[i] for p in pairs[::-1]]]) for i in (0, 1))
+    ps = torch.randn((pools, dcp, nb, bs, d), generator=torch.Generator().manual_seed(d)).to(
+        torch.bfloat16).cuda()
+    want = ps.clone()
+    for r in range(dcp):
+        for a, b in zip(src[r], dst[r]):
+            if a >= 0:
+                want[:, r, b] = want[:, r, a].clone()
+    L, err = lib.Layout(dcp, bs, 1), torch.zeros(1, dtype=I32, device="cuda")
+    lib.pages_copy(L, lib.PoolSet([list(p) for p in ps]), dev(src), dev(dst), err=err)
+    assert torch.equal(ps, want) and err.item() == 0
+    # what cannot be copied touches nothing
+    if order == "mixed":
+        src[:, 1], dst[:, 4] = nb, -1
+        before = ps.clone()
+        lib.pages_copy(L, lib.PoolSet([list(p) for p in ps]), dev(src), dev(dst), err=err)
+        for r in range(dcp):
+            for a, b in zip(src[r], dst[r]):
+                if 0 <= a < nb and 0 <= b < nb:
+                    before[:, r, b] = before[:, r, a].clone()
+        assert torch.equal(ps, before) and err.item() == 4 * pools
