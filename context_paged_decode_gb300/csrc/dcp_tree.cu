@@ -814,7 +814,17 @@ static int tree_call(const dcp_layout_t& layout, const void* q, const int32_t* q
   A.err = err;
   const size_t need = tree_carve(&A, ws, B, layout.dcp_size, S.parts, S.rows, d);
   if (!ws || ws_bytes < need || ((uintptr_t)ws & 15)) return DCP_EWORKSPACE;
-  if (out == q) return DCP_EINVAL;   // other CTAs read the queries until the end
+  // other CTAs read the queries, lists and masks until the end
+  const int64_t rows = (per_rank ? layout.dcp_size : 1) * (int64_t)N * Hq;
+  if (!apart({{out, rows * d * (out_dtype == DCP_F32 ? 4 : 2)}, {lse, rows * 4}, {ws, (int64_t)need}},
+             {{q, (int64_t)N * Hq * d * (dtype == DCP_F32 ? 4 : 2)},
+              {q_start, (int64_t)(B + 1) * 4},
+              {ctx, (int64_t)B * 4},
+              {mask, (int64_t)N * 8},
+              {sink, (int64_t)Hq * 4},
+              {kv.block_table,
+               ((layout.dcp_size - 1) * kv.bt_rank_stride + (int64_t)B * kv.max_vblocks) * 4}}))
+    return DCP_EINVAL;
   cudaError_t e = cudaSuccess;
   if (!A.self) e = launch_chained(tree_plan_kernel, 1, kTreePlanThreads, 0, s, A);
   if (e != cudaSuccess) return launch_status_report(e);

@@ -509,9 +509,9 @@ int dcp_sfa_decode(dcp_layout_t layout, const void* q, int32_t num_reqs, int32_t
  * as in dcp_decode_gqa.
  * Supported: dtype F32 or BF16, head_dim a multiple of 32 up to 256,
  * num_q_heads / num_kv_heads <= 16, scale > 0; q, out, the workspace and the
- * pools 16-byte aligned.  out may not be q, and no other call may use the
- * workspace at the same time (two captured graphs that share one may not
- * overlap).
+ * pools 16-byte aligned.  out, out_lse and the workspace lie apart from one
+ * another and from what is read, and no other call may use the workspace at the
+ * same time (two captured graphs that share one may not overlap).
  */
 int dcp_tree_decode_gqa(dcp_layout_t layout, const void* q, const int32_t* q_start,
                         int32_t num_tokens, int32_t num_reqs, int32_t max_tree,

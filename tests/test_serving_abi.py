@@ -269,3 +269,31 @@ def test_new_lengths_lie_apart_from_what_a_compaction_reads(dcp):
     for mib, size in ((1, 4 * 8), (2, (16 + 12) * 4), (3, 12), (4, 60), (5, 12)):
         for off in (0, size - 4, -8):
             assert move(at(mib, off)) == EINVAL, (mib, off)
+
+
+def test_tree_outputs_lie_apart(dcp):
+    """From the queries, the lists, the masks and the table, which CTAs read to the end."""
+    lib, L = dcp.load(), dcp.Layout(2, 16, 1)
+    at = lambda mib, off=0: C.c_void_p((mib << 20) + off)  # noqa: E731
+    N, B, Hq, d = 5, 2, 8, 128
+    cache = kv(dcp, base=30 << 20)
+    cache.block_table = 1 << 20                  # 2 tables of 2 x 4 entries, 16 apart
+    read = {1: (16 + 8) * 4, 2: N * Hq * d * 2, 3: (B + 1) * 4, 4: B * 4, 5: N * 8, 6: Hq * 4}
+
+    def call(out=at(7), lse=at(8), ws=at(9), partial=False):
+        if partial:
+            return lib.dcp_tree_partial_gqa(L, at(2), at(3), N, B, 4, Hq, 2, d, 1.0, 1, cache, at(4),
+                                            at(5), out, lse, ws, 1 << 40, None, None)
+        return lib.dcp_tree_decode_gqa(L, at(2), at(3), N, B, 4, Hq, 2, d, 1.0, 1, cache, at(4), at(5),
+                                       at(6), out, 1, lse, ws, 1 << 40, None, None)
+
+    for partial in (False, True):
+        for mib, size in read.items():
+            if partial and mib == 6:
+                continue
+            for arg in ("out", "lse", "ws"):
+                for off in (0, (size - 1) // 16 * 16, -16):
+                    assert call(partial=partial, **{arg: at(mib, off)}) == EINVAL, (arg, mib, off)
+        for a, b in (("out", "lse"), ("out", "ws"), ("lse", "ws")):
+            assert call(partial=partial, **{a: at(20), b: at(20, 32)}) == EINVAL
+            assert call(partial=partial, **{b: at(20), a: at(20, 32)}) == EINVAL
