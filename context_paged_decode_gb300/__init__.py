@@ -647,8 +647,10 @@ class Pages:
             stream=None):
         T = 1 if shared else layout.dcp_size
         mk = lambda *shape: torch.empty(shape, dtype=torch.int32, device=device)  # noqa: E731
-        p = cls(mk(T, num_reqs, max_vblocks), mk(num_reqs), mk(T, num_blocks),
-                mk(T, (num_blocks + 31) // 32), num_blocks)
+        # memory of another stream may still be in use by work queued there
+        with torch.cuda.stream(stream):
+            p = cls(mk(T, num_reqs, max_vblocks), mk(num_reqs), mk(T, num_blocks),
+                    mk(T, (num_blocks + 31) // 32), num_blocks)
         pages_init(layout, p, stream=stream)
         return p
 

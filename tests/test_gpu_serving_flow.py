@@ -263,3 +263,25 @@ def test_streams_named_one_by_one(lib):
         assert (src >= 0).all() and (dst >= 0).all()
     for a in ("block_table", "seq_lens", "ref_count", "free_bits"):
         assert torch.equal(getattr(pages[0], a), getattr(pages[1], a))
+
+
+def test_the_state_of_new_pages_belongs_to_its_stream(lib):
+    """As above, for the tensors that Pages.new makes on a stream of the caller's."""
+    L = lib.Layout(2, 16, 1)
+    B, VB, nb = 512, 256, 1 << 18
+    side = torch.cuda.Stream()
+    want = lib.Pages.new(L, B, VB, nb)
+    names = ("block_table", "seq_lens", "ref_count", "free_bits")
+    want = [getattr(want, a).clone() for a in names]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    freed = [torch.empty_like(x) for x in want for _ in range(3)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)         # some 50 ms, then the memory is written
+    for x in freed:
+        x.fill_(77)
+    del freed, x
+    p = lib.Pages.new(L, B, VB, nb, stream=side)
+    torch.cuda.synchronize()
+    for a, w in zip(names, want):
+        assert torch.equal(getattr(p, a), w), a
