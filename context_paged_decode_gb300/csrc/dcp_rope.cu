@@ -10,9 +10,11 @@
 // The angle is needed only modulo one turn.  inv_freq / 2pi is held as a
 // 64-bit fraction of a turn (from two doubles, so that all 64 bits count), and
 // position * fraction in wrapping 64-bit integers is the angle's fraction; its
-// error is the position times 2^-65 of a turn.  A 32-bit float product loses
+// error is the position times 2^-64 of a turn.  A 32-bit float product loses
 // it (a position of 10^6 at frequency 1 is off by 0.03 rad).  The top 32 bits
-// of the fraction go to sincospif.
+// of the fraction count.  A float of them would keep 24, so the nearest quarter
+// turn is taken off them first, the rest goes to sincospif, and what the float
+// of the rest leaves turns its result by the first order.
 //
 // What bounds it: reading q, k, v and writing them once.  The heads of a token
 // are rows of one size; up to 16 KB of them (all of a token's, or a part) are
@@ -120,8 +122,25 @@ __device__ __forceinline__ uint64_t turns_of(float inv_freq) {
   const double f = (double)inv_freq;
   const double hi = f * kInv2Pi;
   const double lo = fma(f, kInv2Pi, -hi) + f * kInv2PiLow;
-  return (uint64_t)((hi - floor(hi)) * 18446744073709551616.0) +
+  return (uint64_t)rint((hi - floor(hi)) * 18446744073709551616.0) +
          (uint64_t)(int64_t)rint(lo * 18446744073709551616.0);
+}
+
+// (cos, sin) of a 64-bit fraction of a turn.  The fraction is rounded to 32 bits
+// (2^-33 of a turn); the float of at most 2^29 leaves at most 2^4 of them, a
+// turn of 2.4e-8 rad, whose second order is far below the results' bits.
+__device__ __forceinline__ float2 turned(uint64_t frac) {
+  const uint32_t top = (uint32_t)((frac + 0x80000000ull) >> 32);
+  const uint32_t quarter = (top + 0x20000000u) >> 30;
+  const int32_t rest = (int32_t)(top - (quarter << 30));       // an eighth of a turn at most
+  const float x = (float)rest;
+  const float left = (float)(rest - (int32_t)x) * 1.4629180792671596e-9f;   // pi 2^-31: in rad
+  float s, c;
+  sincospif(x * 4.656612873077393e-10f, &s, &c);               // 2^-31: in half turns
+  const float s1 = fmaf(c, left, s), c1 = fmaf(-s, left, c);
+  const float a = quarter & 1 ? s1 : c1, b = quarter & 1 ? c1 : s1;
+  // quarters 0 .. 3: (c, s), (-s, c), (-c, -s), (s, -c)
+  return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
 constexpr int kRopeThreads = 256;
@@ -236,11 +255,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const __grid_c
       ax = 0;
     }
     const uint64_t p = (uint64_t)__ldcg(A.pos + (int64_t)ax * A.T + t);
-    const uint64_t frac = p * turns_of(__ldcg(A.inv_freq + i));
-    float s, c;
-    sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
+    const float2 t1 = turned(p * turns_of(__ldcg(A.inv_freq + i)));
     constexpr int kN = kF32 ? 4 : 8;
-    cs[(i % kN) * A.ru + i / kN] = make_float2(c * A.scaling, s * A.scaling);
+    cs[(i % kN) * A.ru + i / kN] = make_float2(t1.x * A.scaling, t1.y * A.scaling);
   }
   __syncthreads();
 #pragma unroll
@@ -353,10 +370,8 @@ rope_bulk_kernel(const __grid_constant__ RopeArgs A, const RopeBulk B) {
     for (int j = 0; j < kRbPairs; ++j) {
       const int i = tid + j * kRbThreads;
       if (j * kRbThreads < A.half && i < A.half) {
-        const uint64_t frac = pos[j] * per[j];
-        float s, c;
-        sincospif((float)(int32_t)(frac >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31
-        tab[(i % kN) * A.ru + i / kN] = make_float2(c * A.scaling, s * A.scaling);
+        const float2 t1 = turned(pos[j] * per[j]);
+        tab[(i % kN) * A.ru + i / kN] = make_float2(t1.x * A.scaling, t1.y * A.scaling);
       }
       pos[j] = position(nxt < B.items ? (int)nxt : B.items, j);
     }

@@ -247,3 +247,33 @@ def test_outputs_over_inputs_are_refused(lib):
     for q_out, k_out in ((over, None), (None, over), (other, other)):
         with pytest.raises(lib.DcpError):
             lib.rope_write_gqa(L, q, k, v, pos, inv, slot, p, p, nb, q_out=q_out, k_out=k_out)
+
+
+def test_the_angle_of_far_positions(lib):
+    """Cosines and sines as they are (pairs (1, 0) in 32 bits), for positions up to 2^32: the angle
+    is exact to 2^-31 of a turn, which is 2 pi 2^-31 of their value at most; sincospi and the two
+    roundings around it stay within 3 ulp, 3 * 2^-23 of the value."""
+    T, rot = 4096, 128
+    rng = np.random.default_rng(11)
+    pos = np.concatenate([rng.integers(0, 1 << 32, T - 96), rng.integers(-(1 << 32), 0, 32),
+                          np.arange(32), (1 << 32) - 1 - np.arange(32)])
+    inv = inv_freqs(rot // 2)
+    inv[1:4] = np.float32(np.pi), np.float32(np.pi / 4), np.float32(2 * np.pi)
+    k = torch.zeros((T, 1, rot), device="cuda")
+    k[..., :rot // 2] = 1.0
+    wide = torch.zeros((T, 1, rot + 16), device="cuda")     # rotated in part: in place by itself
+    wide[..., :rot // 2] = 1.0
+    slot = torch.full((1, T), -1, dtype=torch.int64, device="cuda")
+    L, out = lib.Layout(1, 16, 1), torch.empty_like(k)
+    args = [torch.from_numpy(a).cuda() for a in (pos, inv)]
+    p, pw = pools(1, (1, 1, 16, rot), F32), pools(1, (1, 1, 16, rot + 16), F32)
+    lib.rope_write_gqa(L, None, k, k, *args, slot, p, p, 1, k_out=out)
+    lib.rope_write_gqa(L, wide, wide.clone(), wide.clone(), *args, slot, pw, pw, 1, q_out=wide)
+    x = np.zeros((T, 1, rot))
+    x[..., :rot // 2] = 1.0
+    y, _ = R.rotated(x, pos[None], inv, None, 0, False)
+    tol = 2 * np.pi * 2.0 ** -31 + 3 * 2.0 ** -23 * np.abs(y)
+    for got in (out, wide[..., :rot]):
+        off = np.abs(got.double().cpu().numpy() - y)
+        assert (off <= tol).all(), (off / tol).max()
+    assert (wide[..., rot:] == 0).all()
