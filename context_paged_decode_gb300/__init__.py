@@ -679,10 +679,13 @@ def pages_fork(layout, pages: Pages, parent, child, copy_src=None, copy_dst=None
 class PoolSet:
     """Pools of one shape (keys and values of all layers), each a list of one
     tensor per rank: [num_blocks, heads, block_size, d], or [num_blocks,
-    block_size, d] for latent rows.  Keeps the tensors and their addresses."""
+    block_size, d] for latent rows.  Keeps the tensors and their addresses.  A
+    pool named more than once (layers that share a cache) counts once."""
 
     def __init__(self, pools):
-        self.pools = tuple(tuple(p) for p in pools)
+        # twice the same moves would read what the first had written
+        self.pools = tuple({tuple((t.data_ptr(), t.shape) for t in p): p
+                            for p in map(tuple, pools)}.values())
         flat = [t for p in self.pools for t in p]
         if not flat or len({len(p) for p in self.pools}) != 1:
             raise DcpError("a pool set needs pools with one tensor per rank each")
@@ -694,6 +697,9 @@ class PoolSet:
                     not t.is_cuda or not t.is_contiguous() or t.data_ptr() % 16:
                 raise DcpError("the pools of a set must be contiguous, 16-byte aligned CUDA "
                                "tensors of one type, shape and device")
+        if sum(len({t.data_ptr() for t in p}) for p in self.pools) != \
+                len({t.data_ptr() for t in flat}):
+            raise DcpError("two pools of a set are alike on one rank and not on another")
         self.ranks = len(self.pools[0])
         self.num_blocks, self.block_size = first.shape[0], first.shape[-2]
         self.num_heads = first.shape[1] if first.dim() == 4 else 1

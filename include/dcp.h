@@ -657,8 +657,8 @@ int dcp_pages_fork(dcp_layout_t layout, dcp_pages_t pages, const int32_t* parent
 /*
  * Every pool of a model with pages of the same shape: ptr [num_pools][dcp_size]
  * DEVICE array of device addresses (keys and values of all layers; 16-byte
- * aligned), each [num_blocks][num_heads][block_size][row_bytes].  A latent pool
- * has num_heads 1.  row_bytes is a multiple of 16.
+ * aligned), each [num_blocks][num_heads][block_size][row_bytes] and named once.
+ * A latent pool has num_heads 1.  row_bytes is a multiple of 16.
  */
 typedef struct {
   const uint64_t* ptr;

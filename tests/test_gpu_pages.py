@@ -332,3 +332,25 @@ def test_copies_of_the_same_pages_keep_the_order_of_the_list(lib, order, d):
                 if 0 <= a < nb and 0 <= b < nb:
                     before[:, r, b] = before[:, r, a].clone()
         assert torch.equal(ps, before) and err.item() == 4 * pools
+
+
+def test_a_pool_named_twice_is_moved_once(lib):
+    """Layers that share a cache name it more than once."""
+    dcp, bs, H, d, B = 1, 16, 8, 512, 1300
+    L = lib.Layout(dcp, bs, 1)
+    bt = np.arange(B, dtype=np.int32)[None, :, None]
+    gen = torch.Generator().manual_seed(2)
+    k, v = (torch.randn((B, H, bs, d), generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    want = [x.clone() for x in (k, v)]
+    path = [1, 2, 5, 9]
+    for w, x in zip(want, (k, v)):
+        for i, j in enumerate(path):
+            w[:, :, 3 + i] = x[:, :, 3 + j]
+    new = lib.cache_compact(L, lib.PoolSet([[k], [v], [k], [v], [k]]), dev(bt), B, dev([3] * B),
+                            dev([path] * B), dev([4] * B))
+    assert (new == 7).all()
+    for x, w in zip((k, v), want):
+        assert torch.equal(x, w)
+    for pools in ([[k, v], [v, k]], [[k, v], [k, v.clone()]]):     # alike on a rank and no more
+        with pytest.raises(lib.DcpError):
+            lib.PoolSet(pools)
