@@ -203,12 +203,22 @@ def rank_ptrs(tensors) -> RankPtrs:
     return rp
 
 
+def _rank_stride(block_table, ranks) -> int:
+    """Entries between two ranks' tables; 0 for a table that all ranks share."""
+    if block_table.dim() == 2 or block_table.shape[0] == 1:
+        return 0
+    if block_table.shape[0] < ranks:
+        raise DcpError(f"{block_table.shape[0]} block tables for {ranks} ranks")
+    return block_table.shape[1] * block_table.shape[2]
+
+
 class PagedKV:
     """Per-rank paged pools plus the block table, as the decode calls read them.
 
     k_pools / v_pools: one tensor per rank (GQA: [num_blocks, Hkv, bs, d];
     latent: [num_blocks, bs, kv_dim], v_pools None).  block_table:
-    [dcp, B, max_vb] int32 (one table per rank) or [B, max_vb] (shared).
+    [dcp, B, max_vb] int32 (one table per rank), or a table that all ranks
+    share: [B, max_vb] or [1, B, max_vb].
     """
 
     def __init__(self, k_pools, v_pools, block_table, num_blocks):
@@ -219,12 +229,8 @@ class PagedKV:
         _cuda_contig(block_table, *self.k_pools, *(self.v_pools or []))
         if block_table.dtype != torch.int32:
             raise DcpError("block_table must be int32")
-        if block_table.dim() == 3:
-            self.max_vb = block_table.shape[2]
-            self.bt_rank_stride = block_table.shape[1] * block_table.shape[2]
-        else:
-            self.max_vb = block_table.shape[1]
-            self.bt_rank_stride = 0
+        self.max_vb = block_table.shape[-1]
+        self.bt_rank_stride = _rank_stride(block_table, len(self.k_pools))
 
     def struct(self) -> PagedKVStruct:
         s = PagedKVStruct()
@@ -256,11 +262,8 @@ def slot_mapping(layout, req_idx, positions, block_table, num_blocks, out_rank=N
     lib = load()
     _cuda_contig(req_idx, positions, block_table)
     T = req_idx.shape[0]
-    if block_table.dim() == 3:
-        B, max_vb, stride = block_table.shape[1], block_table.shape[2], \
-            block_table.shape[1] * block_table.shape[2]
-    else:
-        B, max_vb, stride = block_table.shape[0], block_table.shape[1], 0
+    B, max_vb = block_table.shape[-2:]
+    stride = _rank_stride(block_table, layout.dcp_size)
     dev = req_idx.device
     if out_rank is None:
         out_rank = torch.empty(T, dtype=torch.int32, device=dev)
@@ -449,10 +452,7 @@ def sfa_remap(layout, topk, seq_lens, block_table, num_blocks, out_rank=None, ou
     lib = load()
     _cuda_contig(topk, seq_lens, block_table)
     B, K = topk.shape
-    if block_table.dim() == 3:
-        max_vb, stride = block_table.shape[2], block_table.shape[1] * block_table.shape[2]
-    else:
-        max_vb, stride = block_table.shape[1], 0
+    max_vb, stride = block_table.shape[-1], _rank_stride(block_table, layout.dcp_size)
     if out_rank is None:
         out_rank = torch.empty((B, K), dtype=torch.int32, device=topk.device)
     if out_slot is None:
@@ -625,7 +625,7 @@ class Pages:
     block_table [T, B, max_vb] int32 with T = dcp tables (one per rank) or 1 (a
     table that all ranks share), seq_lens [B] int32, ref_count [T, num_blocks]
     int32, free_bits [T, ceil(num_blocks / 32)] int32.  ``Pages.new`` makes them.
-    The decode calls take the table as it is, a shared one as block_table[0].
+    The other calls take the table as it is, a shared one too.
     """
 
     def __init__(self, block_table, seq_lens, ref_count, free_bits, num_blocks):

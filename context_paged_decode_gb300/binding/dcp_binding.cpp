@@ -288,8 +288,9 @@ PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c.block_table = (const int32_t*)ptr(bt, "block_table", at::kInt, bt.sizes(), dev);
     c.num_blocks = nb;
     c.max_vblocks = small(bt.size(dim - 1), "max_vblocks");
-    c.bt_rank_stride = dim == 3 ? bt.size(1) * bt.size(2) : 0;
-    if (dim == 3 && bt.size(0) < L.dcp_size)
+    const bool each = dim == 3 && bt.size(0) != 1;   // one for each rank, not one for all
+    c.bt_rank_stride = each ? bt.size(1) * bt.size(2) : 0;
+    if (each && bt.size(0) < L.dcp_size)
       refuse(std::to_string(bt.size(0)) + " block tables for " + std::to_string(L.dcp_size) +
              " ranks");
     if (bt.size(dim - 2) < B)

@@ -285,3 +285,43 @@ def test_the_state_of_new_pages_belongs_to_its_stream(lib):
     torch.cuda.synchronize()
     for a, w in zip(names, want):
         assert torch.equal(getattr(p, a), w), a
+
+
+@pytest.mark.parametrize("dcp", [1, 3])
+def test_a_shared_table_as_the_state_has_it(lib, dcp):
+    """[1, B, max_vb] is one table for all ranks in every call that takes a table."""
+    L, nb, Hkv, d, B = lib.Layout(dcp, 16, 1), 30, 2, 64, 3
+    pages = lib.Pages.new(L, B, 4, nb, shared=True)
+    lens = [40, 1, 33]
+    lib.pages_resize(L, pages, dev(range(B)), dev(lens))
+    gen = torch.Generator().manual_seed(dcp)
+    k, v = (torch.randn((dcp, nb, Hkv, 16, d), generator=gen).to(BF16).cuda() for _ in range(2))
+    q = torch.randn((B, 8, d), generator=gen).to(BF16).cuda()
+    whole, flat = pages.block_table, pages.block_table[0]
+    assert whole.shape == (1, B, 4)
+    kvs = [lib.PagedKV(list(k), list(v), t, nb) for t in (whole, flat)]
+    req, pos = dev([0, 1, 2, 2]), dev([39, 0, 20, 32], np.int64)
+    topk, seq = dev([[0, 17, 39], [0, 0, 0], [5, 32, 31]]), dev(lens)
+    calls = (lambda t, kv: lib.slot_mapping(L, req, pos, t, nb),
+             lambda t, kv: lib.sfa_remap(L, topk, seq, t, nb),
+             lambda t, kv: lib.decode_gqa(L, q, kv, lib.local_seq_lens(L, seq), d ** -0.5),
+             lambda t, kv: lib.tree_decode_gqa(L, q, kv, dev([0, 1, 2, 3]), seq - 1,
+                                               torch.ones(3, dtype=torch.int64, device="cuda"),
+                                               d ** -0.5, 1),
+             lambda t, kv: lib.tree_partial_gqa(L, q, kv, dev([0, 1, 2, 3]), seq - 1,
+                                                torch.ones(3, dtype=torch.int64, device="cuda"),
+                                                d ** -0.5, 1))
+    for call in calls:
+        for a, b in zip(call(whole, kvs[0]), call(flat, kvs[1])):
+            assert torch.equal(a, b)
+    # two tables are not enough for three ranks
+    two, L3 = torch.cat([whole, whole]), lib.Layout(3, 16, 1)
+    kv2 = lib.PagedKV(list(k[:1]), list(v[:1]), two, nb)
+    for bad in (lambda: lib.slot_mapping(L3, req, pos, two, nb),
+                lambda: lib.sfa_remap(L3, topk, seq, two, nb),
+                lambda: lib.PagedKV([k[0]] * 3, [v[0]] * 3, two, nb),
+                lambda: lib.tree_decode_gqa(L3, q, kv2, dev([0, 1, 2, 3]), seq - 1,
+                                            torch.ones(3, dtype=torch.int64, device="cuda"),
+                                            d ** -0.5, 1)):
+        with pytest.raises(lib.DcpError):
+            bad()
