@@ -354,3 +354,28 @@ def test_a_pool_named_twice_is_moved_once(lib):
     for pools in ([[k, v], [v, k]], [[k, v], [k, v.clone()]]):     # alike on a rank and no more
         with pytest.raises(lib.DcpError):
             lib.PoolSet(pools)
+
+
+def test_compaction_of_more_pools_than_shared_memory_has_addresses_for(lib):
+    """70 pools on 16 ranks: 1120 addresses, of which the kernel keeps 1024 at most."""
+    dcp, bs, H, d, n = 16, 16, 1, 32, 70
+    L = lib.Layout(dcp, bs, 1)
+    ctx, paths = [5, 250, 0], [[1, 4, 9], [0, 2, 3, 5, 8, 13, 21, 34, 55, 60], [7]]
+    rng = np.random.default_rng(n)
+    lens = [c + max(p) + 1 for c, p in zip(ctx, paths)]
+    bt, nb = R.random_tables(rng, lens, dcp, bs)
+    before = torch.randn((n, dcp, nb, bs, d), generator=torch.Generator().manual_seed(n)).cuda()
+    after, want = before.clone(), before.clone()
+    for b, path in enumerate(paths):
+        for i, j in enumerate(path):
+            r, vb, loc = R.place(ctx[b] + i, dcp, bs, 1)
+            r2, vb2, loc2 = R.place(ctx[b] + j, dcp, bs, 1)
+            want[:, r, int(bt[r, b, vb]), loc] = before[:, r2, int(bt[r2, b, vb2]), loc2]
+    path = np.full((3, 10), -9, dtype=np.int32)
+    for b, p in enumerate(paths):
+        path[b, :len(p)] = p
+    err = torch.zeros(1, dtype=I32, device="cuda")
+    new = lib.cache_compact(L, lib.PoolSet([list(p) for p in after]), dev(bt), nb, dev(ctx),
+                            dev(path), dev([len(p) for p in paths]), err=err)
+    assert new.tolist() == [c + len(p) for c, p in zip(ctx, paths)] and err.item() == 0
+    assert torch.equal(after, want)

@@ -277,3 +277,73 @@ def test_the_angle_of_far_positions(lib):
         off = np.abs(got.double().cpu().numpy() - y)
         assert (off <= tol).all(), (off / tol).max()
     assert (wide[..., rot:] == 0).all()
+
+
+# dtype, T, Hq, Hkv, d, rot, interleaved, dcp, bs
+MANY = [
+    (BF16, 6001, 3, 1, 64, 64, False, 8, 16),
+    (BF16, 5000, 2, 2, 128, 32, True, 2, 64),
+    (F32, 701, 64, 8, 128, 128, False, 3, 16),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"{str(c[0])[6:]}-T{c[1]}-{c[2]}.{c[3]}-d{c[4]}")
+def test_many_tokens(lib, case):
+    """More items than the card holds CTAs, so that each goes through several: stages and tables
+    are used again, and what comes next is loaded ahead."""
+    dtype, T, Hq, Hkv, d, rot, inter, dcp, bs = case
+    row = d * (4 if dtype == F32 else 2)
+    parts = -(-(Hq + 2 * Hkv) // min(Hq + 2 * Hkv, 16384 // row))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert T * parts > 2 * 8 * sms or (parts > 1 and T * parts > 2 * 6 * sms)
+    rng = np.random.default_rng(T)
+    nb, axes = T // bs + 3, 3
+    inv, pos = inv_freqs(rot // 2), rng.integers(0, 1 << 20, (axes, T))
+    axis = np.sort(rng.integers(0, axes, rot // 2)).astype(np.int32)
+    slot = slots(rng, T, dcp, nb, bs)
+    x = torch.randn((T, Hq + 2 * Hkv, d), generator=torch.Generator().manual_seed(T)).to(dtype).cuda()
+    q, k, v = x.split([Hq, Hkv, Hkv], 1)
+    kp, vp = pools(dcp, (nb, Hkv, bs, d), dtype), pools(dcp, (nb, Hkv, bs, d), dtype)
+    k_out = torch.empty((T, Hkv, d), dtype=dtype, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = [torch.from_numpy(a).cuda() for a in (pos, inv, slot)]
+    q_out = lib.rope_write_gqa(lib.Layout(dcp, bs, 1), q, k, v, *args, kp, vp, nb,
+                               axis=torch.from_numpy(axis).cuda(), interleaved=inter, k_out=k_out,
+                               err=err)
+    assert err.item() == 0
+    for got, src in ((q_out, q), (k_out, k)):
+        y, mag = R.rotated(src.double().cpu().numpy(), pos, inv, axis, 0, inter)
+        assert (np.abs(got.double().cpu().numpy() - y) <= R.rope_tol(dtype, y, mag)).all()
+        assert torch.equal(got[..., rot:], src[..., rot:])
+    for r in range(dcp):
+        mine = slot[r] >= 0
+        rows = torch.from_numpy(np.nonzero(mine)[0]).cuda()
+        assert torch.equal(stored(kp[r], slot[r][mine], bs, False), k_out[rows])
+        assert torch.equal(stored(vp[r], slot[r][mine], bs, False), v[rows])
+        n = int(mine.sum()) * Hkv * d
+        for p in (kp[r], vp[r]):
+            assert int((p == 7.0).sum()) >= p.numel() - n
+
+
+def test_many_latent_rows(lib):
+    T, Hq, dim, rot, dcp, bs = 1501, 20, 576, 64, 4, 64     # two items a token
+    rng = np.random.default_rng(T)
+    nb = T // bs + 2
+    inv, pos = inv_freqs(rot // 2), rng.integers(0, 1 << 18, (1, T))
+    slot = slots(rng, T, dcp, nb, bs)
+    gen = torch.Generator().manual_seed(T)
+    q = torch.randn((T, Hq, dim), generator=gen).to(BF16).cuda()
+    kv = torch.randn((T, dim), generator=gen).to(BF16).cuda()
+    p = pools(dcp, (nb, bs, dim), BF16)
+    args = [torch.from_numpy(a).cuda() for a in (pos[0], inv, slot)]
+    got = lib.rope_write_mla(lib.Layout(dcp, bs, 1), q, kv, *args, p, nb)
+    at = dim - rot
+    y, mag = R.rotated(q.double().cpu().numpy(), pos, inv, None, at, True)
+    assert (np.abs(got.double().cpu().numpy() - y) <= R.rope_tol(BF16, y, mag)).all()
+    assert torch.equal(got[..., :at], q[..., :at])
+    y, mag = R.rotated(kv.double().cpu().numpy(), pos, inv, None, at, True)
+    tol = R.rope_tol(BF16, y, mag)
+    for r in range(dcp):
+        mine = slot[r] >= 0
+        rows = stored(p[r], slot[r][mine], bs, True).double().cpu().numpy()
+        assert (np.abs(rows - y[mine]) <= tol[mine]).all()

@@ -140,6 +140,118 @@ def plan(c, tc, per_rank=False, most=None):
     return pieces, parts
 
 
+# dtype, Hq, Hkv, d, dcp, bs, I, ctx, T, streams, joined by the last CTA
+LONG = {
+    "one-stream-merged": (BF16, 8, 8, 128, 2, 16, 1, [17000, 15500], [64, 50], 1, False),
+    "two-streams-merged": (BF16, 16, 4, 64, 3, 32, 4, [14001, 13000, 14500], [64, 33, 47], 2, False),
+    "one-stream-joined": (BF16, 32, 2, 64, 2, 16, 16, [1500 + 37 * (i % 17) for i in range(80)],
+                          [1 + i % 8 for i in range(80)], 1, True),
+    "two-streams-joined": (BF16, 16, 4, 128, 4, 16, 1, [1300 + 61 * (i % 13) for i in range(40)],
+                           [64 - i % 31 for i in range(40)], 2, True),
+    "one-stream-joined-wide-heads": (BF16, 16, 4, 128, 8, 64, 1, [1100 + 97 * (i % 11) for i in range(40)],
+                                     [32 - i % 9 for i in range(40)], 1, True),
+}
+
+
+@pytest.mark.parametrize("name", LONG)
+def test_rings_go_round(lib, name):
+    """Runs of more tiles than the rings have slots, several units a run, units that are cut."""
+    *shape, streams, joined = LONG[name]
+    c = Case(lib, *shape, seed=len(name))
+    Hq, Hkv, d, dcp = c.dims[:4]
+    pieces, parts = plan(c, True)
+    assert max(n for _, _, _, n, _ in pieces) >= 8                  # six slots at most
+    assert max(np.bincount([p[0] for p in pieces])) >= 2            # several pieces in a run
+    assert any(not whole for *_, whole in pieces)                   # and some are cut
+    assert (max(c.T) > 128 * Hkv // Hq) == (streams == 2)
+    assert (len(c.T) > 16 and len(c.T) * Hkv >= torch.cuda.get_device_properties(
+        0).multi_processor_count) == joined
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sink = torch.linspace(-2, 9, Hq).cuda()
+    out, lse = lib.tree_decode_gqa(*c.args(lib), sink=sink, err=err)
+    c.check(out, lse, BF16, sink=sink.cpu().numpy())
+    again = lib.tree_decode_gqa(*c.args(lib), sink=sink, err=err)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    out, lse = lib.tree_decode_gqa(*c.args(lib), out_dtype=F32, err=err)
+    c.check(out, lse, F32)
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("name", ["two-streams-merged", "one-stream-joined"])
+def test_rings_go_round_rank_by_rank(lib, name):
+    c = Case(lib, *LONG[name][:-2], seed=3)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    po, pl = lib.tree_partial_gqa(*c.args(lib), err=err)
+    for r in range(c.dims[3]):
+        c.check(po[r], pl[r], F32, rank=r)
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("streams", [1, 2])
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_accumulator_is_rescaled(lib, streams, d):
+    """Tiles whose maximum passes that of the tiles before by more than 2^8, in some rows of a
+    warp and not in others, with what came before still worth a part of the result: in most
+    tiles all tokens score about alike, and now and then a single one scores nine more (in
+    log2 units, times a factor that each row has of its own)."""
+    T = 20 * streams
+    c = Case(lib, BF16, 16, 4, d, 2, 16, 1, [9000, 8800, 9100, 8700, 9050, 8900, 8950, 9011],
+             [T - 1, T, T, T - 3, T, T, T - 2, T], seed=d + streams, scale=1.0)
+    assert (max(c.T) > 32) == (streams == 2)
+    pieces, _ = plan(c, True)
+    assert max(n for _, _, _, n, _ in pieces) >= 12
+    rng = np.random.default_rng(1)
+    # scores: q[0] * k[0] and a little of the rest
+    q, k = c.q.float() * 2.0 ** -6, c.k.float() * 2.0 ** -4
+    q[..., 0] = torch.from_numpy(rng.choice([0.25, 0.5, 1.0, 1.25], q.shape[:2]).astype(np.float32))
+    rises = 0
+    for b in range(len(c.T)):
+        r, page, loc = c.at(b)
+        level = np.zeros(len(r), dtype=np.float32)
+        top, x = 0.0, int(rng.integers(100, 300))
+        while x < len(r):
+            top += 9.0 * float(np.log(2.0))
+            level[x] = top                     # the one token that is high
+            rest = int(rng.integers(150, 700))
+            level[x + 1:x + rest] = top - 6.0 * float(np.log(2.0)) if rng.random() < 0.5 else 0.0
+            x += rest
+            rises += 1
+        k[torch.from_numpy(r), torch.from_numpy(page).long(), :, torch.from_numpy(loc), 0] = \
+            torch.from_numpy(level)[:, None]
+    c.q, c.k = q.to(BF16), k.to(BF16)
+    assert rises > 100
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = lib.tree_decode_gqa(*c.args(lib), out_dtype=F32, err=err)
+    c.check(out, lse, F32)
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("per_rank", [False, True])
+def test_more_entries_than_the_plan_has_threads(lib, dtype, per_rank):
+    """The plan goes over its entries twice when there are more than 256 (requests, or requests
+    on a rank); some have no nodes and some are refused."""
+    B, dcp = (70, 8) if per_rank else (530, 2)
+    rng = np.random.default_rng(5)
+    ctx, T = rng.integers(0, 260, B), rng.integers(0, 7, B)
+    ctx[[3, B - 1]], T[[3, B - 1]] = (1900, 2100), (6, 6)
+    c = Case(lib, dtype, 8, 2, 64, dcp, 16, 1, ctx, T, seed=B)
+    bad = [0, 7, B // 2]
+    args = list(c.args(lib))
+    for b in bad:
+        args[4][b] = -1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    good = [b for b in range(B) if b not in bad]
+    if per_rank:
+        po, pl = lib.tree_partial_gqa(*args, err=err)
+        for r in range(dcp):
+            c.check(po[r], pl[r], F32, rank=r, requests=good)
+    else:
+        out, lse = lib.tree_decode_gqa(*args, err=err)
+        c.check(out, lse, dtype, requests=good)
+    assert err.item() == len(bad)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("T", [3, 40])
 def test_values_that_are_not_finite_in_many_short_units(lib, d, T):
