@@ -22,9 +22,9 @@
 // sent by bulk copies to q_out, k_out and each rank's pool, so no thread waits
 // for global memory and values and unrotated rows pass through no register.
 // The token's cosines and sines are computed meanwhile, once for its heads.
-// Measured: 4096 tokens of 32 + 8 + 8 heads of 128 in bf16, three axes (202 MB)
-// 36-37 us, 5.5 TB/s or 0.81-0.83 of the copy bandwidth; 1025 tokens of 128 + 1
-// latent rows of 576 (305 MB) 51.5 us, 0.87; a decode step of 32 tokens 4.5 us.
+// Measured: 8192 tokens of 32 + 8 + 8 heads of 128 in bf16, three axes (202 MB)
+// 36.6-36.9 us, 5.5 TB/s or 0.81 of the copy bandwidth; 1025 tokens of 128 + 1
+// latent rows of 576 (305 MB) 52 us, 0.87; 256 tokens of a decode step 4.7 us.
 // (With plain loads and stores by a CTA per token the first two took 54 and 75.)
 // In place (q_out is q) only the rotated entries of q move: that is a kernel
 // with a CTA per token and plain loads.
@@ -287,7 +287,7 @@ struct RopeBulk {
 };
 
 // Two stages and eight CTAs an SM: three to five stages, items of 8 or 32 KB, 96
-// or 256 threads and 6 or 12 CTAs were within 1% or slower (4096 tokens).  Eight
+// or 256 threads and 6 or 12 CTAs were within 1% or slower (8192 tokens).  Eight
 // CTAs need the bound on registers: at 72 of them seven fit, and the last wave
 // took the call from 36 us to 47.
 template <bool kF32, bool kHalves>

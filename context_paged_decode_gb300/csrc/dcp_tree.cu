@@ -235,7 +235,7 @@ __device__ __forceinline__ void tg_wait() { asm volatile("cp.async.wait_group 1;
 // the shared-memory reads that feed them (those 66 us are 17 TFLOP/s; a tile's
 // products would take 43% of its cycles, its reads 60%), and on short contexts
 // latency: 2 x 11 nodes over up to 3001 tokens of 2 heads of 64 in fp32 (4.3
-// MB) take 21 to 23 us, the merge 5 of them.
+// MB) take 22.6 to 23.5 us, the merge 5 of them.
 template <typename T, int DPL, int RW>
 __global__ void __launch_bounds__(kTgWarps * 32)
 tree_generic_kernel(const __grid_constant__ TreeArgs A) {
@@ -527,11 +527,12 @@ static int launch_tree_generic(const TreeArgs& A, cudaStream_t s) {
 // request stay as they were.  Latency bounds it: a row waits for its entry, then
 // for its parts, and a kernel this short also for its instructions, so there is
 // one loop with a running maximum.  Few rows have many parts, which two warps
-// fetch at once, eight at a time: a call of 8 nodes over 1500 tokens takes 15.2
-// us, 15.7 with four warps, 16.5 with eight, 17.9 with one; 64 nodes over 65536
-// tokens 77, 79, 86 and 76 us.  Many rows get a warp each, which keeps more of
-// them in flight: with 8 requests of 64 nodes (16384 rows) the call takes 173 us,
-// 208 with four warps.  `joined`: the parts are joined already, only ranks that
+// fetch at once, eight at a time: a call of 8 nodes over 1500 tokens takes 15.9
+// us, 16.1 with four warps, 16.5 with eight, 18.3 with one; 16 x 5 nodes on one
+// key head 19.9, 20.4, 22.7 and 22.4 us, 64 nodes over 65536 tokens 71.5, 73.7,
+// 80.3 and 72.2 (fp32, 2 x 11 nodes, 22.6, 21.5, 20.3 and 30.3).  Many rows get a
+// warp each, which keeps more of them in flight: with 8 requests of 64 nodes
+// (16384 rows) the call takes 153 us, 165 with two warps, 189 with four.  `joined`: the parts are joined already, only ranks that
 // hold nothing are left.  A lane has DPL columns: consecutive ones where a row is
 // 32 DPL wide (kWide), else every 32nd.
 constexpr int64_t kTreeSplitRows = 2048;   // most rows that get two warps each

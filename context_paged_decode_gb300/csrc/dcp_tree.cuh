@@ -162,8 +162,12 @@ __device__ __forceinline__ int64_t tree_extra(const TreeArgs& A, int64_t tiles) 
 }
 
 // The plan of a call with few entries, made by a warp of each CTA for itself:
-// a kernel and a wait less than a plan of its own (one request, 8 nodes, 1500
-// tokens: 16.1 us against 18.9).  CTA 0 leaves it for the merge.
+// a kernel and a wait less than a plan of its own.  With 1, 4, 8 and 16 requests
+// of 8 nodes over up to 1500 tokens 15.9, 20.7, 22.4 and 28.9 us against 18.4,
+// 23.0, 24.6 and 30.7; 16 x 5 nodes on one key head 20.0 against 22.1, fp32 22.7
+// against 25.6.  It gains as much at the last of these as at the first: what ends
+// it is the room that shared memory has beside the tiles, 16 entries (17 at most).
+// CTA 0 leaves it for the merge.
 constexpr int kTreeSelf = 16;
 struct TreeSelf {
   TreeEntry entry[kTreeSelf];
