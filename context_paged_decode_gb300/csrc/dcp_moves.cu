@@ -26,70 +26,114 @@ __device__ __forceinline__ uint4* pool_at(const PoolSet& P, int pool, int dcp, i
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyDepth = 8;     // 16-byte loads in flight per thread
+constexpr int kCopyList = 2048;   // most entries of a list that is kept in shared memory
+constexpr int kCopyBits = 1 << 15;   // of each set of pages, by the low bits of their numbers
+constexpr int kCopySmall = 1024;  // most 16-byte pieces of a small page
 
-// One CTA per (copy, rank, pool): a page is H * bs rows in one piece.  128 open
-// pages of 32 KB on 8 ranks in 2 pools (134 MB) take 14 us beside the launch;
-// a few pages are bound by two dependent loads, 5 us with the launch.
+// A CTA takes `each` copies of one rank and pool: a page is H * bs rows in one
+// piece.  128 open pages of 32 KB on 8 ranks in 2 pools (134 MB) take 23 us from
+// HBM, and four of them 2.7 us, bound by two dependent loads.
 //
 // Copies that touch the same page (one writes what another reads or writes) have
 // to keep the order of the list.  CTAs cannot wait for one another, so the first
 // of them does all such copies of its rank and pool, where each thread moves the
 // same 16 bytes of every page and needs no barrier.  Whether there are any is
-// found from the whole list while the first rows of the page are on their way.
+// found from the whole list, which the CTA has in shared memory, while the first
+// rows of the page are on their way.  Small pages of a long list are shared out to
+// few CTAs, where sets of the pages that are read and written say first that there
+// are none: with 2048 copies on 8 ranks in 2 pools pages of 2, 4, 8 and 16 KB take
+// 60, 62, 90 and 178 us, and 83, 90, 107 and 167 by one CTA a copy that looks for
+// no others (looking through the list for each one makes the first 231 us).  Pages
+// of 32 KB take 322 us, and 318 so; 344 in few CTAs.
 __global__ void __launch_bounds__(kCopyThreads)
 pages_copy_kernel(PoolSet P, int dcp, int tables, const int32_t* src,
-                  const int32_t* dst, int n, int64_t page16, int32_t* err) {
+                  const int32_t* dst, int n, int each, int groups, bool sets, int64_t page16, int32_t* err) {
+  extern __shared__ __align__(16) uint32_t s_mem[];
+  const bool kept = n > 1 && n <= kCopyList;
+  // the sets (pages read, written, written twice), if there are any, and the list
+  uint32_t(*const s_set)[kCopyBits / 32] = reinterpret_cast<uint32_t(*)[kCopyBits / 32]>(s_mem);
+  int* const s_src = reinterpret_cast<int*>(s_mem) + (sets ? 3 * kCopyBits / 32 : 0);
+  int* const s_dst = s_src + n;
   griddep_launch_dependents();   // the next call's first kernel may start its launch
   griddep_wait();                // launched chained: the preceding kernel completed
-  const int64_t units = (int64_t)n * dcp * P.num_pools;
   const int tid = threadIdx.x;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int pool = (int)(u % P.num_pools);
-    const int r = (int)(u / P.num_pools % dcp);
-    const int i = (int)(u / P.num_pools / dcp);
-    const int32_t* from = src + (int64_t)(tables == 1 ? 0 : r) * n;
-    const int32_t* to = dst + (int64_t)(tables == 1 ? 0 : r) * n;
-    const int a = __ldcg(from + i), b = __ldcg(to + i);
+  const int g = blockIdx.x % groups, pool = blockIdx.x / groups % P.num_pools;
+  const int r = blockIdx.x / groups / P.num_pools;
+  const int32_t* from = src + (int64_t)(tables == 1 ? 0 : r) * n;
+  const int32_t* to = dst + (int64_t)(tables == 1 ? 0 : r) * n;
+  uint4* const base = pool_at(P, pool, dcp, r);
+  auto moves = [&](int p, int q) {   // can be made, and has work
+    return p >= 0 && p < P.nb && q >= 0 && q < P.nb && p != q;
+  };
+  if (sets) {
+    for (int j = tid; j < 3 * kCopyBits / 128; j += kCopyThreads)
+      reinterpret_cast<uint4*>(s_mem)[j] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+  }
+  if (n > 1) {
+#pragma unroll 4
+    for (int j = tid; j < n; j += kCopyThreads) {
+      const int p = __ldcg(from + j), q = __ldcg(to + j);
+      if (kept) {
+        s_src[j] = p;
+        s_dst[j] = q;
+      }
+      if (sets && moves(p, q)) {
+        const int w = q % kCopyBits / 32;
+        const uint32_t bit = 1u << (q & 31);
+        atomicOr(&s_set[0][p % kCopyBits / 32], 1u << (p & 31));
+        if (atomicOr(&s_set[1][w], bit) & bit) atomicOr(&s_set[2][w], bit);
+      }
+    }
+    __syncthreads();
+  }
+  auto has = [&](int set, int p) { return (s_set[set][p % kCopyBits / 32] >> (p & 31)) & 1; };
+  auto entry = [&](int j, int& p, int& q) {
+    p = kept ? s_src[j] : __ldcg(from + j);
+    q = kept ? s_dst[j] : __ldcg(to + j);
+  };
+  // does another copy touch a page of copy k, p -> q? (all threads ask)
+  auto shared = [&](int p, int q, int k) {
+    if (sets && !has(1, p) && !has(0, q) && !has(2, q)) return false;
+    bool hit = false;
+    for (int j = tid; j < n; j += kCopyThreads) {
+      int x, y;
+      entry(j, x, y);
+      hit |= j != k && (y == p || x == q || y == q) && moves(x, y);
+    }
+    return __syncthreads_or(hit) != 0;
+  };
+  uint4 x[kCopyDepth];
+  auto load = [&](int p, int64_t c) {
+#pragma unroll
+    for (int j = 0; j < kCopyDepth; ++j)
+      if (c + j * kCopyThreads < page16) x[j] = __ldcg(base + p * page16 + c + j * kCopyThreads);
+  };
+  auto store = [&](int q, int64_t c) {
+#pragma unroll
+    for (int j = 0; j < kCopyDepth; ++j)
+      if (c + j * kCopyThreads < page16) base[q * page16 + c + j * kCopyThreads] = x[j];
+  };
+  const int i1 = min((int64_t)n, ((int64_t)g + 1) * each);
+  for (int i = g * each; i < i1; ++i) {
+    int a, b;
+    entry(i, a, b);
     if (a == -1 && b == -1) continue;
-    uint4* base = pool_at(P, pool, dcp, r);
-    auto moves = [&](int x, int y) {   // is a copy that can be made, and has work
-      return x >= 0 && x < P.nb && y >= 0 && y < P.nb && x != y;
-    };
     if (a < 0 || a >= P.nb || b < 0 || b >= P.nb || !base) {
       if (tid == 0) count_error(err);
       continue;
     }
     if (a == b) continue;
-    // does another copy touch a page of the copy x -> y, number k? (all threads ask)
-    auto shared = [&](int x, int y, int k) {
-      bool hit = false;
-      for (int j = tid; j < n; j += kCopyThreads) {
-        const int p = __ldcg(from + j), q = __ldcg(to + j);
-        hit |= j != k && moves(p, q) && (q == x || p == y || q == y);
-      }
-      return __syncthreads_or(hit) != 0;
-    };
-    uint4 x[kCopyDepth];
-    auto load = [&](int p, int64_t c) {
-#pragma unroll
-      for (int j = 0; j < kCopyDepth; ++j)
-        if (c + j * kCopyThreads < page16) x[j] = __ldcg(base + p * page16 + c + j * kCopyThreads);
-    };
-    auto store = [&](int p, int64_t c) {
-#pragma unroll
-      for (int j = 0; j < kCopyDepth; ++j)
-        if (c + j * kCopyThreads < page16) base[p * page16 + c + j * kCopyThreads] = x[j];
-    };
     load(a, tid);
     if (n > 1 && shared(a, b, i)) {
-      int k = 0;
+      int k = 0, p, q;
       for (; k < i; ++k) {           // an earlier one does them all
-        const int p = __ldcg(from + k), q = __ldcg(to + k);
+        entry(k, p, q);
         if (moves(p, q) && shared(p, q, k)) break;
       }
       if (k < i) continue;
       for (; k < n; ++k) {
-        const int p = __ldcg(from + k), q = __ldcg(to + k);
+        entry(k, p, q);
         if (!moves(p, q) || !shared(p, q, k)) continue;
         for (int64_t c = tid; c < page16; c += kCopyThreads * kCopyDepth) {
           load(p, c);
@@ -261,11 +305,19 @@ int dcp_pages_copy(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* cop
   const PoolSet P{pools.ptr, pools.num_pools, pools.num_heads, pools.row_bytes / 16,
                   pools.num_blocks};
   const int64_t page16 = (int64_t)pools.num_heads * layout.block_size * (pools.row_bytes / 16);
-  const int64_t units = (int64_t)num * layout.dcp_size * pools.num_pools;
-  const int64_t most = (int64_t)32 * num_sms();
+  const int64_t sets = (int64_t)layout.dcp_size * pools.num_pools;
+  if (sets >= (int64_t(1) << 30)) return DCP_EUNSUPPORTED;
+  const bool small = page16 <= kCopySmall;
+  // copies of a CTA: one, unless that would be too many CTAs
+  const int64_t most = (int64_t)(small ? 4 : 32) * num_sms();
+  const int64_t each = ((int64_t)num * sets + most - 1) / most;
+  const int take = (int)(each < num ? each : num), groups = (num - 1) / take + 1;
+  const bool filter = small && take >= 4 && num > kCopyThreads;
+  const size_t smem = (filter ? 3 * kCopyBits / 8 : 0) +
+                      (num > 1 && num <= kCopyList ? 2 * sizeof(int32_t) * num : 0);
   const cudaError_t e = launch_chained(
-      pages_copy_kernel, (unsigned)(units < most ? units : most), kCopyThreads, 0,
-      (cudaStream_t)stream, P, (int)layout.dcp_size, (int)num_tables, copy_src, copy_dst, (int)num,
+      pages_copy_kernel, (unsigned)(groups * sets), kCopyThreads, smem, (cudaStream_t)stream, P,
+      (int)layout.dcp_size, (int)num_tables, copy_src, copy_dst, (int)num, take, groups, filter,
       page16, err_count);
   if (e != cudaSuccess) return launch_status_report(e);
   return launch_status();

@@ -379,3 +379,31 @@ def test_compaction_of_more_pools_than_shared_memory_has_addresses_for(lib):
                             dev(path), dev([len(p) for p in paths]), err=err)
     assert new.tolist() == [c + len(p) for c, p in zip(ctx, paths)] and err.item() == 0
     assert torch.equal(after, want)
+
+
+@pytest.mark.parametrize("n", [300, 2048, 2500])
+@pytest.mark.parametrize("d", [8, 512])
+def test_a_few_copies_of_the_same_pages_in_a_long_list(lib, n, d):
+    """Lists that CTAs share out, that sets of pages look through first (small pages), and that
+    are too long for shared memory; page numbers that fall on the same bits of the sets."""
+    dcp, bs, pools = 2, 16, 2
+    nb = 40000 if d == 8 else 5600
+    rng = np.random.default_rng(n + d)
+    src, dst = (np.empty((dcp, n), dtype=np.int64) for _ in range(2))
+    for r in range(dcp):
+        pages = rng.permutation(nb)[:2 * n]
+        src[r], dst[r] = pages[:n], pages[n:]
+        for i, j in ((5, 200), (n - 1, 17), (77, n // 2)):
+            src[r, i] = dst[r, j]                       # reads what another copy writes
+        dst[r, 90] = dst[r, n - 7]                      # a page is written twice
+        src[r, 33] = dst[r, 33] = -1
+    ps = torch.randn((pools, dcp, nb, bs, d), generator=torch.Generator().manual_seed(n)).to(
+        torch.bfloat16).cuda()
+    want = ps.clone()
+    for r in range(dcp):
+        for a, b in zip(src[r], dst[r]):
+            if a >= 0:
+                want[:, r, b] = want[:, r, a].clone()
+    L, err = lib.Layout(dcp, bs, 1), torch.zeros(1, dtype=I32, device="cuda")
+    lib.pages_copy(L, lib.PoolSet([list(p) for p in ps]), dev(src), dev(dst), err=err)
+    assert torch.equal(ps, want) and err.item() == 0
