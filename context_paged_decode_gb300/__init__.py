@@ -203,7 +203,7 @@ def rank_ptrs(tensors) -> RankPtrs:
     return rp
 
 
-def _rank_stride(block_table, ranks) -> int:
+def _rank_stride(block_table, ranks=1) -> int:
     """Entries between two ranks' tables; 0 for a table that all ranks share."""
     if block_table.dim() == 2 or block_table.shape[0] == 1:
         return 0
@@ -230,9 +230,12 @@ class PagedKV:
         if block_table.dtype != torch.int32:
             raise DcpError("block_table must be int32")
         self.max_vb = block_table.shape[-1]
-        self.bt_rank_stride = _rank_stride(block_table, len(self.k_pools))
+        self.bt_rank_stride = _rank_stride(block_table)
 
-    def struct(self) -> PagedKVStruct:
+    def struct(self, layout=None) -> PagedKVStruct:
+        """The C struct, for a call of this layout (which needs a table for each rank, or one)."""
+        if layout is not None:
+            _rank_stride(self.block_table, layout.dcp_size)
         s = PagedKVStruct()
         s.k = rank_ptrs(self.k_pools)
         s.v = rank_ptrs(self.v_pools)
@@ -303,8 +306,9 @@ def gather_context_mla(layout, kv: PagedKV, req_idx, positions, out=None, err=No
     B = kv.block_table.shape[-2]
     if out is None:
         out = torch.empty((T, kv_dim), dtype=pool.dtype, device=pool.device)
-    _check(lib.dcp_gather_context_mla(layout, kv.struct(), B, kv_dim, _dtype(pool), _p(req_idx),
-                                      _p(positions), T, _p(out), _p(err), _stream(stream)))
+    _check(lib.dcp_gather_context_mla(layout, kv.struct(layout), B, kv_dim, _dtype(pool),
+                                      _p(req_idx), _p(positions), T, _p(out), _p(err),
+                                      _stream(stream)))
     return out
 
 
@@ -336,7 +340,7 @@ def decode_partial_gqa(layout, q, kv: PagedKV, local_lens, scale, part_o=None, p
         part_lse = torch.empty((layout.dcp_size, B, Hq), dtype=torch.float32, device=dev)
     ws = _workspace(layout, KIND_GQA, B, Hq, Hkv, d, dev, workspace)
     _check(lib.dcp_decode_partial_gqa(layout, _p(q), B, Hq, Hkv, d, float(scale), _dtype(q),
-                                      kv.struct(), _p(local_lens), _p(part_o), _p(part_lse),
+                                      kv.struct(layout), _p(local_lens), _p(part_o), _p(part_lse),
                                       _p(ws), ws.numel(), _p(err), _stream(stream)))
     return part_o, part_lse
 
@@ -354,9 +358,9 @@ def decode_gqa(layout, q, kv: PagedKV, local_lens, scale, sink=None, out_dtype=N
     if out_lse is None:
         out_lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
     ws = _workspace(layout, KIND_GQA, B, Hq, Hkv, d, dev, workspace)
-    _check(lib.dcp_decode_gqa(layout, _p(q), B, Hq, Hkv, d, float(scale), _dtype(q), kv.struct(),
-                              _p(local_lens), _p(sink), _p(out), _dtype(out), _p(out_lse),
-                              _p(ws), ws.numel(), _p(err), _stream(stream)))
+    _check(lib.dcp_decode_gqa(layout, _p(q), B, Hq, Hkv, d, float(scale), _dtype(q),
+                              kv.struct(layout), _p(local_lens), _p(sink), _p(out), _dtype(out),
+                              _p(out_lse), _p(ws), ws.numel(), _p(err), _stream(stream)))
     return out, out_lse
 
 
@@ -376,7 +380,7 @@ def decode_gqa_noalloc(layout, q, kv: PagedKV, local_lens, scale, sink=None, out
     if out_lse is None:
         out_lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
     _check(lib.dcp_decode_gqa_noalloc(layout, _p(q), B, Hq, Hkv, d, float(scale), _dtype(q),
-                                      kv.struct(), _p(local_lens), _p(sink), _p(out),
+                                      kv.struct(layout), _p(local_lens), _p(sink), _p(out),
                                       _dtype(out), _p(out_lse), _p(err), _stream(stream)))
     return out, out_lse
 
@@ -424,7 +428,7 @@ def decode_partial_mla(layout, q, kv: PagedKV, local_lens, scale, v_dim=512, par
         part_lse = torch.empty((layout.dcp_size, B, Hq), dtype=torch.float32, device=dev)
     ws = _workspace(layout, KIND_MLA, B, Hq, 1, v_dim, dev, workspace)
     _check(lib.dcp_decode_partial_mla(layout, _p(q), B, Hq, dk, v_dim, float(scale), _dtype(q),
-                                      kv.struct(), _p(local_lens), _p(part_o), _p(part_lse),
+                                      kv.struct(layout), _p(local_lens), _p(part_o), _p(part_lse),
                                       _p(ws), ws.numel(), _p(err), _stream(stream)))
     return part_o, part_lse
 
@@ -442,7 +446,7 @@ def decode_mla(layout, q, kv: PagedKV, local_lens, scale, v_dim=512, sink=None, 
         out_lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
     ws = _workspace(layout, KIND_MLA, B, Hq, 1, v_dim, dev, workspace)
     _check(lib.dcp_decode_mla(layout, _p(q), B, Hq, dk, v_dim, float(scale), _dtype(q),
-                              kv.struct(), _p(local_lens), _p(sink), _p(out), _dtype(out),
+                              kv.struct(layout), _p(local_lens), _p(sink), _p(out), _dtype(out),
                               _p(out_lse), _p(ws), ws.numel(), _p(err), _stream(stream)))
     return out, out_lse
 
@@ -521,8 +525,8 @@ def sfa_compact_blocks(layout, kv: PagedKV, topk, q_req, seq_lens, max_blocks, e
     counts = torch.empty(layout.dcp_size, dtype=torch.int32, device=dev)
     index = torch.empty((Q, K), dtype=torch.int64, device=dev)
     _check(lib.dcp_sfa_compact_blocks(layout, _p(topk), _p(q_req), Q, K, _p(seq_lens),
-                                      kv.block_table.shape[-2], kv.struct(), kv_dim, _dtype(pool),
-                                      int(max_blocks), _p(blocks), _p(ids), _p(counts),
+                                      kv.block_table.shape[-2], kv.struct(layout), kv_dim,
+                                      _dtype(pool), int(max_blocks), _p(blocks), _p(ids), _p(counts),
                                       _p(index), _p(ws), ws.numel(), _p(err), _stream(stream)))
     return blocks, ids, counts, index
 
@@ -539,7 +543,7 @@ def sfa_decode_partial(layout, q, kv: PagedKV, sel_rank, sel_slot, scale, v_dim=
     if part_lse is None:
         part_lse = torch.empty((layout.dcp_size, B, Hq), dtype=torch.float32, device=dev)
     _check(lib.dcp_sfa_decode_partial(layout, _p(q), B, Hq, dk, v_dim, float(scale), _dtype(q),
-                                      kv.struct(), _p(sel_rank), _p(sel_slot), K, _p(part_o),
+                                      kv.struct(layout), _p(sel_rank), _p(sel_slot), K, _p(part_o),
                                       _p(part_lse), _p(err), _stream(stream)))
     return part_o, part_lse
 
@@ -558,7 +562,7 @@ def sfa_decode(layout, q, kv: PagedKV, topk, seq_lens, scale, v_dim=512, sink=No
         out_lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
     ws = _workspace(layout, KIND_SFA, B, Hq, 1, v_dim, dev, workspace)
     _check(lib.dcp_sfa_decode(layout, _p(q), B, Hq, dk, v_dim, float(scale), _dtype(q),
-                              kv.struct(), _p(topk), K, _p(seq_lens), _p(sink), _p(out),
+                              kv.struct(layout), _p(topk), K, _p(seq_lens), _p(sink), _p(out),
                               _dtype(out), _p(out_lse), _p(ws), ws.numel(), _p(err),
                               _stream(stream)))
     return out, out_lse

@@ -319,7 +319,8 @@ def test_a_shared_table_as_the_state_has_it(lib, dcp):
     kv2 = lib.PagedKV(list(k[:1]), list(v[:1]), two, nb)
     for bad in (lambda: lib.slot_mapping(L3, req, pos, two, nb),
                 lambda: lib.sfa_remap(L3, topk, seq, two, nb),
-                lambda: lib.PagedKV([k[0]] * 3, [v[0]] * 3, two, nb),
+                lambda: lib.decode_gqa(L3, q, lib.PagedKV([k[0]] * 3, [v[0]] * 3, two, nb),
+                                       lib.local_seq_lens(L3, seq), d ** -0.5),
                 lambda: lib.tree_decode_gqa(L3, q, kv2, dev([0, 1, 2, 3]), seq - 1,
                                             torch.ones(3, dtype=torch.int64, device="cuda"),
                                             d ** -0.5, 1)):

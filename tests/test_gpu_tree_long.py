@@ -114,7 +114,8 @@ def plan(c, tc, per_rank=False, most=None):
         rows, chunk, tile, parts = (1 if most <= nodes else 2) * nodes * G, 16, 128, sms
         extra = 2 + (1 if per_rank else dcp)
     else:
-        rows, chunk, tile, parts, extra = (16 if most * G <= 16 else 32) // G * G, 64, 64, 2 * sms, 0
+        rows, chunk, tile = (16 if most * G <= 16 else 32) // G * G, 64, 64
+        parts, extra = 2 * sms, 0
     entries = []
     for b, (n, T) in enumerate(zip(c.ctx, c.T)):
         held = np.bincount(places(n + T, dcp, bs, I)[0], minlength=dcp) if T else np.zeros(dcp, int)
@@ -148,7 +149,8 @@ LONG = {
                           [1 + i % 8 for i in range(80)], 1, True),
     "two-streams-joined": (BF16, 16, 4, 128, 4, 16, 1, [1300 + 61 * (i % 13) for i in range(40)],
                            [64 - i % 31 for i in range(40)], 2, True),
-    "one-stream-joined-wide-heads": (BF16, 16, 4, 128, 8, 64, 1, [1100 + 97 * (i % 11) for i in range(40)],
+    "one-stream-joined-wide-heads": (BF16, 16, 4, 128, 8, 64, 1,
+                                     [1100 + 97 * (i % 11) for i in range(40)],
                                      [32 - i % 9 for i in range(40)], 1, True),
 }
 
@@ -331,7 +333,8 @@ def test_nodes_of_many_ranks_that_see_themselves_alone(lib, offset):
 @pytest.mark.parametrize("B", [3, 40])
 def test_a_workspace_aligned_to_sixteen_bytes(lib, dtype, B):
     """And to no more, with a plan made by the kernel's CTAs (3 requests) and one by itself."""
-    c = Case(lib, dtype, 8, 2, 64, 2, 16, 1, [90 + b for b in range(B)], [1 + b % 9 for b in range(B)])
+    c = Case(lib, dtype, 8, 2, 64, 2, 16, 1, [90 + b for b in range(B)],
+             [1 + b % 9 for b in range(B)])
     need = lib.tree_workspace_size(c.layout, B, 9, 8, 2, 64, dtype)
     room = torch.empty(need + 64, dtype=torch.uint8, device="cuda")
     args = c.args(lib)
