@@ -326,3 +326,102 @@ def test_a_shared_table_as_the_state_has_it(lib, dcp):
                                             d ** -0.5, 1)):
         with pytest.raises(lib.DcpError):
             bad()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_pages_beyond_thirty_two_bits(lib, dtype):
+    """A step on the last pages of pools of more than 2^31 elements gives what it gives on the
+    first pages of small ones."""
+    Hq, Hkv, d, bs, B, T = 8, 2, 128, 16, 3, 5
+    far = 2 ** 31 // (Hkv * bs * d)              # pages
+    L = lib.Layout(1, bs, 1)
+    inv = dev(10000.0 ** (-np.arange(64) / 64), np.float32)
+    ctx, mask = dev([40, 0, 100]), dev([1, 3, 5, 13, 17] * B, np.int64)
+    got = []
+    for first, nb in ((0, 40), (far - 3, far + 40)):      # the border lies among them
+        gen = torch.Generator().manual_seed(1)
+        k, v = (torch.empty((nb, Hkv, bs, d), dtype=dtype, device="cuda") for _ in range(2))
+        for p in (k, v):
+            p[first:first + 40] = torch.randn((40, Hkv, bs, d), generator=gen).to(dtype).cuda()
+        bt = (np.random.default_rng(2).permutation(24) + first).astype(np.int32).reshape(1, B, 8)
+        table, pset = dev(bt), lib.PoolSet([[k], [v]])
+        x = torch.randn((B * T, Hq + 2 * Hkv, d), generator=gen).to(dtype).cuda()
+        q, kn, vn = x.split([Hq, Hkv, Hkv], 1)
+        at = ctx.long().repeat_interleave(T) + torch.arange(T, device="cuda").repeat(B)
+        err = torch.zeros(1, dtype=I32, device="cuda")
+        _, slot = lib.slot_mapping(L, dev(np.repeat(np.arange(B), T)), at, table, nb, err=err)
+        qr = lib.rope_write_gqa(L, q, kn, vn, at, inv, slot, [k], [v], nb, err=err)
+        kv = lib.PagedKV([k], [v], table, nb)
+        out, lse = lib.tree_decode_gqa(L, qr, kv, dev(np.arange(B + 1) * T), ctx, mask, 0.1, T,
+                                       err=err)
+        new = lib.cache_compact(L, pset, table, nb, ctx, dev([[0, 2, 3], [1, 4, 0], [3, 0, 0]]),
+                                dev([3, 2, 1]), err=err)
+        lib.pages_copy(L, pset, dev([[first, first + 39]]), dev([[first + 30, first + 31]]), err=err)
+        assert err.item() == 0
+        got.append((qr, out, lse, new, k[first:first + 40].clone(), v[first:first + 40].clone()))
+        del k, v, kv, pset
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_pages_in_a_graph(lib):
+    """Free, fork, copy and grow, captured and replayed on other lists, against the model."""
+    dcp, bs, I, B, VB, nb = 3, 16, 4, 12, 6, 60
+    L = lib.Layout(dcp, bs, I)
+    pages, m = lib.Pages.new(L, B, VB, nb), R.PageModel(dcp, bs, I, B, VB, nb, False)
+    pool = torch.randn((dcp, nb, 2, bs, 32), generator=torch.Generator().manual_seed(0)).cuda()
+    start, pset = pool.clone(), lib.PoolSet([list(pool)])
+    rng = np.random.default_rng(4)
+    lens = rng.integers(1, VB * bs * dcp // 2, 4)
+    lib.pages_resize(L, pages, dev(range(4)), dev(lens))
+    m.resize(np.arange(4), lens)
+    state = [getattr(pages, a) for a in ("block_table", "seq_lens", "ref_count", "free_bits")]
+    before = [x.clone() for x in state]
+    zero, child, parent = torch.zeros(6, dtype=I32, device="cuda"), dev([0] * 6), dev([0] * 6)
+    grown = dev([0] * 6)
+
+    def step():
+        lib.pages_resize(L, pages, child, zero)
+        src, dst = lib.pages_fork(L, pages, parent, child)
+        lib.pages_copy(L, pset, src, dst)
+        s2, d2 = lib.pages_resize(L, pages, child, grown)
+        lib.pages_copy(L, pset, s2, d2)
+        return src, dst, s2, d2
+
+    def lists():
+        c, p = 4 + rng.permutation(8)[:6], rng.integers(0, 4, 6)
+        g = np.minimum(m.seq[p] + rng.integers(-20, 9, 6), VB * bs * dcp).clip(0)
+        for to, x in ((child, c), (parent, p), (grown, g)):
+            to.copy_(dev(x))
+        return c, p, g
+
+    lists()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for x, y in zip(state, before):          # as it was before the warm-up
+        x.copy_(y)
+    pool.copy_(start)
+    want = start.cpu().clone()
+    for _ in range(6):
+        c, p, grow = lists()
+        m.resize(c, np.zeros(6, dtype=int))
+        es = list(m.fork(p, c))
+        es += m.resize(c, grow)
+        g.replay()
+        assert m.err == 0
+        for x, y in zip(got, es):
+            assert np.array_equal(x.cpu().numpy(), y)
+        for a, b in ((es[0], es[1]), (es[2], es[3])):
+            for r in range(dcp):
+                for x, y in zip(a[r], b[r]):
+                    if x >= 0:
+                        want[r, y] = want[r, x].clone()
+        assert torch.equal(pool.cpu(), want)
+        for x, y in zip(state, (m.bt, m.seq, m.ref, m.bits())):
+            assert np.array_equal(x.cpu().numpy(), y)
