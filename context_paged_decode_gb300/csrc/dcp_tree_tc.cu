@@ -10,7 +10,7 @@
 // whole call): 32 requests x 16 nodes, 32 query over 8 key heads of 128, 8
 // ranks, up to 65536 tokens (3.05 GB): 452-466 us, 6.5-6.7 TB/s, 0.97-0.99 of
 // the copy bandwidth.  8 requests x 64 nodes (256 rows) over up to 65536 tokens
-// (655 MB, 149 GFLOP): 152-159 us, 4.2 TB/s and 0.95 PFLOP/s; there a tile's chain
+// (655 MB, 149 GFLOP): 152-160 us, 4.2 TB/s and 0.95 PFLOP/s; there a tile's chain
 // of scores, softmax and products is what the two streams cannot fill (copies of
 // the kernel without the products, or without the exponentials, took 0.93 and
 // 0.97 of its time), and short contexts are bound by what a unit costs beside
