@@ -48,6 +48,17 @@ class PagedKVStruct(C.Structure):
                 ("bt_rank_stride", C.c_int64)]
 
 
+class PagedKV8Struct(C.Structure):
+    _fields_ = [("k", RankPtrs), ("v", RankPtrs), ("scale", RankPtrs), ("num_blocks", C.c_int64),
+                ("block_table", C.c_void_p), ("max_vblocks", C.c_int32),
+                ("bt_rank_stride", C.c_int64)]
+
+
+class ScoresStruct(C.Structure):
+    _fields_ = [("cap", C.c_float), ("window", C.c_int32), ("prefix", C.c_int32),
+                ("slopes", C.c_void_p), ("first", C.c_void_p)]
+
+
 class PagesStruct(C.Structure):
     _fields_ = [("block_table", C.c_void_p), ("seq_lens", C.c_void_p), ("ref_count", C.c_void_p),
                 ("free_bits", C.c_void_p), ("num_reqs", C.c_int32), ("max_vblocks", C.c_int32),
@@ -88,6 +99,7 @@ def load(path: str = LIB_PATH):
     lib = C.CDLL(path)
     i32, i64, vp, f32 = C.c_int32, C.c_int64, C.c_void_p, C.c_float
     L, RP, PK, PG, PS = Layout, RankPtrs, PagedKVStruct, PagesStruct, PoolSetStruct
+    P8, SF = PagedKV8Struct, ScoresStruct
     sig = {
         "dcp_strerror": (C.c_char_p, [C.c_int]),
         "dcp_version": (C.c_int, []),
@@ -142,6 +154,20 @@ def load(path: str = LIB_PATH):
         "dcp_pages_fork": (C.c_int, [L, PG, vp, vp, i32, vp, vp, vp, C.c_size_t, vp, vp]),
         "dcp_pages_copy": (C.c_int, [L, PS, vp, vp, i32, i32, vp, vp]),
         "dcp_cache_compact": (C.c_int, [L, PS, vp, i32, i32, i64, vp, vp, vp, i32, vp, vp, vp]),
+        "dcp_q8_append_gqa": (C.c_int, [L, vp, i64, vp, i64, i32, vp, vp, i32, i32, i32, C.c_int,
+                                        P8, vp, vp]),
+        "dcp_q8_gather_gqa": (C.c_int, [L, P8, i32, i32, i32, vp, vp, i64, vp, vp, C.c_int, vp,
+                                        vp]),
+        "dcp_q8_decode_gqa": (C.c_int, [L, vp, i32, i32, i32, i32, f32, C.c_int, P8, vp, SF, vp,
+                                        vp, C.c_int, vp, vp, C.c_size_t, vp, vp]),
+        "dcp_q8_partial_gqa": (C.c_int, [L, vp, i32, i32, i32, i32, f32, C.c_int, P8, vp, SF, vp,
+                                         vp, vp, C.c_size_t, vp, vp]),
+        "dcp_scored_decode_gqa": (C.c_int, [L, vp, i32, i32, i32, i32, f32, C.c_int, PK, vp, SF,
+                                            vp, vp, C.c_int, vp, vp, C.c_size_t, vp, vp]),
+        "dcp_scored_partial_gqa": (C.c_int, [L, vp, i32, i32, i32, i32, f32, C.c_int, PK, vp, SF,
+                                             vp, vp, vp, C.c_size_t, vp, vp]),
+        "dcp_scored_workspace_size": (C.c_int, [L, i32, i32, i32, i32, i32,
+                                                C.POINTER(C.c_size_t)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -165,7 +191,9 @@ def exported_symbols():
             "dcp_tree_workspace_size", "dcp_tree_partial_gqa", "dcp_tree_decode_gqa",
             "dcp_rope_write_gqa", "dcp_rope_write_mla", "dcp_pages_init",
             "dcp_pages_workspace_size", "dcp_pages_resize", "dcp_pages_fork", "dcp_pages_copy",
-            "dcp_cache_compact"]
+            "dcp_cache_compact", "dcp_q8_append_gqa", "dcp_q8_gather_gqa", "dcp_q8_decode_gqa",
+            "dcp_q8_partial_gqa", "dcp_scored_decode_gqa", "dcp_scored_partial_gqa",
+            "dcp_scored_workspace_size"]
 
 
 def _check(rc):
@@ -725,3 +753,119 @@ def cache_compact(layout, pools: PoolSet, block_table, num_blocks, ctx_lens, pat
     that all ranks share: [B, max_vb] or [1, B, max_vb]."""
     return (_bind or _load_binding()).cache_compact(layout, pools, block_table, num_blocks,
                                                     ctx_lens, path, path_len, new_lens, err, stream)
+
+
+# ---------------------------------------------------------------------------
+# the cache in 8 bits, and scored decode attention
+# ---------------------------------------------------------------------------
+
+class PagedKV8:
+    """A paged cache in 8 bits (see dcp_paged_kv8_t): per-rank pools k_pools and
+    v_pools [num_blocks, Hkv, bs, d] of torch.float8_e4m3fn, per-rank scales
+    [num_blocks, Hkv, 4] float32 (of a page and head that of its keys, that of
+    its values, and two unused), and the block table as for PagedKV."""
+
+    def __init__(self, k_pools, v_pools, scales, block_table, num_blocks):
+        self.k_pools, self.v_pools, self.scales = list(k_pools), list(v_pools), list(scales)
+        self.block_table = block_table
+        self.num_blocks = int(num_blocks)
+        _cuda_contig(block_table, *self.k_pools, *self.v_pools, *self.scales)
+        if block_table.dtype != torch.int32:
+            raise DcpError("block_table must be int32")
+        if any(t.dtype != torch.float8_e4m3fn for t in self.k_pools + self.v_pools):
+            raise DcpError("the pools of an 8-bit cache must be float8_e4m3fn")
+        if any(t.dtype != torch.float32 or t.dim() != 3 or t.shape[-1] != 4 for t in self.scales):
+            raise DcpError("scales must be float32 [blocks, heads, 4]")
+
+    @classmethod
+    def new(cls, layout, num_blocks, num_kv_heads, head_dim, block_table):
+        """An empty cache on the table's device: what its pages hold is written
+        before it is read, but for the scales' unused numbers, which are zeros."""
+        mk = lambda: [torch.empty((num_blocks, num_kv_heads, layout.block_size, head_dim),  # noqa: E731
+                                  dtype=torch.float8_e4m3fn, device=block_table.device)
+                      for _ in range(layout.dcp_size)]
+        return cls(mk(), mk(), [torch.zeros((num_blocks, num_kv_heads, 4), device=block_table.device)
+                                for _ in range(layout.dcp_size)], block_table, num_blocks)
+
+    def struct(self, layout=None):
+        raise DcpError("a cache in 8 bits: the q8_ calls read it")
+
+
+class Scores:
+    """How scores are formed and which tokens are seen (see dcp_scores_t): a cap
+    (0: none), a window of the last tokens (0: all) with the document's first
+    `prefix` tokens beside it, slopes [Hq] float32 of a bias by distance, and
+    the first token [B] int32 of each request's document."""
+
+    def __init__(self, cap=0.0, window=0, prefix=0, slopes=None, first=None):
+        self.cap, self.window, self.prefix = float(cap), int(window), int(prefix)
+        self.slopes, self.first = slopes, first
+
+
+def scored_workspace_size(layout, num_reqs, num_q_heads, num_kv_heads, head_dim, per_rank=False):
+    """Bytes of workspace of the scored_ and q8_ attention calls for this shape."""
+    n = C.c_size_t(0)
+    _check(load().dcp_scored_workspace_size(layout, num_reqs, num_q_heads, num_kv_heads, head_dim,
+                                            int(per_rank), C.byref(n)))
+    return n.value
+
+
+def q8_append_gqa(layout, k, v, kv: PagedKV8, q_start, ctx_lens, err=None, stream=None):
+    """Quantise k, v [N, Hkv, d] into the cache: rows q_start[b] .. q_start[b+1]
+    go to positions ctx_lens[b] .. of request b.  k, v may be slices of one
+    projection."""
+    (_bind or _load_binding()).q8_append(layout, k, v, kv, q_start, ctx_lens, err, stream)
+
+
+def q8_gather_gqa(layout, kv: PagedKV8, req_idx, positions, dtype=torch.bfloat16, k_out=None,
+                  v_out=None, err=None, stream=None):
+    """Keys and values [N, Hkv, d] of tokens (req_idx[t], positions[t])."""
+    return (_bind or _load_binding()).q8_gather(layout, kv, req_idx, positions, dtype, k_out, v_out,
+                                                err, stream)
+
+
+def q8_decode_gqa(layout, q, kv: PagedKV8, seq_lens, scale, scores=None, sink=None, out_dtype=None,
+                  out=None, out_lse=None, workspace=None, err=None, stream=None):
+    """decode_gqa over a cache in 8 bits, from the lengths [B] themselves."""
+    return (_bind or _load_binding()).scored(True, False, layout, q, kv, seq_lens, scale, scores,
+                                             sink, out_dtype, out, out_lse, workspace, err, stream)
+
+
+def q8_partial_gqa(layout, q, kv: PagedKV8, seq_lens, scale, scores=None, part_o=None,
+                   part_lse=None, workspace=None, err=None, stream=None):
+    """q8_decode_gqa's per-rank partials, for lse_merge."""
+    return (_bind or _load_binding()).scored(True, True, layout, q, kv, seq_lens, scale, scores,
+                                             None, None, part_o, part_lse, workspace, err, stream)
+
+
+def scored_decode_gqa(layout, q, kv: PagedKV, seq_lens, scale, scores, sink=None, out_dtype=None,
+                      out=None, out_lse=None, workspace=None, err=None, stream=None):
+    """decode_gqa with scores formed as `scores` says, from the lengths [B]."""
+    return (_bind or _load_binding()).scored(False, False, layout, q, kv, seq_lens, scale, scores,
+                                             sink, out_dtype, out, out_lse, workspace, err, stream)
+
+
+def scored_partial_gqa(layout, q, kv: PagedKV, seq_lens, scale, scores, part_o=None, part_lse=None,
+                       workspace=None, err=None, stream=None):
+    """scored_decode_gqa's per-rank partials, for lse_merge."""
+    return (_bind or _load_binding()).scored(False, True, layout, q, kv, seq_lens, scale, scores,
+                                             None, None, part_o, part_lse, workspace, err, stream)
+
+
+def q8_pages_copy(layout, caches, copy_src, copy_dst, err=None, stream=None):
+    """pages_copy for the caches (of all layers) in 8 bits: their pages and their
+    scales.  `caches` is a Q8Pools."""
+    pages_copy(layout, caches.pages, copy_src, copy_dst, err=err, stream=stream)
+    pages_copy(Layout(layout.dcp_size, 1, 1), caches.scales, copy_src, copy_dst, stream=stream)
+
+
+class Q8Pools:
+    """The pools and scales of several PagedKV8 of one shape, for q8_pages_copy."""
+
+    def __init__(self, caches):
+        caches = list(caches)
+        # as bytes: the copies move them unchanged
+        self.pages = PoolSet([[t.view(torch.uint8) for t in p]
+                              for c in caches for p in (c.k_pools, c.v_pools)])
+        # a head's scales are 16 bytes, its page's one row
+        self.scales = PoolSet([[t.unsqueeze(2) for t in c.scales] for c in caches])

@@ -1,5 +1,6 @@
 // Python binding of the calls around the decode step (drafted trees, rotary
-// writes, pages, compaction) to the C ABI of libdcp.so.
+// writes, pages, compaction), of the 8-bit cache and of scored decode attention
+// to the C ABI of libdcp.so.
 //
 // These calls last a few microseconds on the GPU, and what Python spends on
 // checking their tensors one attribute at a time was several times that (28 us
@@ -39,6 +40,13 @@ struct Lib {
   decltype(&dcp_pages_fork) pages_fork;
   decltype(&dcp_pages_copy) pages_copy;
   decltype(&dcp_cache_compact) cache_compact;
+  decltype(&dcp_q8_append_gqa) q8_append_gqa;
+  decltype(&dcp_q8_gather_gqa) q8_gather_gqa;
+  decltype(&dcp_q8_decode_gqa) q8_decode_gqa;
+  decltype(&dcp_q8_partial_gqa) q8_partial_gqa;
+  decltype(&dcp_scored_decode_gqa) scored_decode_gqa;
+  decltype(&dcp_scored_partial_gqa) scored_partial_gqa;
+  decltype(&dcp_scored_workspace_size) scored_workspace_size;
 } g_lib;
 
 // A refusal on its way to Python (the error is set).
@@ -596,6 +604,204 @@ PyObject* cache_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A paged cache: its pools are [num_blocks, heads, block_size, head_dim] of `type`,
+// e4m3 with scales where `eight`, and its table has rows for B requests.
+struct PagedCache {
+  dcp_paged_kv_t kv = {};
+  dcp_paged_kv8_t kv8 = {};
+  int64_t Hkv, d;
+
+  PagedCache(PyObject* o, const dcp_layout_t& L, bool eight, at::ScalarType type, int64_t B,
+             int dev) {
+    if (PyObject_HasAttr(o, NAME("scales")) != eight)
+      refuse(eight ? "a 16- or 32-bit cache, where one in 8 bits (PagedKV8) is needed"
+                   : "a cache in 8 bits: the q8_ calls read it");
+    Ref kp(attr(o, NAME("k_pools"))), vp(attr(o, NAME("v_pools"))),
+        bto(attr(o, NAME("block_table")));
+    if (vp.o == Py_None) refuse("the cache has no value pools");
+    const int64_t nb = integer_attr(o, NAME("num_blocks"));
+    Ref kseq(PySequence_Fast(kp.o, "k_pools must be a sequence of tensors"));
+    if (PySequence_Fast_GET_SIZE(kseq.o) < 1) refuse("the cache has no pools");
+    const at::Tensor& first = tensor(PySequence_Fast_GET_ITEM(kseq.o, 0), "k_pools");
+    if (first.dim() != 4) refuse("pools must be [blocks, heads, block_size, head_dim]");
+    Hkv = first.size(1);
+    d = first.size(3);
+    if (Hkv < 1) refuse("pools without heads");
+    const int64_t shape[4] = {nb, Hkv, L.block_size, d}, scales[3] = {nb, Hkv, 4};
+    const at::ScalarType pool = eight ? at::kFloat8_e4m3fn : type;
+    kv8.k = kv.k = rank_list(L, kp.o, "k_pools", pool, shape, dev);
+    kv8.v = kv.v = rank_list(L, vp.o, "v_pools", pool, shape, dev);
+    if (eight) {
+      Ref sc(attr(o, NAME("scales")));
+      kv8.scale = rank_list(L, sc.o, "scales", at::kFloat, scales, dev);
+    }
+    const at::Tensor& bt = tensor(bto.o, "block_table");
+    const int64_t dim = bt.dim();
+    if (dim != 2 && dim != 3) refuse("block_table must be [requests, blocks] or [ranks, ...]");
+    kv.block_table = (const int32_t*)ptr(bt, "block_table", at::kInt, bt.sizes(), dev);
+    kv.num_blocks = nb;
+    kv.max_vblocks = small(bt.size(dim - 1), "max_vblocks");
+    const bool each = dim == 3 && bt.size(0) != 1;   // one for each rank, not one for all
+    kv.bt_rank_stride = each ? bt.size(1) * bt.size(2) : 0;
+    if (each && bt.size(0) < L.dcp_size)
+      refuse(std::to_string(bt.size(0)) + " block tables for " + std::to_string(L.dcp_size) +
+             " ranks");
+    if (bt.size(dim - 2) < B)
+      refuse("a block table of " + std::to_string(bt.size(dim - 2)) + " requests, " +
+             std::to_string(B) + " are needed");
+    kv8.num_blocks = kv.num_blocks;
+    kv8.block_table = kv.block_table;
+    kv8.max_vblocks = kv.max_vblocks;
+    kv8.bt_rank_stride = kv.bt_rank_stride;
+  }
+};
+
+// q8_append(layout, k, v, kv, q_start, ctx_lens, err, stream)
+PyObject* q8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 8);
+    const dcp_layout_t L = layout_of(a[0]);
+    const at::Tensor& k = tensor(a[1], "k");
+    const int dev = device_of(k, "k");
+    const OnStream on(a[7], dev);
+    if (k.dim() != 3) refuse("k must be [tokens, heads, head_dim]");
+    const at::ScalarType type = k.scalar_type();
+    const dcp_dtype_t dt = dtype_of(type);
+    const at::Tensor& ctx = tensor(a[5], "ctx_lens");
+    if (ctx.dim() != 1) refuse("ctx_lens must be [requests]");
+    const int64_t B = ctx.size(0), N = k.size(0);
+    const PagedCache c(a[3], L, true, type, B, dev);
+    const int64_t shape[3] = {N, c.Hkv, c.d};
+    int64_t ks, vs;
+    const void* pk = tokens(k, "k", type, shape, dev, ks);
+    const void* pv = tokens(tensor(a[2], "v"), "v", type, shape, dev, vs);
+    const int32_t* start = (const int32_t*)ptr(a[4], "q_start", at::kInt, {B + 1}, dev);
+    const int32_t* pc = (const int32_t*)ptr(ctx, "ctx_lens", at::kInt, {B}, dev);
+    check(g_lib.q8_append_gqa(L, pk, ks, pv, vs, small(N, "tokens"), start, pc,
+                              small(B, "requests"), small(c.Hkv, "heads"), small(c.d, "head_dim"),
+                              dt, c.kv8, err_ptr(a[6], dev), on.st));
+    return given(Py_None);
+  });
+}
+
+// q8_gather(layout, kv, req_idx, positions, dtype, k_out, v_out, err, stream)
+PyObject* q8_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 9);
+    const dcp_layout_t L = layout_of(a[0]);
+    const at::Tensor& req = tensor(a[2], "req_idx");
+    const int dev = device_of(req, "req_idx");
+    const OnStream on(a[8], dev);
+    if (req.dim() != 1) refuse("req_idx must be [tokens]");
+    const int64_t N = req.size(0);
+    if (!THPDtype_Check(a[4])) refuse("dtype must be a torch dtype");
+    at::ScalarType type = ((THPDtype*)a[4])->scalar_type;
+    if (a[5] != Py_None) type = tensor(a[5], "k_out").scalar_type();
+    const dcp_dtype_t dt = dtype_of(type);
+    const PagedCache c(a[1], L, true, type, 0, dev);
+    Ref bto(attr(a[1], NAME("block_table")));
+    const at::Tensor& bt = tensor(bto.o, "block_table");
+    const int64_t shape[3] = {N, c.Hkv, c.d};
+    const int32_t* pr = (const int32_t*)ptr(req, "req_idx", at::kInt, {N}, dev);
+    const int64_t* pp = (const int64_t*)ptr(a[3], "positions", at::kLong, {N}, dev);
+    int32_t* err = err_ptr(a[7], dev);
+    at::Tensor k, v;
+    if (a[5] == Py_None) k = fresh(shape, type, dev);
+    if (a[6] == Py_None) v = fresh(shape, type, dev);
+    void* pk = a[5] == Py_None ? k.data_ptr() : ptr(a[5], "k_out", type, shape, dev);
+    void* pv = a[6] == Py_None ? v.data_ptr() : ptr(a[6], "v_out", type, shape, dev);
+    check(g_lib.q8_gather_gqa(L, c.kv8, small(bt.size(bt.dim() - 2), "requests"),
+                              small(c.Hkv, "heads"), small(c.d, "head_dim"), pr, pp, N, pk, pv, dt,
+                              err, on.st));
+    Ref ko(a[5] == Py_None ? THPVariable_Wrap(k) : given(a[5])),
+        vo(a[6] == Py_None ? THPVariable_Wrap(v) : given(a[6]));
+    return PyTuple_Pack(2, ko.o, vo.o);
+  });
+}
+
+// scored(eight, partial, layout, q, kv, seq_lens, scale, scores, sink, out_dtype, out, out_lse,
+//        workspace, err, stream)
+PyObject* scored(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 15);
+    const bool eight = truth(a[0]), partial = truth(a[1]);
+    const dcp_layout_t L = layout_of(a[2]);
+    const at::Tensor& q = tensor(a[3], "q");
+    const int dev = device_of(q, "q");
+    const OnStream on(a[14], dev);
+    if (q.dim() != 3) refuse("q must be [requests, heads, head_dim]");
+    const int64_t B = q.size(0), Hq = q.size(1), d = q.size(2);
+    const at::ScalarType type = q.scalar_type();
+    const dcp_dtype_t dt = dtype_of(type);
+    const PagedCache c(a[4], L, eight, type, B, dev);
+    if (c.d != d)
+      refuse("q with head_dim " + std::to_string(d) + " over a cache with " + std::to_string(c.d));
+    if (Hq % c.Hkv)
+      refuse(std::to_string(Hq) + " query heads over " + std::to_string(c.Hkv) +
+             " key/value heads");
+    const void* pq = ptr(q, "q", type, q.sizes(), dev);
+    const int32_t* lens = (const int32_t*)ptr(a[5], "seq_lens", at::kInt, {B}, dev);
+    const float scale = (float)number(a[6]);
+    dcp_scores_t f = {};
+    std::optional<Ref> slopes, first;
+    if (a[7] != Py_None) {
+      f.cap = (float)number(attr(a[7], NAME("cap")).o);
+      f.window = small(integer_attr(a[7], NAME("window")), "window");
+      f.prefix = small(integer_attr(a[7], NAME("prefix")), "prefix");
+      slopes.emplace(PyObject_GetAttr(a[7], NAME("slopes")));
+      first.emplace(PyObject_GetAttr(a[7], NAME("first")));
+      f.slopes = (const float*)opt(slopes->o, "slopes", at::kFloat, {Hq}, dev);
+      f.first = (const int32_t*)opt(first->o, "first", at::kInt, {B}, dev);
+    }
+    const float* sink = (const float*)opt(a[8], "sink", at::kFloat, {Hq}, dev);
+    const int32_t b32 = small(B, "requests"), hq = small(Hq, "heads"), hkv = small(c.Hkv, "heads"),
+                  d32 = small(d, "head_dim");
+    size_t need = 0;
+    check(g_lib.scored_workspace_size(L, b32, hq, hkv, d32, partial, &need));
+    const int64_t R = L.dcp_size;
+    std::vector<int64_t> os, ls;
+    if (partial) {
+      os = {R, B, Hq, d};
+      ls = {R, B, Hq};
+    } else {
+      os = {B, Hq, d};
+      ls = {B, Hq};
+    }
+    at::ScalarType odt = type;
+    if (partial)
+      odt = at::kFloat;
+    else if (a[10] != Py_None)
+      odt = tensor(a[10], "out").scalar_type();
+    else if (a[9] != Py_None) {
+      if (!THPDtype_Check(a[9])) refuse("out_dtype must be a torch dtype");
+      odt = ((THPDtype*)a[9])->scalar_type;
+    }
+    const dcp_dtype_t codt = dtype_of(odt);
+    int32_t* err = err_ptr(a[13], dev);
+    at::Tensor o, l;
+    if (a[10] == Py_None) o = fresh(os, odt, dev);
+    if (a[11] == Py_None) l = fresh(ls, at::kFloat, dev);
+    void* po = a[10] == Py_None ? o.data_ptr() : ptr(a[10], "out", odt, os, dev);
+    float* pl = (float*)(a[11] == Py_None ? l.data_ptr() : ptr(a[11], "out_lse", at::kFloat, ls, dev));
+    const Workspace ws(a[12], need, dev);
+    int rc;
+    if (eight)
+      rc = partial ? g_lib.q8_partial_gqa(L, pq, b32, hq, hkv, d32, scale, dt, c.kv8, lens, f,
+                                          (float*)po, pl, ws.p, ws.bytes, err, on.st)
+                   : g_lib.q8_decode_gqa(L, pq, b32, hq, hkv, d32, scale, dt, c.kv8, lens, f, sink,
+                                         po, codt, pl, ws.p, ws.bytes, err, on.st);
+    else
+      rc = partial ? g_lib.scored_partial_gqa(L, pq, b32, hq, hkv, d32, scale, dt, c.kv, lens, f,
+                                              (float*)po, pl, ws.p, ws.bytes, err, on.st)
+                   : g_lib.scored_decode_gqa(L, pq, b32, hq, hkv, d32, scale, dt, c.kv, lens, f,
+                                             sink, po, codt, pl, ws.p, ws.bytes, err, on.st);
+    check(rc);
+    Ref oo(a[10] == Py_None ? THPVariable_Wrap(o) : given(a[10])),
+        ol(a[11] == Py_None ? THPVariable_Wrap(l) : given(a[11]));
+    return PyTuple_Pack(2, oo.o, ol.o);
+  });
+}
+
 // init(path of libdcp.so, DcpError)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -622,6 +828,13 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     get(g_lib.pages_fork, "dcp_pages_fork");
     get(g_lib.pages_copy, "dcp_pages_copy");
     get(g_lib.cache_compact, "dcp_cache_compact");
+    get(g_lib.q8_append_gqa, "dcp_q8_append_gqa");
+    get(g_lib.q8_gather_gqa, "dcp_q8_gather_gqa");
+    get(g_lib.q8_decode_gqa, "dcp_q8_decode_gqa");
+    get(g_lib.q8_partial_gqa, "dcp_q8_partial_gqa");
+    get(g_lib.scored_decode_gqa, "dcp_scored_decode_gqa");
+    get(g_lib.scored_partial_gqa, "dcp_scored_partial_gqa");
+    get(g_lib.scored_workspace_size, "dcp_scored_workspace_size");
     return given(Py_None);
   });
 }
@@ -631,7 +844,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 PyMethodDef g_methods[] = {DCP_METHOD(init),       DCP_METHOD(tree),  DCP_METHOD(rope),
                            DCP_METHOD(pages_init), DCP_METHOD(pages), DCP_METHOD(pages_copy),
-                           DCP_METHOD(cache_compact), {nullptr, nullptr, 0, nullptr}};
+                           DCP_METHOD(cache_compact), DCP_METHOD(q8_append),
+                           DCP_METHOD(q8_gather), DCP_METHOD(scored), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,
                         nullptr,               nullptr,    nullptr, nullptr};

@@ -1,0 +1,547 @@
+// Scored decode attention: one query per request over the sharded paged cache
+// in 16, 32 or 8 bits, with scores that may be capped, biased by distance, or
+// limited to a window, the document's first tokens and the document.  This
+// file has the kernel for any type and shape, the merge of units that were
+// cut, and the entry points; dcp_scored_mma.cu has the tensor-core kernel.
+//
+// With L tokens, the query at position L - 1, and x the position of a key:
+//     t = scale q.k;  t = cap tanh(t / cap);  t = t - slope[h] (L - 1 - x)
+//     lse = ln( sum_seen e^t + e^sink ),  o = sum_seen e^(t - lse) v.
+#include <math.h>
+
+#include "dcp_q8.cuh"
+#include "dcp_scored.cuh"
+
+namespace dcp {
+
+// ---------------------------------------------------------------------------
+// any type and shape
+// ---------------------------------------------------------------------------
+
+// Four values of a cache row in 32 bits.
+template <int kKind>
+struct Four;
+template <>
+struct Four<kCacheF32> {
+  using Raw = float4;
+  static constexpr int kBytes = 16;
+  static __device__ __forceinline__ float4 of(Raw x) { return x; }
+};
+template <>
+struct Four<kCacheBf16> {
+  using Raw = uint2;
+  static constexpr int kBytes = 8;
+  static __device__ __forceinline__ float4 of(Raw x) {
+    return make_float4(bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y));
+  }
+};
+template <>
+struct Four<kCacheE4m3> {
+  using Raw = uint32_t;
+  static constexpr int kBytes = 4;
+  static __device__ __forceinline__ float4 of(Raw x) { return e4m3x4_f32(x); }
+};
+
+// Eight lanes take a token, so a warp takes four at a time and sums a score by
+// three shuffles; HP heads of the unit in one pass over the tokens.  The
+// products run in fp32 on the CUDA cores.
+template <int kKind, int DI, int HP>
+__global__ void __launch_bounds__(kScoredWarps * 32)
+scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
+  using F = Four<kKind>;
+  using Raw = typename F::Raw;
+  __shared__ __align__(16) float s_q[HP][DI * 32];
+  __shared__ __align__(16) float s_o[kScoredWarps][HP][DI * 32];
+  __shared__ float s_m[kScoredWarps][HP], s_l[kScoredWarps][HP];
+  griddep_launch_dependents();   // the merge may start its launch
+  griddep_wait();                // launched chained: the preceding kernel completed
+  const Run run = plan_run<kScoredWarps * 32>(A);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int sub = lane & 7, grp = lane >> 3;
+  const int di = A.d / 32;
+  int64_t start = run.start;
+  int e = run.e, n = 0;
+  bool fresh = true;
+  for (int64_t t = run.t0; t < run.t1;) {
+    if (fresh) {
+      n = entry_tiles(A, e, false);
+      fresh = false;
+    }
+    if (t >= start + (int64_t)n * A.Hkv) {
+      start += (int64_t)n * A.Hkv;
+      ++e;
+      fresh = true;
+      continue;
+    }
+    const int g = (int)((t - start) / n), k0 = (int)(t - start - (int64_t)g * n);
+    const int k1 = (int)min((int64_t)n, k0 + (run.t1 - t));
+    t += k1 - k0;
+    const int b = A.apart ? e % A.B : e, r0 = A.apart ? e / A.B : 0;
+    const int r1 = A.apart ? r0 + 1 : A.S.dcp;
+    const Seen seen = seen_of(A, b, false);
+    const int last = __ldg(A.lens + b) - 1;
+    PieceOut P;
+    P.whole = k0 == 0 && k1 == n;
+    P.slot = blockIdx.x + (int64_t)e * A.Hkv + g;
+    P.row = (int64_t)e * A.Hq + g * A.G;
+    for (int h0 = 0; h0 < A.G; h0 += HP) {
+      __syncthreads();
+      for (int i = tid; i < HP * A.d; i += kScoredWarps * 32) {
+        const int hh = i / A.d, c = i - hh * A.d;
+        const int64_t at = ((int64_t)b * A.Hq + g * A.G + h0 + hh) * A.d + c;
+        s_q[hh][c] = h0 + hh >= A.G ? 0.f
+                     : q_bf16 ? __bfloat162float(((const __nv_bfloat16*)A.q)[at])
+                              : ((const float*)A.q)[at];
+      }
+      __syncthreads();
+      float slope[HP], m[HP], l[HP];
+      float4 o[HP][DI];
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        slope[h] = A.slopes && h0 + h < A.G ? __ldg(A.slopes + g * A.G + h0 + h) : 0.f;
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+#pragma unroll
+        for (int i = 0; i < DI; ++i) o[h][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      for (int k = k0 + warp; k < k1; k += kScoredWarps) {
+        // the k-th tile: rank by rank, first the kept tokens and then the window
+        int r = r0, left = k, p0 = 0, lo = 0, hi = 0;
+        for (; r < r1; ++r) {
+          const RankTokens T = seen.on(A.S, r);
+          const int na = T.a_tiles(), nb = T.b_tiles();
+          if (left < na) {
+            p0 = (T.a0 / kRows + left) * kRows, lo = T.a0, hi = T.a1;
+            break;
+          }
+          left -= na;
+          if (left < nb) {
+            p0 = (T.b0 / kRows + left) * kRows, lo = T.b0, hi = T.b1;
+            break;
+          }
+          left -= nb;
+        }
+        for (int i0 = 0; i0 < kRows; i0 += 4) {
+          const int p = p0 + i0 + grp;
+          const int vb = A.S.by_bs.div(p), loc = p - vb * A.S.bs;
+          bool ok = p >= lo && p < hi;
+          int64_t page = -1;
+          if (ok) {
+            page = vb < A.max_vb
+                       ? (int64_t)__ldg(A.bt + r * A.bt_stride + (int64_t)b * A.max_vb + vb)
+                       : -1;
+            ok = page >= 0 && page < A.nb;
+            if (!ok && sub == 0 && h0 == 0) count_error(A.err);
+          }
+          float4 kk[DI], vv[DI];
+          float ks = 1.f, vs = 1.f;
+          if (ok && kKind == kCacheE4m3) {
+            const float2 s2 = __ldg(reinterpret_cast<const float2*>(A.sc.ptr[r]) +
+                                    (page * A.Hkv + g) * 2);
+            ks = s2.x;
+            vs = s2.y;
+          }
+          const int64_t at = ((page * A.Hkv + g) * A.S.bs + loc) * A.d;
+          const Raw* kr = (const Raw*)((const char*)A.k.ptr[r] + at / 4 * F::kBytes) + sub;
+          const Raw* vr = (const Raw*)((const char*)A.v.ptr[r] + at / 4 * F::kBytes) + sub;
+#pragma unroll
+          for (int i = 0; i < DI; ++i) {
+            kk[i] = vv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (ok && i < di) {
+              kk[i] = F::of(__ldg(kr + 8 * i));
+              vv[i] = F::of(__ldg(vr + 8 * i));
+            }
+          }
+          const float far = (float)(last - A.S.position(vb, r, loc));
+#pragma unroll
+          for (int h = 0; h < HP; ++h) {
+            float dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < DI; ++i) {
+              if (i < di) {
+                const float4 q4 = *reinterpret_cast<const float4*>(&s_q[h][(sub + 8 * i) * 4]);
+                dot = fmaf(q4.x, kk[i].x, dot);
+                dot = fmaf(q4.y, kk[i].y, dot);
+                dot = fmaf(q4.z, kk[i].z, dot);
+                dot = fmaf(q4.w, kk[i].w, dot);
+              }
+            }
+            dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+            dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+            dot += __shfl_xor_sync(0xffffffffu, dot, 4);
+            if (!ok) continue;
+            const float x = formed(A, dot * ks * A.scale, slope[h], far);
+            const float mn = fmaxf(m[h], x);
+            const float ref = mn == -INFINITY ? 0.f : mn;
+            const float a = exp2f(m[h] - ref), w = exp2f(x - ref), wv = w * vs;
+            m[h] = mn;
+            l[h] = l[h] * a + w;
+#pragma unroll
+            for (int i = 0; i < DI; ++i) {
+              o[h][i].x = fmaf(wv, vv[i].x, o[h][i].x * a);
+              o[h][i].y = fmaf(wv, vv[i].y, o[h][i].y * a);
+              o[h][i].z = fmaf(wv, vv[i].z, o[h][i].z * a);
+              o[h][i].w = fmaf(wv, vv[i].w, o[h][i].w * a);
+            }
+          }
+        }
+      }
+      // the four tokens at a time of a warp, then the warps
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        float mx = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float a = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mx);
+        l[h] *= a;
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 8);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 16);
+#pragma unroll
+        for (int i = 0; i < DI; ++i) {
+          float* x = &o[h][i].x;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float y = m[h] == -INFINITY ? 0.f : x[j] * a;
+            y += __shfl_xor_sync(0xffffffffu, y, 8);
+            y += __shfl_xor_sync(0xffffffffu, y, 16);
+            x[j] = y;
+          }
+          if (grp == 0 && i < di)
+            *reinterpret_cast<float4*>(&s_o[warp][h][(sub + 8 * i) * 4]) = o[h][i];
+        }
+        if (lane == 0) {
+          s_m[warp][h] = mx;
+          s_l[warp][h] = l[h];
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < HP * A.d; i += kScoredWarps * 32) {
+        const int hh = i / A.d, c = i - hh * A.d;
+        if (h0 + hh >= A.G) break;
+        float M = -INFINITY, Ls = 0.f, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < kScoredWarps; ++w) M = fmaxf(M, s_m[w][hh]);
+#pragma unroll
+        for (int w = 0; w < kScoredWarps; ++w) {
+          if (s_l[w][hh] == 0.f) continue;   // nothing seen (a sum that is NaN stays)
+          const float a = exp2f(s_m[w][hh] - M);
+          Ls = fmaf(s_l[w][hh], a, Ls);
+          O = fmaf(s_o[w][hh][c], a, O);
+        }
+        const bool any = Ls != 0.f;
+        float weight, lse = any ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+        if (P.whole) lse = with_sink(A.sink, g * A.G + h0 + hh, lse, weight);
+        put_value(A, P, h0 + hh, c, any ? O / Ls : 0.f, weight);
+        if (c == 0) put_lse(A, P, h0 + hh, lse);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// merge
+// ---------------------------------------------------------------------------
+
+constexpr int kMergeThreads = 256;
+
+// A CTA joins the parts of one unit, in the order of its tiles: the heads' LSE
+// first, then each thread four values of a head, the parts shared out to groups
+// of threads that are summed in their order.  Units that one CTA of the main
+// kernel had whole are done already; units without a tile get zeros here.
+__global__ void __launch_bounds__(kMergeThreads)
+scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
+  __shared__ float s_lse[16], s_weight[16];
+  __shared__ __align__(16) float4 s_acc[kMergeThreads];
+  griddep_launch_dependents();   // the next call's first kernel may start its launch
+  griddep_wait();
+  const int u = blockIdx.x, e = u / A.Hkv, g = u - e * A.Hkv, tid = threadIdx.x;
+  const int64_t bef = A.before[e];
+  const int n = (int)(A.before[e + 1] - bef);
+  const int64_t each = A.before[A.entries() + 1];
+  const int64_t t0 = bef * A.Hkv + (int64_t)g * n;
+  const int64_t i0 = t0 / each;
+  const int parts = n ? (int)((t0 + n - 1) / each - i0) + 1 : 0;
+  if (parts == 1) return;
+  const int64_t slot = i0 + u;
+  const int lane = tid & 31, warp = tid >> 5;
+  for (int hh = warp; hh < A.G; hh += kMergeThreads / 32) {
+    const float* pl = A.part_lse + slot * A.G + hh;
+    float m = -INFINITY, s = 0.f;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, pl[(int64_t)i * A.G]);
+    m = warp_max(m);
+    for (int i = lane; i < parts; i += 32) {
+      const float x = pl[(int64_t)i * A.G];
+      if (x != -INFINITY) s += expf(x - m);
+    }
+    s = warp_sum(s);
+    if (lane == 0) {
+      float weight, lse = s == 0.f ? -INFINITY : m + logf(s);
+      s_lse[hh] = lse;
+      lse = with_sink(A.sink, g * A.G + hh, lse, weight);
+      s_weight[hh] = weight;
+      if (A.out_lse) A.out_lse[(int64_t)e * A.Hq + g * A.G + hh] = lse;
+    }
+  }
+  __syncthreads();
+  const int quads = A.d / 4, cols = A.G * quads;
+  const int groups = max(kMergeThreads / cols, 1);
+  const int grp = min(tid / cols, groups);   // the last threads may have no group
+  for (int c0 = 0; c0 < cols; c0 += kMergeThreads) {
+    const int c = c0 + tid - grp * cols;
+    const bool mine = grp < groups && c < cols;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int hh = mine ? c / quads : 0;
+    if (mine) {
+      const float lse = s_lse[hh];
+      const float* pl = A.part_lse + slot * A.G + hh;
+      const float4* po = reinterpret_cast<const float4*>(A.part_o + slot * A.G * A.d) + c;
+#pragma unroll 4
+      for (int i = grp; i < parts; i += groups) {
+        const float x = pl[(int64_t)i * A.G];
+        const float4 y = po[(int64_t)i * cols];
+        if (x != -INFINITY) {
+          const float w = expf(x - lse);
+          acc.x = fmaf(w, y.x, acc.x);
+          acc.y = fmaf(w, y.y, acc.y);
+          acc.z = fmaf(w, y.z, acc.z);
+          acc.w = fmaf(w, y.w, acc.w);
+        }
+      }
+    }
+    if (groups > 1) {
+      s_acc[tid] = acc;
+      __syncthreads();
+      if (tid < cols)
+        for (int j = 1; j < groups; ++j) {
+          const float4 y = s_acc[tid + j * cols];
+          acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
+        }
+    }
+    if (mine && grp == 0) {
+      const float w = s_weight[hh];
+      const int64_t at = (int64_t)e * A.Hq * quads + (int64_t)g * cols + c;
+      acc = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
+      if (A.out_dtype == DCP_F32)
+        reinterpret_cast<float4*>(A.out)[at] = acc;
+      else
+        reinterpret_cast<uint2*>(A.out)[at] =
+            make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+static int generic_ctas() { return num_sms() * 4; }
+
+template <int kKind, int DI>
+static cudaError_t launch_generic(const ScoredArgs& A, bool q_bf16, cudaStream_t s) {
+  const unsigned grid = (unsigned)A.ctas, block = kScoredWarps * 32;
+  return A.G == 1
+             ? launch_chained(scored_generic_kernel<kKind, DI, 1>, grid, block, 0, s, A, q_bf16)
+             : launch_chained(scored_generic_kernel<kKind, DI, 4>, grid, block, 0, s, A, q_bf16);
+}
+
+template <int kKind>
+static cudaError_t launch_generic(const ScoredArgs& A, bool q_bf16, cudaStream_t s) {
+  if (A.d <= 64) return launch_generic<kKind, 2>(A, q_bf16, s);
+  if (A.d <= 128) return launch_generic<kKind, 4>(A, q_bf16, s);
+  return launch_generic<kKind, 8>(A, q_bf16, s);
+}
+
+static bool shape_ok(const dcp_layout_t& L, int B, int Hq, int Hkv, int d) {
+  return shards_ok(L) && B >= 0 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && Hq / Hkv <= 16 &&
+         d >= 32 && d % 32 == 0 && d <= 256;
+}
+
+static size_t before_bytes(int64_t entries) { return align_up((size_t)(entries + 2) * 8, 256); }
+
+static size_t workspace_bytes_of(int64_t entries, int Hq, int Hkv, int d) {
+  const int G = Hq / Hkv;
+  int most = generic_ctas();
+  for (CacheKind kind : {kCacheBf16, kCacheE4m3}) {
+    const int n = scored_mma_ctas(d, G, kind);
+    if (n > most) most = n;
+  }
+  const size_t rows = (size_t)(most + entries * Hkv) * G;
+  return before_bytes(entries) + align_up(rows * 4, 256) + rows * d * 4;
+}
+
+struct Cache {
+  dcp_rank_ptrs_t k, v, sc;
+  int64_t nb;
+  const int32_t* bt;
+  int32_t max_vb;
+  int64_t bt_stride;
+  CacheKind kind;
+};
+
+static bool aligned16(const dcp_rank_ptrs_t& p, int dcp) {
+  for (int r = 0; r < dcp; ++r)
+    if ((uintptr_t)p.ptr[r] & 15) return false;
+  return true;
+}
+
+static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq, int Hkv, int d,
+                       float scale, dcp_dtype_t dtype, const Cache& kv, const int32_t* seq_lens,
+                       const dcp_scores_t& f, const float* sink, bool apart_, void* out,
+                       dcp_dtype_t out_dtype, float* out_lse, void* ws, size_t ws_bytes,
+                       int32_t* err, cudaStream_t s) {
+  if (!shape_ok(layout, B, Hq, Hkv, d) || (dtype != DCP_F32 && dtype != DCP_BF16) ||
+      (out_dtype != DCP_F32 && out_dtype != DCP_BF16) || kv.nb < 0 || kv.max_vb < 0 ||
+      kv.bt_stride < 0 || !isfinite(scale) || !isfinite(f.cap) || f.cap < 0.f || f.window < 0 ||
+      f.prefix < 0)
+    return DCP_EINVAL;
+  if (B == 0) return DCP_OK;
+  const int dcp = layout.dcp_size;
+  const bool scaled = kv.kind == kCacheE4m3;
+  if (!q || !seq_lens || !out || (apart_ && !out_lse) || !kv.bt || !ranks_ok(kv.k, dcp) ||
+      !ranks_ok(kv.v, dcp) || (scaled && !ranks_ok(kv.sc, dcp)))
+    return DCP_EINVAL;
+  const int64_t entries = apart_ ? (int64_t)B * dcp : B;
+  if (entries * Hkv >= (int64_t(1) << 30) ||
+      (uintptr_t)q % 16 || (uintptr_t)out % 16 || (uintptr_t)ws % 16 || !aligned16(kv.k, dcp) ||
+      !aligned16(kv.v, dcp) || (scaled && !aligned16(kv.sc, dcp)))
+    return DCP_EUNSUPPORTED;
+  const size_t need = workspace_bytes_of(entries, Hq, Hkv, d);
+  if (!ws || ws_bytes < need) return DCP_EWORKSPACE;
+  const int64_t es = dtype == DCP_F32 ? 4 : 2, os = out_dtype == DCP_F32 ? 4 : 2;
+  const Bytes reads[] = {{q, (int64_t)B * Hq * d * es},
+                         {seq_lens, (int64_t)B * 4},
+                         {f.slopes, (int64_t)Hq * 4},
+                         {f.first, (int64_t)B * 4},
+                         {sink, (int64_t)Hq * 4},
+                         {kv.bt, ((kv.bt_stride ? dcp - 1 : 0) * kv.bt_stride +
+                                  (int64_t)B * kv.max_vb) * 4}};
+  const Bytes writes[] = {{out, entries * Hq * d * os},
+                          {out_lse, entries * Hq * 4},
+                          {ws, (int64_t)need},
+                          {err, 4}};
+  const int64_t unit = scaled ? 1 : es, pool = kv.nb * Hkv * layout.block_size * d * unit;
+  for (const Bytes& w : writes) {
+    for (const Bytes& r : reads)
+      if (overlap(w, r)) return DCP_EINVAL;
+    for (const Bytes& x : writes)
+      if (&x != &w && overlap(w, x)) return DCP_EINVAL;
+    for (int r = 0; r < dcp; ++r)
+      if (overlap(w, {kv.k.ptr[r], pool}) || overlap(w, {kv.v.ptr[r], pool}) ||
+          (scaled && overlap(w, {kv.sc.ptr[r], kv.nb * Hkv * 16})))
+        return DCP_EINVAL;
+  }
+  ScoredArgs A;
+  memset((void*)&A, 0, sizeof(A));
+  A.S = Shards(layout);
+  A.B = B, A.Hq = Hq, A.Hkv = Hkv, A.G = Hq / Hkv, A.d = d;
+  A.apart = apart_;
+  A.q = q;
+  A.scale = scale;
+  A.cap = f.cap;
+  A.inv_cap = f.cap > 0.f ? 1.f / f.cap : 0.f;
+  A.window = f.window, A.prefix = f.prefix, A.slopes = f.slopes, A.first = f.first;
+  A.lens = seq_lens;
+  A.sink = sink;
+  A.bt = kv.bt, A.max_vb = kv.max_vb, A.bt_stride = kv.bt_stride, A.nb = kv.nb;
+  A.k = kv.k, A.v = kv.v, A.sc = kv.sc;
+  A.out = out, A.out_dtype = out_dtype, A.out_lse = out_lse, A.err = err;
+  char* w = (char*)ws;
+  A.before = (int64_t*)w;
+  w += before_bytes(entries);
+  const bool mma = scored_mma_ok(A, kv.kind, dtype == DCP_BF16);
+  A.ctas = mma ? scored_mma_ctas(d, A.G, kv.kind) : generic_ctas();
+  A.least = 4 * kScoredWarps;
+  A.part_lse = (float*)w;
+  w += align_up((size_t)(A.ctas + entries * Hkv) * A.G * 4, 256);
+  A.part_o = (float*)w;
+  int rc = DCP_OK;
+  if (mma) {
+    rc = launch_scored_mma(A, kv.kind, s);
+    if (rc) return rc;
+  } else {
+    const bool q16 = dtype == DCP_BF16;
+    const cudaError_t e = kv.kind == kCacheF32    ? launch_generic<kCacheF32>(A, q16, s)
+                          : kv.kind == kCacheBf16 ? launch_generic<kCacheBf16>(A, q16, s)
+                                                  : launch_generic<kCacheE4m3>(A, q16, s);
+    if (e != cudaSuccess) return launch_status_report(e);
+  }
+  const cudaError_t e = launch_chained(scored_merge_kernel, (unsigned)(entries * Hkv),
+                                       kMergeThreads, 0, s, A);
+  if (e != cudaSuccess) return launch_status_report(e);
+  return launch_status();
+}
+
+static Cache cache_of(const dcp_paged_kv_t& kv, dcp_dtype_t dtype) {
+  Cache c = {kv.k, kv.v, {}, kv.num_blocks, kv.block_table, kv.max_vblocks, kv.bt_rank_stride,
+             dtype == DCP_F32 ? kCacheF32 : kCacheBf16};
+  return c;
+}
+
+static Cache cache_of(const dcp_paged_kv8_t& kv) {
+  Cache c = {kv.k, kv.v, kv.scale, kv.num_blocks, kv.block_table, kv.max_vblocks,
+             kv.bt_rank_stride, kCacheE4m3};
+  return c;
+}
+
+}  // namespace dcp
+
+using namespace dcp;
+
+extern "C" {
+
+int dcp_scored_workspace_size(dcp_layout_t layout, int32_t num_reqs, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t per_rank,
+                              size_t* bytes) {
+  if (!bytes || !shape_ok(layout, num_reqs, num_q_heads, num_kv_heads, head_dim))
+    return DCP_EINVAL;
+  *bytes = workspace_bytes_of(per_rank ? (int64_t)num_reqs * layout.dcp_size : num_reqs,
+                              num_q_heads, num_kv_heads, head_dim);
+  return DCP_OK;
+}
+
+int dcp_scored_decode_gqa(dcp_layout_t layout, const void* q, int32_t num_reqs,
+                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                          dcp_dtype_t dtype, dcp_paged_kv_t kv, const int32_t* seq_lens,
+                          dcp_scores_t scores, const float* sink, void* out, dcp_dtype_t out_dtype,
+                          float* out_lse, void* workspace, size_t workspace_bytes,
+                          int32_t* err_count, dcp_stream_t stream) {
+  dcp::NvtxRange nvtx_range("dcp_scored_decode_gqa");
+  return scored_call(layout, q, num_reqs, num_q_heads, num_kv_heads, head_dim, scale, dtype,
+                     cache_of(kv, dtype), seq_lens, scores, sink, false, out, out_dtype, out_lse,
+                     workspace, workspace_bytes, err_count, (cudaStream_t)stream);
+}
+
+int dcp_scored_partial_gqa(dcp_layout_t layout, const void* q, int32_t num_reqs,
+                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                           dcp_dtype_t dtype, dcp_paged_kv_t kv, const int32_t* seq_lens,
+                           dcp_scores_t scores, float* part_o, float* part_lse, void* workspace,
+                           size_t workspace_bytes, int32_t* err_count, dcp_stream_t stream) {
+  dcp::NvtxRange nvtx_range("dcp_scored_partial_gqa");
+  return scored_call(layout, q, num_reqs, num_q_heads, num_kv_heads, head_dim, scale, dtype,
+                     cache_of(kv, dtype), seq_lens, scores, nullptr, true, part_o, DCP_F32,
+                     part_lse, workspace, workspace_bytes, err_count, (cudaStream_t)stream);
+}
+
+int dcp_q8_decode_gqa(dcp_layout_t layout, const void* q, int32_t num_reqs, int32_t num_q_heads,
+                      int32_t num_kv_heads, int32_t head_dim, float scale, dcp_dtype_t dtype,
+                      dcp_paged_kv8_t kv, const int32_t* seq_lens, dcp_scores_t scores,
+                      const float* sink, void* out, dcp_dtype_t out_dtype, float* out_lse,
+                      void* workspace, size_t workspace_bytes, int32_t* err_count,
+                      dcp_stream_t stream) {
+  dcp::NvtxRange nvtx_range("dcp_q8_decode_gqa");
+  return scored_call(layout, q, num_reqs, num_q_heads, num_kv_heads, head_dim, scale, dtype,
+                     cache_of(kv), seq_lens, scores, sink, false, out, out_dtype, out_lse,
+                     workspace, workspace_bytes, err_count, (cudaStream_t)stream);
+}
+
+int dcp_q8_partial_gqa(dcp_layout_t layout, const void* q, int32_t num_reqs, int32_t num_q_heads,
+                       int32_t num_kv_heads, int32_t head_dim, float scale, dcp_dtype_t dtype,
+                       dcp_paged_kv8_t kv, const int32_t* seq_lens, dcp_scores_t scores,
+                       float* part_o, float* part_lse, void* workspace, size_t workspace_bytes,
+                       int32_t* err_count, dcp_stream_t stream) {
+  dcp::NvtxRange nvtx_range("dcp_q8_partial_gqa");
+  return scored_call(layout, q, num_reqs, num_q_heads, num_kv_heads, head_dim, scale, dtype,
+                     cache_of(kv), seq_lens, scores, nullptr, true, part_o, DCP_F32, part_lse,
+                     workspace, workspace_bytes, err_count, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,295 @@
+// Shared by the 8-bit cache (dcp_q8_cache.cu) and scored decode attention
+// (dcp_scored.cu, dcp_scored_mma.cu): the sharded layout without divisions,
+// the tokens that a request sees, how they are cut over the CTAs, and how a
+// score is formed.
+#pragma once
+
+#include "dcp_common.cuh"
+#include "dcp_ptx.cuh"
+
+namespace dcp {
+
+// n / d for 0 <= n < 2^31 by a multiplication (round-up method: with
+// l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1 the quotient is
+// (hi(n m) + n) >> l; the sum fits, as both terms are below 2^31).
+struct FastDiv {
+  uint32_t m, d;
+  int l;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div) {
+    l = 0;
+    while (l < 31 && (1u << l) < div) ++l;
+    m = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << l) - div)) / div + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> l);
+  }
+};
+
+// The interleaved layout: page of `bs` tokens per rank in each virtual block
+// of bs * dcp tokens, runs of I tokens going round the ranks.
+struct Shards {
+  int dcp, bs, I, vbs, turn;
+  FastDiv by_vbs, by_turn, by_I, by_bs;
+  Shards() = default;
+  explicit Shards(const dcp_layout_t& L)
+      : dcp(L.dcp_size), bs(L.block_size), I(L.interleave), vbs(L.block_size * L.dcp_size),
+        turn(L.interleave * L.dcp_size), by_vbs(vbs), by_turn(turn), by_I(I), by_bs(bs) {}
+
+  __device__ __forceinline__ void place(int x, int& rank, int& vb, int& loc) const {
+    vb = by_vbs.div(x);
+    const int off = x - vb * vbs, q = by_turn.div(off), in = off - q * turn;
+    rank = by_I.div(in);
+    loc = q * I + in - rank * I;
+  }
+  // Position of place `loc` of rank's page of virtual block vb.
+  __device__ __forceinline__ int position(int vb, int rank, int loc) const {
+    const int q = by_I.div(loc);
+    return vb * vbs + q * turn + rank * I + loc - q * I;
+  }
+};
+
+// Tokens of [0, x) on each rank: what is the same for all ranks is worked out once.
+struct Below {
+  int base, in;   // whole runs, and what is left of the last turn
+  __device__ __forceinline__ Below(const Shards& S, int x) {
+    const int full = S.by_vbs.div(x), rem = x - full * S.vbs, q = S.by_turn.div(rem);
+    base = full * S.bs + q * S.I;
+    in = rem - q * S.turn;
+  }
+  __device__ __forceinline__ int on(const Shards& S, int r) const {
+    return base + min(max(in - r * S.I, 0), S.I);
+  }
+};
+
+inline bool shards_ok(const dcp_layout_t& L) {
+  return layout_ok(L) && (int64_t)L.block_size * L.dcp_size < (int64_t(1) << 30);
+}
+
+// ---------------------------------------------------------------------------
+// scored decode attention
+// ---------------------------------------------------------------------------
+
+constexpr int kRows = 16;          // tokens of a tile: places [16 t, 16 t + 16) of a rank's tokens
+constexpr int kScoredWarps = 4;    // of a CTA
+
+struct ScoredArgs {
+  Shards S;
+  int B, Hq, Hkv, G, d;
+  int apart;                 // per-rank outputs: an entry is a rank of a request
+  const void* q;             // [B][Hq][d]
+  float scale, cap, inv_cap;
+  int window, prefix;
+  const float* slopes;       // [Hq] or NULL
+  const int32_t* first;      // [B] or NULL
+  const int32_t* lens;       // [B]
+  const float* sink;         // [Hq] or NULL
+  const int32_t* bt;
+  int max_vb;
+  int64_t bt_stride, nb;
+  dcp_rank_ptrs_t k, v, sc;
+  void* out;                 // [entries][Hq][d]
+  int out_dtype;
+  float* out_lse;            // [entries][Hq] or NULL
+  int32_t* err;
+  // workspace
+  int64_t* before;           // [entries + 1] tiles of a head in front of an entry, then tiles per CTA
+  float* part_lse;           // [ctas + units][G]
+  float* part_o;             // [ctas + units][G][d]
+  int ctas, least;           // CTAs, and the fewest tiles one is given
+  __device__ __forceinline__ int entries() const { return apart ? B * S.dcp : B; }
+};
+
+// What a request sees of a rank, as two runs of the rank's tokens (the first,
+// kept tokens of the document, and the window), and their tiles.
+struct RankTokens {
+  int a0, a1, b0, b1;
+  __device__ __forceinline__ int a_tiles() const { return a1 > a0 ? (a1 + 15) / 16 - a0 / 16 : 0; }
+  __device__ __forceinline__ int b_tiles() const { return b1 > b0 ? (b1 + 15) / 16 - b0 / 16 : 0; }
+};
+
+struct Seen {
+  Below lo, p, w, n;
+  bool kept;   // there is a run of kept tokens apart from the window
+  __device__ __forceinline__ Seen(const ScoredArgs& A, int lo_, int p_, int w_, int n_)
+      : lo(A.S, lo_), p(A.S, p_), w(A.S, w_), n(A.S, n_), kept(p_ > lo_) {}
+  __device__ __forceinline__ RankTokens on(const Shards& S, int r) const {
+    RankTokens t;
+    t.b0 = w.on(S, r);
+    t.b1 = n.on(S, r);
+    t.a0 = t.a1 = 0;
+    if (kept) {
+      t.a0 = lo.on(S, r);
+      t.a1 = p.on(S, r);
+    }
+    return t;
+  }
+  __device__ __forceinline__ int tiles(const Shards& S, int r) const {
+    const RankTokens t = on(S, r);
+    return t.a_tiles() + t.b_tiles();
+  }
+};
+
+// Length n of the request, and with lo the document's start: tokens x of
+// [lo, n) with x >= w = max(lo, n - window) or x < p = lo + prefix.  Tokens
+// beyond the block table are not there.  Negative lengths count as 0.
+__device__ __forceinline__ Seen seen_of(const ScoredArgs& A, int b, bool count) {
+  const int len = __ldg(A.lens + b), lo0 = A.first ? __ldg(A.first + b) : 0;
+  const int64_t room = (int64_t)A.max_vb * A.S.vbs;
+  if (count && (len < 0 || len > room)) count_error(A.err);
+  const int there = (int)min((int64_t)max(len, 0), room);
+  const int lo = min(max(lo0, 0), there);
+  int w = A.window > 0 ? max(lo, len - A.window) : lo;   // len >= 0 or there = 0
+  w = min(w, there);
+  const int p = (int)min((int64_t)lo + A.prefix, (int64_t)w);
+  // kept tokens that reach the window are one run with it
+  if (p >= w) return Seen(A, 0, 0, lo, there);
+  return Seen(A, lo, p, w, there);
+}
+
+// Entry e is request e % B, on rank e / B where ranks are apart.
+__device__ __forceinline__ int entry_tiles(const ScoredArgs& A, int e, bool count) {
+  const int b = A.apart ? e % A.B : e;
+  const Seen s = seen_of(A, b, count && e < A.B);
+  if (A.apart) return s.tiles(A.S, e / A.B);
+  int n = 0;
+  for (int r = 0; r < A.S.dcp; ++r) n += s.tiles(A.S, r);
+  return n;
+}
+
+// A unit is a key/value head of an entry, its tiles those of the ranks in
+// order.  All units' tiles, end to end (entry by entry, head by head), are cut
+// into runs of `each` tiles, one run a CTA.  The piece of unit u in run i has
+// its partial result at i + u: along the line of tiles either the unit or the
+// run goes up by one from piece to piece, or both, so no two pieces share one.
+struct Run {
+  int64_t t0, t1;   // this CTA's tiles
+  int64_t start;    // first tile of entry e
+  int e;            // entry of t0
+  int64_t each;
+};
+
+// Every thread of the CTA calls it; all get the same.  The lengths are read by
+// every CTA: a plan of one CTA in front would cost a launch (a call of one
+// request takes some 8 us in all).
+template <int kThreads>
+__device__ __forceinline__ Run plan_run(const ScoredArgs& A) {
+  __shared__ int64_t s_sum[kThreads / 32];
+  __shared__ int64_t s_start, s_total;
+  __shared__ int s_e;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int E = A.entries(), c = (E + kThreads - 1) / kThreads;
+  const int e0 = min(tid * c, E), e1 = min(e0 + c, E);
+  const bool keeps = blockIdx.x == 0;
+  int64_t sum = 0;
+  int n0 = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int n = entry_tiles(A, e, keeps);
+    if (e == e0) n0 = n;
+    sum += n;
+  }
+  int64_t upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) s_sum[warp] = upto;
+  if (tid == 0) s_e = E;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) upto += s_sum[w];
+    total += s_sum[w];
+  }
+  Run run;
+  const int64_t all = total * A.Hkv;
+  run.each = max((int64_t)A.least, (all + A.ctas - 1) / A.ctas);
+  run.t0 = min(run.each * blockIdx.x, all);
+  run.t1 = min(run.t0 + run.each, all);
+  int64_t before = upto - sum;
+  if (keeps) {   // for the merge
+    for (int e = e0, n = n0; e < e1; ++e) {
+      if (e > e0) n = entry_tiles(A, e, false);
+      A.before[e] = before;
+      before += n;
+    }
+    if (tid == 0) {
+      A.before[E] = total;
+      A.before[E + 1] = run.each;
+    }
+    before = upto - sum;
+  }
+  // the thread that has the entry of t0
+  if (run.t0 < all && run.t0 >= before * A.Hkv && run.t0 < upto * A.Hkv) {
+    for (int e = e0, n = n0; e < e1; ++e) {
+      if (e > e0) n = entry_tiles(A, e, false);
+      if (run.t0 < (before + n) * A.Hkv) {
+        s_e = e;
+        s_start = before * A.Hkv;
+        break;
+      }
+      before += n;
+    }
+  }
+  __syncthreads();
+  run.e = s_e;
+  run.start = s_start;
+  return run;
+}
+
+// A scaled score in base 2: capped, and less the distance's share.
+__device__ __forceinline__ float formed(const ScoredArgs& A, float t, float slope, float far) {
+  if (A.cap > 0.f) t = A.cap * tanhf(t * A.inv_cap);
+  if (A.slopes) t -= slope * far;
+  return t * kLog2e;
+}
+
+// Result of head `hh` of unit (e, g): the output itself if the piece is the
+// whole unit (with the sink), else the partial result in `slot`.
+struct PieceOut {
+  bool whole;
+  int64_t slot, row;   // row: e * Hq + g * G
+};
+
+__device__ __forceinline__ void put_value(const ScoredArgs& A, const PieceOut& P, int hh, int col,
+                                          float o, float weight) {
+  if (P.whole) {
+    const int64_t at = (P.row + hh) * A.d + col;
+    o *= weight;
+    if (A.out_dtype == DCP_F32)
+      ((float*)A.out)[at] = o;
+    else
+      ((__nv_bfloat16*)A.out)[at] = __float2bfloat16(o);
+  } else {
+    A.part_o[(P.slot * A.G + hh) * A.d + col] = o;
+  }
+}
+
+// Natural LSE with the sink's, and the weight that the values keep beside it.
+__device__ __forceinline__ float with_sink(const float* sink, int h, float lse, float& weight) {
+  weight = 1.f;
+  if (!sink) return lse;
+  const float s = __ldg(sink + h), m = fmaxf(s, lse);
+  if (m == -INFINITY) return lse;
+  const float all = m + logf(expf(s - m) + expf(lse - m));
+  weight = lse == -INFINITY ? 0.f : expf(lse - all);
+  return all;
+}
+
+__device__ __forceinline__ void put_lse(const ScoredArgs& A, const PieceOut& P, int hh, float lse) {
+  if (!P.whole)
+    A.part_lse[P.slot * A.G + hh] = lse;
+  else if (A.out_lse)
+    A.out_lse[P.row + hh] = lse;
+}
+
+// Which kernel a cache takes: the tensor-core kernel (dcp_scored_mma.cu) or
+// the one for any type and shape (dcp_scored.cu).
+enum CacheKind { kCacheF32, kCacheBf16, kCacheE4m3 };
+bool scored_mma_ok(const ScoredArgs& A, CacheKind kind, bool q_bf16);
+int scored_mma_ctas(int d, int G, CacheKind kind);
+int launch_scored_mma(const ScoredArgs& A, CacheKind kind, cudaStream_t s);
+
+}  // namespace dcp

@@ -698,6 +698,153 @@ int dcp_cache_compact(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* 
                       int32_t max_path, int32_t* new_lens, int32_t* err_count,
                       dcp_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The cache in 8 bits, and scored decode attention.
+ * ---------------------------------------------------------------------------
+ * The pages name neither; a serving loop takes them in place of
+ * dcp_cache_write_gqa and dcp_decode_gqa.
+ */
+
+/*
+ * A paged, sequence-sharded KV cache in 8 bits, as dcp_paged_kv_t otherwise.
+ *  k, v        per-rank pools [num_blocks][num_kv_heads][block_size][head_dim]
+ *              of e4m3 numbers.
+ *  scale       per rank [num_blocks][num_kv_heads][4] float32: of a page and
+ *              head the scale of its keys, that of its values, and two that
+ *              nothing reads or writes (16 bytes, so that scales are copied like
+ *              pages).  A number c stands for c * scale.  dcp_q8_append_gqa
+ *              makes powers of two; any positive finite scale is read.
+ * Pools and scales are 16-byte aligned; head_dim is a multiple of 32 up to 256.
+ */
+typedef struct {
+  dcp_rank_ptrs_t k;
+  dcp_rank_ptrs_t v;
+  dcp_rank_ptrs_t scale;
+  int64_t num_blocks;
+  const int32_t* block_table;
+  int32_t max_vblocks;
+  int64_t bt_rank_stride;
+} dcp_paged_kv8_t;
+
+/*
+ * dcp_q8_append_gqa -- quantise the keys and values of new tokens on their way
+ * into the cache.  Token j of request b goes to position ctx_lens[b] + j
+ * (dcp_slot_mapping's rank and slot).
+ *  k, v       [num_tokens][num_kv_heads][head_dim] of dtype; *_stride elements
+ *             between tokens (slices of one projection), heads in one piece.
+ *  q_start    [num_reqs + 1] int32, not decreasing, within [0, num_tokens]:
+ *             request b has rows [q_start[b], q_start[b+1]).
+ *  ctx_lens   [num_reqs] int32 tokens that the cache has already.
+ * Of a page and head, and of its keys and values apart, let A be the largest
+ * finite |x| that the call writes there, and need = 2^ceil(log2(A / 448)), at
+ * least 2^-60.  A page whose first place is written begins anew, with scale
+ * need; any other keeps the larger of its scale and need (a scale that is not
+ * positive and finite counts as none), and if that is larger than before, its
+ * other places c become the e4m3 number nearest to c * before / after.  x is
+ * held as the e4m3 number nearest to x / scale, ties to even; infinities as
+ * +-448, NaN as NaN.
+ * A request with a negative length, rows outside [0, num_tokens] or tokens
+ * beyond max_vblocks bumps err_count and is not written; a page whose table
+ * entry is outside [0, num_blocks) is skipped and counted.  Requests that write
+ * to one page at the same time leave it undefined (a fork's open page is its
+ * own).  k, v and their strides are multiples of 16 bytes and 16-byte aligned,
+ * and lie apart from the cache.
+ */
+int dcp_q8_append_gqa(dcp_layout_t layout, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, int32_t num_tokens, const int32_t* q_start,
+                      const int32_t* ctx_lens, int32_t num_reqs, int32_t num_kv_heads,
+                      int32_t head_dim, dcp_dtype_t dtype, dcp_paged_kv8_t kv, int32_t* err_count,
+                      dcp_stream_t stream);
+
+/*
+ * dcp_q8_gather_gqa -- read tokens back out of the 8-bit cache in the order
+ * given (dcp_gather_context_mla's rules), as c * scale rounded to dtype.
+ *  k_out, v_out [num_tokens][num_kv_heads][head_dim] of dtype, 16-byte aligned.
+ */
+int dcp_q8_gather_gqa(dcp_layout_t layout, dcp_paged_kv8_t kv, int32_t num_reqs,
+                      int32_t num_kv_heads, int32_t head_dim, const int32_t* req_idx,
+                      const int64_t* positions, int64_t num_tokens, void* k_out, void* v_out,
+                      dcp_dtype_t dtype, int32_t* err_count, dcp_stream_t stream);
+
+/*
+ * How a score is formed and which tokens are seen.  With n = seq_lens[b], the
+ * query at position n - 1 and a key at position x:
+ *     t = scale * q.k;   cap > 0: t = cap * tanh(t / cap);
+ *     slopes: t = t - slopes[h] * (n - 1 - x).
+ * Tokens of [first[b], n) are seen (first NULL: 0) that are among the last
+ * `window` of the request (0: all) or the first `prefix` from first[b] on.
+ * All zero and NULL: plain attention.
+ */
+typedef struct {
+  float cap;
+  int32_t window;
+  int32_t prefix;
+  const float* slopes;   /* [num_q_heads] float32 or NULL */
+  const int32_t* first;  /* [num_reqs] int32 or NULL; below 0 counts as 0 */
+} dcp_scores_t;
+
+/*
+ * dcp_scored_decode_gqa -- dcp_decode_gqa with scores formed as above, from the
+ * lengths themselves; only the pages of seen tokens are read.
+ *  seq_lens  [num_reqs] int32, the decode token counted.  A negative length
+ *            counts as 0, tokens beyond max_vblocks are not there; both bump
+ *            err_count.
+ *  out       [num_reqs][num_q_heads][head_dim] of out_dtype, out_lse
+ *            [num_reqs][num_q_heads] float32 or NULL.  A request that sees
+ *            nothing gives o = 0 and lse = -inf (with a sink the sink's logit).
+ * Keys and values of tokens that are not seen do not count, whatever they hold.
+ * Pages whose table entry is outside [0, num_blocks) are skipped and counted,
+ * once or more.
+ * Supported as dcp_decode_gqa; cap >= 0, window >= 0, prefix >= 0; q, out, the
+ * workspace and the pools 16-byte aligned.  out, out_lse and the workspace lie
+ * apart from one another and from what is read, and no other call may use the
+ * workspace at the same time (two captured graphs that share one may not
+ * overlap).  Results do not depend on timing.
+ */
+int dcp_scored_decode_gqa(dcp_layout_t layout, const void* q, int32_t num_reqs,
+                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                          dcp_dtype_t dtype, dcp_paged_kv_t kv, const int32_t* seq_lens,
+                          dcp_scores_t scores, const float* sink, void* out, dcp_dtype_t out_dtype,
+                          float* out_lse, void* workspace, size_t workspace_bytes,
+                          int32_t* err_count, dcp_stream_t stream);
+
+/*
+ * dcp_scored_partial_gqa -- the same per rank, without the sink: what each rank
+ * hands to dcp_lse_merge.
+ *  part_o [dcp_size][num_reqs][num_q_heads][head_dim] float32, part_lse
+ *         [dcp_size][num_reqs][num_q_heads] float32.
+ */
+int dcp_scored_partial_gqa(dcp_layout_t layout, const void* q, int32_t num_reqs,
+                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                           dcp_dtype_t dtype, dcp_paged_kv_t kv, const int32_t* seq_lens,
+                           dcp_scores_t scores, float* part_o, float* part_lse, void* workspace,
+                           size_t workspace_bytes, int32_t* err_count, dcp_stream_t stream);
+
+/*
+ * dcp_q8_decode_gqa, dcp_q8_partial_gqa -- the same over the 8-bit cache; dtype
+ * is that of q.
+ */
+int dcp_q8_decode_gqa(dcp_layout_t layout, const void* q, int32_t num_reqs, int32_t num_q_heads,
+                      int32_t num_kv_heads, int32_t head_dim, float scale, dcp_dtype_t dtype,
+                      dcp_paged_kv8_t kv, const int32_t* seq_lens, dcp_scores_t scores,
+                      const float* sink, void* out, dcp_dtype_t out_dtype, float* out_lse,
+                      void* workspace, size_t workspace_bytes, int32_t* err_count,
+                      dcp_stream_t stream);
+int dcp_q8_partial_gqa(dcp_layout_t layout, const void* q, int32_t num_reqs, int32_t num_q_heads,
+                       int32_t num_kv_heads, int32_t head_dim, float scale, dcp_dtype_t dtype,
+                       dcp_paged_kv8_t kv, const int32_t* seq_lens, dcp_scores_t scores,
+                       float* part_o, float* part_lse, void* workspace, size_t workspace_bytes,
+                       int32_t* err_count, dcp_stream_t stream);
+
+/*
+ * Bytes of workspace of the four calls (for any lengths and scores); per_rank
+ * != 0 for the partial ones.
+ */
+int dcp_scored_workspace_size(dcp_layout_t layout, int32_t num_reqs, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t per_rank,
+                              size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif
