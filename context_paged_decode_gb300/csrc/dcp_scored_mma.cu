@@ -1,6 +1,567 @@
+// Scored decode attention on the tensor cores, over bf16 and e4m3 caches.
+//
+// A unit has up to 16 query heads and any number of tokens, so a product's
+// 16-row side is the tokens and its 8-column side the heads (mma.sync
+// m16n8k16; one or two column tiles of heads):
+//     S^T [16 tokens x 8 heads] = K Q^T,   O^T [16 dims x 8 heads] += V^T P^T.
+// With tcgen05 the heads would fill a fraction of its smallest tile, and e4m3
+// operands would need the other one in 8 bits too.  The calls are bound by the
+// bytes of the cache; what has to stay below that is the instructions a byte.
+//
+// e4m3 numbers become fp16, which holds them exactly.  The query is fp16 too,
+// scaled by a power of two for each head so that its largest entry is near 2^14:
+// bf16's eight bits fit, and only entries below 2^-38 of the largest lose any.
+// The page's scale of the keys goes to the score, that of the values to the
+// weight (below).  Products accumulate in fp32; scores, their maxima and sums
+// are fp32.
+#include <string.h>
+
+#include "dcp_q8.cuh"
 #include "dcp_scored.cuh"
+
 namespace dcp {
-bool scored_mma_ok(const ScoredArgs&, CacheKind, bool) { return false; }
-int scored_mma_ctas(int, int, CacheKind) { return 0; }
-int launch_scored_mma(const ScoredArgs&, CacheKind, cudaStream_t) { return DCP_EUNSUPPORTED; }
+
+struct ScoredMaps {
+  CUtensorMap k[DCP_MAX_RANKS], v[DCP_MAX_RANKS];
+};
+
+__device__ __forceinline__ void mma_f16_16816(float* c, const uint32_t* a, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 tile of 16-bit numbers, transposed across the warp.
+__device__ __forceinline__ uint32_t transposed8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <bool E8>
+__device__ __forceinline__ void mma_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (E8)
+    mma_f16_16816(c, a, b0, b1);
+  else
+    mma_bf16_16816(c, a, b0, b1);
+}
+
+// Sizes of a variant: D dims, e4m3 or bf16, NT tiles of eight heads.
+template <int D, bool E8, int NT>
+struct Shape {
+  static constexpr int kRowBytes = D * (E8 ? 1 : 2);
+  static constexpr int kTileBytes = kRows * kRowBytes;       // of keys, and of values
+  static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;
+  static constexpr int kBoxes = kRowBytes / kBoxBytes;
+  // 16 KB a warp on their way
+  static constexpr int kStages = 16384 / (2 * kTileBytes);
+  static constexpr int kPerSm = NT == 1 ? 3 : 2;
+  static constexpr int kRing = kScoredWarps * kStages * 2 * kTileBytes;
+  static constexpr int kMeta = kScoredWarps * kStages * (16 + 16 + 8);
+  static __host__ __device__ constexpr int smem(int G) {
+    return 1024 + kRing + kMeta + kScoredWarps * G * (D + 4) * 4;
+  }
+  // Byte of 16-byte chunk c of a row, as the copies' swizzle lays it.
+  static __device__ __forceinline__ uint32_t at(int row, int c) {
+    if (kBoxBytes == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+    return (c >> 3) * (kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+  }
+};
+
+constexpr float kSlack = 4.f;    // how far a score may pass its reference, in powers of two
+constexpr float kLift = 10.f;    // fp16 weights are held times 2^10: up to 2^15 with the slack and a
+                                 // scale's fraction, and in full precision down to 2^-24
+constexpr int kScoredStuck = 1 << 20;   // err_count increment for a wait that timed out
+
+// Four warps a CTA, each with a ring of its own for every fourth tile of the
+// CTA's run, filled ahead by TMA over the ends of pieces; a tile's block-table
+// entries are looked up 32 tiles at a time, a tile a lane.  A score is compared
+// with its head's reference only to see whether it passes it by more than 2^4;
+// while none does (one vote), nothing is rescaled and no maximum is shared.
+template <int D, bool E8, int NT>
+__global__ void __launch_bounds__(kScoredWarps * 32, Shape<D, E8, NT>::kPerSm)
+scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ ScoredMaps maps) {
+  using Z = Shape<D, E8, NT>;
+  constexpr int ST = Z::kStages, TB = Z::kTileBytes, KS = D / 16;
+  griddep_launch_dependents();   // the merge may start its launch
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gq = lane >> 2, tq = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * ST * 2 * TB;
+  float* const s_scale = reinterpret_cast<float*>(smem + Z::kRing) + warp * ST * 4;
+  int4* const s_desc = reinterpret_cast<int4*>(smem + Z::kRing + kScoredWarps * ST * 16) + warp * ST;
+  uint64_t* const bars =
+      reinterpret_cast<uint64_t*>(smem + Z::kRing + kScoredWarps * ST * 32) + warp * ST;
+  float* const s_ml = reinterpret_cast<float*>(smem + Z::kRing + Z::kMeta);   // [warps][G][4]
+  float* const s_o = s_ml + kScoredWarps * A.G * 4;                          // [warps][G][D]
+  const uint32_t bar0 = smem_u32(bars);
+  if (lane == 0) {
+    for (int s = 0; s < ST; ++s) mbar_init(bar0 + 8 * s, 1);
+    fence_mbar_init();
+  }
+  if (tid < A.S.dcp) {
+    prefetch_tmap(&maps.k[tid]);
+    prefetch_tmap(&maps.v[tid]);
+  }
+  __syncthreads();
+  griddep_wait();                // launched chained: the preceding kernel completed
+  const Run run = plan_run<kScoredWarps * 32>(A);
+  const uint64_t pol = policy_evict_first();
+  const int mine = run.t1 > run.t0 + warp
+                       ? (int)((run.t1 - run.t0 - warp + kScoredWarps - 1) / kScoredWarps)
+                       : 0;
+
+  // --- tiles on their way: this lane's of the 32 looked up ---
+  int we = run.e, wn = 0;
+  int64_t wstart = run.start;
+  if (mine > 0) wn = entry_tiles(A, we, false);
+  int d_row = -1, d_ph = 0, d_info = 0, d_p0 = 0;
+  auto look_up = [&](int j0) {
+    const int64_t t = run.t0 + warp + (int64_t)(j0 + lane) * kScoredWarps;
+    if (t < run.t1) {
+      while (t >= wstart + (int64_t)wn * A.Hkv) {
+        wstart += (int64_t)wn * A.Hkv;
+        wn = entry_tiles(A, ++we, false);
+      }
+      const int g = (int)((t - wstart) / wn);
+      int left = (int)(t - wstart - (int64_t)g * wn);
+      const int b = A.apart ? we % A.B : we, r0 = A.apart ? we / A.B : 0;
+      const Seen seen = seen_of(A, b, false);
+      int r = r0, lo = 0, hi = 0;
+      for (; r < A.S.dcp; ++r) {   // the tile is there: a rank is found
+        const RankTokens T = seen.on(A.S, r);
+        const int na = T.a_tiles(), nb = T.b_tiles();
+        if (left < na) {
+          d_p0 = (T.a0 / kRows + left) * kRows, lo = T.a0, hi = T.a1;
+          break;
+        }
+        left -= na;
+        if (left < nb) {
+          d_p0 = (T.b0 / kRows + left) * kRows, lo = T.b0, hi = T.b1;
+          break;
+        }
+        left -= nb;
+      }
+      const int vb = A.S.by_bs.div(d_p0);
+      const int64_t page =
+          vb < A.max_vb ? (int64_t)__ldg(A.bt + r * A.bt_stride + (int64_t)b * A.max_vb + vb) : -1;
+      d_info = max(lo - d_p0, 0) | min(hi - d_p0, kRows) << 8 | r << 16;
+      d_row = -1;
+      if (page >= 0 && page < A.nb) {
+        d_ph = (int)(page * A.Hkv + g);
+        d_row = d_ph * A.S.bs + (d_p0 - vb * A.S.bs);
+      }
+    }
+    we = __shfl_sync(0xffffffffu, we, 31);
+    wn = __shfl_sync(0xffffffffu, wn, 31);
+    wstart = __shfl_sync(0xffffffffu, wstart, 31);
+  };
+  bool dead = false;   // a wait timed out: stop waiting and issuing
+  auto issue = [&](int j) {   // the whole warp, for its j-th tile
+    if ((j & 31) == 0) look_up(j);
+    const int row = __shfl_sync(0xffffffffu, d_row, j & 31);
+    const int ph = __shfl_sync(0xffffffffu, d_ph, j & 31);
+    const int info = __shfl_sync(0xffffffffu, d_info, j & 31);
+    const int p0 = __shfl_sync(0xffffffffu, d_p0, j & 31);
+    if (lane == 0 && !dead) {
+      const int st = j % ST, r = info >> 16;
+      const uint32_t bar = bar0 + 8 * st, dst = ring + st * 2 * TB;
+      s_desc[st] = make_int4(row, info, p0, 0);
+      if (row >= 0) {
+        mbar_arrive_expect_tx(bar, 2 * TB + (E8 ? 16 : 0));
+#pragma unroll
+        for (int x = 0; x < Z::kBoxes; ++x) {
+          tma_load_2d_hint(dst + x * kRows * 128, &maps.k[r], x * 128, row, bar, pol);
+          tma_load_2d_hint(dst + TB + x * kRows * 128, &maps.v[r], x * 128, row, bar, pol);
+        }
+        if (E8)
+          bulk_load(smem_u32(s_scale + st * 4), (const char*)A.sc.ptr[r] + (int64_t)ph * 16, 16,
+                    bar);
+      } else {
+        count_error(A.err);
+        mbar_arrive(bar);
+      }
+    }
+  };
+  for (int j = 0; j < ST && j < mine; ++j) issue(j);
+
+  // --- pieces ---
+  int64_t start = run.start;
+  int e = run.e, n = 0, seq = 0;
+  bool fresh = true;
+  for (int64_t t = run.t0; t < run.t1;) {
+    if (fresh) {
+      n = entry_tiles(A, e, false);
+      fresh = false;
+    }
+    if (t >= start + (int64_t)n * A.Hkv) {
+      start += (int64_t)n * A.Hkv;
+      ++e;
+      fresh = true;
+      continue;
+    }
+    const int g = (int)((t - start) / n), k0 = (int)(t - start - (int64_t)g * n);
+    const int k1 = (int)min((int64_t)n, k0 + (run.t1 - t));
+    t += k1 - k0;
+    // this warp's tiles of the run that end before t
+    const int upto = t > run.t0 + warp
+                         ? (int)((t - run.t0 - warp + kScoredWarps - 1) / kScoredWarps)
+                         : 0;
+    const int b = A.apart ? e % A.B : e;
+    const int last = __ldg(A.lens + b) - 1;
+
+    // queries as the B operand: head gq (+ 8), and of heads 2 tq, 2 tq + 1 (+ 8) what a
+    // product is to be multiplied by
+    uint32_t qb[NT][KS][2];
+    float mul[NT][2], slope[NT][2];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+      const bool there = gq + 8 * x < A.G;
+      const __nv_bfloat16* qh =
+          (const __nv_bfloat16*)A.q + ((int64_t)b * A.Hq + g * A.G + gq + 8 * x) * D;
+      float up = 1.f;
+      if (E8) {
+        // the fragments' order of a row of keys: bytes 4 tq .. 4 tq + 3 of each 16
+        uint2 w[KS];
+        float top = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          w[ks] = there ? __ldg(reinterpret_cast<const uint2*>(qh + ks * 16 + tq * 4))
+                        : make_uint2(0u, 0u);
+          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(w[ks].x)), fabsf(bf16_hi(w[ks].x))),
+                                 fmaxf(fabsf(bf16_lo(w[ks].y)), fabsf(bf16_hi(w[ks].y)))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^(14 - exponent of the largest); without a finite one, or with none, 1
+        const int ex = (__float_as_int(top) >> 23) - 127;
+        if (top > 0.f && ex < 128) up = __int_as_float((min(14 - ex, 126) + 127) << 23);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          qb[x][ks][0] = pack_f16(bf16_lo(w[ks].x) * up, bf16_hi(w[ks].x) * up);
+          qb[x][ks][1] = pack_f16(bf16_lo(w[ks].y) * up, bf16_hi(w[ks].y) * up);
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qb[x][ks][i] =
+                there ? __ldg(reinterpret_cast<const uint32_t*>(qh + ks * 16 + i * 8 + tq * 2)) : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int h = 2 * tq + i + 8 * x;
+        mul[x][i] = A.scale;
+        if (E8) mul[x][i] /= __shfl_sync(0xffffffffu, up, (2 * tq + i) * 4);
+        slope[x][i] = A.slopes && h < A.G ? __ldg(A.slopes + g * A.G + h) : 0.f;
+      }
+    }
+    // references: of the scores (ref) and, in 8 bits, of scores and scales together
+    // (vref); thr and vthr are what may not be passed
+    float o[NT][KS][4], l[NT][2], ref[NT][2], thr[NT][2], vref[NT][2], vthr[NT][2];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+#pragma unroll
+      for (int i = 0; i < KS; ++i) o[x][i][0] = o[x][i][1] = o[x][i][2] = o[x][i][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[x][i] = ref[x][i] = vref[x][i] = 0.f;
+        thr[x][i] = vthr[x][i] = -INFINITY;
+      }
+    }
+
+    for (; seq < upto; ++seq) {
+      const int st = seq % ST;
+      if (!dead && !mbar_wait(bar0 + 8 * st, (seq / ST) & 1)) {
+        dead = true;
+        if (lane == 0 && A.err) atomicAdd(A.err, kScoredStuck);
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      const int4 desc = s_desc[st];
+      if (!dead && desc.x >= 0) {
+        const uint32_t kb = ring + st * 2 * TB, vb = kb + TB;
+        const int lo = desc.y & 255, hi = (desc.y >> 8) & 255;
+        float ks_ = 1.f, vmant = 1.f, vexp = 0.f;
+        if (E8) {
+          const float2 s2 = *reinterpret_cast<const float2*>(s_scale + st * 4);
+          ks_ = s2.x;
+          // the values' scale as a fraction of [1, 2) and a power of two
+          const int bits = __float_as_int(s2.y);
+          vmant = __int_as_float((bits & 0x7fffff) | 0x3f800000);
+          vexp = (float)((bits >> 23) - 127);
+        }
+        if (lo > 0 || hi < kRows) {   // values that do not count are zeros, so 0 * NaN is not met
+          for (int i = lane; i < kRows * (Z::kRowBytes / 16); i += 32) {
+            const int row = i / (Z::kRowBytes / 16), c = i % (Z::kRowBytes / 16);
+            if (row < lo || row >= hi)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vb + Z::at(row, c)), "r"(0u)
+                           : "memory");
+          }
+          __syncwarp();
+        }
+        // S^T = K Q^T
+        float s[NT][4];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+        const int mi = lane >> 3;
+        {
+          const int krow = (mi & 1) * 8 + (lane & 7);
+          if (E8) {
+#pragma unroll
+            for (int i = 0; i < KS / 2; ++i) {
+              uint32_t r[4];
+              ldsm_x4(kb + Z::at(krow, 2 * i + (mi >> 1)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t a[4] = {
+                    e4m3x2_f16(r[2 * c] & 0xffffu), e4m3x2_f16(r[2 * c + 1] & 0xffffu),
+                    e4m3x2_f16(r[2 * c] >> 16), e4m3x2_f16(r[2 * c + 1] >> 16)};
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+                  mma_16816<E8>(s[x], a, qb[x][2 * i + c][0], qb[x][2 * i + c][1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              uint32_t a[4];
+              ldsm_x4(kb + Z::at(krow, 2 * i + (mi >> 1)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+              for (int x = 0; x < NT; ++x) mma_16816<E8>(s[x], a, qb[x][i][0], qb[x][i][1]);
+            }
+          }
+        }
+        // scores in base 2, of tokens gq (two heads) and gq + 8
+        const bool in0 = gq >= lo && gq < hi, in1 = gq + 8 >= lo && gq + 8 < hi;
+        float far0 = 0.f, far1 = 0.f;
+        if (A.slopes) {
+          const int r = desc.y >> 16, p = desc.z + gq, page = A.S.by_bs.div(p);
+          far0 = (float)(last - A.S.position(page, r, p - page * A.S.bs));
+          far1 = (float)(last - A.S.position(page, r, p + 8 - page * A.S.bs));
+        }
+        bool over = false;
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int h = i & 1;
+            const float v = formed(A, s[x][i] * (mul[x][h] * ks_), slope[x][h], i < 2 ? far0 : far1);
+            s[x][i] = (i < 2 ? in0 : in1) ? v : -INFINITY;
+            over |= s[x][i] > thr[x][h];
+            if (E8) over |= s[x][i] + vexp > vthr[x][h];
+          }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float m = fmaxf(s[x][h], s[x][h + 2]);
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+              float down = 1.f;
+              if (m > thr[x][h]) {   // never for a tile that sees nothing
+                down = thr[x][h] == -INFINITY ? 0.f : ex2_ftz(ref[x][h] - m);
+                l[x][h] *= down;
+                ref[x][h] = m;
+                thr[x][h] = m + kSlack;
+              }
+              if (E8) {
+                down = 1.f;
+                const float mv = m + vexp;
+                if (mv > vthr[x][h]) {
+                  down = vthr[x][h] == -INFINITY ? 0.f : ex2_ftz(vref[x][h] - mv);
+                  vref[x][h] = mv;
+                  vthr[x][h] = mv + kSlack;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < KS; ++i) {
+                o[x][i][h] *= down;
+                o[x][i][h + 2] *= down;
+              }
+            }
+        }
+        // weights, and as the B operand of P V
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int h = i & 1;
+            p[i] = ex2_ftz(s[x][i] - ref[x][h]);
+            l[x][h] += p[i];
+            if (E8) p[i] = ex2_ftz(s[x][i] + (vexp + kLift) - vref[x][h]) * vmant;
+          }
+          pb[x][0] = transposed8(E8 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
+          pb[x][1] = transposed8(E8 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
+        }
+        // O^T += V^T P^T.  In 8 bits row j of a tile of 16 dims is dim 2 j, row 8 + j dim 2 j + 1.
+        if (E8) {
+          const int vrow = (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+          for (int i = 0; i < KS / 2; ++i) {
+            uint32_t r[4];
+            ldsm_x4_t(vb + Z::at(vrow, 2 * i + (mi >> 1)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // bytes (token, dim) 00 01 10 11 -> 00 10 01 11
+              const uint32_t u = __byte_perm(r[2 * c], 0, 0x3120);
+              const uint32_t w = __byte_perm(r[2 * c + 1], 0, 0x3120);
+              const uint32_t a[4] = {e4m3x2_f16(u & 0xffffu), e4m3x2_f16(u >> 16),
+                                     e4m3x2_f16(w & 0xffffu), e4m3x2_f16(w >> 16)};
+#pragma unroll
+              for (int x = 0; x < NT; ++x) mma_16816<E8>(o[x][2 * i + c], a, pb[x][0], pb[x][1]);
+            }
+          }
+        } else {
+          const int vrow = (mi >> 1) * 8 + (lane & 7);
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            uint32_t a[4];
+            ldsm_x4_t(vb + Z::at(vrow, 2 * i + (mi & 1)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) mma_16816<E8>(o[x][i], a, pb[x][0], pb[x][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (seq + ST < mine) {
+        if (lane == 0) fence_proxy_async_smem();
+        issue(seq + ST);
+      }
+    }
+
+    // --- the piece's result: the warps' sums against a common reference ---
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float sum = l[x][h];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int hh = 2 * tq + h + 8 * x;
+        if (hh >= A.G) continue;
+        if (gq == 0) {
+          const bool any = thr[x][h] != -INFINITY;
+          float* ml = s_ml + (warp * A.G + hh) * 4;
+          ml[0] = any ? ref[x][h] : -INFINITY;
+          ml[1] = sum;
+          ml[2] = !any ? -INFINITY : E8 ? vref[x][h] - kLift : ref[x][h];
+        }
+        float* os = s_o + (warp * A.G + hh) * D;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          os[i * 16 + (E8 ? 2 * gq : gq)] = o[x][i][h];
+          os[i * 16 + (E8 ? 2 * gq + 1 : gq + 8)] = o[x][i][h + 2];
+        }
+      }
+    __syncthreads();
+    PieceOut P;
+    P.whole = k0 == 0 && k1 == n;
+    P.slot = blockIdx.x + (int64_t)e * A.Hkv + g;
+    P.row = (int64_t)e * A.Hq + g * A.G;
+    for (int i = tid; i < A.G * D; i += kScoredWarps * 32) {
+      const int hh = i / D, c = i % D;
+      float M = -INFINITY, V = -INFINITY, Ls = 0.f, O = 0.f;
+#pragma unroll
+      for (int w = 0; w < kScoredWarps; ++w) {
+        M = fmaxf(M, s_ml[(w * A.G + hh) * 4]);
+        V = fmaxf(V, s_ml[(w * A.G + hh) * 4 + 2]);
+      }
+#pragma unroll
+      for (int w = 0; w < kScoredWarps; ++w) {
+        const float* ml = s_ml + (w * A.G + hh) * 4;
+        if (ml[1] == 0.f) continue;   // nothing seen (a sum that is NaN stays)
+        Ls = fmaf(ml[1], ex2_ftz(ml[0] - M), Ls);
+        O = fmaf(s_o[(w * A.G + hh) * D + c], ex2_ftz(ml[2] - V), O);
+      }
+      const bool any = Ls != 0.f;
+      float weight, lse = any ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+      if (P.whole) lse = with_sink(A.sink, g * A.G + hh, lse, weight);
+      put_value(A, P, hh, c, any ? O / Ls * exp2f(V - M) : 0.f, weight);
+      if (c == 0) put_lse(A, P, hh, lse);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+// bf16 queries, heads of 64 or 128, pages of whole tiles, and rows that a
+// tensor map's coordinate can name; anything else runs on the CUDA cores.
+bool scored_mma_ok(const ScoredArgs& A, CacheKind kind, bool q_bf16) {
+  return kind != kCacheF32 && q_bf16 && (A.d == 64 || A.d == 128) && A.S.bs % kRows == 0 &&
+         A.nb * A.Hkv * A.S.bs < (int64_t(1) << 31) && tensor_map_encoder() != nullptr;
+}
+
+// Bytes of rows of `row` bytes, in boxes of 16 rows of up to 128 bytes.
+static bool encode_rows(CUtensorMap* map, const void* base, uint64_t row, uint64_t rows) {
+  cuuint64_t dims[2] = {row, rows > 0 ? rows : 1};
+  cuuint64_t strides[1] = {row};
+  cuuint32_t box[2] = {(cuuint32_t)(row < 128 ? row : 128), kRows};
+  cuuint32_t estr[2] = {1, 1};
+  return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool E8, int NT>
+static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
+  using Z = Shape<D, E8, NT>;
+  if (!allow_smem<scored_mma_kernel<D, E8, NT>>()) return DCP_ECUDA;
+  ScoredMaps maps;
+  memset((void*)&maps, 0, sizeof(maps));
+  const uint64_t rows = (uint64_t)A.nb * A.Hkv * A.S.bs;
+  for (int r = 0; r < A.S.dcp; ++r)
+    if (!encode_rows(&maps.k[r], A.k.ptr[r], Z::kRowBytes, rows) ||
+        !encode_rows(&maps.v[r], A.v.ptr[r], Z::kRowBytes, rows))
+      return DCP_ECUDA;
+  const cudaError_t e = launch_chained(scored_mma_kernel<D, E8, NT>, (unsigned)A.ctas,
+                                       kScoredWarps * 32, Z::smem(A.G), s, A, maps);
+  return e == cudaSuccess ? launch_status() : launch_status_report(e);
+}
+
+template <int D, bool E8>
+static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
+  return A.G <= 8 ? launch_mma<D, E8, 1>(A, s) : launch_mma<D, E8, 2>(A, s);
+}
+
+int launch_scored_mma(const ScoredArgs& A, CacheKind kind, cudaStream_t s) {
+  if (A.d == 64) return kind == kCacheE4m3 ? launch_mma<64, true>(A, s) : launch_mma<64, false>(A, s);
+  return kind == kCacheE4m3 ? launch_mma<128, true>(A, s) : launch_mma<128, false>(A, s);
+}
+
+template <int D, bool E8, int NT>
+static int one_wave(int G) {
+  using Z = Shape<D, E8, NT>;
+  const int fit = 228 * 1024 / (Z::smem(G) + 2048);
+  return num_sms() * (fit < Z::kPerSm ? fit : Z::kPerSm);
+}
+
+int scored_mma_ctas(int d, int G, CacheKind kind) {
+  const bool e8 = kind == kCacheE4m3;
+  if (d == 64)
+    return G <= 8 ? (e8 ? one_wave<64, true, 1>(G) : one_wave<64, false, 1>(G))
+                  : (e8 ? one_wave<64, true, 2>(G) : one_wave<64, false, 2>(G));
+  return G <= 8 ? (e8 ? one_wave<128, true, 1>(G) : one_wave<128, false, 1>(G))
+                : (e8 ? one_wave<128, true, 2>(G) : one_wave<128, false, 2>(G));
+}
+
 }  // namespace dcp
