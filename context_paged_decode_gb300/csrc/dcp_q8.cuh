@@ -11,14 +11,19 @@ namespace dcp {
 
 constexpr int kScaleFloats = 4;   // of a page and head: keys', values', two unused
 
-// Two e4m3 numbers (the low byte first) as fp16, which holds them exactly.
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)h.x | (uint32_t)h.y << 16;
+// Four e4m3 numbers (the low byte first) as fp16, which holds them exactly.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 
 __device__ __forceinline__ float4 e4m3x4_f32(uint32_t four) {
-  const uint32_t a = e4m3x2_f16(four & 0xffffu), b = e4m3x2_f16(four >> 16);
+  uint32_t a, b;
+  e4m3x4_f16(four, a, b);
   const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
   const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
   return make_float4(x.x, x.y, y.x, y.y);

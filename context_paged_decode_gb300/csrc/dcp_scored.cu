@@ -53,7 +53,6 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
   __shared__ __align__(16) float s_q[HP][DI * 32];
   __shared__ __align__(16) float s_o[kScoredWarps][HP][DI * 32];
   __shared__ float s_m[kScoredWarps][HP], s_l[kScoredWarps][HP];
-  griddep_launch_dependents();   // the merge may start its launch
   griddep_wait();                // launched chained: the preceding kernel completed
   const Run run = plan_run<kScoredWarps * 32>(A);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -251,8 +250,8 @@ __global__ void __launch_bounds__(kMergeThreads)
 scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
   __shared__ float s_lse[16], s_weight[16];
   __shared__ __align__(16) float4 s_acc[kMergeThreads];
-  griddep_launch_dependents();   // the next call's first kernel may start its launch
   griddep_wait();
+  griddep_launch_dependents();   // the next call's first kernel may start its launch
   const int u = blockIdx.x, e = u / A.Hkv, g = u - e * A.Hkv, tid = threadIdx.x;
   const int64_t bef = A.before[e];
   const int n = (int)(A.before[e + 1] - bef);

@@ -74,11 +74,15 @@ struct Shape {
     if (kBoxBytes == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
     return (c >> 3) * (kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
   }
+  // The same for chunk 2 i + c from that of chunk c < 2.
+  static __device__ __forceinline__ uint32_t on(uint32_t first, int i) {
+    return (first ^ ((2 * i & 7) << 4)) + (2 * i >> 3) * (kRows * 128);
+  }
 };
 
 constexpr float kSlack = 4.f;    // how far a score may pass its reference, in powers of two
-constexpr float kLift = 10.f;    // fp16 weights are held times 2^10: up to 2^15 with the slack and a
-                                 // scale's fraction, and in full precision down to 2^-24
+constexpr float kLift = 11.f;    // fp16 weights are held times 2^11: up to 2^15 with the slack, and
+                                 // in full precision down to 2^-25
 constexpr int kScoredStuck = 1 << 20;   // err_count increment for a wait that timed out
 
 // Four warps a CTA, each with a ring of its own for every fourth tile of the
@@ -86,12 +90,11 @@ constexpr int kScoredStuck = 1 << 20;   // err_count increment for a wait that t
 // entries are looked up 32 tiles at a time, a tile a lane.  A score is compared
 // with its head's reference only to see whether it passes it by more than 2^4;
 // while none does (one vote), nothing is rescaled and no maximum is shared.
-template <int D, bool E8, int NT>
+template <int D, bool E8, int NT, bool kFormed>
 __global__ void __launch_bounds__(kScoredWarps * 32, Shape<D, E8, NT>::kPerSm)
 scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ ScoredMaps maps) {
   using Z = Shape<D, E8, NT>;
   constexpr int ST = Z::kStages, TB = Z::kTileBytes, KS = D / 16;
-  griddep_launch_dependents();   // the merge may start its launch
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -116,6 +119,11 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
   griddep_wait();                // launched chained: the preceding kernel completed
   const Run run = plan_run<kScoredWarps * 32>(A);
   const uint64_t pol = policy_evict_first();
+  // what this lane gives ldmatrix of a tile's keys and of its values: the rows of the four
+  // 8 x 8 tiles are tokens 0-7 and 8-15 of one chunk and of the next
+  const int mi = lane >> 3;
+  const uint32_t k_at = Z::at((mi & 1) * 8 + (lane & 7), mi >> 1);
+  const uint32_t v_at = E8 ? k_at : Z::at((mi >> 1) * 8 + (lane & 7), mi & 1);
   const int mine = run.t1 > run.t0 + warp
                        ? (int)((run.t1 - run.t0 - warp + kScoredWarps - 1) / kScoredWarps)
                        : 0;
@@ -261,7 +269,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int h = 2 * tq + i + 8 * x;
-        mul[x][i] = A.scale;
+        mul[x][i] = kFormed ? A.scale : A.scale * kLog2e;
         if (E8) mul[x][i] /= __shfl_sync(0xffffffffu, up, (2 * tq + i) * 4);
         slope[x][i] = A.slopes && h < A.G ? __ldg(A.slopes + g * A.G + h) : 0.f;
       }
@@ -291,16 +299,16 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
       if (!dead && desc.x >= 0) {
         const uint32_t kb = ring + st * 2 * TB, vb = kb + TB;
         const int lo = desc.y & 255, hi = (desc.y >> 8) & 255;
-        float ks_ = 1.f, vmant = 1.f, vexp = 0.f;
+        float ks_ = 1.f, vlog = 0.f;   // the keys' scale, and log2 of the values'
         if (E8) {
-          const float2 s2 = *reinterpret_cast<const float2*>(s_scale + st * 4);
-          ks_ = s2.x;
-          // the values' scale as a fraction of [1, 2) and a power of two
-          const int bits = __float_as_int(s2.y);
-          vmant = __int_as_float((bits & 0x7fffff) | 0x3f800000);
-          vexp = (float)((bits >> 23) - 127);
+          const float2 both = *reinterpret_cast<const float2*>(s_scale + st * 4);
+          ks_ = both.x;
+          const int bits = __float_as_int(both.y), mant = bits & 0x7fffff;
+          vlog = (float)((bits >> 23) - 127);     // exact for a power of two
+          if (mant) vlog += log2f(__int_as_float(mant | 0x3f800000));
         }
-        if (lo > 0 || hi < kRows) {   // values that do not count are zeros, so 0 * NaN is not met
+        const bool edge = lo > 0 || hi < kRows;
+        if (edge) {   // values that do not count are zeros, so 0 * NaN is not met
           for (int i = lane; i < kRows * (Z::kRowBytes / 16); i += 32) {
             const int row = i / (Z::kRowBytes / 16), c = i % (Z::kRowBytes / 16);
             if (row < lo || row >= hi)
@@ -309,57 +317,76 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
           }
           __syncwarp();
         }
-        // S^T = K Q^T
-        float s[NT][4];
+        // S^T = K Q^T, in two chains of products
+        float s[NT][4], s2[NT][4];
 #pragma unroll
-        for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
-        const int mi = lane >> 3;
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[x][i] = s2[x][i] = 0.f;
         {
-          const int krow = (mi & 1) * 8 + (lane & 7);
           if (E8) {
 #pragma unroll
             for (int i = 0; i < KS / 2; ++i) {
               uint32_t r[4];
-              ldsm_x4(kb + Z::at(krow, 2 * i + (mi >> 1)), r[0], r[1], r[2], r[3]);
+              ldsm_x4(Z::on(kb + k_at, i), r[0], r[1], r[2], r[3]);
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const uint32_t a[4] = {
-                    e4m3x2_f16(r[2 * c] & 0xffffu), e4m3x2_f16(r[2 * c + 1] & 0xffffu),
-                    e4m3x2_f16(r[2 * c] >> 16), e4m3x2_f16(r[2 * c + 1] >> 16)};
+                uint32_t a[4];
+                e4m3x4_f16(r[2 * c], a[0], a[2]);
+                e4m3x4_f16(r[2 * c + 1], a[1], a[3]);
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
-                  mma_16816<E8>(s[x], a, qb[x][2 * i + c][0], qb[x][2 * i + c][1]);
+                  mma_16816<E8>(c ? s2[x] : s[x], a, qb[x][2 * i + c][0], qb[x][2 * i + c][1]);
               }
             }
           } else {
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
               uint32_t a[4];
-              ldsm_x4(kb + Z::at(krow, 2 * i + (mi >> 1)), a[0], a[1], a[2], a[3]);
+              ldsm_x4(Z::on(kb + k_at, i), a[0], a[1], a[2], a[3]);
 #pragma unroll
-              for (int x = 0; x < NT; ++x) mma_16816<E8>(s[x], a, qb[x][i][0], qb[x][i][1]);
+              for (int x = 0; x < NT; ++x)
+                mma_16816<E8>(i & 1 ? s2[x] : s[x], a, qb[x][i][0], qb[x][i][1]);
             }
           }
         }
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[x][i] += s2[x][i];
         // scores in base 2, of tokens gq (two heads) and gq + 8
-        const bool in0 = gq >= lo && gq < hi, in1 = gq + 8 >= lo && gq + 8 < hi;
-        float far0 = 0.f, far1 = 0.f;
-        if (A.slopes) {
-          const int r = desc.y >> 16, p = desc.z + gq, page = A.S.by_bs.div(p);
-          far0 = (float)(last - A.S.position(page, r, p - page * A.S.bs));
-          far1 = (float)(last - A.S.position(page, r, p + 8 - page * A.S.bs));
+        if (kFormed) {
+          float far[2] = {0.f, 0.f};
+          if (A.slopes) {
+            const int r = desc.y >> 16, p = desc.z + gq, page = A.S.by_bs.div(p);
+            far[0] = (float)(last - A.S.position(page, r, p - page * A.S.bs));
+            far[1] = (float)(last - A.S.position(page, r, p + 8 - page * A.S.bs));
+          }
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              s[x][i] = formed(A, s[x][i] * (mul[x][i & 1] * ks_), slope[x][i & 1], far[i >> 1]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[x][i] *= mul[x][i & 1] * ks_;
+        }
+        if (edge) {
+          const bool in[2] = {gq >= lo && gq < hi, gq + 8 >= lo && gq + 8 < hi};
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[x][i] = in[i >> 1] ? s[x][i] : -INFINITY;
         }
         bool over = false;
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int h = i & 1;
-            const float v = formed(A, s[x][i] * (mul[x][h] * ks_), slope[x][h], i < 2 ? far0 : far1);
-            s[x][i] = (i < 2 ? in0 : in1) ? v : -INFINITY;
-            over |= s[x][i] > thr[x][h];
-            if (E8) over |= s[x][i] + vexp > vthr[x][h];
-          }
+          for (int h = 0; h < 2; ++h)
+            over |= fmaxf(s[x][h], s[x][h + 2]) >
+                    (E8 ? fminf(thr[x][h], vthr[x][h] - vlog) : thr[x][h]);
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int x = 0; x < NT; ++x)
@@ -378,7 +405,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
               }
               if (E8) {
                 down = 1.f;
-                const float mv = m + vexp;
+                const float mv = m + vlog;
                 if (mv > vthr[x][h]) {
                   down = vthr[x][h] == -INFINITY ? 0.f : ex2_ftz(vref[x][h] - mv);
                   vref[x][h] = mv;
@@ -402,35 +429,32 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
             const int h = i & 1;
             p[i] = ex2_ftz(s[x][i] - ref[x][h]);
             l[x][h] += p[i];
-            if (E8) p[i] = ex2_ftz(s[x][i] + (vexp + kLift) - vref[x][h]) * vmant;
+            if (E8) p[i] = ex2_ftz(s[x][i] + (vlog + kLift - vref[x][h]));
           }
           pb[x][0] = transposed8(E8 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
           pb[x][1] = transposed8(E8 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
         }
         // O^T += V^T P^T.  In 8 bits row j of a tile of 16 dims is dim 2 j, row 8 + j dim 2 j + 1.
         if (E8) {
-          const int vrow = (mi & 1) * 8 + (lane & 7);
 #pragma unroll
           for (int i = 0; i < KS / 2; ++i) {
             uint32_t r[4];
-            ldsm_x4_t(vb + Z::at(vrow, 2 * i + (mi >> 1)), r[0], r[1], r[2], r[3]);
+            ldsm_x4_t(Z::on(vb + v_at, i), r[0], r[1], r[2], r[3]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               // bytes (token, dim) 00 01 10 11 -> 00 10 01 11
-              const uint32_t u = __byte_perm(r[2 * c], 0, 0x3120);
-              const uint32_t w = __byte_perm(r[2 * c + 1], 0, 0x3120);
-              const uint32_t a[4] = {e4m3x2_f16(u & 0xffffu), e4m3x2_f16(u >> 16),
-                                     e4m3x2_f16(w & 0xffffu), e4m3x2_f16(w >> 16)};
+              uint32_t a[4];
+              e4m3x4_f16(__byte_perm(r[2 * c], 0, 0x3120), a[0], a[1]);
+              e4m3x4_f16(__byte_perm(r[2 * c + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
               for (int x = 0; x < NT; ++x) mma_16816<E8>(o[x][2 * i + c], a, pb[x][0], pb[x][1]);
             }
           }
         } else {
-          const int vrow = (mi >> 1) * 8 + (lane & 7);
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
             uint32_t a[4];
-            ldsm_x4_t(vb + Z::at(vrow, 2 * i + (mi & 1)), a[0], a[1], a[2], a[3]);
+            ldsm_x4_t(Z::on(vb + v_at, i), a[0], a[1], a[2], a[3]);
 #pragma unroll
             for (int x = 0; x < NT; ++x) mma_16816<E8>(o[x][i], a, pb[x][0], pb[x][1]);
           }
@@ -496,6 +520,10 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
     }
     __syncthreads();
   }
+  // Only now may the merge start its launch, and only after its wait the next
+  // call: 32 requests called in a row take 204 us each so, 315 where both kernels
+  // say so at their start (the next call's CTAs come in beside the merge's).
+  griddep_launch_dependents();
 }
 
 // ---------------------------------------------------------------------------
@@ -522,10 +550,10 @@ static bool encode_rows(CUtensorMap* map, const void* base, uint64_t row, uint64
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool E8, int NT>
+template <int D, bool E8, int NT, bool kFormed>
 static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
   using Z = Shape<D, E8, NT>;
-  if (!allow_smem<scored_mma_kernel<D, E8, NT>>()) return DCP_ECUDA;
+  if (!allow_smem<scored_mma_kernel<D, E8, NT, kFormed>>()) return DCP_ECUDA;
   ScoredMaps maps;
   memset((void*)&maps, 0, sizeof(maps));
   const uint64_t rows = (uint64_t)A.nb * A.Hkv * A.S.bs;
@@ -533,14 +561,16 @@ static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
     if (!encode_rows(&maps.k[r], A.k.ptr[r], Z::kRowBytes, rows) ||
         !encode_rows(&maps.v[r], A.v.ptr[r], Z::kRowBytes, rows))
       return DCP_ECUDA;
-  const cudaError_t e = launch_chained(scored_mma_kernel<D, E8, NT>, (unsigned)A.ctas,
+  const cudaError_t e = launch_chained(scored_mma_kernel<D, E8, NT, kFormed>, (unsigned)A.ctas,
                                        kScoredWarps * 32, Z::smem(A.G), s, A, maps);
   return e == cudaSuccess ? launch_status() : launch_status_report(e);
 }
 
 template <int D, bool E8>
 static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
-  return A.G <= 8 ? launch_mma<D, E8, 1>(A, s) : launch_mma<D, E8, 2>(A, s);
+  if (A.cap > 0.f || A.slopes)
+    return A.G <= 8 ? launch_mma<D, E8, 1, true>(A, s) : launch_mma<D, E8, 2, true>(A, s);
+  return A.G <= 8 ? launch_mma<D, E8, 1, false>(A, s) : launch_mma<D, E8, 2, false>(A, s);
 }
 
 int launch_scored_mma(const ScoredArgs& A, CacheKind kind, cudaStream_t s) {
