@@ -58,23 +58,11 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = lane & 7, grp = lane >> 3;
   const int di = A.d / 32;
-  int64_t start = run.start;
-  int e = run.e, n = 0;
-  bool fresh = true;
-  for (int64_t t = run.t0; t < run.t1;) {
-    if (fresh) {
-      n = entry_tiles(A, e, false);
-      fresh = false;
-    }
-    if (t >= start + (int64_t)n * A.Hkv) {
-      start += (int64_t)n * A.Hkv;
-      ++e;
-      fresh = true;
-      continue;
-    }
-    const int g = (int)((t - start) / n), k0 = (int)(t - start - (int64_t)g * n);
-    const int k1 = (int)min((int64_t)n, k0 + (run.t1 - t));
-    t += k1 - k0;
+  Piece at;
+  at.e = run.e, at.n = run.n, at.start = run.start, at.t = run.t0;
+  while (at.t < run.t1) {
+    at = piece_at(A, run, at.t, at.e, at.n, at.start);
+    const int e = at.e, g = at.g, k0 = at.k0, k1 = at.k1, n = at.n;
     const int b = A.apart ? e % A.B : e, r0 = A.apart ? e / A.B : 0;
     const int r1 = A.apart ? r0 + 1 : A.S.dcp;
     const Seen seen = seen_of(A, b, false);
@@ -241,6 +229,7 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
 // ---------------------------------------------------------------------------
 
 constexpr int kMergeThreads = 256;
+constexpr int kMergeAhead = 8;   // rows a thread asks for at a time
 
 // A CTA joins the parts of one unit, in the order of its tiles: the heads' LSE
 // first, then each thread four values of a head, the parts shared out to groups
@@ -262,6 +251,18 @@ scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
   if (parts == 1) return;
   const int64_t slot = i0 + u;
   const int lane = tid & 31, warp = tid >> 5;
+  // the first rows are on their way before the LSE
+  const int quads = A.d / 4, cols = A.G * quads;
+  const int groups = max(kMergeThreads / cols, 1);
+  const int grp = min(tid / cols, groups);   // the last threads may have no group
+  const float4* const po = reinterpret_cast<const float4*>(A.part_o + slot * A.G * A.d);
+  float4 y[kMergeAhead];
+  const int c_first = tid - grp * cols;
+  if (grp < groups && c_first < cols) {
+#pragma unroll
+    for (int j = 0; j < kMergeAhead; ++j)
+      if (grp + j * groups < parts) y[j] = po[(int64_t)(grp + j * groups) * cols + c_first];
+  }
   for (int hh = warp; hh < A.G; hh += kMergeThreads / 32) {
     const float* pl = A.part_lse + slot * A.G + hh;
     float m = -INFINITY, s = 0.f;
@@ -281,28 +282,30 @@ scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
     }
   }
   __syncthreads();
-  const int quads = A.d / 4, cols = A.G * quads;
-  const int groups = max(kMergeThreads / cols, 1);
-  const int grp = min(tid / cols, groups);   // the last threads may have no group
   for (int c0 = 0; c0 < cols; c0 += kMergeThreads) {
-    const int c = c0 + tid - grp * cols;
+    const int c = c0 + c_first;
     const bool mine = grp < groups && c < cols;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int hh = mine ? c / quads : 0;
     if (mine) {
       const float lse = s_lse[hh];
       const float* pl = A.part_lse + slot * A.G + hh;
-      const float4* po = reinterpret_cast<const float4*>(A.part_o + slot * A.G * A.d) + c;
-#pragma unroll 4
-      for (int i = grp; i < parts; i += groups) {
-        const float x = pl[(int64_t)i * A.G];
-        const float4 y = po[(int64_t)i * cols];
-        if (x != -INFINITY) {
+      for (int i = grp; i < parts; i += kMergeAhead * groups) {
+        if (c0 > 0 || i > grp) {
+#pragma unroll
+          for (int j = 0; j < kMergeAhead; ++j)
+            if (i + j * groups < parts) y[j] = po[(int64_t)(i + j * groups) * cols + c];
+        }
+#pragma unroll
+        for (int j = 0; j < kMergeAhead; ++j) {
+          if (i + j * groups >= parts) continue;
+          const float x = pl[(int64_t)(i + j * groups) * A.G];
+          if (x == -INFINITY) continue;
           const float w = expf(x - lse);
-          acc.x = fmaf(w, y.x, acc.x);
-          acc.y = fmaf(w, y.y, acc.y);
-          acc.z = fmaf(w, y.z, acc.z);
-          acc.w = fmaf(w, y.w, acc.w);
+          acc.x = fmaf(w, y[j].x, acc.x);
+          acc.y = fmaf(w, y[j].y, acc.y);
+          acc.z = fmaf(w, y[j].z, acc.z);
+          acc.w = fmaf(w, y[j].w, acc.w);
         }
       }
     }

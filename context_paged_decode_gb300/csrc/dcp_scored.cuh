@@ -51,7 +51,8 @@ struct Shards {
 
 // Tokens of [0, x) on each rank: what is the same for all ranks is worked out once.
 struct Below {
-  int base, in;   // whole runs, and what is left of the last turn
+  int base = 0, in = 0;   // whole runs, and what is left of the last turn
+  Below() = default;
   __device__ __forceinline__ Below(const Shards& S, int x) {
     const int full = S.by_vbs.div(x), rem = x - full * S.vbs, q = S.by_turn.div(rem);
     base = full * S.bs + q * S.I;
@@ -112,7 +113,13 @@ struct Seen {
   Below lo, p, w, n;
   bool kept;   // there is a run of kept tokens apart from the window
   __device__ __forceinline__ Seen(const ScoredArgs& A, int lo_, int p_, int w_, int n_)
-      : lo(A.S, lo_), p(A.S, p_), w(A.S, w_), n(A.S, n_), kept(p_ > lo_) {}
+      : n(A.S, n_), kept(p_ > lo_) {
+    if (w_ > 0) w = Below(A.S, w_);
+    if (kept) {
+      lo = Below(A.S, lo_);
+      p = Below(A.S, p_);
+    }
+  }
   __device__ __forceinline__ RankTokens on(const Shards& S, int r) const {
     RankTokens t;
     t.b0 = w.on(S, r);
@@ -165,9 +172,31 @@ __device__ __forceinline__ int entry_tiles(const ScoredArgs& A, int e, bool coun
 struct Run {
   int64_t t0, t1;   // this CTA's tiles
   int64_t start;    // first tile of entry e
-  int e;            // entry of t0
+  int e, n;         // entry of t0, and its tiles for a head
   int64_t each;
 };
+
+// A CTA's part of a unit: tiles [k0, k1) of head g of entry e.
+struct Piece {
+  int e, g, k0, k1, n;
+  int64_t start, t;   // first tile of the entry, and the line's tile behind the piece
+};
+
+__device__ __forceinline__ Piece piece_at(const ScoredArgs& A, const Run& run, int64_t t, int e,
+                                          int n, int64_t start) {
+  while (t >= start + (int64_t)n * A.Hkv && e + 1 < A.entries()) {
+    start += (int64_t)n * A.Hkv;
+    n = entry_tiles(A, ++e, false);
+  }
+  Piece p;
+  p.e = e, p.n = n, p.start = start;
+  const int64_t in = t - start;
+  p.g = in < (int64_t(1) << 31) ? (int)((uint32_t)in / (uint32_t)n) : (int)(in / n);
+  p.k0 = (int)(in - (int64_t)p.g * n);
+  p.k1 = (int)min((int64_t)n, p.k0 + (run.t1 - t));
+  p.t = t + (p.k1 - p.k0);
+  return p;
+}
 
 // Every thread of the CTA calls it; all get the same.  The lengths are read by
 // every CTA: a plan of one CTA in front would cost a launch (a call of one
@@ -175,8 +204,8 @@ struct Run {
 template <int kThreads>
 __device__ __forceinline__ Run plan_run(const ScoredArgs& A) {
   __shared__ int64_t s_sum[kThreads / 32];
-  __shared__ int64_t s_start, s_total;
-  __shared__ int s_e;
+  __shared__ int64_t s_start;
+  __shared__ int s_e, s_n;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = A.entries(), c = (E + kThreads - 1) / kThreads;
   const int e0 = min(tid * c, E), e1 = min(e0 + c, E);
@@ -195,7 +224,11 @@ __device__ __forceinline__ Run plan_run(const ScoredArgs& A) {
     if (lane >= o) upto += x;
   }
   if (lane == 31) s_sum[warp] = upto;
-  if (tid == 0) s_e = E;
+  if (tid == 0) {
+    s_e = E;
+    s_n = 0;
+    s_start = 0;
+  }
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
@@ -227,6 +260,7 @@ __device__ __forceinline__ Run plan_run(const ScoredArgs& A) {
       if (e > e0) n = entry_tiles(A, e, false);
       if (run.t0 < (before + n) * A.Hkv) {
         s_e = e;
+        s_n = n;
         s_start = before * A.Hkv;
         break;
       }
@@ -235,6 +269,7 @@ __device__ __forceinline__ Run plan_run(const ScoredArgs& A) {
   }
   __syncthreads();
   run.e = s_e;
+  run.n = s_n;
   run.start = s_start;
   return run;
 }

@@ -129,49 +129,58 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
                        : 0;
 
   // --- tiles on their way: this lane's of the 32 looked up ---
-  int we = run.e, wn = 0;
+  int we = run.e;
   int64_t wstart = run.start;
-  if (mine > 0) wn = entry_tiles(A, we, false);
   int d_row = -1, d_ph = 0, d_info = 0, d_p0 = 0;
   auto look_up = [&](int j0) {
     const int64_t t = run.t0 + warp + (int64_t)(j0 + lane) * kScoredWarps;
-    if (t < run.t1) {
-      while (t >= wstart + (int64_t)wn * A.Hkv) {
-        wstart += (int64_t)wn * A.Hkv;
-        wn = entry_tiles(A, ++we, false);
-      }
-      const int g = (int)((t - wstart) / wn);
-      int left = (int)(t - wstart - (int64_t)g * wn);
+    bool todo = t < run.t1;
+    d_row = -1;
+    const int R = A.apart ? 1 : A.S.dcp;
+    for (;;) {   // entry by entry, a rank's tokens in each lane
       const int b = A.apart ? we % A.B : we, r0 = A.apart ? we / A.B : 0;
-      const Seen seen = seen_of(A, b, false);
-      int r = r0, lo = 0, hi = 0;
-      for (; r < A.S.dcp; ++r) {   // the tile is there: a rank is found
-        const RankTokens T = seen.on(A.S, r);
-        const int na = T.a_tiles(), nb = T.b_tiles();
-        if (left < na) {
-          d_p0 = (T.a0 / kRows + left) * kRows, lo = T.a0, hi = T.a1;
-          break;
-        }
-        left -= na;
-        if (left < nb) {
-          d_p0 = (T.b0 / kRows + left) * kRows, lo = T.b0, hi = T.b1;
-          break;
-        }
-        left -= nb;
+      RankTokens T = seen_of(A, b, false).on(A.S, r0 + min(lane, R - 1));
+      const int na = T.a_tiles();
+      int upto = lane < R ? na + T.b_tiles() : 0;
+#pragma unroll
+      for (int o = 1; o < DCP_MAX_RANKS; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
       }
-      const int vb = A.S.by_bs.div(d_p0);
-      const int64_t page =
-          vb < A.max_vb ? (int64_t)__ldg(A.bt + r * A.bt_stride + (int64_t)b * A.max_vb + vb) : -1;
-      d_info = max(lo - d_p0, 0) | min(hi - d_p0, kRows) << 8 | r << 16;
-      d_row = -1;
-      if (page >= 0 && page < A.nb) {
-        d_ph = (int)(page * A.Hkv + g);
-        d_row = d_ph * A.S.bs + (d_p0 - vb * A.S.bs);
+      const int n = __shfl_sync(0xffffffffu, upto, R - 1);
+      const int64_t in = t - wstart;
+      const bool here = todo && in < (int64_t)n * A.Hkv;
+      int g = 0, left = 0;
+      if (here) {
+        g = in < (int64_t(1) << 31) ? (int)((uint32_t)in / (uint32_t)n) : (int)(in / n);
+        left = (int)(in - (int64_t)g * n);
       }
+      int r = 0;
+      for (int x = 0; x < R - 1; ++x) r += left >= __shfl_sync(0xffffffffu, upto, x);
+      const int up_r = __shfl_sync(0xffffffffu, upto, r), na_r = __shfl_sync(0xffffffffu, na, r);
+      const int a0 = __shfl_sync(0xffffffffu, T.a0, r), a1 = __shfl_sync(0xffffffffu, T.a1, r);
+      const int b0 = __shfl_sync(0xffffffffu, T.b0, r), b1 = __shfl_sync(0xffffffffu, T.b1, r);
+      if (here) {   // first the kept tokens, then the window
+        const int nb_r = (b1 + kRows - 1) / kRows - b0 / kRows;
+        const int k = left - (up_r - na_r - (b1 > b0 ? nb_r : 0));
+        const bool kept = k < na_r;
+        const int lo = kept ? a0 : b0, hi = kept ? a1 : b1;
+        d_p0 = ((lo / kRows) + k - (kept ? 0 : na_r)) * kRows;
+        const int vb = A.S.by_bs.div(d_p0);
+        r += r0;
+        const int64_t page =
+            vb < A.max_vb ? (int64_t)__ldg(A.bt + r * A.bt_stride + (int64_t)b * A.max_vb + vb) : -1;
+        d_info = max(lo - d_p0, 0) | min(hi - d_p0, kRows) << 8 | r << 16;
+        if (page >= 0 && page < A.nb) {
+          d_ph = (int)(page * A.Hkv + g);
+          d_row = d_ph * A.S.bs + (d_p0 - vb * A.S.bs);
+        }
+        todo = false;
+      }
+      if (!__any_sync(0xffffffffu, todo) || we + 1 >= A.entries()) break;
+      wstart += (int64_t)n * A.Hkv;
+      ++we;
     }
-    we = __shfl_sync(0xffffffffu, we, 31);
-    wn = __shfl_sync(0xffffffffu, wn, 31);
-    wstart = __shfl_sync(0xffffffffu, wstart, 31);
   };
   bool dead = false;   // a wait timed out: stop waiting and issuing
   auto issue = [&](int j) {   // the whole warp, for its j-th tile
@@ -200,78 +209,79 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
       }
     }
   };
-  for (int j = 0; j < ST && j < mine; ++j) issue(j);
-
-  // --- pieces ---
-  int64_t start = run.start;
-  int e = run.e, n = 0, seq = 0;
-  bool fresh = true;
-  for (int64_t t = run.t0; t < run.t1;) {
-    if (fresh) {
-      n = entry_tiles(A, e, false);
-      fresh = false;
-    }
-    if (t >= start + (int64_t)n * A.Hkv) {
-      start += (int64_t)n * A.Hkv;
-      ++e;
-      fresh = true;
-      continue;
-    }
-    const int g = (int)((t - start) / n), k0 = (int)(t - start - (int64_t)g * n);
-    const int k1 = (int)min((int64_t)n, k0 + (run.t1 - t));
-    t += k1 - k0;
-    // this warp's tiles of the run that end before t
-    const int upto = t > run.t0 + warp
-                         ? (int)((t - run.t0 - warp + kScoredWarps - 1) / kScoredWarps)
-                         : 0;
-    const int b = A.apart ? e % A.B : e;
-    const int last = __ldg(A.lens + b) - 1;
-
-    // queries as the B operand: head gq (+ 8), and of heads 2 tq, 2 tq + 1 (+ 8) what a
-    // product is to be multiplied by
-    uint32_t qb[NT][KS][2];
-    float mul[NT][2], slope[NT][2];
+  // queries as the B operand: what they are in memory, asked for ahead, of head gq (+ 8);
+  // in 8 bits in the order of a row of keys in its fragments, dims 4 tq .. 4 tq + 3 of each 16
+  uint32_t qb[NT][KS][2];
+  auto ask_queries = [&](const Piece& p) {
+    const int b = A.apart ? p.e % A.B : p.e;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
       const bool there = gq + 8 * x < A.G;
       const __nv_bfloat16* qh =
-          (const __nv_bfloat16*)A.q + ((int64_t)b * A.Hq + g * A.G + gq + 8 * x) * D;
+          (const __nv_bfloat16*)A.q + ((int64_t)b * A.Hq + p.g * A.G + gq + 8 * x) * D;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if (E8) {
+          const uint2 w = there ? __ldg(reinterpret_cast<const uint2*>(qh + ks * 16 + tq * 4))
+                                : make_uint2(0u, 0u);
+          qb[x][ks][0] = w.x;
+          qb[x][ks][1] = w.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qb[x][ks][i] =
+                there ? __ldg(reinterpret_cast<const uint32_t*>(qh + ks * 16 + i * 8 + tq * 2)) : 0u;
+        }
+      }
+    }
+  };
+  Piece at;
+  at.e = run.e, at.n = run.n, at.start = run.start, at.t = run.t0;
+  if (at.t < run.t1) {
+    at = piece_at(A, run, at.t, at.e, at.n, at.start);
+    ask_queries(at);
+  }
+  for (int j = 0; j < ST && j < mine; ++j) issue(j);
+
+  // --- pieces ---
+  int seq = 0;
+  for (bool more = run.t0 < run.t1; more;) {
+    const int e = at.e, g = at.g, k0 = at.k0, k1 = at.k1, n = at.n;
+    // this warp's tiles of the run that end before the piece's
+    const int upto = at.t > run.t0 + warp
+                         ? (int)((at.t - run.t0 - warp + kScoredWarps - 1) / kScoredWarps)
+                         : 0;
+    int last = 0;
+    if (kFormed) last = __ldg(A.lens + (A.apart ? e % A.B : e)) - 1;
+
+    // of heads 2 tq, 2 tq + 1 (+ 8) what a product is to be multiplied by
+    float mul[NT][2], slope[NT][2];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
       float up = 1.f;
       if (E8) {
-        // the fragments' order of a row of keys: bytes 4 tq .. 4 tq + 3 of each 16
-        uint2 w[KS];
         float top = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          w[ks] = there ? __ldg(reinterpret_cast<const uint2*>(qh + ks * 16 + tq * 4))
-                        : make_uint2(0u, 0u);
-          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(w[ks].x)), fabsf(bf16_hi(w[ks].x))),
-                                 fmaxf(fabsf(bf16_lo(w[ks].y)), fabsf(bf16_hi(w[ks].y)))));
-        }
+        for (int ks = 0; ks < KS; ++ks)
+          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(qb[x][ks][0])), fabsf(bf16_hi(qb[x][ks][0]))),
+                                 fmaxf(fabsf(bf16_lo(qb[x][ks][1])), fabsf(bf16_hi(qb[x][ks][1])))));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^(14 - exponent of the largest); without a finite one, or with none, 1
         const int ex = (__float_as_int(top) >> 23) - 127;
         if (top > 0.f && ex < 128) up = __int_as_float((min(14 - ex, 126) + 127) << 23);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          qb[x][ks][0] = pack_f16(bf16_lo(w[ks].x) * up, bf16_hi(w[ks].x) * up);
-          qb[x][ks][1] = pack_f16(bf16_lo(w[ks].y) * up, bf16_hi(w[ks].y) * up);
-        }
-      } else {
-#pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            qb[x][ks][i] =
-                there ? __ldg(reinterpret_cast<const uint32_t*>(qh + ks * 16 + i * 8 + tq * 2)) : 0u;
+            qb[x][ks][i] = pack_f16(bf16_lo(qb[x][ks][i]) * up, bf16_hi(qb[x][ks][i]) * up);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int h = 2 * tq + i + 8 * x;
         mul[x][i] = kFormed ? A.scale : A.scale * kLog2e;
         if (E8) mul[x][i] /= __shfl_sync(0xffffffffu, up, (2 * tq + i) * 4);
-        slope[x][i] = A.slopes && h < A.G ? __ldg(A.slopes + g * A.G + h) : 0.f;
+        slope[x][i] = kFormed && A.slopes && h < A.G ? __ldg(A.slopes + g * A.G + h) : 0.f;
       }
     }
     // references: of the scores (ref) and, in 8 bits, of scores and scales together
@@ -467,6 +477,17 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
       }
     }
 
+    // the next piece, and its queries on their way
+    PieceOut P;
+    P.whole = k0 == 0 && k1 == n;
+    P.slot = blockIdx.x + (int64_t)e * A.Hkv + g;
+    P.row = (int64_t)e * A.Hq + g * A.G;
+    more = at.t < run.t1;
+    if (more) {
+      at = piece_at(A, run, at.t, at.e, at.n, at.start);
+      ask_queries(at);
+    }
+
     // --- the piece's result: the warps' sums against a common reference ---
 #pragma unroll
     for (int x = 0; x < NT; ++x)
@@ -480,43 +501,67 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
         if (hh >= A.G) continue;
         if (gq == 0) {
           const bool any = thr[x][h] != -INFINITY;
-          float* ml = s_ml + (warp * A.G + hh) * 4;
-          ml[0] = any ? ref[x][h] : -INFINITY;
-          ml[1] = sum;
-          ml[2] = !any ? -INFINITY : E8 ? vref[x][h] - kLift : ref[x][h];
+          *reinterpret_cast<float4*>(s_ml + (hh * kScoredWarps + warp) * 4) =
+              make_float4(any ? ref[x][h] : -INFINITY, sum,
+                          !any ? -INFINITY : E8 ? vref[x][h] - kLift : ref[x][h], 0.f);
         }
         float* os = s_o + (warp * A.G + hh) * D;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
-          os[i * 16 + (E8 ? 2 * gq : gq)] = o[x][i][h];
-          os[i * 16 + (E8 ? 2 * gq + 1 : gq + 8)] = o[x][i][h + 2];
+          if (E8) {
+            *reinterpret_cast<float2*>(os + i * 16 + 2 * gq) = make_float2(o[x][i][h], o[x][i][h + 2]);
+          } else {
+            os[i * 16 + gq] = o[x][i][h];
+            os[i * 16 + gq + 8] = o[x][i][h + 2];
+          }
         }
       }
     __syncthreads();
-    PieceOut P;
-    P.whole = k0 == 0 && k1 == n;
-    P.slot = blockIdx.x + (int64_t)e * A.Hkv + g;
-    P.row = (int64_t)e * A.Hq + g * A.G;
-    for (int i = tid; i < A.G * D; i += kScoredWarps * 32) {
-      const int hh = i / D, c = i % D;
-      float M = -INFINITY, V = -INFINITY, Ls = 0.f, O = 0.f;
+    // a head's four numbers of each warp become its four factors
+    if (tid < A.G) {
+      float4* const ml = reinterpret_cast<float4*>(s_ml) + tid * kScoredWarps;
+      float M = -INFINITY, V = -INFINITY, Ls = 0.f;
+      float4 w[kScoredWarps];
 #pragma unroll
-      for (int w = 0; w < kScoredWarps; ++w) {
-        M = fmaxf(M, s_ml[(w * A.G + hh) * 4]);
-        V = fmaxf(V, s_ml[(w * A.G + hh) * 4 + 2]);
+      for (int i = 0; i < kScoredWarps; ++i) {
+        w[i] = ml[i];
+        M = fmaxf(M, w[i].x);
+        V = fmaxf(V, w[i].z);
       }
 #pragma unroll
-      for (int w = 0; w < kScoredWarps; ++w) {
-        const float* ml = s_ml + (w * A.G + hh) * 4;
-        if (ml[1] == 0.f) continue;   // nothing seen (a sum that is NaN stays)
-        Ls = fmaf(ml[1], ex2_ftz(ml[0] - M), Ls);
-        O = fmaf(s_o[(w * A.G + hh) * D + c], ex2_ftz(ml[2] - V), O);
-      }
+      for (int i = 0; i < kScoredWarps; ++i)   // nothing seen: no part (a sum that is NaN has one)
+        if (w[i].y != 0.f) Ls = fmaf(w[i].y, ex2_ftz(w[i].x - M), Ls);
       const bool any = Ls != 0.f;
-      float weight, lse = any ? (M + log2f(Ls)) * kLn2 : -INFINITY;
-      if (P.whole) lse = with_sink(A.sink, g * A.G + hh, lse, weight);
-      put_value(A, P, hh, c, any ? O / Ls * exp2f(V - M) : 0.f, weight);
-      if (c == 0) put_lse(A, P, hh, lse);
+      float weight = 1.f, lse = any ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+      if (P.whole) lse = with_sink(A.sink, g * A.G + tid, lse, weight);
+      put_lse(A, P, tid, lse);
+      const float f = any ? exp2f(V - M) / Ls * weight : 0.f;
+      float* const to = reinterpret_cast<float*>(ml);
+#pragma unroll
+      for (int i = 0; i < kScoredWarps; ++i)
+        to[i] = w[i].y != 0.f ? ex2_ftz(w[i].z - V) * f : 0.f;
+    }
+    __syncthreads();
+    for (int i = tid; i < A.G * (D / 4); i += kScoredWarps * 32) {
+      const float4 f = *reinterpret_cast<const float4*>(s_ml + i / (D / 4) * kScoredWarps * 4);
+      const float4* os = reinterpret_cast<const float4*>(s_o) + i;
+      const float fs[4] = {f.x, f.y, f.z, f.w};
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kScoredWarps; ++w) {
+        const float4 x = os[w * A.G * (D / 4)];
+        y.x = fmaf(x.x, fs[w], y.x);
+        y.y = fmaf(x.y, fs[w], y.y);
+        y.z = fmaf(x.z, fs[w], y.z);
+        y.w = fmaf(x.w, fs[w], y.w);
+      }
+      if (!P.whole)
+        reinterpret_cast<float4*>(A.part_o + P.slot * A.G * D)[i] = y;
+      else if (A.out_dtype == DCP_F32)
+        reinterpret_cast<float4*>((float*)A.out + P.row * D)[i] = y;
+      else
+        reinterpret_cast<uint2*>((__nv_bfloat16*)A.out + P.row * D)[i] =
+            make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
     }
     __syncthreads();
   }
