@@ -451,7 +451,7 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
   w += before_bytes(entries);
   const bool mma = scored_mma_ok(A, kv.kind, dtype == DCP_BF16);
   A.ctas = mma ? scored_mma_ctas(d, A.G, kv.kind) : generic_ctas();
-  A.least = 4 * kScoredWarps;
+  A.least = (mma ? 2 : 1) * kScoredWarps;
   A.part_lse = (float*)w;
   w += align_up((size_t)(A.ctas + entries * Hkv) * A.G * 4, 256);
   A.part_o = (float*)w;

@@ -274,9 +274,22 @@ __device__ __forceinline__ Run plan_run(const ScoredArgs& A) {
   return run;
 }
 
+// tanh: by its series (the terms up to y^9, the next is below 2^-26 of y) for
+// small y, and 1 - 2 / (1 + e^2y) where that loses less than 2^-21.  tanhf, which
+// branches, makes a capped call over 524288 tokens 219 us instead of 212.
+__device__ __forceinline__ float tanh_of(float y) {
+  const float e = ex2_ftz(y * (2.f * kLog2e)), z = y * y;
+  const float far = fmaf(-2.f, __fdividef(1.f, 1.f + e), 1.f);
+  float near = fmaf(z, 62.f / 2835.f, -17.f / 315.f);
+  near = fmaf(near, z, 2.f / 15.f);
+  near = fmaf(near, z, -1.f / 3.f);
+  near = fmaf(near * z, y, y);
+  return fabsf(y) < 0.25f ? near : far;
+}
+
 // A scaled score in base 2: capped, and less the distance's share.
 __device__ __forceinline__ float formed(const ScoredArgs& A, float t, float slope, float far) {
-  if (A.cap > 0.f) t = A.cap * tanhf(t * A.inv_cap);
+  if (A.cap > 0.f) t = A.cap * tanh_of(t * A.inv_cap);
   if (A.slopes) t -= slope * far;
   return t * kLog2e;
 }
