@@ -54,14 +54,20 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
   __shared__ __align__(16) float s_o[kScoredWarps][HP][DI * 32];
   __shared__ float s_m[kScoredWarps][HP], s_l[kScoredWarps][HP];
   griddep_wait();                // launched chained: the preceding kernel completed
-  const Run run = plan_run<kScoredWarps * 32>(A);
+  __shared__ int s_before[kScoredWarps * 32];
+  const Line line = plan_line<kScoredWarps * 32>(A, s_before);
+  const int chunk = blockIdx.x;
+  if (chunk == 0) keep_line<kScoredWarps * 32>(A, line, s_before);
+  const int t0 = min((int64_t)line.each * chunk, (int64_t)line.all);
+  const int t1 = min((int64_t)t0 + line.each, (int64_t)line.all);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = lane & 7, grp = lane >> 3;
   const int di = A.d / 32;
   Piece at;
-  at.e = run.e, at.n = run.n, at.start = run.start, at.t = run.t0;
-  while (at.t < run.t1) {
-    at = piece_at(A, run, at.t, at.e, at.n, at.start);
+  seek_entry<kScoredWarps * 32>(A, line, s_before, t0, at.e, at.start);
+  at.t = t0;
+  while (at.t < t1) {
+    at = piece_at(A, at.t, t1, at.e, at.start);
     const int e = at.e, g = at.g, k0 = at.k0, k1 = at.k1, n = at.n;
     const int b = A.apart ? e % A.B : e, r0 = A.apart ? e / A.B : 0;
     const int r1 = A.apart ? r0 + 1 : A.S.dcp;
@@ -69,7 +75,7 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
     const int last = __ldg(A.lens + b) - 1;
     PieceOut P;
     P.whole = k0 == 0 && k1 == n;
-    P.slot = blockIdx.x + (int64_t)e * A.Hkv + g;
+    P.slot = chunk + (int64_t)e * A.Hkv + g;
     P.row = (int64_t)e * A.Hq + g * A.G;
     for (int h0 = 0; h0 < A.G; h0 += HP) {
       __syncthreads();
@@ -242,14 +248,12 @@ scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
   griddep_wait();
   griddep_launch_dependents();   // the next call's first kernel may start its launch
   const int u = blockIdx.x, e = u / A.Hkv, g = u - e * A.Hkv, tid = threadIdx.x;
-  const int64_t bef = A.before[e];
-  const int n = (int)(A.before[e + 1] - bef);
-  const int64_t each = A.before[A.entries() + 1];
-  const int64_t t0 = bef * A.Hkv + (int64_t)g * n;
-  const int64_t i0 = t0 / each;
+  const int before = A.before[e], n = A.before[e + 1] - before;
+  const uint32_t each = A.before[A.entries() + 1];
+  const uint32_t t0 = before * A.Hkv + g * n, i0 = t0 / each;
   const int parts = n ? (int)((t0 + n - 1) / each - i0) + 1 : 0;
   if (parts == 1) return;
-  const int64_t slot = i0 + u;
+  const int64_t slot = (int64_t)i0 + u;
   const int lane = tid & 31, warp = tid >> 5;
   // the first rows are on their way before the LSE
   const int quads = A.d / 4, cols = A.G * quads;
@@ -357,16 +361,21 @@ static bool shape_ok(const dcp_layout_t& L, int B, int Hq, int Hkv, int d) {
          d >= 32 && d % 32 == 0 && d <= 256;
 }
 
-static size_t before_bytes(int64_t entries) { return align_up((size_t)(entries + 2) * 8, 256); }
+static size_t before_bytes(int64_t entries) { return align_up((size_t)(entries + 2) * 4, 256); }
+
+// Chunks of a call at most: one for each CTA that runs at once.
+static int most_chunks(int d, int G) {
+  int most = generic_ctas();
+  for (CacheKind kind : {kCacheBf16, kCacheE4m3}) {
+    const int n = scored_mma_wave(d, G, kind);
+    if (n > most) most = n;
+  }
+  return most;
+}
 
 static size_t workspace_bytes_of(int64_t entries, int Hq, int Hkv, int d) {
   const int G = Hq / Hkv;
-  int most = generic_ctas();
-  for (CacheKind kind : {kCacheBf16, kCacheE4m3}) {
-    const int n = scored_mma_ctas(d, G, kind);
-    if (n > most) most = n;
-  }
-  const size_t rows = (size_t)(most + entries * Hkv) * G;
+  const size_t rows = (size_t)(most_chunks(d, G) + entries * Hkv) * G;
   return before_bytes(entries) + align_up(rows * 4, 256) + rows * d * 4;
 }
 
@@ -406,6 +415,10 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
       (uintptr_t)q % 16 || (uintptr_t)out % 16 || (uintptr_t)ws % 16 || !aligned16(kv.k, dcp) ||
       !aligned16(kv.v, dcp) || (scaled && !aligned16(kv.sc, dcp)))
     return DCP_EUNSUPPORTED;
+  // the most tiles a full table can have: a rank's first and last of each of two runs may be part
+  const int64_t room = (int64_t)kv.max_vb * layout.block_size * dcp;
+  const int64_t tiles = (room / kRows + 4 * dcp) * B * Hkv;
+  if (tiles >= (int64_t(1) << 30)) return DCP_EUNSUPPORTED;
   const size_t need = workspace_bytes_of(entries, Hq, Hkv, d);
   if (!ws || ws_bytes < need) return DCP_EWORKSPACE;
   const int64_t es = dtype == DCP_F32 ? 4 : 2, os = out_dtype == DCP_F32 ? 4 : 2;
@@ -447,11 +460,14 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
   A.k = kv.k, A.v = kv.v, A.sc = kv.sc;
   A.out = out, A.out_dtype = out_dtype, A.out_lse = out_lse, A.err = err;
   char* w = (char*)ws;
-  A.before = (int64_t*)w;
+  A.before = (int32_t*)w;
   w += before_bytes(entries);
   const bool mma = scored_mma_ok(A, kv.kind, dtype == DCP_BF16);
-  A.ctas = mma ? scored_mma_ctas(d, A.G, kv.kind) : generic_ctas();
   A.least = (mma ? 2 : 1) * kScoredWarps;
+  // no more chunks than a full table has
+  const int64_t useful = (tiles + A.least - 1) / A.least;
+  A.ctas = mma ? scored_mma_wave(d, A.G, kv.kind) : generic_ctas();
+  if (A.ctas > useful) A.ctas = useful > 0 ? (int)useful : 1;
   A.part_lse = (float*)w;
   w += align_up((size_t)(A.ctas + entries * Hkv) * A.G * 4, 256);
   A.part_o = (float*)w;

@@ -94,10 +94,10 @@ struct ScoredArgs {
   float* out_lse;            // [entries][Hq] or NULL
   int32_t* err;
   // workspace
-  int64_t* before;           // [entries + 1] tiles of a head in front of an entry, then tiles per CTA
-  float* part_lse;           // [ctas + units][G]
-  float* part_o;             // [ctas + units][G][d]
-  int ctas, least;           // CTAs, and the fewest tiles one is given
+  int32_t* before;           // [entries + 1] tiles of a head in front of an entry, then a chunk's
+  float* part_lse;           // [chunks + units][G]
+  float* part_o;             // [chunks + units][G][d]
+  int ctas, least;           // chunks at most (the grid), and the fewest tiles of one
   __device__ __forceinline__ int entries() const { return apart ? B * S.dcp : B; }
 };
 
@@ -165,113 +165,104 @@ __device__ __forceinline__ int entry_tiles(const ScoredArgs& A, int e, bool coun
 }
 
 // A unit is a key/value head of an entry, its tiles those of the ranks in
-// order.  All units' tiles, end to end (entry by entry, head by head), are cut
-// into runs of `each` tiles, one run a CTA.  The piece of unit u in run i has
-// its partial result at i + u: along the line of tiles either the unit or the
-// run goes up by one from piece to piece, or both, so no two pieces share one.
-struct Run {
-  int64_t t0, t1;   // this CTA's tiles
-  int64_t start;    // first tile of entry e
-  int e, n;         // entry of t0, and its tiles for a head
-  int64_t each;
+// order.  All units' tiles, end to end (entry by entry, head by head), are a line
+// that is cut into chunks of `each` tiles.  The piece of unit u in chunk i has its
+// partial result at i + u: along the line either the unit or the chunk goes up by
+// one from piece to piece, or both, so no two pieces share one.  The host sees
+// to it that the line has fewer than 2^30 tiles.
+struct Line {
+  int all, each;   // tiles, and those of a chunk
+  int per;         // entries that a thread has counted
 };
 
-// A CTA's part of a unit: tiles [k0, k1) of head g of entry e.
-struct Piece {
-  int e, g, k0, k1, n;
-  int64_t start, t;   // first tile of the entry, and the line's tile behind the piece
-};
-
-__device__ __forceinline__ Piece piece_at(const ScoredArgs& A, const Run& run, int64_t t, int e,
-                                          int n, int64_t start) {
-  while (t >= start + (int64_t)n * A.Hkv && e + 1 < A.entries()) {
-    start += (int64_t)n * A.Hkv;
-    n = entry_tiles(A, ++e, false);
-  }
-  Piece p;
-  p.e = e, p.n = n, p.start = start;
-  const int64_t in = t - start;
-  p.g = in < (int64_t(1) << 31) ? (int)((uint32_t)in / (uint32_t)n) : (int)(in / n);
-  p.k0 = (int)(in - (int64_t)p.g * n);
-  p.k1 = (int)min((int64_t)n, p.k0 + (run.t1 - t));
-  p.t = t + (p.k1 - p.k0);
-  return p;
-}
-
-// Every thread of the CTA calls it; all get the same.  The lengths are read by
-// every CTA: a plan of one CTA in front would cost a launch (a call of one
-// request takes some 8 us in all).
+// Every thread of the CTA calls it; all get the same, and s_before[i] is what
+// lies in front of thread i's entries, in tiles of a head.  The lengths are read
+// by every CTA: a plan of one CTA in front would cost a launch (a call of one
+// request takes some 12 us in all).
 template <int kThreads>
-__device__ __forceinline__ Run plan_run(const ScoredArgs& A) {
-  __shared__ int64_t s_sum[kThreads / 32];
-  __shared__ int64_t s_start;
-  __shared__ int s_e, s_n;
+__device__ __forceinline__ Line plan_line(const ScoredArgs& A, int* s_before) {
+  __shared__ int s_sum[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int E = A.entries(), c = (E + kThreads - 1) / kThreads;
-  const int e0 = min(tid * c, E), e1 = min(e0 + c, E);
-  const bool keeps = blockIdx.x == 0;
-  int64_t sum = 0;
-  int n0 = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int n = entry_tiles(A, e, keeps);
-    if (e == e0) n0 = n;
-    sum += n;
-  }
-  int64_t upto = sum;
+  const int E = A.entries();
+  Line line;
+  line.per = (E + kThreads - 1) / kThreads;
+  const int e0 = min(tid * line.per, E), e1 = min(e0 + line.per, E);
+  int sum = 0;
+  for (int e = e0; e < e1; ++e) sum += entry_tiles(A, e, false);
+  int upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += x;
   }
   if (lane == 31) s_sum[warp] = upto;
-  if (tid == 0) {
-    s_e = E;
-    s_n = 0;
-    s_start = 0;
-  }
   __syncthreads();
-  int64_t total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) upto += s_sum[w];
     total += s_sum[w];
   }
-  Run run;
-  const int64_t all = total * A.Hkv;
-  run.each = max((int64_t)A.least, (all + A.ctas - 1) / A.ctas);
-  run.t0 = min(run.each * blockIdx.x, all);
-  run.t1 = min(run.t0 + run.each, all);
-  int64_t before = upto - sum;
-  if (keeps) {   // for the merge
-    for (int e = e0, n = n0; e < e1; ++e) {
-      if (e > e0) n = entry_tiles(A, e, false);
-      A.before[e] = before;
-      before += n;
-    }
-    if (tid == 0) {
-      A.before[E] = total;
-      A.before[E + 1] = run.each;
-    }
-    before = upto - sum;
-  }
-  // the thread that has the entry of t0
-  if (run.t0 < all && run.t0 >= before * A.Hkv && run.t0 < upto * A.Hkv) {
-    for (int e = e0, n = n0; e < e1; ++e) {
-      if (e > e0) n = entry_tiles(A, e, false);
-      if (run.t0 < (before + n) * A.Hkv) {
-        s_e = e;
-        s_n = n;
-        s_start = before * A.Hkv;
-        break;
-      }
-      before += n;
-    }
-  }
+  s_before[tid] = upto - sum;
+  line.all = total * A.Hkv;
+  line.each = max(A.least, (line.all + A.ctas - 1) / A.ctas);
   __syncthreads();
-  run.e = s_e;
-  run.n = s_n;
-  run.start = s_start;
-  return run;
+  return line;
+}
+
+// For the merge (whoever has chunk 0 calls it): what lies in front of each
+// entry, and the chunks' size.  Counts bad lengths.
+template <int kThreads>
+__device__ __forceinline__ void keep_line(const ScoredArgs& A, const Line& line,
+                                          const int* s_before) {
+  const int E = A.entries(), tid = threadIdx.x;
+  const int e0 = min(tid * line.per, E), e1 = min(e0 + line.per, E);
+  int before = s_before[tid];
+  for (int e = e0; e < e1; ++e) {
+    A.before[e] = before;
+    before += entry_tiles(A, e, true);
+  }
+  if (tid == 0) {
+    A.before[E] = line.all / A.Hkv;
+    A.before[E + 1] = line.each;
+  }
+}
+
+// The entries in front of which tile t of the line does not lie: the first of
+// those that one thread has counted.  The whole warp asks for one t.
+template <int kThreads>
+__device__ __forceinline__ void seek_entry(const ScoredArgs& A, const Line& line,
+                                           const int* s_before, int t, int& e, int& start) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i)
+    n += __popc(__ballot_sync(0xffffffffu, s_before[i * 32 + lane] * A.Hkv <= t));
+  e = min((n - 1) * line.per, A.entries() - 1);
+  start = s_before[n - 1] * A.Hkv;
+}
+
+// A chunk's part of a unit: tiles [k0, k1) of the n of head g of entry e.
+struct Piece {
+  int e, g, k0, k1, n;
+  int start, t;   // first tile of the entry, and the line's tile behind the piece
+};
+
+// The piece that begins with tile t, in a chunk that ends with t1; e and start
+// are an entry at or in front of it.
+__device__ __forceinline__ Piece piece_at(const ScoredArgs& A, int t, int t1, int e, int start) {
+  Piece p;
+  int n = entry_tiles(A, e, false);
+  while (t - start >= n * A.Hkv && e + 1 < A.entries()) {
+    start += n * A.Hkv;
+    n = entry_tiles(A, ++e, false);
+  }
+  p.e = e, p.n = n, p.start = start;
+  p.g = (int)((uint32_t)(t - start) / (uint32_t)max(n, 1));
+  p.k0 = t - start - p.g * n;
+  p.k1 = min(n, p.k0 + (t1 - t));
+  p.t = t + (p.k1 - p.k0);
+  return p;
 }
 
 // tanh: by its series (the terms up to y^9, the next is below 2^-26 of y) for
@@ -337,7 +328,7 @@ __device__ __forceinline__ void put_lse(const ScoredArgs& A, const PieceOut& P, 
 // the one for any type and shape (dcp_scored.cu).
 enum CacheKind { kCacheF32, kCacheBf16, kCacheE4m3 };
 bool scored_mma_ok(const ScoredArgs& A, CacheKind kind, bool q_bf16);
-int scored_mma_ctas(int d, int G, CacheKind kind);
+int scored_mma_wave(int d, int G, CacheKind kind);   // CTAs that run at once
 int launch_scored_mma(const ScoredArgs& A, CacheKind kind, cudaStream_t s);
 
 }  // namespace dcp

@@ -65,7 +65,7 @@ struct Shape {
   static constexpr int kStages = kTileBytes < 4096 ? 12288 / (2 * kTileBytes) : 2;
   static constexpr int kPerSm = NT == 1 ? 3 : 2;
   static constexpr int kRing = kScoredWarps * kStages * 2 * kTileBytes;
-  static constexpr int kMeta = kScoredWarps * kStages * (16 + 16 + 8);
+  static constexpr int kMeta = kScoredWarps * kStages * (16 + 16 + 8 + 8);
   static __host__ __device__ constexpr int smem(int G) {
     return 1024 + kRing + kMeta + kScoredWarps * G * (D + 4) * 4;
   }
@@ -85,30 +85,39 @@ constexpr float kLift = 11.f;    // fp16 weights are held times 2^11: up to 2^15
                                  // in full precision down to 2^-25
 constexpr int kScoredStuck = 1 << 20;   // err_count increment for a wait that timed out
 
-// Four warps a CTA, each with a ring of its own for every fourth tile of the
-// CTA's run, filled ahead by TMA over the ends of pieces; a tile's block-table
-// entries are looked up 32 tiles at a time, a tile a lane.  A score is compared
-// with its head's reference only to see whether it passes it by more than 2^4;
-// while none does (one vote), nothing is rescaled and no maximum is shared.
+// Four warps a CTA use tiles, each every fourth one of the CTA's chunk from a ring
+// of its own; a fifth looks the tiles up, 32 at a time and one in each lane, and
+// fills the rings by TMA, a lane for each, over the ends of pieces.  (Each warp
+// filling its own ring had a quarter of its instructions for that, and what
+// bounded the kernel was the length of a warp's chain of instructions.)
+// A score is compared with its head's reference only to see whether it passes it
+// by more than 2^4; while none does (one vote), nothing is rescaled and no
+// maximum is shared.
+constexpr int kScoredThreads = (kScoredWarps + 1) * 32;
+
+__device__ __forceinline__ void sync_users() {   // the warps that use tiles
+  asm volatile("bar.sync 1, %0;" ::"n"(kScoredWarps * 32) : "memory");
+}
+
 template <int D, bool E8, int NT, bool kFormed>
-__global__ void __launch_bounds__(kScoredWarps * 32, Shape<D, E8, NT>::kPerSm)
+__global__ void __launch_bounds__(kScoredThreads, Shape<D, E8, NT>::kPerSm)
 scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ ScoredMaps maps) {
   using Z = Shape<D, E8, NT>;
   constexpr int ST = Z::kStages, TB = Z::kTileBytes, KS = D / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gq = lane >> 2, tq = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * ST * 2 * TB;
-  float* const s_scale = reinterpret_cast<float*>(smem + Z::kRing) + warp * ST * 4;
-  int4* const s_desc = reinterpret_cast<int4*>(smem + Z::kRing + kScoredWarps * ST * 16) + warp * ST;
-  uint64_t* const bars =
-      reinterpret_cast<uint64_t*>(smem + Z::kRing + kScoredWarps * ST * 32) + warp * ST;
-  float* const s_ml = reinterpret_cast<float*>(smem + Z::kRing + Z::kMeta);   // [warps][G][4]
+  constexpr int NS = kScoredWarps * ST;   // stages: tile k of the chunk has stage k % NS
+  const uint32_t ring = smem_u32(smem);
+  float* const s_scale = reinterpret_cast<float*>(smem + Z::kRing);
+  int4* const s_desc = reinterpret_cast<int4*>(smem + Z::kRing + NS * 16);
+  const uint32_t full = smem_u32(smem + Z::kRing + NS * 32), empty = full + NS * 8;
+  float* const s_ml = reinterpret_cast<float*>(smem + Z::kRing + Z::kMeta);   // [G][warps][4]
   float* const s_o = s_ml + kScoredWarps * A.G * 4;                          // [warps][G][D]
-  const uint32_t bar0 = smem_u32(bars);
-  if (lane == 0) {
-    for (int s = 0; s < ST; ++s) mbar_init(bar0 + 8 * s, 1);
+  __shared__ int s_before[kScoredThreads];
+  if (tid < NS) {
+    mbar_init(full + 8 * tid, 1);
+    mbar_init(empty + 8 * tid, 1);
     fence_mbar_init();
   }
   if (tid < A.S.dcp) {
@@ -117,98 +126,122 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
   }
   __syncthreads();
   griddep_wait();                // launched chained: the preceding kernel completed
-  const Run run = plan_run<kScoredWarps * 32>(A);
-  const uint64_t pol = policy_evict_first();
+  const Line line = plan_line<kScoredThreads>(A, s_before);
+  const int chunk = blockIdx.x;
+  const int t0 = (int)min((int64_t)line.each * chunk, (int64_t)line.all);
+  const int t1 = (int)min((int64_t)t0 + line.each, (int64_t)line.all);
+  if (chunk == 0) keep_line<kScoredThreads>(A, line, s_before);
+  int e0, start0;
+  seek_entry<kScoredThreads>(A, line, s_before, t0, e0, start0);
+
+  if (warp == kScoredWarps) {
+    // --- the warp that fills the rings ---
+    const uint64_t pol = policy_evict_first();
+    int we = e0, wstart = start0;
+    int d_row, d_ph, d_info, d_p0;   // this lane's tile
+    auto look_up = [&](int t) {
+      bool todo = t < t1;
+      d_row = -1, d_ph = d_info = d_p0 = 0;
+      const int R = A.apart ? 1 : A.S.dcp;
+      for (;;) {   // entry by entry, a rank's tokens in each lane
+        const int b = A.apart ? we % A.B : we, r0 = A.apart ? we / A.B : 0;
+        RankTokens T = seen_of(A, b, false).on(A.S, r0 + min(lane, R - 1));
+        const int na = T.a_tiles();
+        int upto = lane < R ? na + T.b_tiles() : 0;
+#pragma unroll
+        for (int o = 1; o < DCP_MAX_RANKS; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
+        }
+        const int n = __shfl_sync(0xffffffffu, upto, R - 1);
+        const bool here = todo && t - wstart < n * A.Hkv;
+        int g = 0, left = 0;
+        if (here) {
+          g = (int)((uint32_t)(t - wstart) / (uint32_t)n);
+          left = t - wstart - g * n;
+        }
+        int r = 0;
+        for (int x = 0; x < R - 1; ++x) r += left >= __shfl_sync(0xffffffffu, upto, x);
+        const int up_r = __shfl_sync(0xffffffffu, upto, r), na_r = __shfl_sync(0xffffffffu, na, r);
+        const int a0 = __shfl_sync(0xffffffffu, T.a0, r), a1 = __shfl_sync(0xffffffffu, T.a1, r);
+        const int b0 = __shfl_sync(0xffffffffu, T.b0, r), b1 = __shfl_sync(0xffffffffu, T.b1, r);
+        if (here) {   // first the kept tokens, then the window
+          const int nb_r = (b1 + kRows - 1) / kRows - b0 / kRows;
+          const int k = left - (up_r - na_r - (b1 > b0 ? nb_r : 0));
+          const bool kept = k < na_r;
+          const int lo = kept ? a0 : b0, hi = kept ? a1 : b1;
+          d_p0 = ((lo / kRows) + k - (kept ? 0 : na_r)) * kRows;
+          const int vb = A.S.by_bs.div(d_p0);
+          r += r0;
+          int64_t page = -1;
+          if (vb < A.max_vb)
+            page = __ldg(A.bt + r * A.bt_stride + (int64_t)b * A.max_vb + vb);
+          d_info = max(lo - d_p0, 0) | min(hi - d_p0, kRows) << 8 | r << 16;
+          if (page >= 0 && page < A.nb) {
+            d_ph = (int)(page * A.Hkv + g);
+            d_row = d_ph * A.S.bs + (d_p0 - vb * A.S.bs);
+          }
+          todo = false;
+        }
+        if (!__any_sync(0xffffffffu, todo) || we + 1 >= A.entries()) break;
+        wstart += n * A.Hkv;
+        ++we;
+      }
+    };
+    int st = lane & 3, turn = 0;   // this lane's next stage, and how often it was filled
+    bool dead = false;             // a wait timed out: fill no more
+    for (int k0 = t0; k0 < t1; k0 += 32) {
+      look_up(k0 + lane);
+      for (int i = 0; i < 32 && k0 + i < t1; i += kScoredWarps) {
+        const int from = i + (lane & 3);
+        const int row = __shfl_sync(0xffffffffu, d_row, from);
+        const int ph = __shfl_sync(0xffffffffu, d_ph, from);
+        const int info = __shfl_sync(0xffffffffu, d_info, from);
+        const int p0 = __shfl_sync(0xffffffffu, d_p0, from);
+        if (lane < kScoredWarps && k0 + from < t1 && !dead) {
+          const uint32_t bar = full + 8 * st, dst = ring + st * 2 * TB;
+          const int r = info >> 16;
+          dead = turn > 0 && !mbar_wait(empty + 8 * st, (turn - 1) & 1);
+          if (!dead) {
+            s_desc[st] = make_int4(row, info, p0, 0);
+            if (row >= 0) {
+              mbar_arrive_expect_tx(bar, 2 * TB + (E8 ? 16 : 0));
+#pragma unroll
+              for (int x = 0; x < Z::kBoxes; ++x) {
+                tma_load_2d_hint(dst + x * kRows * 128, &maps.k[r], x * 128, row, bar, pol);
+                tma_load_2d_hint(dst + TB + x * kRows * 128, &maps.v[r], x * 128, row, bar, pol);
+              }
+              if (E8)
+                bulk_load(smem_u32(s_scale + st * 4), (const char*)A.sc.ptr[r] + (int64_t)ph * 16,
+                          16, bar);
+            } else {
+              count_error(A.err);
+              mbar_arrive(bar);
+            }
+          } else if (A.err) {
+            atomicAdd(A.err, kScoredStuck);
+          }
+          st += kScoredWarps;
+          if (st >= NS) {
+            st -= NS;
+            ++turn;
+          }
+        }
+        __syncwarp();
+      }
+    }
+    griddep_launch_dependents();   // as below
+    return;
+  }
+
+  // --- the warps that use them ---
+  const int gq = lane >> 2, tq = lane & 3;
   // what this lane gives ldmatrix of a tile's keys and of its values: the rows of the four
   // 8 x 8 tiles are tokens 0-7 and 8-15 of one chunk and of the next
   const int mi = lane >> 3;
   const uint32_t k_at = Z::at((mi & 1) * 8 + (lane & 7), mi >> 1);
   const uint32_t v_at = E8 ? k_at : Z::at((mi >> 1) * 8 + (lane & 7), mi & 1);
-  const int mine = run.t1 > run.t0 + warp
-                       ? (int)((run.t1 - run.t0 - warp + kScoredWarps - 1) / kScoredWarps)
-                       : 0;
-
-  // --- tiles on their way: this lane's of the 32 looked up ---
-  int we = run.e;
-  int64_t wstart = run.start;
-  int d_row = -1, d_ph = 0, d_info = 0, d_p0 = 0;
-  auto look_up = [&](int j0) {
-    const int64_t t = run.t0 + warp + (int64_t)(j0 + lane) * kScoredWarps;
-    bool todo = t < run.t1;
-    d_row = -1;
-    const int R = A.apart ? 1 : A.S.dcp;
-    for (;;) {   // entry by entry, a rank's tokens in each lane
-      const int b = A.apart ? we % A.B : we, r0 = A.apart ? we / A.B : 0;
-      RankTokens T = seen_of(A, b, false).on(A.S, r0 + min(lane, R - 1));
-      const int na = T.a_tiles();
-      int upto = lane < R ? na + T.b_tiles() : 0;
-#pragma unroll
-      for (int o = 1; o < DCP_MAX_RANKS; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-      }
-      const int n = __shfl_sync(0xffffffffu, upto, R - 1);
-      const int64_t in = t - wstart;
-      const bool here = todo && in < (int64_t)n * A.Hkv;
-      int g = 0, left = 0;
-      if (here) {
-        g = in < (int64_t(1) << 31) ? (int)((uint32_t)in / (uint32_t)n) : (int)(in / n);
-        left = (int)(in - (int64_t)g * n);
-      }
-      int r = 0;
-      for (int x = 0; x < R - 1; ++x) r += left >= __shfl_sync(0xffffffffu, upto, x);
-      const int up_r = __shfl_sync(0xffffffffu, upto, r), na_r = __shfl_sync(0xffffffffu, na, r);
-      const int a0 = __shfl_sync(0xffffffffu, T.a0, r), a1 = __shfl_sync(0xffffffffu, T.a1, r);
-      const int b0 = __shfl_sync(0xffffffffu, T.b0, r), b1 = __shfl_sync(0xffffffffu, T.b1, r);
-      if (here) {   // first the kept tokens, then the window
-        const int nb_r = (b1 + kRows - 1) / kRows - b0 / kRows;
-        const int k = left - (up_r - na_r - (b1 > b0 ? nb_r : 0));
-        const bool kept = k < na_r;
-        const int lo = kept ? a0 : b0, hi = kept ? a1 : b1;
-        d_p0 = ((lo / kRows) + k - (kept ? 0 : na_r)) * kRows;
-        const int vb = A.S.by_bs.div(d_p0);
-        r += r0;
-        const int64_t page =
-            vb < A.max_vb ? (int64_t)__ldg(A.bt + r * A.bt_stride + (int64_t)b * A.max_vb + vb) : -1;
-        d_info = max(lo - d_p0, 0) | min(hi - d_p0, kRows) << 8 | r << 16;
-        if (page >= 0 && page < A.nb) {
-          d_ph = (int)(page * A.Hkv + g);
-          d_row = d_ph * A.S.bs + (d_p0 - vb * A.S.bs);
-        }
-        todo = false;
-      }
-      if (!__any_sync(0xffffffffu, todo) || we + 1 >= A.entries()) break;
-      wstart += (int64_t)n * A.Hkv;
-      ++we;
-    }
-  };
-  bool dead = false;   // a wait timed out: stop waiting and issuing
-  auto issue = [&](int j) {   // the whole warp, for its j-th tile
-    if ((j & 31) == 0) look_up(j);
-    const int row = __shfl_sync(0xffffffffu, d_row, j & 31);
-    const int ph = __shfl_sync(0xffffffffu, d_ph, j & 31);
-    const int info = __shfl_sync(0xffffffffu, d_info, j & 31);
-    const int p0 = __shfl_sync(0xffffffffu, d_p0, j & 31);
-    if (lane == 0 && !dead) {
-      const int st = j % ST, r = info >> 16;
-      const uint32_t bar = bar0 + 8 * st, dst = ring + st * 2 * TB;
-      s_desc[st] = make_int4(row, info, p0, 0);
-      if (row >= 0) {
-        mbar_arrive_expect_tx(bar, 2 * TB + (E8 ? 16 : 0));
-#pragma unroll
-        for (int x = 0; x < Z::kBoxes; ++x) {
-          tma_load_2d_hint(dst + x * kRows * 128, &maps.k[r], x * 128, row, bar, pol);
-          tma_load_2d_hint(dst + TB + x * kRows * 128, &maps.v[r], x * 128, row, bar, pol);
-        }
-        if (E8)
-          bulk_load(smem_u32(s_scale + st * 4), (const char*)A.sc.ptr[r] + (int64_t)ph * 16, 16,
-                    bar);
-      } else {
-        count_error(A.err);
-        mbar_arrive(bar);
-      }
-    }
-  };
+  bool dead = false;   // a wait timed out: wait no more
   // queries as the B operand: what they are in memory, asked for ahead, of head gq (+ 8);
   // in 8 bits in the order of a row of keys in its fragments, dims 4 tq .. 4 tq + 3 of each 16
   uint32_t qb[NT][KS][2];
@@ -235,22 +268,16 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
       }
     }
   };
+  int st = warp, phase = 0;
   Piece at;
-  at.e = run.e, at.n = run.n, at.start = run.start, at.t = run.t0;
-  if (at.t < run.t1) {
-    at = piece_at(A, run, at.t, at.e, at.n, at.start);
+  if (t0 < t1) {
+    at = piece_at(A, t0, t1, e0, start0);
     ask_queries(at);
   }
-  for (int j = 0; j < ST && j < mine; ++j) issue(j);
-
-  // --- pieces ---
-  int seq = 0;
-  for (bool more = run.t0 < run.t1; more;) {
+  int used = t0 + warp;   // this warp's next tile
+  for (bool more = t0 < t1; more;) {
     const int e = at.e, g = at.g, k0 = at.k0, k1 = at.k1, n = at.n;
-    // this warp's tiles of the run that end before the piece's
-    const int upto = at.t > run.t0 + warp
-                         ? (int)((at.t - run.t0 - warp + kScoredWarps - 1) / kScoredWarps)
-                         : 0;
+    const int upto = at.t;
     int last = 0;
     if (kFormed) last = __ldg(A.lens + (A.apart ? e % A.B : e)) - 1;
 
@@ -298,9 +325,8 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
       }
     }
 
-    for (; seq < upto; ++seq) {
-      const int st = seq % ST;
-      if (!dead && !mbar_wait(bar0 + 8 * st, (seq / ST) & 1)) {
+    for (; used < upto; used += kScoredWarps) {
+      if (!dead && !mbar_wait(full + 8 * st, phase)) {
         dead = true;
         if (lane == 0 && A.err) atomicAdd(A.err, kScoredStuck);
       }
@@ -325,6 +351,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
               asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vb + Z::at(row, c)), "r"(0u)
                            : "memory");
           }
+          fence_proxy_async_smem();   // before the next tile is copied over them
           __syncwarp();
         }
         // S^T = K Q^T, in two chains of products
@@ -471,20 +498,22 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
         }
       }
       __syncwarp();
-      if (seq + ST < mine) {
-        if (lane == 0) fence_proxy_async_smem();
-        issue(seq + ST);
+      if (lane == 0) mbar_arrive(empty + 8 * st);
+      st += kScoredWarps;
+      if (st >= NS) {
+        st -= NS;
+        phase ^= 1;
       }
     }
 
     // the next piece, and its queries on their way
     PieceOut P;
     P.whole = k0 == 0 && k1 == n;
-    P.slot = blockIdx.x + (int64_t)e * A.Hkv + g;
+    P.slot = chunk + (int64_t)e * A.Hkv + g;
     P.row = (int64_t)e * A.Hq + g * A.G;
-    more = at.t < run.t1;
+    more = at.t < t1;
     if (more) {
-      at = piece_at(A, run, at.t, at.e, at.n, at.start);
+      at = piece_at(A, at.t, t1, e, at.start);
       ask_queries(at);
     }
 
@@ -516,7 +545,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
           }
         }
       }
-    __syncthreads();
+    sync_users();
     // a head's four numbers of each warp become its four factors
     if (tid < A.G) {
       float4* const ml = reinterpret_cast<float4*>(s_ml) + tid * kScoredWarps;
@@ -541,7 +570,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
       for (int i = 0; i < kScoredWarps; ++i)
         to[i] = w[i].y != 0.f ? ex2_ftz(w[i].z - V) * f : 0.f;
     }
-    __syncthreads();
+    sync_users();
     for (int i = tid; i < A.G * (D / 4); i += kScoredWarps * 32) {
       const float4 f = *reinterpret_cast<const float4*>(s_ml + i / (D / 4) * kScoredWarps * 4);
       const float4* os = reinterpret_cast<const float4*>(s_o) + i;
@@ -563,7 +592,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
         reinterpret_cast<uint2*>((__nv_bfloat16*)A.out + P.row * D)[i] =
             make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
     }
-    __syncthreads();
+    sync_users();
   }
   // Only now may the merge start its launch, and only after its wait the next
   // call: 32 requests called in a row take 204 us each so, 315 where both kernels
@@ -607,7 +636,7 @@ static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
         !encode_rows(&maps.v[r], A.v.ptr[r], Z::kRowBytes, rows))
       return DCP_ECUDA;
   const cudaError_t e = launch_chained(scored_mma_kernel<D, E8, NT, kFormed>, (unsigned)A.ctas,
-                                       kScoredWarps * 32, Z::smem(A.G), s, A, maps);
+                                       kScoredThreads, Z::smem(A.G), s, A, maps);
   return e == cudaSuccess ? launch_status() : launch_status_report(e);
 }
 
@@ -630,7 +659,7 @@ static int one_wave(int G) {
   return num_sms() * (fit < Z::kPerSm ? fit : Z::kPerSm);
 }
 
-int scored_mma_ctas(int d, int G, CacheKind kind) {
+int scored_mma_wave(int d, int G, CacheKind kind) {
   const bool e8 = kind == kCacheE4m3;
   if (d == 64)
     return G <= 8 ? (e8 ? one_wave<64, true, 1>(G) : one_wave<64, false, 1>(G))
