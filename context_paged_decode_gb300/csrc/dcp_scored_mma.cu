@@ -61,8 +61,8 @@ struct Shape {
   static constexpr int kTileBytes = kRows * kRowBytes;       // of keys, and of values
   static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;
   static constexpr int kBoxes = kRowBytes / kBoxBytes;
-  // 12 KB a warp on their way: with 16 KB 32 requests in 8 bits take 200 us, not 195
-  static constexpr int kStages = kTileBytes < 4096 ? 12288 / (2 * kTileBytes) : 2;
+  // 16 KB a warp on their way: with 12 or 8 KB 524288 tokens in 8 bits take 193 or 201 us, not 190
+  static constexpr int kStages = 16384 / (2 * kTileBytes);
   static constexpr int kPerSm = NT == 1 ? 3 : 2;
   static constexpr int kRing = kScoredWarps * kStages * 2 * kTileBytes;
   static constexpr int kMeta = kScoredWarps * kStages * (16 + 16 + 8 + 8);
