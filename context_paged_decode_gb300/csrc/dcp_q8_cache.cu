@@ -23,8 +23,9 @@ struct AppendArgs {
   int32_t* err;
 };
 
+// Numbers 4 i .. 4 i + 3 of 16 bytes.
 template <typename T>
-__device__ __forceinline__ float4 quad(const uint4& x, int i);   // numbers 4 i .. 4 i + 3 of 16 bytes
+__device__ __forceinline__ float4 quad(const uint4& x, int i);
 template <>
 __device__ __forceinline__ float4 quad<float>(const uint4& x, int) {
   return make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z),
@@ -34,6 +35,29 @@ template <>
 __device__ __forceinline__ float4 quad<__nv_bfloat16>(const uint4& x, int i) {
   const uint32_t a = i ? x.z : x.x, b = i ? x.w : x.y;
   return make_float4(bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b));
+}
+
+// 16 bytes of numbers times a power of two (bf16: two at a time, exact but for
+// results below 2^-126, which are 0 in e4m3).
+template <typename T>
+__device__ __forceinline__ uint4 times(const uint4& x, float by);
+template <>
+__device__ __forceinline__ uint4 times<float>(const uint4& x, float by) {
+  return make_uint4(__float_as_uint(__uint_as_float(x.x) * by),
+                    __float_as_uint(__uint_as_float(x.y) * by),
+                    __float_as_uint(__uint_as_float(x.z) * by),
+                    __float_as_uint(__uint_as_float(x.w) * by));
+}
+template <>
+__device__ __forceinline__ uint4 times<__nv_bfloat16>(const uint4& x, float by) {
+  const __nv_bfloat162 b = __float2bfloat162_rn(by);
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), b);
+    w[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // |x| of a finite number, 0 of others.
@@ -138,10 +162,11 @@ q8_append_kernel(const __grid_constant__ AppendArgs A) {
     n = min(Below(A.S, c + q1 - q0).on(A.S, rank) - page0, A.S.bs) - loc0;
     mine = loc == loc0 + rank * A.S.bs / A.S.dcp % n;
   }
-  const int chunks = A.d * (int)sizeof(T) / 16, rows = max(32 / chunks, 1);
-  const int row = lane / chunks, chunk = lane - row * chunks;   // with chunks > 32: row 0
+  // a lane takes what becomes 16 bytes of a row, of several rows
+  constexpr int kLoads = sizeof(T), kEach = kAppendDepth / kLoads;
+  const int chunks = A.d / 16, rows = 32 / chunks, batch = rows * kEach;
+  const int row = lane / chunks, chunk = lane - row * chunks;
   const bool busy = row < rows;
-  constexpr int kOut = 16 / sizeof(T);   // bytes that 16 bytes become
   for (uint32_t todo = __ballot_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
     const int who = __ffs(todo) - 1;
     const int pr = __shfl_sync(0xffffffffu, rank, who), pv = __shfl_sync(0xffffffffu, vb, who);
@@ -151,33 +176,32 @@ q8_append_kernel(const __grid_constant__ AppendArgs A) {
     // the first rows are on their way before the table's answer
     const char* src = (const char*)A.src[which] + (int64_t)h * A.d * sizeof(T);
     const int64_t stride = A.stride[which];
-    auto load = [&](int i, int ch) {   // place pl + i
-      const int64_t tok = pq + (A.S.position(pv, pr, pl + i) - pc);
-      return __ldg(reinterpret_cast<const uint4*>(src + tok * stride) + ch);
-    };
     const int64_t page =
         __ldg(A.bt + pr * A.bt_stride + (int64_t)pb * A.max_vb + pv);
-    uint4 x[kAppendDepth];
-    auto each_row = [&](bool reload, auto&& use) {   // use(register, place, 16 bytes of the row)
-      for (int ch = chunk; ch < chunks; ch += 32) {
-        for (int i0 = 0; i0 < pn; i0 += rows * kAppendDepth) {
-          if (reload) {
+    uint4 x[kEach][kLoads];
+    auto each_row = [&](bool reload, auto&& use) {   // use(16 numbers of a row, its number)
+      for (int i0 = row; i0 < pn + row; i0 += batch) {
+        if (reload) {
 #pragma unroll
-            for (int j = 0; j < kAppendDepth; ++j) {
-              const int i = i0 + j * rows + row;
-              x[j] = busy && i < pn ? load(i, ch) : make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
+          for (int j = 0; j < kEach; ++j) {
+            const int i = i0 + j * rows;
+            const bool have = busy && i < pn;
+            const int64_t tok = have ? pq + (A.S.position(pv, pr, pl + i) - pc) : 0;
+            const uint4* from = reinterpret_cast<const uint4*>(src + tok * stride) + chunk * kLoads;
 #pragma unroll
-          for (int j = 0; j < kAppendDepth; ++j) {
-            const int i = i0 + j * rows + row;
-            if (busy && i < pn) use(x[j], i, ch);
+            for (int k = 0; k < kLoads; ++k) x[j][k] = have ? __ldg(from + k) : make_uint4(0u, 0u, 0u, 0u);
           }
         }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          if (busy && i0 + j * rows < pn) use(x[j], i0 + j * rows);
       }
     };
     uint32_t most = 0;
-    each_row(true, [&](const uint4& y, int, int) { raise<T>(most, y); });
+    each_row(true, [&](const uint4(&y)[kLoads], int) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) raise<T>(most, y[k]);
+    });
     float top = raised<T>(most);
     if (page < 0 || page >= A.nb) {
       if (lane == 0 && h == 0 && which == 0) count_error(A.err);
@@ -189,10 +213,10 @@ q8_append_kernel(const __grid_constant__ AppendArgs A) {
     top = warp_max(top);
     if (top > 3.402823466e38f) {   // infinities do not count
       top = 0.f;
-      each_row(true, [&](const uint4& y, int, int) {
+      each_row(true, [&](const uint4(&y)[kLoads], int) {
 #pragma unroll
-        for (int k = 0; k < kOut / 4; ++k) {
-          const float4 z = quad<T>(y, k);
+        for (int k = 0; k < 4; ++k) {
+          const float4 z = quad<T>(y[k * kLoads / 4], k * kLoads % 4 ? 1 : 0);
           top = fmaxf(top, fmaxf(fmaxf(size_of(z.x), size_of(z.y)),
                                  fmaxf(size_of(z.z), size_of(z.w))));
         }
@@ -203,28 +227,26 @@ q8_append_kernel(const __grid_constant__ AppendArgs A) {
     const float old = held > 0.f && held <= 3.402823466e38f ? held : 0.f;
     const float now = fmaxf(old, scale_for(top));
     const bool grows = old > 0.f && now > old;
-    const bool once = pn <= rows * kAppendDepth && chunks <= 32;   // still in registers
-    const bool power = (__float_as_uint(now) & 0x7fffffu) == 0;
+    const bool once = pn <= batch;   // still in registers
     const float inv = 1.f / now;     // exact for a power of two; others divide
-    auto write = [&](const uint4& y, int i, int ch, auto&& scaled) {
-      uint8_t* to = dst + (int64_t)(pl + i) * A.d + ch * kOut;
-      const uint32_t lo = f32x4_e4m3(scaled(quad<T>(y, 0)));
-      if (kOut == 4)
-        *reinterpret_cast<uint32_t*>(to) = lo;
-      else
-        *reinterpret_cast<uint2*>(to) = make_uint2(lo, f32x4_e4m3(scaled(quad<T>(y, 1))));
-    };
-    if (power)
-      each_row(!once, [&](const uint4& y, int i, int ch) {
-        write(y, i, ch, [&](float4 z) {
-          return make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv);
-        });
+    uint8_t* const to = dst + (int64_t)pl * A.d + chunk * 16;
+    if ((__float_as_uint(now) & 0x7fffffu) == 0)
+      each_row(!once, [&](const uint4(&y)[kLoads], int i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = f32x4_e4m3(quad<T>(times<T>(y[k * kLoads / 4], inv), k * kLoads % 4 ? 1 : 0));
+        *reinterpret_cast<uint4*>(to + i * A.d) = make_uint4(w[0], w[1], w[2], w[3]);
       });
     else
-      each_row(true, [&](const uint4& y, int i, int ch) {
-        write(y, i, ch, [&](float4 z) {
-          return make_float4(z.x / now, z.y / now, z.z / now, z.w / now);
-        });
+      each_row(true, [&](const uint4(&y)[kLoads], int i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 z = quad<T>(y[k * kLoads / 4], k * kLoads % 4 ? 1 : 0);
+          w[k] = f32x4_e4m3(make_float4(z.x / now, z.y / now, z.z / now, z.w / now));
+        }
+        *reinterpret_cast<uint4*>(to + i * A.d) = make_uint4(w[0], w[1], w[2], w[3]);
       });
     if (grows) {   // the page's other places, 4 numbers a lane
       const float by = old / now;
