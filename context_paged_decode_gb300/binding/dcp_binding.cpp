@@ -9,6 +9,8 @@
 // arguments are handled; every step runs in the library's kernels.
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -184,8 +186,9 @@ dcp_layout_t layout_of(PyObject* o) {
                       small(integer_attr(o, NAME("interleave")), "interleave")};
 }
 
+// Memory of the caching allocator, without the way through the dispatcher.
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, dev));
+  return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, dev), std::nullopt));
 }
 
 // Elements [at, ...) of a buffer as a tensor of its own (a fresh one, no view of
@@ -199,16 +202,36 @@ at::Tensor part(const at::Tensor& all, int64_t from, at::IntArrayRef shape, int 
   return t;
 }
 
+// Two tensors of their own in one piece of memory (the second is small beside the
+// first, and a piece takes the allocator 2 us).
+void fresh_two(at::IntArrayRef s0, at::ScalarType t0, at::Tensor& a, at::IntArrayRef s1,
+               at::ScalarType t1, at::Tensor& b, int dev) {
+  const int64_t n0 = c10::multiply_integers(s0) * (int64_t)c10::elementSize(t0),
+                n1 = c10::multiply_integers(s1) * (int64_t)c10::elementSize(t1);
+  const int64_t from = (n0 + 255) / 256 * 256;
+  const at::Tensor all = fresh({from + n1}, at::kByte, dev);
+  auto make = [&](at::IntArrayRef shape, at::ScalarType type, int64_t at_byte) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    t.unsafeGetTensorImpl()->set_storage_offset(at_byte / (int64_t)c10::elementSize(type));
+    return t;
+  };
+  a = make(s0, t0, 0);
+  b = make(s1, t1, from);
+}
+
 // The call's workspace: the caller's, or one for this call alone (the caching
 // allocator keeps it for the work already in its stream).
 struct Workspace {
-  at::Tensor own;
+  void* own = nullptr;
   void* p;
   size_t bytes;
   Workspace(PyObject* o, size_t need, int dev) {
     if (o == Py_None) {
-      own = fresh({(int64_t)(need > 0 ? need : 1)}, at::kByte, dev);
-      p = own.data_ptr();
+      own = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(
+          need > 0 ? need : 1, c10::cuda::getCurrentCUDAStream(dev).stream());
+      p = own;
       bytes = need;
       return;
     }
@@ -217,6 +240,10 @@ struct Workspace {
       refuse("the workspace must be a contiguous tensor on the call's device");
     p = t.data_ptr();
     bytes = t.nbytes();
+  }
+  Workspace(const Workspace&) = delete;
+  ~Workspace() {
+    if (own) c10::cuda::CUDACachingAllocator::raw_delete(own);
   }
 };
 
@@ -779,8 +806,12 @@ PyObject* scored(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const dcp_dtype_t codt = dtype_of(odt);
     int32_t* err = err_ptr(a[13], dev);
     at::Tensor o, l;
-    if (a[10] == Py_None) o = fresh(os, odt, dev);
-    if (a[11] == Py_None) l = fresh(ls, at::kFloat, dev);
+    if (a[10] == Py_None && a[11] == Py_None)
+      fresh_two(os, odt, o, ls, at::kFloat, l, dev);
+    else if (a[10] == Py_None)
+      o = fresh(os, odt, dev);
+    else if (a[11] == Py_None)
+      l = fresh(ls, at::kFloat, dev);
     void* po = a[10] == Py_None ? o.data_ptr() : ptr(a[10], "out", odt, os, dev);
     float* pl = (float*)(a[11] == Py_None ? l.data_ptr() : ptr(a[11], "out_lse", at::kFloat, ls, dev));
     const Workspace ws(a[12], need, dev);
