@@ -55,8 +55,8 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
   __shared__ float s_m[kScoredWarps][HP], s_l[kScoredWarps][HP];
   griddep_wait();                // launched chained: the preceding kernel completed
   __shared__ int s_before[kScoredWarps * 32];
-  const Line line = plan_line<kScoredWarps * 32>(A, s_before);
   const int chunk = blockIdx.x;
+  const Line line = plan_line<kScoredWarps * 32>(A, chunk, s_before);
   if (chunk == 0) keep_line<kScoredWarps * 32>(A, line, s_before);
   const int t0 = min((int64_t)line.each * chunk, (int64_t)line.all);
   const int t1 = min((int64_t)t0 + line.each, (int64_t)line.all);
@@ -114,37 +114,62 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
           }
           left -= nb;
         }
-        for (int i0 = 0; i0 < kRows; i0 += 4) {
-          const int p = p0 + i0 + grp;
-          const int vb = A.S.by_bs.div(p), loc = p - vb * A.S.bs;
-          bool ok = p >= lo && p < hi;
-          int64_t page = -1;
-          if (ok) {
-            page = vb < A.max_vb
-                       ? (int64_t)__ldg(A.bt + r * A.bt_stride + (int64_t)b * A.max_vb + vb)
-                       : -1;
-            ok = page >= 0 && page < A.nb;
-            if (!ok && sub == 0 && h0 == 0) count_error(A.err);
+        // the four tokens that each lane has a share of: their pages, then row by row the keys
+        // and values, each asked for before the row in front of it is used
+        int64_t ph[kRows / 4];
+        int at_vb[kRows / 4], at_loc[kRows / 4];
+        float2 sc[kRows / 4];
+#pragma unroll
+        for (int i = 0; i < kRows / 4; ++i) {
+          const int p = p0 + 4 * i + grp;
+          at_vb[i] = A.S.by_bs.div(p);
+          at_loc[i] = p - at_vb[i] * A.S.bs;
+          ph[i] = -2;
+          if (p >= lo && p < hi)
+            ph[i] = at_vb[i] < A.max_vb
+                        ? (int64_t)__ldg(A.bt + r * A.bt_stride + (int64_t)b * A.max_vb + at_vb[i])
+                        : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kRows / 4; ++i) {
+          if (ph[i] == -1 || ph[i] < -2 || ph[i] >= A.nb) {
+            if (sub == 0 && h0 == 0) count_error(A.err);
+            ph[i] = -2;
           }
-          float4 kk[DI], vv[DI];
-          float ks = 1.f, vs = 1.f;
-          if (ok && kKind == kCacheE4m3) {
-            const float2 s2 = __ldg(reinterpret_cast<const float2*>(A.sc.ptr[r]) +
-                                    (page * A.Hkv + g) * 2);
-            ks = s2.x;
-            vs = s2.y;
-          }
-          const int64_t at = ((page * A.Hkv + g) * A.S.bs + loc) * A.d;
+          if (ph[i] >= 0) ph[i] = ph[i] * A.Hkv + g;
+          sc[i] = make_float2(1.f, 1.f);
+          if (ph[i] >= 0 && kKind == kCacheE4m3)
+            sc[i] = __ldg(reinterpret_cast<const float2*>(A.sc.ptr[r]) + ph[i] * 2);
+        }
+        Raw kn[DI], vn[DI];
+        auto ask = [&](int i) {
+          const int64_t at = (max(ph[i], (int64_t)0) * A.S.bs + at_loc[i]) * A.d;
           const Raw* kr = (const Raw*)((const char*)A.k.ptr[r] + at / 4 * F::kBytes) + sub;
           const Raw* vr = (const Raw*)((const char*)A.v.ptr[r] + at / 4 * F::kBytes) + sub;
+#pragma unroll
+          for (int j = 0; j < DI; ++j) {
+            if (ph[i] >= 0 && j < di) {
+              kn[j] = __ldg(kr + 8 * j);
+              vn[j] = __ldg(vr + 8 * j);
+            }
+          }
+        };
+        ask(0);
+#pragma unroll
+        for (int i0 = 0; i0 < kRows / 4; ++i0) {
+          const bool ok = ph[i0] >= 0;
+          const int vb = at_vb[i0], loc = at_loc[i0];
+          const float ks = sc[i0].x, vs = sc[i0].y;
+          float4 kk[DI], vv[DI];
 #pragma unroll
           for (int i = 0; i < DI; ++i) {
             kk[i] = vv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (ok && i < di) {
-              kk[i] = F::of(__ldg(kr + 8 * i));
-              vv[i] = F::of(__ldg(vr + 8 * i));
+              kk[i] = F::of(kn[i]);
+              vv[i] = F::of(vn[i]);
             }
           }
+          if (i0 + 1 < kRows / 4) ask(i0 + 1);
           const float far = (float)(last - A.S.position(vb, r, loc));
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
@@ -234,16 +259,19 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
 // merge
 // ---------------------------------------------------------------------------
 
-constexpr int kMergeThreads = 256;
-constexpr int kMergeAhead = 8;   // rows a thread asks for at a time
+constexpr int kMergeThreads = 512;
+constexpr int kMergeAhead = 4;     // rows a thread asks for at a time
+constexpr int kMergeKept = 64;     // parts whose weights are kept
 
 // A CTA joins the parts of one unit, in the order of its tiles: the heads' LSE
-// first, then each thread four values of a head, the parts shared out to groups
-// of threads that are summed in their order.  Units that one CTA of the main
-// kernel had whole are done already; units without a tile get zeros here.
+// and the parts' weights first, a head a warp, while the first rows are on their
+// way; then each thread four values of a head, the parts shared out to groups of
+// threads that are summed in their order.  Units that one CTA of the main kernel
+// had whole are done already; units without a tile get zeros here.  Bound by two
+// dependent loads and the launch: 3 us for 12 parts of 4 heads of 128.
 __global__ void __launch_bounds__(kMergeThreads)
 scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
-  __shared__ float s_lse[16], s_weight[16];
+  __shared__ float s_lse[16], s_keep[16], s_weight[16][kMergeKept];
   __shared__ __align__(16) float4 s_acc[kMergeThreads];
   griddep_wait();
   griddep_launch_dependents();   // the next call's first kernel may start its launch
@@ -255,34 +283,37 @@ scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
   if (parts == 1) return;
   const int64_t slot = (int64_t)i0 + u;
   const int lane = tid & 31, warp = tid >> 5;
-  // the first rows are on their way before the LSE
   const int quads = A.d / 4, cols = A.G * quads;
   const int groups = max(kMergeThreads / cols, 1);
   const int grp = min(tid / cols, groups);   // the last threads may have no group
+  const int c_first = tid - grp * cols;
   const float4* const po = reinterpret_cast<const float4*>(A.part_o + slot * A.G * A.d);
   float4 y[kMergeAhead];
-  const int c_first = tid - grp * cols;
-  if (grp < groups && c_first < cols) {
+  auto ask = [&](int i, int c) {
 #pragma unroll
     for (int j = 0; j < kMergeAhead; ++j)
-      if (grp + j * groups < parts) y[j] = po[(int64_t)(grp + j * groups) * cols + c_first];
-  }
+      if (i + j * groups < parts) y[j] = po[(int64_t)(i + j * groups) * cols + c];
+  };
+  if (grp < groups && c_first < cols) ask(grp, c_first);
   for (int hh = warp; hh < A.G; hh += kMergeThreads / 32) {
     const float* pl = A.part_lse + slot * A.G + hh;
-    float m = -INFINITY, s = 0.f;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, pl[(int64_t)i * A.G]);
+    const float x0 = lane < parts ? pl[(int64_t)lane * A.G] : -INFINITY;
+    const float x1 = lane + 32 < parts ? pl[(int64_t)(lane + 32) * A.G] : -INFINITY;
+    float m = fmaxf(x0, x1);
+    for (int i = lane + 64; i < parts; i += 32) m = fmaxf(m, pl[(int64_t)i * A.G]);
     m = warp_max(m);
-    for (int i = lane; i < parts; i += 32) {
-      const float x = pl[(int64_t)i * A.G];
-      if (x != -INFINITY) s += expf(x - m);
-    }
+    auto weigh = [&](float x, float ref) { return x == -INFINITY ? 0.f : expf(x - ref); };
+    float s = weigh(x0, m) + weigh(x1, m);
+    for (int i = lane + 64; i < parts; i += 32) s += weigh(pl[(int64_t)i * A.G], m);
     s = warp_sum(s);
+    float keep, lse = s == 0.f ? -INFINITY : m + logf(s);
+    const float all = with_sink(A.sink, g * A.G + hh, lse, keep);
+    s_weight[hh][lane] = weigh(x0, lse) * keep;
+    s_weight[hh][lane + 32] = weigh(x1, lse) * keep;
     if (lane == 0) {
-      float weight, lse = s == 0.f ? -INFINITY : m + logf(s);
       s_lse[hh] = lse;
-      lse = with_sink(A.sink, g * A.G + hh, lse, weight);
-      s_weight[hh] = weight;
-      if (A.out_lse) A.out_lse[(int64_t)e * A.Hq + g * A.G + hh] = lse;
+      s_keep[hh] = keep;
+      if (A.out_lse) A.out_lse[(int64_t)e * A.Hq + g * A.G + hh] = all;
     }
   }
   __syncthreads();
@@ -292,20 +323,20 @@ scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int hh = mine ? c / quads : 0;
     if (mine) {
-      const float lse = s_lse[hh];
-      const float* pl = A.part_lse + slot * A.G + hh;
       for (int i = grp; i < parts; i += kMergeAhead * groups) {
-        if (c0 > 0 || i > grp) {
-#pragma unroll
-          for (int j = 0; j < kMergeAhead; ++j)
-            if (i + j * groups < parts) y[j] = po[(int64_t)(i + j * groups) * cols + c];
-        }
+        if (c0 > 0 || i > grp) ask(i, c);
 #pragma unroll
         for (int j = 0; j < kMergeAhead; ++j) {
-          if (i + j * groups >= parts) continue;
-          const float x = pl[(int64_t)(i + j * groups) * A.G];
-          if (x == -INFINITY) continue;
-          const float w = expf(x - lse);
+          const int p = i + j * groups;
+          if (p >= parts) continue;
+          float w;
+          if (p < kMergeKept) {
+            w = s_weight[hh][p];
+          } else {
+            const float x = A.part_lse[(slot + p) * A.G + hh];
+            w = x == -INFINITY ? 0.f : expf(x - s_lse[hh]) * s_keep[hh];
+          }
+          if (w == 0.f) continue;   // a part that saw nothing
           acc.x = fmaf(w, y[j].x, acc.x);
           acc.y = fmaf(w, y[j].y, acc.y);
           acc.z = fmaf(w, y[j].z, acc.z);
@@ -318,14 +349,12 @@ scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
       __syncthreads();
       if (tid < cols)
         for (int j = 1; j < groups; ++j) {
-          const float4 y = s_acc[tid + j * cols];
-          acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
+          const float4 z = s_acc[tid + j * cols];
+          acc.x += z.x, acc.y += z.y, acc.z += z.z, acc.w += z.w;
         }
     }
     if (mine && grp == 0) {
-      const float w = s_weight[hh];
       const int64_t at = (int64_t)e * A.Hq * quads + (int64_t)g * cols + c;
-      acc = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
       if (A.out_dtype == DCP_F32)
         reinterpret_cast<float4*>(A.out)[at] = acc;
       else

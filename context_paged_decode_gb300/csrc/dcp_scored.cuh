@@ -180,7 +180,7 @@ struct Line {
 // by every CTA: a plan of one CTA in front would cost a launch (a call of one
 // request takes some 12 us in all).
 template <int kThreads>
-__device__ __forceinline__ Line plan_line(const ScoredArgs& A, int* s_before) {
+__device__ __forceinline__ Line plan_line(const ScoredArgs& A, int chunk, int* s_before) {
   __shared__ int s_sum[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = A.entries();
@@ -188,7 +188,7 @@ __device__ __forceinline__ Line plan_line(const ScoredArgs& A, int* s_before) {
   line.per = (E + kThreads - 1) / kThreads;
   const int e0 = min(tid * line.per, E), e1 = min(e0 + line.per, E);
   int sum = 0;
-  for (int e = e0; e < e1; ++e) sum += entry_tiles(A, e, false);
+  for (int e = e0; e < e1; ++e) sum += entry_tiles(A, e, chunk == 0);   // counts bad lengths
   int upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -210,8 +210,8 @@ __device__ __forceinline__ Line plan_line(const ScoredArgs& A, int* s_before) {
   return line;
 }
 
-// For the merge (whoever has chunk 0 calls it): what lies in front of each
-// entry, and the chunks' size.  Counts bad lengths.
+// For the merge (the CTA of chunk 0 calls it): what lies in front of each entry,
+// and the chunks' size.
 template <int kThreads>
 __device__ __forceinline__ void keep_line(const ScoredArgs& A, const Line& line,
                                           const int* s_before) {
@@ -220,7 +220,7 @@ __device__ __forceinline__ void keep_line(const ScoredArgs& A, const Line& line,
   int before = s_before[tid];
   for (int e = e0; e < e1; ++e) {
     A.before[e] = before;
-    before += entry_tiles(A, e, true);
+    if (e + 1 < e1) before += entry_tiles(A, e, false);
   }
   if (tid == 0) {
     A.before[E] = line.all / A.Hkv;

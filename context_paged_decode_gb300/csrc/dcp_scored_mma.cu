@@ -126,8 +126,8 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
   }
   __syncthreads();
   griddep_wait();                // launched chained: the preceding kernel completed
-  const Line line = plan_line<kScoredThreads>(A, s_before);
   const int chunk = blockIdx.x;
+  const Line line = plan_line<kScoredThreads>(A, chunk, s_before);
   const int t0 = (int)min((int64_t)line.each * chunk, (int64_t)line.all);
   const int t1 = (int)min((int64_t)t0 + line.each, (int64_t)line.all);
   if (chunk == 0) keep_line<kScoredThreads>(A, line, s_before);
