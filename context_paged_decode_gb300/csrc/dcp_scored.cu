@@ -114,52 +114,49 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
           }
           left -= nb;
         }
-        // the four tokens that each lane has a share of: their pages, then row by row the keys
-        // and values, each asked for before the row in front of it is used
-        int64_t ph[kRows / 4];
-        int at_vb[kRows / 4], at_loc[kRows / 4];
-        float2 sc[kRows / 4];
-#pragma unroll
-        for (int i = 0; i < kRows / 4; ++i) {
-          const int p = p0 + 4 * i + grp;
-          at_vb[i] = A.S.by_bs.div(p);
-          at_loc[i] = p - at_vb[i] * A.S.bs;
-          ph[i] = -2;
-          if (p >= lo && p < hi)
-            ph[i] = at_vb[i] < A.max_vb
-                        ? (int64_t)__ldg(A.bt + r * A.bt_stride + (int64_t)b * A.max_vb + at_vb[i])
-                        : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < kRows / 4; ++i) {
-          if (ph[i] == -1 || ph[i] < -2 || ph[i] >= A.nb) {
-            if (sub == 0 && h0 == 0) count_error(A.err);
-            ph[i] = -2;
+        // a token's page in each lane (twice); then the tokens four at a time, each asked for
+        // before the one in front of it is used
+        const int mine = p0 + (lane & (kRows - 1));
+        const int my_vb = A.S.by_bs.div(mine), my_loc = mine - my_vb * A.S.bs;
+        int64_t my_ph = -1;
+        float2 my_sc = make_float2(1.f, 1.f);
+        if (mine >= lo && mine < hi) {
+          if (my_vb < A.max_vb)
+            my_ph = __ldg(A.bt + r * A.bt_stride + (int64_t)b * A.max_vb + my_vb);
+          if (my_ph < 0 || my_ph >= A.nb) {
+            my_ph = -1;
+            if (lane < kRows && h0 == 0) count_error(A.err);
+          } else {
+            my_ph = my_ph * A.Hkv + g;
+            if (kKind == kCacheE4m3)
+              my_sc = __ldg(reinterpret_cast<const float2*>(A.sc.ptr[r]) + my_ph * 2);
           }
-          if (ph[i] >= 0) ph[i] = ph[i] * A.Hkv + g;
-          sc[i] = make_float2(1.f, 1.f);
-          if (ph[i] >= 0 && kKind == kCacheE4m3)
-            sc[i] = __ldg(reinterpret_cast<const float2*>(A.sc.ptr[r]) + ph[i] * 2);
         }
+        const float my_far = (float)(last - A.S.position(my_vb, r, my_loc));
         Raw kn[DI], vn[DI];
+        bool ok_next = false;
         auto ask = [&](int i) {
-          const int64_t at = (max(ph[i], (int64_t)0) * A.S.bs + at_loc[i]) * A.d;
+          const int64_t ph = __shfl_sync(0xffffffffu, my_ph, i + grp);
+          const int loc = __shfl_sync(0xffffffffu, my_loc, i + grp);
+          const int64_t at = (ph * A.S.bs + loc) * A.d;
           const Raw* kr = (const Raw*)((const char*)A.k.ptr[r] + at / 4 * F::kBytes) + sub;
           const Raw* vr = (const Raw*)((const char*)A.v.ptr[r] + at / 4 * F::kBytes) + sub;
+          ok_next = ph >= 0;
 #pragma unroll
           for (int j = 0; j < DI; ++j) {
-            if (ph[i] >= 0 && j < di) {
+            if (ok_next && j < di) {
               kn[j] = __ldg(kr + 8 * j);
               vn[j] = __ldg(vr + 8 * j);
             }
           }
         };
         ask(0);
-#pragma unroll
-        for (int i0 = 0; i0 < kRows / 4; ++i0) {
-          const bool ok = ph[i0] >= 0;
-          const int vb = at_vb[i0], loc = at_loc[i0];
-          const float ks = sc[i0].x, vs = sc[i0].y;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kRows; i0 += 4) {
+          const bool ok = ok_next;
+          const float ks = __shfl_sync(0xffffffffu, my_sc.x, i0 + grp);
+          const float vs = __shfl_sync(0xffffffffu, my_sc.y, i0 + grp);
+          const float far = __shfl_sync(0xffffffffu, my_far, i0 + grp);
           float4 kk[DI], vv[DI];
 #pragma unroll
           for (int i = 0; i < DI; ++i) {
@@ -169,8 +166,7 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
               vv[i] = F::of(vn[i]);
             }
           }
-          if (i0 + 1 < kRows / 4) ask(i0 + 1);
-          const float far = (float)(last - A.S.position(vb, r, loc));
+          if (i0 + 4 < kRows) ask(i0 + 4);
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
             float dot = 0.f;
@@ -375,7 +371,8 @@ static cudaError_t launch_generic(const ScoredArgs& A, bool q_bf16, cudaStream_t
   const unsigned grid = (unsigned)A.ctas, block = kScoredWarps * 32;
   return A.G == 1
              ? launch_chained(scored_generic_kernel<kKind, DI, 1>, grid, block, 0, s, A, q_bf16)
-             : launch_chained(scored_generic_kernel<kKind, DI, 4>, grid, block, 0, s, A, q_bf16);
+             : launch_chained(scored_generic_kernel<kKind, DI, DI == 8 ? 2 : 4>, grid, block, 0, s, A,
+                              q_bf16);   // 8 values a lane of 2 heads fit into registers
 }
 
 template <int kKind>
