@@ -143,6 +143,23 @@ def test_pages_that_are_not_there(lib):
         assert err.item() == 1
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 150])
+def test_many_requests(lib, B):
+    """Short runs of many requests, long stretches of which have none."""
+    rng = np.random.default_rng(B)
+    T = rng.choice([0, 1, 1, 2, 40], B)
+    T[3:3 + B // 2] = 0
+    ctx = rng.integers(0, 60, B)
+    c = Cache(lib, rng, 1, 32, 2, 16, 1, [int(x + 2 * t) for x, t in zip(ctx, T)])
+    for i in range(2):
+        start = np.r_[0, np.cumsum(T)]
+        k, v = rows(rng, int(start[-1]), 1, 32, BF16, True, (1.0, 20.0))
+        at = [int(x + i * t) for x, t in zip(ctx, T)]
+        c.append(k, v, start, at)
+        c.model(k, v, start, at)
+        c.check()
+
+
 def test_odd_numbers(lib):
     """Zeros, infinities, NaN, the smallest and the largest numbers."""
     rng = np.random.default_rng(7)

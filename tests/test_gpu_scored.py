@@ -316,6 +316,67 @@ def test_captured_with_changing_lengths(lib, cache):
     assert err.item() == 0
 
 
+@pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
+def test_requests_that_see_nothing(lib, cache):
+    """A document that begins at or behind the end; with and without a sink."""
+    q = F32 if cache == F32 else BF16
+    for sink in (False, True):
+        p = Problem(lib, cache, q, 8, 2, 128, 2, 16, 1, [70, 40, 33], sink=sink)
+        first = torch.tensor([70, 1000, -3], dtype=torch.int32, device="cuda")
+        p.form = lib.Scores(first=first, window=20)
+        out, lse = p.run()
+        assert (out[:2] == 0).all()
+        want = p.dsink.expand(2, -1) if sink else torch.full_like(lse[:2], -np.inf)
+        assert torch.equal(lse[:2], want)
+        x, k, v = p.rows[2]
+        p.rows[2] = (x[13:], k[:, 13:], v[:, 13:])
+        p.check(out, lse, skip=(0, 1))
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
+def test_more_requests_than_threads(lib, cache):
+    """Hundreds of requests, some empty, so that a thread counts several; and their ranks apart."""
+    q = F32 if cache == F32 else BF16
+    rng = np.random.default_rng(3)
+    lens = [int(n) for n in rng.choice([0, 0, 1, 5, 16, 40, 100], 700)]
+    lens[350] = 900
+    p = Problem(lib, cache, q, 2, 1, 64, 2, 16, 1, lens, alibi=True)
+    out, lse = p.run()
+    p.check(out, lse)
+    po, pl = p.partial(p.layout, p.q, p.kv, p.dlens, p.scale, p.form)
+    for r in range(2):
+        p.check(po[r], pl[r], rank=r)
+
+
+def test_calls_at_once(lib):
+    """Calls on several streams, each with a workspace of its own, beside one another."""
+    ps = [Problem(lib, c, BF16, 8, 2, 128, 2, 16, 1, [900, 20], seed=i, cap=30.0)
+          for i, c in enumerate((E4M3, BF16, E4M3, BF16))]
+    want = [p.run() for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for p, s in zip(ps, streams):
+            got.append((p, p.run(stream=s)))
+    torch.cuda.synchronize()
+    for p, (o, l) in got:
+        w = want[ps.index(p)]
+        assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+def test_outputs_are_tensors_of_their_own(lib):
+    p = Problem(lib, E4M3, BF16, 3, 1, 64, 1, 16, 1, [50])
+    out, lse = p.run()
+    assert out.is_contiguous() and lse.is_contiguous() and out._base is None and lse._base is None
+    o, l = out.clone(), lse.clone()
+    out.zero_()
+    assert torch.equal(lse, l)
+    out.copy_(o)
+    lse.zero_()
+    assert torch.equal(out, o)
+
+
 def test_another_stream(lib):
     p = Problem(lib, E4M3, BF16, 8, 2, 128, 2, 16, 1, [700, 20])
     want = p.run()
