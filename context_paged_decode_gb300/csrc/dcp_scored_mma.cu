@@ -83,6 +83,7 @@ struct Shape {
 constexpr float kSlack = 4.f;    // how far a score may pass its reference, in powers of two
 constexpr float kLift = 11.f;    // fp16 weights are held times 2^11: up to 2^15 with the slack, and
                                  // in full precision down to 2^-25
+constexpr float kNone = -3e38f;  // a reference before there is a score
 constexpr int kScoredStuck = 1 << 20;   // err_count increment for a wait that timed out
 
 // Four warps a CTA use tiles, each every fourth one of the CTA's chunk from a ring
@@ -311,17 +312,18 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
         slope[x][i] = kFormed && A.slopes && h < A.G ? __ldg(A.slopes + g * A.G + h) : 0.f;
       }
     }
-    // references: of the scores (ref) and, in 8 bits, of scores and scales together
-    // (vref); thr and vthr are what may not be passed
-    float o[NT][KS][4], l[NT][2], ref[NT][2], thr[NT][2], vref[NT][2], vthr[NT][2];
+    // references: of the scores (ref) and, in 8 bits, of scores and the values' scales together
+    // (the score vref and the scale 2^vlift, apart: their sum would lose the scale beside a
+    // score beyond 2^24)
+    float o[NT][KS][4], l[NT][2], ref[NT][2], vref[NT][2], vlift[NT][2];
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[x][i][0] = o[x][i][1] = o[x][i][2] = o[x][i][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        l[x][i] = ref[x][i] = vref[x][i] = 0.f;
-        thr[x][i] = vthr[x][i] = -INFINITY;
+        l[x][i] = vlift[x][i] = 0.f;
+        ref[x][i] = vref[x][i] = kNone;
       }
     }
 
@@ -421,9 +423,11 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            over |= fmaxf(s[x][h], s[x][h + 2]) >
-                    (E8 ? fminf(thr[x][h], vthr[x][h] - vlog) : thr[x][h]);
+          for (int h = 0; h < 2; ++h) {
+            const float m = fmaxf(s[x][h], s[x][h + 2]);
+            over |= m - ref[x][h] > kSlack;
+            if (E8) over |= m - vref[x][h] > kSlack - vlog + vlift[x][h];
+          }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int x = 0; x < NT; ++x)
@@ -434,19 +438,17 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
               float down = 1.f;
-              if (m > thr[x][h]) {   // never for a tile that sees nothing
-                down = thr[x][h] == -INFINITY ? 0.f : ex2_ftz(ref[x][h] - m);
+              if (m - ref[x][h] > kSlack) {   // never for a tile that sees nothing
+                down = ex2_ftz(ref[x][h] - m);
                 l[x][h] *= down;
                 ref[x][h] = m;
-                thr[x][h] = m + kSlack;
               }
               if (E8) {
                 down = 1.f;
-                const float mv = m + vlog;
-                if (mv > vthr[x][h]) {
-                  down = vthr[x][h] == -INFINITY ? 0.f : ex2_ftz(vref[x][h] - mv);
-                  vref[x][h] = mv;
-                  vthr[x][h] = mv + kSlack;
+                if (m - vref[x][h] > kSlack - vlog + vlift[x][h]) {
+                  down = ex2_ftz((vref[x][h] - m) + (vlift[x][h] - vlog));
+                  vref[x][h] = m;
+                  vlift[x][h] = vlog;
                 }
               }
 #pragma unroll
@@ -466,7 +468,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
             const int h = i & 1;
             p[i] = ex2_ftz(s[x][i] - ref[x][h]);
             l[x][h] += p[i];
-            if (E8) p[i] = ex2_ftz(s[x][i] + (vlog + kLift - vref[x][h]));
+            if (E8) p[i] = ex2_ftz((s[x][i] - vref[x][h]) + (vlog - vlift[x][h] + kLift));
           }
           pb[x][0] = transposed8(E8 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
           pb[x][1] = transposed8(E8 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
@@ -528,12 +530,10 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int hh = 2 * tq + h + 8 * x;
         if (hh >= A.G) continue;
-        if (gq == 0) {
-          const bool any = thr[x][h] != -INFINITY;
+        if (gq == 0)
           *reinterpret_cast<float4*>(s_ml + (hh * kScoredWarps + warp) * 4) =
-              make_float4(any ? ref[x][h] : -INFINITY, sum,
-                          !any ? -INFINITY : E8 ? vref[x][h] - kLift : ref[x][h], 0.f);
-        }
+              E8 ? make_float4(ref[x][h], sum, vref[x][h], vlift[x][h] - kLift)
+                 : make_float4(ref[x][h], sum, ref[x][h], 0.f);
         float* os = s_o + (warp * A.G + hh) * D;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
@@ -549,13 +549,12 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
     // a head's four numbers of each warp become its four factors
     if (tid < A.G) {
       float4* const ml = reinterpret_cast<float4*>(s_ml) + tid * kScoredWarps;
-      float M = -INFINITY, V = -INFINITY, Ls = 0.f;
+      float M = kNone, Ls = 0.f;
       float4 w[kScoredWarps];
 #pragma unroll
       for (int i = 0; i < kScoredWarps; ++i) {
         w[i] = ml[i];
         M = fmaxf(M, w[i].x);
-        V = fmaxf(V, w[i].z);
       }
 #pragma unroll
       for (int i = 0; i < kScoredWarps; ++i)   // nothing seen: no part (a sum that is NaN has one)
@@ -564,11 +563,10 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
       float weight = 1.f, lse = any ? (M + log2f(Ls)) * kLn2 : -INFINITY;
       if (P.whole) lse = with_sink(A.sink, g * A.G + tid, lse, weight);
       put_lse(A, P, tid, lse);
-      const float f = any ? exp2f(V - M) / Ls * weight : 0.f;
       float* const to = reinterpret_cast<float*>(ml);
 #pragma unroll
       for (int i = 0; i < kScoredWarps; ++i)
-        to[i] = w[i].y != 0.f ? ex2_ftz(w[i].z - V) * f : 0.f;
+        to[i] = any && w[i].y != 0.f ? exp2f((w[i].z - M) + w[i].w) / Ls * weight : 0.f;
     }
     sync_users();
     for (int i = tid; i < A.G * (D / 4); i += kScoredWarps * 32) {

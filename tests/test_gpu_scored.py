@@ -415,3 +415,29 @@ def test_refusals(lib):
         lib.q8_decode_gqa(L, p.q, p.kv, p.dlens, float("inf"))
     with pytest.raises(lib.DcpError):
         lib.q8_decode_gqa(lib.Layout(2, 32, 1), p.q, p.kv, p.dlens, 1.0)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e6, -1e9, 1e30])
+def test_any_scale(lib, cache, scale):
+    """Scores of nothing, below 0, and so large that one token has all the weight."""
+    q = F32 if cache == F32 else BF16
+    p = Problem(lib, cache, q, 4, 2, 64, 2, 16, 1, [150, 33, 1], sink=scale == 0.0)
+    p.scale = scale
+    out, lse = p.run()
+    if abs(scale) < 1:
+        p.check(out, lse)
+        return
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b in range(3):
+        x, k, v = p.rows[b]
+        for h in range(4):
+            t = np.sort(k[h // 2] @ p.q64[b, h])
+            t = (t if scale > 0 else t[::-1])
+            # the two largest are apart by more than the error of a product of 64 terms
+            size = (np.abs(k[h // 2]) @ np.abs(p.q64[b, h])).max() * 68 * 2.0 ** -24
+            best = (k[h // 2] @ p.q64[b, h] * np.sign(scale)).argmax()
+            assert abs(l[b, h] - abs(t[-1] * scale) * np.sign(t[-1] * scale)) <= 2 * size * abs(scale)
+            if len(t) > 1 and abs(t[-1] - t[-2]) > 2 * size + 100 / abs(scale):
+                assert (np.abs(o[b, h] - v[h // 2][best]) <= np.abs(v[h // 2][best]) * 2.0 ** -7).all()
