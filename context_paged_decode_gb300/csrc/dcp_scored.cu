@@ -42,17 +42,24 @@ struct Four<kCacheE4m3> {
   static __device__ __forceinline__ float4 of(Raw x) { return e4m3x4_f32(x); }
 };
 
-// Eight lanes take a token, so a warp takes four at a time and sums a score by
-// three shuffles; HP heads of the unit in one pass over the tokens.  The
-// products run in fp32 on the CUDA cores.
+// CTAs that run at once, by their registers (the kernel's launch bounds).
+constexpr int generic_per_sm(int di) { return di == 8 ? 2 : di == 4 ? 3 : 4; }
+
+// Eight lanes take a token, so a warp takes four at a time; HP heads of the unit
+// in one pass over the tokens.  The products run in fp32 on the CUDA cores.  The
+// heads' sums over the lanes are exchanged so that each lane gets one head's
+// score, which it forms alone, and the weights go round again: with every score
+// formed by all eight lanes two requests of up to 2048 tokens, 32/8 heads of 128 in
+// fp32, took 40 us (@@).
 template <int kKind, int DI, int HP>
-__global__ void __launch_bounds__(kScoredWarps * 32)
+__global__ void __launch_bounds__(kScoredWarps * 32, generic_per_sm(DI))
 scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
   using F = Four<kKind>;
   using Raw = typename F::Raw;
   __shared__ __align__(16) float s_q[HP][DI * 32];
-  __shared__ __align__(16) float s_o[kScoredWarps][HP][DI * 32];
-  __shared__ float s_m[kScoredWarps][HP], s_l[kScoredWarps][HP];
+  constexpr int kParts = kScoredWarps * 4;   // sums of their own: four tokens of each warp
+  __shared__ __align__(16) float4 s_o[kParts][HP][DI * 8];
+  __shared__ float s_m[kParts][HP], s_l[kParts][HP];
   griddep_wait();                // launched chained: the preceding kernel completed
   __shared__ int s_before[kScoredWarps * 32];
   const int chunk = blockIdx.x;
@@ -87,16 +94,15 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
                               : ((const float*)A.q)[at];
       }
       __syncthreads();
-      float slope[HP], m[HP], l[HP];
+      const int own = sub & (HP - 1);   // this lane's head
+      const float slope =
+          A.slopes && h0 + own < A.G ? __ldg(A.slopes + g * A.G + h0 + own) : 0.f;
+      float m = kNone, l = 0.f;
       float4 o[HP][DI];
 #pragma unroll
-      for (int h = 0; h < HP; ++h) {
-        slope[h] = A.slopes && h0 + h < A.G ? __ldg(A.slopes + g * A.G + h0 + h) : 0.f;
-        m[h] = -INFINITY;
-        l[h] = 0.f;
+      for (int h = 0; h < HP; ++h)
 #pragma unroll
         for (int i = 0; i < DI; ++i) o[h][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
       for (int k = k0 + warp; k < k1; k += kScoredWarps) {
         // the k-th tile: rank by rank, first the kept tokens and then the window
         int r = r0, left = k, p0 = 0, lo = 0, hi = 0;
@@ -167,85 +173,108 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
             }
           }
           if (i0 + 4 < kRows) ask(i0 + 4);
+          float dot[HP];
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
-            float dot = 0.f;
+            dot[h] = 0.f;
 #pragma unroll
             for (int i = 0; i < DI; ++i) {
               if (i < di) {
                 const float4 q4 = *reinterpret_cast<const float4*>(&s_q[h][(sub + 8 * i) * 4]);
-                dot = fmaf(q4.x, kk[i].x, dot);
-                dot = fmaf(q4.y, kk[i].y, dot);
-                dot = fmaf(q4.z, kk[i].z, dot);
-                dot = fmaf(q4.w, kk[i].w, dot);
+                dot[h] = fmaf(q4.x, kk[i].x, dot[h]);
+                dot[h] = fmaf(q4.y, kk[i].y, dot[h]);
+                dot[h] = fmaf(q4.z, kk[i].z, dot[h]);
+                dot[h] = fmaf(q4.w, kk[i].w, dot[h]);
               }
             }
-            dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-            dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-            dot += __shfl_xor_sync(0xffffffffu, dot, 4);
-            if (!ok) continue;
-            const float x = formed(A, dot * ks * A.scale, slope[h], far);
-            const float mn = fmaxf(m[h], x);
-            const float ref = mn == -INFINITY ? 0.f : mn;
-            const float a = exp2f(m[h] - ref), w = exp2f(x - ref), wv = w * vs;
-            m[h] = mn;
-            l[h] = l[h] * a + w;
+          }
+          // the sum over the eight lanes of head `own`: two neighbours share out the heads by
+          // pairs, then pairs of lanes by twos
+#pragma unroll
+          for (int step = 1; step < HP; step *= 2) {
+            const bool up = sub & step;
+#pragma unroll
+            for (int h = 0; h < HP / (2 * step); ++h) {
+              const float give = up ? dot[2 * h] : dot[2 * h + 1];
+              dot[h] = (up ? dot[2 * h + 1] : dot[2 * h]) + __shfl_xor_sync(0xffffffffu, give, step);
+            }
+          }
+#pragma unroll
+          for (int step = HP; step < 8; step *= 2) dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], step);
+          const float x = ok ? formed(A, dot[0] * ks * A.scale, slope, far) : -INFINITY;
+          const bool over = x - m > kSlack;
+          if (__any_sync(0xffffffffu, over)) {
+            const float down = over ? exp2f(m - x) : 1.f;
+            if (over) m = x;
+            l *= down;
+#pragma unroll
+            for (int h = 0; h < HP; ++h) {
+              const float d = __shfl_sync(0xffffffffu, down, (lane & 24) | h);
+#pragma unroll
+              for (int i = 0; i < DI; ++i) {
+                o[h][i].x *= d;
+                o[h][i].y *= d;
+                o[h][i].z *= d;
+                o[h][i].w *= d;
+              }
+            }
+          }
+          const float w = exp2f(x - m);
+          l += w;
+          const float wv = w * vs;
+#pragma unroll
+          for (int h = 0; h < HP; ++h) {
+            const float wh = __shfl_sync(0xffffffffu, wv, (lane & 24) | h);
 #pragma unroll
             for (int i = 0; i < DI; ++i) {
-              o[h][i].x = fmaf(wv, vv[i].x, o[h][i].x * a);
-              o[h][i].y = fmaf(wv, vv[i].y, o[h][i].y * a);
-              o[h][i].z = fmaf(wv, vv[i].z, o[h][i].z * a);
-              o[h][i].w = fmaf(wv, vv[i].w, o[h][i].w * a);
+              o[h][i].x = fmaf(wh, vv[i].x, o[h][i].x);
+              o[h][i].y = fmaf(wh, vv[i].y, o[h][i].y);
+              o[h][i].z = fmaf(wh, vv[i].z, o[h][i].z);
+              o[h][i].w = fmaf(wh, vv[i].w, o[h][i].w);
             }
           }
         }
       }
-      // the four tokens at a time of a warp, then the warps
+      // the sums against a common reference
+      const int part = warp * 4 + grp;
 #pragma unroll
-      for (int h = 0; h < HP; ++h) {
-        float mx = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float a = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mx);
-        l[h] *= a;
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 8);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 16);
+      for (int h = 0; h < HP; ++h)
 #pragma unroll
-        for (int i = 0; i < DI; ++i) {
-          float* x = &o[h][i].x;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float y = m[h] == -INFINITY ? 0.f : x[j] * a;
-            y += __shfl_xor_sync(0xffffffffu, y, 8);
-            y += __shfl_xor_sync(0xffffffffu, y, 16);
-            x[j] = y;
-          }
-          if (grp == 0 && i < di)
-            *reinterpret_cast<float4*>(&s_o[warp][h][(sub + 8 * i) * 4]) = o[h][i];
-        }
-        if (lane == 0) {
-          s_m[warp][h] = mx;
-          s_l[warp][h] = l[h];
-        }
+        for (int i = 0; i < DI; ++i)
+          if (i < di) s_o[part][h][sub + 8 * i] = o[h][i];
+      if (sub < HP) {
+        s_m[part][sub] = m;
+        s_l[part][sub] = l;
       }
       __syncthreads();
-      for (int i = tid; i < HP * A.d; i += kScoredWarps * 32) {
-        const int hh = i / A.d, c = i - hh * A.d;
-        if (h0 + hh >= A.G) break;
-        float M = -INFINITY, Ls = 0.f, O = 0.f;
-#pragma unroll
-        for (int w = 0; w < kScoredWarps; ++w) M = fmaxf(M, s_m[w][hh]);
-#pragma unroll
-        for (int w = 0; w < kScoredWarps; ++w) {
-          if (s_l[w][hh] == 0.f) continue;   // nothing seen (a sum that is NaN stays)
-          const float a = exp2f(s_m[w][hh] - M);
-          Ls = fmaf(s_l[w][hh], a, Ls);
-          O = fmaf(s_o[w][hh][c], a, O);
-        }
+      if (tid < HP && h0 + tid < A.G) {   // a head's sums become the parts' factors
+        float M = kNone, Ls = 0.f;
+        for (int p = 0; p < kParts; ++p) M = fmaxf(M, s_m[p][tid]);
+        for (int p = 0; p < kParts; ++p)   // nothing seen: no part (a sum that is NaN has one)
+          if (s_l[p][tid] != 0.f) Ls = fmaf(s_l[p][tid], exp2f(s_m[p][tid] - M), Ls);
         const bool any = Ls != 0.f;
-        float weight, lse = any ? (M + log2f(Ls)) * kLn2 : -INFINITY;
-        if (P.whole) lse = with_sink(A.sink, g * A.G + h0 + hh, lse, weight);
-        put_value(A, P, h0 + hh, c, any ? O / Ls : 0.f, weight);
-        if (c == 0) put_lse(A, P, h0 + hh, lse);
+        float weight = 1.f, lse = any ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+        if (P.whole) lse = with_sink(A.sink, g * A.G + h0 + tid, lse, weight);
+        put_lse(A, P, h0 + tid, lse);
+        for (int p = 0; p < kParts; ++p)
+          s_l[p][tid] = any && s_l[p][tid] != 0.f ? exp2f(s_m[p][tid] - M) / Ls * weight : 0.f;
+      }
+      __syncthreads();
+      const int quads = A.d / 4;
+      for (int i = tid; i < HP * quads; i += kScoredWarps * 32) {
+        const int hh = i / quads, c = i - hh * quads;
+        if (h0 + hh >= A.G) break;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int p = 0; p < kParts; ++p) {
+          const float f = s_l[p][hh];
+          const float4 v4 = s_o[p][hh][c];
+          y.x = fmaf(f, v4.x, y.x);
+          y.y = fmaf(f, v4.y, y.y);
+          y.z = fmaf(f, v4.z, y.z);
+          y.w = fmaf(f, v4.w, y.w);
+        }
+        put_four(A, P, (h0 + hh) * quads + c, y);
       }
     }
   }
@@ -364,7 +393,7 @@ scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
 // host
 // ---------------------------------------------------------------------------
 
-static int generic_ctas() { return num_sms() * 4; }
+static int generic_ctas(int d) { return num_sms() * generic_per_sm(d <= 64 ? 2 : d <= 128 ? 4 : 8); }
 
 template <int kKind, int DI>
 static cudaError_t launch_generic(const ScoredArgs& A, bool q_bf16, cudaStream_t s) {
@@ -391,7 +420,7 @@ static size_t before_bytes(int64_t entries) { return align_up((size_t)(entries +
 
 // Chunks of a call at most: one for each CTA that runs at once.
 static int most_chunks(int d, int G) {
-  int most = generic_ctas();
+  int most = generic_ctas(d);
   for (CacheKind kind : {kCacheBf16, kCacheE4m3}) {
     const int n = scored_mma_wave(d, G, kind);
     if (n > most) most = n;
@@ -492,7 +521,7 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
   A.least = (mma ? 2 : 1) * kScoredWarps;
   // no more chunks than a full table has
   const int64_t useful = (tiles + A.least - 1) / A.least;
-  A.ctas = mma ? scored_mma_wave(d, A.G, kv.kind) : generic_ctas();
+  A.ctas = mma ? scored_mma_wave(d, A.G, kv.kind) : generic_ctas(d);
   if (A.ctas > useful) A.ctas = useful > 0 ? (int)useful : 1;
   A.part_lse = (float*)w;
   w += align_up((size_t)(A.ctas + entries * Hkv) * A.G * 4, 256);

@@ -265,6 +265,11 @@ __device__ __forceinline__ Piece piece_at(const ScoredArgs& A, int t, int t1, in
   return p;
 }
 
+// A score is compared with its head's reference only to see whether it passes it
+// by more than 2^4; while none of a warp's does (one vote), nothing is rescaled.
+constexpr float kSlack = 4.f;
+constexpr float kNone = -3e38f;  // a reference before there is a score
+
 // tanh: by its series (the terms up to y^9, the next is below 2^-26 of y) for
 // small y, and 1 - 2 / (1 + e^2y) where that loses less than 2^-21.  tanhf, which
 // branches, makes a capped call over 524288 tokens 219 us instead of 212.
@@ -292,18 +297,15 @@ struct PieceOut {
   int64_t slot, row;   // row: e * Hq + g * G
 };
 
-__device__ __forceinline__ void put_value(const ScoredArgs& A, const PieceOut& P, int hh, int col,
-                                          float o, float weight) {
-  if (P.whole) {
-    const int64_t at = (P.row + hh) * A.d + col;
-    o *= weight;
-    if (A.out_dtype == DCP_F32)
-      ((float*)A.out)[at] = o;
-    else
-      ((__nv_bfloat16*)A.out)[at] = __float2bfloat16(o);
-  } else {
-    A.part_o[(P.slot * A.G + hh) * A.d + col] = o;
-  }
+// Four values from column 4 i on, counted over the unit's heads.
+__device__ __forceinline__ void put_four(const ScoredArgs& A, const PieceOut& P, int i, float4 y) {
+  if (!P.whole)
+    reinterpret_cast<float4*>(A.part_o + P.slot * A.G * A.d)[i] = y;
+  else if (A.out_dtype == DCP_F32)
+    reinterpret_cast<float4*>((float*)A.out + P.row * A.d)[i] = y;
+  else
+    reinterpret_cast<uint2*>((__nv_bfloat16*)A.out + P.row * A.d)[i] =
+        make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
 }
 
 // Natural LSE with the sink's, and the weight that the values keep beside it.

@@ -80,10 +80,8 @@ struct Shape {
   }
 };
 
-constexpr float kSlack = 4.f;    // how far a score may pass its reference, in powers of two
 constexpr float kLift = 11.f;    // fp16 weights are held times 2^11: up to 2^15 with the slack, and
                                  // in full precision down to 2^-25
-constexpr float kNone = -3e38f;  // a reference before there is a score
 constexpr int kScoredStuck = 1 << 20;   // err_count increment for a wait that timed out
 
 // Four warps a CTA use tiles, each every fourth one of the CTA's chunk from a ring
@@ -91,9 +89,6 @@ constexpr int kScoredStuck = 1 << 20;   // err_count increment for a wait that t
 // fills the rings by TMA, a lane for each, over the ends of pieces.  (Each warp
 // filling its own ring had a quarter of its instructions for that, and what
 // bounded the kernel was the length of a warp's chain of instructions.)
-// A score is compared with its head's reference only to see whether it passes it
-// by more than 2^4; while none does (one vote), nothing is rescaled and no
-// maximum is shared.
 constexpr int kScoredThreads = (kScoredWarps + 1) * 32;
 
 __device__ __forceinline__ void sync_users() {   // the warps that use tiles
@@ -582,13 +577,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
         y.z = fmaf(x.z, fs[w], y.z);
         y.w = fmaf(x.w, fs[w], y.w);
       }
-      if (!P.whole)
-        reinterpret_cast<float4*>(A.part_o + P.slot * A.G * D)[i] = y;
-      else if (A.out_dtype == DCP_F32)
-        reinterpret_cast<float4*>((float*)A.out + P.row * D)[i] = y;
-      else
-        reinterpret_cast<uint2*>((__nv_bfloat16*)A.out + P.row * D)[i] =
-            make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+      put_four(A, P, i, y);
     }
     sync_users();
   }
