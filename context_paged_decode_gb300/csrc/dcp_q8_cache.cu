@@ -296,25 +296,28 @@ struct GatherArgs {
   const int32_t* req;
   const int64_t* pos;
   int64_t N;
-  int per_cta;           // tokens of a CTA, at most 8
-  FastDiv by_row, by_head;   // pieces of a token's heads, and of one head
+  int per_cta;      // tokens of a CTA
   void* out[2];
   int32_t* err;
 };
 
 constexpr int kGatherThreads = 256;
-constexpr int kGatherDepth = 4;    // loads in flight per thread
+constexpr int kGatherTokens = 16;  // of a CTA at most; a power of two, as CTAs take 1, 2, 4 ...
+static_assert((kGatherTokens & (kGatherTokens - 1)) == 0, "CTAs take 1, 2, 4 ... tokens");
+constexpr int kGatherDepth = 8;    // loads in flight per thread
 
 // A CTA looks up a few tokens' rows; a thread then reads what becomes 16 bytes,
 // so that a warp writes 512 bytes in one piece (16 numbers a thread, written in
-// two or four pieces, took 71 us for 65536 tokens of 8 heads of 128, not 66).
+// two or four pieces, took 71 us for 65536 tokens of 8 heads of 128, not 66), at
+// the same place of every row that it has a part of: what hangs on the place is
+// worked out once (a division for each piece: 66 us, not 64).
 template <typename T>
 __global__ void __launch_bounds__(kGatherThreads)
 q8_gather_kernel(const __grid_constant__ GatherArgs A) {
   using Raw = typename std::conditional<sizeof(T) == 4, uint32_t, uint2>::type;
   constexpr int kVals = 16 / sizeof(T);
-  __shared__ int s_rank[8], s_loc[8];
-  __shared__ int64_t s_page[8];
+  __shared__ const uint8_t* s_row[2][kGatherTokens];   // a token's first head, NULL: missing
+  __shared__ const float* s_scale[kGatherTokens];
   griddep_launch_dependents();   // the next call's first kernel may start its launch
   griddep_wait();                // launched chained: the preceding kernel completed
   const int tid = threadIdx.x;
@@ -329,56 +332,57 @@ q8_gather_kernel(const __grid_constant__ GatherArgs A) {
       A.S.place((int)x, rank, vb, loc);
       page = __ldg(A.bt + rank * A.bt_stride + (int64_t)b * A.max_vb + vb);
     }
-    if (page < 0 || page >= A.nb) {
-      page = -1;
-      count_error(A.err);
-    }
-    s_rank[tid] = rank;
-    s_loc[tid] = loc;
-    s_page[tid] = page;
+    const bool there = page >= 0 && page < A.nb;
+    if (!there) count_error(A.err);
+    const int64_t at = (page * A.Hkv * A.S.bs + loc) * A.d;
+    s_row[0][tid] = there ? (const uint8_t*)A.pool[0].ptr[rank] + at : nullptr;
+    s_row[1][tid] = there ? (const uint8_t*)A.pool[1].ptr[rank] + at : nullptr;
+    s_scale[tid] = there ? (const float*)A.sc.ptr[rank] + page * A.Hkv * kScaleFloats : nullptr;
   }
   __syncthreads();
-  const int per_row = A.Hkv * A.d / kVals, all = 2 * tokens * per_row;   // keys, then values
-  for (int i0 = tid; i0 < all; i0 += kGatherThreads * kGatherDepth) {
-    Raw x[kGatherDepth];
-    float s[kGatherDepth];
+  const int per_row = A.Hkv * A.d / kVals, per_head = A.d / kVals;   // pieces of 16 bytes
+  // threads side by side on one row, as many rows at a time as there are threads for
+  const int side = min(per_row, kGatherThreads), rows = kGatherThreads / side;
+  const int first = tid / side;
+  if (first >= rows) return;
+  for (int piece = tid - first * side; piece < per_row; piece += side) {
+    const int h = piece / per_head;
+    const int64_t at = (int64_t)h * A.S.bs * A.d + (piece - h * per_head) * kVals;
+    for (int r0 = first; r0 < 2 * tokens; r0 += rows * kGatherDepth) {   // keys, then values
+      Raw x[kGatherDepth];
+      float s[kGatherDepth];
 #pragma unroll
-    for (int j = 0; j < kGatherDepth; ++j) {
-      const int i = i0 + j * kGatherThreads;
-      if (i >= all) break;
-      const int tw = A.by_row.div(i), rem = i - tw * per_row;
-      const int which = tw >= tokens, t = tw - which * tokens, h = A.by_head.div(rem);
-      const int64_t page = s_page[t];
-      x[j] = Raw{};
-      s[j] = 0.f;
-      if (page >= 0) {   // a missing token is zeros
-        const int64_t ph = page * A.Hkv + h;
-        const int r = s_rank[t], at = rem - h * (A.d / kVals);
-        const dcp_rank_ptrs_t& pool = A.pool[which];
-        x[j] = __ldg(reinterpret_cast<const Raw*>((const uint8_t*)pool.ptr[r] +
-                                                  (ph * A.S.bs + s_loc[t]) * A.d) + at);
-        s[j] = __ldg((const float*)A.sc.ptr[r] + ph * kScaleFloats + which);
+      for (int j = 0; j < kGatherDepth; ++j) {
+        const int r = r0 + j * rows;
+        if (r >= 2 * tokens) break;
+        const int which = r >= tokens, t = r - which * tokens;
+        const uint8_t* row = s_row[which][t];
+        x[j] = Raw{};
+        s[j] = 0.f;
+        if (row) {   // a missing token is zeros
+          x[j] = __ldg(reinterpret_cast<const Raw*>(row + at));
+          s[j] = __ldg(s_scale[t] + h * kScaleFloats + which);
+        }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kGatherDepth; ++j) {
-      const int i = i0 + j * kGatherThreads;
-      if (i >= all) break;
-      // the CTA's tokens are one piece of each output
-      const int which = i >= tokens * per_row;
-      uint4* out = reinterpret_cast<uint4*>(A.out[which]) + t0 * per_row + (i - which * tokens * per_row);
-      float4 y[kVals / 4];
+      for (int j = 0; j < kGatherDepth; ++j) {
+        const int r = r0 + j * rows;
+        if (r >= 2 * tokens) break;
+        const int which = r >= tokens, t = r - which * tokens;
+        uint4* out = reinterpret_cast<uint4*>(A.out[which]) + (t0 + t) * per_row + piece;
+        float4 y[kVals / 4];
 #pragma unroll
-      for (int k = 0; k < kVals / 4; ++k) {
-        y[k] = e4m3x4_f32(reinterpret_cast<const uint32_t*>(&x[j])[k]);
-        y[k] = make_float4(y[k].x * s[j], y[k].y * s[j], y[k].z * s[j], y[k].w * s[j]);
+        for (int k = 0; k < kVals / 4; ++k) {
+          y[k] = e4m3x4_f32(reinterpret_cast<const uint32_t*>(&x[j])[k]);
+          y[k] = make_float4(y[k].x * s[j], y[k].y * s[j], y[k].z * s[j], y[k].w * s[j]);
+        }
+        if (kVals == 4)
+          *reinterpret_cast<float4*>(out) = y[0];
+        else
+          *out = make_uint4(pack_bf16(y[0].x, y[0].y), pack_bf16(y[0].z, y[0].w),
+                            pack_bf16(y[kVals / 4 - 1].x, y[kVals / 4 - 1].y),
+                            pack_bf16(y[kVals / 4 - 1].z, y[kVals / 4 - 1].w));
       }
-      if (kVals == 4)
-        *reinterpret_cast<float4*>(out) = y[0];
-      else
-        *out = make_uint4(pack_bf16(y[0].x, y[0].y), pack_bf16(y[0].z, y[0].w),
-                          pack_bf16(y[kVals / 4 - 1].x, y[kVals / 4 - 1].y),
-                          pack_bf16(y[kVals / 4 - 1].z, y[kVals / 4 - 1].w));
     }
   }
 }
@@ -493,14 +497,11 @@ int dcp_q8_gather_gqa(dcp_layout_t layout, dcp_paged_kv8_t kv, int32_t num_reqs,
   A.req = req_idx, A.pos = positions, A.N = num_tokens;
   A.out[0] = k_out, A.out[1] = v_out;
   A.err = err_count;
-  const int vals = (int)(16 / es);
-  A.by_row = FastDiv((uint32_t)(row / vals));
-  A.by_head = FastDiv((uint32_t)(head_dim / vals));
-  // a token a CTA while they all run at once, then up to eight (65536 tokens of 8 heads of 128
-  // take 66 us with eight, 68 with 4 or 32; 1500 tokens 4.8 with one, 5.2 with two)
+  // a token a CTA while they all run at once, then up to sixteen (65536 tokens of 8 heads of 128
+  // take 64 us, with 8 or 32 a CTA 69 or 66)
   const int64_t fill = (int64_t)num_sms() * 16;
   A.per_cta = 1;
-  while (A.per_cta < 8 && (num_tokens + A.per_cta - 1) / A.per_cta > fill) A.per_cta *= 2;
+  while (A.per_cta < kGatherTokens && (num_tokens + A.per_cta - 1) / A.per_cta > fill) A.per_cta *= 2;
   const unsigned grid = (unsigned)((num_tokens + A.per_cta - 1) / A.per_cta);
   const cudaError_t e =
       dtype == DCP_F32
