@@ -77,6 +77,8 @@ CASES = [
     (BF16, 1, 32, 16, 8, 8, [3], [400], False),
     (BF16, 1, 128, 4, 1, 1, [3, 0], [20, 9], False),
     (F32, 1, 96, 2, 3, 3, [3, 0], [20, 9], True),
+    (F32, 2, 160, 5, 48, 3, [13, 0, 500], [31, 9, 200], True),
+    (BF16, 2, 224, 2, 16, 4, [13, 0], [31, 90], False),
 ]
 
 
@@ -433,3 +435,71 @@ def test_refusals(lib):
                                    block_table=c.kv.block_table, num_blocks=c.kv.num_blocks), **bad})
     with pytest.raises(lib.DcpError):
         c.kv.struct()
+
+
+@pytest.mark.parametrize("qtype", [BF16, F32], ids=str)
+@pytest.mark.parametrize("graph", [False, True])
+def test_steps_in_a_row(lib, qtype, graph):
+    """Steps that follow one another without a wait (each call's kernels may start before those
+    in front of them have ended) give what they give one by one: lengths are raised on the
+    device, tokens that make scales grow are appended, and the cache is attended and read."""
+    dcp, bs, I, H, Hq, d, steps = 2, 16, 1, 2, 4, 64, 60
+    L = lib.Layout(dcp, bs, I)
+    rng = np.random.default_rng(33)
+    bt, nb = R.random_tables(rng, [200, 150, 90], dcp, bs)
+    tab = torch.from_numpy(bt).cuda()
+    k, v = (torch.from_numpy(rng.standard_normal((steps, 3, H, d))
+                             * rng.choice([0.1, 1.0, 40.0], (steps, 3, 1, 1))).to(BF16).cuda()
+            for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((steps, 3, Hq, d))).to(qtype).cuda()
+    start = torch.arange(4, dtype=torch.int32, device="cuda")
+    req = torch.arange(3, dtype=torch.int32, device="cuda").repeat_interleave(40)
+    form = lib.Scores(cap=20.0, window=50, prefix=3)
+
+    def run(wait):
+        kv = lib.PagedKV8.new(L, nb, H, d, tab)
+        for p in kv.k_pools + kv.v_pools:
+            p.view(torch.uint8).fill_(0x7f)
+        ctx = torch.tensor([0, 17, 30], dtype=torch.int32, device="cuda")
+        first = torch.zeros((47, H, d), dtype=BF16, device="cuda") + 0.5
+        fs = torch.tensor([0, 0, 17, 47], dtype=torch.int32, device="cuda")
+        lib.q8_append_gqa(L, first, first, kv, fs, torch.zeros_like(ctx))
+        lens, pos = torch.empty_like(ctx), torch.empty(120, dtype=torch.int64, device="cuda")
+        back = torch.arange(40, device="cuda").repeat(3)
+        out = torch.zeros((steps, 3, Hq, d), dtype=qtype, device="cuda")
+        lse = torch.zeros((steps, 3, Hq), device="cuda")
+        rows_ = torch.zeros((steps, 120, H, d), device="cuda")
+
+        def steps_():
+            for t in range(steps):
+                lib.q8_append_gqa(L, k[t], v[t], kv, start, ctx)
+                wait()
+                torch.add(ctx, 1, out=lens)
+                lib.q8_decode_gqa(L, q[t], kv, lens, d ** -0.5, scores=form, out=out[t],
+                                  out_lse=lse[t])
+                wait()
+                torch.sub(lens[:, None].long(), 1 + back.view(3, 40), out=pos.view(3, 40)).clamp_(min=0)
+                lib.q8_gather_gqa(L, kv, req, pos, k_out=rows_[t],
+                                  v_out=torch.empty_like(rows_[t]))
+                wait()
+                ctx.copy_(lens)
+
+        if graph and wait is nothing:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                steps_()
+            g.replay()
+        else:
+            steps_()
+        torch.cuda.synchronize()
+        return out, lse, rows_, torch.stack(kv.scales)[..., :2], torch.stack(kv.k_pools).view(torch.uint8)
+
+    def nothing():
+        pass
+
+    want = run(torch.cuda.synchronize)
+    got = run(nothing)
+    for a, b in zip(got, want):
+        assert torch.equal(torch.nan_to_num(a) if a.is_floating_point() else a,
+                           torch.nan_to_num(b) if b.is_floating_point() else b)
+    assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()

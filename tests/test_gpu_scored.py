@@ -136,6 +136,12 @@ CASES = [
     (BF16, BF16, 8, 2, 64, 16, 16, 16, [1999, 256], dict(shared=True)),
     (E4M3, BF16, 8, 2, 64, 16, 16, 16, [1999, 256], dict(shared=True)),
     (E4M3, BF16, 12, 4, 128, 1, 64, 64, [1999, 256], dict(sink=True)),
+    # nine to sixteen query heads for a key/value head; pages of three tiles, five ranks
+    (BF16, BF16, 32, 2, 128, 2, 16, 1, [1100, 37], dict(cap=30.0, sink=True)),
+    (E4M3, BF16, 32, 2, 128, 2, 16, 1, [1100, 37], dict(cap=30.0, alibi=True)),
+    (E4M3, BF16, 18, 2, 64, 5, 48, 3, [1100, 37], dict(window=300)),
+    (BF16, BF16, 11, 1, 128, 5, 48, 3, [1100, 37], dict(alibi=True)),
+    (F32, F32, 12, 1, 128, 5, 48, 3, [600, 37], dict(sink=True)),
     # pages and heads that tiles do not fit
     (BF16, BF16, 6, 2, 96, 2, 24, 3, [301, 11], dict(window=90)),
     (E4M3, BF16, 5, 1, 256, 2, 8, 1, [301, 11], dict(cap=30.0)),
