@@ -523,13 +523,22 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
   const int64_t useful = (tiles + A.least - 1) / A.least;
   A.ctas = mma ? scored_mma_wave(d, A.G, kv.kind) : generic_ctas(d);
   if (A.ctas > useful) A.ctas = useful > 0 ? (int)useful : 1;
+  if (mma) {
+    // the most tiles of a unit, by the table and by the window
+    const int64_t kept = f.window > 0 ? (int64_t)f.window + f.prefix : room;
+    const int64_t tokens = kept < room ? kept : room;
+    const int64_t per_rank = tokens / dcp + 2 * layout.interleave;
+    const int64_t most = apart_ ? per_rank / kRows + 4 : tokens / kRows + 4 * dcp;
+    A.unit_ctas = scored_mma_unit_ctas(d, A.G, kv.kind, entries * Hkv, most);
+    if (A.unit_ctas) A.ctas = (int)(entries * Hkv) * A.unit_ctas;
+  }
   A.part_lse = (float*)w;
   w += align_up((size_t)(A.ctas + entries * Hkv) * A.G * 4, 256);
   A.part_o = (float*)w;
   int rc = DCP_OK;
   if (mma) {
     rc = launch_scored_mma(A, kv.kind, s);
-    if (rc) return rc;
+    if (rc || A.unit_ctas) return rc;
   } else {
     const bool q16 = dtype == DCP_BF16;
     const cudaError_t e = kv.kind == kCacheF32    ? launch_generic<kCacheF32>(A, q16, s)

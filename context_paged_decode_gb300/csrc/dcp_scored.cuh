@@ -98,6 +98,7 @@ struct ScoredArgs {
   float* part_lse;           // [chunks + units][G]
   float* part_o;             // [chunks + units][G][d]
   int ctas, least;           // chunks at most (the grid), and the fewest tiles of one
+  int unit_ctas;             // CTAs of a unit (a cluster) where units are not cut elsewhere, or 0
   __device__ __forceinline__ int entries() const { return apart ? B * S.dcp : B; }
 };
 
@@ -162,6 +163,14 @@ __device__ __forceinline__ int entry_tiles(const ScoredArgs& A, int e, bool coun
   int n = 0;
   for (int r = 0; r < A.S.dcp; ++r) n += s.tiles(A.S, r);
   return n;
+}
+
+// The same by a warp, a rank in each lane.
+__device__ __forceinline__ int entry_tiles_by_warp(const ScoredArgs& A, int e, bool count) {
+  const int lane = threadIdx.x & 31, R = A.apart ? 1 : A.S.dcp;
+  const Seen s = seen_of(A, A.apart ? e % A.B : e, count && lane == 0 && e < A.B);
+  const int r = (A.apart ? e / A.B : 0) + min(lane, R - 1);
+  return __reduce_add_sync(0xffffffffu, lane < R ? s.tiles(A.S, r) : 0);
 }
 
 // A unit is a key/value head of an entry, its tiles those of the ranks in
@@ -248,21 +257,27 @@ struct Piece {
   int start, t;   // first tile of the entry, and the line's tile behind the piece
 };
 
-// The piece that begins with tile t, in a chunk that ends with t1; e and start
-// are an entry at or in front of it.
-__device__ __forceinline__ Piece piece_at(const ScoredArgs& A, int t, int t1, int e, int start) {
+// The piece that begins with tile t, in a chunk that ends with t1, of entry e
+// with n tiles a head.
+__device__ __forceinline__ Piece piece_of(const ScoredArgs& A, int t, int t1, int e, int start,
+                                          int n) {
   Piece p;
-  int n = entry_tiles(A, e, false);
-  while (t - start >= n * A.Hkv && e + 1 < A.entries()) {
-    start += n * A.Hkv;
-    n = entry_tiles(A, ++e, false);
-  }
   p.e = e, p.n = n, p.start = start;
   p.g = (int)((uint32_t)(t - start) / (uint32_t)max(n, 1));
   p.k0 = t - start - p.g * n;
   p.k1 = min(n, p.k0 + (t1 - t));
   p.t = t + (p.k1 - p.k0);
   return p;
+}
+
+// The same with an entry at or in front of it.
+__device__ __forceinline__ Piece piece_at(const ScoredArgs& A, int t, int t1, int e, int start) {
+  int n = entry_tiles(A, e, false);
+  while (t - start >= n * A.Hkv && e + 1 < A.entries()) {
+    start += n * A.Hkv;
+    n = entry_tiles(A, ++e, false);
+  }
+  return piece_of(A, t, t1, e, start, n);
 }
 
 // A score is compared with its head's reference only to see whether it passes it
@@ -329,6 +344,9 @@ __device__ __forceinline__ void put_lse(const ScoredArgs& A, const PieceOut& P, 
 // Which kernel a cache takes: the tensor-core kernel (dcp_scored_mma.cu) or
 // the one for any type and shape (dcp_scored.cu).
 enum CacheKind { kCacheF32, kCacheBf16, kCacheE4m3 };
+// CTAs of a unit where that is better than cutting the line, else 0: `tiles` is
+// the most that a unit can have.
+int scored_mma_unit_ctas(int d, int G, CacheKind kind, int64_t units, int64_t tiles);
 bool scored_mma_ok(const ScoredArgs& A, CacheKind kind, bool q_bf16);
 int scored_mma_wave(int d, int G, CacheKind kind);   // CTAs that run at once
 int launch_scored_mma(const ScoredArgs& A, CacheKind kind, cudaStream_t s);

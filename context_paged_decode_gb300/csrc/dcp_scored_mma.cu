@@ -90,6 +90,21 @@ constexpr int kScoredStuck = 1 << 20;   // err_count increment for a wait that t
 // filling its own ring had a quarter of its instructions for that, and what
 // bounded the kernel was the length of a warp's chain of instructions.)
 constexpr int kScoredThreads = (kScoredWarps + 1) * 32;
+constexpr int kUnitCtas = 8;   // of a unit's cluster at most
+
+__device__ __forceinline__ float remote_f32(uint32_t cluster_addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cluster_addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 remote_f32x4(uint32_t cluster_addr) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return x;
+}
 
 __device__ __forceinline__ void sync_users() {   // the warps that use tiles
   asm volatile("bar.sync 1, %0;" ::"n"(kScoredWarps * 32) : "memory");
@@ -123,12 +138,22 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
   __syncthreads();
   griddep_wait();                // launched chained: the preceding kernel completed
   const int chunk = blockIdx.x;
-  const Line line = plan_line<kScoredThreads>(A, chunk, s_before);
-  const int t0 = (int)min((int64_t)line.each * chunk, (int64_t)line.all);
-  const int t1 = (int)min((int64_t)t0 + line.each, (int64_t)line.all);
-  if (chunk == 0) keep_line<kScoredThreads>(A, line, s_before);
-  int e0, start0;
-  seek_entry<kScoredThreads>(A, line, s_before, t0, e0, start0);
+  int t0, t1, e0, start0, n0 = 0;
+  const int rank = A.unit_ctas ? chunk % A.unit_ctas : 0;
+  if (A.unit_ctas) {   // a part of one unit, on a line of this entry alone
+    const int u = chunk / A.unit_ctas, g = u % A.Hkv;
+    e0 = u / A.Hkv;
+    n0 = entry_tiles_by_warp(A, e0, rank == 0 && g == 0 && warp == 0);
+    t0 = g * n0 + (int)((int64_t)n0 * rank / A.unit_ctas);
+    t1 = g * n0 + (int)((int64_t)n0 * (rank + 1) / A.unit_ctas);
+    start0 = 0;
+  } else {
+    const Line line = plan_line<kScoredThreads>(A, chunk, s_before);
+    t0 = (int)min((int64_t)line.each * chunk, (int64_t)line.all);
+    t1 = (int)min((int64_t)t0 + line.each, (int64_t)line.all);
+    if (chunk == 0) keep_line<kScoredThreads>(A, line, s_before);
+    seek_entry<kScoredThreads>(A, line, s_before, t0, e0, start0);
+  }
 
   if (warp == kScoredWarps) {
     // --- the warp that fills the rings ---
@@ -226,6 +251,10 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
         __syncwarp();
       }
     }
+    if (A.unit_ctas > 1) {   // as the others
+      cluster_sync();
+      cluster_sync();
+    }
     griddep_launch_dependents();   // as below
     return;
   }
@@ -267,7 +296,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
   int st = warp, phase = 0;
   Piece at;
   if (t0 < t1) {
-    at = piece_at(A, t0, t1, e0, start0);
+    at = A.unit_ctas ? piece_of(A, t0, t1, e0, start0, n0) : piece_at(A, t0, t1, e0, start0);
     ask_queries(at);
   }
   int used = t0 + warp;   // this warp's next tile
@@ -505,7 +534,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
 
     // the next piece, and its queries on their way
     PieceOut P;
-    P.whole = k0 == 0 && k1 == n;
+    P.whole = A.unit_ctas ? A.unit_ctas == 1 : k0 == 0 && k1 == n;
     P.slot = chunk + (int64_t)e * A.Hkv + g;
     P.row = (int64_t)e * A.Hq + g * A.G;
     more = at.t < t1;
@@ -557,7 +586,10 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
       const bool any = Ls != 0.f;
       float weight = 1.f, lse = any ? (M + log2f(Ls)) * kLn2 : -INFINITY;
       if (P.whole) lse = with_sink(A.sink, g * A.G + tid, lse, weight);
-      put_lse(A, P, tid, lse);
+      if (A.unit_ctas > 1)
+        s_ml[tid * kScoredWarps * 4 + kScoredWarps] = lse;   // for the cluster
+      else
+        put_lse(A, P, tid, lse);
       float* const to = reinterpret_cast<float*>(ml);
 #pragma unroll
       for (int i = 0; i < kScoredWarps; ++i)
@@ -577,9 +609,68 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
         y.z = fmaf(x.z, fs[w], y.z);
         y.w = fmaf(x.w, fs[w], y.w);
       }
-      put_four(A, P, i, y);
+      if (A.unit_ctas > 1)
+        reinterpret_cast<float4*>(s_o)[i] = y;   // for the cluster, over what only it has read
+      else
+        put_four(A, P, i, y);
     }
     sync_users();
+  }
+  if (A.unit_ctas > 1) {
+    // --- the cluster's results joined, each CTA a share of the columns ---
+    const int g = chunk / A.unit_ctas % A.Hkv;
+    if (t0 == t1 && tid < A.G) s_ml[tid * kScoredWarps * 4 + kScoredWarps] = -INFINITY;
+    __syncwarp();
+    cluster_sync();
+    PieceOut P;
+    P.whole = true;
+    P.slot = 0;
+    P.row = (int64_t)e0 * A.Hq + g * A.G;
+    for (int i = tid * A.unit_ctas + rank; i < A.G * (D / 4);
+         i += kScoredWarps * 32 * A.unit_ctas) {
+      const int hh = i / (D / 4);
+      float l[kUnitCtas];
+      float4 y[kUnitCtas];
+      float M = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < kUnitCtas; ++c) {
+        l[c] = -INFINITY;
+        if (c >= A.unit_ctas) continue;
+        l[c] = remote_f32(mapa_shared(smem_u32(s_ml + hh * kScoredWarps * 4 + kScoredWarps), c));
+        y[c] = remote_f32x4(mapa_shared(smem_u32(s_o) + i * 16, c));
+      }
+#pragma unroll
+      for (int c = 0; c < kUnitCtas; ++c) M = fmaxf(M, l[c]);
+#pragma unroll
+      for (int c = 0; c < kUnitCtas; ++c)
+        if (l[c] != -INFINITY) sum += expf(l[c] - M);
+      float weight, lse = sum == 0.f ? -INFINITY : M + logf(sum);
+      const float all = with_sink(A.sink, g * A.G + hh, lse, weight);
+      float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kUnitCtas; ++c) {
+        if (l[c] == -INFINITY) continue;   // it has seen nothing
+        const float w = expf(l[c] - lse) * weight;
+        z.x = fmaf(w, y[c].x, z.x);
+        z.y = fmaf(w, y[c].y, z.y);
+        z.z = fmaf(w, y[c].z, z.z);
+        z.w = fmaf(w, y[c].w, z.w);
+      }
+      put_four(A, P, i, z);
+      if (i % (D / 4) == 0) put_lse(A, P, hh, all);
+    }
+    __syncwarp();
+    cluster_sync();   // all have read what is in this CTA
+  } else if (A.unit_ctas == 1 && t0 == t1) {   // nothing is seen
+    PieceOut P;
+    P.whole = true;
+    P.slot = 0;
+    const int g = chunk % A.Hkv;
+    P.row = (int64_t)e0 * A.Hq + g * A.G;
+    for (int i = tid; i < A.G * (D / 4); i += kScoredWarps * 32)
+      put_four(A, P, i, make_float4(0.f, 0.f, 0.f, 0.f));
+    float weight;
+    if (tid < A.G) put_lse(A, P, tid, with_sink(A.sink, g * A.G + tid, -INFINITY, weight));
   }
   // Only now may the merge start its launch, and only after its wait the next
   // call: 32 requests called in a row take 204 us each so, 315 where both kernels
@@ -622,8 +713,20 @@ static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
     if (!encode_rows(&maps.k[r], A.k.ptr[r], Z::kRowBytes, rows) ||
         !encode_rows(&maps.v[r], A.v.ptr[r], Z::kRowBytes, rows))
       return DCP_ECUDA;
-  const cudaError_t e = launch_chained(scored_mma_kernel<D, E8, NT, kFormed>, (unsigned)A.ctas,
-                                       kScoredThreads, Z::smem(A.G), s, A, maps);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)A.ctas);
+  cfg.blockDim = dim3(kScoredThreads);
+  cfg.dynamicSmemBytes = Z::smem(A.G);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // as launch_chained
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)A.unit_ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = A.unit_ctas > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, scored_mma_kernel<D, E8, NT, kFormed>, A, maps);
   return e == cudaSuccess ? launch_status() : launch_status_report(e);
 }
 
@@ -653,6 +756,20 @@ int scored_mma_wave(int d, int G, CacheKind kind) {
                   : (e8 ? one_wave<64, true, 2>(G) : one_wave<64, false, 2>(G));
   return G <= 8 ? (e8 ? one_wave<128, true, 1>(G) : one_wave<128, false, 1>(G))
                 : (e8 ? one_wave<128, true, 2>(G) : one_wave<128, false, 2>(G));
+}
+
+// A unit whole in a cluster of one, two, four or eight CTAs needs no second
+// kernel: that is worth kJoinTiles tiles a warp, which the cluster may have more
+// than an even cut of the line would give.
+int scored_mma_unit_ctas(int d, int G, CacheKind kind, int64_t units, int64_t tiles) {
+  constexpr int64_t kJoinTiles = 8;
+  const int64_t wave = scored_mma_wave(d, G, kind);
+  int c = kUnitCtas;
+  while (c > 1 && units * c > wave) c /= 2;
+  if (units * c > wave) return 0;
+  const int64_t here = (tiles + kScoredWarps * c - 1) / (kScoredWarps * c);
+  const int64_t even = tiles * units / (kScoredWarps * wave);
+  return here - even <= kJoinTiles ? c : 0;
 }
 
 }  // namespace dcp

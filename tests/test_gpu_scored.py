@@ -18,7 +18,7 @@ class Problem:
     """Random requests: lens, per-request seen tokens and their keys and values, and the cache."""
 
     def __init__(self, lib, cache, qtype, Hq, Hkv, d, dcp, bs, I, lens, cap=0.0, window=0, prefix=0,
-                 alibi=False, docs=False, sink=False, shared=False, seed=0, spread=1.0):
+                 alibi=False, docs=False, sink=False, shared=False, seed=0, spread=1.0, room=0):
         rng = np.random.default_rng(seed + 1000 * d + sum(lens))
         self.lib, self.qtype, self.Hq, self.Hkv, self.d = lib, qtype, Hq, Hkv, d
         self.lens, self.cap, self.G, self.dcp, self.bs, self.I = lens, cap, Hq // Hkv, dcp, bs, I
@@ -26,7 +26,8 @@ class Problem:
         self.layout = lib.Layout(dcp, bs, I)
         tables = 1 if shared else dcp
         vbs = bs * dcp
-        bt, nb = R.random_tables(rng, lens, tables, bs * dcp // tables)
+        # a table with room for more tokens: a request's tiles are cut elsewhere then
+        bt, nb = R.random_tables(rng, lens, tables, bs * dcp // tables, max_vb=room // vbs)
         q = torch.from_numpy(rng.standard_normal((B, Hq, d)) * spread).to(qtype)
         self.q, self.q64 = q.cuda(), q.double().numpy()
         self.first = np.array([rng.integers(0, max(n, 1)) if docs else 0 for n in lens])
@@ -156,10 +157,11 @@ def name(c):
             + "-".join(c[9]))
 
 
+@pytest.mark.parametrize("room", [0, 1 << 20])
 @pytest.mark.parametrize("case", CASES, ids=name)
-def test_fused_and_partials(lib, case):
+def test_fused_and_partials(lib, case, room):
     cache, qtype, Hq, Hkv, d, dcp, bs, I, lens, more = case
-    p = Problem(lib, cache, qtype, Hq, Hkv, d, dcp, bs, I, lens, **more)
+    p = Problem(lib, cache, qtype, Hq, Hkv, d, dcp, bs, I, lens, room=room, **more)
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     out, lse = p.run(err=err)
     assert out.dtype == qtype and err.item() == 0
@@ -237,12 +239,13 @@ def test_visible_nan_and_infinities_reach_the_output(lib, cache):
 
 
 @pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
+@pytest.mark.parametrize("room", [0, 1 << 20])
 @pytest.mark.parametrize("one", [False, True])
-def test_values_of_any_size(lib, cache, one):
+def test_values_of_any_size(lib, cache, one, room):
     """Scales and values from the smallest to the largest: what counts is not lost beside them."""
     q = F32 if cache == F32 else BF16
     lens = [9] if one else [400, 31]
-    p = Problem(lib, cache, q, 4, 2, 128, 2, 16, 1, lens, seed=3)
+    p = Problem(lib, cache, q, 4, 2, 128, 2, 16, 1, lens, seed=3, room=room)
     for b in range(len(lens)):
         x, k, v = p.rows[b]
         for vb in range(p.bt.shape[-1]):
@@ -300,9 +303,10 @@ def test_a_long_flat_tail_beside_one_large_weight(lib, cache):
 
 
 @pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
-def test_captured_with_changing_lengths(lib, cache):
+@pytest.mark.parametrize("room", [0, 1 << 20])
+def test_captured_with_changing_lengths(lib, cache, room):
     q = F32 if cache == F32 else BF16
-    p = Problem(lib, cache, q, 8, 2, 128, 2, 16, 1, [700, 650, 20], cap=30.0, sink=True)
+    p = Problem(lib, cache, q, 8, 2, 128, 2, 16, 1, [700, 650, 20], cap=30.0, sink=True, room=room)
     B, Hq, d = p.q.shape
     ws = torch.empty(lib.scored_workspace_size(p.layout, B, Hq, 2, d), dtype=torch.uint8,
                      device="cuda")
@@ -323,19 +327,21 @@ def test_captured_with_changing_lengths(lib, cache):
 
 
 @pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
-def test_requests_that_see_nothing(lib, cache):
+@pytest.mark.parametrize("room", [0, 1 << 20])
+def test_requests_that_see_nothing(lib, cache, room):
     """A document that begins at or behind the end; with and without a sink."""
     q = F32 if cache == F32 else BF16
     for sink in (False, True):
-        p = Problem(lib, cache, q, 8, 2, 128, 2, 16, 1, [70, 40, 33], sink=sink)
+        p = Problem(lib, cache, q, 8, 2, 128, 2, 16, 1, [70, 40, 33], sink=sink, room=room)
         first = torch.tensor([70, 1000, -3], dtype=torch.int32, device="cuda")
-        p.form = lib.Scores(first=first, window=20)
+        p.form = lib.Scores(first=first, window=20 if room == 0 else 1 << 30)
         out, lse = p.run()
         assert (out[:2] == 0).all()
         want = p.dsink.expand(2, -1) if sink else torch.full_like(lse[:2], -np.inf)
         assert torch.equal(lse[:2], want)
         x, k, v = p.rows[2]
-        p.rows[2] = (x[13:], k[:, 13:], v[:, 13:])
+        n = 13 if room == 0 else 0
+        p.rows[2] = (x[n:], k[:, n:], v[:, n:])
         p.check(out, lse, skip=(0, 1))
 
 
@@ -424,11 +430,12 @@ def test_refusals(lib):
 
 
 @pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
+@pytest.mark.parametrize("room", [0, 1 << 20])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1e6, -1e9, 1e30])
-def test_any_scale(lib, cache, scale):
+def test_any_scale(lib, cache, scale, room):
     """Scores of nothing, below 0, and so large that one token has all the weight."""
     q = F32 if cache == F32 else BF16
-    p = Problem(lib, cache, q, 4, 2, 64, 2, 16, 1, [150, 33, 1], sink=scale == 0.0)
+    p = Problem(lib, cache, q, 4, 2, 64, 2, 16, 1, [150, 33, 1], sink=scale == 0.0, room=room)
     p.scale = scale
     out, lse = p.run()
     if abs(scale) < 1:
