@@ -62,26 +62,36 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
   __shared__ float s_m[kParts][HP], s_l[kParts][HP];
   griddep_wait();                // launched chained: the preceding kernel completed
   __shared__ int s_before[kScoredWarps * 32];
+  __shared__ float s_lse[HP];
   const int chunk = blockIdx.x;
-  const Line line = plan_line<kScoredWarps * 32>(A, chunk, s_before);
-  if (chunk == 0) keep_line<kScoredWarps * 32>(A, line, s_before);
-  const int t0 = min((int64_t)line.each * chunk, (int64_t)line.all);
-  const int t1 = min((int64_t)t0 + line.each, (int64_t)line.all);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = lane & 7, grp = lane >> 3;
   const int di = A.d / 32;
   Piece at;
-  seek_entry<kScoredWarps * 32>(A, line, s_before, t0, at.e, at.start);
-  at.t = t0;
-  while (at.t < t1) {
-    at = piece_at(A, at.t, t1, at.e, at.start);
+  int t1 = 0;
+  if (A.unit_ctas) {   // a part of one unit, perhaps an empty one
+    const int u = chunk / A.unit_ctas, rank = chunk % A.unit_ctas;
+    at.e = u / A.Hkv, at.g = u % A.Hkv;
+    at.n = entry_tiles_by_warp(A, at.e, rank == 0 && at.g == 0 && warp == 0);
+    at.k0 = (int)((int64_t)at.n * rank / A.unit_ctas);
+    at.k1 = (int)((int64_t)at.n * (rank + 1) / A.unit_ctas);
+    at.t = 0;
+  } else {
+    const Line line = plan_line<kScoredWarps * 32>(A, chunk, s_before);
+    if (chunk == 0) keep_line<kScoredWarps * 32>(A, line, s_before);
+    at.t = (int)min((int64_t)line.each * chunk, (int64_t)line.all);
+    t1 = (int)min((int64_t)at.t + line.each, (int64_t)line.all);
+    seek_entry<kScoredWarps * 32>(A, line, s_before, at.t, at.e, at.start);
+  }
+  for (bool more = A.unit_ctas || at.t < t1; more; more = at.t < t1) {
+    if (!A.unit_ctas) at = piece_at(A, at.t, t1, at.e, at.start);
     const int e = at.e, g = at.g, k0 = at.k0, k1 = at.k1, n = at.n;
     const int b = A.apart ? e % A.B : e, r0 = A.apart ? e / A.B : 0;
     const int r1 = A.apart ? r0 + 1 : A.S.dcp;
     const Seen seen = seen_of(A, b, false);
     const int last = __ldg(A.lens + b) - 1;
     PieceOut P;
-    P.whole = k0 == 0 && k1 == n;
+    P.whole = A.unit_ctas ? A.unit_ctas == 1 : k0 == 0 && k1 == n;
     P.slot = chunk + (int64_t)e * A.Hkv + g;
     P.row = (int64_t)e * A.Hq + g * A.G;
     for (int h0 = 0; h0 < A.G; h0 += HP) {
@@ -255,7 +265,10 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
         const bool any = Ls != 0.f;
         float weight = 1.f, lse = any ? (M + log2f(Ls)) * kLn2 : -INFINITY;
         if (P.whole) lse = with_sink(A.sink, g * A.G + h0 + tid, lse, weight);
-        put_lse(A, P, h0 + tid, lse);
+        if (A.unit_ctas > 1)
+          s_lse[tid] = lse;   // for the cluster
+        else
+          put_lse(A, P, h0 + tid, lse);
         for (int p = 0; p < kParts; ++p)
           s_l[p][tid] = any && s_l[p][tid] != 0.f ? exp2f(s_m[p][tid] - M) / Ls * weight : 0.f;
       }
@@ -274,7 +287,17 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
           y.z = fmaf(f, v4.z, y.z);
           y.w = fmaf(f, v4.w, y.w);
         }
-        put_four(A, P, (h0 + hh) * quads + c, y);
+        if (A.unit_ctas > 1)
+          s_o[0][hh][c] = y;   // for the cluster, over what only it has read
+        else
+          put_four(A, P, (h0 + hh) * quads + c, y);
+      }
+      if (A.unit_ctas > 1) {
+        __syncwarp();
+        cluster_sync();
+        join_cluster(A, e, g, h0, min(HP, A.G - h0), quads, s_lse, 1, &s_o[0][0][0], DI * 8);
+        __syncwarp();
+        cluster_sync();   // all have read what is in this CTA
       }
     }
   }
@@ -395,13 +418,15 @@ scored_merge_kernel(const __grid_constant__ ScoredArgs A) {
 
 static int generic_ctas(int d) { return num_sms() * generic_per_sm(d <= 64 ? 2 : d <= 128 ? 4 : 8); }
 
+// Heads of a pass over the tokens: 8 values a lane of 2 heads fit into registers.
+constexpr int heads_a_pass(int d, int G) { return G == 1 ? 1 : d <= 128 ? 4 : 2; }
+
 template <int kKind, int DI>
 static cudaError_t launch_generic(const ScoredArgs& A, bool q_bf16, cudaStream_t s) {
-  const unsigned grid = (unsigned)A.ctas, block = kScoredWarps * 32;
-  return A.G == 1
-             ? launch_chained(scored_generic_kernel<kKind, DI, 1>, grid, block, 0, s, A, q_bf16)
-             : launch_chained(scored_generic_kernel<kKind, DI, DI == 8 ? 2 : 4>, grid, block, 0, s, A,
-                              q_bf16);   // 8 values a lane of 2 heads fit into registers
+  constexpr unsigned block = kScoredWarps * 32;
+  constexpr int HP = heads_a_pass(DI * 32, 2);
+  return A.G == 1 ? launch_scored<scored_generic_kernel<kKind, DI, 1>>(A, block, 0, s, A, q_bf16)
+                  : launch_scored<scored_generic_kernel<kKind, DI, HP>>(A, block, 0, s, A, q_bf16);
 }
 
 template <int kKind>
@@ -417,6 +442,35 @@ static bool shape_ok(const dcp_layout_t& L, int B, int Hq, int Hkv, int d) {
 }
 
 static size_t before_bytes(int64_t entries) { return align_up((size_t)(entries + 2) * 4, 256); }
+
+// CTAs of a unit where that is better than cutting the line, else 0.  A unit whole
+// in a cluster of up to sixteen CTAs needs no plan and no second kernel, 4 us: that
+// is worth a few tiles a warp, which the cluster may have more than an even cut of
+// the line would give.  On the tensor cores 8 (8 bits, 32/8 heads of 128: one
+// request of 3000 tokens 9.2 us in a cluster and 12.4 by the line, 6000 tokens 11.5
+// and 12.4, 12000 tokens, 8.5 more a warp, 16.9 and 16.3; 16 requests of 200 tokens
+// 8.0 and 13.4); on CUDA cores 3.7 of 64 dims in one pass (fp32, 8/2 heads of 64, two
+// requests of 2000 tokens 11.4 and 16.2, of 4000, 3.6 more a warp, 15.4 and 17.6, of
+// 9000 25.6 and 17.5; 32/8 heads of 128, 4000 tokens, 1.8 more, 34.8 and 33.9).
+// Fewer CTAs do where a warp has few tiles: an 8-bit request of 300 tokens takes 8.7
+// us in sixteen, 7.4 in four, and one of 1500 8.5 and 8.2 in eight.
+// `wave` CTAs run at once; `tiles` are the most of a unit.
+static int unit_ctas_of(bool mma, int d, int G, int64_t wave, int64_t units, int64_t tiles) {
+  // clusters that run at once, by cudaOccupancyMaxActiveClusters: larger ones leave gaps
+  auto fits = [&](int c) {
+    return units * c * 1000 <= wave * (c == 16 ? 700 : c == 8 ? 890 : c == 4 ? 960 : 1000);
+  };
+  auto few = [&](int half) {
+    return tiles <= (!mma ? 1 : half == 8 ? 4 : 3) * kScoredWarps * half;
+  };
+  int c = kUnitCtas;
+  while (c > 1 && (!fits(c) || few(c / 2))) c /= 2;
+  if (!fits(c)) return 0;
+  const double more = (double)tiles / kScoredWarps * (1. / c - (double)units / wave);
+  if (mma) return more <= 8. ? c : 0;
+  const int hp = heads_a_pass(d, G), passes = (G + hp - 1) / hp;
+  return more * passes * d <= 3.7 * 64. ? c : 0;
+}
 
 // Chunks of a call at most: one for each CTA that runs at once.
 static int most_chunks(int d, int G) {
@@ -521,24 +575,22 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
   A.least = (mma ? 2 : 1) * kScoredWarps;
   // no more chunks than a full table has
   const int64_t useful = (tiles + A.least - 1) / A.least;
-  A.ctas = mma ? scored_mma_wave(d, A.G, kv.kind) : generic_ctas(d);
-  if (A.ctas > useful) A.ctas = useful > 0 ? (int)useful : 1;
-  if (mma) {
-    // the most tiles of a unit, by the table and by the window
-    const int64_t kept = f.window > 0 ? (int64_t)f.window + f.prefix : room;
-    const int64_t tokens = kept < room ? kept : room;
-    const int64_t per_rank = tokens / dcp + 2 * layout.interleave;
-    const int64_t most = apart_ ? per_rank / kRows + 4 : tokens / kRows + 4 * dcp;
-    A.unit_ctas = scored_mma_unit_ctas(d, A.G, kv.kind, entries * Hkv, most);
-    if (A.unit_ctas) A.ctas = (int)(entries * Hkv) * A.unit_ctas;
-  }
+  const int wave = mma ? scored_mma_wave(d, A.G, kv.kind) : generic_ctas(d);
+  A.ctas = (int64_t)wave > useful ? (useful > 0 ? (int)useful : 1) : wave;
+  // the most tiles of a unit, by the table and by the window
+  const int64_t kept = f.window > 0 ? (int64_t)f.window + f.prefix : room;
+  const int64_t tokens = kept < room ? kept : room;
+  const int64_t per_rank = tokens / dcp + 2 * layout.interleave;
+  const int64_t most = apart_ ? per_rank / kRows + 4 : tokens / kRows + 4 * dcp;
+  A.unit_ctas = unit_ctas_of(mma, d, A.G, wave, entries * Hkv, most);
+  if (A.unit_ctas) A.ctas = (int)(entries * Hkv) * A.unit_ctas;
   A.part_lse = (float*)w;
   w += align_up((size_t)(A.ctas + entries * Hkv) * A.G * 4, 256);
   A.part_o = (float*)w;
   int rc = DCP_OK;
   if (mma) {
     rc = launch_scored_mma(A, kv.kind, s);
-    if (rc || A.unit_ctas) return rc;
+    if (rc) return rc;
   } else {
     const bool q16 = dtype == DCP_BF16;
     const cudaError_t e = kv.kind == kCacheF32    ? launch_generic<kCacheF32>(A, q16, s)
@@ -546,6 +598,7 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
                                                   : launch_generic<kCacheE4m3>(A, q16, s);
     if (e != cudaSuccess) return launch_status_report(e);
   }
+  if (A.unit_ctas) return launch_status();
   const cudaError_t e = launch_chained(scored_merge_kernel, (unsigned)(entries * Hkv),
                                        kMergeThreads, 0, s, A);
   if (e != cudaSuccess) return launch_status_report(e);

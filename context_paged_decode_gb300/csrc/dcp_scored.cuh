@@ -341,12 +341,98 @@ __device__ __forceinline__ void put_lse(const ScoredArgs& A, const PieceOut& P, 
     A.out_lse[P.row + hh] = lse;
 }
 
+__device__ __forceinline__ float remote_f32(uint32_t cluster_addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cluster_addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 remote_f32x4(uint32_t cluster_addr) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return x;
+}
+
+// A unit that a cluster has whole: each CTA, the lines of CTA `rank` of C, has a part
+// of its tiles and in shared memory that part's result for heads [h0, h0 + heads): their
+// LSE at lse[h * lse_step] and `quads` times four values at o[h * o_step].  Between two
+// cluster barriers the cluster's first kScoredWarps warps call this: as many lanes a
+// column as there are CTAs, each with one CTA's part, a CTA every C-th column.
+__device__ __forceinline__ void join_cluster(const ScoredArgs& A, int e, int g, int h0, int heads,
+                                             int quads, const float* lse, int lse_step,
+                                             const float4* o, int o_step) {
+  const int C = A.unit_ctas, rank = blockIdx.x % C, columns = heads * quads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & (C - 1);
+  PieceOut P;
+  P.whole = true;
+  P.slot = 0;
+  P.row = (int64_t)e * A.Hq + g * A.G;
+  for (int first = warp * 32; first < columns; first += kScoredWarps * 32) {
+    const int own = first + (lane & ~(C - 1)) + rank;
+    const int i = own < columns ? own : 0, h = i / quads;
+    const float l = remote_f32(mapa_shared(smem_u32(lse + h * lse_step), c));
+    const float4 y = remote_f32x4(mapa_shared(smem_u32(o + h * o_step + (i - h * quads)), c));
+    const bool any = l != -INFINITY;   // else it has seen nothing
+    float M = l;
+    for (int x = 1; x < C; x *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    float sum = any ? expf(l - M) : 0.f;
+    for (int x = 1; x < C; x *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    float weight, mine = sum == 0.f ? -INFINITY : M + logf(sum);
+    const float all = with_sink(A.sink, g * A.G + h0 + h, mine, weight);
+    const float w = any ? expf(l - mine) * weight : 0.f;
+    float4 z = any ? make_float4(w * y.x, w * y.y, w * y.z, w * y.w)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 1; x < C; x *= 2) {
+      z.x += __shfl_xor_sync(0xffffffffu, z.x, x);
+      z.y += __shfl_xor_sync(0xffffffffu, z.y, x);
+      z.z += __shfl_xor_sync(0xffffffffu, z.z, x);
+      z.w += __shfl_xor_sync(0xffffffffu, z.w, x);
+    }
+    if (own >= columns || c != 0) continue;
+    put_four(A, P, h0 * quads + i, z);
+    if (i % quads == 0) put_lse(A, P, h0 + h, all);
+  }
+}
+
+constexpr int kUnitCtas = 16;   // of a unit's cluster at most
+
+// As launch_chained, the grid in clusters of a unit's CTAs.
+template <auto kKernel, class... Args>
+inline cudaError_t launch_scored(const ScoredArgs& A, unsigned block, size_t smem, cudaStream_t s,
+                                 const Args&... args) {
+  if (A.unit_ctas > 8) {   // beyond what every device has: allowed once per device
+    static bool allowed[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool kept = dev >= 0 && dev < 64;
+    if (!kept || !allowed[dev]) {
+      e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      if (kept) allowed[dev] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)A.ctas);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)A.unit_ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = A.unit_ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kKernel, args...);
+}
+
 // Which kernel a cache takes: the tensor-core kernel (dcp_scored_mma.cu) or
 // the one for any type and shape (dcp_scored.cu).
 enum CacheKind { kCacheF32, kCacheBf16, kCacheE4m3 };
-// CTAs of a unit where that is better than cutting the line, else 0: `tiles` is
-// the most that a unit can have.
-int scored_mma_unit_ctas(int d, int G, CacheKind kind, int64_t units, int64_t tiles);
 bool scored_mma_ok(const ScoredArgs& A, CacheKind kind, bool q_bf16);
 int scored_mma_wave(int d, int G, CacheKind kind);   // CTAs that run at once
 int launch_scored_mma(const ScoredArgs& A, CacheKind kind, cudaStream_t s);

@@ -90,21 +90,6 @@ constexpr int kScoredStuck = 1 << 20;   // err_count increment for a wait that t
 // filling its own ring had a quarter of its instructions for that, and what
 // bounded the kernel was the length of a warp's chain of instructions.)
 constexpr int kScoredThreads = (kScoredWarps + 1) * 32;
-constexpr int kUnitCtas = 16;   // of a unit's cluster at most
-
-__device__ __forceinline__ float remote_f32(uint32_t cluster_addr) {
-  float x;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cluster_addr) : "memory");
-  return x;
-}
-__device__ __forceinline__ float4 remote_f32x4(uint32_t cluster_addr) {
-  float4 x;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-               : "r"(cluster_addr)
-               : "memory");
-  return x;
-}
 
 __device__ __forceinline__ void sync_users() {   // the warps that use tiles
   asm volatile("bar.sync 1, %0;" ::"n"(kScoredWarps * 32) : "memory");
@@ -622,37 +607,8 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
     if (t0 == t1 && tid < A.G) s_ml[tid * kScoredWarps * 4 + kScoredWarps] = -INFINITY;
     __syncwarp();
     cluster_sync();
-    PieceOut P;
-    P.whole = true;
-    P.slot = 0;
-    P.row = (int64_t)e0 * A.Hq + g * A.G;
-    // as many lanes a column as the cluster has CTAs, each with one CTA's part
-    const int C = A.unit_ctas, columns = A.G * (D / 4), c = lane & (C - 1);
-    for (int first = warp * 32; first < columns; first += kScoredWarps * 32) {
-      const int own = first + (lane & ~(C - 1)) + rank;
-      const int i = own < columns ? own : rank, hh = i / (D / 4);
-      const float l = remote_f32(mapa_shared(smem_u32(s_ml + hh * kScoredWarps * 4 + kScoredWarps), c));
-      const float4 y = remote_f32x4(mapa_shared(smem_u32(s_o) + i * 16, c));
-      const bool any = l != -INFINITY;   // else it has seen nothing
-      float M = l;
-      for (int x = 1; x < C; x *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-      float sum = any ? expf(l - M) : 0.f;
-      for (int x = 1; x < C; x *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      float weight, lse = sum == 0.f ? -INFINITY : M + logf(sum);
-      const float all = with_sink(A.sink, g * A.G + hh, lse, weight);
-      const float w = any ? expf(l - lse) * weight : 0.f;
-      float4 z = any ? make_float4(w * y.x, w * y.y, w * y.z, w * y.w)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = 1; x < C; x *= 2) {
-        z.x += __shfl_xor_sync(0xffffffffu, z.x, x);
-        z.y += __shfl_xor_sync(0xffffffffu, z.y, x);
-        z.z += __shfl_xor_sync(0xffffffffu, z.z, x);
-        z.w += __shfl_xor_sync(0xffffffffu, z.w, x);
-      }
-      if (own >= columns || c != 0) continue;
-      put_four(A, P, i, z);
-      if (i % (D / 4) == 0) put_lse(A, P, hh, all);
-    }
+    join_cluster(A, e0, g, 0, A.G, D / 4, s_ml + kScoredWarps, kScoredWarps * 4,
+                 reinterpret_cast<const float4*>(s_o), D / 4);
     __syncwarp();
     cluster_sync();   // all have read what is in this CTA
   } else if (A.unit_ctas == 1 && t0 == t1) {   // nothing is seen
@@ -696,22 +652,6 @@ static bool encode_rows(CUtensorMap* map, const void* base, uint64_t row, uint64
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Allow clusters of sixteen CTAs, once per device.
-template <int D, bool E8, int NT, bool kFormed>
-static bool allow_wide() {
-  static bool done[64] = {false};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  if (dev >= 0 && dev < 64 && done[dev]) return true;
-  if (cudaFuncSetAttribute(scored_mma_kernel<D, E8, NT, kFormed>,
-                           cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-    cudaGetLastError();   // not sticky: leave no error for the next call to misread
-    return false;
-  }
-  if (dev >= 0 && dev < 64) done[dev] = true;
-  return true;
-}
-
 template <int D, bool E8, int NT, bool kFormed>
 static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
   using Z = Shape<D, E8, NT>;
@@ -723,21 +663,8 @@ static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
     if (!encode_rows(&maps.k[r], A.k.ptr[r], Z::kRowBytes, rows) ||
         !encode_rows(&maps.v[r], A.v.ptr[r], Z::kRowBytes, rows))
       return DCP_ECUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)A.ctas);
-  cfg.blockDim = dim3(kScoredThreads);
-  cfg.dynamicSmemBytes = Z::smem(A.G);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // as launch_chained
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)A.unit_ctas;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = A.unit_ctas > 1 ? 2 : 1;
-  if (A.unit_ctas > 8 && !allow_wide<D, E8, NT, kFormed>()) return DCP_ECUDA;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, scored_mma_kernel<D, E8, NT, kFormed>, A, maps);
+  const cudaError_t e = launch_scored<scored_mma_kernel<D, E8, NT, kFormed>>(
+      A, kScoredThreads, Z::smem(A.G), s, A, maps);
   return e == cudaSuccess ? launch_status() : launch_status_report(e);
 }
 
@@ -767,28 +694,6 @@ int scored_mma_wave(int d, int G, CacheKind kind) {
                   : (e8 ? one_wave<64, true, 2>(G) : one_wave<64, false, 2>(G));
   return G <= 8 ? (e8 ? one_wave<128, true, 1>(G) : one_wave<128, false, 1>(G))
                 : (e8 ? one_wave<128, true, 2>(G) : one_wave<128, false, 2>(G));
-}
-
-// A unit whole in a cluster of up to sixteen CTAs needs no plan and no second
-// kernel: that is worth kJoinTiles tiles a warp, which the cluster may have more
-// than an even cut of the line would give.  In 8 bits, 32/8 heads of 128, one
-// request of 300 and 3000 tokens takes 7.4 and 10.7 us in clusters of eight, 10.9
-// and 12.3 by the line, and one of 6000 (12 tiles a warp) 15.6 and 12.4; 16
-// requests of 1000 in clusters of two 13.0 and 16.5.
-int scored_mma_unit_ctas(int d, int G, CacheKind kind, int64_t units, int64_t tiles) {
-  constexpr int64_t kJoinTiles = 8;
-  const int64_t wave = scored_mma_wave(d, G, kind);
-  // clusters that run at once, by cudaOccupancyMaxActiveClusters: larger ones leave gaps
-  auto fits = [&](int c) {
-    return units * c * 1000 <= wave * (c == 16 ? 700 : c == 8 ? 890 : c == 4 ? 960 : 1000);
-  };
-  int c = kUnitCtas;
-  auto few = [&](int half) { return tiles <= (half == 8 ? 4 : 3) * kScoredWarps * half; };
-  while (c > 1 && (!fits(c) || few(c / 2))) c /= 2;
-  if (!fits(c)) return 0;
-  const int64_t here = (tiles + kScoredWarps * c - 1) / (kScoredWarps * c);
-  const int64_t even = tiles * units / (kScoredWarps * wave);
-  return here - even <= kJoinTiles ? c : 0;
 }
 
 }  // namespace dcp

@@ -149,6 +149,12 @@ CASES = [
     (BF16, BF16, 3, 3, 128, 2, 1, 1, [301, 11], {}),
     (F32, F32, 16, 1, 256, 2, 16, 1, [301, 11], {}),
     (E4M3, F32, 2, 2, 32, 2, 16, 1, [301, 11], dict(alibi=True)),
+    # several passes of heads over one cluster's tokens, the last of them not full
+    (F32, F32, 16, 1, 64, 2, 16, 1, [300, 0, 37, 1], dict(sink=True)),
+    (E4M3, F32, 14, 2, 64, 2, 16, 1, [200, 5], dict(alibi=True, cap=30.0)),
+    # one request long enough for clusters of sixteen
+    (E4M3, BF16, 8, 2, 128, 2, 16, 1, [3001], dict(cap=30.0, sink=True)),
+    (BF16, BF16, 16, 1, 64, 2, 16, 1, [3001], {}),
 ]
 
 
@@ -358,6 +364,17 @@ def test_more_requests_than_threads(lib, cache):
     po, pl = p.partial(p.layout, p.q, p.kv, p.dlens, p.scale, p.form)
     for r in range(2):
         p.check(po[r], pl[r], rank=r)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
+def test_windows_of_more_units_than_ctas(lib, cache):
+    """Windows and kept tokens where units are cut anywhere, and several lie in one CTA."""
+    q = F32 if cache == F32 else BF16
+    rng = np.random.default_rng(4)
+    lens = [int(n) for n in rng.choice([0, 1, 20, 45, 64, 333, 500], 170)]
+    p = Problem(lib, cache, q, 8, 4, 64, 2, 16, 1, lens, window=37, prefix=5, docs=True, cap=20.0,
+                sink=True)
+    p.check(*p.run())
 
 
 def test_calls_at_once(lib):
