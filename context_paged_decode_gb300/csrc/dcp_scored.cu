@@ -1,8 +1,8 @@
 // Scored decode attention: one query per request over the sharded paged cache
 // in 16, 32 or 8 bits, with scores that may be capped, biased by distance, or
 // limited to a window, the document's first tokens and the document.  This
-// file has the kernel for any type and shape, the merge of units that were
-// cut, and the entry points; dcp_scored_mma.cu has the tensor-core kernel.
+// file has the kernel for any type and shape, the choice between units whole in a
+// cluster and units cut anywhere, the merge of the latter, and the entry points; dcp_scored_mma.cu has the tensor-core kernel.
 //
 // With L tokens, the query at position L - 1, and x the position of a key:
 //     t = scale q.k;  t = cap tanh(t / cap);  t = t - slope[h] (L - 1 - x)
@@ -50,7 +50,7 @@ constexpr int generic_per_sm(int di) { return di == 8 ? 2 : di == 4 ? 3 : 4; }
 // heads' sums over the lanes are exchanged so that each lane gets one head's
 // score, which it forms alone, and the weights go round again: with every score
 // formed by all eight lanes two requests of up to 2048 tokens, 32/8 heads of 128 in
-// fp32, took 40 us, not 26.  Bound by its instructions and few warps an SM.
+// fp32, took 40 us, not 26 (by the line both; in clusters 22).  Bound by its instructions and few warps an SM.
 template <int kKind, int DI, int HP>
 __global__ void __launch_bounds__(kScoredWarps * 32, generic_per_sm(DI))
 scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
@@ -581,7 +581,11 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
   const int64_t kept = f.window > 0 ? (int64_t)f.window + f.prefix : room;
   const int64_t tokens = kept < room ? kept : room;
   const int64_t per_rank = tokens / dcp + 2 * layout.interleave;
-  const int64_t most = apart_ ? per_rank / kRows + 4 : tokens / kRows + 4 * dcp;
+  int64_t most = apart_ ? per_rank / kRows + 4 : tokens / kRows + 4 * dcp;
+  // Of packed documents half a table is expected: 16 in up to 9001 tokens, 16/1 heads of
+  // 64, take 12.7 us in clusters and 16.2 by the line; 16 requests that fill 9000 tokens,
+  // 16/1 heads of 128, would take 27 and 24.
+  if (f.first) most = (most + 1) / 2;
   A.unit_ctas = unit_ctas_of(mma, d, A.G, wave, entries * Hkv, most);
   if (A.unit_ctas) A.ctas = (int)(entries * Hkv) * A.unit_ctas;
   A.part_lse = (float*)w;

@@ -186,8 +186,8 @@ struct Line {
 
 // Every thread of the CTA calls it; all get the same, and s_before[i] is what
 // lies in front of thread i's entries, in tiles of a head.  The lengths are read
-// by every CTA: a plan of one CTA in front would cost a launch (a call of one
-// request takes some 12 us in all).
+// by every CTA: a plan of one CTA in front would cost a launch, of the 12 to 16
+// us that the shortest calls take that are cut by the line.
 template <int kThreads>
 __device__ __forceinline__ Line plan_line(const ScoredArgs& A, int chunk, int* s_before) {
   __shared__ int s_sum[kThreads / 32];
