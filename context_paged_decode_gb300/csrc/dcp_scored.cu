@@ -510,8 +510,8 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
                        int32_t* err, cudaStream_t s) {
   if (!shape_ok(layout, B, Hq, Hkv, d) || (dtype != DCP_F32 && dtype != DCP_BF16) ||
       (out_dtype != DCP_F32 && out_dtype != DCP_BF16) || kv.nb < 0 || kv.max_vb < 0 ||
-      kv.bt_stride < 0 || !isfinite(scale) || !isfinite(f.cap) || f.cap < 0.f || f.window < 0 ||
-      f.prefix < 0)
+      kv.bt_stride < 0 || !isfinite(scale) || !(f.cap == 0.f || isnormal(f.cap)) ||
+      f.cap < 0.f || f.window < 0 || f.prefix < 0)
     return DCP_EINVAL;
   if (B == 0) return DCP_OK;
   const int dcp = layout.dcp_size;
@@ -527,7 +527,8 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
   // the most tiles a full table can have: a rank's first and last of each of two runs may be part
   const int64_t room = (int64_t)kv.max_vb * layout.block_size * dcp;
   const int64_t tiles = (room / kRows + 4 * dcp) * B * Hkv;
-  if (tiles >= (int64_t(1) << 30)) return DCP_EUNSUPPORTED;
+  // a rank's tokens and a tile's rest fit in 31 bits (and `tiles`, then, in 64)
+  if (room > INT32_MAX - 256 || tiles >= (int64_t(1) << 30)) return DCP_EUNSUPPORTED;
   const size_t need = workspace_bytes_of(entries, Hq, Hkv, d);
   if (!ws || ws_bytes < need) return DCP_EWORKSPACE;
   const int64_t es = dtype == DCP_F32 ? 4 : 2, os = out_dtype == DCP_F32 ? 4 : 2;

@@ -796,11 +796,12 @@ typedef struct {
  * Keys and values of tokens that are not seen do not count, whatever they hold.
  * Pages whose table entry is outside [0, num_blocks) are skipped and counted,
  * once or more.
- * Supported as dcp_decode_gqa; cap >= 0, window >= 0, prefix >= 0; q, out, the
- * workspace and the pools 16-byte aligned.  out, out_lse and the workspace lie
- * apart from one another and from what is read, and no other call may use the
- * workspace at the same time (two captured graphs that share one may not
- * overlap).  Results do not depend on timing.
+ * Supported as dcp_decode_gqa; cap 0 or at least 2^-126, window >= 0, prefix >=
+ * 0; q, out, the workspace and the pools 16-byte aligned; tables with room for
+ * fewer than 2^31 - 256 tokens of a request, and 2^34 of all requests and heads.
+ * out, out_lse and the workspace lie apart from one another and from what is
+ * read, and no other call may use the workspace at the same time (two captured
+ * graphs that share one may not overlap).  Results do not depend on timing.
  */
 int dcp_scored_decode_gqa(dcp_layout_t layout, const void* q, int32_t num_reqs,
                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,

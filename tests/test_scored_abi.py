@@ -44,6 +44,7 @@ def test_attention(dcp, eight, partial):  # noqa: F811
            dict(Hq=34, Hkv=2), dict(Hkv=0), dict(d=0), dict(d=48), dict(d=288), dict(dt=2),
            dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(lens=None),
            dict(out=None), dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf")),
+           dict(cap=1e-39),   # 1 / cap is beyond 32 bits
            dict(window=-1), dict(prefix=-1), dict(cache=make(dcp, nb=-1)),
            dict(cache=make(dcp, max_vb=-1)), dict(cache=make(dcp, n=1)),
            # outputs, workspace and what is read lie apart
@@ -58,7 +59,11 @@ def test_attention(dcp, eight, partial):  # noqa: F811
     assert call(ws=None) == EWORKSPACE and call(n=100) == EWORKSPACE
     for b in (dict(q=C.c_void_p((1 << 20) + 2)), dict(out=C.c_void_p((1 << 50) + 8)),
               dict(ws=C.c_void_p((1 << 51) + 8)), dict(cache=make(dcp, base=(1 << 40) + 8)),
-              dict(B=1 << 29)):
+              dict(B=1 << 29),
+              # room for more tokens of a request than 31 bits count, products beyond 63 bits
+              dict(B=1, Hkv=1, cache=make(dcp, max_vb=1 << 26)),
+              dict(layout=dcp.Layout(2, 1 << 28, 1), B=4096, Hq=8192, Hkv=8192,
+                   cache=make(dcp, nb=0, max_vb=(1 << 31) - 1))):
         assert call(**b) == EUNSUPPORTED, b
 
 
