@@ -252,7 +252,7 @@ q8_append_kernel(const __grid_constant__ AppendArgs A) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           w[k] = f32x4_e4m3(quad<T>(times<T>(y[k * kLoads / 4], inv), k * kLoads % 4 ? 1 : 0));
-        *reinterpret_cast<uint4*>(to + i * A.d) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(to + (int64_t)i * A.d) = make_uint4(w[0], w[1], w[2], w[3]);
       });
     else
       each_row(true, [&](const uint4(&y)[kLoads], int i) {
@@ -262,17 +262,21 @@ q8_append_kernel(const __grid_constant__ AppendArgs A) {
           const float4 z = quad<T>(y[k * kLoads / 4], k * kLoads % 4 ? 1 : 0);
           w[k] = f32x4_e4m3(make_float4(z.x / now, z.y / now, z.z / now, z.w / now));
         }
-        *reinterpret_cast<uint4*>(to + i * A.d) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(to + (int64_t)i * A.d) = make_uint4(w[0], w[1], w[2], w[3]);
       });
-    if (grows) {   // the page's other places, 4 numbers a lane
+    if (grows) {   // the page's other places
       const float by = old / now;
-      const int quads = A.d / 4;
-      for (int i = lane; i < A.S.bs * quads; i += 32) {
-        const int l = i / quads;
+      for (int l = row; busy && l < A.S.bs; l += rows) {
         if (l >= pl && l < pl + pn) continue;
-        uint32_t* to = reinterpret_cast<uint32_t*>(dst) + i;
-        const float4 y = e4m3x4_f32(*to);
-        *to = f32x4_e4m3(make_float4(y.x * by, y.y * by, y.z * by, y.w * by));
+        uint4* const at = reinterpret_cast<uint4*>(dst + (int64_t)l * A.d) + chunk;
+        const uint4 held4 = *at;
+        uint32_t w[4] = {held4.x, held4.y, held4.z, held4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 y = e4m3x4_f32(w[k]);
+          w[k] = f32x4_e4m3(make_float4(y.x * by, y.y * by, y.z * by, y.w * by));
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
     __syncwarp();
