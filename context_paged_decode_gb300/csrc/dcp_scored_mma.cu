@@ -352,7 +352,10 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
           ks_ = both.x;
           const int bits = __float_as_int(both.y), mant = bits & 0x7fffff;
           vlog = (float)((bits >> 23) - 127);     // exact for a power of two
-          if (mant) vlog += log2f(__int_as_float(mant | 0x3f800000));
+          if ((bits >> 23) == 0)                  // below 2^-126; of 0 -inf, a weight of nothing
+            vlog = log2f(both.y * 0x1p24f) - 24.f;
+          else if (mant)
+            vlog += log2f(__int_as_float(mant | 0x3f800000));
         }
         const bool edge = lo > 0 || hi < kRows;
         if (edge) {   // values that do not count are zeros, so 0 * NaN is not met
@@ -541,7 +544,7 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
         if (hh >= A.G) continue;
         if (gq == 0)
           *reinterpret_cast<float4*>(s_ml + (hh * kScoredWarps + warp) * 4) =
-              E8 ? make_float4(ref[x][h], sum, vref[x][h], vlift[x][h] - kLift)
+              E8 ? make_float4(ref[x][h], sum, vref[x][h], vlift[x][h])
                  : make_float4(ref[x][h], sum, ref[x][h], 0.f);
         float* os = s_o + (warp * A.G + hh) * D;
 #pragma unroll
@@ -555,7 +558,10 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
         }
       }
     sync_users();
-    // a head's four numbers of each warp become its four factors
+    // a head's four numbers of each warp become its four factors, and one for all that is
+    // multiplied first: in one product the lift and a long request's sum would take a values'
+    // scale of 2^-110 out of 32 bits.  The factors are held times 2^-kSlack, as a score may
+    // pass its reference by that beside a scale of 2^127.
     if (tid < A.G) {
       float4* const ml = reinterpret_cast<float4*>(s_ml) + tid * kScoredWarps;
       float M = kNone, Ls = 0.f;
@@ -578,21 +584,24 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
       float* const to = reinterpret_cast<float*>(ml);
 #pragma unroll
       for (int i = 0; i < kScoredWarps; ++i)
-        to[i] = any && w[i].y != 0.f ? exp2f((w[i].z - M) + w[i].w) / Ls * weight : 0.f;
+        to[i] = any && w[i].y != 0.f ? exp2f((w[i].z - M) + (w[i].w - kSlack)) : 0.f;
+      to[kScoredWarps + 1] = any ? exp2f(kSlack - (E8 ? kLift : 0.f)) / Ls * weight : 0.f;
     }
     sync_users();
     for (int i = tid; i < A.G * (D / 4); i += kScoredWarps * 32) {
-      const float4 f = *reinterpret_cast<const float4*>(s_ml + i / (D / 4) * kScoredWarps * 4);
+      const float* const of_head = s_ml + i / (D / 4) * kScoredWarps * 4;
+      const float4 f = *reinterpret_cast<const float4*>(of_head);
+      const float all = of_head[kScoredWarps + 1];
       const float4* os = reinterpret_cast<const float4*>(s_o) + i;
       const float fs[4] = {f.x, f.y, f.z, f.w};
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kScoredWarps; ++w) {
         const float4 x = os[w * A.G * (D / 4)];
-        y.x = fmaf(x.x, fs[w], y.x);
-        y.y = fmaf(x.y, fs[w], y.y);
-        y.z = fmaf(x.z, fs[w], y.z);
-        y.w = fmaf(x.w, fs[w], y.w);
+        y.x = fmaf(x.x * all, fs[w], y.x);
+        y.y = fmaf(x.y * all, fs[w], y.y);
+        y.z = fmaf(x.z * all, fs[w], y.z);
+        y.w = fmaf(x.w * all, fs[w], y.w);
       }
       if (A.unit_ctas > 1)
         reinterpret_cast<float4*>(s_o)[i] = y;   // for the cluster, over what only it has read
