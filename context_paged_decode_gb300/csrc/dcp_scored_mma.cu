@@ -10,7 +10,9 @@
 //
 // e4m3 numbers become fp16, which holds them exactly.  The query is fp16 too,
 // scaled by a power of two for each head so that its largest entry is near 2^14:
-// bf16's eight bits fit, and only entries below 2^-38 of the largest lose any.
+// bf16's eight bits fit down to 2^-31 of the largest; smaller entries lose bits
+// of theirs (fp16's last step is 2^-24 of one, 2^-38 of the largest), and what is
+// below half of that step becomes 0.
 // The page's scale of the keys goes to the score, that of the values to the
 // weight (below).  Products accumulate in fp32; scores, their maxima and sums
 // are fp32.
@@ -304,9 +306,9 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
                                  fmaxf(fabsf(bf16_lo(qb[x][ks][1])), fabsf(bf16_hi(qb[x][ks][1])))));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^(14 - exponent of the largest); without a finite one, or with none, 1
+        // 2^(14 - exponent of the largest); beside an infinity the others stay finite; all 0 or NaN: 1
         const int ex = (__float_as_int(top) >> 23) - 127;
-        if (top > 0.f && ex < 128) up = __int_as_float((min(14 - ex, 126) + 127) << 23);
+        if (top > 0.f) up = __int_as_float((min(14 - ex, 126) + 127) << 23);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll

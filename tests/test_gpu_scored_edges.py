@@ -47,3 +47,51 @@ def test_values_scales_of_any_size(lib, q, room, lens):
         t[..., 1] = 0.0
     out, lse = p.run(out_dtype=F32)
     assert (out == 0).all() and torch.isfinite(lse).all()
+
+
+def one_hot(p, dims):
+    """Every token's key is 1 at its number modulo `dims`, else 0, with scales of 1."""
+    for r, pool in enumerate(p.kv.k_pools):
+        pool.copy_(torch.zeros(pool.shape, device="cuda").to(E4M3))
+        p.kv.scales[r][..., 0] = 1.0
+    one = torch.ones(1, device="cuda").to(E4M3).view(torch.uint8)
+    for b in range(len(p.lens)):
+        for pos in range(p.lens[b]):
+            r, vb, loc = R.place(pos, p.dcp, p.bs, p.I)
+            p.kv.k_pools[r].view(torch.uint8)[int(p.bt[r, b, vb]), :, loc, pos % dims] = one
+
+
+@pytest.mark.parametrize("q", [BF16, F32], ids=str)
+def test_small_entries_of_a_query(lib, q):
+    """A token whose key picks out one entry of the query, down to 2^-45 of the largest: exact to
+    2^-31 of it, and off by at most half of 2^-38 of it below (bf16 queries)."""
+    p = Problem(lib, E4M3, q, 1, 1, 64, 1, 16, 1, [1] * 48)
+    one_hot(p, 1)
+    p.q.zero_()
+    p.q[:, 0, 1] = 3.0                     # the largest; no key has that dimension
+    vals = torch.tensor([1.2890625 * 2.0 ** (1 - e) for e in range(48)])
+    p.q[:, 0, 0] = vals.to(q).cuda()
+    x = p.q[:, 0, 0].double().cpu().numpy()
+    for scale in (1.0, 2.0 ** 40):         # the smallest of them are scores of weight with this
+        out, lse = p.decode(p.layout, p.q, p.kv, p.dlens, scale, None)
+        got = lse[:, 0].double().cpu().numpy() / scale
+        off = 0.0 if q == F32 else np.where(x >= 3.0 * 2.0 ** -31, 0.0, 2.0 * 2.0 ** -39)
+        # log2(e), ln(2) and the products with them: 6 roundings at most
+        assert (np.abs(got - x) <= np.abs(x) * 6 * 2.0 ** -24 + off).all(), (scale, got, x)
+
+
+@pytest.mark.parametrize("q", [BF16, F32], ids=str)
+def test_infinities_of_a_query(lib, q):
+    """Beside an infinite entry the others stay finite: a score of -infinity has no weight."""
+    p = Problem(lib, E4M3, q, 2, 1, 64, 1, 16, 1, [20])
+    one_hot(p, 1)
+    for pool in p.kv.k_pools:              # a second dimension that all keys have
+        pool.view(torch.uint8)[..., 1] = torch.ones(1, device="cuda").to(E4M3).view(torch.uint8)
+    p.q.zero_()
+    p.q[0, 0, 0] = -float("inf")
+    p.q[0, 0, 1] = 2.0 ** 100              # no infinity of its own
+    p.q[0, 1, 1] = float("nan")
+    sink = torch.tensor([0.5, 0.5], device="cuda")
+    out, lse = p.decode(p.layout, p.q, p.kv, p.dlens, 1.0, None, sink=sink)
+    assert (out[0, 0] == 0).all() and lse[0, 0].item() == 0.5
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
