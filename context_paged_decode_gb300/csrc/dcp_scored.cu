@@ -60,6 +60,7 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
   constexpr int kParts = kScoredWarps * 4;   // sums of their own: four tokens of each warp
   __shared__ __align__(16) float4 s_o[kParts][HP][DI * 8];
   __shared__ float s_m[kParts][HP], s_l[kParts][HP];
+  __shared__ float s_unit[kParts];   // what a part's values are held in units of
   griddep_wait();                // launched chained: the preceding kernel completed
   __shared__ int s_before[kScoredWarps * 32];
   __shared__ float s_lse[HP];
@@ -108,6 +109,9 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
       const float slope =
           A.slopes && h0 + own < A.G ? __ldg(A.slopes + g * A.G + h0 + own) : 0.f;
       float m = kNone, l = 0.f;
+      // 8-bit values are summed in units of the largest power of two of a scale so far: a sum of
+      // values near the largest numbers would leave 32 bits, and so would small ones' weights
+      float unit = 0x1p-126f, per_unit = 0x1p126f;
       float4 o[HP][DI];
 #pragma unroll
       for (int h = 0; h < HP; ++h)
@@ -213,10 +217,17 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
           for (int step = HP; step < 8; step *= 2) dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], step);
           const float x = ok ? formed(A, dot[0] * ks * A.scale, slope, far) : -INFINITY;
           const bool over = x - m > kSlack;
-          if (__any_sync(0xffffffffu, over)) {
-            const float down = over ? exp2f(m - x) : 1.f;
+          const bool larger = kKind == kCacheE4m3 && ok && vs >= 2.f * unit;
+          if (__any_sync(0xffffffffu, over || larger)) {
+            float down = over ? exp2f(m - x) : 1.f;
             if (over) m = x;
             l *= down;
+            if (larger) {
+              const int e = __float_as_int(vs) & 0x7f800000;   // its power of two
+              per_unit = __int_as_float(e == 0x7f000000 ? 0x00400000 : 0x7f000000 - e);
+              down *= unit * per_unit;
+              unit = __int_as_float(e);
+            }
 #pragma unroll
             for (int h = 0; h < HP; ++h) {
               const float d = __shfl_sync(0xffffffffu, down, (lane & 24) | h);
@@ -231,7 +242,7 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
           }
           const float w = exp2f(x - m);
           l += w;
-          const float wv = w * vs;
+          const float wv = kKind == kCacheE4m3 ? w * (vs * per_unit) : w;
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
             const float wh = __shfl_sync(0xffffffffu, wv, (lane & 24) | h);
@@ -252,6 +263,7 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
 #pragma unroll
         for (int i = 0; i < DI; ++i)
           if (i < di) s_o[part][h][sub + 8 * i] = o[h][i];
+      if (sub == 0) s_unit[part] = kKind == kCacheE4m3 ? unit : 1.f;
       if (sub < HP) {
         s_m[part][sub] = m;
         s_l[part][sub] = l;
@@ -280,12 +292,12 @@ scored_generic_kernel(const __grid_constant__ ScoredArgs A, bool q_bf16) {
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int p = 0; p < kParts; ++p) {
-          const float f = s_l[p][hh];
+          const float f = s_l[p][hh], unit_p = s_unit[p];
           const float4 v4 = s_o[p][hh][c];
-          y.x = fmaf(f, v4.x, y.x);
-          y.y = fmaf(f, v4.y, y.y);
-          y.z = fmaf(f, v4.z, y.z);
-          y.w = fmaf(f, v4.w, y.w);
+          y.x = fmaf(f * v4.x, unit_p, y.x);
+          y.y = fmaf(f * v4.y, unit_p, y.y);
+          y.z = fmaf(f * v4.z, unit_p, y.z);
+          y.w = fmaf(f * v4.w, unit_p, y.w);
         }
         if (A.unit_ctas > 1)
           s_o[0][hh][c] = y;   // for the cluster, over what only it has read
