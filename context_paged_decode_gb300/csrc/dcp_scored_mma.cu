@@ -472,8 +472,14 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
               }
             }
         }
-        // weights, and as the B operand of P V
-        uint32_t pb[NT][2];
+        // weights, and as the B operand of P V: of 8 bits in fp16, which is off by 2^-11 of each
+        // at most, an eighth of an output's rounding.  In bf16 they would be off by 2^-8, as
+        // much as the output, so there they are the sum of two numbers, to 2^-15: the upper half
+        // of the 32 bits, and the rest rounded.  The rest is made larger by 2^-24 of the weight,
+        // so that it is not 0, which beside a value of infinity would give NaN.  A second product
+        // a tile costs nothing beside the bytes (a window of 4096 tokens, 32 requests, 90.2 us
+        // with either, bias over whole contexts 74.0).
+        uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
           float p[4];
@@ -484,8 +490,18 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
             l[x][h] += p[i];
             if (E8) p[i] = ex2_ftz((s[x][i] - vref[x][h]) + (vlog - vlift[x][h] + kLift));
           }
-          pb[x][0] = transposed8(E8 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
-          pb[x][1] = transposed8(E8 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float p0 = p[2 * i], p1 = p[2 * i + 1];
+            if (E8) {
+              pb[x][i] = transposed8(pack_f16(p0, p1));
+            } else {
+              const uint32_t hi = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+              pb[x][i] = transposed8(hi);
+              pl[x][i] = transposed8(pack_bf16(fmaf(p0, 0x1p-24f, p0 - bf16_lo(hi)),
+                                               fmaf(p1, 0x1p-24f, p1 - bf16_hi(hi))));
+            }
+          }
         }
         // O^T += V^T P^T.  In 8 bits row j of a tile of 16 dims is dim 2 j, row 8 + j dim 2 j + 1.
         if (E8) {
@@ -509,7 +525,10 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
             uint32_t a[4];
             ldsm_x4_t(Z::on(vb + v_at, i), a[0], a[1], a[2], a[3]);
 #pragma unroll
-            for (int x = 0; x < NT; ++x) mma_16816<E8>(o[x][i], a, pb[x][0], pb[x][1]);
+            for (int x = 0; x < NT; ++x) {
+              mma_16816<E8>(o[x][i], a, pb[x][0], pb[x][1]);
+              mma_16816<E8>(o[x][i], a, pl[x][0], pl[x][1]);
+            }
           }
         }
       }

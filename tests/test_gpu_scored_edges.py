@@ -95,3 +95,76 @@ def test_infinities_of_a_query(lib, q):
     out, lse = p.decode(p.layout, p.q, p.kv, p.dlens, 1.0, None, sink=sink)
     assert (out[0, 0] == 0).all() and lse[0, 0].item() == 0.5
     assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+
+
+def check_tight(p, out, lse, rounding, floor):
+    """The bounds of a kernel in 32 bits whose weights are off by `rounding` relatively, and by
+    `floor` of the largest weight times its page's scale of the values."""
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, n in enumerate(p.lens):
+        x, k, v = p.rows[b]
+        for h in range(p.Hq):
+            g = h // p.G
+            sink = p.sink[h] if p.sink is not None else None
+            eo, el, to, tl = S.attend(F32, out.dtype, p.q64[b, h], k[g], v[g], x, n, p.scale, p.cap,
+                                      p.slopes[h], sink)
+            t = k[g] @ p.q64[b, h] * p.scale
+            t = p.cap * np.tanh(t / p.cap) if p.cap else t
+            w = np.exp(t - p.slopes[h] * (n - 1 - x) - el)
+            to = to + 1.05 * rounding * (w @ np.abs(v[g])) + floor * w.max(initial=0.0) * np.abs(v[g]).sum(0)
+            what = f"request {b} head {h} of {n} tokens"
+            assert (np.abs(o[b, h] - eo) <= to).all(), (what, (np.abs(o[b, h] - eo) / to).max())
+            assert abs(l[b, h] - el) <= tl, what
+
+
+# cache, q, d, rounding of the weights, floor.  On the tensor cores bf16 caches take weights in two
+# bf16 terms, the upper bits and the rest, which is at most 2^-7 of the weight and off by 2^-8 of it,
+# together 2^-15 (and 2^-24); 8-bit ones in fp16, held times 2^11 (at least,
+# for the largest), so that what falls below fp16's smallest step loses 2^-25 of one at most: 2^-36
+# of the largest, and 2^-30 where scales differ by 2^6.  On the CUDA cores nothing is rounded.
+WEIGHTS = [(BF16, BF16, 128, 1.01 * 2.0 ** -15, 0.0), (BF16, BF16, 64, 1.01 * 2.0 ** -15, 0.0),
+           (E4M3, BF16, 128, 2.0 ** -11, 2.0 ** -30), (E4M3, BF16, 64, 2.0 ** -11, 2.0 ** -30),
+           (E4M3, F32, 128, 0.0, 0.0), (BF16, BF16, 96, 0.0, 0.0), (F32, F32, 128, 0.0, 0.0)]
+
+
+@pytest.mark.parametrize("room", [0, 1 << 20])
+@pytest.mark.parametrize("more", [{}, dict(cap=20.0, alibi=True, sink=True)], ids=["", "formed"])
+@pytest.mark.parametrize("case", WEIGHTS, ids=lambda c: f"{str(c[0])[6:]}-q{str(c[1])[6:]}-d{c[2]}")
+def test_roundings_of_the_weights(lib, case, room, more):
+    cache, q, d, rounding, floor = case
+    for Hq, Hkv in ((8, 2), (16, 1)):
+        p = Problem(lib, cache, q, Hq, Hkv, d, 2, 16, 1, [1500, 37, 1], room=room, seed=6, **more)
+        check_tight(p, *p.run(out_dtype=F32), rounding, floor)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
+@pytest.mark.parametrize("window, prefix", [(700, 5), (100000, 0), (2500, 300)])
+def test_windows_cut_anywhere(lib, cache, window, prefix):
+    """Heads of 128 with a window and kept tokens: units too long for a cluster and more units than
+    CTAs, whole and by ranks."""
+    q = F32 if cache == F32 else BF16
+    rng = np.random.default_rng(window)
+    lens = [3000, 2999] if window > 1000 else [int(n) for n in rng.choice([0, 1, 20, 333, 900], 150)]
+    p = Problem(lib, cache, q, 8, 4, 128, 2, 16, 1, lens, window=window, prefix=prefix, cap=20.0,
+                sink=True, room=1 << 20)
+    p.check(*p.run())
+    po, pl = p.partial(p.layout, p.q, p.kv, p.dlens, p.scale, p.form)
+    for r in range(2):
+        p.check(po[r], pl[r], rank=r)
+
+
+@pytest.mark.parametrize("cache, d", [(BF16, 128), (BF16, 64), (BF16, 96), (F32, 128)], ids=str)
+@pytest.mark.parametrize("room", [0, 1 << 20])
+def test_infinite_values(lib, cache, d, room):
+    """A value of infinity gives one, whatever the weight's bits (a weight of 1 among them)."""
+    p = Problem(lib, cache, F32 if cache == F32 else BF16, 8, 2, d, 2, 16, 1, [300, 40, 1], room=room)
+    for b, pos, c, x in ((0, 200, 3, float("inf")), (0, 7, 9, -float("inf")), (2, 0, 5, float("inf"))):
+        r, vb, loc = R.place(pos, 2, 16, 1)
+        p.kv.v_pools[r][int(p.bt[r, b, vb]), :, loc, c] = x
+    out, lse = p.run()
+    assert (out[0, :, 3] == float("inf")).all() and (out[0, :, 9] == -float("inf")).all()
+    assert (out[2, :, 5] == float("inf")).all()
+    rest = torch.ones(d, dtype=torch.bool, device="cuda")
+    rest[[3, 9, 5]] = False
+    assert torch.isfinite(out[..., rest]).all() and torch.isfinite(out[1]).all()
+    assert torch.isfinite(lse).all()
