@@ -97,6 +97,37 @@ def test_infinities_of_a_query(lib, q):
     assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
 
 
+@pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
+@pytest.mark.parametrize("cap", [1.0, 50.0])
+def test_a_capped_score(lib, cache, cap):
+    """Requests of one token: the LSE is the score, cap * tanh(y / cap), over the range of y."""
+    n = 1500
+    y = np.exp(np.linspace(np.log(1e-3), np.log(12.0), n)) * cap
+    y[::2] *= -1
+    p = Problem(lib, cache, F32 if cache == F32 else BF16, 1, 1, 64, 1, 16, 1, [1] * n)
+    p.q.zero_()
+    pages = p.bt[0, :, 0].long()
+    for pool in p.kv.k_pools:
+        pool.copy_(torch.zeros(pool.shape, device="cuda").to(cache))
+    if cache == E4M3:         # y is a page's scale
+        p.q[:, 0, 0] = torch.from_numpy(np.sign(y)).to(p.q.dtype).cuda()
+        p.kv.scales[0][pages, 0, 0] = torch.from_numpy(np.abs(y)).float().cuda()
+        p.kv.k_pools[0].view(torch.uint8)[pages, 0, 0, 0] = torch.ones(1).to(E4M3).view(torch.uint8).cuda()
+        y = (p.q[:, 0, 0].double() * p.kv.scales[0][pages, 0, 0].double()).cpu().numpy()
+    else:                     # of bf16 a product of two numbers, exactly; in 32 bits y itself
+        q = torch.from_numpy(y).to(p.q.dtype)
+        k = (torch.from_numpy(y) / q.double()).to(BF16).to(cache)
+        p.q[:, 0, 0] = q.cuda()
+        p.kv.k_pools[0][pages, 0, 0, 0] = k.cuda()
+        y = (q.double() * k.double()).numpy()
+    out, lse = p.decode(p.layout, p.q, p.kv, p.dlens, 1.0, lib.Scores(cap=cap))
+    t = cap * np.tanh(y / cap)
+    off = np.abs(lse[:, 0].double().cpu().numpy() / t - 1) * 2.0 ** 24
+    # in units of 2^-24: tanh 8; y 1 / cap, the constant 1 / cap and the product with the cap 1 each
+    # (nothing for a cap of 1); the changes to base 2 and back 1 each, and their constants 1
+    assert off.max() <= (11 if cap == 1.0 else 14), (off.max(), y[off.argmax()])
+
+
 def check_tight(p, out, lse, rounding, floor):
     """The bounds of a kernel in 32 bits whose weights are off by `rounding` relatively, and by
     `floor` of the largest weight times its page's scale of the values."""
