@@ -27,3 +27,19 @@ def test_a_page_beyond_31_bits(lib):
     want = (x[pos].float() / scale).to(E4M3).float() * scale
     for got in lib.q8_gather_gqa(L, kv, req, pos, dtype=F32):
         assert torch.equal(got, want)
+
+
+def test_bad_requests_leave_the_cache_alone(lib):
+    """Requests whose rows leave those given, in front or behind: nothing of them is written, and
+    what the others write is as ever."""
+    from tests.test_gpu_q8_cache import Cache, rows
+
+    rng = np.random.default_rng(15)
+    c = Cache(lib, rng, 2, 64, 2, 16, 1, [200] * 6)
+    k, v = rows(rng, 60, 2, 64, BF16, True)
+    start, ctx = [-4, 10, 10, 30, 40, 45, 70], [9, 0, 0, 0, 3, 0]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.append(k, v, start, ctx, err=err)
+    c.model(k, v, start, ctx, skip=(0, 5))
+    c.check()
+    assert err.item() == 2
