@@ -433,19 +433,34 @@ static int generic_ctas(int d) { return num_sms() * generic_per_sm(d <= 64 ? 2 :
 // Heads of a pass over the tokens: 8 values a lane of 2 heads fit into registers.
 constexpr int heads_a_pass(int d, int G) { return G == 1 ? 1 : d <= 128 ? 4 : 2; }
 
-template <int kKind, int DI>
-static cudaError_t launch_generic(const ScoredArgs& A, bool q_bf16, cudaStream_t s) {
-  constexpr unsigned block = kScoredWarps * 32;
-  constexpr int HP = heads_a_pass(DI * 32, 2);
-  return A.G == 1 ? launch_scored<scored_generic_kernel<kKind, DI, 1>>(A, block, 0, s, A, q_bf16)
-                  : launch_scored<scored_generic_kernel<kKind, DI, HP>>(A, block, 0, s, A, q_bf16);
-}
+// The kernel's variants, each with what the host asks of it.
+template <int kKind, int DI, int HP>
+struct Generic {
+  static constexpr auto kKernel = scored_generic_kernel<kKind, DI, HP>;
+  static constexpr unsigned kBlock = kScoredWarps * 32;
 
-template <int kKind>
-static cudaError_t launch_generic(const ScoredArgs& A, bool q_bf16, cudaStream_t s) {
-  if (A.d <= 64) return launch_generic<kKind, 2>(A, q_bf16, s);
-  if (A.d <= 128) return launch_generic<kKind, 4>(A, q_bf16, s);
-  return launch_generic<kKind, 8>(A, q_bf16, s);
+  static int clusters(int ctas) { return clusters_at_once<kKernel>(ctas, 0, kBlock, 0); }
+
+  static int launch(const ScoredArgs& A, bool q_bf16, cudaStream_t s) {
+    const cudaError_t e = launch_scored<kKernel>(A, kBlock, 0, s, A, q_bf16);
+    return e == cudaSuccess ? launch_status() : launch_status_report(e);
+  }
+};
+
+// `use` of the variant that a call takes.
+template <int kKind, class Use>
+static int with_generic(const ScoredArgs& A, Use&& use) {
+  if (A.d <= 64)
+    return A.G == 1 ? use(Generic<kKind, 2, 1>()) : use(Generic<kKind, 2, heads_a_pass(64, 2)>());
+  if (A.d <= 128)
+    return A.G == 1 ? use(Generic<kKind, 4, 1>()) : use(Generic<kKind, 4, heads_a_pass(128, 2)>());
+  return A.G == 1 ? use(Generic<kKind, 8, 1>()) : use(Generic<kKind, 8, heads_a_pass(256, 2)>());
+}
+template <class Use>
+static int with_generic(const ScoredArgs& A, CacheKind kind, Use&& use) {
+  return kind == kCacheF32    ? with_generic<kCacheF32>(A, use)
+         : kind == kCacheBf16 ? with_generic<kCacheBf16>(A, use)
+                              : with_generic<kCacheE4m3>(A, use);
 }
 
 static bool shape_ok(const dcp_layout_t& L, int B, int Hq, int Hkv, int d) {
@@ -455,33 +470,41 @@ static bool shape_ok(const dcp_layout_t& L, int B, int Hq, int Hkv, int d) {
 
 static size_t before_bytes(int64_t entries) { return align_up((size_t)(entries + 2) * 4, 256); }
 
-// CTAs of a unit where that is better than cutting the line, else 0.  A unit whole
-// in a cluster of up to sixteen CTAs needs no plan and no second kernel, 4 us: that
-// is worth a few tiles a warp, which the cluster may have more than an even cut of
-// the line would give.  On the tensor cores 8 (8 bits, 32/8 heads of 128: one
-// request of 3000 tokens 9.2 us in a cluster and 12.4 by the line, 6000 tokens 11.5
-// and 12.4, 12000 tokens, 8.5 more a warp, 16.9 and 16.3; 16 requests of 200 tokens
-// 8.0 and 13.4); on CUDA cores 3.7 of 64 dims in one pass (fp32, 8/2 heads of 64, two
-// requests of 2000 tokens 11.4 and 16.2, of 4000, 3.6 more a warp, 15.4 and 17.6, of
-// 9000 25.6 and 17.5; 32/8 heads of 128, 4000 tokens, 1.8 more, 34.8 and 33.9).
-// Fewer CTAs do where a warp has few tiles: an 8-bit request of 300 tokens takes 8.7
-// us in sixteen, 7.4 in four, and one of 1500 8.5 and 8.2 in eight.
+// CTAs of a unit where that is better than cutting the line, else 0.  A unit whole in a
+// cluster needs no plan and no second kernel; its warps go through more rounds of tiles (one
+// tile a warp) than those of an even cut of the line, on which one more is counted where chunks
+// may end a unit and begin the next.  What the line's plan, second launch and merge are worth in
+// such rounds is by sweeps of both ways, over 1414 calls on the tensor cores and 765 on CUDA
+// cores (all caches, 1 to 16 heads a unit, heads of 64 to 256, 1 to 32 requests of 64 to 24000
+// tokens): on the tensor cores 5, and 3/4 for each round of the merge's loads, as few units leave
+// it many parts (8 bits: one request of 6000 tokens, 32/8 heads of 128, 11.7 us in clusters and
+// 12.0 by the line, 24000 tokens 27.2 and 19.9; two of 12000 with 16/1 heads 19.1 and 31.1); on
+// CUDA cores 3 of 64 dims in one pass of heads (fp32: two requests of 400 tokens, 16/1 heads of
+// 128, 47 and 77 us; of 12000, 8/2 heads of 64, 31 and 20).  The calls of the sweeps take 2.0%
+// to 2.6% and 1.6% more so than by the better way for each.
+// Of the cluster sizes that run at once the smallest that leaves a warp 3 tiles at most (CUDA
+// cores 1.5), else the largest: of 8 bits, 32/8 heads, 400 tokens take 6.9 us in eight CTAs and 7.6
+// in sixteen, 3000 tokens 10.1 and 9.2; 2 or 4 tiles in place of 3 cost 1% in the mean.
 // `wave` CTAs run at once; `tiles` are the most of a unit.
-static int unit_ctas_of(bool mma, int d, int G, int64_t wave, int64_t units, int64_t tiles) {
-  // clusters that run at once, by cudaOccupancyMaxActiveClusters: larger ones leave gaps
-  auto fits = [&](int c) {
-    return units * c * 1000 <= wave * (c == 16 ? 700 : c == 8 ? 890 : c == 4 ? 960 : 1000);
-  };
-  auto few = [&](int half) {
-    return tiles <= (!mma ? 1 : half == 8 ? 4 : 3) * kScoredWarps * half;
-  };
+template <class AtOnce>
+static int unit_ctas_of(const ScoredArgs& A, bool mma, int64_t wave, int64_t units, int64_t tiles,
+                        AtOnce&& at_once) {
+  auto rounds = [](int64_t n, int64_t warps) { return (n + warps - 1) / warps; };
   int c = kUnitCtas;
-  while (c > 1 && (!fits(c) || few(c / 2))) c /= 2;
-  if (!fits(c)) return 0;
-  const double more = (double)tiles / kScoredWarps * (1. / c - (double)units / wave);
-  if (mma) return more <= 8. ? c : 0;
-  const int hp = heads_a_pass(d, G), passes = (G + hp - 1) / hp;
-  return more * passes * d <= 3.7 * 64. ? c : 0;
+  while (c > 1 && (2 * tiles <= (mma ? 6 : 3) * kScoredWarps * (c / 2) || at_once(c) < units)) c /= 2;
+  if (at_once(c) < units) return 0;
+  int64_t each = (tiles * units + wave - 1) / wave;   // tiles of a chunk of the line
+  if (each < A.least) each = A.least;
+  const int64_t more =
+      rounds(tiles, (int64_t)kScoredWarps * c) - rounds(each, kScoredWarps) - (units > 1);
+  if (!mma) {
+    const int hp = heads_a_pass(A.d, A.G), passes = (A.G + hp - 1) / hp;
+    return more * passes * A.d <= 3 * 64 ? c : 0;
+  }
+  // the merge: parts of a unit, of which `groups` times kMergeAhead come at a time
+  const int cols = A.G * A.d / 4, groups = cols < kMergeThreads ? kMergeThreads / cols : 1;
+  const double loads = (double)rounds(tiles, each) / (groups * kMergeAhead);
+  return more <= 5. + .75 * loads ? c : 0;
 }
 
 // Chunks of a call at most: one for each CTA that runs at once.
@@ -590,16 +613,18 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
   const int64_t useful = (tiles + A.least - 1) / A.least;
   const int wave = mma ? scored_mma_wave(d, A.G, kv.kind) : generic_ctas(d);
   A.ctas = (int64_t)wave > useful ? (useful > 0 ? (int)useful : 1) : wave;
-  // the most tiles of a unit, by the table and by the window
+  // the most tiles of a unit, by the table and by the window: a rank's last may be part, of a
+  // window its first too, and both of kept tokens.  (Where documents start is not known here: a
+  // call is cut as if they started at 0.)
   const int64_t kept = f.window > 0 ? (int64_t)f.window + f.prefix : room;
   const int64_t tokens = kept < room ? kept : room;
-  const int64_t per_rank = tokens / dcp + 2 * layout.interleave;
-  int64_t most = apart_ ? per_rank / kRows + 4 : tokens / kRows + 4 * dcp;
-  // Of packed documents half a table is expected: 16 in up to 9001 tokens, 16/1 heads of
-  // 64, take 12.7 us in clusters and 16.2 by the line; 16 requests that fill 9000 tokens,
-  // 16/1 heads of 128, would take 27 and 24.
-  if (f.first) most = (most + 1) / 2;
-  A.unit_ctas = unit_ctas_of(mma, d, A.G, wave, entries * Hkv, most);
+  const int ends = f.window <= 0 ? 1 : f.prefix > 0 ? 4 : 2;
+  const int64_t most = apart_ ? (tokens / dcp + 2 * layout.interleave) / kRows + ends
+                              : tokens / kRows + ends * dcp;
+  A.unit_ctas = unit_ctas_of(A, mma, wave, entries * Hkv, most, [&](int ctas) {
+    return mma ? scored_mma_clusters(A, kv.kind, ctas)
+               : with_generic(A, kv.kind, [&](auto v) { return v.clusters(ctas); });
+  });
   if (A.unit_ctas) A.ctas = (int)(entries * Hkv) * A.unit_ctas;
   A.part_lse = (float*)w;
   w += align_up((size_t)(A.ctas + entries * Hkv) * A.G * 4, 256);
@@ -607,14 +632,10 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
   int rc = DCP_OK;
   if (mma) {
     rc = launch_scored_mma(A, kv.kind, s);
-    if (rc) return rc;
   } else {
-    const bool q16 = dtype == DCP_BF16;
-    const cudaError_t e = kv.kind == kCacheF32    ? launch_generic<kCacheF32>(A, q16, s)
-                          : kv.kind == kCacheBf16 ? launch_generic<kCacheBf16>(A, q16, s)
-                                                  : launch_generic<kCacheE4m3>(A, q16, s);
-    if (e != cudaSuccess) return launch_status_report(e);
+    rc = with_generic(A, kv.kind, [&](auto v) { return v.launch(A, dtype == DCP_BF16, s); });
   }
+  if (rc) return rc;
   if (A.unit_ctas) return launch_status();
   const cudaError_t e = launch_chained(scored_merge_kernel, (unsigned)(entries * Hkv),
                                        kMergeThreads, 0, s, A);

@@ -399,22 +399,61 @@ __device__ __forceinline__ void join_cluster(const ScoredArgs& A, int e, int g, 
 
 constexpr int kUnitCtas = 16;   // of a unit's cluster at most
 
+// Clusters beyond the eight CTAs that every device has: allowed once per device.
+template <auto kKernel>
+inline cudaError_t allow_clusters(int ctas) {
+  if (ctas <= 8) return cudaSuccess;
+  static bool allowed[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool kept = dev >= 0 && dev < 64;
+  if (kept && allowed[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && kept) allowed[dev] = true;
+  return e;
+}
+
+inline cudaLaunchAttribute cluster_of(int ctas) {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = (unsigned)ctas;
+  a.val.clusterDim.y = a.val.clusterDim.z = 1;
+  return a;
+}
+
+// Clusters of 1, 2, 4, 8 or 16 CTAs of a kernel that run at once on the current device (the
+// larger ones leave gaps, how many depends on the kernel's registers and shared memory), and 0
+// if that cannot be told.  Asked once for each size and number of heads, on which `smem` depends.
+template <auto kKernel>
+inline int clusters_at_once(int ctas, int heads, unsigned block, size_t smem) {
+  static int known[64][kUnitCtas + 1][17] = {};   // and 1
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const bool kept = dev >= 0 && dev < 64;
+  if (kept && known[dev][ctas][heads]) return known[dev][ctas][heads] - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr = cluster_of(ctas);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (allow_clusters<kKernel>(ctas) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();   // left for no other call to read
+    n = 0;
+  }
+  if (kept) known[dev][ctas][heads] = n + 1;
+  return n;
+}
+
 // As launch_chained, the grid in clusters of a unit's CTAs.
 template <auto kKernel, class... Args>
 inline cudaError_t launch_scored(const ScoredArgs& A, unsigned block, size_t smem, cudaStream_t s,
                                  const Args&... args) {
-  if (A.unit_ctas > 8) {   // beyond what every device has: allowed once per device
-    static bool allowed[64] = {false};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const bool kept = dev >= 0 && dev < 64;
-    if (!kept || !allowed[dev]) {
-      e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return e;
-      if (kept) allowed[dev] = true;
-    }
-  }
+  const cudaError_t e = allow_clusters<kKernel>(A.unit_ctas);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)A.ctas);
   cfg.blockDim = dim3(block);
@@ -423,9 +462,7 @@ inline cudaError_t launch_scored(const ScoredArgs& A, unsigned block, size_t sme
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)A.unit_ctas;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  attr[1] = cluster_of(A.unit_ctas);
   cfg.attrs = attr;
   cfg.numAttrs = A.unit_ctas > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kKernel, args...);
@@ -436,6 +473,7 @@ inline cudaError_t launch_scored(const ScoredArgs& A, unsigned block, size_t sme
 enum CacheKind { kCacheF32, kCacheBf16, kCacheE4m3 };
 bool scored_mma_ok(const ScoredArgs& A, CacheKind kind, bool q_bf16);
 int scored_mma_wave(int d, int G, CacheKind kind);   // CTAs that run at once
+int scored_mma_clusters(const ScoredArgs& A, CacheKind kind, int ctas);   // that run at once
 int launch_scored_mma(const ScoredArgs& A, CacheKind kind, cudaStream_t s);
 
 }  // namespace dcp

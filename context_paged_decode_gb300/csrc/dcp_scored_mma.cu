@@ -682,32 +682,51 @@ static bool encode_rows(CUtensorMap* map, const void* base, uint64_t row, uint64
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The kernel's variants, each with what the host asks of it.
 template <int D, bool E8, int NT, bool kFormed>
-static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
+struct Variant {
   using Z = Shape<D, E8, NT>;
-  if (!allow_smem<scored_mma_kernel<D, E8, NT, kFormed>>()) return DCP_ECUDA;
-  ScoredMaps maps;
-  memset((void*)&maps, 0, sizeof(maps));
-  const uint64_t rows = (uint64_t)A.nb * A.Hkv * A.S.bs;
-  for (int r = 0; r < A.S.dcp; ++r)
-    if (!encode_rows(&maps.k[r], A.k.ptr[r], Z::kRowBytes, rows) ||
-        !encode_rows(&maps.v[r], A.v.ptr[r], Z::kRowBytes, rows))
-      return DCP_ECUDA;
-  const cudaError_t e = launch_scored<scored_mma_kernel<D, E8, NT, kFormed>>(
-      A, kScoredThreads, Z::smem(A.G), s, A, maps);
-  return e == cudaSuccess ? launch_status() : launch_status_report(e);
+  static constexpr auto kKernel = scored_mma_kernel<D, E8, NT, kFormed>;
+
+  static int clusters(const ScoredArgs& A, int ctas) {
+    return allow_smem<kKernel>() ? clusters_at_once<kKernel>(ctas, A.G, kScoredThreads, Z::smem(A.G))
+                                 : 0;
+  }
+
+  static int launch(const ScoredArgs& A, cudaStream_t s) {
+    if (!allow_smem<kKernel>()) return DCP_ECUDA;
+    ScoredMaps maps;
+    memset((void*)&maps, 0, sizeof(maps));
+    const uint64_t rows = (uint64_t)A.nb * A.Hkv * A.S.bs;
+    for (int r = 0; r < A.S.dcp; ++r)
+      if (!encode_rows(&maps.k[r], A.k.ptr[r], Z::kRowBytes, rows) ||
+          !encode_rows(&maps.v[r], A.v.ptr[r], Z::kRowBytes, rows))
+        return DCP_ECUDA;
+    const cudaError_t e = launch_scored<kKernel>(A, kScoredThreads, Z::smem(A.G), s, A, maps);
+    return e == cudaSuccess ? launch_status() : launch_status_report(e);
+  }
+};
+
+// `use` of the variant that a call takes.
+template <int D, bool E8, class Use>
+static int with_variant(const ScoredArgs& A, Use&& use) {
+  if (A.cap > 0.f || A.slopes)
+    return A.G <= 8 ? use(Variant<D, E8, 1, true>()) : use(Variant<D, E8, 2, true>());
+  return A.G <= 8 ? use(Variant<D, E8, 1, false>()) : use(Variant<D, E8, 2, false>());
+}
+template <class Use>
+static int with_variant(const ScoredArgs& A, CacheKind kind, Use&& use) {
+  if (A.d == 64)
+    return kind == kCacheE4m3 ? with_variant<64, true>(A, use) : with_variant<64, false>(A, use);
+  return kind == kCacheE4m3 ? with_variant<128, true>(A, use) : with_variant<128, false>(A, use);
 }
 
-template <int D, bool E8>
-static int launch_mma(const ScoredArgs& A, cudaStream_t s) {
-  if (A.cap > 0.f || A.slopes)
-    return A.G <= 8 ? launch_mma<D, E8, 1, true>(A, s) : launch_mma<D, E8, 2, true>(A, s);
-  return A.G <= 8 ? launch_mma<D, E8, 1, false>(A, s) : launch_mma<D, E8, 2, false>(A, s);
+int scored_mma_clusters(const ScoredArgs& A, CacheKind kind, int ctas) {
+  return with_variant(A, kind, [&](auto v) { return v.clusters(A, ctas); });
 }
 
 int launch_scored_mma(const ScoredArgs& A, CacheKind kind, cudaStream_t s) {
-  if (A.d == 64) return kind == kCacheE4m3 ? launch_mma<64, true>(A, s) : launch_mma<64, false>(A, s);
-  return kind == kCacheE4m3 ? launch_mma<128, true>(A, s) : launch_mma<128, false>(A, s);
+  return with_variant(A, kind, [&](auto v) { return v.launch(A, s); });
 }
 
 template <int D, bool E8, int NT>

@@ -199,3 +199,27 @@ def test_infinite_values(lib, cache, d, room):
     rest[[3, 9, 5]] = False
     assert torch.isfinite(out[..., rest]).all() and torch.isfinite(out[1]).all()
     assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3, F32], ids=str)
+@pytest.mark.parametrize("tokens", [300, 1500, 5000, 12000])
+def test_documents_from_0_are_requests(lib, cache, tokens):
+    """A call whose documents all start at 0 is cut as one without starts, and gives the same bits."""
+    q = F32 if cache == F32 else BF16
+    L, B, H, d, bs = lib.Layout(3, 32, 4), 16, 1, 64, 32
+    blocks = -(-tokens // 96)
+    bt = torch.arange(B * blocks, dtype=torch.int32, device="cuda").view(1, B, blocks).expand(3, -1, -1).contiguous()
+    mk = lambda: [torch.randn((B * blocks, H, bs, d), device="cuda").to(cache) for _ in range(3)]  # noqa: E731
+    if cache == E4M3:
+        kv = lib.PagedKV8(mk(), mk(), [torch.ones((B * blocks, H, 4), device="cuda") for _ in range(3)],
+                          bt, B * blocks)
+        decode = lib.q8_decode_gqa
+    else:
+        kv, decode = lib.PagedKV(mk(), mk(), bt, B * blocks), lib.scored_decode_gqa
+    x = torch.randn((B, 16, d), device="cuda").to(q)
+    lens = torch.linspace(tokens // 16, tokens, B, device="cuda").int()
+    zeros = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for kw in ({}, dict(window=tokens // 2, prefix=4)):
+        a = decode(L, x, kv, lens, d ** -0.5, lib.Scores(first=zeros, **kw))
+        b = decode(L, x, kv, lens, d ** -0.5, lib.Scores(**kw))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
