@@ -474,17 +474,21 @@ static size_t before_bytes(int64_t entries) { return align_up((size_t)(entries +
 // cluster needs no plan and no second kernel; its warps go through more rounds of tiles (one
 // tile a warp) than those of an even cut of the line, on which one more is counted where chunks
 // may end a unit and begin the next.  What the line's plan, second launch and merge are worth in
-// such rounds is by sweeps of both ways, over 1414 calls on the tensor cores and 765 on CUDA
-// cores (all caches, 1 to 16 heads a unit, heads of 64 to 256, 1 to 32 requests of 64 to 24000
-// tokens): on the tensor cores 5, and 3/4 for each round of the merge's loads, as few units leave
-// it many parts (8 bits: one request of 6000 tokens, 32/8 heads of 128, 11.7 us in clusters and
-// 12.0 by the line, 24000 tokens 27.2 and 19.9; two of 12000 with 16/1 heads 19.1 and 31.1); on
-// CUDA cores 3 of 64 dims in one pass of heads (fp32: two requests of 400 tokens, 16/1 heads of
-// 128, 47 and 77 us; of 12000, 8/2 heads of 64, 31 and 20).  The calls of the sweeps take 2.0%
-// to 2.6% and 1.6% more so than by the better way for each.
+// such rounds is by sweeps of both ways over 1860 calls (all caches, 1 to 16 heads a unit, heads
+// of 64 to 256, 1 to 32 requests, tables for 800 to 24000 tokens that are full, half full, full to
+// a quarter or to a sixteenth): on the tensor cores 10, and 1.5 for each round of the merge's
+// loads, as few units leave it many parts; on CUDA cores 6 of 64 dims in one pass of heads.  For
+// full tables half of each would be best, for nearly empty ones more: of tables 24000 tokens wide
+// on the tensor cores, two requests with 16/1 heads of 128 in 8 bits take 28.9 us in clusters and
+// 38.0 by the line, of 1500 tokens 11.6 and 16.3; 16 requests, 16/1 heads of 64 in bf16, of 9000
+// tokens in tables for 9000 19.8 and 18.2, of 4500 13.5 and 16.7; one in 8 bits, 32/8 heads, of
+// 24000 tokens in a table for 24000 27.3 and 20.1 (the line is taken), of 12000 in one for 12000
+// 16.8 and 16.0; on CUDA cores two of 3000 in fp32, 8/2 heads of 64, in tables for 6000 13.3 and
+// 12.8, of 1500 11.4 and 16.5.
 // Of the cluster sizes that run at once the smallest that leaves a warp 3 tiles at most (CUDA
 // cores 1.5), else the largest: of 8 bits, 32/8 heads, 400 tokens take 6.9 us in eight CTAs and 7.6
-// in sixteen, 3000 tokens 10.1 and 9.2; 2 or 4 tiles in place of 3 cost 1% in the mean.
+// in sixteen, 3000 tokens 10.1 and 9.2; of 1414 calls that fill their tables 2 or 4 tiles in place
+// of 3 cost 1% in the mean.
 // `wave` CTAs run at once; `tiles` are the most of a unit.
 template <class AtOnce>
 static int unit_ctas_of(const ScoredArgs& A, bool mma, int64_t wave, int64_t units, int64_t tiles,
@@ -499,12 +503,12 @@ static int unit_ctas_of(const ScoredArgs& A, bool mma, int64_t wave, int64_t uni
       rounds(tiles, (int64_t)kScoredWarps * c) - rounds(each, kScoredWarps) - (units > 1);
   if (!mma) {
     const int hp = heads_a_pass(A.d, A.G), passes = (A.G + hp - 1) / hp;
-    return more * passes * A.d <= 3 * 64 ? c : 0;
+    return more * passes * A.d <= 6 * 64 ? c : 0;
   }
   // the merge: parts of a unit, of which `groups` times kMergeAhead come at a time
   const int cols = A.G * A.d / 4, groups = cols < kMergeThreads ? kMergeThreads / cols : 1;
   const double loads = (double)rounds(tiles, each) / (groups * kMergeAhead);
-  return more <= 5. + .75 * loads ? c : 0;
+  return more <= 10. + 1.5 * loads ? c : 0;
 }
 
 // Chunks of a call at most: one for each CTA that runs at once.
