@@ -354,8 +354,8 @@ scored_mma_kernel(const __grid_constant__ ScoredArgs A, const __grid_constant__ 
           ks_ = both.x;
           const int bits = __float_as_int(both.y), mant = bits & 0x7fffff;
           vlog = (float)((bits >> 23) - 127);     // exact for a power of two
-          if ((bits >> 23) == 0)                  // below 2^-126; of 0 -inf, a weight of nothing
-            vlog = log2f(both.y * 0x1p24f) - 24.f;
+          if ((uint32_t)bits - 0x00800000u >= 0x7f000000u)   // below 2^-126 (of 0 -inf, a weight of
+            vlog = log2f(both.y * 0x1p24f) - 24.f;           // nothing), or no scale: NaN or inf
           else if (mant)
             vlog += log2f(__int_as_float(mant | 0x3f800000));
         }

@@ -714,7 +714,8 @@ int dcp_cache_compact(dcp_layout_t layout, dcp_pool_set_t pools, const int32_t* 
  *              head the scale of its keys, that of its values, and two that
  *              nothing reads or writes (16 bytes, so that scales are copied like
  *              pages).  A number c stands for c * scale.  dcp_q8_append_gqa
- *              makes powers of two; any positive finite scale is read.
+ *              makes powers of two; any positive finite scale is read, and 0
+ *              stands for zeros.
  * Pools and scales are 16-byte aligned; head_dim is a multiple of 32 up to 256.
  */
 typedef struct {
@@ -742,10 +743,12 @@ typedef struct {
  * need; any other keeps the larger of its scale and need (a scale that is not
  * positive and finite counts as none), and if that is larger than before, its
  * other places c become the e4m3 number nearest to c * before / after.  x is
- * held as the e4m3 number nearest to x / scale, ties to even; infinities as
- * +-448, NaN as NaN.
+ * held as the e4m3 number nearest to x / scale, ties to even (beside a scale
+ * that is no power of two: to the quotient in 32 bits); infinities as +-448, NaN
+ * as NaN.
  * A request with a negative length, rows outside [0, num_tokens] or tokens
- * beyond max_vblocks bumps err_count and is not written; a page whose table
+ * beyond max_vblocks bumps err_count and is not written (with no tokens or no
+ * requests nothing is looked at); a page whose table
  * entry is outside [0, num_blocks) is skipped and counted.  Requests that write
  * to one page at the same time leave it undefined (a fork's open page is its
  * own).  k, v and their strides are multiples of 16 bytes and 16-byte aligned,

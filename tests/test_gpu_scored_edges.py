@@ -223,3 +223,55 @@ def test_documents_from_0_are_requests(lib, cache, tokens):
         a = decode(L, x, kv, lens, d ** -0.5, lib.Scores(first=zeros, **kw))
         b = decode(L, x, kv, lens, d ** -0.5, lib.Scores(**kw))
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("q", [BF16, F32], ids=str)
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_scales_that_are_none_show(lib, q, which, bad):
+    """A seen page whose scale is NaN or infinite does not give numbers that look like results."""
+    p = Problem(lib, E4M3, q, 4, 1, 64, 2, 16, 1, [100, 40])
+    p.kv.scales[1][int(p.bt[1, 0, 1]), 0, which] = bad
+    out, lse = p.run()
+    assert not torch.isfinite(out[0]).any() and torch.isfinite(out[1]).all()
+    assert torch.isfinite(lse[1]).all() and (which == 1 or not torch.isfinite(lse[0]).any())
+
+
+FIRST = """
+import torch, sys
+sys.path.insert(0, {root!r})
+import context_paged_decode_gb300 as dcp
+L = dcp.Layout(2, 16, 1)
+bt = torch.zeros((2, 1, 1), dtype=torch.int32, device="cuda")
+lens = torch.tensor([20], dtype=torch.int32, device="cuda")
+calls = []
+for dt in (torch.bfloat16, torch.float32):
+    for d in (64, 256):
+        q = torch.ones((1, 4, d), dtype=dt, device="cuda")
+        pool = [torch.ones((1, 2, 16, d), dtype=dt, device="cuda")] * 2
+        kv8 = dcp.PagedKV8([p.to(torch.float8_e4m3fn) for p in pool], [p.to(torch.float8_e4m3fn) for p in pool],
+                           [torch.ones((1, 2, 4), device="cuda")] * 2, bt, 1)
+        calls.append((dcp.scored_decode_gqa, q, dcp.PagedKV(pool, pool, bt, 1)))
+        calls.append((dcp.q8_decode_gqa, q, kv8))
+torch.cuda.synchronize()
+for call, q, kv in calls:
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = call(L, q, kv, lens, 1.0, dcp.Scores())
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, torch.ones_like(q)), call
+print("ok")
+"""
+
+
+def test_first_calls_captured():
+    """In a process of their own, calls that are captured before any other has run."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root)], capture_output=True, text=True,
+                       timeout=100)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
