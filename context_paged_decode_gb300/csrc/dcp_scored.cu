@@ -8,6 +8,7 @@
 //     t = scale q.k;  t = cap tanh(t / cap);  t = t - slope[h] (L - 1 - x)
 //     lse = ln( sum_seen e^t + e^sink ),  o = sum_seen e^(t - lse) v.
 #include <math.h>
+#include <algorithm>
 
 #include "dcp_q8.cuh"
 #include "dcp_scored.cuh"
@@ -472,43 +473,45 @@ static size_t before_bytes(int64_t entries) { return align_up((size_t)(entries +
 
 // CTAs of a unit where that is better than cutting the line, else 0.  A unit whole in a
 // cluster needs no plan and no second kernel; its warps go through more rounds of tiles (one
-// tile a warp) than those of an even cut of the line, on which one more is counted where chunks
-// may end a unit and begin the next.  What the line's plan, second launch and merge are worth in
-// such rounds is by sweeps of both ways over 1860 calls (all caches, 1 to 16 heads a unit, heads
-// of 64 to 256, 1 to 32 requests, tables for 800 to 24000 tokens that are full, half full, full to
-// a quarter or to a sixteenth): on the tensor cores 10, and 1.5 for each round of the merge's
-// loads, as few units leave it many parts; on CUDA cores 6 of 64 dims in one pass of heads.  For
-// full tables half of each would be best, for nearly empty ones more: of tables 24000 tokens wide
-// on the tensor cores, two requests with 16/1 heads of 128 in 8 bits take 28.9 us in clusters and
-// 38.0 by the line, of 1500 tokens 11.6 and 16.3; 16 requests, 16/1 heads of 64 in bf16, of 9000
-// tokens in tables for 9000 19.8 and 18.2, of 4500 13.5 and 16.7; one in 8 bits, 32/8 heads, of
-// 24000 tokens in a table for 24000 27.3 and 20.1 (the line is taken), of 12000 in one for 12000
-// 16.8 and 16.0; on CUDA cores two of 3000 in fp32, 8/2 heads of 64, in tables for 6000 13.3 and
-// 12.8, of 1500 11.4 and 16.5.
+// tile a warp) than those of an even cut of the line.  How long requests are is not known here:
+// the table is a bound, the line evens out requests of unlike lengths, and a cluster waits for
+// the longest.  So the line is counted as if all requests but one filled half of the table, and
+// with a round more where chunks may end a unit and begin the next.  What its plan, second launch
+// and merge are worth in rounds is by sweeps of both ways over 2584 calls with full tables or
+// with mixed lengths (all caches, 1 to 16 heads a unit, heads of 64 to 256, 1 to 32 requests of 64
+// to 48000 tokens) and 1860 with tables that are full, half full, full to a quarter or to a
+// sixteenth: on the tensor cores 10, and one for each round of the merge's loads, as few units
+// leave it many parts; on CUDA cores 3 of 64 dims in one pass of heads.  Where the table is full
+// less would be better, where it is nearly empty more:
+//   8 bits, two requests, 16/1 heads of 128, table for 24000: of 24000 tokens 28.9 us in clusters
+//     and 38.0 by the line, of 1500 11.6 and 16.3;
+//   bf16, 16 requests, 16/1 heads of 64, table for 9000: of 9000 19.8 and 18.2, of 4500 13.5 and 16.7;
+//   8 bits, one, 32/8 heads: of 24000 in a table for as many 27.3 and 20.1 (the line is taken);
+//   fp32, two, 8/2 heads of 64, table for 3000: of 3000 13.4 and 12.9, of 1500 11.3 and 16.5.
 // Of the cluster sizes that run at once the smallest that leaves a warp 3 tiles at most (CUDA
 // cores 1.5), else the largest: of 8 bits, 32/8 heads, 400 tokens take 6.9 us in eight CTAs and 7.6
-// in sixteen, 3000 tokens 10.1 and 9.2; of 1414 calls that fill their tables 2 or 4 tiles in place
-// of 3 cost 1% in the mean.
+// in sixteen, 3000 tokens 10.1 and 9.2.
 // `wave` CTAs run at once; `tiles` are the most of a unit.
 template <class AtOnce>
 static int unit_ctas_of(const ScoredArgs& A, bool mma, int64_t wave, int64_t units, int64_t tiles,
                         AtOnce&& at_once) {
-  auto rounds = [](int64_t n, int64_t warps) { return (n + warps - 1) / warps; };
+  auto rounds = [](int64_t n, int64_t at_a_time) { return (n + at_a_time - 1) / at_a_time; };
   int c = kUnitCtas;
   while (c > 1 && (2 * tiles <= (mma ? 6 : 3) * kScoredWarps * (c / 2) || at_once(c) < units)) c /= 2;
   if (at_once(c) < units) return 0;
-  int64_t each = (tiles * units + wave - 1) / wave;   // tiles of a chunk of the line
+  // tiles of a chunk of the line
+  int64_t each = rounds(rounds(tiles * units * (A.B + 1), 2 * (int64_t)A.B), wave);
   if (each < A.least) each = A.least;
   const int64_t more =
       rounds(tiles, (int64_t)kScoredWarps * c) - rounds(each, kScoredWarps) - (units > 1);
   if (!mma) {
     const int hp = heads_a_pass(A.d, A.G), passes = (A.G + hp - 1) / hp;
-    return more * passes * A.d <= 6 * 64 ? c : 0;
+    return more * passes * A.d <= 3 * 64 ? c : 0;
   }
   // the merge: parts of a unit, of which `groups` times kMergeAhead come at a time
   const int cols = A.G * A.d / 4, groups = cols < kMergeThreads ? kMergeThreads / cols : 1;
   const double loads = (double)rounds(tiles, each) / (groups * kMergeAhead);
-  return more <= 10. + 1.5 * loads ? c : 0;
+  return more <= 10. + loads ? c : 0;
 }
 
 // Chunks of a call at most: one for each CTA that runs at once.
@@ -623,8 +626,11 @@ static int scored_call(const dcp_layout_t& layout, const void* q, int B, int Hq,
   const int64_t kept = f.window > 0 ? (int64_t)f.window + f.prefix : room;
   const int64_t tokens = kept < room ? kept : room;
   const int ends = f.window <= 0 ? 1 : f.prefix > 0 ? 4 : 2;
-  const int64_t most = apart_ ? (tokens / dcp + 2 * layout.interleave) / kRows + ends
-                              : tokens / kRows + ends * dcp;
+  const int64_t per_rank = (tokens / dcp + 2 * layout.interleave) / kRows + ends;
+  // a rank's part of the table, and a tile for each token, bound them too
+  const int64_t held = ((int64_t)kv.max_vb * layout.block_size + kRows - 1) / kRows;
+  int64_t most = apart_ ? per_rank : tokens / kRows + ends * dcp;
+  most = std::min({most, apart_ ? held : held * dcp, tokens});
   A.unit_ctas = unit_ctas_of(A, mma, wave, entries * Hkv, most, [&](int ctas) {
     return mma ? scored_mma_clusters(A, kv.kind, ctas)
                : with_generic(A, kv.kind, [&](auto v) { return v.clusters(ctas); });
