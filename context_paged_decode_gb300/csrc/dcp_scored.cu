@@ -477,7 +477,7 @@ static size_t before_bytes(int64_t entries) { return align_up((size_t)(entries +
 // the table is a bound, the line evens out requests of unlike lengths, and a cluster waits for
 // the longest.  So the line is counted as if all requests but one filled half of the table, and
 // with a round more where chunks may end a unit and begin the next.  What its plan, second launch
-// and merge are worth in rounds is by sweeps of both ways over 2584 calls with full tables or
+// and merge are worth in rounds is by sweeps of both ways over 3208 calls with full tables or
 // with mixed lengths (all caches, 1 to 16 heads a unit, heads of 64 to 256, 1 to 32 requests of 64
 // to 48000 tokens) and 1860 with tables that are full, half full, full to a quarter or to a
 // sixteenth: on the tensor cores 10, and one for each round of the merge's loads, as few units
